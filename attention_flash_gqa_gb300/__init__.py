@@ -18,6 +18,13 @@ Entry points (same names as the C ABI):
 * ``attn_bwd(q, k, v, o, lse, dO, ...)``  -> (dQ, dK, dV); dense or packed (cu_seqlens)
 * ``attn_merge_lse(o_parts, lse_parts, ...)`` attention results over disjoint key sets -> (o, lse)
 * ``attn_decode_paged(q, k_cache, v_cache, block_table, seq_lens, ...)`` -> (o, lse[B,Hq])
+* ``attn_paged_plan(kv_lens, new_lens, free_pages, block_table, pages_held, free_used, total_new, ...)``
+  pages, positions and cache slots of a serving step, from request lengths -> PagedPlan
+* ``attn_qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, ...)`` RMS norm of every head and
+  rotary position encoding -> (q_out, k_out); ``attn_qk_norm_rope_bwd`` its gradient;
+  ``attn_qk_norm_rope_paged`` the same with K and V written into the paged caches by slot -> q_out
+* ``attn_tree_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, tree_mask, max_q_len, ...)``
+  drafted token trees over a paged cache: packed rows [T,Hq,D] -> (o, lse[Hq,T])
 * ``attn_workspace_size``, ``attn_get_device_status``, ``attn_status_string``
 * ``attn_selftest_wait_timeout`` (exercises the bounded-wait failure reporting)
 """
@@ -27,13 +34,16 @@ import ctypes
 import math
 import os
 import threading
+from typing import Any, NamedTuple
 
 __all__ = [
     "AttnError", "attn_fwd", "attn_fwd_varlen", "attn_fwd_paged", "attn_bwd", "attn_decode_paged", "attn_workspace_size",
     "attn_get_device_status", "attn_status_string", "library_path", "load_library",
     "attn_launch_count", "attn_profile_start", "attn_profile_stop", "attn_decode_paged_noalloc",
-    "attn_selftest_wait_timeout", "attn_merge_lse",
+    "attn_selftest_wait_timeout", "attn_merge_lse", "attn_paged_plan", "PagedPlan", "attn_qk_norm_rope",
+    "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_paged", "attn_tree_paged",
     "ATTN_OP_FWD", "ATTN_OP_FWD_VARLEN", "ATTN_OP_BWD", "ATTN_OP_BWD_VARLEN", "ATTN_OP_DECODE_PAGED",
+    "ATTN_OP_QK_NORM_ROPE_BWD", "ATTN_OP_TREE_PAGED",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,6 +52,7 @@ _lock = threading.Lock()
 _lib = None
 
 ATTN_OP_FWD, ATTN_OP_FWD_VARLEN, ATTN_OP_BWD, ATTN_OP_BWD_VARLEN, ATTN_OP_DECODE_PAGED = 0, 1, 2, 3, 4
+ATTN_OP_QK_NORM_ROPE_BWD, ATTN_OP_TREE_PAGED = 5, 6
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ERR_MISALIGNED",
           4: "ATTN_ERR_WORKSPACE", 5: "ATTN_ERR_LAUNCH", 6: "ATTN_ERR_DEVICE_TIMEOUT", 7: "ATTN_ERR_DEVICE_BOUNDS",
           8: "ATTN_ERR_NO_DEVICE"}
@@ -89,6 +100,15 @@ def load_library():
         lib.attn_profile_start.restype = I
         lib.attn_profile_stop.argtypes = [ctypes.c_char_p, Z]
         lib.attn_profile_stop.restype = I
+        LL = ctypes.c_longlong
+        lib.attn_paged_plan.argtypes = [P] * 13 + [I] * 6 + [P]
+        lib.attn_qk_norm_rope.argtypes = [P] * 8 + [I] * 6 + [LL, LL, F, F, I, I, P]
+        lib.attn_qk_norm_rope_bwd.argtypes = [P] * 12 + [I] * 6 + [LL] * 4 + [F, F, I, I, P, Z, P]
+        lib.attn_qk_norm_rope_paged.argtypes = [P] * 11 + [I] * 8 + [LL] * 3 + [F, F, I, I, P]
+        lib.attn_tree_paged.argtypes = [P] * 10 + [I] * 10 + [F, I, P, Z, P]
+        for f in (lib.attn_paged_plan, lib.attn_qk_norm_rope, lib.attn_qk_norm_rope_bwd, lib.attn_qk_norm_rope_paged,
+                  lib.attn_tree_paged):
+            f.restype = I
         for f in (lib.attn_fwd, lib.attn_fwd_varlen, lib.attn_fwd_paged, lib.attn_bwd, lib.attn_decode_paged, lib.attn_get_device_status):
             f.restype = I
         _lib = lib
@@ -356,4 +376,293 @@ def attn_decode_paged_noalloc(q, k_cache, v_cache, block_table, seq_lens, o, lse
             _bf16(o, "o"), _ptr(lse), B, Hq, Hkv, D, page_size, block_table.shape[1], num_pages, scale, int(window),
             _stream_ptr(stream, q.device))
     _check(rc, "attn_decode_paged_noalloc")
+    return o, lse
+
+
+class PagedPlan(NamedTuple):
+    """What attn_paged_plan writes (int32 tensors)."""
+
+    seq_lens: Any     # [R] cached tokens including the new ones
+    cu_q: Any         # [R + 1] first row of each request
+    positions: Any    # [total_new] position of each row
+    slots: Any        # [total_new] cache slot of each row, -1: none
+    pages_held: Any   # [R] pages in each block-table row
+    free_used: Any    # [1] pages taken of the free list
+    admitted: Any     # [1] requests served
+
+
+def _check_i32(name, t, shape, device):
+    import torch
+
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
+    return t.data_ptr()
+
+
+def _cuda_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _allocating(stream, make):
+    """make(), its tensors belonging to the stream that the call runs on."""
+    import torch
+
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _run(fn, what, device, stream, *args):
+    import torch
+
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, _stream_ptr(stream, device))
+    else:
+        with torch.cuda.device(device):  # the library works on the current device
+            rc = fn(*args, _stream_ptr(stream, device))
+    if rc != 0:
+        raise AttnError(rc, what)
+
+
+def attn_paged_plan(kv_lens, new_lens, free_pages, block_table, pages_held, free_used, total_new: int, *, num_pages: int,
+                    page_size: int = 16, out: PagedPlan | None = None, stream=None) -> PagedPlan:
+    """The plan of a serving step over a paged cache, from lengths on the device (all int32).
+
+    kv_lens, new_lens, pages_held [R]: cached tokens, tokens to add and pages held of every request;
+    free_pages [F] page ids to hand out in order, free_used [1] how many are taken already; block_table
+    [R, max_pages], whose rows get the new pages in place; total_new: rows of positions and slots (a
+    step of varying size may pass more than it fills: the rest gets slot -1). ``out`` gives the
+    tensors to write; its seq_lens, pages_held and free_used may be kv_lens, pages_held and free_used
+    themselves (a state kept in place). See include/attn.h for admission and refusals.
+    """
+    import torch
+
+    dev = _cuda_device(kv_lens, "kv_lens")
+    R, F, T = kv_lens.numel(), free_pages.numel(), int(total_new)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [num_reqs, max_pages]")
+    if T < 0:
+        raise ValueError("total_new must not be negative")
+    if out is None:
+        def make():
+            buf = torch.empty(3 * R + 2 * T + 3, dtype=torch.int32, device=dev)
+            return PagedPlan(*buf.split([R, R + 1, T, T, R, 1, 1]))
+
+        out = _allocating(stream, make)
+    _run(load_library().attn_paged_plan, "attn_paged_plan", dev, stream,
+         _check_i32("kv_lens", kv_lens, (R,), dev), _check_i32("new_lens", new_lens, (R,), dev),
+         _check_i32("pages_held", pages_held, (R,), dev), _check_i32("free_pages", free_pages, (F,), dev),
+         _check_i32("free_used", free_used, (1,), dev),
+         _check_i32("block_table", block_table, (R, block_table.shape[1]), dev),
+         _check_i32("out.seq_lens", out.seq_lens, (R,), dev), _check_i32("out.cu_q", out.cu_q, (R + 1,), dev),
+         _check_i32("out.positions", out.positions, (T,), dev), _check_i32("out.slots", out.slots, (T,), dev),
+         _check_i32("out.pages_held", out.pages_held, (R,), dev), _check_i32("out.free_used", out.free_used, (1,), dev),
+         _check_i32("out.admitted", out.admitted, (1,), dev), R, T, F, int(page_size), block_table.shape[1],
+         int(num_pages))
+    return out
+
+
+def _rows(t, name, device=None):
+    """A [..., H, D] bf16 tensor as T tokens: (pointer, leading shape, T, H, D, token stride)."""
+    import torch
+
+    if t.dtype != torch.bfloat16 or not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor on the call's device")
+    shape, st = t.shape, t.stride()
+    if len(shape) not in (3, 4):
+        raise ValueError(f"{name} must be [T, H, D] or [B, S, H, D]")
+    H, D = shape[-2], shape[-1]
+    if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if len(shape) == 3:
+        T, step = shape[0], st[0]
+    else:
+        T = shape[0] * shape[1]
+        step = st[1] if shape[1] > 1 else st[0]
+        if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
+            raise ValueError(f"{name}: tokens must be evenly spaced across the batch")
+    return t.data_ptr(), shape[:-2], T, H, D, (step if T > 1 else H * D)
+
+
+def _dense_rows(t, name, lead, H, D, device):
+    import torch
+
+    if t.dtype != torch.bfloat16 or t.device != device or not t.is_contiguous() or tuple(t.shape) != (*lead, H, D):
+        raise ValueError(f"{name} must be a contiguous bfloat16 tensor of shape {(*lead, H, D)} on {device}")
+    return t.data_ptr()
+
+
+def _norm_weights(q_weight, k_weight, D, device):
+    """Pointers of the norm weights and whether they are fp32."""
+    import torch
+
+    kinds = {w.dtype for w in (q_weight, k_weight) if w is not None}
+    if len(kinds) > 1 or not kinds <= {torch.bfloat16, torch.float32}:
+        raise ValueError("q_weight and k_weight must both be bfloat16 or both float32")
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.device != device or not w.is_contiguous() or tuple(w.shape) != (D,)):
+            raise ValueError(f"{n} must be a contiguous tensor of shape ({D},) on {device}")
+    return (None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+            int(kinds == {torch.float32}))
+
+
+def _angles(positions, cos_sin, lead, T, device):
+    """Pointers of positions and table, rotated dims and table rows."""
+    import torch
+
+    if cos_sin is None:
+        return None, None, 0, 0
+    if (cos_sin.dtype != torch.float32 or cos_sin.device != device or not cos_sin.is_contiguous() or cos_sin.dim() != 2):
+        raise ValueError(f"cos_sin must be a contiguous float32 tensor [max_pos, rot_dim] on {device}")
+    if cos_sin.shape[1] == 0:
+        return None, None, 0, 0
+    if positions is None or tuple(positions.shape) not in (tuple(lead), (T,)):
+        raise ValueError(f"positions must be an int32 tensor of shape {tuple(lead)}")
+    return _check_i32("positions", positions, tuple(positions.shape), device), cos_sin.data_ptr(), cos_sin.shape[1], cos_sin.shape[0]
+
+
+def attn_qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, q_out=None, k_out=None, *, eps: float = 1e-6,
+                      weight_offset: float = 0.0, interleaved: bool = False, stream=None):
+    """RMS norm of every query and key head, then the rotary position encoding -> (q_out, k_out).
+
+    q [T,Hq,D], k [T,Hkv,D] (or [B,S,H,D]) bf16, possibly slices of a fused projection; q_weight, k_weight
+    [D] bf16 or fp32 (None: no weight), applied as weight_offset + w; positions int32 [T]; cos_sin fp32
+    [max_pos, rot_dim], cos then sin of the rot_dim/2 angles of each position (None: no rotation).
+    """
+    import torch
+
+    qp, lead, T, Hq, D, qs = _rows(q, "q")
+    dev = q.device
+    kp, klead, _, Hkv, Dk, ks = _rows(k, "k", dev)
+    if klead != lead or Dk != D:
+        raise ValueError("q and k must have the same tokens and head size")
+    wq, wk, w32 = _norm_weights(q_weight, k_weight, D, dev)
+    pos, table, rot, rows = _angles(positions, cos_sin, lead, T, dev)
+    if q_out is None:
+        q_out = _allocating(stream, lambda: torch.empty((*lead, Hq, D), dtype=torch.bfloat16, device=dev))
+    if k_out is None:
+        k_out = _allocating(stream, lambda: torch.empty((*lead, Hkv, D), dtype=torch.bfloat16, device=dev))
+    _run(load_library().attn_qk_norm_rope, "attn_qk_norm_rope", dev, stream, qp, kp,
+         _dense_rows(q_out, "q_out", lead, Hq, D, dev), _dense_rows(k_out, "k_out", lead, Hkv, D, dev), wq, wk, pos, table,
+         T, Hq, Hkv, D, rot, rows, qs, ks, float(eps), float(weight_offset), w32, int(bool(interleaved)))
+    return q_out, k_out
+
+
+def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, cos_sin, dq=None, dk=None, *,
+                          eps: float = 1e-6, weight_offset: float = 0.0, interleaved: bool = False, workspace=None,
+                          stream=None):
+    """Gradient of attn_qk_norm_rope -> (dq, dk, dq_weight, dk_weight); the weight gradients are fp32 [D].
+
+    dq_out, dk_out: gradients of its results (contiguous bf16); the rest as passed to the forward.
+    dq / dk may be given, as slices of a fused projection's gradient too.
+    """
+    import torch
+
+    qp, lead, T, Hq, D, qs = _rows(q, "q")
+    dev = q.device
+    kp, klead, _, Hkv, Dk, ks = _rows(k, "k", dev)
+    if klead != lead or Dk != D:
+        raise ValueError("q and k must have the same tokens and head size")
+    wq, wk, w32 = _norm_weights(q_weight, k_weight, D, dev)
+    pos, table, rot, rows = _angles(positions, cos_sin, lead, T, dev)
+    need = attn_workspace_size(ATTN_OP_QK_NORM_ROPE_BWD, D=D)
+
+    def make():
+        return (torch.empty((*lead, Hq, D), dtype=torch.bfloat16, device=dev) if dq is None else dq,
+                torch.empty((*lead, Hkv, D), dtype=torch.bfloat16, device=dev) if dk is None else dk,
+                torch.empty((2, D), dtype=torch.float32, device=dev),
+                torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace)
+
+    dq, dk, dw, ws = _allocating(stream, make)
+    dqp, qlead, _, h, d, dqs = _rows(dq, "dq", dev)
+    dkp, klead, _, hk, dd, dks = _rows(dk, "dk", dev)
+    if (qlead, h, d) != (lead, Hq, D) or (klead, hk, dd) != (lead, Hkv, D):
+        raise ValueError("dq and dk must have the shapes of q and k")
+    dqw, dkw = dw[0], dw[1]
+    _run(load_library().attn_qk_norm_rope_bwd, "attn_qk_norm_rope_bwd", dev, stream,
+         _dense_rows(dq_out, "dq_out", lead, Hq, D, dev), _dense_rows(dk_out, "dk_out", lead, Hkv, D, dev), qp, kp, dqp, dkp,
+         dqw.data_ptr(), dkw.data_ptr(), wq, wk, pos, table, T, Hq, Hkv, D, rot, rows, qs, ks, dqs, dks, float(eps),
+         float(weight_offset), w32, int(bool(interleaved)), _ptr(ws), ws.numel() * ws.element_size())
+    return dq, dk, dqw, dkw
+
+
+def _caches(k_cache, v_cache, device, D):
+    import torch
+
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype != torch.bfloat16 or t.device != device or not t.is_contiguous() or t.dim() != 4 or t.shape[3] != D:
+            raise ValueError(f"{n} must be a contiguous bfloat16 tensor [num_pages, page_size, Hkv, {D}] on {device}")
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    return k_cache.shape[:3]
+
+
+def attn_qk_norm_rope_paged(q, k, v, q_weight, k_weight, positions, slots, cos_sin, k_cache, v_cache, q_out=None, *,
+                            eps: float = 1e-6, weight_offset: float = 0.0, interleaved: bool = False, stream=None):
+    """attn_qk_norm_rope for serving: returns q_out; k (normed and turned) and v go into the paged caches
+    [pages,16,Hkv,D] in place, each token at its slot (int32 [T], of attn_paged_plan; -1: padding)."""
+    import torch
+
+    qp, lead, T, Hq, D, qs = _rows(q, "q")
+    dev = q.device
+    kp, klead, _, Hkv, Dk, ks = _rows(k, "k", dev)
+    vp, vlead, _, Hv, Dv, vs = _rows(v, "v", dev)
+    if klead != lead or Dk != D or vlead != lead or (Hv, Dv) != (Hkv, D):
+        raise ValueError("q, k and v must have the same tokens and head size, k and v the same heads")
+    wq, wk, w32 = _norm_weights(q_weight, k_weight, D, dev)
+    pos, table, rot, rows = _angles(positions, cos_sin, lead, T, dev)
+    num_pages, page_size, Hc = _caches(k_cache, v_cache, dev, D)
+    if Hc != Hkv:
+        raise ValueError("the caches' heads are not k's")
+    if tuple(slots.shape) not in (tuple(lead), (T,)):
+        raise ValueError(f"slots must be an int32 tensor of shape {tuple(lead)}")
+    if q_out is None:
+        q_out = _allocating(stream, lambda: torch.empty((*lead, Hq, D), dtype=torch.bfloat16, device=dev))
+    _run(load_library().attn_qk_norm_rope_paged, "attn_qk_norm_rope_paged", dev, stream, qp, kp, vp,
+         _dense_rows(q_out, "q_out", lead, Hq, D, dev), k_cache.data_ptr(), v_cache.data_ptr(), wq, wk, pos,
+         _check_i32("slots", slots, tuple(slots.shape), dev), table, T, Hq, Hkv, D, rot, rows, page_size, num_pages, qs, ks,
+         vs, float(eps), float(weight_offset), w32, int(bool(interleaved)))
+    return q_out
+
+
+def attn_tree_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, tree_mask, max_q_len: int, o=None, lse=None, *,
+                    positions=None, window: int = 0, scale: float | None = None, workspace=None, stream=None):
+    """Attention of drafted token trees over a paged cache -> (o, lse[Hq,T]).
+
+    q [T,Hq,D]: the drafted tokens of all requests packed by cu_q int32 [R+1], the last of their
+    seq_lens int32 [R] cached tokens; tree_mask int32 [T, words]: bit d of a row (word d // 32) set where it
+    sees its request's drafted token d; every row sees the context before the drafted tokens, with
+    window > 0 only the keys less than `window` behind its position (positions int32 [T]).
+    """
+    import torch
+
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
+    T, Hq, D = q.shape
+    dev = _cuda_device(q, "q")
+    num_pages, page_size, Hkv = _caches(k_cache, v_cache, dev, D)
+    R = seq_lens.numel()
+    if block_table.dim() != 2 or tree_mask.dim() != 2:
+        raise ValueError("block_table must be [num_reqs, max_pages] and tree_mask [T, words]")
+    if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous() or tuple(lse.shape) != (Hq, T)):
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape {(Hq, T)} on {dev}")
+    need = attn_workspace_size(ATTN_OP_TREE_PAGED, Hq=Hq, Hkv=Hkv, S=int(max_q_len), D=D)
+
+    def make():
+        return (torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev) if o is None else o,
+                torch.empty((Hq, T), dtype=torch.float32, device=dev) if lse is None else lse,
+                torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None and need else workspace)
+
+    o, lse, ws = _allocating(stream, make)
+    _run(load_library().attn_tree_paged, "attn_tree_paged", dev, stream, _dense_rows(q, "q", (T,), Hq, D, dev),
+         k_cache.data_ptr(), v_cache.data_ptr(), _check_i32("block_table", block_table, (R, block_table.shape[1]), dev),
+         _check_i32("seq_lens", seq_lens, (R,), dev), _check_i32("cu_q", cu_q, (R + 1,), dev),
+         _check_i32("tree_mask", tree_mask, (T, tree_mask.shape[1]), dev),
+         None if positions is None else _check_i32("positions", positions, (T,), dev),
+         _dense_rows(o, "o", (T,), Hq, D, dev), lse.data_ptr(), R, T, int(max_q_len), tree_mask.shape[1], Hq, Hkv, D,
+         page_size, block_table.shape[1], num_pages, float(scale if scale is not None else 1.0 / math.sqrt(D)), int(window),
+         _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
     return o, lse

@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libattn_gb300.so")
 BUILD_DIR = os.path.join(HERE, "_build_tmp")
 SOURCES = ["api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd_small.cu", "decode_paged.cu", "decode_paged_noalloc.cu",
-           "merge_lse.cu"]
+           "merge_lse.cu", "paged_plan.cu", "qk_norm_rope.cu", "tree_paged.cu"]
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -192,6 +192,38 @@ bool make_decode_swz_map(CUtensorMap* m, const void* base, int D, int H, int num
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool head_dim_ok(int D) { return D == 64 || D == 128 || D == 256 || D == 512; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+size_t norm_rope_bwd_ws(int D) { return align256((size_t)attn::norm_rope_bwd_max_ctas() * 2 * D * 4); }
+
+bool tree_shape_ok(int Hq, int Hkv, int max_q, int D) {
+    return Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && Hq / Hkv <= 128 && Hkv <= 256 && max_q >= 0 && max_q <= 256 && head_dim_ok(D);
+}
+size_t tree_ws(int Hq, int Hkv, int max_q, int D) {
+    (void)Hq, (void)Hkv, (void)max_q, (void)D;
+    return 0;
+}
+
+// Arguments that the three head-norm calls share. `rows` with a T of zero need no pointers.
+int check_norm_rope(const attn::NormRopeLaunch& L) {
+    if (L.T < 0 || L.Hq < 1 || L.Hkv < 1 || L.rot < 0 || L.max_pos < 0) return ATTN_ERR_INVALID_ARG;
+    if (!(L.eps > 0.f) || !std::isfinite(L.eps) || !std::isfinite(L.weight_offset)) return ATTN_ERR_INVALID_ARG;
+    if (!head_dim_ok(L.D) || L.rot % 16 != 0 || L.rot > L.D || L.Hq > 2048 || L.Hkv > 2048 || L.T > (1 << 30))
+        return ATTN_ERR_UNSUPPORTED;
+    if (!aligned4(L.q_weight) || !aligned4(L.k_weight)) return ATTN_ERR_MISALIGNED;
+    if (L.T == 0) return ATTN_OK;
+    if (!L.q || !L.k || (L.rot > 0 && (!L.positions || !L.cos_sin))) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(L.q) || !aligned16(L.k) || (L.rot > 0 && (!aligned4(L.positions) || !aligned16(L.cos_sin))))
+        return ATTN_ERR_MISALIGNED;
+    return ATTN_OK;
+}
+// A token stride of H heads: 16-byte multiples; `out` rows must not overlap.
+int check_token_stride(long long stride, int H, int D, bool out) {
+    if (stride < 0 || (out && stride < (long long)H * D)) return ATTN_ERR_INVALID_ARG;
+    return stride % 8 ? ATTN_ERR_MISALIGNED : ATTN_OK;
+}
+
 int fwd_common(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_bf16* o, float* lse,
                const int32_t* cu, int nseq, int S, long long rows, int batch_dim, int Hq, int Hkv, int D, float scale,
                int window, void* stream) {
@@ -308,7 +340,7 @@ int attn_profile_stop(char* buf, size_t buf_bytes) {
 }
 
 
-int attn_version(void) { return 100; }
+int attn_version(void) { return 200; }
 
 const char* attn_status_string(int s) {
     switch (s) {
@@ -334,6 +366,8 @@ size_t attn_workspace_size(int op, int B, int Hq, int Hkv, int S, int D, int num
         case ATTN_OP_BWD:
         case ATTN_OP_BWD_VARLEN: return bwd_ws((long long)B * S, Hq, D);
         case ATTN_OP_DECODE_PAGED: return decode_ws(B, Hq, Hkv, D);
+        case ATTN_OP_QK_NORM_ROPE_BWD: return head_dim_ok(D) ? norm_rope_bwd_ws(D) : 0;
+        case ATTN_OP_TREE_PAGED: return tree_shape_ok(Hq, Hkv, S, D) ? tree_ws(Hq, Hkv, S, D) : 0;
         default: return 0;
     }
 }
@@ -509,6 +543,163 @@ int attn_merge_lse(const attn_bf16* o_parts, const float* lse_parts, attn_bf16* 
     L.o_parts = o_parts, L.lse_parts = lse_parts, L.o = o, L.lse = lse;
     L.P = num_parts, L.B = B, L.S = S, L.H = H, L.D = D, L.sms = dev->sms;
     return attn::launch_merge_lse(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+int attn_paged_plan(const int32_t* kv_lens, const int32_t* new_lens, const int32_t* pages_held,
+                    const int32_t* free_pages, const int32_t* free_used, int32_t* block_table, int32_t* seq_lens,
+                    int32_t* cu_q, int32_t* positions, int32_t* slots, int32_t* pages_held_out, int32_t* free_used_out,
+                    int32_t* admitted, int num_reqs, int total_new, int num_free, int page_size, int max_pages_per_seq,
+                    int num_pages, void* stream) {
+    if (num_reqs < 0 || total_new < 0 || num_free < 0 || page_size <= 0 || max_pages_per_seq < 0 || num_pages < 0)
+        return ATTN_ERR_INVALID_ARG;
+    if (page_size != 16 || num_reqs > 16384 || num_pages > (1 << 26) || total_new > (1 << 30) ||
+        max_pages_per_seq > (1 << 24))
+        return ATTN_ERR_UNSUPPORTED;
+    if (!free_used || !free_used_out || !admitted || !cu_q) return ATTN_ERR_INVALID_ARG;
+    if (num_reqs > 0 && (!kv_lens || !new_lens || !pages_held || !seq_lens || !pages_held_out)) return ATTN_ERR_INVALID_ARG;
+    if (num_reqs > 0 && max_pages_per_seq > 0 && !block_table) return ATTN_ERR_INVALID_ARG;
+    if ((total_new > 0 && (!positions || !slots)) || (num_free > 0 && !free_pages)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned4(kv_lens) || !aligned4(new_lens) || !aligned4(pages_held) || !aligned4(free_pages) || !aligned4(free_used) ||
+        !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(cu_q) || !aligned4(positions) || !aligned4(slots) ||
+        !aligned4(pages_held_out) || !aligned4(free_used_out) || !aligned4(admitted))
+        return ATTN_ERR_MISALIGNED;
+    const DeviceInfo* dev = device_info();
+    if (!dev) return ATTN_ERR_NO_DEVICE;
+    attn::PlanLaunch L;
+    L.kv_lens = kv_lens, L.new_lens = new_lens, L.held = pages_held, L.free_pages = free_pages, L.used = free_used;
+    L.table = block_table, L.seq_lens = seq_lens, L.cu_q = cu_q, L.positions = positions, L.slots = slots;
+    L.held_out = pages_held_out, L.used_out = free_used_out, L.admitted = admitted, L.status = dev->status;
+    L.R = num_reqs, L.T = total_new, L.F = num_free, L.max_pages = max_pages_per_seq, L.num_pages = num_pages;
+    L.sms = dev->sms;
+    L.in_place = seq_lens == kv_lens || pages_held_out == pages_held || free_used_out == free_used;
+    return attn::launch_paged_plan(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+int attn_qk_norm_rope(const attn_bf16* q, const attn_bf16* k, attn_bf16* q_out, attn_bf16* k_out, const void* q_weight,
+                      const void* k_weight, const int32_t* positions, const float* cos_sin, int T, int Hq, int Hkv,
+                      int D, int rot_dim, int max_pos, long long q_stride, long long k_stride, float eps,
+                      float weight_offset, int weight_fp32, int interleaved, void* stream) {
+    attn::NormRopeLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    L.q = q, L.k = k, L.q_out = q_out, L.k_out = k_out, L.q_weight = q_weight, L.k_weight = k_weight;
+    L.positions = positions, L.cos_sin = cos_sin, L.q_stride = q_stride, L.k_stride = k_stride;
+    L.T = T, L.Hq = Hq, L.Hkv = Hkv, L.D = D, L.rot = rot_dim, L.max_pos = max_pos;
+    L.eps = eps, L.weight_offset = weight_offset, L.weight_fp32 = weight_fp32 != 0, L.interleaved = interleaved != 0;
+    int st = check_norm_rope(L);
+    if (st) return st;
+    if ((st = check_token_stride(q_stride, Hq, D, false)) || (st = check_token_stride(k_stride, Hkv, D, false))) return st;
+    if (T == 0) return ATTN_OK;
+    if (!q_out || !k_out) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q_out) || !aligned16(k_out)) return ATTN_ERR_MISALIGNED;
+    if ((q_out == q && q_stride != (long long)Hq * D && T > 1) || (k_out == k && k_stride != (long long)Hkv * D && T > 1))
+        return ATTN_ERR_INVALID_ARG;  // in place only over contiguous rows
+    const DeviceInfo* dev = device_info();
+    if (!dev) return ATTN_ERR_NO_DEVICE;
+    L.status = dev->status, L.sms = dev->sms;
+    return attn::launch_norm_rope(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+int attn_qk_norm_rope_bwd(const attn_bf16* dq_out, const attn_bf16* dk_out, const attn_bf16* q, const attn_bf16* k,
+                          attn_bf16* dq, attn_bf16* dk, float* dq_weight, float* dk_weight, const void* q_weight,
+                          const void* k_weight, const int32_t* positions, const float* cos_sin, int T, int Hq, int Hkv,
+                          int D, int rot_dim, int max_pos, long long q_stride, long long k_stride, long long dq_stride,
+                          long long dk_stride, float eps, float weight_offset, int weight_fp32, int interleaved,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+    attn::NormRopeLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    L.dq_out = dq_out, L.dk_out = dk_out, L.q = q, L.k = k, L.dq = dq, L.dk = dk;
+    L.dq_weight = dq_weight, L.dk_weight = dk_weight, L.q_weight = q_weight, L.k_weight = k_weight;
+    L.positions = positions, L.cos_sin = cos_sin;
+    L.q_stride = q_stride, L.k_stride = k_stride, L.dq_stride = dq_stride, L.dk_stride = dk_stride;
+    L.T = T, L.Hq = Hq, L.Hkv = Hkv, L.D = D, L.rot = rot_dim, L.max_pos = max_pos;
+    L.eps = eps, L.weight_offset = weight_offset, L.weight_fp32 = weight_fp32 != 0, L.interleaved = interleaved != 0;
+    int st = check_norm_rope(L);
+    if (st) return st;
+    if ((st = check_token_stride(q_stride, Hq, D, false)) || (st = check_token_stride(k_stride, Hkv, D, false)) ||
+        (st = check_token_stride(dq_stride, Hq, D, true)) || (st = check_token_stride(dk_stride, Hkv, D, true)))
+        return st;
+    if (T > 0 && (!dq_out || !dk_out || !dq || !dk)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk) || !aligned4(dq_weight) ||
+        !aligned4(dk_weight))
+        return ATTN_ERR_MISALIGNED;
+    if (T > 1 && ((dq == dq_out && dq_stride != (long long)Hq * D) || (dk == dk_out && dk_stride != (long long)Hkv * D) ||
+                  (dq == q && dq_stride != q_stride) || (dk == k && dk_stride != k_stride)))
+        return ATTN_ERR_INVALID_ARG;  // in place only over the same rows
+    if (!workspace || workspace_bytes < norm_rope_bwd_ws(D)) return ATTN_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return ATTN_ERR_MISALIGNED;
+    const DeviceInfo* dev = device_info();
+    if (!dev) return ATTN_ERR_NO_DEVICE;
+    L.part = static_cast<float*>(workspace);
+    L.status = dev->status, L.sms = dev->sms;
+    return attn::launch_norm_rope_bwd(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+int attn_qk_norm_rope_paged(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_bf16* q_out,
+                            attn_bf16* k_cache, attn_bf16* v_cache, const void* q_weight, const void* k_weight,
+                            const int32_t* positions, const int32_t* slots, const float* cos_sin, int T, int Hq, int Hkv,
+                            int D, int rot_dim, int max_pos, int page_size, int num_pages, long long q_stride,
+                            long long k_stride, long long v_stride, float eps, float weight_offset, int weight_fp32,
+                            int interleaved, void* stream) {
+    attn::NormRopeLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    L.q = q, L.k = k, L.v = v, L.q_out = q_out, L.k_out = k_cache, L.v_out = v_cache;
+    L.q_weight = q_weight, L.k_weight = k_weight, L.positions = positions, L.slots = slots, L.cos_sin = cos_sin;
+    L.q_stride = q_stride, L.k_stride = k_stride, L.v_stride = v_stride;
+    L.T = T, L.Hq = Hq, L.Hkv = Hkv, L.D = D, L.rot = rot_dim, L.max_pos = max_pos;
+    L.eps = eps, L.weight_offset = weight_offset, L.weight_fp32 = weight_fp32 != 0, L.interleaved = interleaved != 0;
+    int st = check_norm_rope(L);
+    if (st) return st;
+    if (page_size <= 0 || num_pages < 0) return ATTN_ERR_INVALID_ARG;
+    if (page_size != 16 || num_pages > (1 << 26)) return ATTN_ERR_UNSUPPORTED;
+    if ((st = check_token_stride(q_stride, Hq, D, false)) || (st = check_token_stride(k_stride, Hkv, D, false)) ||
+        (st = check_token_stride(v_stride, Hkv, D, false)))
+        return st;
+    if (T == 0) return ATTN_OK;
+    if (!v || !slots || !q_out || !k_cache || !v_cache) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(v) || !aligned4(slots) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache))
+        return ATTN_ERR_MISALIGNED;
+    if (q_out == q && q_stride != (long long)Hq * D && T > 1) return ATTN_ERR_INVALID_ARG;
+    const DeviceInfo* dev = device_info();
+    if (!dev) return ATTN_ERR_NO_DEVICE;
+    L.num_slots = num_pages * 16;
+    L.status = dev->status, L.sms = dev->sms;
+    return attn::launch_norm_rope_paged(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+int attn_tree_paged(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache, const int32_t* block_table,
+                    const int32_t* seq_lens, const int32_t* cu_q, const int32_t* tree_mask, const int32_t* positions,
+                    attn_bf16* o, float* lse, int num_reqs, int total_q, int max_q_len, int mask_words, int Hq, int Hkv,
+                    int D, int page_size, int max_pages_per_seq, int num_pages, float scale, int window, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    if (num_reqs < 0 || total_q < 0 || max_q_len < 0 || mask_words < 0 || max_pages_per_seq < 0 || num_pages < 0 ||
+        page_size <= 0)
+        return ATTN_ERR_INVALID_ARG;
+    int st = check_common(Hq, Hkv, scale, 1, window);
+    if (st) return st;
+    if (!tree_shape_ok(Hq, Hkv, max_q_len, D) || page_size != 16 || mask_words > 8 || num_reqs > 4096 ||
+        max_pages_per_seq > (1 << 24) || num_pages > (1 << 26))
+        return ATTN_ERR_UNSUPPORTED;
+    if (mask_words * 32 < max_q_len) return ATTN_ERR_INVALID_ARG;
+    if (num_reqs == 0 || total_q == 0 || max_q_len == 0) return ATTN_OK;  // nothing to read or write
+    if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !cu_q || !tree_mask || !o || !lse ||
+        (window > 0 && !positions))
+        return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(lse) ||
+        !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(cu_q) || !aligned4(tree_mask) || !aligned4(positions))
+        return ATTN_ERR_MISALIGNED;
+    if (num_pages == 0 || max_pages_per_seq == 0) return ATTN_ERR_INVALID_ARG;  // drafted tokens need cached pages
+    const size_t need = tree_ws(Hq, Hkv, max_q_len, D);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
+    if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return ATTN_ERR_MISALIGNED;
+    const DeviceInfo* dev = device_info();
+    if (!dev) return ATTN_ERR_NO_DEVICE;
+    attn::TreeLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    L.q = q, L.k_cache = k_cache, L.v_cache = v_cache, L.block_table = block_table, L.seq_lens = seq_lens, L.cu_q = cu_q;
+    L.mask = tree_mask, L.positions = positions, L.o = o, L.lse = lse, L.status = dev->status;
+    L.R = num_reqs, L.T = total_q, L.max_q = max_q_len, L.words = mask_words, L.Hq = Hq, L.Hkv = Hkv, L.D = D;
+    L.max_pages = max_pages_per_seq, L.num_pages = num_pages, L.window = window, L.sms = dev->sms, L.scale = scale;
+    return attn::launch_tree_paged(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 int attn_selftest_wait_timeout(int limit_ms, void* stream) {

@@ -96,4 +96,49 @@ struct MergeLaunch {
 };
 cudaError_t launch_merge_lse(const MergeLaunch& L, cudaStream_t stream);
 
+// ---- plan of a step over a paged cache ------------------------------------------------------
+struct PlanLaunch {
+    const int32_t *kv_lens, *new_lens, *held, *free_pages, *used;  // used: one value
+    int32_t *table;                                                // [R, max_pages]
+    int32_t *seq_lens, *cu_q, *positions, *slots, *held_out, *used_out, *admitted;
+    unsigned* status;
+    int R, T, F, max_pages, num_pages, sms;
+    bool in_place;  // seq_lens / held_out / used_out is kv_lens / held / used
+};
+cudaError_t launch_paged_plan(const PlanLaunch& L, cudaStream_t stream);
+
+// ---- head norm with rotary position encoding -------------------------------------------------
+struct NormRopeLaunch {
+    const uint16_t *q, *k, *v;          // rows [T] of H x D, token strides below
+    const uint16_t *dq_out, *dk_out;    // gradient: of the results, contiguous
+    uint16_t *q_out, *k_out, *v_out;    // contiguous; paged: k_out / v_out are the caches
+    uint16_t *dq, *dk;                  // gradient: token strides below
+    const void *q_weight, *k_weight;    // [D] bf16 or fp32, or null
+    float *dq_weight, *dk_weight;       // [D] fp32
+    float* part;                        // gradient: [CTAs][2][D]
+    const int32_t *positions, *slots;   // slots: paged only
+    const float* cos_sin;               // [max_pos, rot]: cos | sin
+    unsigned* status;
+    long long q_stride, k_stride, v_stride, dq_stride, dk_stride;  // elements
+    int T, Hq, Hkv, D, rot, max_pos, num_slots, sms;
+    float eps, weight_offset;
+    bool weight_fp32, interleaved;
+};
+int norm_rope_bwd_max_ctas();  // CTAs of the gradient kernel at most
+cudaError_t launch_norm_rope(const NormRopeLaunch& L, cudaStream_t stream);
+cudaError_t launch_norm_rope_paged(const NormRopeLaunch& L, cudaStream_t stream);
+cudaError_t launch_norm_rope_bwd(const NormRopeLaunch& L, cudaStream_t stream);
+
+// ---- attention of drafted token trees over a paged cache --------------------------------------
+struct TreeLaunch {
+    const uint16_t *q, *k_cache, *v_cache;
+    const int32_t *block_table, *seq_lens, *cu_q, *mask, *positions;
+    uint16_t* o;
+    float* lse;
+    unsigned* status;
+    int R, T, max_q, words, Hq, Hkv, D, max_pages, num_pages, window, sms;
+    float scale;
+};
+cudaError_t launch_tree_paged(const TreeLaunch& L, cudaStream_t stream);
+
 }  // namespace attn

@@ -1,0 +1,188 @@
+// The plan of one step over a paged cache, made on the GPU from the requests' lengths: which pages each
+// request takes, and for every new token its position, its cache slot and its row.
+//
+// With kv_b cached tokens, n_b new ones and held_b pages in the block table, request b needs
+//     need_b = max(0, ceil((kv_b + n_b) / 16) - held_b)
+// more pages. Requests are admitted in order up to the first one whose tokens would pass the T rows or
+// whose pages would pass the F free ones; from there on nothing is taken (n_b = need_b = 0). Then
+//     cu_q = exclusive prefix sum of n,   off = exclusive prefix sum of need,
+//     table[b, held_b + i] = free[used + off_b + i]           for i < need_b,
+//     row cu_q[b] + i: position kv_b + i, slot = table[b, position / 16] * 16 + position % 16.
+//
+// There is next to nothing to move (24 bytes a request, 8 a token, 8 a page taken), so the call is bound
+// by latency: one launch, and no value passes from one CTA to another. Every CTA scans all requests
+// itself into shared memory (R <= 16384: two prefix sums of 64 KB) and then fills its share of the rows
+// and pages, finding the request of a row by bisection of the prefix sums. A new page's id is read from
+// the free list, not from the table, so no row waits for another thread's table entry.
+//
+// The lengths, held pages and the free list's cursor may be updated in place: the CTAs are then one
+// cluster, and all of them have read the old state before the first writes the new (a cluster barrier).
+// Otherwise the grid is as wide as the rows need.
+#include <cuda_runtime.h>
+
+#include "attn_internal.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCluster = 8;
+constexpr int kPage = 16;
+
+// What request b asks for; an inconsistent one asks for nothing.
+struct Ask {
+    int n, need;
+    bool bad;
+};
+__device__ __forceinline__ Ask ask_of(const PlanLaunch& a, int b) {
+    const int kv = a.kv_lens[b], n = a.new_lens[b], held = a.held[b];
+    const long long cap = (long long)a.max_pages * kPage;
+    if (kv < 0 || n < 0 || held < 0 || held > a.max_pages || kv > (long long)held * kPage || (long long)kv + n > cap)
+        return {0, 0, true};
+    const int pages = (int)(((long long)kv + n + kPage - 1) / kPage);
+    return {n, pages > held ? pages - held : 0, false};
+}
+
+// Largest b with first[b] <= x, over first[0 .. count).
+__device__ __forceinline__ int owner(const int* first, int count, int x) {
+    int lo = 0, hi = count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+template <bool IN_PLACE>
+__global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_constant__ PlanLaunch a) {
+    extern __shared__ int prefix[];
+    const int R = a.R;
+    int* cu = prefix;           // [R + 1] tokens before request b
+    int* off = prefix + R + 1;  // [R + 1] pages taken before request b
+    __shared__ long long warp_n[kWarps], warp_p[kWarps];
+    __shared__ int first_out;  // first request that is not admitted
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int used = *a.used;
+    const bool used_ok = used >= 0 && used <= a.F;
+    const long long room = used_ok ? a.F - used : 0;
+    if (tid == 0) first_out = R;
+
+    // each thread's run of requests, then the scan of the threads' sums (64 bits: lengths are not trusted)
+    const int per = (R + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, R), b1 = min(b0 + per, R);
+    long long sn = 0, sp = 0;
+    bool bad = !used_ok;
+    for (int b = b0; b < b1; ++b) {
+        const Ask k = ask_of(a, b);
+        sn += k.n, sp += k.need;
+        bad |= k.bad;
+    }
+    long long xn = sn, xp = sp;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long yn = __shfl_up_sync(0xffffffffu, xn, d), yp = __shfl_up_sync(0xffffffffu, xp, d);
+        if (lane >= d) xn += yn, xp += yp;
+    }
+    if (lane == 31) warp_n[warp] = xn, warp_p[warp] = xp;
+    __syncthreads();
+    xn -= sn, xp -= sp;
+    for (int w = 0; w < warp; ++w) xn += warp_n[w], xp += warp_p[w];
+    const int big = 0x7fffffff;
+    for (int b = b0; b < b1; ++b) {
+        const Ask k = ask_of(a, b);
+        cu[b] = (int)min(xn, (long long)big), off[b] = (int)min(xp, (long long)big);
+        xn += k.n, xp += k.need;
+        if (xn > a.T || xp > room) {
+            atomicMin(&first_out, b);
+            bad = true;
+            // the sums only grow: the rest of this run is not admitted either
+            for (int i = b + 1; i < b1; ++i) cu[i] = off[i] = big;
+            break;
+        }
+    }
+    if (tid == kThreads - 1) cu[R] = (int)min(xn, (long long)big), off[R] = (int)min(xp, (long long)big);
+    if (bad) atomicOr(a.status, DEVSTAT_BOUNDS);
+    __syncthreads();
+    const int adm = first_out;  // requests 0 .. adm - 1 are served
+    const int tokens = cu[adm], pages = off[adm];
+
+    const int gtid = blockIdx.x * kThreads + tid, gsize = gridDim.x * kThreads;
+    auto checked = [&](int page) -> int {
+        if (page >= 0 && page < a.num_pages) return page;
+        atomicOr(a.status, DEVSTAT_BOUNDS);
+        return -1;
+    };
+    // pages taken -> block table
+    for (int i = gtid; i < pages; i += gsize) {
+        const int b = owner(off, adm, i);
+        a.table[(size_t)b * a.max_pages + a.held[b] + (i - off[b])] = checked(a.free_pages[used + i]);
+    }
+    // rows
+    for (int t = gtid; t < a.T; t += gsize) {
+        int pos = 0, slot = -1;
+        if (t < tokens) {
+            const int b = owner(cu, adm, t);
+            pos = a.kv_lens[b] + (t - cu[b]);
+            const int p = pos / kPage, held = a.held[b];
+            const int page = checked(p < held ? a.table[(size_t)b * a.max_pages + p] : a.free_pages[used + off[b] + p - held]);
+            if (page >= 0) slot = page * kPage + pos % kPage;
+        }
+        a.positions[t] = pos;
+        a.slots[t] = slot;
+    }
+    // the new state
+    if (IN_PLACE) cluster_sync_all();  // every CTA of the grid has read the old one
+    for (int b = gtid; b < R; b += gsize) {
+        const bool in = b < adm;
+        // in place, another thread of the grid never writes request b: its old state is still there
+        const int kv = a.kv_lens[b], held = a.held[b];
+        a.cu_q[b] = in ? cu[b] : tokens;
+        a.seq_lens[b] = in ? kv + (cu[b + 1] - cu[b]) : kv;
+        a.held_out[b] = in ? held + (off[b + 1] - off[b]) : held;
+    }
+    if (gtid == 0) {
+        a.cu_q[R] = tokens;
+        *a.used_out = used + pages;
+        *a.admitted = adm;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_plan(const PlanLaunch& L, cudaStream_t stream) {
+    const size_t smem = (size_t)(L.R + 1) * 2 * sizeof(int);
+    const long long items = (long long)L.T > L.R ? L.T : L.R;
+    const long long want = (items + kThreads - 1) / kThreads;
+    const ProfMark m = prof_begin(stream, "paged_plan");
+    cudaError_t e;
+    if (L.in_place) {
+        e = cudaFuncSetAttribute(paged_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = want < kCluster ? (unsigned)(want < 1 ? 1 : want) : kCluster;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(attr[0].val.clusterDim.x);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, paged_plan_kernel<true>, L);
+    } else {
+        e = cudaFuncSetAttribute(paged_plan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        const int grid = (int)(want < 1 ? 1 : want < L.sms ? want : L.sms);
+        paged_plan_kernel<false><<<grid, kThreads, smem, stream>>>(L);
+        e = cudaSuccess;
+    }
+    prof_end(stream, m);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace attn

@@ -1,0 +1,384 @@
+// RMS norm of every query and key head with the rotary position encoding in the same pass: the
+// step between the projections and the attention kernels, forward, gradient, and the serving form
+// that writes K and V straight into the paged cache.
+//
+// Per row x (one head of one token, D values) with weight v = offset + w, r = rsqrt(mean(x^2) + eps):
+//     xh = r x,   n = v xh,   y = R n
+// R turns the pairs of the first `rot` dims by the token's angles (cos and sin from a table of the
+// caller's): (a, b) -> (a cos - b sin, b cos + a sin), pairs (i, i + rot/2) or, interleaved,
+// (2i, 2i + 1). The gradient, for dy:
+//     dn = R^T dy,   dw = sum over rows of dn xh,   g = v dn,   dx = r (g - xh mean(g xh))
+// All of it is evaluated in fp32 from the bf16 inputs; the results round once to bf16 (dw stays fp32).
+//
+// Memory bound: a row is read once and written once (gradient: x and dy in, dx out). A thread owns
+// 16 dims of a row as two 16-byte chunks chosen so that both members of every rotated pair are its
+// own: chunks (j, j + rot/16) for j < rot/16, else (2j, 2j + 1); interleaved, always (2j, 2j + 1).
+// Either way its angles are 8j .. 8j + 7. D / 16 lanes share a row, so a warp takes 512 / D rows at a
+// time and the only exchange is the butterfly sum of a row's lanes. A task is one token's block of
+// kU such passes, all queries or all keys; a warp keeps its block and walks the tokens, so the norm
+// weights (and, in the gradient, their sums) stay in registers and a token's angles are loaded once
+// for kU passes. All loads of a task are issued before the first is used.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "attn_internal.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUF = 4;  // passes per task, forward
+constexpr int kUB = 2;  // passes per task, gradient (two streams in)
+constexpr int kMaxCtas = 1024;  // sizes the gradient's workspace
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[16], int at) {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x[at + 2 * e] = __uint_as_float(v[e] << 16);
+        x[at + 2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[16], int at) {
+    uint4 w;
+    w.x = pack_bf16x2(x[at], x[at + 1]), w.y = pack_bf16x2(x[at + 2], x[at + 3]);
+    w.z = pack_bf16x2(x[at + 4], x[at + 5]), w.w = pack_bf16x2(x[at + 6], x[at + 7]);
+    return w;
+}
+
+// Sum over the LPR lanes that share a row.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+    for (int off = LPR / 2; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// The rotation of a thread's 16 dims (sin negated: its transpose).
+__device__ __forceinline__ void turn(float (&x)[16], const float (&c)[8], const float (&s)[8], bool inter) {
+    if (inter) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float a = x[2 * e], b = x[2 * e + 1];
+            x[2 * e] = a * c[e] - b * s[e], x[2 * e + 1] = b * c[e] + a * s[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float a = x[e], b = x[8 + e];
+            x[e] = a * c[e] - b * s[e], x[8 + e] = b * c[e] + a * s[e];
+        }
+    }
+}
+
+// What a warp works on: block `blk` of every token it walks.
+struct Block {
+    int kind;   // 0: queries, 1: keys, 2: values (paged form)
+    int head0;  // first head
+    int heads;  // heads of that kind
+};
+template <int RPT>  // rows (heads) per task
+__device__ __forceinline__ Block block_of(int blk, int Hq, int Hkv) {
+    const int nq = (Hq + RPT - 1) / RPT, nk = (Hkv + RPT - 1) / RPT;
+    if (blk < nq) return {0, blk * RPT, Hq};
+    if (blk < nq + nk) return {1, (blk - nq) * RPT, Hkv};
+    return {2, (blk - nq - nk) * RPT, Hkv};
+}
+
+// A thread's 16 effective weights, offset + w (1 without weights).
+__device__ __forceinline__ void load_weights(const NormRopeLaunch& a, const void* w, int c0, int c1, float (&v)[16]) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const int d = (e < 8 ? 8 * c0 : 8 * c1) + (e & 7);
+        if (!w) v[e] = 1.f;
+        else if (a.weight_fp32) v[e] = a.weight_offset + static_cast<const float*>(w)[d];
+        else v[e] = a.weight_offset + __uint_as_float((uint32_t) static_cast<const uint16_t*>(w)[d] << 16);
+    }
+}
+
+__device__ __forceinline__ void load_angles(const NormRopeLaunch& a, int pos, int j, float (&c)[8], float (&s)[8]) {
+    const float* row = a.cos_sin + (size_t)pos * a.rot + 8 * j;
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(row + e));
+        const float4 y = __ldg(reinterpret_cast<const float4*>(row + a.rot / 2 + e));
+        c[e] = x.x, c[e + 1] = x.y, c[e + 2] = x.z, c[e + 3] = x.w;
+        s[e] = y.x, s[e + 1] = y.y, s[e + 2] = y.z, s[e + 3] = y.w;
+    }
+}
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeLaunch a) {
+    constexpr int LPR = D / 16, RPW = 32 / LPR, RPT = RPW * kUF;
+    const int lane = threadIdx.x & 31, j = lane % LPR, sub = lane / LPR;
+    const int nblk = (a.Hq + RPT - 1) / RPT + (PAGED ? 2 : 1) * ((a.Hkv + RPT - 1) / RPT);
+    const int warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int lanes = gridDim.x * kWarps / nblk;  // token lanes: a warp takes tokens warp / nblk + i * lanes
+    if (warp >= lanes * nblk) return;
+    const Block b = block_of<RPT>(warp % nblk, a.Hq, a.Hkv);
+    const int rc = a.rot / 16;  // lanes whose dims are rotated
+    const bool rotated = j < rc;
+    const int c0 = rotated && !a.interleaved ? j : 2 * j, c1 = rotated && !a.interleaved ? j + rc : 2 * j + 1;
+    float v[16];
+    if (b.kind < 2) load_weights(a, b.kind == 0 ? a.q_weight : a.k_weight, c0, c1, v);
+    const uint16_t* src = b.kind == 0 ? a.q : b.kind == 1 ? a.k : a.v;
+    const long long stride = b.kind == 0 ? a.q_stride : b.kind == 1 ? a.k_stride : a.v_stride;
+    uint16_t* dst = b.kind == 0 ? a.q_out : b.kind == 1 ? a.k_out : a.v_out;
+
+    for (int t = warp / nblk; t < a.T; t += lanes) {
+        long long orow = t;  // output row: the token, or its cache slot
+        if (PAGED) {
+            const int slot = a.slots[t];
+            if (slot == -1) continue;  // a padding row
+            if (slot < 0 || slot >= a.num_slots) {
+                if (lane == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
+                continue;
+            }
+            if (b.kind) orow = slot;
+        }
+        uint4 raw[kUF][2];
+#pragma unroll
+        for (int u = 0; u < kUF; ++u) {
+            const int h = b.head0 + u * RPW + sub;
+            if (h < b.heads) {
+                const uint16_t* row = src + (size_t)t * stride + (size_t)h * D;
+                raw[u][0] = *reinterpret_cast<const uint4*>(row + 8 * c0);
+                raw[u][1] = *reinterpret_cast<const uint4*>(row + 8 * c1);
+            } else {
+                raw[u][0] = raw[u][1] = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        float c[8], s[8];
+        if (a.rot > 0) {
+            const int pos = a.positions[t];
+            if (pos < 0 || pos >= a.max_pos) {
+                if (lane == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
+                continue;
+            }
+            if (rotated && b.kind < 2) load_angles(a, pos, j, c, s);
+        }
+#pragma unroll
+        for (int u = 0; u < kUF; ++u) {
+            const int h = b.head0 + u * RPW + sub;
+            if (b.kind < 2) {
+                float x[16];
+                unpack8(raw[u][0], x, 0);
+                unpack8(raw[u][1], x, 8);
+                float ss = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+                const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = x[e] * r * v[e];
+                if (rotated) turn(x, c, s, a.interleaved);
+                raw[u][0] = pack8(x, 0);
+                raw[u][1] = pack8(x, 8);
+            }
+            if (h < b.heads) {
+                uint16_t* row = dst + ((size_t)orow * b.heads + h) * D;
+                *reinterpret_cast<uint4*>(row + 8 * c0) = raw[u][0];
+                *reinterpret_cast<uint4*>(row + 8 * c1) = raw[u][1];
+            }
+        }
+    }
+}
+
+// The gradient. Each CTA leaves its sums of dn xh in part[CTA][query | key][D], in an order of its own
+// that depends on the launch alone; norm_rope_dw_kernel adds them up.
+template <int D>
+__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeLaunch a) {
+    constexpr int LPR = D / 16, RPW = 32 / LPR, RPT = RPW * kUB;
+    const int lane = threadIdx.x & 31, j = lane % LPR, sub = lane / LPR, wid = threadIdx.x >> 5;
+    const int nblk = (a.Hq + RPT - 1) / RPT + (a.Hkv + RPT - 1) / RPT;
+    const int warp = blockIdx.x * kWarps + wid;
+    const int lanes = gridDim.x * kWarps / nblk;
+    const bool works = warp < lanes * nblk;
+    const Block b = block_of<RPT>(warp % nblk, a.Hq, a.Hkv);
+    const int rc = a.rot / 16;
+    const bool rotated = j < rc;
+    const int c0 = rotated && !a.interleaved ? j : 2 * j, c1 = rotated && !a.interleaved ? j + rc : 2 * j + 1;
+    float v[16], dw[16];
+    load_weights(a, b.kind == 0 ? a.q_weight : a.k_weight, c0, c1, v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) dw[e] = 0.f;
+    const uint16_t* src = b.kind == 0 ? a.q : a.k;
+    const uint16_t* gsrc = b.kind == 0 ? a.dq_out : a.dk_out;
+    const long long stride = b.kind == 0 ? a.q_stride : a.k_stride;
+    const long long ostride = b.kind == 0 ? a.dq_stride : a.dk_stride;
+    uint16_t* dst = b.kind == 0 ? a.dq : a.dk;
+
+    for (int t = warp / nblk; works && t < a.T; t += lanes) {
+        uint4 xr[kUB][2], gr[kUB][2];
+#pragma unroll
+        for (int u = 0; u < kUB; ++u) {
+            const int h = b.head0 + u * RPW + sub;
+            xr[u][0] = xr[u][1] = gr[u][0] = gr[u][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (h < b.heads) {
+                const uint16_t* row = src + (size_t)t * stride + (size_t)h * D;
+                const uint16_t* grow = gsrc + ((size_t)t * b.heads + h) * D;
+                xr[u][0] = *reinterpret_cast<const uint4*>(row + 8 * c0);
+                xr[u][1] = *reinterpret_cast<const uint4*>(row + 8 * c1);
+                gr[u][0] = *reinterpret_cast<const uint4*>(grow + 8 * c0);
+                gr[u][1] = *reinterpret_cast<const uint4*>(grow + 8 * c1);
+            }
+        }
+        float c[8], s[8];
+        if (a.rot > 0) {
+            const int pos = a.positions[t];
+            if (pos < 0 || pos >= a.max_pos) {
+                if (lane == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
+                continue;
+            }
+            if (rotated) {
+                load_angles(a, pos, j, c, s);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] = -s[e];  // the transpose
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUB; ++u) {
+            const int h = b.head0 + u * RPW + sub;
+            float x[16], g[16];
+            unpack8(xr[u][0], x, 0);
+            unpack8(xr[u][1], x, 8);
+            unpack8(gr[u][0], g, 0);
+            unpack8(gr[u][1], g, 8);
+            if (rotated) turn(g, c, s, a.interleaved);  // dn
+            float ss = 0.f, sg = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                ss = fmaf(x[e], x[e], ss);
+                sg = fmaf(g[e] * v[e], x[e], sg);
+            }
+            const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
+            const float m = row_sum<LPR>(sg) * (1.f / D) * r;  // mean(g xh)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float xh = x[e] * r;
+                dw[e] = fmaf(g[e], xh, dw[e]);
+                x[e] = r * (g[e] * v[e] - xh * m);
+            }
+            if (h < b.heads) {
+                uint16_t* row = dst + (size_t)t * ostride + (size_t)h * D;
+                *reinterpret_cast<uint4*>(row + 8 * c0) = pack8(x, 0);
+                *reinterpret_cast<uint4*>(row + 8 * c1) = pack8(x, 8);
+            }
+        }
+    }
+    // the warp's row groups, then the CTA's warps, in order
+    __shared__ float sums[kWarps][D];
+    __shared__ int kinds[kWarps];
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+#pragma unroll
+        for (int off = LPR; off < 32; off <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], off);
+    if (sub == 0) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sums[wid][(e < 8 ? 8 * c0 : 8 * c1) + (e & 7)] = dw[e];
+    }
+    if (lane == 0) kinds[wid] = works ? b.kind : -1;
+    __syncthreads();
+    float* part = a.part + (size_t)blockIdx.x * 2 * D;
+    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+        float acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            if (kinds[w] == i / D) acc += sums[w][i % D];
+        part[i] = acc;
+    }
+}
+
+// dw[i] = sum over the CTAs of part[CTA][i]: 32 columns a CTA, its warps take every kDwWarps-th partial.
+constexpr int kDwWarps = 16;
+__global__ void __launch_bounds__(kDwWarps * 32) norm_rope_dw_kernel(const float* part, float* dqw, float* dkw, int D, int n) {
+    __shared__ float acc[kDwWarps][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    float x = 0.f;
+    for (int i = w; i < n; i += kDwWarps) x += part[(size_t)i * 2 * D + col];
+    acc[w][lane] = x;
+    __syncthreads();
+    if (w == 0) {
+        x = 0.f;
+#pragma unroll
+        for (int i = 0; i < kDwWarps; ++i) x += acc[i][lane];
+        float* out = col < D ? dqw : dkw;
+        if (out) out[col < D ? col : col - D] = x;
+    }
+}
+
+// CTAs for `tasks` warp tasks: enough for all of them at once, at most `per_sm` per SM, and at least one
+// warp for each block of a token.
+int norm_grid(long long T, int nblk, int sms, int per_sm) {
+    const long long want = (T * nblk + kWarps - 1) / kWarps, least = (nblk + kWarps - 1) / kWarps;
+    long long g = (long long)sms * per_sm;
+    if (want < g) g = want;
+    if (g > kMaxCtas) g = kMaxCtas;
+    if (g < least) g = least;  // at most 2048 heads of each kind: 4096 / kWarps
+    return (int)g;
+}
+
+constexpr int kFwdPerSm = 4, kBwdPerSm = 4;
+
+template <int D, bool PAGED>
+cudaError_t launch_fwd_d(const NormRopeLaunch& L, cudaStream_t stream) {
+    constexpr int RPT = 512 / D * kUF;
+    const int nblk = (L.Hq + RPT - 1) / RPT + (PAGED ? 2 : 1) * ((L.Hkv + RPT - 1) / RPT);
+    const ProfMark m = prof_begin(stream, PAGED ? "qk_norm_rope_paged" : "qk_norm_rope");
+    norm_rope_kernel<D, PAGED><<<norm_grid(L.T, nblk, L.sms, kFwdPerSm), kThreads, 0, stream>>>(L);
+    prof_end(stream, m);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_bwd_d(const NormRopeLaunch& L, cudaStream_t stream) {
+    constexpr int RPT = 512 / D * kUB;
+    const int nblk = (L.Hq + RPT - 1) / RPT + (L.Hkv + RPT - 1) / RPT;
+    const int grid = norm_grid(L.T, nblk, L.sms, kBwdPerSm);
+    ProfMark m = prof_begin(stream, "qk_norm_rope_bwd");
+    norm_rope_bwd_kernel<D><<<grid, kThreads, 0, stream>>>(L);
+    prof_end(stream, m);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    m = prof_begin(stream, "qk_norm_rope_dw");
+    norm_rope_dw_kernel<<<2 * D / 32, kDwWarps * 32, 0, stream>>>(L.part, L.dq_weight, L.dk_weight, D, grid);
+    prof_end(stream, m);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int norm_rope_bwd_max_ctas() { return kMaxCtas; }
+
+cudaError_t launch_norm_rope(const NormRopeLaunch& L, cudaStream_t stream) {
+    switch (L.D) {
+        case 64: return launch_fwd_d<64, false>(L, stream);
+        case 128: return launch_fwd_d<128, false>(L, stream);
+        case 256: return launch_fwd_d<256, false>(L, stream);
+        case 512: return launch_fwd_d<512, false>(L, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_norm_rope_paged(const NormRopeLaunch& L, cudaStream_t stream) {
+    switch (L.D) {
+        case 64: return launch_fwd_d<64, true>(L, stream);
+        case 128: return launch_fwd_d<128, true>(L, stream);
+        case 256: return launch_fwd_d<256, true>(L, stream);
+        case 512: return launch_fwd_d<512, true>(L, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_norm_rope_bwd(const NormRopeLaunch& L, cudaStream_t stream) {
+    switch (L.D) {
+        case 64: return launch_bwd_d<64>(L, stream);
+        case 128: return launch_bwd_d<128>(L, stream);
+        case 256: return launch_bwd_d<256>(L, stream);
+        case 512: return launch_bwd_d<512>(L, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace attn

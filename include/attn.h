@@ -36,8 +36,8 @@
  *    exceeded its time limit) do not trap: the kernel records a flag and finishes,
  *    and attn_get_device_status() reports it.
  *  - Supported shapes: D in {64, 128, 256, 512} for prefill / backward, D in {128, 256} for
- *    decode, D in {64, 128, 256, 512} for the merge; Hq % Hkv == 0, causal = 1. bf16 values
- *    are passed as raw 16-bit patterns.
+ *    decode, D in {64, 128, 256, 512} for the merge, the head norm and the tree attention;
+ *    Hq % Hkv == 0, causal = 1. bf16 values are passed as raw 16-bit patterns.
  */
 #ifndef ATTN_GB300_ATTN_H
 #define ATTN_GB300_ATTN_H
@@ -75,7 +75,9 @@ enum {
     ATTN_OP_FWD_VARLEN = 1,
     ATTN_OP_BWD = 2,
     ATTN_OP_BWD_VARLEN = 3,
-    ATTN_OP_DECODE_PAGED = 4
+    ATTN_OP_DECODE_PAGED = 4,
+    ATTN_OP_QK_NORM_ROPE_BWD = 5,
+    ATTN_OP_TREE_PAGED = 6
 };
 
 /*
@@ -249,9 +251,141 @@ ATTN_API int attn_merge_lse(const attn_bf16* o_parts, const float* lse_parts, at
                             int B, int S, int H, int D, void* stream);
 
 /*
+ * attn_paged_plan -- the plan of one serving step over a paged cache, made on the GPU from the
+ * requests' lengths: the pages every request takes and, for every new token, its position, its
+ * cache slot and its row. Its outputs are what attn_qk_norm_rope_paged, attn_fwd_paged,
+ * attn_tree_paged and attn_decode_paged read.
+ *   kv_lens, new_lens, pages_held int32 [num_reqs]: tokens request b has cached, tokens it adds,
+ *   pages already in its block-table row (they may be more than its cached tokens need: the
+ *   pages of rejected drafts). free_pages int32 [num_free]: page ids that may be handed out, in
+ *   order; free_used int32 [1]: how many of them are already taken.
+ *   block_table int32 [num_reqs, max_pages_per_seq], updated in place: entries
+ *   pages_held[b] .. of request b get the pages it takes, ceil((kv + new) / 16) - pages_held[b]
+ *   of them if that is positive; no other entry is written.
+ *   seq_lens [num_reqs] = kv + new; cu_q [num_reqs + 1]: exclusive prefix sum of the new tokens;
+ *   positions, slots [total_new]: row cu_q[b] + i has position kv_lens[b] + i and slot
+ *   page * 16 + position % 16 of the page that holds it; rows past cu_q[num_reqs] get position 0
+ *   and slot -1. pages_held_out [num_reqs] and free_used_out [1]: the state after the step.
+ *   admitted [1]: requests served. Requests are admitted in order, up to the first whose tokens
+ *   would pass total_new rows or whose pages would pass num_free; from that one on (all of it
+ *   reported as ATTN_ERR_DEVICE_BOUNDS) requests get no rows and no pages: an empty cu_q slice,
+ *   seq_lens = kv_lens. So does a request whose own lengths are inconsistent (a negative value, more
+ *   pages held than max_pages_per_seq, more tokens cached than pages held, more tokens than the
+ *   block-table row can address); the requests after it are served. A page id outside
+ *   [0, num_pages) is reported, stored as -1, and slots in it are -1.
+ *   seq_lens may be kv_lens, pages_held_out may be pages_held and free_used_out may be free_used
+ *   (an update in place); no other overlap of inputs and outputs is allowed.
+ *   Supported: page_size = 16, num_reqs <= 16384, num_pages <= 2^26. total_new, num_free and
+ *   num_reqs may be zero (pointers to nothing may be NULL). All pointers 4-byte aligned.
+ */
+ATTN_API int attn_paged_plan(const int32_t* kv_lens, const int32_t* new_lens, const int32_t* pages_held,
+                             const int32_t* free_pages, const int32_t* free_used, int32_t* block_table,
+                             int32_t* seq_lens, int32_t* cu_q, int32_t* positions, int32_t* slots,
+                             int32_t* pages_held_out, int32_t* free_used_out, int32_t* admitted, int num_reqs,
+                             int total_new, int num_free, int page_size, int max_pages_per_seq, int num_pages,
+                             void* stream);
+
+/*
+ * attn_qk_norm_rope -- RMS norm of every query and key head, then the rotary position encoding, in
+ * one pass: the step from the projections to the attention calls above. For a head's row x:
+ *   n = (weight_offset + w) * x / sqrt(mean(x^2) + eps)
+ *   y = n with the pairs of its first rot_dim dims turned by the angles of the token's position:
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * evaluated in fp32 and rounded once to bf16. Pairs are dims (i, i + rot_dim/2), i < rot_dim/2, or
+ * with interleaved = 1 dims (2i, 2i + 1); pair i takes column i of the table's cos and sin.
+ *   q [T, Hq, D], k [T, Hkv, D] bf16: heads contiguous within a token, tokens q_stride / k_stride
+ *   elements apart (slices of a fused projection need no copy; strides are multiples of 8).
+ *   q_weight, k_weight [D], bf16 or (weight_fp32 = 1) fp32; NULL: no weight, n = x / rms.
+ *   positions int32 [T]; cos_sin fp32 [max_pos, rot_dim]: row p holds cos of the rot_dim/2 angles
+ *   of position p, then their sin. A token with a position outside [0, max_pos) is reported as
+ *   ATTN_ERR_DEVICE_BOUNDS and its output rows are left as they were. rot_dim = 0: no
+ *   rotation; positions and cos_sin are not read and may be NULL.
+ *   q_out [T, Hq, D], k_out [T, Hkv, D] bf16, contiguous. q_out may be q and k_out may be k when those
+ *   are contiguous too; no other overlap.
+ *   Supported: D in {64, 128, 256, 512}, rot_dim a multiple of 16 up to D, eps > 0, Hq and Hkv
+ *   (independent of each other here) 1 .. 2048, T <= 2^30. T = 0: nothing to do. No workspace.
+ */
+ATTN_API int attn_qk_norm_rope(const attn_bf16* q, const attn_bf16* k, attn_bf16* q_out, attn_bf16* k_out,
+                               const void* q_weight, const void* k_weight, const int32_t* positions,
+                               const float* cos_sin, int T, int Hq, int Hkv, int D, int rot_dim, int max_pos,
+                               long long q_stride, long long k_stride, float eps, float weight_offset,
+                               int weight_fp32, int interleaved, void* stream);
+
+/*
+ * attn_qk_norm_rope_bwd -- gradient of attn_qk_norm_rope. q, k, weights, positions, table and options as
+ * in the forward; dq_out [T, Hq, D], dk_out [T, Hkv, D] bf16, contiguous: the gradients of its results
+ * (dQ and dK of attn_bwd).
+ *   dq [T, Hq, D], dk [T, Hkv, D] bf16 out, tokens dq_stride / dk_stride elements apart (slices of a
+ *   fused projection's gradient). dq_weight, dk_weight [D] fp32 out: sums over every token and
+ *   head, in an order that depends on the sizes and the device alone (the same bits every time);
+ *   NULL: not wanted. With no weight (q_weight NULL) they are the gradient of a unit weight.
+ *   dq may be dq_out or q, dk may be dk_out or k, where both have the same strides.
+ *   A token with a position out of range is reported; it adds nothing and its dq / dk rows are
+ *   left as they were. T = 0: the weight gradients are set to zero.
+ *   workspace: attn_workspace_size(ATTN_OP_QK_NORM_ROPE_BWD, 0, 0, 0, 0, D, ...) bytes, 256-byte aligned;
+ *   contents on entry do not matter. Calls that share a workspace must not overlap on the GPU.
+ */
+ATTN_API int attn_qk_norm_rope_bwd(const attn_bf16* dq_out, const attn_bf16* dk_out, const attn_bf16* q,
+                                   const attn_bf16* k, attn_bf16* dq, attn_bf16* dk, float* dq_weight,
+                                   float* dk_weight, const void* q_weight, const void* k_weight,
+                                   const int32_t* positions, const float* cos_sin, int T, int Hq, int Hkv, int D,
+                                   int rot_dim, int max_pos, long long q_stride, long long k_stride,
+                                   long long dq_stride, long long dk_stride, float eps, float weight_offset,
+                                   int weight_fp32, int interleaved, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * attn_qk_norm_rope_paged -- attn_qk_norm_rope for serving: q goes to q_out, and k (normed and turned) and v
+ * (as it is) go straight into the paged caches, each token at its slot.
+ *   v [T, Hkv, D] bf16, tokens v_stride elements apart. slots int32 [T], of attn_paged_plan: slot s is
+ *   token s % 16 of page s / 16. k_cache, v_cache [num_pages, page_size, Hkv, D] bf16, updated in
+ *   place. A token with slot -1 is padding: nothing of it is read or written, q_out included. Any
+ *   other slot outside the cache, or a position outside the table, is reported as
+ *   ATTN_ERR_DEVICE_BOUNDS and the token's rows are left as they were. Slots of different tokens
+ *   must differ (of two tokens with one slot, either one's values may end up in each part of it).
+ *   page_size = 16, num_pages <= 2^26; everything else as in attn_qk_norm_rope.
+ */
+ATTN_API int attn_qk_norm_rope_paged(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_bf16* q_out,
+                                     attn_bf16* k_cache, attn_bf16* v_cache, const void* q_weight,
+                                     const void* k_weight, const int32_t* positions, const int32_t* slots,
+                                     const float* cos_sin, int T, int Hq, int Hkv, int D, int rot_dim, int max_pos,
+                                     int page_size, int num_pages, long long q_stride, long long k_stride,
+                                     long long v_stride, float eps, float weight_offset, int weight_fp32,
+                                     int interleaved, void* stream);
+
+/*
+ * attn_tree_paged -- attention of drafted token trees over a paged cache: the verification step of
+ * speculative decoding. As in attn_fwd_paged each request's n_b = cu_q[b+1] - cu_q[b] query rows are the
+ * last n_b of its seq_lens[b] = L_b cached tokens, but instead of a causal order among them, row i sees
+ * the drafted tokens that its mask row names:
+ *   key j < L_b - n_b (the context): visible, or with window > 0 only if p_i - j < window, where
+ *     p_i = max(positions[i], L_b - n_b) is the row's position (context length + depth in its tree);
+ *   key L_b - n_b + d (drafted token d): visible if bit d % 32 of word d / 32 of the row's mask is
+ *     set (normally its ancestors and itself). Bits of d >= n_b are ignored.
+ *   A row that sees no key gets o = 0 and lse = -inf.
+ *   q, o [total_q, Hq, D] bf16, lse [Hq, total_q] fp32, caches, block_table, seq_lens, cu_q,
+ *   max_q_len and the device checks of requests and page ids as in attn_fwd_paged.
+ *   tree_mask int32 [total_q, mask_words], mask_words >= ceil(max_q_len / 32). positions int32
+ *   [total_q], needed with window > 0 only (else NULL).
+ *   Supported: D in {64, 128, 256, 512}, Hq / Hkv <= 128, page_size = 16, max_q_len <= 256,
+ *   mask_words <= 8, num_reqs <= 4096, Hkv <= 256, num_pages <= 2^26.
+ *   workspace: attn_workspace_size(ATTN_OP_TREE_PAGED, 0, Hq, Hkv, max_q_len, D, ...) bytes, 256-byte
+ *   aligned: partial results of the key ranges that several CTAs share. Contents on entry do not matter.
+ *   Calls that share a workspace must not overlap on the GPU.
+ *   With num_reqs, total_q or max_q_len zero there is nothing to compute (pointers may be NULL).
+ */
+ATTN_API int attn_tree_paged(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
+                             const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q,
+                             const int32_t* tree_mask, const int32_t* positions, attn_bf16* o, float* lse,
+                             int num_reqs, int total_q, int max_q_len, int mask_words, int Hq, int Hkv, int D,
+                             int page_size, int max_pages_per_seq, int num_pages, float scale, int window,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * attn_workspace_size -- bytes of workspace an operation needs (0 if none).
  *   For ATTN_OP_BWD: B, Hq, S, D; for ATTN_OP_BWD_VARLEN pass B = 1 and S = total tokens.
- *   For ATTN_OP_DECODE_PAGED: B, Hq, Hkv, D. Unused arguments are ignored. Returns 0 for an
+ *   For ATTN_OP_DECODE_PAGED: B, Hq, Hkv, D. For ATTN_OP_QK_NORM_ROPE_BWD: D. For ATTN_OP_TREE_PAGED: Hq,
+ *   Hkv, S = max_q_len, D. Unused arguments are ignored. Returns 0 for an
  *   unknown op, and for a decode problem no decode kernel takes (D not 128 / 256, Hq not a
  *   supported multiple of Hkv), whose call is rejected anyway. Pure host arithmetic; needs no
  *   GPU.
