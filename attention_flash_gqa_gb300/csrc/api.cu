@@ -85,11 +85,11 @@ const DeviceInfo* device_info() {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// 4-D map over a [batch, rows, heads, dim] bf16 tensor, box = 64 dims x 1 head x box_rows rows.
-bool make_map(CUtensorMap* m, const void* base, int D, int H, int rows, int batch, int box_rows = 128) {
+// 4-D map over a [batch, rows, heads, dim] bf16 tensor, box = 64 dims x box_heads heads x box_rows rows.
+bool make_map(CUtensorMap* m, const void* base, int D, int H, int rows, int batch, int box_rows = 128, int box_heads = 1) {
     cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)rows, (cuuint64_t)batch};
     cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2, (cuuint64_t)rows * H * D * 2};
-    cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
+    cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
     return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -201,8 +201,7 @@ bool tree_shape_ok(int Hq, int Hkv, int max_q, int D) {
     return Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && Hq / Hkv <= 128 && Hkv <= 256 && max_q >= 0 && max_q <= 256 && head_dim_ok(D);
 }
 size_t tree_ws(int Hq, int Hkv, int max_q, int D) {
-    (void)Hq, (void)Hkv, (void)max_q, (void)D;
-    return 0;
+    return max_q > 0 ? align256(attn::tree_workspace_bytes(Hq / Hkv, max_q, D)) : 0;
 }
 
 // Arguments that the three head-norm calls share. `rows` with a T of zero need no pointers.
@@ -689,13 +688,18 @@ int attn_tree_paged(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf1
         return ATTN_ERR_MISALIGNED;
     if (num_pages == 0 || max_pages_per_seq == 0) return ATTN_ERR_INVALID_ARG;  // drafted tokens need cached pages
     const size_t need = tree_ws(Hq, Hkv, max_q_len, D);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
-    if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return ATTN_ERR_MISALIGNED;
+    if (!workspace || workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return ATTN_ERR_MISALIGNED;
     const DeviceInfo* dev = device_info();
     if (!dev) return ATTN_ERR_NO_DEVICE;
     attn::TreeLaunch L;
     std::memset(&L, 0, sizeof(L));
-    L.q = q, L.k_cache = k_cache, L.v_cache = v_cache, L.block_table = block_table, L.seq_lens = seq_lens, L.cu_q = cu_q;
+    const int G = Hq / Hkv;
+    if (!make_map(&L.tq, q, D, Hq, total_q, 1, attn::tree_tokens_per_tile(G), G) ||
+        !make_cache_map(&L.tk, k_cache, D, Hkv, num_pages) || !make_cache_map(&L.tv, v_cache, D, Hkv, num_pages))
+        return ATTN_ERR_LAUNCH;
+    L.workspace = workspace;
+    L.block_table = block_table, L.seq_lens = seq_lens, L.cu_q = cu_q;
     L.mask = tree_mask, L.positions = positions, L.o = o, L.lse = lse, L.status = dev->status;
     L.R = num_reqs, L.T = total_q, L.max_q = max_q_len, L.words = mask_words, L.Hq = Hq, L.Hkv = Hkv, L.D = D;
     L.max_pages = max_pages_per_seq, L.num_pages = num_pages, L.window = window, L.sms = dev->sms, L.scale = scale;
