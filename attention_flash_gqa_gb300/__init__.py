@@ -31,6 +31,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -391,38 +392,69 @@ class PagedPlan(NamedTuple):
     admitted: Any     # [1] requests served
 
 
-def _check_i32(name, t, shape, device):
+# The calls below are short on the GPU, so their argument checks are kept cheap: attributes are compared
+# one by one and nothing is built before a check has failed.
+
+def _i32(t, shape, idx, name):
+    """Pointer of a contiguous int32 tensor of that shape on GPU idx."""
     import torch
 
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
-    return t.data_ptr()
+    if t.dtype is torch.int32 and t.get_device() == idx and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on cuda:{idx}")
 
 
-def _cuda_device(t, name):
-    if not t.is_cuda:
+def _dense(t, shape, idx, name):
+    """Pointer of a contiguous bfloat16 tensor of that shape on GPU idx."""
+    import torch
+
+    if t.dtype is torch.bfloat16 and t.get_device() == idx and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous bfloat16 tensor of shape {tuple(shape)} on cuda:{idx}")
+
+
+def _index(t, name):
+    idx = t.get_device()
+    if idx < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return idx
 
 
-def _allocating(stream, make):
-    """make(), its tensors belonging to the stream that the call runs on."""
+def _new(shape, dtype, idx, stream):
+    """A tensor of the stream that the call runs on."""
     import torch
 
     if stream is None:
-        return make()
+        return torch.empty(shape, dtype=dtype, device=idx)
     with torch.cuda.stream(stream):
-        return make()
+        return torch.empty(shape, dtype=dtype, device=idx)
 
 
-def _run(fn, what, device, stream, *args):
+@functools.lru_cache(maxsize=4096)
+def _need(op, Hq, Hkv, S, D):
+    return attn_workspace_size(op, 0, Hq, Hkv, S, D)
+
+
+def _scratch(workspace, nbytes, idx, stream):
+    """The call's workspace and its size. One of its own (of its stream, or of the graph being captured) unless
+    the caller gives one: calls on different streams, or in different graphs, then never share it."""
     import torch
 
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, _stream_ptr(stream, device))
+    if workspace is None:
+        return _new(nbytes, torch.uint8, idx, stream), nbytes
+    if workspace.get_device() != idx or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{idx}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _run(fn, what, idx, stream, *args):
+    import torch
+
+    if torch.cuda.current_device() == idx:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(device):  # the library works on the current device
-            rc = fn(*args, _stream_ptr(stream, device))
+        with torch.cuda.device(idx):  # the library works on the current device
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream)
     if rc != 0:
         raise AttnError(rc, what)
 
@@ -440,88 +472,102 @@ def attn_paged_plan(kv_lens, new_lens, free_pages, block_table, pages_held, free
     """
     import torch
 
-    dev = _cuda_device(kv_lens, "kv_lens")
+    idx = _index(kv_lens, "kv_lens")
     R, F, T = kv_lens.numel(), free_pages.numel(), int(total_new)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [num_reqs, max_pages]")
     if T < 0:
         raise ValueError("total_new must not be negative")
+    maxp, rs, one = block_table.shape[1], (R,), (1,)
+    ins = (_i32(kv_lens, rs, idx, "kv_lens"), _i32(new_lens, rs, idx, "new_lens"), _i32(pages_held, rs, idx, "pages_held"),
+           _i32(free_pages, (F,), idx, "free_pages"), _i32(free_used, one, idx, "free_used"),
+           _i32(block_table, (R, maxp), idx, "block_table"))
     if out is None:
-        def make():
-            buf = torch.empty(3 * R + 2 * T + 3, dtype=torch.int32, device=dev)
-            return PagedPlan(*buf.split([R, R + 1, T, T, R, 1, 1]))
-
-        out = _allocating(stream, make)
-    _run(load_library().attn_paged_plan, "attn_paged_plan", dev, stream,
-         _check_i32("kv_lens", kv_lens, (R,), dev), _check_i32("new_lens", new_lens, (R,), dev),
-         _check_i32("pages_held", pages_held, (R,), dev), _check_i32("free_pages", free_pages, (F,), dev),
-         _check_i32("free_used", free_used, (1,), dev),
-         _check_i32("block_table", block_table, (R, block_table.shape[1]), dev),
-         _check_i32("out.seq_lens", out.seq_lens, (R,), dev), _check_i32("out.cu_q", out.cu_q, (R + 1,), dev),
-         _check_i32("out.positions", out.positions, (T,), dev), _check_i32("out.slots", out.slots, (T,), dev),
-         _check_i32("out.pages_held", out.pages_held, (R,), dev), _check_i32("out.free_used", out.free_used, (1,), dev),
-         _check_i32("out.admitted", out.admitted, (1,), dev), R, T, F, int(page_size), block_table.shape[1],
+        buf = _new(3 * R + 2 * T + 3, torch.int32, idx, stream)
+        out = PagedPlan._make(torch.split_with_sizes(buf, (R, R + 1, T, T, R, 1, 1)))
+        at = buf.data_ptr()
+        outs = (at, at + 4 * R, at + 8 * R + 4, at + 8 * R + 4 + 4 * T, at + 8 * R + 4 + 8 * T, at + 12 * R + 4 + 8 * T,
+                at + 12 * R + 8 + 8 * T)
+    else:
+        outs = (_i32(out.seq_lens, rs, idx, "out.seq_lens"), _i32(out.cu_q, (R + 1,), idx, "out.cu_q"),
+                _i32(out.positions, (T,), idx, "out.positions"), _i32(out.slots, (T,), idx, "out.slots"),
+                _i32(out.pages_held, rs, idx, "out.pages_held"), _i32(out.free_used, one, idx, "out.free_used"),
+                _i32(out.admitted, one, idx, "out.admitted"))
+    _run(load_library().attn_paged_plan, "attn_paged_plan", idx, stream, *ins, *outs, R, T, F, int(page_size), maxp,
          int(num_pages))
     return out
 
 
-def _rows(t, name, device=None):
-    """A [..., H, D] bf16 tensor as T tokens: (pointer, leading shape, T, H, D, token stride)."""
+def _rows(t, name, idx):
+    """A [T, H, D] or [B, S, H, D] bfloat16 tensor as (T, H, D, token stride)."""
     import torch
 
-    if t.dtype != torch.bfloat16 or not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be a bfloat16 CUDA tensor on the call's device")
+    if t.dtype is not torch.bfloat16 or t.get_device() != idx:
+        raise ValueError(f"{name} must be a bfloat16 tensor on cuda:{idx}")
     shape, st = t.shape, t.stride()
-    if len(shape) not in (3, 4):
-        raise ValueError(f"{name} must be [T, H, D] or [B, S, H, D]")
-    H, D = shape[-2], shape[-1]
-    if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
     if len(shape) == 3:
-        T, step = shape[0], st[0]
-    else:
-        T = shape[0] * shape[1]
-        step = st[1] if shape[1] > 1 else st[0]
-        if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
+        T, H, D = shape
+        step = st[0]
+    elif len(shape) == 4:
+        B, S, H, D = shape
+        T, step = B * S, (st[1] if S > 1 else st[0])
+        if B > 1 and S > 1 and st[0] != S * st[1]:
             raise ValueError(f"{name}: tokens must be evenly spaced across the batch")
-    return t.data_ptr(), shape[:-2], T, H, D, (step if T > 1 else H * D)
+    else:
+        raise ValueError(f"{name} must be [T, H, D] or [B, S, H, D]")
+    if (st[-1] != 1 and D > 1) or (st[-2] != D and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return T, H, D, (step if T > 1 else H * D)
 
 
-def _dense_rows(t, name, lead, H, D, device):
+def _qk(q, k, idx):
+    T, Hq, D, qs = _rows(q, "q", idx)
+    Tk, Hkv, Dk, ks = _rows(k, "k", idx)
+    if Tk != T or Dk != D or q.dim() != k.dim() or q.shape[0] != k.shape[0]:
+        raise ValueError("q and k must have the same tokens and head size")
+    return T, Hq, Hkv, D, qs, ks
+
+
+def _norm_weight(w, D, idx, name):
+    """Pointer of a norm weight, and 1 if it is fp32, 0 if bfloat16, None if there is none."""
     import torch
 
-    if t.dtype != torch.bfloat16 or t.device != device or not t.is_contiguous() or tuple(t.shape) != (*lead, H, D):
-        raise ValueError(f"{name} must be a contiguous bfloat16 tensor of shape {(*lead, H, D)} on {device}")
-    return t.data_ptr()
+    if w is None:
+        return None, None
+    kind = 0 if w.dtype is torch.bfloat16 else 1 if w.dtype is torch.float32 else -1
+    if kind < 0 or w.get_device() != idx or w.shape != (D,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bfloat16 or float32 tensor of shape ({D},) on cuda:{idx}")
+    return w.data_ptr(), kind
 
 
-def _norm_weights(q_weight, k_weight, D, device):
+def _norm_weights(q_weight, k_weight, D, idx):
     """Pointers of the norm weights and whether they are fp32."""
-    import torch
-
-    kinds = {w.dtype for w in (q_weight, k_weight) if w is not None}
-    if len(kinds) > 1 or not kinds <= {torch.bfloat16, torch.float32}:
+    wq, fq = _norm_weight(q_weight, D, idx, "q_weight")
+    wk, fk = _norm_weight(k_weight, D, idx, "k_weight")
+    if fq is not None and fk is not None and fq != fk:
         raise ValueError("q_weight and k_weight must both be bfloat16 or both float32")
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.device != device or not w.is_contiguous() or tuple(w.shape) != (D,)):
-            raise ValueError(f"{n} must be a contiguous tensor of shape ({D},) on {device}")
-    return (None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
-            int(kinds == {torch.float32}))
+    return wq, wk, fq or fk or 0
 
 
-def _angles(positions, cos_sin, lead, T, device):
+def _per_token(t, q, T, idx, name):
+    """Pointer of an int32 tensor with a value per token of q: [T], or q's [B, S]."""
+    return _i32(t, (T,) if t.dim() == 1 else q.shape[:-2], idx, name)
+
+
+def _angles(positions, cos_sin, q, T, idx):
     """Pointers of positions and table, rotated dims and table rows."""
     import torch
 
     if cos_sin is None:
         return None, None, 0, 0
-    if (cos_sin.dtype != torch.float32 or cos_sin.device != device or not cos_sin.is_contiguous() or cos_sin.dim() != 2):
-        raise ValueError(f"cos_sin must be a contiguous float32 tensor [max_pos, rot_dim] on {device}")
-    if cos_sin.shape[1] == 0:
+    if cos_sin.dtype is not torch.float32 or cos_sin.get_device() != idx or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError(f"cos_sin must be a contiguous float32 tensor [max_pos, rot_dim] on cuda:{idx}")
+    rows, rot = cos_sin.shape
+    if rot == 0:
         return None, None, 0, 0
-    if positions is None or tuple(positions.shape) not in (tuple(lead), (T,)):
-        raise ValueError(f"positions must be an int32 tensor of shape {tuple(lead)}")
-    return _check_i32("positions", positions, tuple(positions.shape), device), cos_sin.data_ptr(), cos_sin.shape[1], cos_sin.shape[0]
+    if positions is None:
+        raise ValueError("positions are needed with cos_sin")
+    return _per_token(positions, q, T, idx, "positions"), cos_sin.data_ptr(), rot, rows
 
 
 def attn_qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, q_out=None, k_out=None, *, eps: float = 1e-6,
@@ -534,20 +580,17 @@ def attn_qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, q_out=None, 
     """
     import torch
 
-    qp, lead, T, Hq, D, qs = _rows(q, "q")
-    dev = q.device
-    kp, klead, _, Hkv, Dk, ks = _rows(k, "k", dev)
-    if klead != lead or Dk != D:
-        raise ValueError("q and k must have the same tokens and head size")
-    wq, wk, w32 = _norm_weights(q_weight, k_weight, D, dev)
-    pos, table, rot, rows = _angles(positions, cos_sin, lead, T, dev)
+    idx = _index(q, "q")
+    T, Hq, Hkv, D, qs, ks = _qk(q, k, idx)
+    wq, wk, w32 = _norm_weights(q_weight, k_weight, D, idx)
+    pos, table, rot, rows = _angles(positions, cos_sin, q, T, idx)
     if q_out is None:
-        q_out = _allocating(stream, lambda: torch.empty((*lead, Hq, D), dtype=torch.bfloat16, device=dev))
+        q_out = _new(q.shape, torch.bfloat16, idx, stream)
     if k_out is None:
-        k_out = _allocating(stream, lambda: torch.empty((*lead, Hkv, D), dtype=torch.bfloat16, device=dev))
-    _run(load_library().attn_qk_norm_rope, "attn_qk_norm_rope", dev, stream, qp, kp,
-         _dense_rows(q_out, "q_out", lead, Hq, D, dev), _dense_rows(k_out, "k_out", lead, Hkv, D, dev), wq, wk, pos, table,
-         T, Hq, Hkv, D, rot, rows, qs, ks, float(eps), float(weight_offset), w32, int(bool(interleaved)))
+        k_out = _new(k.shape, torch.bfloat16, idx, stream)
+    _run(load_library().attn_qk_norm_rope, "attn_qk_norm_rope", idx, stream, q.data_ptr(), k.data_ptr(),
+         _dense(q_out, q.shape, idx, "q_out"), _dense(k_out, k.shape, idx, "k_out"), wq, wk, pos, table, T, Hq, Hkv, D, rot,
+         rows, qs, ks, eps, weight_offset, w32, 1 if interleaved else 0)
     return q_out, k_out
 
 
@@ -561,43 +604,38 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, c
     """
     import torch
 
-    qp, lead, T, Hq, D, qs = _rows(q, "q")
-    dev = q.device
-    kp, klead, _, Hkv, Dk, ks = _rows(k, "k", dev)
-    if klead != lead or Dk != D:
-        raise ValueError("q and k must have the same tokens and head size")
-    wq, wk, w32 = _norm_weights(q_weight, k_weight, D, dev)
-    pos, table, rot, rows = _angles(positions, cos_sin, lead, T, dev)
-    need = attn_workspace_size(ATTN_OP_QK_NORM_ROPE_BWD, D=D)
-
-    def make():
-        return (torch.empty((*lead, Hq, D), dtype=torch.bfloat16, device=dev) if dq is None else dq,
-                torch.empty((*lead, Hkv, D), dtype=torch.bfloat16, device=dev) if dk is None else dk,
-                torch.empty((2, D), dtype=torch.float32, device=dev),
-                torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace)
-
-    dq, dk, dw, ws = _allocating(stream, make)
-    dqp, qlead, _, h, d, dqs = _rows(dq, "dq", dev)
-    dkp, klead, _, hk, dd, dks = _rows(dk, "dk", dev)
-    if (qlead, h, d) != (lead, Hq, D) or (klead, hk, dd) != (lead, Hkv, D):
-        raise ValueError("dq and dk must have the shapes of q and k")
-    dqw, dkw = dw[0], dw[1]
-    _run(load_library().attn_qk_norm_rope_bwd, "attn_qk_norm_rope_bwd", dev, stream,
-         _dense_rows(dq_out, "dq_out", lead, Hq, D, dev), _dense_rows(dk_out, "dk_out", lead, Hkv, D, dev), qp, kp, dqp, dkp,
-         dqw.data_ptr(), dkw.data_ptr(), wq, wk, pos, table, T, Hq, Hkv, D, rot, rows, qs, ks, dqs, dks, float(eps),
-         float(weight_offset), w32, int(bool(interleaved)), _ptr(ws), ws.numel() * ws.element_size())
+    idx = _index(q, "q")
+    T, Hq, Hkv, D, qs, ks = _qk(q, k, idx)
+    wq, wk, w32 = _norm_weights(q_weight, k_weight, D, idx)
+    pos, table, rot, rows = _angles(positions, cos_sin, q, T, idx)
+    dqs, dks = Hq * D, Hkv * D
+    if dq is None:
+        dq = _new(q.shape, torch.bfloat16, idx, stream)
+    elif dq.shape != q.shape:
+        raise ValueError("dq must have the shape of q")
+    else:
+        dqs = _rows(dq, "dq", idx)[3]
+    if dk is None:
+        dk = _new(k.shape, torch.bfloat16, idx, stream)
+    elif dk.shape != k.shape:
+        raise ValueError("dk must have the shape of k")
+    else:
+        dks = _rows(dk, "dk", idx)[3]
+    dqw, dkw = _new((2, D), torch.float32, idx, stream).unbind()
+    ws, nbytes = _scratch(workspace, _need(ATTN_OP_QK_NORM_ROPE_BWD, 0, 0, 0, D), idx, stream)
+    _run(load_library().attn_qk_norm_rope_bwd, "attn_qk_norm_rope_bwd", idx, stream,
+         _dense(dq_out, q.shape, idx, "dq_out"), _dense(dk_out, k.shape, idx, "dk_out"), q.data_ptr(), k.data_ptr(),
+         dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), wq, wk, pos, table, T, Hq, Hkv, D, rot, rows, qs, ks,
+         dqs, dks, eps, weight_offset, w32, 1 if interleaved else 0, ws.data_ptr(), nbytes)
     return dq, dk, dqw, dkw
 
 
-def _caches(k_cache, v_cache, device, D):
-    import torch
-
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype != torch.bfloat16 or t.device != device or not t.is_contiguous() or t.dim() != 4 or t.shape[3] != D:
-            raise ValueError(f"{n} must be a contiguous bfloat16 tensor [num_pages, page_size, Hkv, {D}] on {device}")
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
-    return k_cache.shape[:3]
+def _caches(k_cache, v_cache, D, idx):
+    """Pointers and [num_pages, page_size, Hkv] of a pair of caches."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[3] != D:
+        raise ValueError(f"k_cache must be [num_pages, page_size, Hkv, {D}]")
+    return _dense(k_cache, shape, idx, "k_cache"), _dense(v_cache, shape, idx, "v_cache"), shape[0], shape[1], shape[2]
 
 
 def attn_qk_norm_rope_paged(q, k, v, q_weight, k_weight, positions, slots, cos_sin, k_cache, v_cache, q_out=None, *,
@@ -606,25 +644,21 @@ def attn_qk_norm_rope_paged(q, k, v, q_weight, k_weight, positions, slots, cos_s
     [pages,16,Hkv,D] in place, each token at its slot (int32 [T], of attn_paged_plan; -1: padding)."""
     import torch
 
-    qp, lead, T, Hq, D, qs = _rows(q, "q")
-    dev = q.device
-    kp, klead, _, Hkv, Dk, ks = _rows(k, "k", dev)
-    vp, vlead, _, Hv, Dv, vs = _rows(v, "v", dev)
-    if klead != lead or Dk != D or vlead != lead or (Hv, Dv) != (Hkv, D):
-        raise ValueError("q, k and v must have the same tokens and head size, k and v the same heads")
-    wq, wk, w32 = _norm_weights(q_weight, k_weight, D, dev)
-    pos, table, rot, rows = _angles(positions, cos_sin, lead, T, dev)
-    num_pages, page_size, Hc = _caches(k_cache, v_cache, dev, D)
+    idx = _index(q, "q")
+    T, Hq, Hkv, D, qs, ks = _qk(q, k, idx)
+    if v.shape != k.shape:
+        raise ValueError("v must have the shape of k")
+    vs = _rows(v, "v", idx)[3]
+    wq, wk, w32 = _norm_weights(q_weight, k_weight, D, idx)
+    pos, table, rot, rows = _angles(positions, cos_sin, q, T, idx)
+    kc, vc, num_pages, page_size, Hc = _caches(k_cache, v_cache, D, idx)
     if Hc != Hkv:
         raise ValueError("the caches' heads are not k's")
-    if tuple(slots.shape) not in (tuple(lead), (T,)):
-        raise ValueError(f"slots must be an int32 tensor of shape {tuple(lead)}")
     if q_out is None:
-        q_out = _allocating(stream, lambda: torch.empty((*lead, Hq, D), dtype=torch.bfloat16, device=dev))
-    _run(load_library().attn_qk_norm_rope_paged, "attn_qk_norm_rope_paged", dev, stream, qp, kp, vp,
-         _dense_rows(q_out, "q_out", lead, Hq, D, dev), k_cache.data_ptr(), v_cache.data_ptr(), wq, wk, pos,
-         _check_i32("slots", slots, tuple(slots.shape), dev), table, T, Hq, Hkv, D, rot, rows, page_size, num_pages, qs, ks,
-         vs, float(eps), float(weight_offset), w32, int(bool(interleaved)))
+        q_out = _new(q.shape, torch.bfloat16, idx, stream)
+    _run(load_library().attn_qk_norm_rope_paged, "attn_qk_norm_rope_paged", idx, stream, q.data_ptr(), k.data_ptr(),
+         v.data_ptr(), _dense(q_out, q.shape, idx, "q_out"), kc, vc, wq, wk, pos, _per_token(slots, q, T, idx, "slots"), table,
+         T, Hq, Hkv, D, rot, rows, page_size, num_pages, qs, ks, vs, eps, weight_offset, w32, 1 if interleaved else 0)
     return q_out
 
 
@@ -639,30 +673,28 @@ def attn_tree_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, tree_mask,
     """
     import torch
 
-    if q.dim() != 3:
+    idx = _index(q, "q")
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must be [T, Hq, D]")
-    T, Hq, D = q.shape
-    dev = _cuda_device(q, "q")
-    num_pages, page_size, Hkv = _caches(k_cache, v_cache, dev, D)
+    T, Hq, D = shape
+    qp = _dense(q, shape, idx, "q")
+    kc, vc, num_pages, page_size, Hkv = _caches(k_cache, v_cache, D, idx)
     R = seq_lens.numel()
     if block_table.dim() != 2 or tree_mask.dim() != 2:
         raise ValueError("block_table must be [num_reqs, max_pages] and tree_mask [T, words]")
-    if lse is not None and (lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous() or tuple(lse.shape) != (Hq, T)):
-        raise ValueError(f"lse must be a contiguous float32 tensor of shape {(Hq, T)} on {dev}")
-    need = attn_workspace_size(ATTN_OP_TREE_PAGED, Hq=Hq, Hkv=Hkv, S=int(max_q_len), D=D)
-
-    def make():
-        return (torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev) if o is None else o,
-                torch.empty((Hq, T), dtype=torch.float32, device=dev) if lse is None else lse,
-                torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None and need else workspace)
-
-    o, lse, ws = _allocating(stream, make)
-    _run(load_library().attn_tree_paged, "attn_tree_paged", dev, stream, _dense_rows(q, "q", (T,), Hq, D, dev),
-         k_cache.data_ptr(), v_cache.data_ptr(), _check_i32("block_table", block_table, (R, block_table.shape[1]), dev),
-         _check_i32("seq_lens", seq_lens, (R,), dev), _check_i32("cu_q", cu_q, (R + 1,), dev),
-         _check_i32("tree_mask", tree_mask, (T, tree_mask.shape[1]), dev),
-         None if positions is None else _check_i32("positions", positions, (T,), dev),
-         _dense_rows(o, "o", (T,), Hq, D, dev), lse.data_ptr(), R, T, int(max_q_len), tree_mask.shape[1], Hq, Hkv, D,
-         page_size, block_table.shape[1], num_pages, float(scale if scale is not None else 1.0 / math.sqrt(D)), int(window),
-         _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+    maxp, words, top = block_table.shape[1], tree_mask.shape[1], int(max_q_len)
+    if o is None:
+        o = _new(shape, torch.bfloat16, idx, stream)
+    if lse is None:
+        lse = _new((Hq, T), torch.float32, idx, stream)
+    elif lse.dtype is not torch.float32 or lse.get_device() != idx or lse.shape != (Hq, T) or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape {(Hq, T)} on cuda:{idx}")
+    ws, nbytes = _scratch(workspace, _need(ATTN_OP_TREE_PAGED, Hq, Hkv, top, D), idx, stream)
+    _run(load_library().attn_tree_paged, "attn_tree_paged", idx, stream, qp, kc, vc,
+         _i32(block_table, (R, maxp), idx, "block_table"), _i32(seq_lens, (R,), idx, "seq_lens"),
+         _i32(cu_q, (R + 1,), idx, "cu_q"), _i32(tree_mask, (T, words), idx, "tree_mask"),
+         None if positions is None else _i32(positions, (T,), idx, "positions"), _dense(o, shape, idx, "o"), lse.data_ptr(), R,
+         T, top, words, Hq, Hkv, D, page_size, maxp, num_pages, scale if scale is not None else 1.0 / math.sqrt(D), int(window),
+         ws.data_ptr(), nbytes)
     return o, lse

@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         auto release_slot = [&]() {
-            if (lane == 0) umma_commit(smem_u32(&empty[slot]));
+            if (elect_one()) umma_commit(smem_u32(&empty[slot]));
             if (++slot == C::kStages) slot = 0, ++round;
         };
         Walk<D> ws, wp;
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(&full[slot], round, 0x46)) return false;
                 const uint64_t dk = sdesc_sw128(sSlots + slot * C::kSlotBytes, 16, C::kGroupStride);
                 const uint64_t dq = sdesc_at(dq0, C::kSubs * c * kSubBytes);
-                if (lane == 0) {
+                if (elect_one()) {
 #pragma unroll
                     for (int sub = 0; sub < C::kSubs; ++sub)
 #pragma unroll
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 release_slot();
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 umma_commit(smem_u32(&s_full[js % C::kSBuf]));
                 if (ws.ends()) umma_commit(smem_u32(&q_free[qb]));
             }
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint64_t dv = sdesc_sw128(vslot, 1024, C::kGroupStride);
                     for (int kk = 0; kk < wp.np; ++kk)  // a page of 16 keys per step
                         umma_bf16_ts(tO + c * C::kSlotCols, tP + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_at(dv, kk * C::kPageBytes), idO,
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 release_slot();
             }
-            if (lane == 0) umma_commit(smem_u32(&pv_done[buf]));
+            if (elect_one()) umma_commit(smem_u32(&pv_done[buf]));
             ++jp;
             wp.next(a);
             return true;
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // S(j + kSBuf) over the buffer that P(j) came from: the pipe runs in order
             if (ok && ws.more()) ok = issue_s();
         }
-        if (lane == 0) {
+        if (elect_one()) {
             umma_commit(smem_u32(mma_idle));
             mbar_drain(smem_u32(mma_idle), 0, a.status, 0x4a);
         }
