@@ -10,21 +10,30 @@
 // keys spread over the whole GPU.
 //  * A row tile packs the drafted tokens and the G query heads of one KV head into the 128 rows of
 //    an MMA (row = token * G + head, 128 / G tokens a tile), so a KV head's keys serve all of them.
+//  * At D <= 128 tensor memory holds two O accumulators, so a CTA has two sets of softmax warps, each
+//    with its own O, Q tile and running state. Where a request has more rows than one tile, two row
+//    tiles go through together, one per set, and share every key tile (12 requests of 5 to 24 thousand
+//    keys and 33 to 64 drafts, Hq 32, Hkv 8, D 128: alone, each of the two row tiles read all of K and
+//    V from DRAM). Otherwise consecutive segments alternate between the sets: one set's epilogue runs
+//    beside the other's first tiles.
 //  * A unit of work is one page (16 keys) of one segment = (request, KV head, 256-column half of O at
-//    D = 512, row tile). All units are laid end to end and CTA k takes the k-th equal share: it may
-//    finish one segment, run through some and start another. A segment that one CTA covers is
-//    written out by it; of a shared one every CTA leaves (O, m, l) unnormalised in the workspace and
-//    tree_merge_kernel combines them (launched with programmatic serialisation behind this grid).
-//  * Inside a CTA the pages are taken in tiles of up to eight (128 keys) through the pipeline of the
-//    prefill forward, and the pipeline runs on across segments. Tensor memory: O (fp32, up to 256
-//    columns) and 3 (D <= 128) or 2 score buffers of 128 columns, P (bf16) over the scores. Only
-//    the pages of a tile that exist are loaded and multiplied (N of Q K^T and K of P V follow them,
-//    a page being one K step of 16), so only the last page's slots past L need care: the issuer's
-//    warp zeroes those V rows before their P V (P is 0 there, but 0 * NaN is not).
+//    D = 512, row tile or pair of them). All units are laid end to end and CTA k takes the k-th equal
+//    share: it may finish one segment, run through some and start another. A segment that one CTA
+//    covers is written out by it; of a shared one every CTA leaves (O, m, l) unnormalised in the
+//    workspace and tree_merge_kernel combines them (launched with programmatic serialisation).
+//  * Inside a CTA the pages are taken in tiles of up to eight (128 keys) through an mbarrier ring, and
+//    the pipeline runs on across segments. Tensor memory: O (fp32, up to 256 columns in all) and two
+//    score buffers of 128 columns, P (bf16) over the scores. Only the pages of a tile that exist are
+//    loaded and multiplied (N of Q K^T and K of P V follow them, a page being one K step of 16), so
+//    only the last page's slots past L need care: a fixer warp zeroes those V rows before their P V (P
+//    is 0 there, but 0 * NaN is not).
 //
-// Warp roles (320 threads): 0 TMA producer (lanes 0-7: a page each), 1 MMA issuer, 2-9 softmax
-// (warps w and w + 4 share TMEM lane quarter w & 3, each on 64 of a tile's 128 keys). Quarters
-// without rows only keep the barriers going.
+// Warp roles: four softmax warps a set (0-3, and 4-7 at two sets), one TMEM lane quarter each and one
+// thread a row, so nothing of a row is exchanged; then an idle warp, the fixer, the TMA producer (lanes
+// 0-7: a page each) and the MMA issuer. The last two sit on the schedulers of quarters 2 and 3, which
+// have no rows where a tile has 64 or fewer. Quarters without rows only keep the barriers going. The
+// issuer is one thread that reads what to do from a word the producer leaves with every copy: walking
+// the work itself took it longer than the MMAs (per 128-key tile 1.4 us, of which 0.56 us of MMAs).
 #include <cuda_runtime.h>
 
 #include "attn_internal.h"
@@ -35,47 +44,51 @@ namespace {
 
 constexpr int kPage = 16;
 constexpr int kTilePages = 8;
-constexpr int kThreads = 320;
-constexpr int kWarps = kThreads / 32;
-constexpr int kSoftmaxWarps = 8;
+constexpr int kSetWarps = 4;
 constexpr uint32_t kSubBytes = 16384;  // 128 rows x 64 bf16
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMinPages = 8;   // a CTA's share at least: one tile
 constexpr int kMaxGrid = 192;  // sizes the workspace
 
+__host__ __device__ constexpr int tree_sets(int D) { return D <= 128 ? 2 : 1; }
+
 template <int D>
 struct TreeCfg {
     static constexpr int kDV = D < 256 ? D : 256;      // O columns per segment
     static constexpr int kSplit = D / kDV;
-    static constexpr int kSBuf = kDV <= 128 ? 3 : 2;   // score buffers in tensor memory
+    static constexpr int kSets = tree_sets(D);
+    static constexpr int kFixer = kSets * kSetWarps + 1, kProducer = kFixer + 1, kIssuer = kProducer + 1;
+    static constexpr int kWarps = kIssuer + 1;
+    static constexpr int kThreads = kWarps * 32;
     static constexpr int kSubs = D >= 128 ? 2 : 1;     // 64-column sub-tiles per slot
     static constexpr int kSlotCols = 64 * kSubs;
     static constexpr uint32_t kSlotBytes = kSubs * kSubBytes;
     static constexpr int kKC = D / kSlotCols;          // slots per K tile
     static constexpr int kVC = kDV / kSlotCols;        // slots per V tile
-    static constexpr int kQBufs = D == 64 ? 2 : 1;
-    static constexpr int kStages = D == 512 ? 3 : D == 256 ? 5 : D == 128 ? 6 : 12;
+    // ring depth: what shared memory leaves next to the Q tiles
+    static constexpr int kStages = D == 512 ? 3 : D == 256 ? 5 : D == 128 ? 5 : 12;
     static constexpr uint32_t kQBytes = D * 256;       // 128 rows
     static constexpr uint32_t kPageBytes = 2048 * kSubs;     // one page's rows in a slot
     static constexpr uint32_t kGroupStride = 1024 * kSubs;   // 8 rows of both sub-tiles
-    static constexpr uint32_t kOffSlots = kQBufs * kQBytes;
-    static constexpr uint32_t kOffXch = kOffSlots + kStages * kSlotBytes;  // [2][128] fp32
-    static constexpr uint32_t kOffBar = kOffXch + 1024;
+    static constexpr uint32_t kOffSlots = kSets * kQBytes;
+    static constexpr uint32_t kOffBar = kOffSlots + kStages * kSlotBytes;
     static constexpr uint32_t kOffScan = kOffBar + 512;
-    static constexpr uint32_t kSmem = kOffScan + 256 + 1024;
+    static constexpr uint32_t kSmem = kOffScan + 192 + 1024;
     static constexpr int kRowF = kDV + 4;              // partial row: O, m, l, 2 pad
+    // tensor memory: O of set i at 0 + i * kDV, score buffers at the top
+    static_assert(kSets * kDV + 256 <= 512, "tensor memory");
     static_assert(kSmem <= 232448, "shared memory");
-    static_assert(kQBufs == 1 || kQBufs == 2, "Q buffers");
+    static_assert(kSets == 1 || (kKC == 1 && kVC == 1 && kStages >= 4), "two sets: one slot a tile, K and V in turn");
 };
 
 // What the merge of a segment needs; one per CTA, for the segment that starts in it and ends elsewhere.
 struct TreeSpan {
-    int ctas;   // CTAs that share the segment (0: none)
-    int row0;   // first token row of the tile
-    int rows;   // rows of the tile (tokens * G)
-    int head0;  // first query head
-    int col0;   // first O column
-    int pad[3];
+    int ctas;     // CTAs that share the segment (0: none)
+    int row0;     // its first token row
+    int rows[2];  // rows (tokens * G) of its row tiles
+    int head0;    // first query head
+    int col0;     // first O column
+    int pad[2];
 };
 
 struct TreeArgs {
@@ -91,9 +104,10 @@ struct TreeArgs {
 
 // A request as the walk sees it; no units if it is empty or inconsistent.
 struct Req {
-    int start, n, L, pg0, npg, tiles;
+    int start, n, L, pg0, npg, groups;  // groups: row tiles, or pairs of them
     bool bad;
 };
+template <int D>
 __device__ __forceinline__ Req load_req(const TreeArgs& a, int b) {
     Req r;
     r.start = a.cu_q[b];
@@ -102,36 +116,64 @@ __device__ __forceinline__ Req load_req(const TreeArgs& a, int b) {
     r.bad = r.start < 0 || r.n < 0 || r.n > a.max_q || r.start > a.T - r.n || r.n > r.L ||
             (long long)r.L > (long long)a.max_pages * kPage;
     if (r.bad || r.n == 0) {
-        r.n = r.npg = r.pg0 = r.tiles = 0;
+        r.n = r.npg = r.pg0 = r.groups = 0;
         return r;
     }
     const int c = r.L - r.n;
     r.pg0 = a.window > 0 && c >= a.window ? (c - a.window + 1) / kPage : 0;  // no row sees an earlier key
     r.npg = (r.L + kPage - 1) / kPage - r.pg0;
-    r.tiles = (r.n + a.tokens_tile - 1) / a.tokens_tile;
+    const int tokens = a.tokens_tile * TreeCfg<D>::kSets;
+    r.groups = (r.n + tokens - 1) / tokens;
     return r;
 }
 template <int D>
 __device__ __forceinline__ long long req_units(const TreeArgs& a, const Req& r) {
-    return (long long)r.npg * r.tiles * a.Hkv * TreeCfg<D>::kSplit;
+    return (long long)r.npg * r.groups * a.Hkv * TreeCfg<D>::kSplit;
 }
 
-// Walks the tiles of a CTA's share.
+// A copy's word: pages of the tile in bits 0-3, rows of its last page to keep in bits 4-7 (0: all), and
+enum : uint32_t {
+    kBegins = 1u << 8,    // first tile of a piece
+    kEnds = 1u << 9,      // last tile of a piece
+    kDual = 1u << 10,     // both sets work on it
+    kSet1 = 1u << 11,     // otherwise: set 1 does
+    kLast = 1u << 12,     // last tile of the share
+    kIsV = 1u << 13,      // a copy of V
+    kChunkEnd = 1u << 14  // the tile's last copy
+};
+
+// Walks the tiles of a CTA's share; the producer and the softmax warps follow the same walk.
 template <int D>
 struct Walk {
+    using C = TreeCfg<D>;
     Req r;
     int b, seg, pg, np;  // request, segment in it, first page (from pg0) and pages of the tile
+    int head, split, tok0;  // of the segment; tok0: first drafted token of its rows
     long long left;      // pages of the share from here on
     bool begins;         // first tile of a piece (a segment's pages in this CTA)
+    bool dual;           // two row tiles: one for each set
+    int set;             // the set that takes the piece (dual: both)
+    int turn;            // the next single piece's set
 
     __device__ __forceinline__ void start(const TreeArgs& a, int b_, long long off, long long units) {
         b = b_;
-        r = load_req(a, b);
+        r = load_req<D>(a, b);
         seg = (int)(off / r.npg);
         pg = (int)(off - (long long)seg * r.npg);
         left = units;
-        begins = true;
+        turn = 0;
+        piece(a);
         size();
+    }
+    __device__ __forceinline__ void piece(const TreeArgs& a) {
+        begins = true;
+        const int group = seg % r.groups, hs = seg / r.groups;
+        split = C::kSplit > 1 ? hs % C::kSplit : 0;
+        head = C::kSplit > 1 ? hs / C::kSplit : hs;
+        tok0 = group * a.tokens_tile * C::kSets;
+        dual = C::kSets == 2 && tok0 + a.tokens_tile < r.n;
+        set = 0;
+        if (C::kSets == 2 && !dual) set = turn, turn ^= 1;
     }
     __device__ __forceinline__ void size() {
         np = min(kTilePages, r.npg - pg);
@@ -144,20 +186,24 @@ struct Walk {
         begins = false;
         if (left <= 0) return;
         if (pg == r.npg) {
-            pg = 0, begins = true;
-            if (++seg == r.tiles * a.Hkv * TreeCfg<D>::kSplit) {
+            pg = 0;
+            if (++seg == r.groups * a.Hkv * C::kSplit) {
                 seg = 0;
-                do r = load_req(a, ++b);  // the share holds more units: there is another request
+                do r = load_req<D>(a, ++b);  // the share holds more units: there is another request
                 while (r.npg == 0);
             }
+            piece(a);
         }
         size();
     }
-    __device__ __forceinline__ int tile() const { return seg % r.tiles; }
-    __device__ __forceinline__ int split() const { return seg / r.tiles % TreeCfg<D>::kSplit; }
-    __device__ __forceinline__ int head() const { return seg / (r.tiles * TreeCfg<D>::kSplit); }
-    // the tile holds the request's last page, and slots of it lie past L
-    __device__ __forceinline__ bool tail() const { return pg + np == r.npg && r.L % kPage != 0; }
+    // what the issuer and the fixer need of the tile
+    __device__ __forceinline__ uint32_t word() const {
+        const int tail = pg + np == r.npg ? r.L % kPage : 0;  // rows of its last page, if slots of it lie past L
+        return (uint32_t)np | (uint32_t)tail << 4 | (begins ? kBegins : 0u) | (ends() ? kEnds : 0u) | (dual ? kDual : 0u) |
+               (set ? kSet1 : 0u) | (left == np ? kLast : 0u);
+    }
+    // whether set s works on the piece
+    __device__ __forceinline__ bool mine(int s) const { return dual || set == s; }
 };
 
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
@@ -168,9 +214,9 @@ __device__ __forceinline__ int owner_of(long long u, long long P, int G) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
     tree_paged_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                      const __grid_constant__ CUtensorMap tv, TreeArgs a) {
+                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ TreeArgs a) {
     using C = TreeCfg<D>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -179,37 +225,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     uint64_t* full = bars;                   // [kStages]
     uint64_t* empty = full + C::kStages;     // [kStages]
+    // per set: its Q tile is loaded / was last read, its O was read out
     uint64_t* q_full = empty + C::kStages;   // [2]
     uint64_t* q_free = q_full + 2;           // [2]
-    // per score buffer (step j uses j % kSBuf): at most one pending phase each, as in the prefill forward
-    uint64_t* s_full = q_free + 2;           // [3]
-    uint64_t* p_full = s_full + 3;           // [3]
-    uint64_t* pv_done = p_full + 3;          // [3]
-    uint64_t* o_free = pv_done + 3;          // the epilogue has read O
-    uint64_t* mma_idle = o_free + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_idle + 1);
+    uint64_t* o_free = q_free + 2;           // [2]
+    // per set and score buffer (index 2 set + buffer): at most one pending phase each, and only the set's
+    // own steps, so that it sees every phase
+    uint64_t* s_full = o_free + 2;           // [4]
+    uint64_t* p_full = s_full + 4;           // [4]
+    uint64_t* pv_done = p_full + 4;          // [4]
+    uint64_t* vfix = pv_done + 4;            // [kStages] the last page's V rows past L are zeroed
+    uint64_t* mma_idle = vfix + C::kStages;
+    uint32_t* words = reinterpret_cast<uint32_t*>(mma_idle + 1);  // [kStages] the copies' words
+    uint32_t* tmem_slot = words + C::kStages;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     long long* scan = reinterpret_cast<long long*>(smem + C::kOffScan);  // [kWarps], then the share's start
+    static_assert((3 * C::kStages + 19) * 8 + C::kStages * 4 + 8 <= 512 && (C::kWarps + 2) * 8 <= 192, "barrier area");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int k = blockIdx.x;
 
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
-            mbar_init(smem_u32(&empty[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 2);  // the MMAs that read it, and the fixer
+            mbar_init(smem_u32(&vfix[s]), 1);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&q_full[i]), 1), mbar_init(smem_u32(&q_free[i]), 1);
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&q_full[i]), 1);
+            mbar_init(smem_u32(&q_free[i]), 1);
+            mbar_init(smem_u32(&o_free[i]), kSetWarps);
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init(smem_u32(&s_full[i]), 1);
-            mbar_init(smem_u32(&p_full[i]), kSoftmaxWarps);
+            mbar_init(smem_u32(&p_full[i]), kSetWarps);
             mbar_init(smem_u32(&pv_done[i]), 1);
         }
-        mbar_init(smem_u32(o_free), kSoftmaxWarps);
         mbar_init(smem_u32(mma_idle), 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (warp == C::kIssuer) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
@@ -219,11 +274,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the CTA's share: units before each thread's run of requests ---------------------------
-    const int per = (a.R + kThreads - 1) / kThreads;
+    const int per = (a.R + C::kThreads - 1) / C::kThreads;
     const int b0 = min(tid * per, a.R), b1 = min(b0 + per, a.R);
     long long sum = 0;
     for (int b = b0; b < b1; ++b) {
-        const Req r = load_req(a, b);
+        const Req r = load_req<D>(a, b);
         if (r.bad && k == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
         sum += req_units<D>(a, r);
     }
@@ -237,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     long long P = 0;
     x -= sum;
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < C::kWarps; ++w) {
         if (w < warp) x += scan[w];
         P += scan[w];
     }
@@ -247,9 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long u0 = works ? (long long)k * P / Gc : 0, u1 = works ? (long long)(k + 1) * P / Gc : 0;
     if (works && x <= u0 && u0 < x + sum) {
         for (int b = b0; b < b1; ++b) {
-            const long long n = req_units<D>(a, load_req(a, b));
+            const long long n = req_units<D>(a, load_req<D>(a, b));
             if (u0 < x + n) {
-                scan[kWarps] = b, scan[kWarps + 1] = u0 - x;
+                scan[C::kWarps] = b, scan[C::kWarps + 1] = u0 - x;
                 break;
             }
             x += n;
@@ -260,17 +315,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
-    const uint32_t tO = tbase, tS0 = tbase + 512 - C::kSBuf * 128;
-    const int first_b = (int)scan[kWarps];
-    const long long first_off = scan[kWarps + 1];
+    const uint32_t tO = tbase, tS0 = tbase + 256;
+    const int first_b = (int)scan[C::kWarps];
+    const long long first_off = scan[C::kWarps + 1];
+    // The ring's slots go round in the order of the copies. One set: K and V slots in the issuer's order, K(0)
+    // K(1) V(0) K(2) V(1) .. (a K tile of D = 512 is longer than the ring). Two sets: K(0) V(0) K(1) V(1) ..,
+    // since two row tiles return to a key tile's slots: tile i's K is copy 2 i, its V copy 2 i + 1.
 
     if (!works) {
         // no units left for this CTA
-    } else if (warp == 0) {
+    } else if (warp == C::kProducer) {
         // ------------------------------- TMA producer ----------------------------------------
         if (lane == 0) prefetch_tmap(&tq), prefetch_tmap(&tk), prefetch_tmap(&tv);
         int slot = 0, round = 0;
         bool ok = true;
+        int q_uses[2] = {0, 0};
         auto page_id = [&](const Walk<D>& w) -> int {  // lane i: id of the tile's page i
             if (lane >= w.np) return 0;
             int id = a.block_table[(size_t)w.b * a.max_pages + w.r.pg0 + w.pg + lane];
@@ -281,54 +340,69 @@ __global__ void __launch_bounds__(kThreads, 1)
             return id;
         };
         // one slot: np pages, lane i loads page i's 16 rows x kSlotCols columns
-        auto load_slot = [&](const CUtensorMap* map, int chunk, int np, int id) -> bool {
+        auto load_slot = [&](const CUtensorMap* map, int chunk, int np, int id, uint32_t word) -> bool {
             if (round > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[slot]), (round - 1) & 1, abort_flag, a.status, 0x41)))
                 return false;
             const uint32_t fb = smem_u32(&full[slot]);
-            if (lane == 0) mbar_expect_tx(fb, np * C::kPageBytes);
+            if (lane == 0) {
+                words[slot] = word;
+                mbar_expect_tx(fb, np * C::kPageBytes);
+            }
             __syncwarp();
             if (lane < np) tma_load_5d(sSlots + slot * C::kSlotBytes + lane * C::kPageBytes, map, fb, 0, 0, chunk, 0, id);
             if (++slot == C::kStages) slot = 0, ++round;
             return true;
         };
+        auto load_q = [&](const Walk<D>& w, int s, int tok) -> bool {  // rows of drafted tokens tok .. of the piece
+            const int uses = s ? q_uses[1] : q_uses[0];
+            if (uses > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&q_free[s]), (uses - 1) & 1, abort_flag, a.status, 0x42)))
+                return false;
+            if (lane == 0) {
+                const uint32_t fb = smem_u32(&q_full[s]);
+                mbar_expect_tx(fb, (uint32_t)(D / 64) * a.G * a.tokens_tile * 128);
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(sQ + s * C::kQBytes + c * kSubBytes, &tq, fb, c * 64, w.head * a.G, w.r.start + tok, 0);
+            }
+            __syncwarp();
+            if (s) ++q_uses[1];
+            else ++q_uses[0];
+            return true;
+        };
         Walk<D> wk, wv;
         wk.start(a, first_b, first_off, u1 - u0);
         wv = wk;
-        int idk = page_id(wk), idv = idk, pieces = 0;
+        int idk = page_id(wk), idv = idk;
         auto load_k = [&]() -> bool {
             if (wk.begins) {
-                const int qb = pieces % C::kQBufs;
-                if (pieces >= C::kQBufs &&
-                    !__all_sync(0xffffffffu, mbar_wait(smem_u32(&q_free[qb]), (pieces / C::kQBufs - 1) & 1, abort_flag, a.status, 0x42)))
-                    return false;
-                if (lane == 0) {
-                    const uint32_t fb = smem_u32(&q_full[qb]);
-                    mbar_expect_tx(fb, (uint32_t)(D / 64) * a.G * a.tokens_tile * 128);
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load_4d(sQ + qb * C::kQBytes + c * kSubBytes, &tq, fb, c * 64, wk.head() * a.G,
-                                    wk.r.start + wk.tile() * a.tokens_tile, 0);
-                }
-                __syncwarp();
-                ++pieces;
+                if (!load_q(wk, wk.set, wk.tok0)) return false;
+                if (wk.dual && !load_q(wk, 1, wk.tok0 + a.tokens_tile)) return false;
             }
             for (int c = 0; c < C::kKC; ++c)
-                if (!load_slot(&tk, wk.head() * (D / 64) + c * C::kSubs, wk.np, idk)) return false;
+                if (!load_slot(&tk, wk.head * (D / 64) + c * C::kSubs, wk.np, idk, wk.word())) return false;
+            if (C::kSets == 2) idv = idk, wv = wk;
             wk.next(a);
             if (wk.more()) idk = page_id(wk);
             return true;
         };
         auto load_v = [&]() -> bool {
             for (int c = 0; c < C::kVC; ++c)
-                if (!load_slot(&tv, wv.head() * (D / 64) + wv.split() * (C::kDV / 64) + c * C::kSubs, wv.np, idv)) return false;
-            wv.next(a);
-            if (wv.more()) idv = page_id(wv);
+                if (!load_slot(&tv, wv.head * (D / 64) + wv.split * (C::kDV / 64) + c * C::kSubs, wv.np, idv,
+                               wv.word() | kIsV | (c == C::kVC - 1 ? kChunkEnd : 0u)))
+                    return false;
+            if (C::kSets == 1) {
+                wv.next(a);
+                if (wv.more()) idv = page_id(wv);
+            }
             return true;
         };
-        // the issuer's order: K(0) .. K(kSBuf - 1), then V(j), K(j + kSBuf)
-        for (int i = 0; ok && i < C::kSBuf && wk.more(); ++i) ok = load_k();
-        while (ok && wv.more()) {
-            ok = load_v();
-            if (ok && wk.more()) ok = load_k();
+        if constexpr (C::kSets == 2) {
+            while (ok && wk.more()) ok = load_k() && load_v();
+        } else {
+            for (int i = 0; ok && i < 2 && wk.more(); ++i) ok = load_k();
+            while (ok && wv.more()) {
+                ok = load_v();
+                if (ok && wk.more()) ok = load_k();
+            }
         }
         // every issued copy has landed before the CTA may leave
         if (lane == 0) {
@@ -337,152 +411,204 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int last = s + ((issued - 1 - s) / C::kStages) * C::kStages;
                 mbar_drain(smem_u32(&full[s]), (last / C::kStages) & 1, a.status, 0x43);
             }
-            for (int i = 0; i < C::kQBufs && i < pieces; ++i) {
-                const int last = i + ((pieces - 1 - i) / C::kQBufs) * C::kQBufs;
-                mbar_drain(smem_u32(&q_full[i]), (last / C::kQBufs) & 1, a.status, 0x44);
-            }
+            if (q_uses[0] > 0) mbar_drain(smem_u32(&q_full[0]), (q_uses[0] - 1) & 1, a.status, 0x44);
+            if (q_uses[1] > 0) mbar_drain(smem_u32(&q_full[1]), (q_uses[1] - 1) & 1, a.status, 0x44);
         }
-    } else if (warp == 1) {
+    } else if (warp == C::kFixer) {
+        // ---------- follows every copy; zeroes V rows past L in a request's last page ---------------
+        int slot = 0, phase = 0;
+        while (true) {
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[slot]), phase, abort_flag, a.status, 0x4b))) break;
+            const uint32_t word = words[slot];
+            const int keep = word >> 4 & 15;
+            if ((word & kIsV) && keep) {
+                const uint32_t base = sSlots + slot * C::kSlotBytes + ((word & 15) - 1) * C::kPageBytes;
+                for (int e = lane; e < (kPage - keep) * 8 * C::kSubs; e += 32) {  // 16-byte pieces
+                    const int row = keep + e / (8 * C::kSubs), sub = (e >> 3) % C::kSubs;
+                    st_shared_v4(base + (row >> 3) * C::kGroupStride + sub * 1024 + (row & 7) * 128 + (e & 7) * 16, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&vfix[slot]));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&empty[slot]));
+            if ((word & kLast) && (word & kChunkEnd)) break;
+            if (++slot == C::kStages) slot = 0, phase ^= 1;
+        }
+    } else if (warp == C::kIssuer) {
         // ------------------------------- MMA issuer -------------------------------------------
-        // lane 0 issues; the other lanes follow it to zero V rows
-        constexpr uint32_t idO = idesc_bf16_f32(128, C::kSlotCols, false, true);  // V is N-major
-        int slot = 0, round = 0, pieces_s = 0, pieces_o = 0, js = 0, jp = 0;
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, int phase, unsigned site) -> bool {
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, abort_flag, a.status, site))) return false;
-            tc_fence_after();
-            return true;
-        };
-        auto release_slot = [&]() {
-            if (elect_one()) umma_commit(smem_u32(&empty[slot]));
-            if (++slot == C::kStages) slot = 0, ++round;
-        };
-        Walk<D> ws, wp;
-        ws.start(a, first_b, first_off, u1 - u0);
-        wp = ws;
-        auto issue_s = [&]() -> bool {
-            if (ws.begins) {
-                if (!wait(&q_full[pieces_s % C::kQBufs], pieces_s / C::kQBufs, 0x45)) return false;
-                ++pieces_s;
-            }
-            const int qb = (pieces_s - 1) % C::kQBufs;
-            const uint32_t dst = tS0 + (js % C::kSBuf) * 128;
-            const uint32_t idS = idesc_bf16_f32(128, ws.np * kPage, false, false);
-            const uint64_t dq0 = sdesc_sw128(sQ + qb * C::kQBytes, 16, 1024);
-            for (int c = 0; c < C::kKC; ++c) {
-                if (!wait(&full[slot], round, 0x46)) return false;
-                const uint64_t dk = sdesc_sw128(sSlots + slot * C::kSlotBytes, 16, C::kGroupStride);
-                const uint64_t dq = sdesc_at(dq0, C::kSubs * c * kSubBytes);
-                if (elect_one()) {
-#pragma unroll
-                    for (int sub = 0; sub < C::kSubs; ++sub)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_bf16_ss(dst, sdesc_at(dq, sub * kSubBytes + kk * 32), sdesc_at(dk, sub * 1024 + kk * 32), idS,
-                                         (c | sub | kk) ? 1u : 0u);
-                }
-                release_slot();
-            }
-            if (elect_one()) {
-                umma_commit(smem_u32(&s_full[js % C::kSBuf]));
-                if (ws.ends()) umma_commit(smem_u32(&q_free[qb]));
-            }
-            ++js;
-            ws.next(a);
-            return true;
-        };
-        auto issue_pv = [&]() -> bool {
-            const int buf = jp % C::kSBuf;
-            if (!wait(&p_full[buf], jp / C::kSBuf, 0x47)) return false;
-            if (wp.begins) {
-                // the piece before has been read out of O
-                if (pieces_o > 0 && !wait(o_free, pieces_o - 1, 0x48)) return false;
-                ++pieces_o;
-            }
-            const uint32_t tP = tS0 + buf * 128;
-            for (int c = 0; c < C::kVC; ++c) {
-                if (!wait(&full[slot], round, 0x49)) return false;
-                const uint32_t vslot = sSlots + slot * C::kSlotBytes;
-                if (wp.tail()) {  // zero the last page's rows past L
-                    const int r0 = wp.r.L % kPage;
-                    const uint32_t base = vslot + (wp.np - 1) * C::kPageBytes;
-                    for (int e = lane; e < (kPage - r0) * 8 * C::kSubs; e += 32) {  // 16-byte pieces
-                        const int row = r0 + e / (8 * C::kSubs), sub = (e >> 3) % C::kSubs;
-                        st_shared_v4(base + (row >> 3) * C::kGroupStride + sub * 1024 + (row & 7) * 128 + (e & 7) * 16, 0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (elect_one()) {
-                    const uint64_t dv = sdesc_sw128(vslot, 1024, C::kGroupStride);
-                    for (int kk = 0; kk < wp.np; ++kk)  // a page of 16 keys per step
-                        umma_bf16_ts(tO + c * C::kSlotCols, tP + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_at(dv, kk * C::kPageBytes), idO,
-                                     (!wp.begins || kk > 0) ? 1u : 0u);
-                }
-                release_slot();
-            }
-            if (elect_one()) umma_commit(smem_u32(&pv_done[buf]));
-            ++jp;
-            wp.next(a);
-            return true;
-        };
-        for (int i = 0; ok && i < C::kSBuf && ws.more(); ++i) ok = issue_s();
-        while (ok && wp.more()) {
-            ok = issue_pv();
-            // S(j + kSBuf) over the buffer that P(j) came from: the pipe runs in order
-            if (ok && ws.more()) ok = issue_s();
-        }
+        // A step is a key tile for one row tile; step j uses score buffer j % 2, and S(j + 2) follows P V(j),
+        // which has read P from that buffer (the pipe runs in order). Two row tiles: tile i is steps s
+        // (set 0) and s + 1 (set 1).
         if (elect_one()) {
+            constexpr uint32_t idO = idesc_bf16_f32(128, C::kSlotCols, false, true);  // V is N-major
+            auto wait = [&](uint64_t* bar, uint32_t phase, unsigned site) -> bool {
+                return mbar_wait(smem_u32(bar), phase, abort_flag, a.status, site);
+            };
+            // ring positions: K and V in turn at two sets, else one position for both
+            struct Pos {
+                int slot;
+                uint32_t phase;
+                __device__ __forceinline__ void advance(int n) {
+                    slot += n;
+                    if (slot >= C::kStages) slot -= C::kStages, phase ^= 1u;
+                }
+            };
+            Pos pk = {0, 0u}, pv = {C::kSets == 2 ? 1 : 0, 0u};
+            Pos& vpos = C::kSets == 2 ? pv : pk;
+            uint32_t ws = 0u, wp = 0u;                    // the tiles' words
+            uint32_t half_s = 0u, half_p = 0u;            // which of a pair's row tiles is next
+            uint32_t buf_s = 0u, buf_p = 0u, fix_phase = 0u;  // fix_phase: bits by slot
+            uint32_t q_phase = 0u, o_phase = 0u, o_used = 0u, p_phase = 0u;  // bits by set, or 2 set + buffer
+            bool more_s = true, more_p = true, ok = true;
+            auto issue_s = [&]() -> bool {
+                uint32_t set = 0u;
+                bool last_use = true;
+#pragma unroll 1
+                for (int c = 0; c < C::kKC; ++c) {
+                    if (half_s == 0u) {
+                        if (!wait(&full[pk.slot], pk.phase, 0x46)) return false;
+                        ws = words[pk.slot];
+                    }
+                    if (c == 0) {
+                        set = (ws & kDual) ? half_s : (ws & kSet1) ? 1u : 0u;
+                        last_use = !(ws & kDual) || half_s;
+                        if (ws & kBegins) {
+                            if (!wait(&q_full[set], q_phase >> set & 1u, 0x45)) return false;
+                            q_phase ^= 1u << set;
+                        }
+                    }
+                    tc_fence_after();
+                    const uint32_t dst = tS0 + buf_s * 128, idS = idesc_bf16_f32(128, (ws & 15u) * kPage, false, false);
+                    const uint64_t dk = sdesc_sw128(sSlots + pk.slot * C::kSlotBytes, 16, C::kGroupStride);
+                    const uint64_t dq = sdesc_sw128(sQ + set * C::kQBytes + C::kSubs * c * kSubBytes, 16, 1024);
+#pragma unroll
+                    for (int i = 0; i < 4 * C::kSubs; ++i)
+                        umma_bf16_ss(dst, sdesc_at(dq, (i >> 2) * kSubBytes + (i & 3) * 32), sdesc_at(dk, (i >> 2) * 1024 + (i & 3) * 32), idS,
+                                     (c | i) ? 1u : 0u);
+                    if (last_use) {
+                        umma_commit(smem_u32(&empty[pk.slot]));
+                        pk.advance(C::kSets);
+                    }
+                }
+                umma_commit(smem_u32(&s_full[2 * set + buf_s]));
+                if (ws & kEnds) umma_commit(smem_u32(&q_free[set]));
+                buf_s ^= 1u;
+                half_s = last_use ? 0u : 1u;
+                if (last_use && (ws & kLast)) more_s = false;
+                return true;
+            };
+            auto issue_pv = [&]() -> bool {
+                uint32_t set = 0u;
+                bool last_use = true;
+#pragma unroll 1
+                for (int c = 0; c < C::kVC; ++c) {
+                    if (half_p == 0u) {
+                        if (!wait(&full[vpos.slot], vpos.phase, 0x49)) return false;
+                        wp = words[vpos.slot];
+                        if (wp >> 4 & 15u) {
+                            if (!wait(&vfix[vpos.slot], fix_phase >> vpos.slot & 1u, 0x4f)) return false;
+                            fix_phase ^= 1u << vpos.slot;
+                        }
+                    }
+                    if (c == 0) {
+                        set = (wp & kDual) ? half_p : (wp & kSet1) ? 1u : 0u;
+                        last_use = !(wp & kDual) || half_p;
+                        if (wp & kBegins) {  // the set's piece before has been read out of O
+                            if ((o_used >> set & 1u) && !wait(&o_free[set], o_phase >> set & 1u, 0x48)) return false;
+                            if (o_used >> set & 1u) o_phase ^= 1u << set;
+                            o_used |= 1u << set;
+                        }
+                        const uint32_t i = 2u * set + buf_p;
+                        if (!wait(&p_full[i], p_phase >> i & 1u, 0x47)) return false;
+                        p_phase ^= 1u << i;
+                    }
+                    tc_fence_after();
+                    const uint64_t dv = sdesc_sw128(sSlots + vpos.slot * C::kSlotBytes, 1024, C::kGroupStride);
+                    const uint32_t tP = tS0 + buf_p * 128, tD = tO + set * C::kDV + c * C::kSlotCols;
+                    const int np = wp & 15u;
+                    // a page of 16 keys per MMA; keys 64 h .. of P at columns 64 h ..
+                    umma_bf16_ts(tD, tP, dv, idO, (wp & kBegins) ? 0u : 1u);
+                    if (np == kTilePages) {
+#pragma unroll
+                        for (int kk = 1; kk < kTilePages; ++kk)
+                            umma_bf16_ts(tD, tP + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_at(dv, kk * C::kPageBytes), idO, 1u);
+                    } else {
+#pragma unroll 1
+                        for (int kk = 1; kk < np; ++kk)
+                            umma_bf16_ts(tD, tP + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_at(dv, kk * C::kPageBytes), idO, 1u);
+                    }
+                    if (last_use) {
+                        umma_commit(smem_u32(&empty[vpos.slot]));
+                        vpos.advance(C::kSets);
+                    }
+                }
+                umma_commit(smem_u32(&pv_done[2 * set + buf_p]));
+                buf_p ^= 1u;
+                half_p = last_use ? 0u : 1u;
+                if (last_use && (wp & kLast)) more_p = false;
+                return true;
+            };
+            ok = issue_s();
+            if (ok && more_s) ok = issue_s();
+            while (ok && more_p) {
+                ok = issue_pv();
+                if (ok && more_s) ok = issue_s();
+            }
             umma_commit(smem_u32(mma_idle));
             mbar_drain(smem_u32(mma_idle), 0, a.status, 0x4a);
         }
         __syncwarp();
-    } else {
+    } else if (warp < C::kSets * kSetWarps) {
         // --------------------------------- softmax ----------------------------------------------
-        const int quad = warp & 3, hf = (warp - 2) >> 2;
+        const int set = warp / kSetWarps, quad = warp & 3;
         const int row = quad * 32 + lane;  // row of the tile = TMEM lane
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-        const uint32_t pair_bar = 1 + quad;
-        float* xch = reinterpret_cast<float*>(smem + C::kOffXch);
+        const uint32_t tOset = tO + set * C::kDV + lane_base;
         float m_ref = -INFINITY, l = 0.f;
-        int first_key = 0, token = 0, pg_begin = 0, tok0 = 0, rows = 0, ctx = 0;
-        bool busy = false;
-        bool ok = true;
+        int first_key = 0, token = 0, pg_begin = 0, rows = 0, ctx = 0;
+        int step = 0, uses[2] = {0, 0};  // global step of the tile; the set's uses of each buffer
+        int prev = 0, prev_use = 0;      // buffer of the set's step before, and which use of it
+        bool busy = false, ok = true;
         Walk<D> w;
         w.start(a, first_b, first_off, u1 - u0);
-        for (int j = 0; ok && w.more(); ++j, w.next(a)) {
-            const int buf = j % C::kSBuf;
+        for (; ok && w.more(); step += w.dual ? 2 : 1, w.next(a)) {
+            if (!w.mine(set)) continue;
+            const int buf = (step + (w.dual ? set : 0)) & 1;
+            const int use = buf ? uses[1]++ : uses[0]++;
             if (w.begins) {
+                const int tok = w.tok0 + (w.dual && set ? a.tokens_tile : 0);  // of the request
                 ctx = w.r.L - w.r.n;
-                tok0 = w.tile() * a.tokens_tile;  // of the request
-                rows = min(a.tokens_tile, w.r.n - tok0) * a.G;
-                busy = quad * 32 < rows;          // the quarter has rows (uniform over the pair)
+                rows = min(a.tokens_tile, w.r.n - tok) * a.G;
+                busy = quad * 32 < rows;  // the quarter has rows
                 m_ref = -INFINITY, l = 0.f;
                 pg_begin = w.pg;
-                token = w.r.start + min(tok0 + row / a.G, w.r.n - 1);
+                token = w.r.start + min(tok + row / a.G, w.r.n - 1);
                 first_key = a.window > 0 ? max(0, min(ctx, max(a.positions[token], ctx) - a.window + 1)) : 0;
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[buf]), (j / C::kSBuf) & 1, abort_flag, a.status, 0x4c));
-            if (busy) {
+            const uint32_t tS = tS0 + buf * 128 + lane_base;
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[2 * set + buf]), use & 1, abort_flag, a.status, 0x4c));
+            if (busy && ok) {
+                // The scores are taken 64 at a time; the upper 64 stay in registers until their
+                // exponentials, the lower 64 are read again (128 of them would not fit beside the rest).
                 float s[64];
                 float mx = -INFINITY;
-                if (ok) {
-                    tc_fence_after();
-                    {
-                        uint32_t raw[2][32];
+                const int key0 = (w.r.pg0 + w.pg) * kPage;
+                const bool edge = __any_sync(0xffffffffu, key0 + 127 >= ctx || w.np < kTilePages || key0 < first_key);
+                auto load = [&](int half) {  // keys 64 half .. of the tile, hidden ones at -inf
+                    uint32_t raw[2][32];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) tmem_ld32(tS0 + buf * 128 + 64 * hf + c * 32 + lane_base, raw[c]);
-                        tmem_ld_wait();
+                    for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 * half + c * 32, raw[c]);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
-                    }
-                    const int key0 = (w.r.pg0 + w.pg) * kPage + 64 * hf;
-                    const int cols = w.np * kPage - 64 * hf;  // loaded keys of this half
-                    if (__any_sync(0xffffffffu, key0 + 63 >= ctx || cols < 64 || key0 < first_key)) {
-                        uint64_t vis = low_bits(cols) & ~low_bits(first_key - key0);
-                        const int dc = ctx - key0;  // column of the first drafted token
+                        for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
+                    if (edge) {
+                        const int k0 = key0 + 64 * half;
+                        uint64_t vis = low_bits(w.np * kPage - 64 * half) & ~low_bits(first_key - k0);
+                        const int dc = ctx - k0;  // column of the first drafted token
                         if (dc < 64) {
                             const int d0 = max(0, -dc), wi = d0 >> 5, sh = d0 & 31;
                             const int32_t* mw = a.mask + (size_t)token * a.words;
@@ -499,6 +625,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!(v1 >> c & 1u)) s[32 + c] = -INFINITY;
                         }
                     }
+                };
+                auto largest = [&]() {
                     float m8[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) m8[i] = s[i];
@@ -506,80 +634,82 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 8; c < 64; c += 8)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], s[c + i]);
-                    mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-                    xch[hf * 128 + row] = mx;
-                }
-                ok = named_bar_and(pair_bar, 64, ok);
-                if (!ok) break;
-                mx = fmaxf(mx, xch[(1 - hf) * 128 + row]);
-                named_bar_sync(pair_bar, 64);  // both read before the buffer is reused
+                    mx = fmaxf(mx, fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))));
+                };
+                tc_fence_after();
+                load(0);
+                largest();
+                load(1);
+                largest();
+                // The running maximum is lazy: it moves only when a row's tile maximum exceeds it by more than
+                // 2^8, so p stays below that and most tiles need no rescale.
                 const float m_tile = mx * a.scale_log2;
-                float alpha = 1.f;
-                const bool moved = m_tile > m_ref + kRescaleLog2;  // lazy: p stays below 2^8
-                if (moved) {
-                    alpha = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_tile);
-                    m_ref = m_tile;
-                }
-                const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                uint32_t pk[32];
-                // l sums p in fp32; the P of the product is rounded to bf16 (an MMA takes both operands
-                // in V's type), half a step of 2^-8 that averages out over the keys
-#pragma unroll
-                for (int c = 0; c < 64; c += 2) {
-                    const float p0 = fast_exp2(fmaf(s[c], a.scale_log2, -m_use));
-                    const float p1 = fast_exp2(fmaf(s[c + 1], a.scale_log2, -m_use));
-                    rs[(c >> 1) & 7] += p0 + p1;
-                    pk[c >> 1] = pack_bf16x2(p0, p1);
-                }
-                l = l * alpha + (((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7])));
-                if (!w.begins && __any_sync(0xffffffffu, moved)) {  // the same for the pair
-                    const int jp = j - 1;
-                    const bool okw = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[jp % C::kSBuf]), (jp / C::kSBuf) & 1,
-                                                                       abort_flag, a.status, 0x4d));
-                    ok = named_bar_and(pair_bar, 64, okw);
-                    if (!ok) break;
-                    tc_fence_after();
+                const bool moved = m_tile > m_ref + kRescaleLog2;
+                if (__any_sync(0xffffffffu, moved)) {
+                    const float alpha = !moved ? 1.f : m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_tile);
+                    if (moved) m_ref = m_tile;
+                    l *= alpha;
+                    if (!w.begins) {
+                        // P V of the set's step before, and so every earlier one, is complete
+                        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + prev]), prev_use & 1, abort_flag, a.status, 0x4d));
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll 1
-                    for (int c = hf * (C::kDV / 64); c < (hf + 1) * (C::kDV / 64); ++c) {
-                        uint32_t raw[32];
-                        tmem_ld32(tO + c * 32 + lane_base, raw);
-                        tmem_ld_wait();
+                        for (int c = 0; c < C::kDV / 32; ++c) {
+                            uint32_t raw[32];
+                            tmem_ld32(tOset + c * 32, raw);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
-                        tmem_st32(tO + c * 32 + lane_base, raw);
+                            for (int e = 0; e < 32; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
+                            tmem_st32(tOset + c * 32, raw);
+                        }
                     }
                 }
-                tmem_st32(tS0 + buf * 128 + 64 * hf + lane_base, pk);
+                const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                float2 rs[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(-m_use, -m_use);
+                // l sums p in fp32; the P of the product is rounded to bf16 (an MMA takes both operands
+                // in V's type), half a step of 2^-8 that averages out over the keys
+                auto exponentials = [&](int half) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 64; e += 2) {
+                        const float2 x2 = __ffma2_rn(make_float2(s[e], s[e + 1]), sc, mm);
+                        const float2 p2 = make_float2(fast_exp2(x2.x), fast_exp2(x2.y));
+                        rs[(e >> 1) & 1] = __fadd2_rn(rs[(e >> 1) & 1], p2);
+                        pk[e >> 1] = pack_bf16x2(p2.x, p2.y);
+                    }
+                    tmem_st32(tS + 64 * half, pk);
+                };
+                exponentials(1);
+                load(0);
+                exponentials(0);
+                l += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
                 tmem_st_wait();
                 tc_fence_before();
             }
             if (!ok) break;
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&p_full[buf]));
+            if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * set + buf]));
+            prev = buf, prev_use = use;
             if (!w.ends()) continue;
 
             // ---- the piece is done: results, or this CTA's partials --------------------------------
             // (a quarter without rows waits as well: its arrival on o_free must not run a piece ahead)
-            const bool okw = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[buf]), (j / C::kSBuf) & 1, abort_flag, a.status, 0x4e));
-            if (!busy) ok = okw;
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + buf]), use & 1, abort_flag, a.status, 0x4e));
+            if (!ok) break;
+            tc_fence_after();
             if (busy) {
-                xch[hf * 128 + row] = l;
-                ok = named_bar_and(pair_bar, 64, okw);
-                if (!ok) break;
-                tc_fence_after();
-                l += xch[(1 - hf) * 128 + row];
-                named_bar_sync(pair_bar, 64);
                 const bool from = pg_begin == 0, to = w.pg + w.np == w.r.npg;
                 const bool row_ok = row < rows;
-                const int head = w.head() * a.G + row % a.G, col0 = w.split() * C::kDV;
+                const int head = w.head * a.G + row % a.G, col0 = w.split * C::kDV;
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 uint16_t* orow = a.o + ((size_t)token * a.Hq + head) * D + col0;
-                float* prow = a.part + ((size_t)(2 * k + (from ? 1 : 0)) * a.rows_cap + row) * C::kRowF;
+                float* prow = a.part + ((size_t)(2 * k + (from ? 1 : 0)) * a.rows_cap + (w.dual && set ? 128 : 0) + row) * C::kRowF;
 #pragma unroll 1
-                for (int c = hf * (C::kDV / 64); c < (hf + 1) * (C::kDV / 64); ++c) {
+                for (int c = 0; c < C::kDV / 32; ++c) {
                     uint32_t raw[32];
-                    tmem_ld32(tO + c * 32 + lane_base, raw);
+                    tmem_ld32(tOset + c * 32, raw);
                     tmem_ld_wait();
                     if (!row_ok) continue;
                     if (from && to) {
@@ -598,29 +728,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<uint4*>(prow + c * 32 + e) = make_uint4(raw[e], raw[e + 1], raw[e + 2], raw[e + 3]);
                     }
                 }
-                if (row_ok && hf == 0) {
+                if (row_ok) {
                     if (!(from && to)) prow[C::kDV] = m_ref, prow[C::kDV + 1] = l;
                     else if (col0 == 0)
                         a.lse[(size_t)head * a.T + token] = l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
                 }
             }
-            if (!ok) break;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(o_free));
-            if (warp == 2 && lane == 0 && w.left == w.np) {  // the share's last piece
+            if (lane == 0) mbar_arrive(smem_u32(&o_free[set]));
+            // the share's last piece: does its segment go on elsewhere?
+            if (quad == 0 && lane == 0 && w.left == w.np && (!w.dual || set == 0)) {
                 TreeSpan sp = {};
                 if (pg_begin == 0 && w.pg + w.np < w.r.npg) {
                     const long long last = u1 - 1 + (w.r.npg - (w.pg + w.np));  // the segment's last unit
                     sp.ctas = owner_of(last, P, Gc) - k + 1;
-                    sp.row0 = w.r.start + tok0, sp.rows = rows, sp.head0 = w.head() * a.G, sp.col0 = w.split() * C::kDV;
+                    sp.row0 = w.r.start + w.tok0, sp.head0 = w.head * a.G, sp.col0 = w.split * C::kDV;
+                    sp.rows[0] = rows;
+                    sp.rows[1] = w.dual ? min(a.tokens_tile, w.r.n - w.tok0 - a.tokens_tile) * a.G : 0;
                 }
                 a.span[k] = sp;
             }
         }
     }
     __syncthreads();
-    if (warp == 1) {
+    if (warp == C::kIssuer) {
         tc_fence_after();
         tmem_dealloc(tbase, 512);
     }
@@ -641,8 +773,10 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a) {
     const TreeSpan sp = a.span[blockIdx.x];
     if (sp.ctas == 0) return;
     constexpr int VPR = C::kDV / 8;
-    for (int it = blockIdx.y * kMergeThreads + threadIdx.x; it < sp.rows * VPR; it += kMergeY * kMergeThreads) {
-        const int row = it / VPR, col = it % VPR * 8;
+    for (int it = blockIdx.y * kMergeThreads + threadIdx.x; it < (sp.rows[0] + sp.rows[1]) * VPR; it += kMergeY * kMergeThreads) {
+        const int r = it / VPR, col = it % VPR * 8;
+        const int second = r >= sp.rows[0], tile_row = second ? r - sp.rows[0] : r;
+        const int row = second * 128 + tile_row;  // of the partials
         float M = -INFINITY, l = 0.f, O[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int q0 = 0; q0 < sp.ctas; q0 += kFold) {
             float2 ml[kFold];
@@ -680,7 +814,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a) {
             M = Mn;
         }
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        const int token = sp.row0 + row / a.G, head = sp.head0 + row % a.G;
+        const int token = sp.row0 + second * a.tokens_tile + tile_row / a.G, head = sp.head0 + tile_row % a.G;
         uint4 x;
         x.x = pack_bf16x2(O[0] * inv, O[1] * inv), x.y = pack_bf16x2(O[2] * inv, O[3] * inv);
         x.z = pack_bf16x2(O[4] * inv, O[5] * inv), x.w = pack_bf16x2(O[6] * inv, O[7] * inv);
@@ -696,8 +830,9 @@ cudaError_t launch_t(const TreeLaunch& L, TreeArgs a, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(tree_paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
     // at most one CTA per tile of the longest step that fits the arguments
-    const long long tiles = (L.max_q + a.tokens_tile - 1) / a.tokens_tile;
-    const long long most = ((long long)L.max_pages * L.R * tiles * L.Hkv * C::kSplit + kMinPages - 1) / kMinPages;
+    const int tokens = a.tokens_tile * C::kSets;
+    const long long groups = (L.max_q + tokens - 1) / tokens;
+    const long long most = ((long long)L.max_pages * L.R * groups * L.Hkv * C::kSplit + kMinPages - 1) / kMinPages;
     int grid = L.sms < kMaxGrid ? L.sms : kMaxGrid;
     if (most < grid) grid = (int)most;
     cudaLaunchAttribute attr[1];
@@ -705,7 +840,7 @@ cudaError_t launch_t(const TreeLaunch& L, TreeArgs a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -724,9 +859,10 @@ cudaError_t launch_t(const TreeLaunch& L, TreeArgs a, cudaStream_t stream) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-int rows_cap(int G, int max_q) {
+// Rows of a partial: those of one row tile, or two tiles of 128.
+int rows_cap(int G, int max_q, int D) {
     const int tokens = 128 / G;
-    return (max_q < tokens ? max_q : tokens) * G;
+    return max_q <= tokens ? max_q * G : tree_sets(D) * 128;
 }
 constexpr size_t kSpanBytes = (kMaxGrid * sizeof(TreeSpan) + 255) & ~size_t(255);
 
@@ -736,7 +872,7 @@ int tree_tokens_per_tile(int G) { return 128 / G; }
 
 size_t tree_workspace_bytes(int G, int max_q, int D) {
     const int dv = D < 256 ? D : 256;
-    return kSpanBytes + (size_t)2 * kMaxGrid * rows_cap(G, max_q) * (dv + 4) * 4;
+    return kSpanBytes + (size_t)2 * kMaxGrid * rows_cap(G, max_q, D) * (dv + 4) * 4;
 }
 
 cudaError_t launch_tree_paged(const TreeLaunch& L, cudaStream_t stream) {
@@ -746,7 +882,7 @@ cudaError_t launch_tree_paged(const TreeLaunch& L, cudaStream_t stream) {
     a.span = static_cast<TreeSpan*>(L.workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(L.workspace) + kSpanBytes);
     a.R = L.R, a.T = L.T, a.max_q = L.max_q, a.words = L.words, a.Hq = L.Hq, a.Hkv = L.Hkv, a.G = L.Hq / L.Hkv;
-    a.tokens_tile = tree_tokens_per_tile(a.G), a.rows_cap = rows_cap(a.G, L.max_q);
+    a.tokens_tile = tree_tokens_per_tile(a.G), a.rows_cap = rows_cap(a.G, L.max_q, L.D);
     a.max_pages = L.max_pages, a.num_pages = L.num_pages, a.window = L.window;
     a.scale_log2 = L.scale * 1.4426950408889634f;
     switch (L.D) {
