@@ -550,10 +550,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                 if (last_use && (wp & kLast)) more_p = false;
                 return true;
             };
-            ok = issue_s();
-            if (ok && more_s) ok = issue_s();
-            while (ok && more_p) {
-                ok = issue_pv();
+            for (int step = 0; ok && more_p; ++step) {
+                if (step >= 2) ok = issue_pv();
                 if (ok && more_s) ok = issue_s();
             }
             umma_commit(smem_u32(mma_idle));
@@ -590,100 +588,100 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             const uint32_t tS = tS0 + buf * 128 + lane_base;
             ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[2 * set + buf]), use & 1, abort_flag, a.status, 0x4c));
             if (busy && ok) {
-                // The scores are taken 64 at a time; the upper 64 stay in registers until their
-                // exponentials, the lower 64 are read again (128 of them would not fit beside the rest).
+                // Two passes over the tile's scores, 64 at a time: the maximum of the lower and the upper half,
+                // then the exponentials of the upper half, still in registers, and of the lower one, read
+                // again. One loop, so that each part's code is there once: a CTA of a short call runs some
+                // twenty tiles, and unrolled the body's instruction fetches cost more than its arithmetic
+                // (batch of 64 at D = 128: 58 us unrolled).
                 float s[64];
                 float mx = -INFINITY;
+                float2 rs[2] = {{0.f, 0.f}, {0.f, 0.f}}, mm = {0.f, 0.f};
+                const float2 sc = make_float2(a.scale_log2, a.scale_log2);
                 const int key0 = (w.r.pg0 + w.pg) * kPage;
                 const bool edge = __any_sync(0xffffffffu, key0 + 127 >= ctx || w.np < kTilePages || key0 < first_key);
-                auto load = [&](int half) {  // keys 64 half .. of the tile, hidden ones at -inf
-                    uint32_t raw[2][32];
+                tc_fence_after();
+#pragma unroll 1
+                for (int pass = 0; pass < 4; ++pass) {
+                    const int half = pass == 1 || pass == 2;
+                    if (pass != 2) {  // scores of keys 64 half .. of the tile, hidden ones at -inf
+                        uint32_t raw[2][32];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 * half + c * 32, raw[c]);
-                    tmem_ld_wait();
+                        for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 * half + c * 32, raw[c]);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
-                    if (edge) {
-                        const int k0 = key0 + 64 * half;
-                        uint64_t vis = low_bits(w.np * kPage - 64 * half) & ~low_bits(first_key - k0);
-                        const int dc = ctx - k0;  // column of the first drafted token
-                        if (dc < 64) {
-                            const int d0 = max(0, -dc), wi = d0 >> 5, sh = d0 & 31;
-                            const int32_t* mw = a.mask + (size_t)token * a.words;
-                            auto word = [&](int i) -> uint64_t { return i < a.words ? (uint64_t)(uint32_t)mw[i] : 0ull; };
-                            uint64_t bits = (word(wi) | word(wi + 1) << 32) >> sh;
-                            if (sh) bits |= word(wi + 2) << (64 - sh);
-                            bits &= low_bits(w.r.n - d0);
-                            vis &= low_bits(dc) | bits << max(dc, 0);
-                        }
-                        const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
+                            for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
+                        if (edge) {
+                            const int k0 = key0 + 64 * half;
+                            uint64_t vis = low_bits(w.np * kPage - 64 * half) & ~low_bits(first_key - k0);
+                            const int dc = ctx - k0;  // column of the first drafted token
+                            if (dc < 64) {
+                                const int d0 = max(0, -dc), wi = d0 >> 5, sh = d0 & 31;
+                                const int32_t* mw = a.mask + (size_t)token * a.words;
+                                auto word = [&](int i) -> uint64_t { return i < a.words ? (uint64_t)(uint32_t)mw[i] : 0ull; };
+                                uint64_t bits = (word(wi) | word(wi + 1) << 32) >> sh;
+                                if (sh) bits |= word(wi + 2) << (64 - sh);
+                                bits &= low_bits(w.r.n - d0);
+                                vis &= low_bits(dc) | bits << max(dc, 0);
+                            }
+                            const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            if (!(v0 >> c & 1u)) s[c] = -INFINITY;
-                            if (!(v1 >> c & 1u)) s[32 + c] = -INFINITY;
+                            for (int c = 0; c < 32; ++c) {
+                                if (!(v0 >> c & 1u)) s[c] = -INFINITY;
+                                if (!(v1 >> c & 1u)) s[32 + c] = -INFINITY;
+                            }
                         }
                     }
-                };
-                auto largest = [&]() {
-                    float m8[8];
+                    if (pass < 2) {
+                        float m8[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) m8[i] = s[i];
+                        for (int i = 0; i < 8; ++i) m8[i] = s[i];
 #pragma unroll
-                    for (int c = 8; c < 64; c += 8)
+                        for (int c = 8; c < 64; c += 8)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], s[c + i]);
-                    mx = fmaxf(mx, fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))));
-                };
-                tc_fence_after();
-                load(0);
-                largest();
-                load(1);
-                largest();
-                // The running maximum is lazy: it moves only when a row's tile maximum exceeds it by more than
-                // 2^8, so p stays below that and most tiles need no rescale.
-                const float m_tile = mx * a.scale_log2;
-                const bool moved = m_tile > m_ref + kRescaleLog2;
-                if (__any_sync(0xffffffffu, moved)) {
-                    const float alpha = !moved ? 1.f : m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_tile);
-                    if (moved) m_ref = m_tile;
-                    l *= alpha;
-                    if (!w.begins) {
-                        // P V of the set's step before, and so every earlier one, is complete
-                        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + prev]), prev_use & 1, abort_flag, a.status, 0x4d));
-                        if (!ok) break;
-                        tc_fence_after();
+                            for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], s[c + i]);
+                        mx = fmaxf(mx, fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))));
+                        if (pass == 0) continue;
+                        // The running maximum is lazy: it moves only when a row's tile maximum exceeds it by more
+                        // than 2^8, so p stays below that and most tiles need no rescale.
+                        const float m_tile = mx * a.scale_log2;
+                        const bool moved = m_tile > m_ref + kRescaleLog2;
+                        if (__any_sync(0xffffffffu, moved)) {
+                            const float alpha = !moved ? 1.f : m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_tile);
+                            if (moved) m_ref = m_tile;
+                            l *= alpha;
+                            if (!w.begins) {
+                                // P V of the set's step before, and so every earlier one, is complete
+                                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + prev]), prev_use & 1, abort_flag, a.status, 0x4d));
+                                if (!ok) break;
+                                tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < C::kDV / 32; ++c) {
-                            uint32_t raw[32];
-                            tmem_ld32(tOset + c * 32, raw);
-                            tmem_ld_wait();
+                                for (int c = 0; c < C::kDV / 16; ++c) {
+                                    uint32_t raw[16];
+                                    tmem_ld16(tOset + c * 16, raw);
+                                    tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
-                            tmem_st32(tOset + c * 32, raw);
+                                    for (int e = 0; e < 16; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
+                                    tmem_st16(tOset + c * 16, raw);
+                                }
+                            }
                         }
+                        mm.x = mm.y = m_ref == -INFINITY ? 0.f : -m_ref;
+                    } else {
+                        // l sums p in fp32; the P of the product is rounded to bf16 (an MMA takes both operands
+                        // in V's type), half a step of 2^-8 that averages out over the keys
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int e = 0; e < 64; e += 2) {
+                            const float2 x2 = __ffma2_rn(make_float2(s[e], s[e + 1]), sc, mm);
+                            const float2 p2 = make_float2(fast_exp2(x2.x), fast_exp2(x2.y));
+                            rs[(e >> 1) & 1] = __fadd2_rn(rs[(e >> 1) & 1], p2);
+                            pk[e >> 1] = pack_bf16x2(p2.x, p2.y);
+                        }
+                        tmem_st32(tS + 64 * half, pk);
                     }
                 }
-                const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                float2 rs[2] = {{0.f, 0.f}, {0.f, 0.f}};
-                const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(-m_use, -m_use);
-                // l sums p in fp32; the P of the product is rounded to bf16 (an MMA takes both operands
-                // in V's type), half a step of 2^-8 that averages out over the keys
-                auto exponentials = [&](int half) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int e = 0; e < 64; e += 2) {
-                        const float2 x2 = __ffma2_rn(make_float2(s[e], s[e + 1]), sc, mm);
-                        const float2 p2 = make_float2(fast_exp2(x2.x), fast_exp2(x2.y));
-                        rs[(e >> 1) & 1] = __fadd2_rn(rs[(e >> 1) & 1], p2);
-                        pk[e >> 1] = pack_bf16x2(p2.x, p2.y);
-                    }
-                    tmem_st32(tS + 64 * half, pk);
-                };
-                exponentials(1);
-                load(0);
-                exponentials(0);
                 l += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
                 tmem_st_wait();
                 tc_fence_before();
