@@ -147,19 +147,19 @@ template <int D>
 struct Walk {
     using C = TreeCfg<D>;
     Req r;
-    int b, seg, pg, np;  // request, segment in it, first page (from pg0) and pages of the tile
+    int b, seg, pg, np;     // request, segment in it, first page (from pg0) and pages of the tile
     int head, split, tok0;  // of the segment; tok0: first drafted token of its rows
-    long long left;      // pages of the share from here on
-    bool begins;         // first tile of a piece (a segment's pages in this CTA)
-    bool dual;           // two row tiles: one for each set
-    int set;             // the set that takes the piece (dual: both)
-    int turn;            // the next single piece's set
+    int left;               // pages of the share from here on
+    bool begins, ends;      // first / last tile of a piece (a segment's pages in this CTA)
+    bool dual;              // two row tiles: one for each set
+    int set;                // the set that takes the piece (dual: both)
+    int turn;               // the next single piece's set
 
-    __device__ __forceinline__ void start(const TreeArgs& a, int b_, long long off, long long units) {
+    __device__ __forceinline__ void start(const TreeArgs& a, int b_, int off, int units) {
         b = b_;
         r = load_req<D>(a, b);
-        seg = (int)(off / r.npg);
-        pg = (int)(off - (long long)seg * r.npg);
+        seg = off / r.npg;
+        pg = off - seg * r.npg;
         left = units;
         turn = 0;
         piece(a);
@@ -176,17 +176,17 @@ struct Walk {
         if (C::kSets == 2 && !dual) set = turn, turn ^= 1;
     }
     __device__ __forceinline__ void size() {
-        np = min(kTilePages, r.npg - pg);
-        if (left < np) np = (int)left;
+        const int most = min(r.npg - pg, left);
+        np = min(kTilePages, most);
+        ends = np == most;
     }
     __device__ __forceinline__ bool more() const { return left > 0; }
-    __device__ __forceinline__ bool ends() const { return pg + np == r.npg || left == np; }
     __device__ __forceinline__ void next(const TreeArgs& a) {
         pg += np, left -= np;
         begins = false;
-        if (left <= 0) return;
-        if (pg == r.npg) {
-            pg = 0;
+        if (ends) {
+            if (left == 0) return;
+            pg = 0;  // a piece ends before the share does only with its segment
             if (++seg == r.groups * a.Hkv * C::kSplit) {
                 seg = 0;
                 do r = load_req<D>(a, ++b);  // the share holds more units: there is another request
@@ -199,7 +199,7 @@ struct Walk {
     // what the issuer and the fixer need of the tile
     __device__ __forceinline__ uint32_t word() const {
         const int tail = pg + np == r.npg ? r.L % kPage : 0;  // rows of its last page, if slots of it lie past L
-        return (uint32_t)np | (uint32_t)tail << 4 | (begins ? kBegins : 0u) | (ends() ? kEnds : 0u) | (dual ? kDual : 0u) |
+        return (uint32_t)np | (uint32_t)tail << 4 | (begins ? kBegins : 0u) | (ends ? kEnds : 0u) | (dual ? kDual : 0u) |
                (set ? kSet1 : 0u) | (left == np ? kLast : 0u);
     }
     // whether set s works on the piece
@@ -208,9 +208,11 @@ struct Walk {
 
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
-// CTA that owns unit u when P units are split evenly over G CTAs.
-__device__ __forceinline__ int owner_of(long long u, long long P, int G) {
-    return (int)(((u + 1) * (long long)G - 1) / P);
+// P units over G CTAs: the first P % G of them take one more than the others.
+__device__ __forceinline__ int share_start(int k, int q, int rem) { return k * q + min(k, rem); }
+__device__ __forceinline__ int owner_of(int u, int q, int rem) {
+    const int big = rem * (q + 1);
+    return u < big ? u / (q + 1) : rem + (u - big) / q;
 }
 
 template <int D>
@@ -239,8 +241,9 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
     uint32_t* words = reinterpret_cast<uint32_t*>(mma_idle + 1);  // [kStages] the copies' words
     uint32_t* tmem_slot = words + C::kStages;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    long long* scan = reinterpret_cast<long long*>(smem + C::kOffScan);  // [kWarps], then the share's start
-    static_assert((3 * C::kStages + 19) * 8 + C::kStages * 4 + 8 <= 512 && (C::kWarps + 2) * 8 <= 192, "barrier area");
+    long long* scan = reinterpret_cast<long long*>(smem + C::kOffScan);  // [kWarps]
+    int* first = reinterpret_cast<int*>(scan + C::kWarps);               // where the share starts
+    static_assert((3 * C::kStages + 19) * 8 + C::kStages * 4 + 8 <= 512 && (C::kWarps + 1) * 8 <= 192, "barrier area");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int k = blockIdx.x;
 
@@ -296,15 +299,21 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
         if (w < warp) x += scan[w];
         P += scan[w];
     }
-    const long long want = (P + kMinPages - 1) / kMinPages;
-    const int Gc = (int)(want < (long long)gridDim.x ? want : (long long)gridDim.x);
+    // (a step of 2^31 page visits or more, far beyond what a cache can hold, is reported and left alone)
+    if (P > 0x7fffffffll) {
+        if (tid == 0 && k == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
+        P = 0;
+    }
+    const int units = (int)P;
+    const int Gc = units > 0 ? min((units - 1) / kMinPages + 1, (int)gridDim.x) : 0;
     const bool works = k < Gc;  // uniform
-    const long long u0 = works ? (long long)k * P / Gc : 0, u1 = works ? (long long)(k + 1) * P / Gc : 0;
+    const int q = works ? units / Gc : 0, rem = units - q * Gc;
+    const int u0 = share_start(k, q, rem), share = works ? q + (k < rem) : 0;
     if (works && x <= u0 && u0 < x + sum) {
         for (int b = b0; b < b1; ++b) {
             const long long n = req_units<D>(a, load_req<D>(a, b));
             if (u0 < x + n) {
-                scan[C::kWarps] = b, scan[C::kWarps + 1] = u0 - x;
+                first[0] = b, first[1] = u0 - (int)x;
                 break;
             }
             x += n;
@@ -316,8 +325,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
     const uint32_t tO = tbase, tS0 = tbase + 256;
-    const int first_b = (int)scan[C::kWarps];
-    const long long first_off = scan[C::kWarps + 1];
+    const int first_b = first[0], first_off = first[1];
     // The ring's slots go round in the order of the copies. One set: K and V slots in the issuer's order, K(0)
     // K(1) V(0) K(2) V(1) .. (a K tile of D = 512 is longer than the ring). Two sets: K(0) V(0) K(1) V(1) ..,
     // since two row tiles return to a key tile's slots: tile i's K is copy 2 i, its V copy 2 i + 1.
@@ -369,7 +377,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             return true;
         };
         Walk<D> wk, wv;
-        wk.start(a, first_b, first_off, u1 - u0);
+        wk.start(a, first_b, first_off, share);
         wv = wk;
         int idk = page_id(wk), idv = idk;
         auto load_k = [&]() -> bool {
@@ -566,15 +574,18 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
         const uint32_t tOset = tO + set * C::kDV + lane_base;
         float m_ref = -INFINITY, l = 0.f;
         int first_key = 0, token = 0, pg_begin = 0, rows = 0, ctx = 0;
-        int step = 0, uses[2] = {0, 0};  // global step of the tile; the set's uses of each buffer
-        int prev = 0, prev_use = 0;      // buffer of the set's step before, and which use of it
+        int step = 0;                       // global step of the tile (its parity: the score buffer)
+        uint32_t phases = 0u;               // of the set's two buffers
+        int prev = 0;                       // the set's step before: buffer, and its phase
+        uint32_t prev_phase = 0u;
         bool busy = false, ok = true;
         Walk<D> w;
-        w.start(a, first_b, first_off, u1 - u0);
+        w.start(a, first_b, first_off, share);
         for (; ok && w.more(); step += w.dual ? 2 : 1, w.next(a)) {
             if (!w.mine(set)) continue;
             const int buf = (step + (w.dual ? set : 0)) & 1;
-            const int use = buf ? uses[1]++ : uses[0]++;
+            const uint32_t phase = phases >> buf & 1u;
+            phases ^= 1u << buf;
             if (w.begins) {
                 const int tok = w.tok0 + (w.dual && set ? a.tokens_tile : 0);  // of the request
                 ctx = w.r.L - w.r.n;
@@ -586,7 +597,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                 first_key = a.window > 0 ? max(0, min(ctx, max(a.positions[token], ctx) - a.window + 1)) : 0;
             }
             const uint32_t tS = tS0 + buf * 128 + lane_base;
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[2 * set + buf]), use & 1, abort_flag, a.status, 0x4c));
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[2 * set + buf]), phase, abort_flag, a.status, 0x4c));
             if (busy && ok) {
                 // Two passes over the tile's scores, 64 at a time: the maximum of the lower and the upper half,
                 // then the exponentials of the upper half, still in registers, and of the lower one, read
@@ -653,7 +664,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                             l *= alpha;
                             if (!w.begins) {
                                 // P V of the set's step before, and so every earlier one, is complete
-                                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + prev]), prev_use & 1, abort_flag, a.status, 0x4d));
+                                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + prev]), prev_phase, abort_flag, a.status, 0x4d));
                                 if (!ok) break;
                                 tc_fence_after();
 #pragma unroll 1
@@ -689,12 +700,12 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             if (!ok) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * set + buf]));
-            prev = buf, prev_use = use;
-            if (!w.ends()) continue;
+            prev = buf, prev_phase = phase;
+            if (!w.ends) continue;
 
             // ---- the piece is done: results, or this CTA's partials --------------------------------
             // (a quarter without rows waits as well: its arrival on o_free must not run a piece ahead)
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + buf]), use & 1, abort_flag, a.status, 0x4e));
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + buf]), phase, abort_flag, a.status, 0x4e));
             if (!ok) break;
             tc_fence_after();
             if (busy) {
@@ -739,8 +750,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             if (quad == 0 && lane == 0 && w.left == w.np && (!w.dual || set == 0)) {
                 TreeSpan sp = {};
                 if (pg_begin == 0 && w.pg + w.np < w.r.npg) {
-                    const long long last = u1 - 1 + (w.r.npg - (w.pg + w.np));  // the segment's last unit
-                    sp.ctas = owner_of(last, P, Gc) - k + 1;
+                    // the segment's last unit
+                    sp.ctas = owner_of(u0 + share - 1 + (w.r.npg - (w.pg + w.np)), q, rem) - k + 1;
                     sp.row0 = w.r.start + w.tok0, sp.head0 = w.head * a.G, sp.col0 = w.split * C::kDV;
                     sp.rows[0] = rows;
                     sp.rows[1] = w.dual ? min(a.tokens_tile, w.r.n - w.tok0 - a.tokens_tile) * a.G : 0;
