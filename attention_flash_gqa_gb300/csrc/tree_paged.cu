@@ -16,13 +16,14 @@
 //    keys and 33 to 64 drafts, Hq 32, Hkv 8, D 128: alone, each of the two row tiles read all of K and
 //    V from DRAM). Otherwise consecutive segments alternate between the sets: one set's epilogue runs
 //    beside the other's first tiles.
-//  * A unit of work is one page (16 keys) of one segment = (request, KV head, 256-column half of O at
-//    D = 512, row tile or pair of them). All units are laid end to end and CTA k takes the k-th equal
-//    share: it may finish one segment, run through some and start another. A segment that one CTA
-//    covers is written out by it; of a shared one every CTA leaves (O, m, l) unnormalised in the
-//    workspace and tree_merge_kernel combines them (launched with programmatic serialisation).
-//  * Inside a CTA the pages are taken in tiles of up to eight (128 keys) through an mbarrier ring, and
-//    the pipeline runs on across segments. Tensor memory: O (fp32, up to 256 columns in all) and two
+//  * A unit of work is one key tile, up to eight pages (128 keys), of one segment = (request, KV head,
+//    256-column half of O at D = 512, row tile or pair of them). All units are laid end to end and CTA k
+//    takes the k-th equal share: it may finish one segment, run through some and start another. (Equal
+//    shares of pages left some CTAs a third more tiles than others, and a tile costs the softmax the same
+//    however few pages it has.) A segment that one CTA covers is written out by it; of a shared one every
+//    CTA leaves (O, m, l) unnormalised in the workspace and tree_merge_kernel combines them (launched
+//    with programmatic serialisation).
+//  * The tiles go through an mbarrier ring, and the pipeline runs on across segments. Tensor memory: O (fp32, up to 256 columns in all) and two
 //    score buffers of 128 columns, P (bf16) over the scores. Only the pages of a tile that exist are
 //    loaded and multiplied (N of Q K^T and K of P V follow them, a page being one K step of 16), so
 //    only the last page's slots past L need care: a fixer warp zeroes those V rows before their P V (P
@@ -47,7 +48,6 @@ constexpr int kTilePages = 8;
 constexpr int kSetWarps = 4;
 constexpr uint32_t kSubBytes = 16384;  // 128 rows x 64 bf16
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kMinPages = 8;   // a CTA's share at least: one tile
 constexpr int kMaxGrid = 192;  // sizes the workspace
 
 __host__ __device__ constexpr int tree_sets(int D) { return D <= 128 ? 2 : 1; }
@@ -104,7 +104,7 @@ struct TreeArgs {
 
 // A request as the walk sees it; no units if it is empty or inconsistent.
 struct Req {
-    int start, n, L, pg0, npg, groups;  // groups: row tiles, or pairs of them
+    int start, n, L, pg0, npg, tiles, groups;  // tiles: key tiles; groups: row tiles, or pairs of them
     bool bad;
 };
 template <int D>
@@ -116,19 +116,20 @@ __device__ __forceinline__ Req load_req(const TreeArgs& a, int b) {
     r.bad = r.start < 0 || r.n < 0 || r.n > a.max_q || r.start > a.T - r.n || r.n > r.L ||
             (long long)r.L > (long long)a.max_pages * kPage;
     if (r.bad || r.n == 0) {
-        r.n = r.npg = r.pg0 = r.groups = 0;
+        r.n = r.npg = r.pg0 = r.tiles = r.groups = 0;
         return r;
     }
     const int c = r.L - r.n;
     r.pg0 = a.window > 0 && c >= a.window ? (c - a.window + 1) / kPage : 0;  // no row sees an earlier key
     r.npg = (r.L + kPage - 1) / kPage - r.pg0;
+    r.tiles = (r.npg + kTilePages - 1) / kTilePages;
     const int tokens = a.tokens_tile * TreeCfg<D>::kSets;
     r.groups = (r.n + tokens - 1) / tokens;
     return r;
 }
 template <int D>
 __device__ __forceinline__ long long req_units(const TreeArgs& a, const Req& r) {
-    return (long long)r.npg * r.groups * a.Hkv * TreeCfg<D>::kSplit;
+    return (long long)r.tiles * r.groups * a.Hkv * TreeCfg<D>::kSplit;
 }
 
 // A copy's word: pages of the tile in bits 0-3, rows of its last page to keep in bits 4-7 (0: all), and
@@ -149,7 +150,7 @@ struct Walk {
     Req r;
     int b, seg, pg, np;     // request, segment in it, first page (from pg0) and pages of the tile
     int head, split, tok0;  // of the segment; tok0: first drafted token of its rows
-    int left;               // pages of the share from here on
+    int left;               // tiles of the share from here on
     bool begins, ends;      // first / last tile of a piece (a segment's pages in this CTA)
     bool dual;              // two row tiles: one for each set
     int set;                // the set that takes the piece (dual: both)
@@ -158,8 +159,8 @@ struct Walk {
     __device__ __forceinline__ void start(const TreeArgs& a, int b_, int off, int units) {
         b = b_;
         r = load_req<D>(a, b);
-        seg = off / r.npg;
-        pg = off - seg * r.npg;
+        seg = off / r.tiles;
+        pg = (off - seg * r.tiles) * kTilePages;
         left = units;
         turn = 0;
         piece(a);
@@ -176,13 +177,12 @@ struct Walk {
         if (C::kSets == 2 && !dual) set = turn, turn ^= 1;
     }
     __device__ __forceinline__ void size() {
-        const int most = min(r.npg - pg, left);
-        np = min(kTilePages, most);
-        ends = np == most;
+        np = min(kTilePages, r.npg - pg);
+        ends = pg + np == r.npg || left == 1;
     }
     __device__ __forceinline__ bool more() const { return left > 0; }
     __device__ __forceinline__ void next(const TreeArgs& a) {
-        pg += np, left -= np;
+        pg += np, --left;
         begins = false;
         if (ends) {
             if (left == 0) return;
@@ -200,7 +200,7 @@ struct Walk {
     __device__ __forceinline__ uint32_t word() const {
         const int tail = pg + np == r.npg ? r.L % kPage : 0;  // rows of its last page, if slots of it lie past L
         return (uint32_t)np | (uint32_t)tail << 4 | (begins ? kBegins : 0u) | (ends ? kEnds : 0u) | (dual ? kDual : 0u) |
-               (set ? kSet1 : 0u) | (left == np ? kLast : 0u);
+               (set ? kSet1 : 0u) | (left == 1 ? kLast : 0u);
     }
     // whether set s works on the piece
     __device__ __forceinline__ bool mine(int s) const { return dual || set == s; }
@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
         *abort_flag = 0;
         fence_mbar_init();
     }
+    if (tid == C::kProducer * 32) prefetch_tmap(&tq), prefetch_tmap(&tk), prefetch_tmap(&tv);
     if (warp == C::kIssuer) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
@@ -299,25 +300,29 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
         if (w < warp) x += scan[w];
         P += scan[w];
     }
-    // (a step of 2^31 page visits or more, far beyond what a cache can hold, is reported and left alone)
+    // (a step of 2^31 tiles or more, far beyond what a cache can hold, is reported and left alone)
     if (P > 0x7fffffffll) {
         if (tid == 0 && k == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
         P = 0;
     }
     const int units = (int)P;
-    const int Gc = units > 0 ? min((units - 1) / kMinPages + 1, (int)gridDim.x) : 0;
+    const int Gc = min(units, (int)gridDim.x);
     const bool works = k < Gc;  // uniform
     const int q = works ? units / Gc : 0, rem = units - q * Gc;
     const int u0 = share_start(k, q, rem), share = works ? q + (k < rem) : 0;
     if (works && x <= u0 && u0 < x + sum) {
-        for (int b = b0; b < b1; ++b) {
-            const long long n = req_units<D>(a, load_req<D>(a, b));
-            if (u0 < x + n) {
-                first[0] = b, first[1] = u0 - (int)x;
-                break;
-            }
+        Req r;
+        int b = b0, off = 0;
+        for (;; ++b) {
+            r = load_req<D>(a, b);
+            const long long n = req_units<D>(a, r);
+            off = u0 - (int)x;
+            if (off < n) break;
             x += n;
         }
+        first[0] = b, first[1] = off;
+        // the producer's first page ids, on their way while the CTA meets
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.block_table + (size_t)b * a.max_pages + r.pg0 + off % r.tiles * kTilePages));
     }
     if (tid == 0) a.span[k].ctas = 0;  // until the share's last piece says otherwise
     tc_fence_before();
@@ -334,21 +339,18 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
         // no units left for this CTA
     } else if (warp == C::kProducer) {
         // ------------------------------- TMA producer ----------------------------------------
-        if (lane == 0) prefetch_tmap(&tq), prefetch_tmap(&tk), prefetch_tmap(&tv);
         int slot = 0, round = 0;
         bool ok = true;
         int q_uses[2] = {0, 0};
-        auto page_id = [&](const Walk<D>& w) -> int {  // lane i: id of the tile's page i
-            if (lane >= w.np) return 0;
-            int id = a.block_table[(size_t)w.b * a.max_pages + w.r.pg0 + w.pg + lane];
+        auto page_id = [&](const Walk<D>& w) -> int {  // lane i: id of the tile's page i (checked at its use)
+            return lane < w.np ? a.block_table[(size_t)w.b * a.max_pages + w.r.pg0 + w.pg + lane] : 0;
+        };
+        // one slot: np pages, lane i loads page i's 16 rows x kSlotCols columns
+        auto load_slot = [&](const CUtensorMap* map, int chunk, int np, int id, uint32_t word) -> bool {
             if (id < 0 || id >= a.num_pages) {
                 atomicOr(a.status, DEVSTAT_BOUNDS);
                 id = 0;
             }
-            return id;
-        };
-        // one slot: np pages, lane i loads page i's 16 rows x kSlotCols columns
-        auto load_slot = [&](const CUtensorMap* map, int chunk, int np, int id, uint32_t word) -> bool {
             if (round > 0 && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[slot]), (round - 1) & 1, abort_flag, a.status, 0x41)))
                 return false;
             const uint32_t fb = smem_u32(&full[slot]);
@@ -747,11 +749,11 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&o_free[set]));
             // the share's last piece: does its segment go on elsewhere?
-            if (quad == 0 && lane == 0 && w.left == w.np && (!w.dual || set == 0)) {
+            if (quad == 0 && lane == 0 && w.left == 1 && (!w.dual || set == 0)) {
                 TreeSpan sp = {};
                 if (pg_begin == 0 && w.pg + w.np < w.r.npg) {
                     // the segment's last unit
-                    sp.ctas = owner_of(u0 + share - 1 + (w.r.npg - (w.pg + w.np)), q, rem) - k + 1;
+                    sp.ctas = owner_of(u0 + share - 1 + (w.r.npg - (w.pg + w.np) + kTilePages - 1) / kTilePages, q, rem) - k + 1;
                     sp.row0 = w.r.start + w.tok0, sp.head0 = w.head * a.G, sp.col0 = w.split * C::kDV;
                     sp.rows[0] = rows;
                     sp.rows[1] = w.dual ? min(a.tokens_tile, w.r.n - w.tok0 - a.tokens_tile) * a.G : 0;
@@ -841,7 +843,7 @@ cudaError_t launch_t(const TreeLaunch& L, TreeArgs a, cudaStream_t stream) {
     // at most one CTA per tile of the longest step that fits the arguments
     const int tokens = a.tokens_tile * C::kSets;
     const long long groups = (L.max_q + tokens - 1) / tokens;
-    const long long most = ((long long)L.max_pages * L.R * groups * L.Hkv * C::kSplit + kMinPages - 1) / kMinPages;
+    const long long most = ((long long)L.max_pages + kTilePages) / kTilePages * L.R * groups * L.Hkv * C::kSplit;
     int grid = L.sms < kMaxGrid ? L.sms : kMaxGrid;
     if (most < grid) grid = (int)most;
     cudaLaunchAttribute attr[1];
