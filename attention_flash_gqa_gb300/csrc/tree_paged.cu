@@ -215,7 +215,7 @@ __device__ __forceinline__ int owner_of(int u, int q, int rem) {
     return u < big ? u / (q + 1) : rem + (u - big) / q;
 }
 
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
     tree_paged_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ TreeArgs a) {
@@ -337,6 +337,263 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
 
     if (!works) {
         // no units left for this CTA
+    } else if (warp < C::kSets * kSetWarps) {
+        // Registers for a row of scores: 12 warps at 168 are 64512, and 8 x 32 x 208 + 4 x 32 x 80 = 63488 of
+        // them are handed out again.
+        if constexpr (WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        // --------------------------------- softmax ----------------------------------------------
+        const int set = warp / kSetWarps, quad = warp & 3;
+        const int row = quad * 32 + lane;  // row of the tile = TMEM lane
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        const uint32_t tOset = tO + set * C::kDV + lane_base;
+        float m_ref = -INFINITY, l = 0.f;
+        int first_key = 0, token = 0, pg_begin = 0, rows = 0, ctx = 0;
+        int step = 0;                       // global step of the tile (its parity: the score buffer)
+        uint32_t phases = 0u;               // of the set's two buffers
+        int prev = 0;                       // the set's step before: buffer, and its phase
+        uint32_t prev_phase = 0u;
+        bool busy = false, ok = true;
+        Walk<D> w;
+        w.start(a, first_b, first_off, share);
+        for (; ok && w.more(); step += w.dual ? 2 : 1, w.next(a)) {
+            if (!w.mine(set)) continue;
+            const int buf = (step + (w.dual ? set : 0)) & 1;
+            const uint32_t phase = phases >> buf & 1u;
+            phases ^= 1u << buf;
+            if (w.begins) {
+                const int tok = w.tok0 + (w.dual && set ? a.tokens_tile : 0);  // of the request
+                ctx = w.r.L - w.r.n;
+                rows = min(a.tokens_tile, w.r.n - tok) * a.G;
+                busy = quad * 32 < rows;  // the quarter has rows
+                m_ref = -INFINITY, l = 0.f;
+                pg_begin = w.pg;
+                token = w.r.start + min(tok + row / a.G, w.r.n - 1);
+                first_key = a.window > 0 ? max(0, min(ctx, max(a.positions[token], ctx) - a.window + 1)) : 0;
+            }
+            const uint32_t tS = tS0 + buf * 128 + lane_base;
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[2 * set + buf]), phase, abort_flag, a.status, 0x4c));
+            if (busy && ok) {
+                const int key0 = (w.r.pg0 + w.pg) * kPage;
+                const bool edge = __any_sync(0xffffffffu, key0 + 127 >= ctx || w.np < kTilePages || key0 < first_key);
+                auto visible = [&](int half) -> uint64_t {  // the row's visible keys of 64 half .. of the tile
+                    const int k0 = key0 + 64 * half;
+                    uint64_t vis = low_bits(w.np * kPage - 64 * half) & ~low_bits(first_key - k0);
+                    const int dc = ctx - k0;  // column of the first drafted token
+                    if (dc < 64) {
+                        const int d0 = max(0, -dc), wi = d0 >> 5, sh = d0 & 31;
+                        const int32_t* mw = a.mask + (size_t)token * a.words;
+                        auto word = [&](int i) -> uint64_t { return i < a.words ? (uint64_t)(uint32_t)mw[i] : 0ull; };
+                        uint64_t bits = (word(wi) | word(wi + 1) << 32) >> sh;
+                        if (sh) bits |= word(wi + 2) << (64 - sh);
+                        bits &= low_bits(w.r.n - d0);
+                        vis &= low_bits(dc) | bits << max(dc, 0);
+                    }
+                    return vis;
+                };
+                // The running maximum is lazy: it moves only when a row's tile maximum exceeds it by more than
+                // 2^8, so p stays below that and most tiles need no rescale.
+                auto move_max = [&](float mx) -> bool {
+                    const float m_tile = mx * a.scale_log2;
+                    const bool moved = m_tile > m_ref + kRescaleLog2;
+                    if (!__any_sync(0xffffffffu, moved)) return true;
+                    const float alpha = !moved ? 1.f : m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_tile);
+                    if (moved) m_ref = m_tile;
+                    l *= alpha;
+                    if (w.begins) return true;
+                    // P V of the set's step before, and so every earlier one, is complete
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + prev]), prev_phase, abort_flag, a.status, 0x4d));
+                    if (!ok) return false;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < C::kDV / 16; ++c) {
+                        uint32_t raw[16];
+                        tmem_ld16(tOset + c * 16, raw);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
+                        tmem_st16(tOset + c * 16, raw);
+                    }
+                    return true;
+                };
+                float2 rs[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+                tc_fence_after();
+                // l sums p in fp32; the P of the product is rounded to bf16 (an MMA takes both operands in V's
+                // type), half a step of 2^-8 that averages out over the keys.
+                // WIDE: the whole row of 128 scores in registers (12 long contexts, two row tiles: 172 us against
+                // 184 in the other form). Otherwise two passes over the tile, 64 scores at a time: the maximum of
+                // the lower and the upper half, then the exponentials of the upper half, still in registers, and
+                // of the lower one, read again. One loop, so that each part's code is there once: a CTA of a short
+                // call runs some twenty tiles, and the instruction fetches of a longer body cost more than they
+                // save (batch of 64: 43.6 us against 49.8).
+                if constexpr (WIDE) {
+                    float s[128];
+                    {
+                        uint32_t raw[4][32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, raw[c]);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
+                    }
+                    if (edge) {  // hidden keys to -inf
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint64_t vis = visible(half);
+                            const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                if (!(v0 >> c & 1u)) s[64 * half + c] = -INFINITY;
+                                if (!(v1 >> c & 1u)) s[64 * half + 32 + c] = -INFINITY;
+                            }
+                        }
+                    }
+                    float m8[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) m8[i] = s[i];
+#pragma unroll
+                    for (int c = 8; c < 128; c += 8)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], s[c + i]);
+                    const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+                    if (!move_max(mx)) break;
+                    const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                    const float2 mm = make_float2(-m_use, -m_use);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int e = 0; e < 64; e += 2) {
+                            const float2 x2 = __ffma2_rn(make_float2(s[64 * half + e], s[64 * half + e + 1]), sc, mm);
+                            const float2 p2 = make_float2(fast_exp2(x2.x), fast_exp2(x2.y));
+                            rs[(e >> 1) & 1] = __fadd2_rn(rs[(e >> 1) & 1], p2);
+                            pk[e >> 1] = pack_bf16x2(p2.x, p2.y);
+                        }
+                        tmem_st32(tS + 64 * half, pk);
+                    }
+                } else {
+                    float s[64];
+                    float mx = -INFINITY;
+                    float2 mm = {0.f, 0.f};
+#pragma unroll 1
+                    for (int pass = 0; pass < 4; ++pass) {
+                        const int half = pass == 1 || pass == 2;
+                        if (pass != 2) {  // scores of keys 64 half .. of the tile, hidden ones at -inf
+                            uint32_t raw[2][32];
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 * half + c * 32, raw[c]);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
+                            if (edge) {
+                                const uint64_t vis = visible(half);
+                                const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) {
+                                    if (!(v0 >> c & 1u)) s[c] = -INFINITY;
+                                    if (!(v1 >> c & 1u)) s[32 + c] = -INFINITY;
+                                }
+                            }
+                        }
+                        if (pass < 2) {
+                            float m8[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) m8[i] = s[i];
+#pragma unroll
+                            for (int c = 8; c < 64; c += 8)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], s[c + i]);
+                            mx = fmaxf(mx, fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))));
+                            if (pass == 0) continue;
+                            if (!move_max(mx)) break;
+                            mm.x = mm.y = m_ref == -INFINITY ? 0.f : -m_ref;
+                        } else {
+                            uint32_t pk[32];
+#pragma unroll
+                            for (int e = 0; e < 64; e += 2) {
+                                const float2 x2 = __ffma2_rn(make_float2(s[e], s[e + 1]), sc, mm);
+                                const float2 p2 = make_float2(fast_exp2(x2.x), fast_exp2(x2.y));
+                                rs[(e >> 1) & 1] = __fadd2_rn(rs[(e >> 1) & 1], p2);
+                                pk[e >> 1] = pack_bf16x2(p2.x, p2.y);
+                            }
+                            tmem_st32(tS + 64 * half, pk);
+                        }
+                    }
+                }
+                l += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
+                tmem_st_wait();
+                tc_fence_before();
+            }
+            if (!ok) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * set + buf]));
+            prev = buf, prev_phase = phase;
+            if (!w.ends) continue;
+
+            // ---- the piece is done: results, or this CTA's partials --------------------------------
+            // (a quarter without rows waits as well: its arrival on o_free must not run a piece ahead)
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + buf]), phase, abort_flag, a.status, 0x4e));
+            if (!ok) break;
+            tc_fence_after();
+            if (busy) {
+                const bool from = pg_begin == 0, to = w.pg + w.np == w.r.npg;
+                const bool row_ok = row < rows;
+                const int head = w.head * a.G + row % a.G, col0 = w.split * C::kDV;
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                uint16_t* orow = a.o + ((size_t)token * a.Hq + head) * D + col0;
+                float* prow = a.part + ((size_t)(2 * k + (from ? 1 : 0)) * a.rows_cap + (w.dual && set ? 128 : 0) + row) * C::kRowF;
+#pragma unroll 1
+                for (int c = 0; c < C::kDV / 32; ++c) {
+                    uint32_t raw[32];
+                    tmem_ld32(tOset + c * 32, raw);
+                    tmem_ld_wait();
+                    if (!row_ok) continue;
+                    if (from && to) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 x4;
+                            x4.x = pack_bf16x2(__uint_as_float(raw[e]) * inv, __uint_as_float(raw[e + 1]) * inv);
+                            x4.y = pack_bf16x2(__uint_as_float(raw[e + 2]) * inv, __uint_as_float(raw[e + 3]) * inv);
+                            x4.z = pack_bf16x2(__uint_as_float(raw[e + 4]) * inv, __uint_as_float(raw[e + 5]) * inv);
+                            x4.w = pack_bf16x2(__uint_as_float(raw[e + 6]) * inv, __uint_as_float(raw[e + 7]) * inv);
+                            *reinterpret_cast<uint4*>(orow + c * 32 + e) = x4;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4*>(prow + c * 32 + e) = make_uint4(raw[e], raw[e + 1], raw[e + 2], raw[e + 3]);
+                    }
+                }
+                if (row_ok) {
+                    if (!(from && to)) prow[C::kDV] = m_ref, prow[C::kDV + 1] = l;
+                    else if (col0 == 0)
+                        a.lse[(size_t)head * a.T + token] = l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&o_free[set]));
+            // the share's last piece: does its segment go on elsewhere?
+            if (quad == 0 && lane == 0 && w.left == 1 && (!w.dual || set == 0)) {
+                TreeSpan sp = {};
+                if (pg_begin == 0 && w.pg + w.np < w.r.npg) {
+                    // the segment's last unit
+                    sp.ctas = owner_of(u0 + share - 1 + (w.r.npg - (w.pg + w.np) + kTilePages - 1) / kTilePages, q, rem) - k + 1;
+                    sp.row0 = w.r.start + w.tok0, sp.head0 = w.head * a.G, sp.col0 = w.split * C::kDV;
+                    sp.rows[0] = rows;
+                    sp.rows[1] = w.dual ? min(a.tokens_tile, w.r.n - w.tok0 - a.tokens_tile) * a.G : 0;
+                }
+                a.span[k] = sp;
+            }
+        }
+    } else {
+        if constexpr (WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    }
+    if (!works || warp < C::kSets * kSetWarps) {
     } else if (warp == C::kProducer) {
         // ------------------------------- TMA producer ----------------------------------------
         int slot = 0, round = 0;
@@ -568,199 +825,6 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             mbar_drain(smem_u32(mma_idle), 0, a.status, 0x4a);
         }
         __syncwarp();
-    } else if (warp < C::kSets * kSetWarps) {
-        // --------------------------------- softmax ----------------------------------------------
-        const int set = warp / kSetWarps, quad = warp & 3;
-        const int row = quad * 32 + lane;  // row of the tile = TMEM lane
-        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-        const uint32_t tOset = tO + set * C::kDV + lane_base;
-        float m_ref = -INFINITY, l = 0.f;
-        int first_key = 0, token = 0, pg_begin = 0, rows = 0, ctx = 0;
-        int step = 0;                       // global step of the tile (its parity: the score buffer)
-        uint32_t phases = 0u;               // of the set's two buffers
-        int prev = 0;                       // the set's step before: buffer, and its phase
-        uint32_t prev_phase = 0u;
-        bool busy = false, ok = true;
-        Walk<D> w;
-        w.start(a, first_b, first_off, share);
-        for (; ok && w.more(); step += w.dual ? 2 : 1, w.next(a)) {
-            if (!w.mine(set)) continue;
-            const int buf = (step + (w.dual ? set : 0)) & 1;
-            const uint32_t phase = phases >> buf & 1u;
-            phases ^= 1u << buf;
-            if (w.begins) {
-                const int tok = w.tok0 + (w.dual && set ? a.tokens_tile : 0);  // of the request
-                ctx = w.r.L - w.r.n;
-                rows = min(a.tokens_tile, w.r.n - tok) * a.G;
-                busy = quad * 32 < rows;  // the quarter has rows
-                m_ref = -INFINITY, l = 0.f;
-                pg_begin = w.pg;
-                token = w.r.start + min(tok + row / a.G, w.r.n - 1);
-                first_key = a.window > 0 ? max(0, min(ctx, max(a.positions[token], ctx) - a.window + 1)) : 0;
-            }
-            const uint32_t tS = tS0 + buf * 128 + lane_base;
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[2 * set + buf]), phase, abort_flag, a.status, 0x4c));
-            if (busy && ok) {
-                // Two passes over the tile's scores, 64 at a time: the maximum of the lower and the upper half,
-                // then the exponentials of the upper half, still in registers, and of the lower one, read
-                // again. One loop, so that each part's code is there once: a CTA of a short call runs some
-                // twenty tiles, and unrolled the body's instruction fetches cost more than its arithmetic
-                // (batch of 64 at D = 128: 58 us unrolled).
-                float s[64];
-                float mx = -INFINITY;
-                float2 rs[2] = {{0.f, 0.f}, {0.f, 0.f}}, mm = {0.f, 0.f};
-                const float2 sc = make_float2(a.scale_log2, a.scale_log2);
-                const int key0 = (w.r.pg0 + w.pg) * kPage;
-                const bool edge = __any_sync(0xffffffffu, key0 + 127 >= ctx || w.np < kTilePages || key0 < first_key);
-                tc_fence_after();
-#pragma unroll 1
-                for (int pass = 0; pass < 4; ++pass) {
-                    const int half = pass == 1 || pass == 2;
-                    if (pass != 2) {  // scores of keys 64 half .. of the tile, hidden ones at -inf
-                        uint32_t raw[2][32];
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 * half + c * 32, raw[c]);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
-                        if (edge) {
-                            const int k0 = key0 + 64 * half;
-                            uint64_t vis = low_bits(w.np * kPage - 64 * half) & ~low_bits(first_key - k0);
-                            const int dc = ctx - k0;  // column of the first drafted token
-                            if (dc < 64) {
-                                const int d0 = max(0, -dc), wi = d0 >> 5, sh = d0 & 31;
-                                const int32_t* mw = a.mask + (size_t)token * a.words;
-                                auto word = [&](int i) -> uint64_t { return i < a.words ? (uint64_t)(uint32_t)mw[i] : 0ull; };
-                                uint64_t bits = (word(wi) | word(wi + 1) << 32) >> sh;
-                                if (sh) bits |= word(wi + 2) << (64 - sh);
-                                bits &= low_bits(w.r.n - d0);
-                                vis &= low_bits(dc) | bits << max(dc, 0);
-                            }
-                            const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                if (!(v0 >> c & 1u)) s[c] = -INFINITY;
-                                if (!(v1 >> c & 1u)) s[32 + c] = -INFINITY;
-                            }
-                        }
-                    }
-                    if (pass < 2) {
-                        float m8[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) m8[i] = s[i];
-#pragma unroll
-                        for (int c = 8; c < 64; c += 8)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], s[c + i]);
-                        mx = fmaxf(mx, fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))));
-                        if (pass == 0) continue;
-                        // The running maximum is lazy: it moves only when a row's tile maximum exceeds it by more
-                        // than 2^8, so p stays below that and most tiles need no rescale.
-                        const float m_tile = mx * a.scale_log2;
-                        const bool moved = m_tile > m_ref + kRescaleLog2;
-                        if (__any_sync(0xffffffffu, moved)) {
-                            const float alpha = !moved ? 1.f : m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_tile);
-                            if (moved) m_ref = m_tile;
-                            l *= alpha;
-                            if (!w.begins) {
-                                // P V of the set's step before, and so every earlier one, is complete
-                                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + prev]), prev_phase, abort_flag, a.status, 0x4d));
-                                if (!ok) break;
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int c = 0; c < C::kDV / 16; ++c) {
-                                    uint32_t raw[16];
-                                    tmem_ld16(tOset + c * 16, raw);
-                                    tmem_ld_wait();
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
-                                    tmem_st16(tOset + c * 16, raw);
-                                }
-                            }
-                        }
-                        mm.x = mm.y = m_ref == -INFINITY ? 0.f : -m_ref;
-                    } else {
-                        // l sums p in fp32; the P of the product is rounded to bf16 (an MMA takes both operands
-                        // in V's type), half a step of 2^-8 that averages out over the keys
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int e = 0; e < 64; e += 2) {
-                            const float2 x2 = __ffma2_rn(make_float2(s[e], s[e + 1]), sc, mm);
-                            const float2 p2 = make_float2(fast_exp2(x2.x), fast_exp2(x2.y));
-                            rs[(e >> 1) & 1] = __fadd2_rn(rs[(e >> 1) & 1], p2);
-                            pk[e >> 1] = pack_bf16x2(p2.x, p2.y);
-                        }
-                        tmem_st32(tS + 64 * half, pk);
-                    }
-                }
-                l += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
-                tmem_st_wait();
-                tc_fence_before();
-            }
-            if (!ok) break;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * set + buf]));
-            prev = buf, prev_phase = phase;
-            if (!w.ends) continue;
-
-            // ---- the piece is done: results, or this CTA's partials --------------------------------
-            // (a quarter without rows waits as well: its arrival on o_free must not run a piece ahead)
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + buf]), phase, abort_flag, a.status, 0x4e));
-            if (!ok) break;
-            tc_fence_after();
-            if (busy) {
-                const bool from = pg_begin == 0, to = w.pg + w.np == w.r.npg;
-                const bool row_ok = row < rows;
-                const int head = w.head * a.G + row % a.G, col0 = w.split * C::kDV;
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-                uint16_t* orow = a.o + ((size_t)token * a.Hq + head) * D + col0;
-                float* prow = a.part + ((size_t)(2 * k + (from ? 1 : 0)) * a.rows_cap + (w.dual && set ? 128 : 0) + row) * C::kRowF;
-#pragma unroll 1
-                for (int c = 0; c < C::kDV / 32; ++c) {
-                    uint32_t raw[32];
-                    tmem_ld32(tOset + c * 32, raw);
-                    tmem_ld_wait();
-                    if (!row_ok) continue;
-                    if (from && to) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint4 x4;
-                            x4.x = pack_bf16x2(__uint_as_float(raw[e]) * inv, __uint_as_float(raw[e + 1]) * inv);
-                            x4.y = pack_bf16x2(__uint_as_float(raw[e + 2]) * inv, __uint_as_float(raw[e + 3]) * inv);
-                            x4.z = pack_bf16x2(__uint_as_float(raw[e + 4]) * inv, __uint_as_float(raw[e + 5]) * inv);
-                            x4.w = pack_bf16x2(__uint_as_float(raw[e + 6]) * inv, __uint_as_float(raw[e + 7]) * inv);
-                            *reinterpret_cast<uint4*>(orow + c * 32 + e) = x4;
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4*>(prow + c * 32 + e) = make_uint4(raw[e], raw[e + 1], raw[e + 2], raw[e + 3]);
-                    }
-                }
-                if (row_ok) {
-                    if (!(from && to)) prow[C::kDV] = m_ref, prow[C::kDV + 1] = l;
-                    else if (col0 == 0)
-                        a.lse[(size_t)head * a.T + token] = l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&o_free[set]));
-            // the share's last piece: does its segment go on elsewhere?
-            if (quad == 0 && lane == 0 && w.left == 1 && (!w.dual || set == 0)) {
-                TreeSpan sp = {};
-                if (pg_begin == 0 && w.pg + w.np < w.r.npg) {
-                    // the segment's last unit
-                    sp.ctas = owner_of(u0 + share - 1 + (w.r.npg - (w.pg + w.np) + kTilePages - 1) / kTilePages, q, rem) - k + 1;
-                    sp.row0 = w.r.start + w.tok0, sp.head0 = w.head * a.G, sp.col0 = w.split * C::kDV;
-                    sp.rows[0] = rows;
-                    sp.rows[1] = w.dual ? min(a.tokens_tile, w.r.n - w.tok0 - a.tokens_tile) * a.G : 0;
-                }
-                a.span[k] = sp;
-            }
-        }
     }
     __syncthreads();
     if (warp == C::kIssuer) {
@@ -835,10 +899,10 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a) {
     }
 }
 
-template <int D>
+template <int D, bool WIDE>
 cudaError_t launch_t(const TreeLaunch& L, TreeArgs a, cudaStream_t stream) {
     using C = TreeCfg<D>;
-    cudaError_t e = cudaFuncSetAttribute(tree_paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(tree_paged_kernel<D, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
     // at most one CTA per tile of the longest step that fits the arguments
     const int tokens = a.tokens_tile * C::kSets;
@@ -858,7 +922,7 @@ cudaError_t launch_t(const TreeLaunch& L, TreeArgs a, cudaStream_t stream) {
     cfg.numAttrs = 1;
     static const char* const kNames[4] = {"tree_paged_d64", "tree_paged_d128", "tree_paged_d256", "tree_paged_d512"};
     ProfMark m = prof_begin(stream, kNames[D == 64 ? 0 : D == 128 ? 1 : D == 256 ? 2 : 3]);
-    e = cudaLaunchKernelEx(&cfg, tree_paged_kernel<D>, L.tq, L.tk, L.tv, a);
+    e = cudaLaunchKernelEx(&cfg, tree_paged_kernel<D, WIDE>, L.tq, L.tk, L.tv, a);
     prof_end(stream, m);
     if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
     cfg.gridDim = dim3(grid, kMergeY);
@@ -896,11 +960,12 @@ cudaError_t launch_tree_paged(const TreeLaunch& L, cudaStream_t stream) {
     a.tokens_tile = tree_tokens_per_tile(a.G), a.rows_cap = rows_cap(a.G, L.max_q, L.D);
     a.max_pages = L.max_pages, a.num_pages = L.num_pages, a.window = L.window;
     a.scale_log2 = L.scale * 1.4426950408889634f;
+    const bool wide = L.max_q > a.tokens_tile;  // a request may have two row tiles
     switch (L.D) {
-        case 64: return launch_t<64>(L, a, stream);
-        case 128: return launch_t<128>(L, a, stream);
-        case 256: return launch_t<256>(L, a, stream);
-        case 512: return launch_t<512>(L, a, stream);
+        case 64: return wide ? launch_t<64, true>(L, a, stream) : launch_t<64, false>(L, a, stream);
+        case 128: return wide ? launch_t<128, true>(L, a, stream) : launch_t<128, false>(L, a, stream);
+        case 256: return launch_t<256, false>(L, a, stream);
+        case 512: return launch_t<512, false>(L, a, stream);
         default: return cudaErrorInvalidValue;
     }
 }
