@@ -17,7 +17,7 @@
 // time and the only exchange is the butterfly sum of a row's lanes. A task is one token's block of
 // kU such passes, all queries or all keys; a warp keeps its block and walks the tokens, so the norm
 // weights (and, in the gradient, their sums) stay in registers and a token's angles are loaded once
-// for kU passes. All loads of a task are issued before the first is used.
+// for kU passes. All loads of a task are issued before the first is used (the gradient: see there).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,7 +30,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUF = 4;  // passes per task, forward
-constexpr int kUB = 2;  // passes per task, gradient (two streams in)
+constexpr int kUB = 4;  // passes per task, gradient
 constexpr int kMaxCtas = 1024;  // sizes the gradient's workspace
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[16], int at) {
@@ -48,11 +48,15 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[16], int at) {
     return w;
 }
 
-// Sum over the LPR lanes that share a row.
+// The LPR lanes that share row group `sub`, and a sum over them.
 template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
+__device__ __forceinline__ unsigned row_peers(int sub) {
+    return LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << (sub * LPR & 31);
+}
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v, unsigned peers = 0xffffffffu) {
 #pragma unroll
-    for (int off = LPR / 2; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    for (int off = LPR / 2; off; off >>= 1) v += __shfl_xor_sync(peers, v, off);
     return v;
 }
 
@@ -185,11 +189,23 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
     }
 }
 
-// The gradient. Each CTA leaves its sums of dn xh in part[CTA][query | key][D], in an order of its own
-// that depends on the launch alone; norm_rope_dw_kernel adds them up.
+// The gradient. The rows of a task come into shared memory by bulk copies, 4 KB of x and 4 KB of dy, into a
+// ring of kRing stages that each warp has for itself: its lane 0 refills a stage as soon as the warp has
+// read it, so 12 warps an SM keep up to 192 KB on their way (with loads into registers, 163 of them and
+// 48 KB on their way, 18001 tokens of 36 heads of 512 took 487 us, 4.1 TB/s). Each CTA leaves its sums of
+// dn xh in part[CTA][query | key][D], in an order of its own that depends on the launch alone;
+// norm_rope_dw_kernel adds them up.
+constexpr int kRing = 2;
+constexpr int kStageBytes = 8192;
+constexpr int kBwdSmem = kWarps * kRing * kStageBytes + 256;
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeLaunch a) {
     constexpr int LPR = D / 16, RPW = 32 / LPR, RPT = RPW * kUB;
+    static_assert(RPT * D * 4 == kStageBytes, "a stage holds a task's x and dy");
+    extern __shared__ __align__(128) uint8_t ring[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kWarps * kRing * kStageBytes);  // [kWarps][kRing]
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kWarps * kRing);
     const int lane = threadIdx.x & 31, j = lane % LPR, sub = lane / LPR, wid = threadIdx.x >> 5;
     const int nblk = (a.Hq + RPT - 1) / RPT + (a.Hkv + RPT - 1) / RPT;
     const int warp = blockIdx.x * kWarps + wid;
@@ -199,52 +215,62 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
     const int rc = a.rot / 16;
     const bool rotated = j < rc;
     const int c0 = rotated && !a.interleaved ? j : 2 * j, c1 = rotated && !a.interleaved ? j + rc : 2 * j + 1;
+    const uint16_t* src = (b.kind == 0 ? a.q : a.k) + (size_t)b.head0 * D;
+    const uint16_t* gsrc = (b.kind == 0 ? a.dq_out : a.dk_out) + (size_t)b.head0 * D;
+    const long long stride = b.kind == 0 ? a.q_stride : a.k_stride;
+    const long long ostride = b.kind == 0 ? a.dq_stride : a.dk_stride;
+    uint16_t* dst = (b.kind == 0 ? a.dq : a.dk) + (size_t)b.head0 * D;
+    const int rows = min(RPT, b.heads - b.head0);
+    uint8_t* mine = ring + wid * kRing * kStageBytes;
+    uint64_t* full = bars + wid * kRing;
+    if (threadIdx.x == 0) *abort_flag = 0;
+    if (lane == 0)
+        for (int s = 0; s < kRing; ++s) mbar_init(smem_u32(&full[s]), 1);
+    fence_mbar_init();
+    __syncthreads();
+    auto fetch = [&](int t, int s) {  // lane 0
+        const uint32_t bar = smem_u32(&full[s]), at = smem_u32(mine + s * kStageBytes);
+        const uint32_t bytes = rows * D * 2;
+        mbar_expect_tx(bar, 2 * bytes);
+        bulk_load(at, src + (size_t)t * stride, bytes, bar);
+        bulk_load(at + kStageBytes / 2, gsrc + (size_t)t * b.heads * D, bytes, bar);
+    };
+    const int t0 = warp / nblk;
+    if (works && lane == 0)
+        for (int s = 0; s < kRing; ++s)
+            if (t0 + (long long)s * lanes < a.T) fetch(t0 + s * lanes, s);
     float v[16], dw[16];
     load_weights(a, b.kind == 0 ? a.q_weight : a.k_weight, c0, c1, v);
 #pragma unroll
     for (int e = 0; e < 16; ++e) dw[e] = 0.f;
-    const uint16_t* src = b.kind == 0 ? a.q : a.k;
-    const uint16_t* gsrc = b.kind == 0 ? a.dq_out : a.dk_out;
-    const long long stride = b.kind == 0 ? a.q_stride : a.k_stride;
-    const long long ostride = b.kind == 0 ? a.dq_stride : a.dk_stride;
-    uint16_t* dst = b.kind == 0 ? a.dq : a.dk;
 
-    for (int t = warp / nblk; works && t < a.T; t += lanes) {
-        uint4 xr[kUB][2], gr[kUB][2];
-#pragma unroll
-        for (int u = 0; u < kUB; ++u) {
-            const int h = b.head0 + u * RPW + sub;
-            xr[u][0] = xr[u][1] = gr[u][0] = gr[u][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (h < b.heads) {
-                const uint16_t* row = src + (size_t)t * stride + (size_t)h * D;
-                const uint16_t* grow = gsrc + ((size_t)t * b.heads + h) * D;
-                xr[u][0] = *reinterpret_cast<const uint4*>(row + 8 * c0);
-                xr[u][1] = *reinterpret_cast<const uint4*>(row + 8 * c1);
-                gr[u][0] = *reinterpret_cast<const uint4*>(grow + 8 * c0);
-                gr[u][1] = *reinterpret_cast<const uint4*>(grow + 8 * c1);
-            }
-        }
+    int stage = 0, phase = 0;
+    for (int t = t0; works && t < a.T; t += lanes) {
+        bool skip = false;
         float c[8], s[8];
         if (a.rot > 0) {
             const int pos = a.positions[t];
-            if (pos < 0 || pos >= a.max_pos) {
+            skip = pos < 0 || pos >= a.max_pos;
+            if (skip) {
                 if (lane == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
-                continue;
-            }
-            if (rotated) {
+            } else if (rotated) {
                 load_angles(a, pos, j, c, s);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s[e] = -s[e];  // the transpose
             }
         }
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, abort_flag, a.status, 0x51))) break;
+        const uint8_t* xs = mine + stage * kStageBytes;
 #pragma unroll
         for (int u = 0; u < kUB; ++u) {
-            const int h = b.head0 + u * RPW + sub;
+            const int r = u * RPW + sub;
+            if (skip || r >= rows) continue;  // a row's lanes agree
             float x[16], g[16];
-            unpack8(xr[u][0], x, 0);
-            unpack8(xr[u][1], x, 8);
-            unpack8(gr[u][0], g, 0);
-            unpack8(gr[u][1], g, 8);
+            const uint8_t* xrow = xs + r * D * 2;
+            unpack8(*reinterpret_cast<const uint4*>(xrow + 16 * c0), x, 0);
+            unpack8(*reinterpret_cast<const uint4*>(xrow + 16 * c1), x, 8);
+            unpack8(*reinterpret_cast<const uint4*>(xrow + kStageBytes / 2 + 16 * c0), g, 0);
+            unpack8(*reinterpret_cast<const uint4*>(xrow + kStageBytes / 2 + 16 * c1), g, 8);
             if (rotated) turn(g, c, s, a.interleaved);  // dn
             float ss = 0.f, sg = 0.f;
 #pragma unroll
@@ -252,20 +278,22 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
                 ss = fmaf(x[e], x[e], ss);
                 sg = fmaf(g[e] * v[e], x[e], sg);
             }
-            const float r = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
-            const float m = row_sum<LPR>(sg) * (1.f / D) * r;  // mean(g xh)
+            const unsigned peers = row_peers<LPR>(sub);
+            const float rr = rsqrtf(row_sum<LPR>(ss, peers) * (1.f / D) + a.eps);
+            const float m = row_sum<LPR>(sg, peers) * (1.f / D) * rr;  // mean(g xh)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const float xh = x[e] * r;
+                const float xh = x[e] * rr;
                 dw[e] = fmaf(g[e], xh, dw[e]);
-                x[e] = r * (g[e] * v[e] - xh * m);
+                x[e] = rr * (g[e] * v[e] - xh * m);
             }
-            if (h < b.heads) {
-                uint16_t* row = dst + (size_t)t * ostride + (size_t)h * D;
-                *reinterpret_cast<uint4*>(row + 8 * c0) = pack8(x, 0);
-                *reinterpret_cast<uint4*>(row + 8 * c1) = pack8(x, 8);
-            }
+            uint16_t* row = dst + (size_t)t * ostride + (size_t)r * D;
+            *reinterpret_cast<uint4*>(row + 8 * c0) = pack8(x, 0);
+            *reinterpret_cast<uint4*>(row + 8 * c1) = pack8(x, 8);
         }
+        __syncwarp();  // the stage has been read
+        if (lane == 0 && t + (long long)kRing * lanes < a.T) fetch(t + kRing * lanes, stage);
+        if (++stage == kRing) stage = 0, phase ^= 1;
     }
     // the warp's row groups, then the CTA's warps, in order
     __shared__ float sums[kWarps][D];
@@ -319,7 +347,7 @@ int norm_grid(long long T, int nblk, int sms, int per_sm) {
     return (int)g;
 }
 
-constexpr int kFwdPerSm = 4, kBwdPerSm = 4;
+constexpr int kFwdPerSm = 4, kBwdPerSm = 3;
 
 template <int D, bool PAGED>
 cudaError_t launch_fwd_d(const NormRopeLaunch& L, cudaStream_t stream) {
@@ -336,10 +364,12 @@ cudaError_t launch_bwd_d(const NormRopeLaunch& L, cudaStream_t stream) {
     constexpr int RPT = 512 / D * kUB;
     const int nblk = (L.Hq + RPT - 1) / RPT + (L.Hkv + RPT - 1) / RPT;
     const int grid = norm_grid(L.T, nblk, L.sms, kBwdPerSm);
+    cudaError_t e = cudaFuncSetAttribute(norm_rope_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+    if (e != cudaSuccess) return e;
     ProfMark m = prof_begin(stream, "qk_norm_rope_bwd");
-    norm_rope_bwd_kernel<D><<<grid, kThreads, 0, stream>>>(L);
+    norm_rope_bwd_kernel<D><<<grid, kThreads, kBwdSmem, stream>>>(L);
     prof_end(stream, m);
-    cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     m = prof_begin(stream, "qk_norm_rope_dw");
     norm_rope_dw_kernel<<<2 * D / 32, kDwWarps * 32, 0, stream>>>(L.part, L.dq_weight, L.dk_weight, D, grid);
