@@ -483,11 +483,14 @@ def attn_paged_plan(kv_lens, new_lens, free_pages, block_table, pages_held, free
            _i32(free_pages, (F,), idx, "free_pages"), _i32(free_used, one, idx, "free_used"),
            _i32(block_table, (R, maxp), idx, "block_table"))
     if out is None:
-        buf = _new(3 * R + 2 * T + 3, torch.int32, idx, stream)
-        out = PagedPlan._make(torch.split_with_sizes(buf, (R, R + 1, T, T, R, 1, 1)))
+        pad = -T % 4  # positions and slots start at 16 bytes
+        buf = _new(3 * R + 2 * (T + pad) + 3, torch.int32, idx, stream)
+        positions, _, slots, _, cu_q, seq_lens, held, used, admitted = torch.split_with_sizes(
+            buf, (T, pad, T, pad, R + 1, R, R, 1, 1))
+        out = PagedPlan(seq_lens, cu_q, positions, slots, held, used, admitted)
         at = buf.data_ptr()
-        outs = (at, at + 4 * R, at + 8 * R + 4, at + 8 * R + 4 + 4 * T, at + 8 * R + 4 + 8 * T, at + 12 * R + 4 + 8 * T,
-                at + 12 * R + 8 + 8 * T)
+        cu = at + 8 * (T + pad)
+        outs = (cu + 4 * R + 4, cu, at, at + 4 * (T + pad), cu + 8 * R + 4, cu + 12 * R + 4, cu + 12 * R + 8)
     else:
         outs = (_i32(out.seq_lens, rs, idx, "out.seq_lens"), _i32(out.cu_q, (R + 1,), idx, "out.cu_q"),
                 _i32(out.positions, (T,), idx, "out.positions"), _i32(out.slots, (T,), idx, "out.slots"),

@@ -12,8 +12,13 @@
 // There is next to nothing to move (24 bytes a request, 8 a token, 8 a page taken), so the call is bound
 // by latency: one launch, and no value passes from one CTA to another. Every CTA scans all requests
 // itself into shared memory (R <= 16384: two prefix sums of 64 KB) and then fills its share of the rows
-// and pages, finding the request of a row by bisection of the prefix sums. A new page's id is read from
-// the free list, not from the table, so no row waits for another thread's table entry.
+// and pages. Where there are more rows than threads, a thread takes four consecutive ones: it finds the
+// request of the first by bisection of the prefix sums, steps on from there, reads a page id once for
+// rows of one page, and stores 16 bytes at a time where the outputs are aligned (1000 requests, 500
+// thousand rows: 7.7 us against 9.5 a row at a time). Otherwise it takes one (64 requests of one row each:
+// 3.1 us against 5.0 by fours, whose rows read the state of four requests one after the other). A new
+// page's id is read from the free list, not from the table, so no row waits for another thread's table
+// entry.
 //
 // The lengths, held pages and the free list's cursor may be updated in place: the CTAs are then one
 // cluster, and all of them have read the old state before the first writes the new (a cluster barrier).
@@ -56,7 +61,7 @@ __device__ __forceinline__ int owner(const int* first, int count, int x) {
     return lo;
 }
 
-template <bool IN_PLACE>
+template <bool IN_PLACE, int PER>  // PER: rows a thread takes at a time
 __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_constant__ PlanLaunch a) {
     extern __shared__ int prefix[];
     const int R = a.R;
@@ -121,17 +126,37 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         a.table[(size_t)b * a.max_pages + a.held[b] + (i - off[b])] = checked(a.free_pages[used + i]);
     }
     // rows
-    for (int t = gtid; t < a.T; t += gsize) {
-        int pos = 0, slot = -1;
-        if (t < tokens) {
-            const int b = owner(cu, adm, t);
-            pos = a.kv_lens[b] + (t - cu[b]);
-            const int p = pos / kPage, held = a.held[b];
-            const int page = checked(p < held ? a.table[(size_t)b * a.max_pages + p] : a.free_pages[used + off[b] + p - held]);
-            if (page >= 0) slot = page * kPage + pos % kPage;
+    const bool wide = PER == 4 && ((reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.slots)) & 15u) == 0;
+    const int groups = a.T / PER + (a.T % PER != 0);
+    for (int g = gtid; g < groups; g += gsize) {
+        const int t0 = PER * g;
+        int pos[PER], slot[PER];
+        int b = t0 < tokens ? owner(cu, adm, t0) : 0, at = -1, page = -1;  // page: of block-table entry `at`
+        int kv = 0, held = 0, row = -1;                                    // of request `row`
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int t = t0 + i;
+            pos[i] = 0, slot[i] = -1;
+            if (t < tokens) {
+                while (t >= cu[b + 1]) ++b;
+                if (b != row) row = b, at = -1, kv = a.kv_lens[b], held = a.held[b];
+                pos[i] = kv + (t - cu[b]);
+                const int p = pos[i] / kPage;
+                if (p != at) {
+                    at = p;
+                    page = checked(p < held ? a.table[(size_t)b * a.max_pages + p] : a.free_pages[used + off[b] + p - held]);
+                }
+                if (page >= 0) slot[i] = page * kPage + pos[i] % kPage;
+            }
         }
-        a.positions[t] = pos;
-        a.slots[t] = slot;
+        if (wide && t0 + PER <= a.T) {
+            *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[PER > 1], pos[PER / 2], pos[PER - 1]);
+            *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[PER > 1], slot[PER / 2], slot[PER - 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (t0 + i < a.T) a.positions[t0 + i] = pos[i], a.slots[t0 + i] = slot[i];
+        }
     }
     // the new state
     if (IN_PLACE) cluster_sync_all();  // every CTA of the grid has read the old one
@@ -148,41 +173,43 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         *a.used_out = used + pages;
         *a.admitted = adm;
     }
+    // A decode call behind this kernel starts as its last CTAs leave, and reads seq_lens and the block table
+    // before it waits for this grid's end: they are visible by then.
+    __threadfence();
+}
+
+template <bool IN_PLACE, int PER>
+cudaError_t launch_t(const PlanLaunch& L, cudaStream_t stream) {
+    const size_t smem = (size_t)(L.R + 1) * 2 * sizeof(int);
+    cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel<IN_PLACE, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const long long rows = ((long long)L.T + PER - 1) / PER, items = rows > L.R ? rows : L.R;
+    const long long want = items > kThreads ? (items + kThreads - 1) / kThreads : 1, most = IN_PLACE ? kCluster : L.sms;
+    const int grid = (int)(want < most ? want : most);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = grid;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = IN_PLACE ? 1 : 0;
+    const ProfMark m = prof_begin(stream, "paged_plan");
+    e = cudaLaunchKernelEx(&cfg, paged_plan_kernel<IN_PLACE, PER>, L);
+    prof_end(stream, m);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_paged_plan(const PlanLaunch& L, cudaStream_t stream) {
-    const size_t smem = (size_t)(L.R + 1) * 2 * sizeof(int);
-    const long long items = (long long)L.T > L.R ? L.T : L.R;
-    const long long want = (items + kThreads - 1) / kThreads;
-    const ProfMark m = prof_begin(stream, "paged_plan");
-    cudaError_t e;
-    if (L.in_place) {
-        e = cudaFuncSetAttribute(paged_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = want < kCluster ? (unsigned)(want < 1 ? 1 : want) : kCluster;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.gridDim = dim3(attr[0].val.clusterDim.x);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = stream;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, paged_plan_kernel<true>, L);
-    } else {
-        e = cudaFuncSetAttribute(paged_plan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        const int grid = (int)(want < 1 ? 1 : want < L.sms ? want : L.sms);
-        paged_plan_kernel<false><<<grid, kThreads, smem, stream>>>(L);
-        e = cudaSuccess;
-    }
-    prof_end(stream, m);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    const bool fours = L.T > (L.in_place ? kCluster : L.sms) * kThreads;
+    if (L.in_place) return fours ? launch_t<true, 4>(L, stream) : launch_t<true, 1>(L, stream);
+    return fours ? launch_t<false, 4>(L, stream) : launch_t<false, 1>(L, stream);
 }
 
 }  // namespace attn

@@ -187,6 +187,9 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
             }
         }
     }
+    // A decode call behind this kernel starts as its last CTAs leave, and copies pages before it waits for
+    // this grid's end: the rows are visible by then.
+    if (PAGED) __threadfence();
 }
 
 // The gradient. The rows of a task come into shared memory by bulk copies, 4 KB of x and 4 KB of dy, into a
