@@ -1,7 +1,8 @@
 """Fused flash-style GQA attention for NVIDIA GB300 (sm_103a).
 
 Thin Python binding over the C ABI in ``include/attn.h`` (``libattn_gb300.so``):
-argument marshalling only. Every step of the computation runs in the library's
+argument marshalling only (by ctypes; for the calls that are short on the GPU by the native
+module ``_ops``). Every step of the computation runs in the library's
 CUDA kernels; there is no CPU or PyTorch fallback, and importing a function whose
 library is missing raises immediately.
 
@@ -31,7 +32,6 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 import threading
@@ -392,71 +392,27 @@ class PagedPlan(NamedTuple):
     admitted: Any     # [1] requests served
 
 
-# The calls below are short on the GPU, so their argument checks are kept cheap: attributes are compared
-# one by one and nothing is built before a check has failed.
-
-def _i32(t, shape, idx, name):
-    """Pointer of a contiguous int32 tensor of that shape on GPU idx."""
-    import torch
-
-    if t.dtype is torch.int32 and t.get_device() == idx and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on cuda:{idx}")
+_bound = None
 
 
-def _dense(t, shape, idx, name):
-    """Pointer of a contiguous bfloat16 tensor of that shape on GPU idx."""
-    import torch
+def _native():
+    """The native part of the binding (csrc/py_ops.cpp): the calls below are short on the GPU, so their argument
+    checks, output allocation and C call are one function of it each. Outputs and workspaces that are not given
+    belong to the stream of the call (or to the graph being captured): calls on different streams, or in
+    different graphs, never share them."""
+    global _bound
+    if _bound is None:
+        import torch  # noqa: F401  (the module uses torch's own library)
 
-    if t.dtype is torch.bfloat16 and t.get_device() == idx and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous bfloat16 tensor of shape {tuple(shape)} on cuda:{idx}")
-
-
-def _index(t, name):
-    idx = t.get_device()
-    if idx < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return idx
-
-
-def _new(shape, dtype, idx, stream):
-    """A tensor of the stream that the call runs on."""
-    import torch
-
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=idx)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=idx)
-
-
-@functools.lru_cache(maxsize=4096)
-def _need(op, Hq, Hkv, S, D):
-    return attn_workspace_size(op, 0, Hq, Hkv, S, D)
-
-
-def _scratch(workspace, nbytes, idx, stream):
-    """The call's workspace and its size. One of its own (of its stream, or of the graph being captured) unless
-    the caller gives one: calls on different streams, or in different graphs, then never share it."""
-    import torch
-
-    if workspace is None:
-        return _new(nbytes, torch.uint8, idx, stream), nbytes
-    if workspace.get_device() != idx or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{idx}")
-    return workspace, workspace.numel() * workspace.element_size()
-
-
-def _run(fn, what, idx, stream, *args):
-    import torch
-
-    if torch.cuda.current_device() == idx:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream)
-    else:
-        with torch.cuda.device(idx):  # the library works on the current device
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream)
-    if rc != 0:
-        raise AttnError(rc, what)
+        load_library()
+        try:
+            from . import _ops as ops
+        except ImportError as e:
+            raise RuntimeError("attention_flash_gqa_gb300/_ops.so is missing or does not fit this torch: build it "
+                               "(python -m attention_flash_gqa_gb300._build or __graft_entry__.build())") from e
+        ops.load(_LIB_PATH, AttnError, PagedPlan)
+        _bound = ops
+    return _bound
 
 
 def attn_paged_plan(kv_lens, new_lens, free_pages, block_table, pages_held, free_used, total_new: int, *, num_pages: int,
@@ -470,107 +426,8 @@ def attn_paged_plan(kv_lens, new_lens, free_pages, block_table, pages_held, free
     tensors to write; its seq_lens, pages_held and free_used may be kv_lens, pages_held and free_used
     themselves (a state kept in place). See include/attn.h for admission and refusals.
     """
-    import torch
-
-    idx = _index(kv_lens, "kv_lens")
-    R, F, T = kv_lens.numel(), free_pages.numel(), int(total_new)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [num_reqs, max_pages]")
-    if T < 0:
-        raise ValueError("total_new must not be negative")
-    maxp, rs, one = block_table.shape[1], (R,), (1,)
-    ins = (_i32(kv_lens, rs, idx, "kv_lens"), _i32(new_lens, rs, idx, "new_lens"), _i32(pages_held, rs, idx, "pages_held"),
-           _i32(free_pages, (F,), idx, "free_pages"), _i32(free_used, one, idx, "free_used"),
-           _i32(block_table, (R, maxp), idx, "block_table"))
-    if out is None:
-        pad = -T % 4  # positions and slots start at 16 bytes
-        buf = _new(3 * R + 2 * (T + pad) + 3, torch.int32, idx, stream)
-        positions, _, slots, _, cu_q, seq_lens, held, used, admitted = torch.split_with_sizes(
-            buf, (T, pad, T, pad, R + 1, R, R, 1, 1))
-        out = PagedPlan(seq_lens, cu_q, positions, slots, held, used, admitted)
-        at = buf.data_ptr()
-        cu = at + 8 * (T + pad)
-        outs = (cu + 4 * R + 4, cu, at, at + 4 * (T + pad), cu + 8 * R + 4, cu + 12 * R + 4, cu + 12 * R + 8)
-    else:
-        outs = (_i32(out.seq_lens, rs, idx, "out.seq_lens"), _i32(out.cu_q, (R + 1,), idx, "out.cu_q"),
-                _i32(out.positions, (T,), idx, "out.positions"), _i32(out.slots, (T,), idx, "out.slots"),
-                _i32(out.pages_held, rs, idx, "out.pages_held"), _i32(out.free_used, one, idx, "out.free_used"),
-                _i32(out.admitted, one, idx, "out.admitted"))
-    _run(load_library().attn_paged_plan, "attn_paged_plan", idx, stream, *ins, *outs, R, T, F, int(page_size), maxp,
-         int(num_pages))
-    return out
-
-
-def _rows(t, name, idx):
-    """A [T, H, D] or [B, S, H, D] bfloat16 tensor as (T, H, D, token stride)."""
-    import torch
-
-    if t.dtype is not torch.bfloat16 or t.get_device() != idx:
-        raise ValueError(f"{name} must be a bfloat16 tensor on cuda:{idx}")
-    shape, st = t.shape, t.stride()
-    if len(shape) == 3:
-        T, H, D = shape
-        step = st[0]
-    elif len(shape) == 4:
-        B, S, H, D = shape
-        T, step = B * S, (st[1] if S > 1 else st[0])
-        if B > 1 and S > 1 and st[0] != S * st[1]:
-            raise ValueError(f"{name}: tokens must be evenly spaced across the batch")
-    else:
-        raise ValueError(f"{name} must be [T, H, D] or [B, S, H, D]")
-    if (st[-1] != 1 and D > 1) or (st[-2] != D and H > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return T, H, D, (step if T > 1 else H * D)
-
-
-def _qk(q, k, idx):
-    T, Hq, D, qs = _rows(q, "q", idx)
-    Tk, Hkv, Dk, ks = _rows(k, "k", idx)
-    if Tk != T or Dk != D or q.dim() != k.dim() or q.shape[0] != k.shape[0]:
-        raise ValueError("q and k must have the same tokens and head size")
-    return T, Hq, Hkv, D, qs, ks
-
-
-def _norm_weight(w, D, idx, name):
-    """Pointer of a norm weight, and 1 if it is fp32, 0 if bfloat16, None if there is none."""
-    import torch
-
-    if w is None:
-        return None, None
-    kind = 0 if w.dtype is torch.bfloat16 else 1 if w.dtype is torch.float32 else -1
-    if kind < 0 or w.get_device() != idx or w.shape != (D,) or not w.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous bfloat16 or float32 tensor of shape ({D},) on cuda:{idx}")
-    return w.data_ptr(), kind
-
-
-def _norm_weights(q_weight, k_weight, D, idx):
-    """Pointers of the norm weights and whether they are fp32."""
-    wq, fq = _norm_weight(q_weight, D, idx, "q_weight")
-    wk, fk = _norm_weight(k_weight, D, idx, "k_weight")
-    if fq is not None and fk is not None and fq != fk:
-        raise ValueError("q_weight and k_weight must both be bfloat16 or both float32")
-    return wq, wk, fq or fk or 0
-
-
-def _per_token(t, q, T, idx, name):
-    """Pointer of an int32 tensor with a value per token of q: [T], or q's [B, S]."""
-    return _i32(t, (T,) if t.dim() == 1 else q.shape[:-2], idx, name)
-
-
-def _angles(positions, cos_sin, q, T, idx):
-    """Pointers of positions and table, rotated dims and table rows."""
-    import torch
-
-    if cos_sin is None:
-        return None, None, 0, 0
-    if cos_sin.dtype is not torch.float32 or cos_sin.get_device() != idx or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-        raise ValueError(f"cos_sin must be a contiguous float32 tensor [max_pos, rot_dim] on cuda:{idx}")
-    rows, rot = cos_sin.shape
-    if rot == 0:
-        return None, None, 0, 0
-    if positions is None:
-        raise ValueError("positions are needed with cos_sin")
-    return _per_token(positions, q, T, idx, "positions"), cos_sin.data_ptr(), rot, rows
+    return (_bound or _native()).paged_plan(kv_lens, new_lens, free_pages, block_table, pages_held, free_used, total_new, num_pages,
+                                          page_size, out, stream)
 
 
 def attn_qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, q_out=None, k_out=None, *, eps: float = 1e-6,
@@ -581,20 +438,8 @@ def attn_qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin, q_out=None, 
     [D] bf16 or fp32 (None: no weight), applied as weight_offset + w; positions int32 [T]; cos_sin fp32
     [max_pos, rot_dim], cos then sin of the rot_dim/2 angles of each position (None: no rotation).
     """
-    import torch
-
-    idx = _index(q, "q")
-    T, Hq, Hkv, D, qs, ks = _qk(q, k, idx)
-    wq, wk, w32 = _norm_weights(q_weight, k_weight, D, idx)
-    pos, table, rot, rows = _angles(positions, cos_sin, q, T, idx)
-    if q_out is None:
-        q_out = _new(q.shape, torch.bfloat16, idx, stream)
-    if k_out is None:
-        k_out = _new(k.shape, torch.bfloat16, idx, stream)
-    _run(load_library().attn_qk_norm_rope, "attn_qk_norm_rope", idx, stream, q.data_ptr(), k.data_ptr(),
-         _dense(q_out, q.shape, idx, "q_out"), _dense(k_out, k.shape, idx, "k_out"), wq, wk, pos, table, T, Hq, Hkv, D, rot,
-         rows, qs, ks, eps, weight_offset, w32, 1 if interleaved else 0)
-    return q_out, k_out
+    return (_bound or _native()).norm_rope(q, k, q_weight, k_weight, positions, cos_sin, q_out, k_out, eps, weight_offset,
+                                         interleaved, stream)
 
 
 def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, cos_sin, dq=None, dk=None, *,
@@ -605,64 +450,16 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, c
     dq_out, dk_out: gradients of its results (contiguous bf16); the rest as passed to the forward.
     dq / dk may be given, as slices of a fused projection's gradient too.
     """
-    import torch
-
-    idx = _index(q, "q")
-    T, Hq, Hkv, D, qs, ks = _qk(q, k, idx)
-    wq, wk, w32 = _norm_weights(q_weight, k_weight, D, idx)
-    pos, table, rot, rows = _angles(positions, cos_sin, q, T, idx)
-    dqs, dks = Hq * D, Hkv * D
-    if dq is None:
-        dq = _new(q.shape, torch.bfloat16, idx, stream)
-    elif dq.shape != q.shape:
-        raise ValueError("dq must have the shape of q")
-    else:
-        dqs = _rows(dq, "dq", idx)[3]
-    if dk is None:
-        dk = _new(k.shape, torch.bfloat16, idx, stream)
-    elif dk.shape != k.shape:
-        raise ValueError("dk must have the shape of k")
-    else:
-        dks = _rows(dk, "dk", idx)[3]
-    dqw, dkw = _new((2, D), torch.float32, idx, stream).unbind()
-    ws, nbytes = _scratch(workspace, _need(ATTN_OP_QK_NORM_ROPE_BWD, 0, 0, 0, D), idx, stream)
-    _run(load_library().attn_qk_norm_rope_bwd, "attn_qk_norm_rope_bwd", idx, stream,
-         _dense(dq_out, q.shape, idx, "dq_out"), _dense(dk_out, k.shape, idx, "dk_out"), q.data_ptr(), k.data_ptr(),
-         dq.data_ptr(), dk.data_ptr(), dqw.data_ptr(), dkw.data_ptr(), wq, wk, pos, table, T, Hq, Hkv, D, rot, rows, qs, ks,
-         dqs, dks, eps, weight_offset, w32, 1 if interleaved else 0, ws.data_ptr(), nbytes)
-    return dq, dk, dqw, dkw
-
-
-def _caches(k_cache, v_cache, D, idx):
-    """Pointers and [num_pages, page_size, Hkv] of a pair of caches."""
-    shape = k_cache.shape
-    if len(shape) != 4 or shape[3] != D:
-        raise ValueError(f"k_cache must be [num_pages, page_size, Hkv, {D}]")
-    return _dense(k_cache, shape, idx, "k_cache"), _dense(v_cache, shape, idx, "v_cache"), shape[0], shape[1], shape[2]
+    return (_bound or _native()).norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, cos_sin, dq, dk, eps,
+                                             weight_offset, interleaved, workspace, stream)
 
 
 def attn_qk_norm_rope_paged(q, k, v, q_weight, k_weight, positions, slots, cos_sin, k_cache, v_cache, q_out=None, *,
                             eps: float = 1e-6, weight_offset: float = 0.0, interleaved: bool = False, stream=None):
     """attn_qk_norm_rope for serving: returns q_out; k (normed and turned) and v go into the paged caches
     [pages,16,Hkv,D] in place, each token at its slot (int32 [T], of attn_paged_plan; -1: padding)."""
-    import torch
-
-    idx = _index(q, "q")
-    T, Hq, Hkv, D, qs, ks = _qk(q, k, idx)
-    if v.shape != k.shape:
-        raise ValueError("v must have the shape of k")
-    vs = _rows(v, "v", idx)[3]
-    wq, wk, w32 = _norm_weights(q_weight, k_weight, D, idx)
-    pos, table, rot, rows = _angles(positions, cos_sin, q, T, idx)
-    kc, vc, num_pages, page_size, Hc = _caches(k_cache, v_cache, D, idx)
-    if Hc != Hkv:
-        raise ValueError("the caches' heads are not k's")
-    if q_out is None:
-        q_out = _new(q.shape, torch.bfloat16, idx, stream)
-    _run(load_library().attn_qk_norm_rope_paged, "attn_qk_norm_rope_paged", idx, stream, q.data_ptr(), k.data_ptr(),
-         v.data_ptr(), _dense(q_out, q.shape, idx, "q_out"), kc, vc, wq, wk, pos, _per_token(slots, q, T, idx, "slots"), table,
-         T, Hq, Hkv, D, rot, rows, page_size, num_pages, qs, ks, vs, eps, weight_offset, w32, 1 if interleaved else 0)
-    return q_out
+    return (_bound or _native()).norm_rope_paged(q, k, v, q_weight, k_weight, positions, slots, cos_sin, k_cache, v_cache, q_out, eps,
+                                               weight_offset, interleaved, stream)
 
 
 def attn_tree_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, tree_mask, max_q_len: int, o=None, lse=None, *,
@@ -674,30 +471,7 @@ def attn_tree_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, tree_mask,
     sees its request's drafted token d; every row sees the context before the drafted tokens, with
     window > 0 only the keys less than `window` behind its position (positions int32 [T]).
     """
-    import torch
-
-    idx = _index(q, "q")
-    shape = q.shape
-    if len(shape) != 3:
-        raise ValueError("q must be [T, Hq, D]")
-    T, Hq, D = shape
-    qp = _dense(q, shape, idx, "q")
-    kc, vc, num_pages, page_size, Hkv = _caches(k_cache, v_cache, D, idx)
-    R = seq_lens.numel()
-    if block_table.dim() != 2 or tree_mask.dim() != 2:
-        raise ValueError("block_table must be [num_reqs, max_pages] and tree_mask [T, words]")
-    maxp, words, top = block_table.shape[1], tree_mask.shape[1], int(max_q_len)
-    if o is None:
-        o = _new(shape, torch.bfloat16, idx, stream)
-    if lse is None:
-        lse = _new((Hq, T), torch.float32, idx, stream)
-    elif lse.dtype is not torch.float32 or lse.get_device() != idx or lse.shape != (Hq, T) or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous float32 tensor of shape {(Hq, T)} on cuda:{idx}")
-    ws, nbytes = _scratch(workspace, _need(ATTN_OP_TREE_PAGED, Hq, Hkv, top, D), idx, stream)
-    _run(load_library().attn_tree_paged, "attn_tree_paged", idx, stream, qp, kc, vc,
-         _i32(block_table, (R, maxp), idx, "block_table"), _i32(seq_lens, (R,), idx, "seq_lens"),
-         _i32(cu_q, (R + 1,), idx, "cu_q"), _i32(tree_mask, (T, words), idx, "tree_mask"),
-         None if positions is None else _i32(positions, (T,), idx, "positions"), _dense(o, shape, idx, "o"), lse.data_ptr(), R,
-         T, top, words, Hq, Hkv, D, page_size, maxp, num_pages, scale if scale is not None else 1.0 / math.sqrt(D), int(window),
-         ws.data_ptr(), nbytes)
-    return o, lse
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    return (_bound or _native()).tree_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, tree_mask, max_q_len, o, lse, positions,
+                                          window, scale, workspace, stream)

@@ -1,7 +1,9 @@
-"""Compile the CUDA sources of this package into ``libattn_gb300.so`` (in-tree).
+"""Compile the CUDA sources of this package into ``libattn_gb300.so`` (in-tree), and the native part of
+the Python binding into ``_ops.so``.
 
-nvcc only, one ``-gencode`` for sm_103a, translation units compiled in parallel and
-linked with ``nvcc -shared``. Used by ``__graft_entry__.build()`` and the tests.
+The library: nvcc only, one ``-gencode`` for sm_103a, translation units compiled in parallel and
+linked with ``nvcc -shared``. The binding: one C++ file against torch's headers, by g++ beside them.
+Used by ``__graft_entry__.build()`` and the tests.
 """
 from __future__ import annotations
 
@@ -13,6 +15,8 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libattn_gb300.so")
+OPS = os.path.join(HERE, "_ops.so")
+OPS_SOURCE = os.path.join(CSRC, "py_ops.cpp")
 BUILD_DIR = os.path.join(HERE, "_build_tmp")
 SOURCES = ["api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd_small.cu", "decode_paged.cu", "decode_paged_noalloc.cu",
            "merge_lse.cu", "paged_plan.cu", "qk_norm_rope.cu", "tree_paged.cu"]
@@ -33,10 +37,32 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(OPS):
         return False
     t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    header = os.path.join(os.path.dirname(HERE), "include", "attn.h")
+    return (all(os.path.getmtime(f) <= t for f in _inputs()) and
+            all(os.path.getmtime(f) <= os.path.getmtime(OPS) for f in (OPS_SOURCE, header)))
+
+
+def _build_ops() -> None:
+    """Compile the native part of the Python binding against the torch of this machine."""
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = OPS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared", OPS_SOURCE, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for py_ops.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, OPS)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -57,8 +83,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ops = ex.submit(_build_ops)
         results = list(ex.map(compile_one, SOURCES))
+        ops.result()
     if verbose:
         for _, err in results:
             print(err)
