@@ -127,6 +127,17 @@ void check(int status, const char* what) {
     throw Raised();
 }
 
+// `count` values of a one-dimensional buffer from `first` on, as a tensor of its storage (made directly: a
+// view operation of torch's takes about 1 us).
+at::Tensor part_of(const at::Tensor& buf, int64_t first, int64_t count) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(buf.storage()), buf.key_set(),
+                                                            buf.dtype());
+    const int64_t size[1] = {count}, stride[1] = {1};
+    t.unsafeGetTensorImpl()->set_storage_offset(buf.storage_offset() + first);
+    t.unsafeGetTensorImpl()->set_sizes_and_strides(size, stride);
+    return t;
+}
+
 // Runs f, with what it throws as a Python error.
 template <class F>
 PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
@@ -220,7 +231,7 @@ PyObject* paged_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
         PyObject* r = type->tp_alloc(type, 7);
         if (!r) throw Raised();
         for (int i = 0; i < 7; ++i) {
-            PyObject* o = THPVariable_Wrap(buf.narrow(0, first[i], shapes[i][0]));
+            PyObject* o = THPVariable_Wrap(part_of(buf, first[i], shapes[i][0]));
             if (!o) {
                 Py_DECREF(r);
                 throw Raised();
@@ -373,7 +384,7 @@ PyObject* norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 d[i] = ro.at, step[i] = ro.step;
             }
         }
-        const int64_t sw[2] = {2, x.rq.D};
+        const int64_t sw[1] = {2 * x.rq.D};
         const at::Tensor dw = place.make(sw, at::kFloat);
         float* dwp = static_cast<float*>(dw.data_ptr());
         at::Tensor own;
@@ -383,7 +394,7 @@ PyObject* norm_rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                   x.table, (int)x.rq.T, (int)x.rq.H, (int)x.rk.H, (int)x.rq.D, x.rot, x.max_pos, x.rq.step, x.rk.step,
                                   step[0], step[1], x.eps, x.offset, x.fp32, x.inter, ws, bytes, place.stream),
               "attn_qk_norm_rope_bwd");
-        r[2].made = dw.select(0, 0), r[3].made = dw.select(0, 1);
+        r[2].made = part_of(dw, 0, x.rq.D), r[3].made = part_of(dw, x.rq.D, x.rq.D);
         return tuple(r);
     });
 }
