@@ -181,7 +181,9 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
 template <bool IN_PLACE, int PER>
 cudaError_t launch_t(const PlanLaunch& L, cudaStream_t stream) {
     const size_t smem = (size_t)(L.R + 1) * 2 * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel<IN_PLACE, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaSuccess;
+    if (smem > 48 * 1024 - 512)  // beyond what a kernel may use unasked (static shared memory counts)
+        e = cudaFuncSetAttribute(paged_plan_kernel<IN_PLACE, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const long long rows = ((long long)L.T + PER - 1) / PER, items = rows > L.R ? rows : L.R;
     const long long want = items > kThreads ? (items + kThreads - 1) / kThreads : 1, most = IN_PLACE ? kCluster : L.sms;

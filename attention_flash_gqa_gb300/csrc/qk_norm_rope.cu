@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
     const int rc = a.rot / 16;
     const bool rotated = j < rc;
     const int c0 = rotated && !a.interleaved ? j : 2 * j, c1 = rotated && !a.interleaved ? j + rc : 2 * j + 1;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // norm_rope_dw_kernel waits for this grid
     const uint16_t* src = (b.kind == 0 ? a.q : a.k) + (size_t)b.head0 * D;
     const uint16_t* gsrc = (b.kind == 0 ? a.dq_out : a.dk_out) + (size_t)b.head0 * D;
     const long long stride = b.kind == 0 ? a.q_stride : a.k_stride;
@@ -262,7 +263,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
                 for (int e = 0; e < 8; ++e) s[e] = -s[e];  // the transpose
             }
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, abort_flag, a.status, 0x51))) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, abort_flag, a.status, 0x51))) {
+            // given up: copies into the ring may still be landing, the CTA must outlast them
+            const uint64_t since = globaltimer();
+            while (globaltimer() - since < 100000ull) __nanosleep(1000);
+            break;
+        }
         const uint8_t* xs = mine + stage * kStageBytes;
 #pragma unroll
         for (int u = 0; u < kUB; ++u) {
@@ -326,6 +332,7 @@ constexpr int kDwWarps = 16;
 __global__ void __launch_bounds__(kDwWarps * 32) norm_rope_dw_kernel(const float* part, float* dqw, float* dkw, int D, int n) {
     __shared__ float acc[kDwWarps][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the gradient kernel runs
     float x = 0.f;
     for (int i = w; i < n; i += kDwWarps) x += part[(size_t)i * 2 * D + col];
     acc[w][lane] = x;
@@ -375,9 +382,18 @@ cudaError_t launch_bwd_d(const NormRopeLaunch& L, cudaStream_t stream) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     m = prof_begin(stream, "qk_norm_rope_dw");
-    norm_rope_dw_kernel<<<2 * D / 32, kDwWarps * 32, 0, stream>>>(L.part, L.dq_weight, L.dk_weight, D, grid);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(2 * D / 32);
+    cfg.blockDim = dim3(kDwWarps * 32);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, (const float*)L.part, L.dq_weight, L.dk_weight, D, grid);
     prof_end(stream, m);
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace

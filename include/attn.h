@@ -362,13 +362,21 @@ ATTN_API int attn_qk_norm_rope_paged(const attn_bf16* q, const attn_bf16* k, con
  *     p_i = max(positions[i], L_b - n_b) is the row's position (context length + depth in its tree);
  *   key L_b - n_b + d (drafted token d): visible if bit d % 32 of word d / 32 of the row's mask is
  *     set (normally its ancestors and itself). Bits of d >= n_b are ignored.
- *   A row that sees no key gets o = 0 and lse = -inf.
+ *   A row that sees no key gets o = 0 and lse = -inf. Hidden keys' K may hold anything; the V of every key
+ *   in the pages that some row may see (from key L_b - n_b - window + 1 on, up to L_b) must be finite,
+ *   since a hidden key enters the sum with probability zero. Slots past L_b are never used.
  *   q, o [total_q, Hq, D] bf16, lse [Hq, total_q] fp32, caches, block_table, seq_lens, cu_q,
  *   max_q_len and the device checks of requests and page ids as in attn_fwd_paged.
  *   tree_mask int32 [total_q, mask_words], mask_words >= ceil(max_q_len / 32). positions int32
  *   [total_q], needed with window > 0 only (else NULL).
  *   Supported: D in {64, 128, 256, 512}, Hq / Hkv <= 128, page_size = 16, max_q_len <= 256,
- *   mask_words <= 8, num_reqs <= 4096, Hkv <= 256, num_pages <= 2^26.
+ *   mask_words <= 8, num_reqs <= 4096, Hkv <= 256, num_pages <= 2^26. (A step of 2^31 key tiles or more,
+ *   counted per request, KV head and row tile, is reported as ATTN_ERR_DEVICE_BOUNDS and not computed.)
+ *   Enqueues two kernels with programmatic stream serialisation, the attention and the merge of its
+ *   partial results. Both wait on the device for the kernels in front of them before they read or write
+ *   anything; the merge allows the kernel behind it to start early, as the merge of attn_decode_paged
+ *   does (the same rule: o and lse may be the q of a decode call that follows, not its caches, table or
+ *   lengths).
  *   workspace: attn_workspace_size(ATTN_OP_TREE_PAGED, 0, Hq, Hkv, max_q_len, D, ...) bytes, 256-byte
  *   aligned: partial results of the key ranges that several CTAs share. Contents on entry do not matter.
  *   Calls that share a workspace must not overlap on the GPU.

@@ -129,6 +129,46 @@ def test_masks_are_taken_as_they_are():
     compare(p)
 
 
+def test_hidden_keys_may_hold_anything():
+    """K of a key that no row sees: NaN and infinities in drafted tokens and before the window."""
+    for D in (64, 128, 256, 512):
+        p = problem([300], [12], 4, 2, D)
+        p["mask"] &= ~(1 << 5)  # nobody sees drafted token 5, not even itself
+        ref_k = p["kc"].clone()
+        at = 305
+        p["kc"][p["table"][0, at // 16], at % 16] = math.nan
+        first = 300 - 100 + 1  # of the window
+        for j in (first - 1, first - first % 16):
+            p["kc"][p["table"][0, j // 16], j % 16] = math.inf
+        o, lse = run(p, window=100)
+        assert attn.attn_get_device_status() == 0
+        p["kc"] = ref_k
+        ro, to, rl, tl = ref.tree(p["q"], p["kc"], p["vc"], p["table"], p["lens"], p["cu"], p["mask"], p["scale"], 100, p["pos"])
+        ref.close("o", o, ro, to)
+        ref.close("lse", lse, rl, tl)
+
+
+def test_nothing_to_do():
+    p = problem([40], [3], 4, 2, 128)
+    e = lambda *s: torch.empty(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    for top in (0, 3):
+        o, lse = attn.attn_tree_paged(p["q"].cuda()[:0], p["kc"].cuda(), p["vc"].cuda(), e(0, 4), e(0), i32([0]), e(0, 1), top)
+        assert o.shape == (0, 4, 128) and lse.shape == (4, 0)
+    # requests without drafted tokens only: nothing is written
+    o = torch.full((2, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    attn.attn_tree_paged(torch.zeros_like(o), p["kc"].cuda(), p["vc"].cuda(), p["table"].cuda(), i32(p["lens"]), i32([0, 0]),
+                         e(2, 1), 3, o)
+    assert attn.attn_get_device_status() == 0 and (o == 7.0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_single_tiles_and_pairs_in_turn(D):
+    """Requests of one, two and three row tiles after one another, short enough that a CTA meets several."""
+    n = [3, 40, 1, 70, 90, 2, 33, 64, 5, 6] * 6
+    ctx = [(53 * i) % 300 for i in range(len(n))]
+    compare(problem(ctx, n, 8, 2, D))
+
+
 def test_causal_chain_is_chunked_prefill():
     """A tree that is a chain is the causal chunk of attn_fwd_paged."""
     p = problem([100, 0, 513], [31, 20, 1], 8, 2, 256, poison=False)
