@@ -695,7 +695,7 @@ int attn_tree_paged(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf1
     attn::TreeLaunch L;
     std::memset(&L, 0, sizeof(L));
     const int G = Hq / Hkv;
-    if (!make_map(&L.tq, q, D, Hq, total_q, 1, attn::tree_tokens_per_tile(G), G) ||
+    if (!make_map(&L.tq, q, D, Hq, total_q, 1, attn::tree_tokens_per_copy(G, max_q_len), G) ||
         !make_cache_map(&L.tk, k_cache, D, Hkv, num_pages) || !make_cache_map(&L.tv, v_cache, D, Hkv, num_pages))
         return ATTN_ERR_LAUNCH;
     L.workspace = workspace;

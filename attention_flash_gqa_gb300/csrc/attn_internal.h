@@ -130,7 +130,7 @@ cudaError_t launch_norm_rope_paged(const NormRopeLaunch& L, cudaStream_t stream)
 cudaError_t launch_norm_rope_bwd(const NormRopeLaunch& L, cudaStream_t stream);
 
 // ---- attention of drafted token trees over a paged cache --------------------------------------
-// tq: 4-D over q [D, Hq, T, 1], box 64 x G x tree_tokens_per_tile x 1; tk / tv as in the paged prefill
+// tq: 4-D over q [D, Hq, T, 1], box 64 x G x tree_tokens_per_copy x 1; tk / tv as in the paged prefill
 struct TreeLaunch {
     CUtensorMap tq, tk, tv;
     const int32_t *block_table, *seq_lens, *cu_q, *mask, *positions;
@@ -141,7 +141,7 @@ struct TreeLaunch {
     int R, T, max_q, words, Hq, Hkv, D, max_pages, num_pages, window, sms;
     float scale;
 };
-int tree_tokens_per_tile(int G);  // drafted tokens of a 128-row tile
+int tree_tokens_per_copy(int G, int max_q);  // drafted tokens of a copy of Q: those of a 128-row tile, or fewer
 size_t tree_workspace_bytes(int G, int max_q, int D);
 cudaError_t launch_tree_paged(const TreeLaunch& L, cudaStream_t stream);
 

@@ -16,8 +16,10 @@
 //    keys and 33 to 64 drafts, Hq 32, Hkv 8, D 128: alone, each of the two row tiles read all of K and
 //    V from DRAM). Otherwise consecutive segments alternate between the sets: one set's epilogue runs
 //    beside the other's first tiles.
-//  * A unit of work is one key tile, up to eight pages (128 keys), of one segment = (request, KV head,
-//    256-column half of O at D = 512, row tile or pair of them). All units are laid end to end and CTA k
+//  * At D = 512 a CTA computes one 256-column half of O; the two CTAs of a key range run side by side
+//    (CTAs 2 i and 2 i + 1), so the second copy of K, for the scores, comes from L2.
+//  * A unit of work is one key tile, up to eight pages (128 keys), of one segment = (request, KV head, row
+//    tile or pair of them). All units are laid end to end and CTA k
 //    takes the k-th equal share: it may finish one segment, run through some and start another. (Equal
 //    shares of pages left some CTAs a third more tiles than others, and a tile costs the softmax the same
 //    however few pages it has.) A segment that one CTA covers is written out by it; of a shared one every
@@ -65,25 +67,28 @@ struct TreeCfg {
     static constexpr uint32_t kSlotBytes = kSubs * kSubBytes;
     static constexpr int kKC = D / kSlotCols;          // slots per K tile
     static constexpr int kVC = kDV / kSlotCols;        // slots per V tile
-    // ring depth: what shared memory leaves next to the Q tiles
-    static constexpr int kStages = D == 512 ? 3 : D == 256 ? 5 : D == 128 ? 5 : 12;
-    static constexpr uint32_t kQBytes = D * 256;       // 128 rows
+    // The Q tiles and the ring share kPool bytes. Q holds the rows that a step's largest tile has (a multiple
+    // of 8); the MMAs read 128 all the same, past its end whatever follows, for rows of the product that
+    // nobody uses. The ring takes what is left, up to kMaxStages slots: at D = 512 three with 128 rows, six
+    // with 32.
+    static constexpr uint32_t kPool = 229376;
+    static constexpr int kMaxStages = D == 64 ? 12 : 6;
     static constexpr uint32_t kPageBytes = 2048 * kSubs;     // one page's rows in a slot
     static constexpr uint32_t kGroupStride = 1024 * kSubs;   // 8 rows of both sub-tiles
-    static constexpr uint32_t kOffSlots = kSets * kQBytes;
-    static constexpr uint32_t kOffBar = kOffSlots + kStages * kSlotBytes;
+    static constexpr uint32_t kOffBar = kPool;
     static constexpr uint32_t kOffScan = kOffBar + 512;
     static constexpr uint32_t kSmem = kOffScan + 192 + 1024;
     static constexpr int kRowF = kDV + 4;              // partial row: O, m, l, 2 pad
     // tensor memory: O of set i at 0 + i * kDV, score buffers at the top
     static_assert(kSets * kDV + 256 <= 512, "tensor memory");
     static_assert(kSmem <= 232448, "shared memory");
-    static_assert(kSets == 1 || (kKC == 1 && kVC == 1 && kStages >= 4), "two sets: one slot a tile, K and V in turn");
+    static_assert(kSets == 1 || (kKC == 1 && kVC == 1), "two sets: one slot a tile, K and V in turn");
+    static_assert((kPool - kSets * D * 256) / kSlotBytes >= (kSets == 2 ? 4 : 3), "the ring's depth with 128 rows");
 };
 
 // What the merge of a segment needs; one per CTA, for the segment that starts in it and ends elsewhere.
 struct TreeSpan {
-    int ctas;     // CTAs that share the segment (0: none)
+    int ctas;     // shares of the units that hold part of it (0: just this one)
     int row0;     // its first token row
     int rows[2];  // rows (tokens * G) of its row tiles
     int head0;    // first query head
@@ -99,6 +104,7 @@ struct TreeArgs {
     float* part;      // [2 * grid][rows_cap][kRowF]
     TreeSpan* span;   // [grid]
     int R, T, max_q, words, Hq, Hkv, G, tokens_tile, rows_cap, max_pages, num_pages, window;
+    int q_tokens, q_rows, stages;  // tokens of a copy of Q, rows of a Q tile in shared memory, slots of the ring
     float scale_log2;
 };
 
@@ -129,7 +135,7 @@ __device__ __forceinline__ Req load_req(const TreeArgs& a, int b) {
 }
 template <int D>
 __device__ __forceinline__ long long req_units(const TreeArgs& a, const Req& r) {
-    return (long long)r.tiles * r.groups * a.Hkv * TreeCfg<D>::kSplit;
+    return (long long)r.tiles * r.groups * a.Hkv;
 }
 
 // A copy's word: pages of the tile in bits 0-3, rows of its last page to keep in bits 4-7 (0: all), and
@@ -149,7 +155,7 @@ struct Walk {
     using C = TreeCfg<D>;
     Req r;
     int b, seg, pg, np;     // request, segment in it, first page (from pg0) and pages of the tile
-    int head, split, tok0;  // of the segment; tok0: first drafted token of its rows
+    int head, tok0;         // of the segment; tok0: first drafted token of its rows
     int left;               // tiles of the share from here on
     bool begins, ends;      // first / last tile of a piece (a segment's pages in this CTA)
     bool dual;              // two row tiles: one for each set
@@ -168,9 +174,8 @@ struct Walk {
     }
     __device__ __forceinline__ void piece(const TreeArgs& a) {
         begins = true;
-        const int group = seg % r.groups, hs = seg / r.groups;
-        split = C::kSplit > 1 ? hs % C::kSplit : 0;
-        head = C::kSplit > 1 ? hs / C::kSplit : hs;
+        const int group = seg % r.groups;
+        head = seg / r.groups;
         tok0 = group * a.tokens_tile * C::kSets;
         dual = C::kSets == 2 && tok0 + a.tokens_tile < r.n;
         set = 0;
@@ -187,7 +192,7 @@ struct Walk {
         if (ends) {
             if (left == 0) return;
             pg = 0;  // a piece ends before the share does only with its segment
-            if (++seg == r.groups * a.Hkv * C::kSplit) {
+            if (++seg == r.groups * a.Hkv) {
                 seg = 0;
                 do r = load_req<D>(a, ++b);  // the share holds more units: there is another request
                 while (r.npg == 0);
@@ -223,12 +228,14 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t sQ = sbase, sSlots = sbase + C::kOffSlots;
+    const int stages = a.stages;
+    const uint32_t q_sub = a.q_rows * 128, q_bytes = q_sub * (D / 64);  // a 64-column sub-tile of Q, all of it
+    const uint32_t sQ = sbase, sSlots = sbase + C::kSets * q_bytes;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-    uint64_t* full = bars;                   // [kStages]
-    uint64_t* empty = full + C::kStages;     // [kStages]
+    uint64_t* full = bars;                      // [kMaxStages]
+    uint64_t* empty = full + C::kMaxStages;     // [kMaxStages]
     // per set: its Q tile is loaded / was last read, its O was read out
-    uint64_t* q_full = empty + C::kStages;   // [2]
+    uint64_t* q_full = empty + C::kMaxStages;   // [2]
     uint64_t* q_free = q_full + 2;           // [2]
     uint64_t* o_free = q_free + 2;           // [2]
     // per set and score buffer (index 2 set + buffer): at most one pending phase each, and only the set's
@@ -236,19 +243,20 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
     uint64_t* s_full = o_free + 2;           // [4]
     uint64_t* p_full = s_full + 4;           // [4]
     uint64_t* pv_done = p_full + 4;          // [4]
-    uint64_t* vfix = pv_done + 4;            // [kStages] the last page's V rows past L are zeroed
-    uint64_t* mma_idle = vfix + C::kStages;
-    uint32_t* words = reinterpret_cast<uint32_t*>(mma_idle + 1);  // [kStages] the copies' words
-    uint32_t* tmem_slot = words + C::kStages;
+    uint64_t* vfix = pv_done + 4;            // [kMaxStages] the last page's V rows past L are zeroed
+    uint64_t* mma_idle = vfix + C::kMaxStages;
+    uint32_t* words = reinterpret_cast<uint32_t*>(mma_idle + 1);  // [kMaxStages] the copies' words
+    uint32_t* tmem_slot = words + C::kMaxStages;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     long long* scan = reinterpret_cast<long long*>(smem + C::kOffScan);  // [kWarps]
     int* first = reinterpret_cast<int*>(scan + C::kWarps);               // where the share starts
-    static_assert((3 * C::kStages + 19) * 8 + C::kStages * 4 + 8 <= 512 && (C::kWarps + 1) * 8 <= 192, "barrier area");
+    static_assert((3 * C::kMaxStages + 19) * 8 + C::kMaxStages * 4 + 8 <= 512 && (C::kWarps + 1) * 8 <= 192, "barrier area");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int k = blockIdx.x;
+    const int part = k / C::kSplit, split = k % C::kSplit;  // its share of the units, and of O's columns
 
     if (tid == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
+        for (int s = 0; s < C::kMaxStages; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 2);  // the MMAs that read it, and the fixer
             mbar_init(smem_u32(&vfix[s]), 1);
@@ -306,10 +314,10 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
         P = 0;
     }
     const int units = (int)P;
-    const int Gc = min(units, (int)gridDim.x);
-    const bool works = k < Gc;  // uniform
+    const int Gc = min(units, (int)gridDim.x / C::kSplit);
+    const bool works = part < Gc;  // uniform
     const int q = works ? units / Gc : 0, rem = units - q * Gc;
-    const int u0 = share_start(k, q, rem), share = works ? q + (k < rem) : 0;
+    const int u0 = share_start(part, q, rem), share = works ? q + (part < rem) : 0;
     if (works && x <= u0 && u0 < x + sum) {
         Req r;
         int b = b0, off = 0;
@@ -542,7 +550,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             if (busy) {
                 const bool from = pg_begin == 0, to = w.pg + w.np == w.r.npg;
                 const bool row_ok = row < rows;
-                const int head = w.head * a.G + row % a.G, col0 = w.split * C::kDV;
+                const int head = w.head * a.G + row % a.G, col0 = split * C::kDV;
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 uint16_t* orow = a.o + ((size_t)token * a.Hq + head) * D + col0;
                 float* prow = a.part + ((size_t)(2 * k + (from ? 1 : 0)) * a.rows_cap + (w.dual && set ? 128 : 0) + row) * C::kRowF;
@@ -582,8 +590,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                 TreeSpan sp = {};
                 if (pg_begin == 0 && w.pg + w.np < w.r.npg) {
                     // the segment's last unit
-                    sp.ctas = owner_of(u0 + share - 1 + (w.r.npg - (w.pg + w.np) + kTilePages - 1) / kTilePages, q, rem) - k + 1;
-                    sp.row0 = w.r.start + w.tok0, sp.head0 = w.head * a.G, sp.col0 = w.split * C::kDV;
+                    sp.ctas = owner_of(u0 + share - 1 + (w.r.npg - (w.pg + w.np) + kTilePages - 1) / kTilePages, q, rem) - part + 1;
+                    sp.row0 = w.r.start + w.tok0, sp.head0 = w.head * a.G, sp.col0 = split * C::kDV;
                     sp.rows[0] = rows;
                     sp.rows[1] = w.dual ? min(a.tokens_tile, w.r.n - w.tok0 - a.tokens_tile) * a.G : 0;
                 }
@@ -617,7 +625,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             }
             __syncwarp();
             if (lane < np) tma_load_5d(sSlots + slot * C::kSlotBytes + lane * C::kPageBytes, map, fb, 0, 0, chunk, 0, id);
-            if (++slot == C::kStages) slot = 0, ++round;
+            if (++slot == stages) slot = 0, ++round;
             return true;
         };
         auto load_q = [&](const Walk<D>& w, int s, int tok) -> bool {  // rows of drafted tokens tok .. of the piece
@@ -626,9 +634,9 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                 return false;
             if (lane == 0) {
                 const uint32_t fb = smem_u32(&q_full[s]);
-                mbar_expect_tx(fb, (uint32_t)(D / 64) * a.G * a.tokens_tile * 128);
+                mbar_expect_tx(fb, (uint32_t)(D / 64) * a.G * a.q_tokens * 128);
                 for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(sQ + s * C::kQBytes + c * kSubBytes, &tq, fb, c * 64, w.head * a.G, w.r.start + tok, 0);
+                    tma_load_4d(sQ + s * q_bytes + c * q_sub, &tq, fb, c * 64, w.head * a.G, w.r.start + tok, 0);
             }
             __syncwarp();
             if (s) ++q_uses[1];
@@ -653,7 +661,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
         };
         auto load_v = [&]() -> bool {
             for (int c = 0; c < C::kVC; ++c)
-                if (!load_slot(&tv, wv.head * (D / 64) + wv.split * (C::kDV / 64) + c * C::kSubs, wv.np, idv,
+                if (!load_slot(&tv, wv.head * (D / 64) + split * (C::kDV / 64) + c * C::kSubs, wv.np, idv,
                                wv.word() | kIsV | (c == C::kVC - 1 ? kChunkEnd : 0u)))
                     return false;
             if (C::kSets == 1) {
@@ -673,10 +681,10 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
         }
         // every issued copy has landed before the CTA may leave
         if (lane == 0) {
-            const int issued = round * C::kStages + slot;
-            for (int s = 0; s < C::kStages && s < issued; ++s) {
-                const int last = s + ((issued - 1 - s) / C::kStages) * C::kStages;
-                mbar_drain(smem_u32(&full[s]), (last / C::kStages) & 1, a.status, 0x43);
+            const int issued = round * stages + slot;
+            for (int s = 0; s < stages && s < issued; ++s) {
+                const int last = s + ((issued - 1 - s) / stages) * stages;
+                mbar_drain(smem_u32(&full[s]), (last / stages) & 1, a.status, 0x43);
             }
             if (q_uses[0] > 0) mbar_drain(smem_u32(&q_full[0]), (q_uses[0] - 1) & 1, a.status, 0x44);
             if (q_uses[1] > 0) mbar_drain(smem_u32(&q_full[1]), (q_uses[1] - 1) & 1, a.status, 0x44);
@@ -701,7 +709,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&empty[slot]));
             if ((word & kLast) && (word & kChunkEnd)) break;
-            if (++slot == C::kStages) slot = 0, phase ^= 1;
+            if (++slot == stages) slot = 0, phase ^= 1;
         }
     } else if (warp == C::kIssuer) {
         // ------------------------------- MMA issuer -------------------------------------------
@@ -717,9 +725,9 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             struct Pos {
                 int slot;
                 uint32_t phase;
-                __device__ __forceinline__ void advance(int n) {
+                __device__ __forceinline__ void advance(int n, int stages) {
                     slot += n;
-                    if (slot >= C::kStages) slot -= C::kStages, phase ^= 1u;
+                    if (slot >= stages) slot -= stages, phase ^= 1u;
                 }
             };
             Pos pk = {0, 0u}, pv = {C::kSets == 2 ? 1 : 0, 0u};
@@ -749,14 +757,14 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                     tc_fence_after();
                     const uint32_t dst = tS0 + buf_s * 128, idS = idesc_bf16_f32(128, (ws & 15u) * kPage, false, false);
                     const uint64_t dk = sdesc_sw128(sSlots + pk.slot * C::kSlotBytes, 16, C::kGroupStride);
-                    const uint64_t dq = sdesc_sw128(sQ + set * C::kQBytes + C::kSubs * c * kSubBytes, 16, 1024);
+                    const uint64_t dq = sdesc_sw128(sQ + set * q_bytes + C::kSubs * c * q_sub, 16, 1024);
 #pragma unroll
                     for (int i = 0; i < 4 * C::kSubs; ++i)
-                        umma_bf16_ss(dst, sdesc_at(dq, (i >> 2) * kSubBytes + (i & 3) * 32), sdesc_at(dk, (i >> 2) * 1024 + (i & 3) * 32), idS,
+                        umma_bf16_ss(dst, sdesc_at(dq, (i >> 2) * q_sub + (i & 3) * 32), sdesc_at(dk, (i >> 2) * 1024 + (i & 3) * 32), idS,
                                      (c | i) ? 1u : 0u);
                     if (last_use) {
                         umma_commit(smem_u32(&empty[pk.slot]));
-                        pk.advance(C::kSets);
+                        pk.advance(C::kSets, stages);
                     }
                 }
                 umma_commit(smem_u32(&s_full[2 * set + buf_s]));
@@ -808,7 +816,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                     }
                     if (last_use) {
                         umma_commit(smem_u32(&empty[vpos.slot]));
-                        vpos.advance(C::kSets);
+                        vpos.advance(C::kSets, stages);
                     }
                 }
                 umma_commit(smem_u32(&pv_done[2 * set + buf_p]));
@@ -862,7 +870,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a) {
                 v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
                 const int q = q0 + i;
                 if (q < sp.ctas) {
-                    const float* p = a.part + ((size_t)(2 * (blockIdx.x + q) + (q == 0 ? 1 : 0)) * a.rows_cap + row) * C::kRowF;
+                    const float* p = a.part + ((size_t)(2 * (blockIdx.x + q * C::kSplit) + (q == 0 ? 1 : 0)) * a.rows_cap + row) * C::kRowF;
                     ml[i] = __ldcg(reinterpret_cast<const float2*>(p + C::kDV));
                     v[i][0] = __ldcg(reinterpret_cast<const float4*>(p + col));
                     v[i][1] = __ldcg(reinterpret_cast<const float4*>(p + col) + 1);
@@ -902,14 +910,17 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(TreeArgs a) {
 template <int D, bool WIDE>
 cudaError_t launch_t(const TreeLaunch& L, TreeArgs a, cudaStream_t stream) {
     using C = TreeCfg<D>;
+    const int fit = (int)((C::kPool - C::kSets * a.q_rows * D * 2) / C::kSlotBytes);
+    a.stages = fit < C::kMaxStages ? fit : C::kMaxStages;
     cudaError_t e = cudaFuncSetAttribute(tree_paged_kernel<D, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
     // at most one CTA per tile of the longest step that fits the arguments
     const int tokens = a.tokens_tile * C::kSets;
     const long long groups = (L.max_q + tokens - 1) / tokens;
-    const long long most = ((long long)L.max_pages + kTilePages) / kTilePages * L.R * groups * L.Hkv * C::kSplit;
-    int grid = L.sms < kMaxGrid ? L.sms : kMaxGrid;
+    const long long most = ((long long)L.max_pages + kTilePages) / kTilePages * L.R * groups * L.Hkv;
+    int grid = (L.sms < kMaxGrid ? L.sms : kMaxGrid) / C::kSplit;
     if (most < grid) grid = (int)most;
+    grid *= C::kSplit;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -943,7 +954,7 @@ constexpr size_t kSpanBytes = (kMaxGrid * sizeof(TreeSpan) + 255) & ~size_t(255)
 
 }  // namespace
 
-int tree_tokens_per_tile(int G) { return 128 / G; }
+int tree_tokens_per_copy(int G, int max_q) { return max_q < 128 / G ? max_q : 128 / G; }
 
 size_t tree_workspace_bytes(int G, int max_q, int D) {
     const int dv = D < 256 ? D : 256;
@@ -957,9 +968,11 @@ cudaError_t launch_tree_paged(const TreeLaunch& L, cudaStream_t stream) {
     a.span = static_cast<TreeSpan*>(L.workspace);
     a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(L.workspace) + kSpanBytes);
     a.R = L.R, a.T = L.T, a.max_q = L.max_q, a.words = L.words, a.Hq = L.Hq, a.Hkv = L.Hkv, a.G = L.Hq / L.Hkv;
-    a.tokens_tile = tree_tokens_per_tile(a.G), a.rows_cap = rows_cap(a.G, L.max_q, L.D);
+    a.tokens_tile = 128 / a.G, a.rows_cap = rows_cap(a.G, L.max_q, L.D);
     a.max_pages = L.max_pages, a.num_pages = L.num_pages, a.window = L.window;
     a.scale_log2 = L.scale * 1.4426950408889634f;
+    a.q_tokens = tree_tokens_per_copy(a.G, L.max_q);
+    a.q_rows = (a.G * a.q_tokens + 7) / 8 * 8;
     const bool wide = L.max_q > a.tokens_tile;  // a request may have two row tiles
     switch (L.D) {
         case 64: return wide ? launch_t<64, true>(L, a, stream) : launch_t<64, false>(L, a, stream);
