@@ -604,6 +604,8 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
     if (!works || warp < C::kSets * kSetWarps) {
     } else if (warp == C::kProducer) {
         // ------------------------------- TMA producer ----------------------------------------
+        // what a step reads once goes through L2 as the first to be evicted
+        const uint64_t policy = l2_policy_evict_first();
         int slot = 0, round = 0;
         bool ok = true;
         int q_uses[2] = {0, 0};
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             return lane < w.np ? a.block_table[(size_t)w.b * a.max_pages + w.r.pg0 + w.pg + lane] : 0;
         };
         // one slot: np pages, lane i loads page i's 16 rows x kSlotCols columns
-        auto load_slot = [&](const CUtensorMap* map, int chunk, int np, int id, uint32_t word) -> bool {
+        auto load_slot = [&](const CUtensorMap* map, int chunk, int np, int id, uint32_t word, bool once) -> bool {
             if (id < 0 || id >= a.num_pages) {
                 atomicOr(a.status, DEVSTAT_BOUNDS);
                 id = 0;
@@ -624,7 +626,11 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                 mbar_expect_tx(fb, np * C::kPageBytes);
             }
             __syncwarp();
-            if (lane < np) tma_load_5d(sSlots + slot * C::kSlotBytes + lane * C::kPageBytes, map, fb, 0, 0, chunk, 0, id);
+            if (lane < np) {
+                const uint32_t dst = sSlots + slot * C::kSlotBytes + lane * C::kPageBytes;
+                if (once) tma_load_5d_hint(dst, map, fb, 0, 0, chunk, 0, id, policy);
+                else tma_load_5d(dst, map, fb, 0, 0, chunk, 0, id);
+            }
             if (++slot == stages) slot = 0, ++round;
             return true;
         };
@@ -653,7 +659,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                 if (wk.dual && !load_q(wk, 1, wk.tok0 + a.tokens_tile)) return false;
             }
             for (int c = 0; c < C::kKC; ++c)
-                if (!load_slot(&tk, wk.head * (D / 64) + c * C::kSubs, wk.np, idk, wk.word())) return false;
+                if (!load_slot(&tk, wk.head * (D / 64) + c * C::kSubs, wk.np, idk, wk.word(), C::kSplit == 1 && wk.r.groups == 1)) return false;
             if (C::kSets == 2) idv = idk, wv = wk;
             wk.next(a);
             if (wk.more()) idk = page_id(wk);
@@ -662,7 +668,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
         auto load_v = [&]() -> bool {
             for (int c = 0; c < C::kVC; ++c)
                 if (!load_slot(&tv, wv.head * (D / 64) + split * (C::kDV / 64) + c * C::kSubs, wv.np, idv,
-                               wv.word() | kIsV | (c == C::kVC - 1 ? kChunkEnd : 0u)))
+                               wv.word() | kIsV | (c == C::kVC - 1 ? kChunkEnd : 0u), wv.r.groups == 1))
                     return false;
             if (C::kSets == 1) {
                 wv.next(a);
