@@ -7,36 +7,47 @@
 // A row that sees nothing gets o = 0 and lse = -inf.
 //
 // Few rows over many keys: K and V must be read once for all rows that share them, and one request's
-// keys spread over the whole GPU.
+// keys spread over the whole GPU. The floor is the bytes of K and V: a byte serves one FLOP for each row
+// of its KV head, and the tensor cores could do some 280 in the time it takes to arrive.
 //  * A row tile packs the drafted tokens and the G query heads of one KV head into the 128 rows of
 //    an MMA (row = token * G + head, 128 / G tokens a tile), so a KV head's keys serve all of them.
 //  * At D <= 128 tensor memory holds two O accumulators, so a CTA has two sets of softmax warps, each
 //    with its own O, Q tile and running state. Where a request has more rows than one tile, two row
 //    tiles go through together, one per set, and share every key tile (12 requests of 5 to 24 thousand
-//    keys and 33 to 64 drafts, Hq 32, Hkv 8, D 128: alone, each of the two row tiles read all of K and
-//    V from DRAM). Otherwise consecutive segments alternate between the sets: one set's epilogue runs
-//    beside the other's first tiles.
+//    keys and 33 to 64 drafts, Hq 32, Hkv 8, D 128: 193 us, against 299 when each of the two row tiles
+//    read all of K and V for itself; 170 with the later steps). Otherwise consecutive segments alternate
+//    between the sets: one set's epilogue runs beside the other's first tiles. (Key tiles of one segment
+//    in turn to both sets, whose results the epilogue then adds: 45 us against 39 for a batch of 64.)
 //  * At D = 512 a CTA computes one 256-column half of O; the two CTAs of a key range run side by side
 //    (CTAs 2 i and 2 i + 1), so the second copy of K, for the scores, comes from L2.
-//  * A unit of work is one key tile, up to eight pages (128 keys), of one segment = (request, KV head, row
-//    tile or pair of them). All units are laid end to end and CTA k
-//    takes the k-th equal share: it may finish one segment, run through some and start another. (Equal
-//    shares of pages left some CTAs a third more tiles than others, and a tile costs the softmax the same
-//    however few pages it has.) A segment that one CTA covers is written out by it; of a shared one every
-//    CTA leaves (O, m, l) unnormalised in the workspace and tree_merge_kernel combines them (launched
-//    with programmatic serialisation).
-//  * The tiles go through an mbarrier ring, and the pipeline runs on across segments. Tensor memory: O (fp32, up to 256 columns in all) and two
-//    score buffers of 128 columns, P (bf16) over the scores. Only the pages of a tile that exist are
-//    loaded and multiplied (N of Q K^T and K of P V follow them, a page being one K step of 16), so
-//    only the last page's slots past L need care: a fixer warp zeroes those V rows before their P V (P
-//    is 0 there, but 0 * NaN is not).
+//  * A unit of work is one key tile, up to eight pages (128 keys), of one segment = (request, KV head,
+//    row tile or pair of them). All units are laid end to end and CTA k takes the k-th equal share: it
+//    may finish one segment, run through some and start another. (Pages as units: 46.6 us against 43.6
+//    for a batch of 64. Some CTAs then had a third more tiles than others, and a tile costs the softmax
+//    the same however few pages it has.) A segment that one CTA covers is written out by it; of a shared
+//    one every CTA leaves (O, m, l) unnormalised in the workspace and tree_merge_kernel, launched with
+//    programmatic serialisation, combines them.
+//  * The tiles go through an mbarrier ring, and the pipeline runs on across segments. Tensor memory: O
+//    (fp32, up to 256 columns in all) and two score buffers of 128 columns, P (bf16) over the scores.
+//    Only the pages of a tile that exist are loaded and multiplied (N of Q K^T and K of P V follow them,
+//    a page being one K step of 16), so only the last page's slots past L need care: a fixer warp zeroes
+//    those V rows before their P V (P is 0 there, but 0 * NaN is not).
+//
+// What bounds it, 152 SMs: at D = 256 the memory (64 requests of 1 to 4 thousand keys, window 1024:
+// 185 us, 6.0 TB/s of K and V). At D = 128 and up to 128 rows a request (64 requests of 256 to 1024 keys
+// and 5 to 16 drafts: 40 us, 4.3 TB/s) a key tile takes the softmax of its set 1.2 us, the loads 1.5 us
+// and the producer's copies 1.2 us, all overlapped; 3 us pass before the first load, 3 until it arrives
+// and 4 in the last tile, the epilogue and the merge. With two row tiles (170 us, 4.9 TB/s) each set has
+// one score buffer, so its softmax (0.95 us) and the MMAs between two of them (1 us) take turns.
 //
 // Warp roles: four softmax warps a set (0-3, and 4-7 at two sets), one TMEM lane quarter each and one
 // thread a row, so nothing of a row is exchanged; then an idle warp, the fixer, the TMA producer (lanes
 // 0-7: a page each) and the MMA issuer. The last two sit on the schedulers of quarters 2 and 3, which
 // have no rows where a tile has 64 or fewer. Quarters without rows only keep the barriers going. The
 // issuer is one thread that reads what to do from a word the producer leaves with every copy: walking
-// the work itself took it longer than the MMAs (per 128-key tile 1.4 us, of which 0.56 us of MMAs).
+// the work itself took it longer than the MMAs (per 128-key tile 1.4 us, of which 0.56 us of MMAs). The
+// idle warp as a second producer, for V alone, gained 1 % at two row tiles and cost 4 % of the batch of
+// 64, whose busy quarter it shares a scheduler with.
 #include <cuda_runtime.h>
 
 #include "attn_internal.h"
@@ -138,7 +149,7 @@ __device__ __forceinline__ long long req_units(const TreeArgs& a, const Req& r) 
     return (long long)r.tiles * r.groups * a.Hkv;
 }
 
-// A copy's word: pages of the tile in bits 0-3, rows of its last page to keep in bits 4-7 (0: all), and
+// A copy's word: pages of the tile in bits 0-3, rows of its last page to keep in bits 4-7 (0: all), and flags.
 enum : uint32_t {
     kBegins = 1u << 8,    // first tile of a piece
     kEnds = 1u << 9,      // last tile of a piece
@@ -465,12 +476,12 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                 tc_fence_after();
                 // l sums p in fp32; the P of the product is rounded to bf16 (an MMA takes both operands in V's
                 // type), half a step of 2^-8 that averages out over the keys.
-                // WIDE: the whole row of 128 scores in registers (12 long contexts, two row tiles: 172 us against
-                // 184 in the other form). Otherwise two passes over the tile, 64 scores at a time: the maximum of
+                // WIDE: the whole row of 128 scores in registers (12 long contexts, two row tiles: 174 us against
+                // 181 in the other form). Otherwise two passes over the tile, 64 scores at a time: the maximum of
                 // the lower and the upper half, then the exponentials of the upper half, still in registers, and
                 // of the lower one, read again. One loop, so that each part's code is there once: a CTA of a short
                 // call runs some twenty tiles, and the instruction fetches of a longer body cost more than they
-                // save (batch of 64: 43.6 us against 49.8).
+                // save (batch of 64: 39.4 us against 47.8 with the whole row).
                 if constexpr (WIDE) {
                     float s[128];
                     {

@@ -239,6 +239,30 @@ def test_inconsistent_requests_are_reported_and_skipped(D):
     check(L, [0, 3, 2, 14, 18], 6, list(rows[1]) + list(rows[2]))  # decreasing, then more than max_q_len
 
 
+@pytest.mark.parametrize("D", [64, 128, 512])
+@pytest.mark.parametrize("R", [1, 31, 32, 33, 64, 65])
+def test_numbers_of_requests(D, R):
+    """Up to 32 requests each warp finds its share alone, beyond that the CTA does; the one in the middle is skipped."""
+    p = problem([(61 * i) % 200 for i in range(R)], [i % 4 if i else 2 for i in range(R)], 4, 2, D)
+    bad = R // 2 if R > 1 else None
+    lens = list(p["lens"])
+    if bad is not None:
+        lens[bad] = -1
+    T = p["cu"][-1]
+    o = torch.full((T, 4, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4, T), 7.0, device="cuda")
+    attn.attn_tree_paged(p["q"].cuda(), p["kc"].cuda(), p["vc"].cuda(), p["table"].cuda(), i32(lens), i32(p["cu"]), p["mask"].cuda(),
+                         3, o, lse, scale=p["scale"])
+    assert attn.attn_get_device_status() == (0 if bad is None else 7)
+    ro, to, rl, tl = ref.tree(p["q"], p["kc"], p["vc"], p["table"], p["lens"], p["cu"], p["mask"], p["scale"])
+    good = torch.ones(T, dtype=torch.bool)
+    if bad is not None:
+        good[p["cu"][bad]: p["cu"][bad + 1]] = False
+    ref.close("o", o.cpu()[good], ro[good], to[good])
+    ref.close("lse", lse.cpu()[:, good], rl[:, good], tl[:, good])
+    assert (o.cpu()[~good] == 7.0).all() and (lse.cpu()[:, ~good] == 7.0).all()
+
+
 def test_bad_page_ids_are_reported():
     """A page id outside the pool stands for page 0; other requests are not touched."""
     p = problem([40, 30], [3, 5], 4, 2, 128, poison=False)
