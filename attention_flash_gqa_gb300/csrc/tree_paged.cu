@@ -70,7 +70,8 @@ struct TreeCfg {
     static constexpr int kDV = D < 256 ? D : 256;      // O columns per segment
     static constexpr int kSplit = D / kDV;
     static constexpr int kSets = tree_sets(D);
-    static constexpr int kFixer = kSets * kSetWarps + 1, kProducer = kFixer + 1, kIssuer = kProducer + 1;
+    // (at one set kIssuer0 is idle, so that the others keep their schedulers)
+    static constexpr int kIssuer0 = kSets * kSetWarps, kFixer = kIssuer0 + 1, kProducer = kFixer + 1, kIssuer = kProducer + 1;
     static constexpr int kWarps = kIssuer + 1;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kSubs = D >= 128 ? 2 : 1;     // 64-column sub-tiles per slot
@@ -231,11 +232,12 @@ __device__ __forceinline__ int owner_of(int u, int q, int rem) {
     return u < big ? u / (q + 1) : rem + (u - big) / q;
 }
 
-template <int D, bool WIDE>
+template <int D>
 __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
     tree_paged_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ TreeArgs a) {
     using C = TreeCfg<D>;
+    constexpr bool kHalf = C::kSets == 2;  // steps of half a key tile
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < C::kMaxStages; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
-            mbar_init(smem_u32(&empty[s]), 2);  // the MMAs that read it, and the fixer
+            mbar_init(smem_u32(&empty[s]), C::kSets + 1);  // each issuer's MMAs that read it, and the fixer
             mbar_init(smem_u32(&vfix[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             mbar_init(smem_u32(&p_full[i]), kSetWarps);
             mbar_init(smem_u32(&pv_done[i]), 1);
         }
-        mbar_init(smem_u32(mma_idle), 1);
+        mbar_init(smem_u32(mma_idle), C::kSets);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -394,9 +396,6 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
     if (!works) {
         // no units left for this CTA
     } else if (warp < C::kSets * kSetWarps) {
-        // Registers for a row of scores: 12 warps at 168 are 64512, and 8 x 32 x 208 + 4 x 32 x 80 = 63488 of
-        // them are handed out again.
-        if constexpr (WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // --------------------------------- softmax ----------------------------------------------
         const int set = warp / kSetWarps, quad = warp & 3;
         const int row = quad * 32 + lane;  // row of the tile = TMEM lane
@@ -404,18 +403,15 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
         const uint32_t tOset = tO + set * C::kDV + lane_base;
         float m_ref = -INFINITY, l = 0.f;
         int first_key = 0, token = 0, pg_begin = 0, rows = 0, ctx = 0;
-        int step = 0;                       // global step of the tile (its parity: the score buffer)
+        int step = 0;                       // tile of the share
         uint32_t phases = 0u;               // of the set's two buffers
         int prev = 0;                       // the set's step before: buffer, and its phase
         uint32_t prev_phase = 0u;
         bool busy = false, ok = true;
         Walk<D> w;
         w.start(a, first_b, first_req, first_off, share);
-        for (; ok && w.more(); step += w.dual ? 2 : 1, w.next(a)) {
+        for (; ok && w.more(); ++step, w.next(a)) {
             if (!w.mine(set)) continue;
-            const int buf = (step + (w.dual ? set : 0)) & 1;
-            const uint32_t phase = phases >> buf & 1u;
-            phases ^= 1u << buf;
             if (w.begins) {
                 const int tok = w.tok0 + (w.dual && set ? a.tokens_tile : 0);  // of the request
                 ctx = w.r.L - w.r.n;
@@ -426,173 +422,174 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                 token = w.r.start + min(tok + row / a.G, w.r.n - 1);
                 first_key = a.window > 0 ? max(0, min(ctx, max(a.positions[token], ctx) - a.window + 1)) : 0;
             }
-            const uint32_t tS = tS0 + buf * 128 + lane_base;
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[2 * set + buf]), phase, abort_flag, a.status, 0x4c));
-            if (busy && ok) {
-                const int key0 = (w.r.pg0 + w.pg) * kPage;
-                const bool edge = __any_sync(0xffffffffu, key0 + 127 >= ctx || w.np < kTilePages || key0 < first_key);
-                auto visible = [&](int half) -> uint64_t {  // the row's visible keys of 64 half .. of the tile
-                    const int k0 = key0 + 64 * half;
-                    uint64_t vis = low_bits(w.np * kPage - 64 * half) & ~low_bits(first_key - k0);
-                    const int dc = ctx - k0;  // column of the first drafted token
-                    if (dc < 64) {
-                        const int d0 = max(0, -dc), wi = d0 >> 5, sh = d0 & 31;
-                        const int32_t* mw = a.mask + (size_t)token * a.words;
-                        auto word = [&](int i) -> uint64_t { return i < a.words ? (uint64_t)(uint32_t)mw[i] : 0ull; };
-                        uint64_t bits = (word(wi) | word(wi + 1) << 32) >> sh;
-                        if (sh) bits |= word(wi + 2) << (64 - sh);
-                        bits &= low_bits(w.r.n - d0);
-                        vis &= low_bits(dc) | bits << max(dc, 0);
-                    }
-                    return vis;
-                };
-                // The running maximum is lazy: it moves only when a row's tile maximum exceeds it by more than
-                // 2^8, so p stays below that and most tiles need no rescale.
-                auto move_max = [&](float mx) -> bool {
-                    const float m_tile = mx * a.scale_log2;
-                    const bool moved = m_tile > m_ref + kRescaleLog2;
-                    if (!__any_sync(0xffffffffu, moved)) return true;
-                    const float alpha = !moved ? 1.f : m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_tile);
-                    if (moved) m_ref = m_tile;
-                    l *= alpha;
-                    if (w.begins) return true;
-                    // P V of the set's step before, and so every earlier one, is complete
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + prev]), prev_phase, abort_flag, a.status, 0x4d));
-                    if (!ok) return false;
+            const int steps = kHalf && w.np > kTilePages / 2 ? 2 : 1;
+#pragma unroll 1
+            for (int h = 0; h < steps; ++h) {
+                const int buf = kHalf ? h : step & 1;
+                const uint32_t phase = phases >> buf & 1u;
+                phases ^= 1u << buf;
+                const uint32_t tS = tS0 + (kHalf ? (2 * set + h) * 64 : buf * 128) + lane_base;
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[2 * set + buf]), phase, abort_flag, a.status, 0x4c));
+                if (busy && ok) {
+                    const int key0 = (w.r.pg0 + w.pg) * kPage;
+                    const bool edge = __any_sync(0xffffffffu, key0 + 127 >= ctx || w.np < kTilePages || key0 < first_key);
+                    auto visible = [&](int half) -> uint64_t {  // the row's visible keys of 64 half .. of the tile
+                        const int k0 = key0 + 64 * half;
+                        uint64_t vis = low_bits(w.np * kPage - 64 * half) & ~low_bits(first_key - k0);
+                        const int dc = ctx - k0;  // column of the first drafted token
+                        if (dc < 64) {
+                            const int d0 = max(0, -dc), wi = d0 >> 5, sh = d0 & 31;
+                            const int32_t* mw = a.mask + (size_t)token * a.words;
+                            auto word = [&](int i) -> uint64_t { return i < a.words ? (uint64_t)(uint32_t)mw[i] : 0ull; };
+                            uint64_t bits = (word(wi) | word(wi + 1) << 32) >> sh;
+                            if (sh) bits |= word(wi + 2) << (64 - sh);
+                            bits &= low_bits(w.r.n - d0);
+                            vis &= low_bits(dc) | bits << max(dc, 0);
+                        }
+                        return vis;
+                    };
+                    // The running maximum is lazy: it moves only when a row's tile maximum exceeds it by more than
+                    // 2^8, so p stays below that and most tiles need no rescale.
+                    auto move_max = [&](float mx) -> bool {
+                        const float m_tile = mx * a.scale_log2;
+                        const bool moved = m_tile > m_ref + kRescaleLog2;
+                        if (!__any_sync(0xffffffffu, moved)) return true;
+                        const float alpha = !moved ? 1.f : m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m_tile);
+                        if (moved) m_ref = m_tile;
+                        l *= alpha;
+                        if (w.begins && h == 0) return true;
+                        // P V of the set's step before, and so every earlier one, is complete
+                        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + prev]), prev_phase, abort_flag, a.status, 0x4d));
+                        if (!ok) return false;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < C::kDV / 16; ++c) {
+                            uint32_t raw[16];
+                            tmem_ld16(tOset + c * 16, raw);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
+                            tmem_st16(tOset + c * 16, raw);
+                        }
+                        return true;
+                    };
+                    float2 rs[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                    const float2 sc = make_float2(a.scale_log2, a.scale_log2);
                     tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < C::kDV / 16; ++c) {
-                        uint32_t raw[16];
-                        tmem_ld16(tOset + c * 16, raw);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) raw[e] = __float_as_uint(__uint_as_float(raw[e]) * alpha);
-                        tmem_st16(tOset + c * 16, raw);
-                    }
-                    return true;
-                };
-                float2 rs[2] = {{0.f, 0.f}, {0.f, 0.f}};
-                const float2 sc = make_float2(a.scale_log2, a.scale_log2);
-                tc_fence_after();
-                // l sums p in fp32; the P of the product is rounded to bf16 (an MMA takes both operands in V's
-                // type), half a step of 2^-8 that averages out over the keys.
-                // WIDE: the whole row of 128 scores in registers (12 long contexts, two row tiles: 174 us against
-                // 181 in the other form). Otherwise two passes over the tile, 64 scores at a time: the maximum of
-                // the lower and the upper half, then the exponentials of the upper half, still in registers, and
-                // of the lower one, read again. One loop, so that each part's code is there once: a CTA of a short
-                // call runs some twenty tiles, and the instruction fetches of a longer body cost more than they
-                // save (batch of 64: 39.4 us against 47.8 with the whole row).
-                if constexpr (WIDE) {
-                    float s[128];
-                    {
-                        uint32_t raw[4][32];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, raw[c]);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
-                    }
-                    if (edge) {  // hidden keys to -inf
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const uint64_t vis = visible(half);
-                            const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                if (!(v0 >> c & 1u)) s[64 * half + c] = -INFINITY;
-                                if (!(v1 >> c & 1u)) s[64 * half + 32 + c] = -INFINITY;
-                            }
-                        }
-                    }
-                    float m8[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) m8[i] = s[i];
-#pragma unroll
-                    for (int c = 8; c < 128; c += 8)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], s[c + i]);
-                    const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-                    if (!move_max(mx)) break;
-                    const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                    const float2 mm = make_float2(-m_use, -m_use);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int e = 0; e < 64; e += 2) {
-                            const float2 x2 = __ffma2_rn(make_float2(s[64 * half + e], s[64 * half + e + 1]), sc, mm);
-                            const float2 p2 = make_float2(fast_exp2(x2.x), fast_exp2(x2.y));
-                            rs[(e >> 1) & 1] = __fadd2_rn(rs[(e >> 1) & 1], p2);
-                            pk[e >> 1] = pack_bf16x2(p2.x, p2.y);
-                        }
-                        tmem_st32(tS + 64 * half, pk);
-                    }
-                } else {
-                    float s[64];
-                    float mx = -INFINITY;
-                    float2 mm = {0.f, 0.f};
-#pragma unroll 1
-                    for (int pass = 0; pass < 4; ++pass) {
-                        const int half = pass == 1 || pass == 2;
-                        if (pass != 2) {  // scores of keys 64 half .. of the tile, hidden ones at -inf
+                    // l sums p in fp32; the P of the product is rounded to bf16 (an MMA takes both operands in V's
+                    // type), half a step of 2^-8 that averages out over the keys.
+                    // Two sets: the half tile's 64 scores in registers. One set: two passes over the tile, 64 scores at a
+                    // time: the maximum of the lower and the upper half, then the exponentials of the upper half, still
+                    // in registers, and of the lower one, read again. One loop, so that each part's code is there once:
+                    // a CTA of a short call runs some twenty tiles, and the instruction fetches of a longer body cost
+                    // more than they save (64 requests, window 1024, D 256: 192 us against 202 unrolled).
+                    if constexpr (kHalf) {
+                        float s[64];
+                        {
                             uint32_t raw[2][32];
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 * half + c * 32, raw[c]);
+                            for (int c = 0; c < 2; ++c) tmem_ld32(tS + c * 32, raw[c]);
                             tmem_ld_wait();
 #pragma unroll
                             for (int c = 0; c < 2; ++c)
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
-                            if (edge) {
-                                const uint64_t vis = visible(half);
-                                const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
+                        }
+                        if (edge) {  // hidden keys to -inf
+                            const uint64_t vis = visible(h);
+                            const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
 #pragma unroll
-                                for (int c = 0; c < 32; ++c) {
-                                    if (!(v0 >> c & 1u)) s[c] = -INFINITY;
-                                    if (!(v1 >> c & 1u)) s[32 + c] = -INFINITY;
+                            for (int c = 0; c < 32; ++c) {
+                                if (!(v0 >> c & 1u)) s[c] = -INFINITY;
+                                if (!(v1 >> c & 1u)) s[32 + c] = -INFINITY;
+                            }
+                        }
+                        float m8[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) m8[i] = s[i];
+#pragma unroll
+                        for (int c = 8; c < 64; c += 8)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], s[c + i]);
+                        const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+                        if (!move_max(mx)) break;
+                        const float m_use = m_ref == -INFINITY ? 0.f : -m_ref;
+                        const float2 mm = make_float2(m_use, m_use);
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int e = 0; e < 64; e += 2) {
+                            const float2 x2 = __ffma2_rn(make_float2(s[e], s[e + 1]), sc, mm);
+                            const float2 p2 = make_float2(fast_exp2(x2.x), fast_exp2(x2.y));
+                            rs[(e >> 1) & 1] = __fadd2_rn(rs[(e >> 1) & 1], p2);
+                            pk[e >> 1] = pack_bf16x2(p2.x, p2.y);
+                        }
+                        tmem_st32(tS, pk);
+                    } else {
+                        float s[64];
+                        float mx = -INFINITY;
+                        float2 mm = {0.f, 0.f};
+#pragma unroll 1
+                        for (int pass = 0; pass < 4; ++pass) {
+                            const int half = pass == 1 || pass == 2;
+                            if (pass != 2) {  // scores of keys 64 half .. of the tile, hidden ones at -inf
+                                uint32_t raw[2][32];
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) tmem_ld32(tS + 64 * half + c * 32, raw[c]);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
+                                if (edge) {
+                                    const uint64_t vis = visible(half);
+                                    const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
+#pragma unroll
+                                    for (int c = 0; c < 32; ++c) {
+                                        if (!(v0 >> c & 1u)) s[c] = -INFINITY;
+                                        if (!(v1 >> c & 1u)) s[32 + c] = -INFINITY;
+                                    }
                                 }
                             }
-                        }
-                        if (pass < 2) {
-                            float m8[8];
+                            if (pass < 2) {
+                                float m8[8];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) m8[i] = s[i];
+                                for (int i = 0; i < 8; ++i) m8[i] = s[i];
 #pragma unroll
-                            for (int c = 8; c < 64; c += 8)
+                                for (int c = 8; c < 64; c += 8)
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], s[c + i]);
-                            mx = fmaxf(mx, fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))));
-                            if (pass == 0) continue;
-                            if (!move_max(mx)) break;
-                            mm.x = mm.y = m_ref == -INFINITY ? 0.f : -m_ref;
-                        } else {
-                            uint32_t pk[32];
+                                    for (int i = 0; i < 8; ++i) m8[i] = fmaxf(m8[i], s[c + i]);
+                                mx = fmaxf(mx, fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))));
+                                if (pass == 0) continue;
+                                if (!move_max(mx)) break;
+                                mm.x = mm.y = m_ref == -INFINITY ? 0.f : -m_ref;
+                            } else {
+                                uint32_t pk[32];
 #pragma unroll
-                            for (int e = 0; e < 64; e += 2) {
-                                const float2 x2 = __ffma2_rn(make_float2(s[e], s[e + 1]), sc, mm);
-                                const float2 p2 = make_float2(fast_exp2(x2.x), fast_exp2(x2.y));
-                                rs[(e >> 1) & 1] = __fadd2_rn(rs[(e >> 1) & 1], p2);
-                                pk[e >> 1] = pack_bf16x2(p2.x, p2.y);
+                                for (int e = 0; e < 64; e += 2) {
+                                    const float2 x2 = __ffma2_rn(make_float2(s[e], s[e + 1]), sc, mm);
+                                    const float2 p2 = make_float2(fast_exp2(x2.x), fast_exp2(x2.y));
+                                    rs[(e >> 1) & 1] = __fadd2_rn(rs[(e >> 1) & 1], p2);
+                                    pk[e >> 1] = pack_bf16x2(p2.x, p2.y);
+                                }
+                                tmem_st32(tS + 64 * half, pk);
                             }
-                            tmem_st32(tS + 64 * half, pk);
                         }
                     }
+                    l += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
+                    tmem_st_wait();
+                    tc_fence_before();
                 }
-                l += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
-                tmem_st_wait();
-                tc_fence_before();
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * set + buf]));
+                prev = buf, prev_phase = phase;
             }
             if (!ok) break;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * set + buf]));
-            prev = buf, prev_phase = phase;
             if (!w.ends) continue;
 
             // ---- the piece is done: results, or this CTA's partials --------------------------------
             // (a quarter without rows waits as well: its arrival on o_free must not run a piece ahead)
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + buf]), phase, abort_flag, a.status, 0x4e));
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[2 * set + prev]), prev_phase, abort_flag, a.status, 0x4e));
             if (!ok) break;
             tc_fence_after();
             if (busy) {
@@ -646,8 +643,6 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                 a.span[k] = sp;
             }
         }
-    } else {
-        if constexpr (WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     }
     if (!works || warp < C::kSets * kSetWarps) {
     } else if (warp == C::kProducer) {
@@ -765,97 +760,166 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             if ((word & kLast) && (word & kChunkEnd)) break;
             if (++slot == stages) slot = 0, phase ^= 1;
         }
-    } else if (warp == C::kIssuer) {
-        // ------------------------------- MMA issuer -------------------------------------------
-        // A step is a key tile for one row tile; step j uses score buffer j % 2, and S(j + 2) follows P V(j),
-        // which has read P from that buffer (the pipe runs in order). Two row tiles: tile i is steps s
-        // (set 0) and s + 1 (set 1).
+    } else if (C::kSets == 2 && (warp == C::kIssuer || warp == C::kIssuer0)) {
+        // ------------------------------- MMA issuers at two sets, one for each -----------------
+        // A step is half a key tile: scores of (set, half) go to that pair's buffer of 64 columns, after the P V
+        // that last read it (the pipe runs in order). Beside P V of tile i - 1 come the scores of tile i.
+        if (elect_one()) {
+            constexpr uint32_t idO = idesc_bf16_f32(128, C::kSlotCols, false, true);  // V is N-major
+            const uint32_t set = warp == C::kIssuer ? 1u : 0u;
+            auto wait = [&](uint64_t* bar, uint32_t phase, unsigned site) -> bool {
+                return mbar_wait(smem_u32(bar), phase, abort_flag, a.status, site);
+            };
+            auto mine = [&](uint32_t word) -> bool { return (word & kDual) || ((word & kSet1) ? 1u : 0u) == set; };
+            const uint64_t dq = sdesc_sw128(sQ + set * q_bytes, 16, 1024);
+            const uint32_t tD = tO + set * C::kDV, tB = tS0 + set * 128;
+            int ks = 0, vs = 1;                                   // slots of K and V
+            uint32_t k_phase = 0u, v_phase = 0u, fix_phase = 0u;  // fix_phase: bits by slot
+            uint32_t q_phase = 0u, o_phase = 0u, p_phase = 0u;    // p_phase: bits by half
+            bool o_used = false, ok = true, more_s = true, before = false;
+            uint32_t ws = 0u, wp = 0u;  // the words of tiles i and i - 1
+            do {
+                if (before) {
+                    if (!(ok = wait(&full[vs], v_phase, 0x49))) break;
+                    if (wp >> 4 & 15u) {
+                        if (mine(wp) && !(ok = wait(&vfix[vs], fix_phase >> vs & 1u, 0x4f))) break;
+                        fix_phase ^= 1u << vs;
+                    }
+                }
+                const bool does_p = before && mine(wp);
+                bool does_s = false;
+#pragma unroll
+                for (uint32_t h = 0; h < 2u; ++h) {
+                    const int np = min((int)(wp & 15u) - 4 * (int)h, 4);
+                    if (does_p && np > 0) {
+                        const bool fresh = (wp & kBegins) && h == 0u;
+                        if (fresh) {  // the set's piece before has been read out of O
+                            if (o_used && !(ok = wait(&o_free[set], o_phase, 0x48))) break;
+                            if (o_used) o_phase ^= 1u;
+                            o_used = true;
+                        }
+                        if (!(ok = wait(&p_full[2 * set + h], p_phase >> h & 1u, 0x47))) break;
+                        p_phase ^= 1u << h;
+                        tc_fence_after();
+                        const uint64_t dv = sdesc_sw128(sSlots + vs * C::kSlotBytes + h * 4 * C::kPageBytes, 1024, C::kGroupStride);
+                        const uint32_t tP = tB + h * 64;
+                        umma_bf16_ts(tD, tP, dv, idO, fresh ? 0u : 1u);
+#pragma unroll
+                        for (int kk = 1; kk < 4; ++kk)
+                            if (kk < np) umma_bf16_ts(tD, tP + kk * 8, sdesc_at(dv, kk * C::kPageBytes), idO, 1u);
+                        umma_commit(smem_u32(&pv_done[2 * set + h]));
+                    }
+                    if (h == 0u && more_s) {
+                        if (!(ok = wait(&full[ks], k_phase, 0x46))) break;
+                        ws = words[ks];
+                        does_s = mine(ws);
+                        if (does_s && (ws & kBegins)) {
+                            if (!(ok = wait(&q_full[set], q_phase, 0x45))) break;
+                            q_phase ^= 1u;
+                        }
+                        tc_fence_after();
+                    }
+                    const int keys = min((int)(ws & 15u) * kPage - 64 * (int)h, 64);
+                    if (does_s && keys > 0) {
+                        const uint32_t idS = idesc_bf16_f32(128, keys, false, false);
+                        const uint64_t dk = sdesc_sw128(sSlots + ks * C::kSlotBytes + h * 8 * C::kGroupStride, 16, C::kGroupStride);
+#pragma unroll
+                        for (int i = 0; i < 4 * C::kSubs; ++i)
+                            umma_bf16_ss(tB + h * 64, sdesc_at(dq, (i >> 2) * q_sub + (i & 3) * 32), sdesc_at(dk, (i >> 2) * 1024 + (i & 3) * 32),
+                                         idS, i ? 1u : 0u);
+                        umma_commit(smem_u32(&s_full[2 * set + h]));
+                    }
+                }
+                if (!ok) break;
+                if (before) {  // done with the V slot
+                    if (does_p) umma_commit(smem_u32(&empty[vs]));
+                    else mbar_arrive(smem_u32(&empty[vs]));
+                    vs += 2;
+                    if (vs >= stages) vs -= stages, v_phase ^= 1u;
+                    if (wp & kLast) break;
+                }
+                if (more_s) {  // and with the K slot
+                    if (does_s) {
+                        umma_commit(smem_u32(&empty[ks]));
+                        if (ws & kEnds) umma_commit(smem_u32(&q_free[set]));
+                    } else {
+                        mbar_arrive(smem_u32(&empty[ks]));
+                    }
+                    ks += 2;
+                    if (ks >= stages) ks -= stages, k_phase ^= 1u;
+                    wp = ws, before = true;
+                    if (ws & kLast) more_s = false;
+                }
+            } while (true);
+            umma_commit(smem_u32(mma_idle));
+            mbar_drain(smem_u32(mma_idle), 0, a.status, 0x4a);
+        }
+        __syncwarp();
+    } else if (C::kSets == 1 && warp == C::kIssuer) {
+        // ------------------------------- MMA issuer at one set --------------------------------
+        // A step is a key tile; step j uses score buffer j % 2, and S(j + 2) follows P V(j), which has read P
+        // from that buffer (the pipe runs in order).
         if (elect_one()) {
             constexpr uint32_t idO = idesc_bf16_f32(128, C::kSlotCols, false, true);  // V is N-major
             auto wait = [&](uint64_t* bar, uint32_t phase, unsigned site) -> bool {
                 return mbar_wait(smem_u32(bar), phase, abort_flag, a.status, site);
             };
-            // ring positions: K and V in turn at two sets, else one position for both
-            struct Pos {
-                int slot;
-                uint32_t phase;
-                __device__ __forceinline__ void advance(int n, int stages) {
-                    slot += n;
-                    if (slot >= stages) slot -= stages, phase ^= 1u;
-                }
+            int slot = 0;  // of the ring, and its phase
+            uint32_t phase = 0u;
+            auto advance = [&]() {
+                if (++slot == stages) slot = 0, phase ^= 1u;
             };
-            Pos pk = {0, 0u}, pv = {C::kSets == 2 ? 1 : 0, 0u};
-            Pos& vpos = C::kSets == 2 ? pv : pk;
-            uint32_t ws = 0u, wp = 0u;                    // the tiles' words
-            uint32_t half_s = 0u, half_p = 0u;            // which of a pair's row tiles is next
+            uint32_t ws = 0u, wp = 0u;                        // the tiles' words
             uint32_t buf_s = 0u, buf_p = 0u, fix_phase = 0u;  // fix_phase: bits by slot
-            uint32_t q_phase = 0u, o_phase = 0u, o_used = 0u, p_phase = 0u;  // bits by set, or 2 set + buffer
-            bool more_s = true, more_p = true, ok = true;
+            uint32_t q_phase = 0u, o_phase = 0u, p_phase = 0u;  // p_phase: bits by buffer
+            bool more_s = true, more_p = true, ok = true, o_used = false;
             auto issue_s = [&]() -> bool {
-                uint32_t set = 0u;
-                bool last_use = true;
 #pragma unroll 1
                 for (int c = 0; c < C::kKC; ++c) {
-                    if (half_s == 0u) {
-                        if (!wait(&full[pk.slot], pk.phase, 0x46)) return false;
-                        ws = words[pk.slot];
-                    }
-                    if (c == 0) {
-                        set = (ws & kDual) ? half_s : (ws & kSet1) ? 1u : 0u;
-                        last_use = !(ws & kDual) || half_s;
-                        if (ws & kBegins) {
-                            if (!wait(&q_full[set], q_phase >> set & 1u, 0x45)) return false;
-                            q_phase ^= 1u << set;
-                        }
+                    if (!wait(&full[slot], phase, 0x46)) return false;
+                    ws = words[slot];
+                    if (c == 0 && (ws & kBegins)) {
+                        if (!wait(&q_full[0], q_phase, 0x45)) return false;
+                        q_phase ^= 1u;
                     }
                     tc_fence_after();
                     const uint32_t dst = tS0 + buf_s * 128, idS = idesc_bf16_f32(128, (ws & 15u) * kPage, false, false);
-                    const uint64_t dk = sdesc_sw128(sSlots + pk.slot * C::kSlotBytes, 16, C::kGroupStride);
-                    const uint64_t dq = sdesc_sw128(sQ + set * q_bytes + C::kSubs * c * q_sub, 16, 1024);
+                    const uint64_t dk = sdesc_sw128(sSlots + slot * C::kSlotBytes, 16, C::kGroupStride);
+                    const uint64_t dq = sdesc_sw128(sQ + C::kSubs * c * q_sub, 16, 1024);
 #pragma unroll
                     for (int i = 0; i < 4 * C::kSubs; ++i)
                         umma_bf16_ss(dst, sdesc_at(dq, (i >> 2) * q_sub + (i & 3) * 32), sdesc_at(dk, (i >> 2) * 1024 + (i & 3) * 32), idS,
                                      (c | i) ? 1u : 0u);
-                    if (last_use) {
-                        umma_commit(smem_u32(&empty[pk.slot]));
-                        pk.advance(C::kSets, stages);
-                    }
+                    umma_commit(smem_u32(&empty[slot]));
+                    advance();
                 }
-                umma_commit(smem_u32(&s_full[2 * set + buf_s]));
-                if (ws & kEnds) umma_commit(smem_u32(&q_free[set]));
+                umma_commit(smem_u32(&s_full[buf_s]));
+                if (ws & kEnds) umma_commit(smem_u32(&q_free[0]));
                 buf_s ^= 1u;
-                half_s = last_use ? 0u : 1u;
-                if (last_use && (ws & kLast)) more_s = false;
+                if (ws & kLast) more_s = false;
                 return true;
             };
             auto issue_pv = [&]() -> bool {
-                uint32_t set = 0u;
-                bool last_use = true;
 #pragma unroll 1
                 for (int c = 0; c < C::kVC; ++c) {
-                    if (half_p == 0u) {
-                        if (!wait(&full[vpos.slot], vpos.phase, 0x49)) return false;
-                        wp = words[vpos.slot];
-                        if (wp >> 4 & 15u) {
-                            if (!wait(&vfix[vpos.slot], fix_phase >> vpos.slot & 1u, 0x4f)) return false;
-                            fix_phase ^= 1u << vpos.slot;
-                        }
+                    if (!wait(&full[slot], phase, 0x49)) return false;
+                    wp = words[slot];
+                    if (wp >> 4 & 15u) {
+                        if (!wait(&vfix[slot], fix_phase >> slot & 1u, 0x4f)) return false;
+                        fix_phase ^= 1u << slot;
                     }
                     if (c == 0) {
-                        set = (wp & kDual) ? half_p : (wp & kSet1) ? 1u : 0u;
-                        last_use = !(wp & kDual) || half_p;
-                        if (wp & kBegins) {  // the set's piece before has been read out of O
-                            if ((o_used >> set & 1u) && !wait(&o_free[set], o_phase >> set & 1u, 0x48)) return false;
-                            if (o_used >> set & 1u) o_phase ^= 1u << set;
-                            o_used |= 1u << set;
+                        if (wp & kBegins) {  // the piece before has been read out of O
+                            if (o_used && !wait(&o_free[0], o_phase, 0x48)) return false;
+                            if (o_used) o_phase ^= 1u;
+                            o_used = true;
                         }
-                        const uint32_t i = 2u * set + buf_p;
-                        if (!wait(&p_full[i], p_phase >> i & 1u, 0x47)) return false;
-                        p_phase ^= 1u << i;
+                        if (!wait(&p_full[buf_p], p_phase >> buf_p & 1u, 0x47)) return false;
+                        p_phase ^= 1u << buf_p;
                     }
                     tc_fence_after();
-                    const uint64_t dv = sdesc_sw128(sSlots + vpos.slot * C::kSlotBytes, 1024, C::kGroupStride);
-                    const uint32_t tP = tS0 + buf_p * 128, tD = tO + set * C::kDV + c * C::kSlotCols;
+                    const uint64_t dv = sdesc_sw128(sSlots + slot * C::kSlotBytes, 1024, C::kGroupStride);
+                    const uint32_t tP = tS0 + buf_p * 128, tD = tO + c * C::kSlotCols;
                     const int np = wp & 15u;
                     // a page of 16 keys per MMA; keys 64 h .. of P at columns 64 h ..
                     umma_bf16_ts(tD, tP, dv, idO, (wp & kBegins) ? 0u : 1u);
@@ -868,15 +932,12 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                         for (int kk = 1; kk < np; ++kk)
                             umma_bf16_ts(tD, tP + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_at(dv, kk * C::kPageBytes), idO, 1u);
                     }
-                    if (last_use) {
-                        umma_commit(smem_u32(&empty[vpos.slot]));
-                        vpos.advance(C::kSets, stages);
-                    }
+                    umma_commit(smem_u32(&empty[slot]));
+                    advance();
                 }
-                umma_commit(smem_u32(&pv_done[2 * set + buf_p]));
+                umma_commit(smem_u32(&pv_done[buf_p]));
                 buf_p ^= 1u;
-                half_p = last_use ? 0u : 1u;
-                if (last_use && (wp & kLast)) more_p = false;
+                if (wp & kLast) more_p = false;
                 return true;
             };
             for (int step = 0; ok && more_p; ++step) {
@@ -963,12 +1024,12 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
     }
 }
 
-template <int D, bool WIDE>
+template <int D>
 cudaError_t launch_t(const TreeLaunch& L, TreeArgs a, cudaStream_t stream) {
     using C = TreeCfg<D>;
     const int fit = (int)((C::kPool - C::kSets * a.q_rows * D * 2) / C::kSlotBytes);
     a.stages = fit < C::kMaxStages ? fit : C::kMaxStages;
-    cudaError_t e = cudaFuncSetAttribute(tree_paged_kernel<D, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(tree_paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
     // at most one CTA per tile of the longest step that fits the arguments
     const int tokens = a.tokens_tile * C::kSets;
@@ -989,7 +1050,7 @@ cudaError_t launch_t(const TreeLaunch& L, TreeArgs a, cudaStream_t stream) {
     cfg.numAttrs = 1;
     static const char* const kNames[4] = {"tree_paged_d64", "tree_paged_d128", "tree_paged_d256", "tree_paged_d512"};
     ProfMark m = prof_begin(stream, kNames[D == 64 ? 0 : D == 128 ? 1 : D == 256 ? 2 : 3]);
-    e = cudaLaunchKernelEx(&cfg, tree_paged_kernel<D, WIDE>, L.tq, L.tk, L.tv, a);
+    e = cudaLaunchKernelEx(&cfg, tree_paged_kernel<D>, L.tq, L.tk, L.tv, a);
     prof_end(stream, m);
     if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
     const int merge_y = (a.rows_cap * (C::kDV / 8) + kMergeThreads - 1) / kMergeThreads;
@@ -1030,12 +1091,11 @@ cudaError_t launch_tree_paged(const TreeLaunch& L, cudaStream_t stream) {
     a.scale_log2 = L.scale * 1.4426950408889634f;
     a.q_tokens = tree_tokens_per_copy(a.G, L.max_q);
     a.q_rows = (a.G * a.q_tokens + 7) / 8 * 8;
-    const bool wide = L.max_q > a.tokens_tile;  // a request may have two row tiles
     switch (L.D) {
-        case 64: return wide ? launch_t<64, true>(L, a, stream) : launch_t<64, false>(L, a, stream);
-        case 128: return wide ? launch_t<128, true>(L, a, stream) : launch_t<128, false>(L, a, stream);
-        case 256: return launch_t<256, false>(L, a, stream);
-        case 512: return launch_t<512, false>(L, a, stream);
+        case 64: return launch_t<64>(L, a, stream);
+        case 128: return launch_t<128>(L, a, stream);
+        case 256: return launch_t<256>(L, a, stream);
+        case 512: return launch_t<512>(L, a, stream);
         default: return cudaErrorInvalidValue;
     }
 }
