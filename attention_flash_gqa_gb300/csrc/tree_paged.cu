@@ -12,12 +12,13 @@
 //  * A row tile packs the drafted tokens and the G query heads of one KV head into the 128 rows of
 //    an MMA (row = token * G + head, 128 / G tokens a tile), so a KV head's keys serve all of them.
 //  * At D <= 128 tensor memory holds two O accumulators, so a CTA has two sets of softmax warps, each
-//    with its own O, Q tile and running state. Where a request has more rows than one tile, two row
-//    tiles go through together, one per set, and share every key tile (12 requests of 5 to 24 thousand
-//    keys and 33 to 64 drafts, Hq 32, Hkv 8, D 128: 193 us, against 299 when each of the two row tiles
-//    read all of K and V for itself; 170 with the later steps). Otherwise consecutive segments alternate
-//    between the sets: one set's epilogue runs beside the other's first tiles. (Key tiles of one segment
-//    in turn to both sets, whose results the epilogue then adds: 45 us against 39 for a batch of 64.)
+//    with its own O, Q tile, running state, score buffers and MMA issuer. Where a request has more rows
+//    than one tile, two row tiles go through together, one per set, and share every key tile (12 requests
+//    of 5 to 24 thousand keys and 33 to 64 drafts, Hq 32, Hkv 8, D 128: 193 us, against 299 when each of
+//    the two row tiles read all of K and V for itself; 167 with the later steps). Otherwise consecutive
+//    segments alternate between the sets: one set's epilogue runs beside the other's first tiles. (Key
+//    tiles of one segment in turn to both sets, whose results the epilogue then adds: 45 us against 39
+//    for a batch of 64.)
 //  * At D = 512 a CTA computes one 256-column half of O; the two CTAs of a key range run side by side
 //    (CTAs 2 i and 2 i + 1), so the second copy of K, for the scores, comes from L2.
 //  * A unit of work is one key tile, up to eight pages (128 keys), of one segment = (request, KV head,
@@ -28,26 +29,30 @@
 //    one every CTA leaves (O, m, l) unnormalised in the workspace and tree_merge_kernel, launched with
 //    programmatic serialisation, combines them.
 //  * The tiles go through an mbarrier ring, and the pipeline runs on across segments. Tensor memory: O
-//    (fp32, up to 256 columns in all) and two score buffers of 128 columns, P (bf16) over the scores.
+//    (fp32, up to 256 columns in all) and 256 columns of scores, P (bf16) over them. One set: two buffers
+//    of a key tile each. Two sets: two buffers of half a key tile for each, so that a set's softmax of one
+//    half runs beside the MMAs of its other half (one buffer of a whole tile per set: 169 us for the 12 long
+//    contexts, 54 for 32 requests of 1 to 4 thousand keys at D = 64, against 167 and 51; with P in shared
+//    memory instead, which leaves three slots of the ring, 260 for the long ones).
 //    Only the pages of a tile that exist are loaded and multiplied (N of Q K^T and K of P V follow them,
 //    a page being one K step of 16), so only the last page's slots past L need care: a fixer warp zeroes
 //    those V rows before their P V (P is 0 there, but 0 * NaN is not).
 //
 // What bounds it, 152 SMs: at D = 256 the memory (64 requests of 1 to 4 thousand keys, window 1024:
 // 185 us, 6.0 TB/s of K and V). At D = 128 and up to 128 rows a request (64 requests of 256 to 1024 keys
-// and 5 to 16 drafts: 40 us, 4.3 TB/s) a key tile takes the softmax of its set 1.2 us, the loads 1.5 us
-// and the producer's copies 1.2 us, all overlapped; 3 us pass before the first load, 3 until it arrives
-// and 4 in the last tile, the epilogue and the merge. With two row tiles (170 us, 4.9 TB/s) each set has
-// one score buffer, so its softmax (0.95 us) and the MMAs between two of them (1 us) take turns.
+// and 5 to 16 drafts: 40 us, 4.3 TB/s) the memory too, once it runs (1.45 us a key tile and SM): 3 us pass
+// before the first load, 3 until it arrives, and 8 from the first CTA's end to the merge's. With two row
+// tiles (167 us, 5.0 TB/s; 180 once the clock has come down under load) the softmax: the two sets' warps
+// of a quarter share a scheduler, and half a tile takes both some 1700 cycles, of which 530 are the
+// exponential unit's. At D = 64 (51 us, 3.3 TB/s) the softmax of one set, some 1000 cycles for half a tile.
 //
 // Warp roles: four softmax warps a set (0-3, and 4-7 at two sets), one TMEM lane quarter each and one
-// thread a row, so nothing of a row is exchanged; then an idle warp, the fixer, the TMA producer (lanes
-// 0-7: a page each) and the MMA issuer. The last two sit on the schedulers of quarters 2 and 3, which
-// have no rows where a tile has 64 or fewer. Quarters without rows only keep the barriers going. The
-// issuer is one thread that reads what to do from a word the producer leaves with every copy: walking
-// the work itself took it longer than the MMAs (per 128-key tile 1.4 us, of which 0.56 us of MMAs). The
-// idle warp as a second producer, for V alone, gained 1 % at two row tiles and cost 4 % of the batch of
-// 64, whose busy quarter it shares a scheduler with.
+// thread a row, so nothing of a row is exchanged; then set 0's MMA issuer (idle at one set), the fixer, the
+// TMA producer (lanes 0-7: a page each) and the other MMA issuer. The last two sit on the schedulers of
+// quarters 2 and 3, which have no rows where a tile has 64 or fewer. Quarters without rows only keep the
+// barriers going. An issuer is one thread that reads what to do from a word the producer leaves with every
+// copy: walking the work itself took it longer than the MMAs (per 128-key tile 1.4 us, of which 0.56 us of
+// MMAs). One issuer for both sets' half tiles took 2.9 us a tile (244 us for the 12 long contexts).
 #include <cuda_runtime.h>
 
 #include "attn_internal.h"
@@ -70,7 +75,7 @@ struct TreeCfg {
     static constexpr int kDV = D < 256 ? D : 256;      // O columns per segment
     static constexpr int kSplit = D / kDV;
     static constexpr int kSets = tree_sets(D);
-    // (at one set kIssuer0 is idle, so that the others keep their schedulers)
+    // kIssuer0 is set 0's at two sets, and idle at one
     static constexpr int kIssuer0 = kSets * kSetWarps, kFixer = kIssuer0 + 1, kProducer = kFixer + 1, kIssuer = kProducer + 1;
     static constexpr int kWarps = kIssuer + 1;
     static constexpr int kThreads = kWarps * 32;
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
     if (tid == 0) a.span[k].ctas = 0;  // until the share's last piece says otherwise
     // The ring's slots go round in the order of the copies. One set: K and V slots in the issuer's order, K(0)
     // K(1) V(0) K(2) V(1) .. (a K tile of D = 512 is longer than the ring). Two sets: K(0) V(0) K(1) V(1) ..,
-    // since two row tiles return to a key tile's slots: tile i's K is copy 2 i, its V copy 2 i + 1.
+    // each issuer following all of them: tile i's K is copy 2 i, its V copy 2 i + 1.
 
     if (!works) {
         // no units left for this CTA
