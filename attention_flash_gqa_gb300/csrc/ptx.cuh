@@ -246,6 +246,9 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(r));
     return r != 0;
 }
+// Waits until the kernels in front of a launch with programmatic serialisation have finished and their writes
+// are visible (returns at once in any other launch).
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Named barrier over `n` threads (a multiple of 32).
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t n) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");

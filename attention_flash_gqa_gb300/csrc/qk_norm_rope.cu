@@ -116,6 +116,7 @@ __device__ __forceinline__ void load_angles(const NormRopeLaunch& a, int pos, in
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeLaunch a) {
     constexpr int LPR = D / 16, RPW = 32 / LPR, RPT = RPW * kUF;
+    griddep_wait();
     const int lane = threadIdx.x & 31, j = lane % LPR, sub = lane / LPR;
     const int nblk = (a.Hq + RPT - 1) / RPT + (PAGED ? 2 : 1) * ((a.Hkv + RPT - 1) / RPT);
     const int warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -218,6 +219,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
     const int rc = a.rot / 16;
     const bool rotated = j < rc;
     const int c0 = rotated && !a.interleaved ? j : 2 * j, c1 = rotated && !a.interleaved ? j + rc : 2 * j + 1;
+    griddep_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // norm_rope_dw_kernel waits for this grid
     const uint16_t* src = (b.kind == 0 ? a.q : a.k) + (size_t)b.head0 * D;
     const uint16_t* gsrc = (b.kind == 0 ? a.dq_out : a.dk_out) + (size_t)b.head0 * D;
@@ -332,7 +334,7 @@ constexpr int kDwWarps = 16;
 __global__ void __launch_bounds__(kDwWarps * 32) norm_rope_dw_kernel(const float* part, float* dqw, float* dkw, int D, int n) {
     __shared__ float acc[kDwWarps][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the gradient kernel runs
+    griddep_wait();  // launched while the gradient kernel runs
     float x = 0.f;
     for (int i = w; i < n; i += kDwWarps) x += part[(size_t)i * 2 * D + col];
     acc[w][lane] = x;
@@ -359,14 +361,31 @@ int norm_grid(long long T, int nblk, int sms, int per_sm) {
 
 constexpr int kFwdPerSm = 4, kBwdPerSm = 3;
 
+// A launch with programmatic serialisation: its CTAs may start while the kernel in front ends, and wait for it
+// (griddep_wait) before they read or write anything.
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), int grid, int threads, int smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 template <int D, bool PAGED>
 cudaError_t launch_fwd_d(const NormRopeLaunch& L, cudaStream_t stream) {
     constexpr int RPT = 512 / D * kUF;
     const int nblk = (L.Hq + RPT - 1) / RPT + (PAGED ? 2 : 1) * ((L.Hkv + RPT - 1) / RPT);
     const ProfMark m = prof_begin(stream, PAGED ? "qk_norm_rope_paged" : "qk_norm_rope");
-    norm_rope_kernel<D, PAGED><<<norm_grid(L.T, nblk, L.sms, kFwdPerSm), kThreads, 0, stream>>>(L);
+    const cudaError_t e = launch_early(norm_rope_kernel<D, PAGED>, norm_grid(L.T, nblk, L.sms, kFwdPerSm), kThreads, 0, stream, L);
     prof_end(stream, m);
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int D>
@@ -377,21 +396,11 @@ cudaError_t launch_bwd_d(const NormRopeLaunch& L, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(norm_rope_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
     if (e != cudaSuccess) return e;
     ProfMark m = prof_begin(stream, "qk_norm_rope_bwd");
-    norm_rope_bwd_kernel<D><<<grid, kThreads, kBwdSmem, stream>>>(L);
+    e = launch_early(norm_rope_bwd_kernel<D>, grid, kThreads, kBwdSmem, stream, L);
     prof_end(stream, m);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
     m = prof_begin(stream, "qk_norm_rope_dw");
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(2 * D / 32);
-    cfg.blockDim = dim3(kDwWarps * 32);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, (const float*)L.part, L.dq_weight, L.dk_weight, D, grid);
+    e = launch_early(norm_rope_dw_kernel, 2 * D / 32, kDwWarps * 32, 0, stream, (const float*)L.part, L.dq_weight, L.dk_weight, D, grid);
     prof_end(stream, m);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

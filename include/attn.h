@@ -277,6 +277,9 @@ ATTN_API int attn_merge_lse(const attn_bf16* o_parts, const float* lse_parts, at
  *   (an update in place); no other overlap of inputs and outputs is allowed.
  *   Supported: page_size = 16, num_reqs <= 16384, num_pages <= 2^26. total_new, num_free and
  *   num_reqs may be zero (pointers to nothing may be NULL). All pointers 4-byte aligned.
+ *   Launched with programmatic stream serialisation, like the head-norm calls below: the kernel may be
+ *   placed on the GPU while the one in front ends, and waits there for all earlier work of the stream
+ *   before it reads or writes anything. It does not let the kernel behind it start before its own end.
  */
 ATTN_API int attn_paged_plan(const int32_t* kv_lens, const int32_t* new_lens, const int32_t* pages_held,
                              const int32_t* free_pages, const int32_t* free_used, int32_t* block_table,
