@@ -195,3 +195,51 @@ def test_training_step(D, rot, window):
         check(name, to_np(got.reshape(T, -1)), want.numpy())
     check("dqw", to_np(dqw), w64[0].grad.numpy())
     check("dkw", to_np(dkw), w64[1].grad.numpy())
+
+
+def test_fork_and_join_in_a_graph():
+    """Plan on one captured stream, a head norm on another, joined before the cache write, the trees and a decode step."""
+    R, Hq, Hkv, D, rot, pages = 5, 8, 2, 128, 64, 60
+    s = Cache(R, Hkv, D, pages, 10, 3)
+    g = torch.Generator().manual_seed(11)
+    s.kc.normal_(), s.vc.normal_()
+    n = [4, 1, 7, 2, 3]
+    T = sum(n)
+    s.held += 2
+    s.table[:, :2] = torch.arange(2 * R, dtype=torch.int32, device="cuda").view(R, 2)
+    s.free = torch.arange(2 * R, pages, dtype=torch.int32, device="cuda")
+    ctx, new = i32([20, 3, 31, 0, 17]), i32(n)
+    q, k, v = (torch.randn(T, h, D, generator=g).bfloat16().cuda() for h in (Hq, Hkv, Hkv))
+    cs = ref.table(100, rot).cuda()
+    words = [ref.random_tree(x, 1, g)[0] for x in n]
+    mask = torch.tensor([m for w in words for m in w], dtype=torch.int32).reshape(T, 1).cuda()
+    table = s.table.clone()
+
+    def run(side=None):
+        main = torch.cuda.current_stream()
+        if side is not None:
+            side.wait_stream(main)
+        p = attn.attn_paged_plan(ctx, new, s.free, table, s.held, s.used, T, num_pages=pages)
+        with torch.cuda.stream(side if side is not None else main):
+            extra = attn.attn_qk_norm_rope(q, k, None, None, torch.arange(T, dtype=torch.int32, device="cuda"), cs, eps=EPS)
+        if side is not None:
+            main.wait_stream(side)
+        qo = attn.attn_qk_norm_rope_paged(q, k, v, None, None, p.positions, p.slots, cs, s.kc, s.vc, eps=EPS)
+        o, lse = attn.attn_tree_paged(qo, s.kc, s.vc, table, p.seq_lens, p.cu_q, mask, max(n), scale=0.1)
+        do, dl = attn.attn_decode_paged(qo[:R].contiguous(), s.kc, s.vc, table, p.seq_lens, scale=0.1)
+        return [*p, *extra, qo, o, lse, do, dl]
+
+    want = run()
+    torch.cuda.synchronize()
+    keep = s.kc.clone(), s.vc.clone()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        got = run(side)
+    for _ in range(3):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(s.kc, keep[0]) and torch.equal(s.vc, keep[1])
+    assert attn.attn_get_device_status() == 0
