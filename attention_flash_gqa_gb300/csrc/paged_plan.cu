@@ -12,11 +12,12 @@
 // There is next to nothing to move (24 bytes a request, 8 a token, 8 a page taken), so the call is bound
 // by latency: one launch, and no value passes from one CTA to another. Every CTA scans all requests
 // itself into shared memory (R <= 16384: two prefix sums of 64 KB) and then fills its share of the rows
-// and pages. Where there are more rows than threads, a thread takes four consecutive ones: it finds the
-// request of the first by bisection of the prefix sums, steps on from there, reads a page id once for
-// rows of one page, and stores 16 bytes at a time where the outputs are aligned (1000 requests, 500
-// thousand rows: 7.5 us against 9.5 a row at a time). Otherwise it takes one (64 requests of one row each:
-// 3.3 us against 5.0 by fours, whose rows read the state of four requests one after the other). A new
+// and pages. Where there are more rows than threads, a thread takes four consecutive ones, or eight if there
+// are more than four a thread: it finds the request of the first by bisection of the prefix sums, steps on
+// from there, reads a page id once for rows of one page, and stores 16 bytes at a time where the outputs are
+// aligned (1000 requests, 500 thousand rows: 7.2 us by eights, 7.6 by fours, 9.5 a row at a time). Otherwise
+// it takes one (64 requests of one row each: 3.3 us against 5.0 by fours, whose rows read the state of four
+// requests one after the other). A new
 // page's id is read from the free list, not from the table, so no row waits for another thread's table
 // entry.
 //
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         a.table[(size_t)b * a.max_pages + a.held[b] + (i - off[b])] = checked(a.free_pages[used + i]);
     }
     // rows
-    const bool wide = PER == 4 && ((reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.slots)) & 15u) == 0;
+    const bool wide = PER >= 4 && ((reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.slots)) & 15u) == 0;
     const int groups = a.T / PER + (a.T % PER != 0);
     for (int g = gtid; g < groups; g += gsize) {
         const int t0 = PER * g;
@@ -152,8 +153,11 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
             }
         }
         if (wide && t0 + PER <= a.T) {
-            *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[PER > 1], pos[PER / 2], pos[PER - 1]);
-            *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[PER > 1], slot[PER / 2], slot[PER - 1]);
+#pragma unroll
+            for (int i = 0; i + 3 < PER; i += 4) {
+                *reinterpret_cast<int4*>(a.positions + t0 + i) = make_int4(pos[i], pos[i + 1], pos[i + 2], pos[i + 3]);
+                *reinterpret_cast<int4*>(a.slots + t0 + i) = make_int4(slot[i], slot[i + 1], slot[i + 2], slot[i + 3]);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
@@ -213,9 +217,10 @@ cudaError_t launch_t(const PlanLaunch& L, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_paged_plan(const PlanLaunch& L, cudaStream_t stream) {
-    const bool fours = L.T > (L.in_place ? kCluster : L.sms) * kThreads;
-    if (L.in_place) return fours ? launch_t<true, 4>(L, stream) : launch_t<true, 1>(L, stream);
-    return fours ? launch_t<false, 4>(L, stream) : launch_t<false, 1>(L, stream);
+    const int threads = (L.in_place ? kCluster : L.sms) * kThreads;
+    if (L.T / 4 > threads) return L.in_place ? launch_t<true, 8>(L, stream) : launch_t<false, 8>(L, stream);
+    if (L.T > threads) return L.in_place ? launch_t<true, 4>(L, stream) : launch_t<false, 4>(L, stream);
+    return L.in_place ? launch_t<true, 1>(L, stream) : launch_t<false, 1>(L, stream);
 }
 
 }  // namespace attn

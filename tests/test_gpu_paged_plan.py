@@ -74,6 +74,14 @@ def test_plan(R, lo, hi, new_lo, new_hi, in_place):
         compare(problem(R, lo, hi, new_lo, new_hi, 100 * R + seed, pad=seed * 5), in_place)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan_many_rows(in_place):
+    """More rows than four for each thread of the GPU, ending inside a thread's run."""
+    p = problem(300, 0, 100, 500, 2700, 21, pad=3)
+    assert p["T"] > 400000
+    compare(p, in_place)
+
+
 def test_plan_largest_batch():
     """16384 requests, two of them with everything: the prefix sums fill 128 KB of shared memory."""
     p = problem(16384, 0, 20, 0, 2, 5)
