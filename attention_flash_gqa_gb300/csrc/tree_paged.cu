@@ -66,6 +66,7 @@ constexpr int kTilePages = 8;
 constexpr int kSetWarps = 4;
 constexpr uint32_t kSubBytes = 16384;  // 128 rows x 64 bf16
 constexpr float kRescaleLog2 = 8.0f;
+constexpr int kFewUnits = 1 << 14;  // beyond that many units equal shares are long enough
 constexpr int kMaxGrid = 192;  // sizes the workspace
 
 __host__ __device__ constexpr int tree_sets(int D) { return D <= 128 ? 2 : 1; }
@@ -121,6 +122,7 @@ struct TreeArgs {
     float* part;      // [2 * grid][rows_cap][kRowF]
     TreeSpan* span;   // [grid]
     int R, T, max_q, words, Hq, Hkv, G, tokens_tile, rows_cap, max_pages, num_pages, window;
+    int part_cost, min_share;      // see launch_t
     int q_tokens, q_rows, stages;  // tokens of a copy of Q, rows of a Q tile in shared memory, slots of the ring
     float scale_log2;
 };
@@ -230,6 +232,9 @@ struct Walk {
 
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
+// ceil(x / y) for 1 <= y, 0 <= x < 2^22: the margin of half a unit in the numerator outweighs the roundings.
+__device__ __forceinline__ int ceil_div(int x, int y) { return __float2int_rd(__fdividef((float)(x + y) - 0.5f, (float)y)); }
+
 // P units over G CTAs: the first P % G of them take one more than the others.
 __device__ __forceinline__ int share_start(int k, int q, int rem) { return k * q + min(k, rem); }
 __device__ __forceinline__ int owner_of(int u, int q, int rem) {
@@ -311,6 +316,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
     // ---- the CTA's share -----------------------------------------------------------------------
     long long P = 0;  // units of the step
     int q = 0, rem = 0, u0 = 0, share = 0, first_b = 0, first_off = 0;
+    int chunks = 0;  // shares that a segment is cut into, if each lies in one segment
     Req first_req = {};
     // (a step of 2^31 tiles or more, far beyond what a cache can hold, is reported and left alone)
     auto shares = [&]() -> bool {  // whether the CTA has one
@@ -339,11 +345,50 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             if (lane >= d) x += y;
         }
         P = __shfl_sync(0xffffffffu, x, 31);
-        works = shares();
-        const unsigned at = __ballot_sync(0xffffffffu, works && x - n <= u0 && u0 < x);
+        // Shares that lie in one segment each, where those are not much longer than equal shares of the whole: a CTA
+        // then leaves one partial result instead of two (3 requests, window 1024, up to 37 drafts, 30 heads over 5, D
+        // 256: 22.0 us against 28.3; 4 requests of 700 to 2162 keys, 33 to 41 drafts, 12 heads over 3, D 128: 19.0
+        // against 24.5; the search costs calls that do not end up so 0.1 to 0.4 us).
+        const int G = gridDim.x / C::kSplit;
+        unsigned at = 0u;
+        bool aligned = false;
+        if (__builtin_expect((P > G || a.min_share > 1) && P < kFewUnits, 0)) {
+            const int segs = r.groups * a.Hkv;
+            int most = max(ceil_div((int)P, G), a.min_share), c, total;  // tiles of a share, shares of a segment, of all
+            const int end = max(most, (4 * (int)P + G * a.part_cost / 2) / (4 * G));
+            do {
+                c = ceil_div(r.tiles, most);
+                total = (int)__reduce_add_sync(0xffffffffu, (unsigned)(segs * c));
+            } while (total > G && ++most <= end);
+            if (total <= G) {
+                aligned = true;
+                works = part < total;
+                int y = segs * c;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int z = __shfl_up_sync(0xffffffffu, y, d);
+                    if (lane >= d) y += z;
+                }
+                const int off = part - (y - segs * c);
+                at = __ballot_sync(0xffffffffu, off >= 0 && part < y);
+                if (off >= 0 && part < y) {
+                    const int each = ceil_div(r.tiles, c), seg_ = ceil_div(off + 1, c) - 1, chunk = off - seg_ * c;
+                    first_off = seg_ * r.tiles + chunk * each;
+                    share = min(each, r.tiles - chunk * each);
+                    chunks = c;
+                }
+            }
+        }
+        if (!aligned) {
+            works = shares();
+            at = __ballot_sync(0xffffffffu, works && x - n <= u0 && u0 < x);
+            first_off = u0 - (int)(x - n);
+        }
         if (at) {
             first_b = __ffs(at) - 1;
-            first_off = __shfl_sync(0xffffffffu, u0 - (int)(x - n), first_b);
+            first_off = __shfl_sync(0xffffffffu, first_off, first_b);
+            share = __shfl_sync(0xffffffffu, share, first_b);
+            chunks = __shfl_sync(0xffffffffu, chunks, first_b);
             first_req.start = __shfl_sync(0xffffffffu, r.start, first_b);
             first_req.n = __shfl_sync(0xffffffffu, r.n, first_b);
             first_req.L = __shfl_sync(0xffffffffu, r.L, first_b);
@@ -639,8 +684,9 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
             if (quad == 0 && lane == 0 && w.left == 1 && (!w.dual || set == 0)) {
                 TreeSpan sp = {};
                 if (pg_begin == 0 && w.pg + w.np < w.r.npg) {
-                    // the segment's last unit
-                    sp.ctas = owner_of(u0 + share - 1 + (w.r.npg - (w.pg + w.np) + kTilePages - 1) / kTilePages, q, rem) - part + 1;
+                    // (else the CTA that holds the segment's last unit)
+                    sp.ctas = chunks > 0 ? chunks
+                                         : owner_of(u0 + share - 1 + (w.r.npg - (w.pg + w.np) + kTilePages - 1) / kTilePages, q, rem) - part + 1;
                     sp.row0 = w.r.start + w.tok0, sp.head0 = w.head * a.G, sp.col0 = split * C::kDV;
                     sp.rows[0] = rows;
                     sp.rows[1] = w.dual ? min(a.tokens_tile, w.r.n - w.tok0 - a.tokens_tile) * a.G : 0;
@@ -1037,6 +1083,10 @@ cudaError_t launch_t(const TreeLaunch& L, TreeArgs a, cudaStream_t stream) {
     a.stages = fit < C::kMaxStages ? fit : C::kMaxStages;
     cudaError_t e = cudaFuncSetAttribute(tree_paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
+    // Bytes that a piece's partial result costs, written and read, in quarters of a key tile's; shares shorter than
+    // that cost more than they gain.
+    a.part_cost = a.rows_cap * C::kDV / (8 * (D + C::kDV));
+    a.min_share = a.part_cost < 6 ? 1 : (a.part_cost + 2) / 4;
     // at most one CTA per tile of the longest step that fits the arguments
     const int tokens = a.tokens_tile * C::kSets;
     const long long groups = (L.max_q + tokens - 1) / tokens;

@@ -263,6 +263,14 @@ def test_numbers_of_requests(D, R):
     assert (o.cpu()[~good] == 7.0).all() and (lse.cpu()[:, ~good] == 7.0).all()
 
 
+@pytest.mark.parametrize("D,Hkv,G,n,window", [(256, 5, 6, [37, 5, 20], 1024), (256, 1, 4, [58, 3, 30], 0), (128, 3, 4, [41, 33, 37], 0),
+                                               (512, 4, 4, [4, 6, 1], 0), (64, 11, 2, [28, 12, 3], 0), (128, 4, 1, [6, 6, 6], 0)])
+def test_shares_within_segments(D, Hkv, G, n, window):
+    """Few units: every CTA's share lies in one segment, and segments of different lengths are cut evenly."""
+    for seed, ctx in enumerate(([1500, 300, 2300], [129, 127, 120], [640, 0, 9])):
+        compare(problem(ctx, n, Hkv * G, Hkv, D, seed=seed), window)
+
+
 def test_bad_page_ids_are_reported():
     """A page id outside the pool stands for page 0; other requests are not touched."""
     p = problem([40, 30], [3, 5], 4, 2, 128, poison=False)
