@@ -453,6 +453,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
         const uint32_t tOset = tO + set * C::kDV + lane_base;
         float m_ref = -INFINITY, l = 0.f;
         int first_key = 0, token = 0, pg_begin = 0, rows = 0, ctx = 0;
+        uint64_t bits0 = 0;
         int step = 0;                       // tile of the share
         uint32_t phases = 0u;               // of the set's two buffers
         int prev = 0;                       // the set's step before: buffer, and its phase
@@ -470,6 +471,9 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                 m_ref = -INFINITY, l = 0.f;
                 pg_begin = w.pg;
                 token = w.r.start + min(tok + row / a.G, w.r.n - 1);
+                // the row's first 64 mask bits, on their way while the scores are made
+                const int32_t* mw = a.mask + (size_t)token * a.words;
+                bits0 = (uint64_t)(uint32_t)mw[0] | (a.words > 1 ? (uint64_t)(uint32_t)mw[1] << 32 : 0ull);
                 first_key = a.window > 0 ? max(0, min(ctx, max(a.positions[token], ctx) - a.window + 1)) : 0;
             }
             const int steps = kHalf && w.np > kTilePages / 2 ? 2 : 1;
@@ -488,11 +492,17 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                         uint64_t vis = low_bits(w.np * kPage - 64 * half) & ~low_bits(first_key - k0);
                         const int dc = ctx - k0;  // column of the first drafted token
                         if (dc < 64) {
-                            const int d0 = max(0, -dc), wi = d0 >> 5, sh = d0 & 31;
-                            const int32_t* mw = a.mask + (size_t)token * a.words;
-                            auto word = [&](int i) -> uint64_t { return i < a.words ? (uint64_t)(uint32_t)mw[i] : 0ull; };
-                            uint64_t bits = (word(wi) | word(wi + 1) << 32) >> sh;
-                            if (sh) bits |= word(wi + 2) << (64 - sh);
+                            const int d0 = max(0, -dc);
+                            uint64_t bits;
+                            if (d0 == 0 || a.words <= 2) {
+                                bits = d0 < 64 ? bits0 >> d0 : 0ull;
+                            } else {
+                                const int wi = d0 >> 5, sh = d0 & 31;
+                                const int32_t* mw = a.mask + (size_t)token * a.words;
+                                auto word = [&](int i) -> uint64_t { return i < a.words ? (uint64_t)(uint32_t)mw[i] : 0ull; };
+                                bits = (word(wi) | word(wi + 1) << 32) >> sh;
+                                if (sh) bits |= word(wi + 2) << (64 - sh);
+                            }
                             bits &= low_bits(w.r.n - d0);
                             vis &= low_bits(dc) | bits << max(dc, 0);
                         }
