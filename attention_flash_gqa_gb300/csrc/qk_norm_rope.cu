@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUF = 4;  // passes per task, forward
+constexpr int kUF = 4;  // passes per task, forward (1 where heads are few: see launch_fwd_d)
 constexpr int kUB = 4;  // passes per task, gradient
 constexpr int kMaxCtas = 1024;  // sizes the gradient's workspace
 
@@ -118,9 +118,9 @@ __device__ __forceinline__ void load_angles(const NormRopeLaunch& a, int pos, in
     }
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, int U>
 __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ NormRopeLaunch a) {
-    constexpr int LPR = D / 16, RPW = 32 / LPR, RPT = RPW * kUF;
+    constexpr int LPR = D / 16, RPW = 32 / LPR, RPT = RPW * U;
     griddep_wait();
     const int lane = threadIdx.x & 31, j = lane % LPR, sub = lane / LPR;
     const int nblk = (a.Hq + RPT - 1) / RPT + (PAGED ? 2 : 1) * ((a.Hkv + RPT - 1) / RPT);
@@ -148,9 +148,9 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
             }
             if (b.kind) orow = slot;
         }
-        uint4 raw[kUF][2];
+        uint4 raw[U][2];
 #pragma unroll
-        for (int u = 0; u < kUF; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int h = b.head0 + u * RPW + sub;
             if (h < b.heads) {
                 const uint16_t* row = src + (size_t)t * stride + (size_t)h * D;
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
             if (rotated && b.kind < 2) load_angles(a, pos, j, c, s);
         }
 #pragma unroll
-        for (int u = 0; u < kUF; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int h = b.head0 + u * RPW + sub;
             if (b.kind < 2) {
                 float x[16];
@@ -359,12 +359,12 @@ int norm_grid(long long T, int nblk, int sms, int per_sm) {
     const long long want = (T * nblk + kWarps - 1) / kWarps, least = (nblk + kWarps - 1) / kWarps;
     long long g = (long long)sms * per_sm;
     if (want < g) g = want;
-    if (g > kMaxCtas) g = kMaxCtas;
     if (g < least) g = least;  // at most 2048 heads of each kind: 4096 / kWarps
     return (int)g;
 }
 
-constexpr int kFwdPerSm = 4, kBwdPerSm = 3;
+constexpr int kFwdPerSm = 4, kFewPerSm = 12, kBwdPerSm = 3;
+constexpr int kMaxSms = kMaxCtas / kBwdPerSm;  // more of them are not used by the gradient
 
 // A launch with programmatic serialisation: its CTAs may start while the kernel in front ends, and wait for it
 // (griddep_wait) before they read or write anything.
@@ -383,21 +383,37 @@ cudaError_t launch_early(void (*kernel)(Params...), int grid, int threads, int s
     return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
 }
 
-template <int D, bool PAGED>
-cudaError_t launch_fwd_d(const NormRopeLaunch& L, cudaStream_t stream) {
-    constexpr int RPT = 512 / D * kUF;
+template <int D, bool PAGED, int U>
+cudaError_t launch_fwd_u(const NormRopeLaunch& L, int per_sm, cudaStream_t stream) {
+    constexpr int RPT = 512 / D * U;
     const int nblk = (L.Hq + RPT - 1) / RPT + (PAGED ? 2 : 1) * ((L.Hkv + RPT - 1) / RPT);
     const ProfMark m = prof_begin(stream, PAGED ? "qk_norm_rope_paged" : "qk_norm_rope");
-    const cudaError_t e = launch_early(norm_rope_kernel<D, PAGED>, norm_grid(L.T, nblk, L.sms, kFwdPerSm), kThreads, 0, stream, L);
+    const cudaError_t e = launch_early(norm_rope_kernel<D, PAGED, U>, norm_grid(L.T, nblk, L.sms, per_sm), kThreads, 0, stream, L);
     prof_end(stream, m);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// A task has four passes and an SM four CTAs, whose loads are all in flight; but where the heads leave most of a
+// task's rows empty, tasks of one pass, and twelve CTAs an SM, have more of them on their way (17030 tokens, 3 + 3
+// heads of 64: 11.6 us against 28.3; 36190 tokens, 8 + 2 + 2 heads of 128 into the cache: 57 against 98; 333 tokens, 12
+// + 3 heads of 64: 2.6 against 3.3). Where more than half of the rows are there it is the other way round (11076
+// tokens, 10 + 5 + 5 heads of 256: 60 against 53; 16384 tokens, 32 + 16 heads of 256: 158 against 125), and where the
+// tasks of four passes come to about one a warp (921 tokens, 15 + 15 + 15 heads of 64: 6.0 against 5.2).
+template <int D, bool PAGED>
+cudaError_t launch_fwd_d(const NormRopeLaunch& L, cudaStream_t stream) {
+    constexpr int RPW = 512 / D, RPT = RPW * kUF, kinds = PAGED ? 2 : 1;
+    const int nblk = (L.Hq + RPT - 1) / RPT + kinds * ((L.Hkv + RPT - 1) / RPT);
+    const long long tasks = (long long)L.T * nblk, warps = (long long)L.sms * kFwdPerSm * kWarps;
+    if (L.Hq + kinds * L.Hkv <= nblk * RPT / 2 && (tasks <= warps / 2 || tasks > 2 * warps))
+        return launch_fwd_u<D, PAGED, 1>(L, kFewPerSm, stream);
+    return launch_fwd_u<D, PAGED, kUF>(L, kFwdPerSm, stream);
 }
 
 template <int D>
 cudaError_t launch_bwd_d(const NormRopeLaunch& L, cudaStream_t stream) {
     constexpr int RPT = 512 / D * kUB;
     const int nblk = (L.Hq + RPT - 1) / RPT + (L.Hkv + RPT - 1) / RPT;
-    const int grid = norm_grid(L.T, nblk, L.sms, kBwdPerSm);
+    const int grid = norm_grid(L.T, nblk, L.sms < kMaxSms ? L.sms : kMaxSms, kBwdPerSm);
     cudaError_t e = cudaFuncSetAttribute(norm_rope_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
     if (e != cudaSuccess) return e;
     ProfMark m = prof_begin(stream, "qk_norm_rope_bwd");
