@@ -201,20 +201,23 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
 // The gradient. The rows of a task come into shared memory by bulk copies, 4 KB of x and 4 KB of dy, into a
 // ring of kRing stages that each warp has for itself: its lane 0 refills a stage as soon as the warp has
 // read it, so 12 warps an SM keep up to 192 KB on their way (with loads into registers, 163 of them and
-// 48 KB on their way, 18001 tokens of 36 heads of 512 took 487 us, 4.1 TB/s). Each CTA leaves its sums of
-// dn xh in part[CTA][query | key][D], in an order of its own that depends on the launch alone;
-// norm_rope_dw_kernel adds them up.
+// 48 KB on their way, 18001 tokens of 36 heads of 512 took 487 us, 4.1 TB/s; now 294 us, 6.8 TB/s). At D = 512
+// tasks of fewer rows get more, smaller stages (5664 tokens, 5 + 5 heads: 38.5 us against 39.6, and the loop with
+// a variable depth is compiled to 167 registers instead of 128: 294 us against 312 for the 36 heads); at D <= 256
+// deeper rings cost up to 8 %. Each CTA leaves its sums of dn xh in part[CTA][query | key][D], in an order of its
+// own that depends on the launch alone; norm_rope_dw_kernel adds them up.
 constexpr int kRing = 2;
 constexpr int kStageBytes = 8192;
-constexpr int kBwdSmem = kWarps * kRing * kStageBytes + 256;
+constexpr int kMaxRing = 8;  // D = 512
+constexpr int kBwdSmem = kWarps * kRing * kStageBytes + kWarps * kMaxRing * 8 + 64;
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_constant__ NormRopeLaunch a) {
     constexpr int LPR = D / 16, RPW = 32 / LPR, RPT = RPW * kUB;
     static_assert(RPT * D * 4 == kStageBytes, "a stage holds a task's x and dy");
     extern __shared__ __align__(128) uint8_t ring[];
-    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kWarps * kRing * kStageBytes);  // [kWarps][kRing]
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kWarps * kRing);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kWarps * kRing * kStageBytes);  // [kWarps][kMaxRing]
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kWarps * kMaxRing);
     const int lane = threadIdx.x & 31, j = lane % LPR, sub = lane / LPR, wid = threadIdx.x >> 5;
     const int nblk = (a.Hq + RPT - 1) / RPT + (a.Hkv + RPT - 1) / RPT;
     const int warp = blockIdx.x * kWarps + wid;
@@ -233,22 +236,23 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
     uint16_t* dst = (b.kind == 0 ? a.dq : a.dk) + (size_t)b.head0 * D;
     const int rows = b.rows;
     uint8_t* mine = ring + wid * kRing * kStageBytes;
-    uint64_t* full = bars + wid * kRing;
+    uint64_t* full = bars + wid * kMaxRing;
+    const uint32_t bytes = rows * D * 2;  // of x, and of dy; a stage holds both
+    const int depth = D == 512 ? min(kMaxRing, (int)(kRing * kStageBytes / (2 * bytes))) : kRing;
     if (threadIdx.x == 0) *abort_flag = 0;
     if (lane == 0)
-        for (int s = 0; s < kRing; ++s) mbar_init(smem_u32(&full[s]), 1);
+        for (int s = 0; s < kMaxRing; ++s) mbar_init(smem_u32(&full[s]), 1);
     fence_mbar_init();
     __syncthreads();
     auto fetch = [&](int t, int s) {  // lane 0
-        const uint32_t bar = smem_u32(&full[s]), at = smem_u32(mine + s * kStageBytes);
-        const uint32_t bytes = rows * D * 2;
+        const uint32_t bar = smem_u32(&full[s]), at = smem_u32(mine + s * 2 * bytes);
         mbar_expect_tx(bar, 2 * bytes);
         bulk_load(at, src + (size_t)t * stride, bytes, bar);
-        bulk_load(at + kStageBytes / 2, gsrc + (size_t)t * b.heads * D, bytes, bar);
+        bulk_load(at + bytes, gsrc + (size_t)t * b.heads * D, bytes, bar);
     };
     const int t0 = warp / nblk;
     if (works && lane == 0)
-        for (int s = 0; s < kRing; ++s)
+        for (int s = 0; s < depth; ++s)
             if (t0 + (long long)s * lanes < a.T) fetch(t0 + s * lanes, s);
     float v[16], dw[16];
     load_weights(a, b.kind == 0 ? a.q_weight : a.k_weight, c0, c1, v);
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
             while (globaltimer() - since < 100000ull) __nanosleep(1000);
             break;
         }
-        const uint8_t* xs = mine + stage * kStageBytes;
+        const uint8_t* xs = mine + stage * 2 * bytes;
 #pragma unroll
         for (int u = 0; u < kUB; ++u) {
             const int r = u * RPW + sub;
@@ -285,8 +289,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
             const uint8_t* xrow = xs + r * D * 2;
             unpack8(*reinterpret_cast<const uint4*>(xrow + 16 * c0), x, 0);
             unpack8(*reinterpret_cast<const uint4*>(xrow + 16 * c1), x, 8);
-            unpack8(*reinterpret_cast<const uint4*>(xrow + kStageBytes / 2 + 16 * c0), g, 0);
-            unpack8(*reinterpret_cast<const uint4*>(xrow + kStageBytes / 2 + 16 * c1), g, 8);
+            unpack8(*reinterpret_cast<const uint4*>(xrow + bytes + 16 * c0), g, 0);
+            unpack8(*reinterpret_cast<const uint4*>(xrow + bytes + 16 * c1), g, 8);
             if (rotated) turn(g, c, s, a.interleaved);  // dn
             float ss = 0.f, sg = 0.f;
 #pragma unroll
@@ -308,8 +312,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
             *reinterpret_cast<uint4*>(row + 8 * c1) = pack8(x, 8);
         }
         __syncwarp();  // the stage has been read
-        if (lane == 0 && t + (long long)kRing * lanes < a.T) fetch(t + kRing * lanes, stage);
-        if (++stage == kRing) stage = 0, phase ^= 1;
+        if (lane == 0 && t + (long long)depth * lanes < a.T) fetch(t + depth * lanes, stage);
+        if (++stage == depth) stage = 0, phase ^= 1;
     }
     // the warp's row groups, then the CTA's warps, in order
     __shared__ float sums[kWarps][D];
