@@ -357,6 +357,109 @@ __global__ void __launch_bounds__(kDwWarps * 32) norm_rope_dw_kernel(const float
     }
 }
 
+// The paged form of long calls, with its rows in rings like the gradient's: 4 KB a stage, two stages a warp, five
+// CTAs an SM (8468 tokens, 10 + 2 + 2 heads of 512: 42.2 us against 53.9 with loads into registers; 12590 tokens,
+// 30 + 15 + 15 of 64: 35.4 against 43.7; 4096 tokens, 32 + 4 + 4 of 512: 56.2 against 57.7). The form that is not
+// paged keeps the registers: 16384 tokens, 32 + 16 heads of 256, 124.8 us against 138 to 142 with rings.
+constexpr int kFwdRing = 2;
+constexpr int kFwdStage = 4096;
+constexpr int kFwdSmem = kWarps * kFwdRing * kFwdStage + kWarps * kFwdRing * 8 + 64;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) norm_rope_ring_kernel(const __grid_constant__ NormRopeLaunch a) {
+    constexpr int LPR = D / 16, RPW = 32 / LPR, RPT = RPW * kUF;
+    static_assert(RPT * D * 2 == kFwdStage, "a stage holds a task's rows");
+    extern __shared__ __align__(128) uint8_t ring[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kWarps * kFwdRing * kFwdStage);  // [kWarps][kFwdRing]
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kWarps * kFwdRing);
+    griddep_wait();
+    const int lane = threadIdx.x & 31, j = lane % LPR, sub = lane / LPR, wid = threadIdx.x >> 5;
+    const int nblk = (a.Hq + RPT - 1) / RPT + 2 * ((a.Hkv + RPT - 1) / RPT);
+    const int warp = blockIdx.x * kWarps + wid;
+    const int lanes = gridDim.x * kWarps / nblk;
+    const bool works = warp < lanes * nblk;
+    const Block b = block_of<RPT, true>(warp % nblk, a.Hq, a.Hkv);
+    const int rc = a.rot / 16;
+    const bool rotated = j < rc;
+    const int c0 = rotated && !a.interleaved ? j : 2 * j, c1 = rotated && !a.interleaved ? j + rc : 2 * j + 1;
+    const uint16_t* src = (b.kind == 0 ? a.q : b.kind == 1 ? a.k : a.v) + (size_t)b.head0 * D;
+    const long long stride = b.kind == 0 ? a.q_stride : b.kind == 1 ? a.k_stride : a.v_stride;
+    uint16_t* dst = (b.kind == 0 ? a.q_out : b.kind == 1 ? a.k_out : a.v_out) + (size_t)b.head0 * D;
+    uint8_t* mine = ring + wid * kFwdRing * kFwdStage;
+    uint64_t* full = bars + wid * kFwdRing;
+    const uint32_t bytes = b.rows * D * 2;
+    if (threadIdx.x == 0) *abort_flag = 0;
+    if (lane == 0)
+        for (int s = 0; s < kFwdRing; ++s) mbar_init(smem_u32(&full[s]), 1);
+    fence_mbar_init();
+    __syncthreads();
+    if (!works) return;
+    auto fetch = [&](int t, int s) {  // lane 0
+        const uint32_t bar = smem_u32(&full[s]);
+        mbar_expect_tx(bar, bytes);
+        bulk_load(smem_u32(mine + s * kFwdStage), src + (size_t)t * stride, bytes, bar);
+    };
+    const int t0 = warp / nblk;
+    if (lane == 0)
+        for (int s = 0; s < kFwdRing; ++s)
+            if (t0 + (long long)s * lanes < a.T) fetch(t0 + s * lanes, s);
+    float v[16];
+    if (b.kind < 2) load_weights(a, b.kind == 0 ? a.q_weight : a.k_weight, c0, c1, v);
+    int stage = 0, phase = 0;
+    for (int t = t0; t < a.T; t += lanes) {
+        const int slot = a.slots[t];
+        const size_t orow = b.kind ? slot : t;  // output row: the token, or its cache slot
+        bool skip = slot == -1;                 // a padding row
+        bool bad = !skip && (slot < 0 || slot >= a.num_slots);
+        float c[8], s[8];
+        if (a.rot > 0) {
+            const int pos = a.positions[t];
+            if (!skip) bad |= pos < 0 || pos >= a.max_pos;
+            if (!skip && !bad && rotated && b.kind < 2) load_angles(a, pos, j, c, s);
+        }
+        if (bad) {
+            skip = true;
+            if (lane == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, abort_flag, a.status, 0x52))) {
+            // given up: copies into the ring may still be landing, the CTA must outlast them
+            const uint64_t since = globaltimer();
+            while (globaltimer() - since < 100000ull) __nanosleep(1000);
+            break;
+        }
+        const uint8_t* xs = mine + stage * kFwdStage;
+#pragma unroll
+        for (int u = 0; u < kUF; ++u) {
+            const int r = u * RPW + sub;
+            if (skip || r >= b.rows) continue;  // a row's lanes agree
+            uint4 lo = *reinterpret_cast<const uint4*>(xs + r * D * 2 + 16 * c0), hi = *reinterpret_cast<const uint4*>(xs + r * D * 2 + 16 * c1);
+            if (b.kind < 2) {
+                float x[16];
+                unpack8(lo, x, 0);
+                unpack8(hi, x, 8);
+                float ss = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+                const float rr = rsqrtf(row_sum<LPR>(ss, row_peers<LPR>(sub)) * (1.f / D) + a.eps);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = x[e] * rr * v[e];
+                if (rotated) turn(x, c, s, a.interleaved);
+                lo = pack8(x, 0);
+                hi = pack8(x, 8);
+            }
+            uint16_t* row = dst + (orow * b.heads + r) * D;
+            *reinterpret_cast<uint4*>(row + 8 * c0) = lo;
+            *reinterpret_cast<uint4*>(row + 8 * c1) = hi;
+        }
+        __syncwarp();  // the stage has been read
+        if (lane == 0 && t + (long long)kFwdRing * lanes < a.T) fetch(t + kFwdRing * lanes, stage);
+        if (++stage == kFwdRing) stage = 0, phase ^= 1;
+    }
+    // A decode call behind this kernel starts as its last CTAs leave, and copies pages before it waits for
+    // this grid's end: the rows are visible by then.
+    __threadfence();
+}
+
 // CTAs for `tasks` warp tasks: enough for all of them at once, at most `per_sm` per SM, and at least one
 // warp for each block of a token.
 int norm_grid(long long T, int nblk, int sms, int per_sm) {
@@ -367,6 +470,7 @@ int norm_grid(long long T, int nblk, int sms, int per_sm) {
     return (int)g;
 }
 
+constexpr int kRingPerSm = 5;
 constexpr int kFwdPerSm = 4, kFewPerSm = 12, kBwdPerSm = 3;
 constexpr int kMaxSms = kMaxCtas / kBwdPerSm;  // more of them are not used by the gradient
 
@@ -410,6 +514,16 @@ cudaError_t launch_fwd_d(const NormRopeLaunch& L, cudaStream_t stream) {
     const long long tasks = (long long)L.T * nblk, warps = (long long)L.sms * kFwdPerSm * kWarps;
     if (L.Hq + kinds * L.Hkv <= nblk * RPT / 2 && (tasks <= warps / 2 || tasks > 2 * warps))
         return launch_fwd_u<D, PAGED, 1>(L, kFewPerSm, stream);
+    if constexpr (PAGED) {
+        if (tasks > 3 * warps) {  // (418 tokens, 96 + 16 + 16 heads of 256, 2.8 tasks a warp: 14.3 us in rings, 13.0 not)
+            cudaError_t e = cudaFuncSetAttribute(norm_rope_ring_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFwdSmem);
+            if (e != cudaSuccess) return e;
+            const ProfMark m = prof_begin(stream, "qk_norm_rope_paged");
+            e = launch_early(norm_rope_ring_kernel<D>, norm_grid(L.T, nblk, L.sms, kRingPerSm), kThreads, kFwdSmem, stream, L);
+            prof_end(stream, m);
+            return e != cudaSuccess ? e : cudaGetLastError();
+        }
+    }
     return launch_fwd_u<D, PAGED, kUF>(L, kFwdPerSm, stream);
 }
 

@@ -342,8 +342,8 @@ ATTN_API int attn_qk_norm_rope_bwd(const attn_bf16* dq_out, const attn_bf16* dk_
  * (as it is) go straight into the paged caches, each token at its slot.
  *   v [T, Hkv, D] bf16, tokens v_stride elements apart. slots int32 [T], of attn_paged_plan: slot s is
  *   token s % 16 of page s / 16. k_cache, v_cache [num_pages, page_size, Hkv, D] bf16, updated in
- *   place. A token with slot -1 is padding: nothing of it is read or written, q_out included. Any
- *   other slot outside the cache, or a position outside the table, is reported as
+ *   place. A token with slot -1 is padding: its values are not used and nothing of it is written,
+ *   q_out included. Any other slot outside the cache, or a position outside the table, is reported as
  *   ATTN_ERR_DEVICE_BOUNDS and the token's rows are left as they were. Slots of different tokens
  *   must differ (of two tokens with one slot, either one's values may end up in each part of it).
  *   page_size = 16, num_pages <= 2^26; everything else as in attn_qk_norm_rope.

@@ -130,6 +130,38 @@ def test_paged(T, Hq, Hkv, D, rot, inter, fused, w32, off):
     assert torch.equal(caches[1].view(-1, Hkv, D).double().cpu(), want)
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,inter,fused,w32,off", [(2500, 5, 5, 512, 128, False, True, False, 0.0),
+                                                                (2503, 12, 4, 256, 256, False, False, True, 1.0),
+                                                                (2600, 30, 15, 64, 32, True, True, False, 0.0),
+                                                                (2500, 14, 14, 128, 0, False, True, False, 0.0)])
+def test_paged_long(T, Hq, Hkv, D, rot, inter, fused, w32, off):
+    """Several tasks for each warp of the GPU: the rows come through rings."""
+    test_paged(T, Hq, Hkv, D, rot, inter, fused, w32, off)
+
+
+def test_paged_long_in_place_with_bad_tokens():
+    T, Hq, Hkv, D = 3000, 20, 5, 128
+    p, d = problem(T, Hq, Hkv, D, 64)
+    slots, pos = torch.arange(T, dtype=torch.int32), p["pos"].clone()
+    slots[1000], slots[1001], slots[5] = -7, T + 40, -1
+    pos[2000], pos[7] = 500, -1
+    dead = torch.zeros(T, dtype=torch.bool)
+    dead[[1000, 1001, 5, 2000, 7]] = True
+    caches = [torch.full((-(-T // 16), 16, Hkv, D), 2.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    q = d["q"]
+    out = attn.attn_qk_norm_rope_paged(q, d["k"], d["v"], d["qw"], d["kw"], pos.cuda(), slots.cuda(), d["cs"], *caches, q, eps=EPS)
+    assert out is q and attn.attn_get_device_status() == 7
+    y, tol = ref.norm_rope(p["q"], p["qw"], angles(p), EPS, 0.0, False)
+    y[dead], tol[dead] = p["q"].double()[dead], 0.0
+    ref.close("q", q, y, tol)
+    y, tol = ref.norm_rope(p["k"], p["kw"], angles(p), EPS, 0.0, False)
+    y[dead], tol[dead] = 2.0, 0.0
+    ref.close("k cache", caches[0].view(-1, Hkv, D)[:T], y, tol)
+    want = p["v"].clone()
+    want[dead] = 2.0
+    assert torch.equal(caches[1].view(-1, Hkv, D)[:T].cpu(), want)
+
+
 def test_no_weights_batch_layout_and_in_place():
     p, d = problem(60, 4, 2, 128, 64)
     want = attn.attn_qk_norm_rope(d["q"], d["k"], None, None, d["pos"], d["cs"])
