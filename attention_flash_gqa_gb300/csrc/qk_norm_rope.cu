@@ -17,7 +17,8 @@
 // time and the only exchange is the butterfly sum of a row's lanes. A task is one token's block of
 // kU such passes, all queries or all keys; a warp keeps its block and walks the tokens, so the norm
 // weights (and, in the gradient, their sums) stay in registers and a token's angles are loaded once
-// for kU passes. All loads of a task are issued before the first is used (the gradient: see there).
+// for kU passes. All loads of a task are issued before the first is used; in the gradient, and in long calls
+// of the paged form, they come through rings in shared memory (see there).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
