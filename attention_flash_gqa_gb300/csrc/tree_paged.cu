@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                 const bool from = pg_begin == 0, to = w.pg + w.np == w.r.npg;
                 const bool row_ok = row < rows;
                 const int head = w.head * a.G + row % a.G, col0 = split * C::kDV;
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = l == 0.f ? 0.f : 1.f / l;  // (l of a row with NaN scores is NaN, and so are o and lse)
                 uint16_t* orow = a.o + ((size_t)token * a.Hq + head) * D + col0;
                 float* prow = a.part + ((size_t)(2 * k + (from ? 1 : 0)) * a.rows_cap + (w.dual && set ? 128 : 0) + row) * C::kRowF;
 #pragma unroll 1
@@ -682,9 +682,11 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                     }
                 }
                 if (row_ok) {
-                    if (!(from && to)) prow[C::kDV] = m_ref, prow[C::kDV + 1] = l;
+                    // NaN scores move no maximum: a partial with some has m = inf, so that the merge, which passes over
+                    // those with m = -inf, makes the row NaN whatever its other partials hold
+                    if (!(from && to)) prow[C::kDV] = l == l ? m_ref : INFINITY, prow[C::kDV + 1] = l;
                     else if (col0 == 0)
-                        a.lse[(size_t)head * a.T + token] = l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+                        a.lse[(size_t)head * a.T + token] = l == 0.f ? -INFINITY : (m_ref + __log2f(l)) * 0.69314718055994531f;
                 }
             }
             tc_fence_before();
@@ -1075,14 +1077,14 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
             }
             M = Mn;
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         const int token = sp.row0 + second * a.tokens_tile + tile_row / a.G, head = sp.head0 + tile_row % a.G;
         uint4 x;
         x.x = pack_bf16x2(O[0] * inv, O[1] * inv), x.y = pack_bf16x2(O[2] * inv, O[3] * inv);
         x.z = pack_bf16x2(O[4] * inv, O[5] * inv), x.w = pack_bf16x2(O[6] * inv, O[7] * inv);
         *reinterpret_cast<uint4*>(a.o + ((size_t)token * a.Hq + head) * D + sp.col0 + col) = x;
         if (col == 0 && sp.col0 == 0)
-            a.lse[(size_t)head * a.T + token] = l > 0.f ? (M + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+            a.lse[(size_t)head * a.T + token] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.69314718055994531f;
     }
 }
 

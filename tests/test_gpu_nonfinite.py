@@ -1,0 +1,100 @@
+"""Non-finite inputs in places that count: a row whose scores hold a NaN comes out as NaN, whichever of its keys
+are NaN and however they are split over the GPU, and no other row is touched."""
+import math
+
+import pytest
+import torch
+
+import attention_flash_gqa_gb300 as attn
+import operator_ref as ref
+from test_gpu_tree_paged import i32, problem, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from attention_flash_gqa_gb300 import _build
+
+    _build.build()
+    attn.load_library()
+    torch.cuda.set_device(0)
+    attn.attn_get_device_status()
+
+
+def definition(p, window=0, **other):
+    p = dict(p, **other)
+    return ref.tree(p["q"], p["kc"], p["vc"], p["table"], p["lens"], p["cu"], p["mask"], p["scale"], window, p["pos"])
+
+
+def rows_but(nan, got, want, tol, what):
+    """NaN where `nan` [T, Hq] says so, within the tolerance elsewhere."""
+    assert torch.isnan(got.cpu()[nan]).all(), what
+    ref.close(what, got.cpu()[~nan], want[~nan], tol[~nan])
+
+
+# one key tile (a single CTA writes the row), many tiles (partial results are merged), a batch of both
+CONTEXTS = [([40], [5]), ([9000], [5]), ([0, 700, 30, 2500], [3, 9, 1, 33])]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+@pytest.mark.parametrize("ctx,n", CONTEXTS)
+def test_tree_query_rows(D, ctx, n):
+    p = problem(ctx, n, 4, 2, D, seed=51)
+    T = sum(n)
+    nan = torch.zeros(T, 4, dtype=torch.bool)
+    nan[0, 1] = nan[T - 1, 3] = nan[T // 2, 0] = True
+    q = p["q"].clone()
+    q[nan] = math.nan
+    q[0, 1] = p["q"][0, 1]
+    q[0, 1, 7] = math.nan  # one value is enough
+    ro, to, rl, tl = definition(p)
+    o, lse = run(dict(p, q=q))
+    assert attn.attn_get_device_status() == 0
+    rows_but(nan, o, ro, to, "o")
+    rows_but(nan, lse.t(), rl.t(), tl.t(), "lse")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+@pytest.mark.parametrize("window", [0, 4000])
+@pytest.mark.parametrize("first,count", [(0, 2000), (5500, 1), (5100, 300), (8990, 10)])
+def test_tree_visible_keys(D, window, first, count):
+    """K of one head is NaN for a stretch of the context (as long as several CTAs' shares, or a single key):
+    every row of that head's group is NaN, unless the window hides all of the stretch."""
+    p = problem([9000], [6], 4, 2, D, seed=52)
+    ro, to, rl, tl = definition(p, window)
+    kc = p["kc"].clone()
+    for j in range(first, first + count):
+        kc[p["table"][0, j // 16], j % 16, 1] = math.nan
+    o, lse = run(dict(p, kc=kc), window)
+    assert attn.attn_get_device_status() == 0
+    nan = torch.zeros(6, 4, dtype=torch.bool)
+    start = (torch.maximum(p["pos"], torch.tensor(9000)) - window + 1) if window else torch.zeros(6)
+    nan[:, 2:] = (start < first + count)[:, None]
+    rows_but(nan, o, ro, to, "o")
+    rows_but(nan, lse.t(), rl.t(), tl.t(), "lse")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+@pytest.mark.parametrize("ctx", [20, 3000])
+def test_tree_infinite_scores(D, ctx):
+    """A score of +inf leaves no finite result, one of -inf counts as a key with probability zero."""
+    p = problem([ctx], [8], 4, 2, D, seed=53)
+    p["mask"][:] = -1  # every row sees every drafted token
+    j = ctx + 5
+    kc = p["kc"].clone()
+    kc[p["table"][0, j // 16], j % 16, 0, 3] = math.inf
+    up = torch.zeros(8, 4, dtype=torch.bool)
+    up[:, :2] = p["q"][:, :2, 3] > 0
+    assert up.any() and not up[:, :2].all() and (p["q"][:, :, 3] != 0).all()
+    mask = p["mask"].clone()
+    mask &= ~(1 << 5)
+    ro, to, rl, tl = definition(p, mask=mask)  # heads 0 and 1: without the key
+    so, st, sl, sm = definition(p)
+    ro[:, 2:], to[:, 2:], rl[2:], tl[2:] = so[:, 2:], st[:, 2:], sl[2:], sm[2:]
+    o, lse = run(dict(p, kc=kc))
+    assert attn.attn_get_device_status() == 0
+    o, lse = o.cpu(), lse.t().cpu()
+    assert not torch.isfinite(o[up]).any() and not torch.isfinite(lse[up]).any() and (lse[up] != -math.inf).all()
+    ref.close("o", o[~up], ro[~up], to[~up])
+    ref.close("lse", lse[~up], rl.t()[~up], tl.t()[~up])
