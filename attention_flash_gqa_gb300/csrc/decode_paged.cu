@@ -630,7 +630,9 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
         ok = __shfl_sync(0xffffffffu, rel_ok, 0) && ok;
 
         // ---- end of this request inside this CTA: write its partials (o, m, l) -----------
-        // The merge kernel that follows this grid combines each request's slots.
+        // The merge kernel that follows this grid combines each request's slots. NaN scores move no maximum:
+        // a slot with some carries m = inf, so that the merge, which passes over those with m = -inf, makes the
+        // row NaN whatever its other slots hold.
         if (u + 1 == start[b + 1] || u + 1 == u1) {
             // slot of (request b, CTA k, token half): (b + k) * 2 + half
             float* slot = a.part + ((size_t)(b + k) * 2 + half) * a.Hq * kRowF;
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
                     for (int n8 = 0; n8 < 16; ++n8)
                         *reinterpret_cast<float2*>(row + 8 * n8 + 2 * mc) = make_float2(oa[n8][0], oa[n8][1]);
                     if (mc == 0) {
-                        row[D] = m_run;
+                        row[D] = l_run == l_run ? m_run : INFINITY;
                         row[D + 1] = l_run;
                     }
                 }
@@ -660,7 +662,7 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
                         *reinterpret_cast<float4*>(row + dim0 + e) =
                             make_float4(acc_o[hh][e], acc_o[hh][e + 1], acc_o[hh][e + 2], acc_o[hh][e + 3]);
                     if (lane == hh) {
-                        row[D] = m_run;
+                        row[D] = l_run == l_run ? m_run : INFINITY;
                         row[D + 1] = l_run;
                     }
                 }
@@ -794,12 +796,12 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(MergeArgs m
             }
             M = Mc;
         }
-        const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+        const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // NaN where a score is
         uint4 w0;
         w0.x = pack_bf16x2(O[0] * inv, O[1] * inv), w0.y = pack_bf16x2(O[2] * inv, O[3] * inv);
         w0.z = pack_bf16x2(O[4] * inv, O[5] * inv), w0.w = pack_bf16x2(O[6] * inv, O[7] * inv);
         *reinterpret_cast<uint4*>(m.o + ((size_t)b * m.Hq + h) * D + d0) = w0;
-        if (d0 == 0) m.lse[(size_t)b * m.Hq + h] = Ls > 0.f ? (M + __log2f(Ls)) * 0.69314718055994531f : -INFINITY;
+        if (d0 == 0) m.lse[(size_t)b * m.Hq + h] = Ls == 0.f ? -INFINITY : (M + __log2f(Ls)) * 0.69314718055994531f;
     }
 }
 

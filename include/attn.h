@@ -174,7 +174,7 @@ ATTN_API int attn_bwd(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v
  *   window: 0 = the query sees all L cached keys; W > 0 = only keys max(0, L-W) .. L-1 (pages
  *   wholly before the window are not read); W < 0 is rejected.
  *   o [B, Hq, D] bf16 out, lse [B, Hq] fp32 out.
- *   A request with L = 0 gets o = 0 and lse = -inf. Page ids outside [0, num_pages) or
+ *   A request with L = 0 gets o = 0 and lse = -inf; a row with a NaN score gets NaN for both. Page ids outside [0, num_pages) or
  *   lengths beyond max_pages_per_seq * page_size are not read: the affected tokens are
  *   skipped and ATTN_ERR_DEVICE_BOUNDS is recorded for attn_get_device_status().
  *   Supported: D = 128 with Hq / Hkv in {1, 2, 4, 8}, D = 256 with Hq / Hkv in {1, 2, 4};

@@ -98,3 +98,34 @@ def test_tree_infinite_scores(D, ctx):
     assert not torch.isfinite(o[up]).any() and not torch.isfinite(lse[up]).any() and (lse[up] != -math.inf).all()
     ref.close("o", o[~up], ro[~up], to[~up])
     ref.close("lse", lse[~up], rl.t()[~up], tl.t()[~up])
+
+
+@pytest.mark.parametrize("window", [0, 4000])
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 2, 128), (4, 2, 128), (8, 2, 128), (32, 8, 128), (16, 2, 128), (2, 2, 256), (8, 4, 256), (16, 4, 256)])
+def test_decode(Hq, Hkv, D, window):
+    """A decode step is a tree of one token: NaN query rows, and NaN keys of one head in some of a request's pages."""
+    G = Hq // Hkv
+    p = problem([8999, 4, 699], [1, 1, 1], Hq, Hkv, D, seed=54)
+    ro, to, rl, tl = definition(p, window)
+
+    def check(nan, **other):
+        d = dict(p, **other)
+        o, lse = attn.attn_decode_paged(d["q"].cuda(), d["kc"].cuda(), d["vc"].cuda(), d["table"].cuda(), i32(d["lens"]),
+                                        scale=d["scale"], window=window)
+        assert attn.attn_get_device_status() == 0
+        rows_but(nan, o, ro, to, "o")
+        rows_but(nan, lse, rl.t(), tl.t(), "lse")
+
+    nan = torch.zeros(3, Hq, dtype=torch.bool)
+    check(nan)
+    q = p["q"].clone()
+    nan[0, 1] = nan[1, 0] = nan[2, Hq - 1] = True
+    q[nan] = math.nan
+    check(nan, q=q)
+    for first, count in ((0, 2000), (5500, 1), (8000, 999)):
+        kc = p["kc"].clone()
+        for j in range(first, first + count):
+            kc[p["table"][0, j // 16], j % 16, 1] = math.nan
+        nan = torch.zeros(3, Hq, dtype=torch.bool)
+        nan[0, G: 2 * G] = not window or first + count > 5000
+        check(nan, kc=kc)
