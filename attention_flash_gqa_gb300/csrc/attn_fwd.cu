@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int qrow = q0 + r;  // query row index within the sequence's rows
             const bool row_ok = qrow < nq;
             const bool packed = PAGED || a.cu_seqlens;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // (l is NaN where a score is)
             uint16_t* orow = a.o + ((size_t)(packed ? seq_start + qrow : seq * a.S + qrow) * a.Hq + h) * a.D + dv0;
 #pragma unroll 1
             for (int c = hf * (C::kDV / 64); c < (hf + 1) * (C::kDV / 64); ++c) {
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (row_ok && split == 0 && hf == 0) {
-                const float lse = l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+                const float lse = l == 0.f ? -INFINITY : (m_ref + __log2f(l)) * 0.69314718055994531f;
                 const size_t li = packed ? (size_t)h * a.T + seq_start + qrow : ((size_t)seq * a.Hq + h) * a.S + qrow;
                 a.lse[li] = lse;
             }

@@ -85,7 +85,7 @@ enum {
  *   q   [B, S, Hq,  D] bf16      k, v [B, S, Hkv, D] bf16      (BSHD, contiguous)
  *   o   [B, S, Hq,  D] bf16 out  lse  [B, Hq, S] fp32 out, natural log
  *   scale: finite and > 0 (typically 1/sqrt(D)); causal must be 1; window <= 0 means no
- *   window, otherwise query i sees keys i-window+1 .. i.
+ *   window, otherwise query i sees keys i-window+1 .. i. A row with a NaN score gets NaN for o and lse.
  *   workspace: may be NULL (the forward needs none; attn_workspace_size returns 0).
  * Defined by the Gemma4 FFPA page, "Integration" (dense no-mask path) and the
  * sliding-window layers of the issue-3232 page.

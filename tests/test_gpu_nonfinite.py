@@ -129,3 +129,42 @@ def test_decode(Hq, Hkv, D, window):
         nan = torch.zeros(3, Hq, dtype=torch.bool)
         nan[0, G: 2 * G] = not window or first + count > 5000
         check(nan, kc=kc)
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 4, 2), (128, 4, 2), (256, 4, 2), (512, 4, 2), (512, 3, 3)])
+@pytest.mark.parametrize("window", [0, 300])
+def test_forward(D, Hq, Hkv, window):
+    """The same of the causal forward, dense and over a paged cache: NaN query rows, a NaN key."""
+    n, j = 700, 150
+    p = problem([0], [n], Hq, Hkv, D, seed=55)
+    g = torch.Generator().manual_seed(56)
+    q, kc = p["q"].clone(), p["kc"].clone()
+    q[300, 1, 5] = q[699, 0, 0] = math.nan
+    kc[p["table"][0, j // 16], j % 16, Hkv - 1] = math.nan
+    k, v = (c[p["table"][0, : -(-n // 16)].long()].flatten(0, 1)[:n][None].cuda() for c in (kc, p["vc"]))
+    i = torch.arange(n)
+    nan = torch.zeros(n, Hq, dtype=torch.bool)
+    nan[300, 1] = nan[699, 0] = True
+    nan[:, Hq - Hq // Hkv:] |= ((i >= j) & (i - j < window if window else i >= 0))[:, None]
+    for o, lse in (attn.attn_fwd(q[None].cuda(), k.contiguous(), v.contiguous(), window=window, scale=p["scale"]),
+                   attn.attn_fwd_paged(q.cuda(), kc.cuda(), p["vc"].cuda(), p["table"].cuda(), i32([n]), i32([0, n]), n, window=window,
+                                       scale=p["scale"])):
+        assert attn.attn_get_device_status() == 0
+        o, lse = o.view(n, Hq, D).cpu(), lse.view(Hq, n).t().cpu()
+        for x in (o, lse):
+            assert torch.isnan(x[nan]).all() and torch.isfinite(x[~nan]).all()
+        rows = i[torch.randperm(n, generator=g)[:20]]
+        for r in rows.tolist():  # the others are the definition's
+            lo = max(0, r - window + 1) if window else 0
+            for h in range(Hq):
+                if nan[r, h]:
+                    continue
+                kk, vv = (c[0, lo: r + 1, h // (Hq // Hkv)].double().cpu() for c in (k, v))
+                s = kk @ q[r, h].double() * p["scale"]
+                a = kk.abs() @ q[r, h].double().abs() * p["scale"]
+                x = torch.logsumexp(s, 0)
+                w = (s - x).exp()
+                e = ((2 * D + 8) * ref.U * a + 4 * ref.U * s.abs() + 2.0 ** -21).amax()  # as in operator_ref.tree
+                tol = (ref.BF + 2 * e + len(s) * ref.U) * (w @ vv.abs()) + ref.BF * (w @ vv).abs()
+                ref.close("o", o[r, h], w @ vv, tol)
+                ref.close("lse", lse[r, h][None], x[None], (e + len(s) * ref.U + 2.0 ** -21 * (1 + x.abs()))[None])
