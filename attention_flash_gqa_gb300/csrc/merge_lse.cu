@@ -9,7 +9,7 @@
 //     lse = ln sum_p exp(lse_p),   o = sum_p exp(lse_p - lse) o_p
 // evaluated with the largest lse_p factored out. A part with lse_p = -inf had no allowed key
 // and contributes nothing (its o_p is never multiplied in, even if it holds NaN). A row where
-// every part is empty gets o = 0 and lse = -inf.
+// every part is empty gets o = 0 and lse = -inf; one with a NaN lse_p (a NaN score) gets NaN for both.
 //
 // Memory bound: every byte of every part is read once. D/8 threads share a row, each owning one
 // 16-byte vector (8 dims) of it, so a 256-thread block covers 256 / (D/8) rows per pass. Rows
@@ -82,16 +82,17 @@ __global__ void __launch_bounds__(kThreads) merge_lse_kernel(MergeArgs a) {
                               : make_uint4(0u, 0u, 0u, 0u);
                 }
                 float cm = m;
+                bool any = false;
 #pragma unroll
-                for (int u = 0; u < kChunk; ++u) cm = fmaxf(cm, x[u]);
-                if (cm == -INFINITY) continue;  // no key in any part so far
+                for (int u = 0; u < kChunk; ++u) cm = fmaxf(cm, x[u]), any |= x[u] != -INFINITY;
+                if (!any) continue;  // no key in these parts
                 const float rescale = m == -INFINITY ? 0.f : expf(m - cm);
                 sum *= rescale;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] *= rescale;
 #pragma unroll
                 for (int u = 0; u < kChunk; ++u) {
-                    if (x[u] > -INFINITY) {  // an empty part's o is never multiplied in
+                    if (x[u] != -INFINITY) {  // an empty part's o is never multiplied in; a NaN lse makes the row NaN
                         const float wt = expf(x[u] - cm);
                         sum += wt;
                         const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
@@ -105,8 +106,8 @@ __global__ void __launch_bounds__(kThreads) merge_lse_kernel(MergeArgs a) {
                 m = cm;
             }
         }
-        const float L = m == -INFINITY ? -INFINITY : m + logf(sum);
-        const float inv = m == -INFINITY ? 0.f : 1.f / sum;
+        const float L = sum == 0.f ? -INFINITY : m + logf(sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         // Every read of this pass precedes its writes, so o / lse may be part 0's own buffers
         // (an in-place running merge): each o vector is read and written by one thread, and a
         // row's lse parts are read by all of its threads before one of them writes lse.

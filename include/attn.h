@@ -238,7 +238,8 @@ ATTN_API size_t attn_decode_paged_noalloc_max_bytes(void);
  * sum of exp(scale * q.k) over them), as every forward of this library returns them. Per row:
  *   lse = ln sum_p exp(lse_p),   o = sum_p exp(lse_p - lse) * o_p   (fp32, o rounded to bf16)
  * A part with lse_p = -inf (no allowed key) contributes nothing, whatever its o_p holds; a row
- * with no key in any part gets o = 0, lse = -inf. lse values must be finite or -inf.
+ * with no key in any part gets o = 0, lse = -inf. One with a NaN lse_p in any part (a NaN score there) gets
+ * NaN for both. lse values must not be +inf.
  *   o_parts [num_parts, B, S, H, D] bf16 and lse_parts [num_parts, B, H, S] fp32: the parts
  *   stacked in the forward's layouts (packed [T, H, D] / [H, T] results: B = 1, S = T).
  *   o [B, S, H, D] bf16 out, lse [B, H, S] fp32 out. The outputs may be part 0's own buffers

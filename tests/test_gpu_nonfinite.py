@@ -168,3 +168,29 @@ def test_forward(D, Hq, Hkv, window):
                 tol = (ref.BF + 2 * e + len(s) * ref.U) * (w @ vv.abs()) + ref.BF * (w @ vv).abs()
                 ref.close("o", o[r, h], w @ vv, tol)
                 ref.close("lse", lse[r, h][None], x[None], (e + len(s) * ref.U + 2.0 ** -21 * (1 + x.abs()))[None])
+
+
+@pytest.mark.parametrize("P", [1, 2, 3, 8])
+@pytest.mark.parametrize("D", [64, 512])
+def test_merge(P, D):
+    """A part whose lse is NaN makes the row NaN, beside finite parts and beside empty ones; empty parts still hide theirs."""
+    S, H = 40, 3
+    g = torch.Generator().manual_seed(57 + P)
+    op, lp = torch.randn(P, 1, S, H, D, generator=g).bfloat16(), torch.randn(P, 1, H, S, generator=g)
+    lp[:, 0, 1, 5:9] = -math.inf  # no key in any part
+    if P > 1:
+        lp[P - 1, 0, :, 20:24] = -math.inf
+        op[P - 1, 0, 20:24] = math.nan  # of an empty part: not looked at
+    w = lp.double().softmax(0).nan_to_num(0.0).transpose(2, 3)[..., None]
+    want = (w * op.double().nan_to_num(0.0)).sum(0)
+    # fp32 over P parts: P + 8 roundings and the exponentials' (2 ulp, arguments up to 8), then bf16
+    tol = ref.BF * want.abs() + (P + 32) * ref.U * (w * op.double().nan_to_num(0.0).abs()).sum(0)
+    x = lp.double().logsumexp(0)
+    nan = torch.zeros(1, S, H, dtype=torch.bool)
+    for p, s, h in ((0, 3, 0), (P - 1, 9, 2), (P // 2, 6, 1), (0, 21, 1)):  # (6, 1): every other part is empty
+        lp[p, 0, h, s] = math.nan
+        nan[0, s, h] = True
+    o, lse = attn.attn_merge_lse(op.cuda(), lp.cuda())
+    assert attn.attn_get_device_status() == 0
+    rows_but(nan, o, want, tol, "o")
+    rows_but(nan, lse.transpose(1, 2), x.transpose(1, 2), torch.full((1, S, H), (P + 32) * ref.U * 8, dtype=torch.float64), "lse")
