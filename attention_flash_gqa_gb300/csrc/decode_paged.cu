@@ -168,15 +168,6 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = a.B;
-    // Launched with programmatic stream serialisation, so the grid may start while the kernel
-    // before it on the stream still runs when that kernel allows it (the merge kernel of a previous
-    // decode call does; a kernel launched without the attribute finishes first). The prologue
-    // and the first page copies read only seq_lens, block_table and the caches; the consumer
-    // warps wait (griddepcontrol.wait) for the predecessor's completion before they read q or
-    // write the partials, so the call keeps plain stream order for everything else. The merge
-    // kernel that follows may be scheduled at once: it waits for this grid before it reads.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
@@ -186,6 +177,14 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
         for (int s = 0; s < kStages; ++s) released[s] = 0;
         fence_mbar_init();
     }
+    // Launched with programmatic stream serialisation: the CTAs may be resident before the kernel in front
+    // ends, but every thread waits for its end here, before the first read. Only this wait makes that kernel's
+    // writes visible, to plain loads and to the page copies, also where it lets this one start no earlier than its
+    // last CTA's exit: lengths, block table or pages may be what it wrote. A grid that finds nothing to do waits
+    // too, so that a kernel behind it that waits for it has waited for everything before. The merge may be
+    // scheduled from here on (it reads seq_lens, written by then, and waits for this grid before the rest).
+    griddep_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- page prefix sums over requests: start[b] = pages before request b ----------
     {
@@ -354,7 +353,6 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
     };
 
     // ---------------------------------- consumers ----------------------------------------
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     // Every consumer warp serves one KV head for all G query heads of its group (one K/V
     // row read feeds all of them) with its own running softmax state; when two warps share
     // a head (token halves), they are merged like split partials at the end.

@@ -179,9 +179,6 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         *a.used_out = used + pages;
         *a.admitted = adm;
     }
-    // A decode call behind this kernel starts as its last CTAs leave, and reads seq_lens and the block table
-    // before it waits for this grid's end: they are visible by then.
-    __threadfence();
 }
 
 template <bool IN_PLACE, int PER>

@@ -194,9 +194,6 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
             }
         }
     }
-    // A decode call behind this kernel starts as its last CTAs leave, and copies pages before it waits for
-    // this grid's end: the rows are visible by then.
-    if (PAGED) __threadfence();
 }
 
 // The gradient. The rows of a task come into shared memory by bulk copies, 4 KB of x and 4 KB of dy, into a
@@ -456,9 +453,6 @@ __global__ void __launch_bounds__(kThreads) norm_rope_ring_kernel(const __grid_c
         if (lane == 0 && t + (long long)kFwdRing * lanes < a.T) fetch(t + kFwdRing * lanes, stage);
         if (++stage == kFwdRing) stage = 0, phase ^= 1;
     }
-    // A decode call behind this kernel starts as its last CTAs leave, and copies pages before it waits for
-    // this grid's end: the rows are visible by then.
-    __threadfence();
 }
 
 // CTAs for `tasks` warp tasks: enough for all of them at once, at most `per_sm` per SM, and at least one

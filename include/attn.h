@@ -184,15 +184,11 @@ ATTN_API int attn_bwd(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v
  *   each request's offset into them. Contents on entry do not matter. Calls that share a
  *   workspace must not overlap on the GPU.
  *   Enqueues two kernels on `stream`: the split decode and the merge of its partials, both
- *   launched with programmatic stream serialisation. The merge may become resident while the
- *   decode grid runs and waits on the device for that grid's completion. The decode grid may
- *   start while the kernel enqueued just before it still runs, if that kernel allows dependents
- *   to launch early (the merge of a previous decode call does; a kernel launched without that
- *   attribute, the default, always finishes first): it then reads seq_lens, block_table and the
- *   caches before that kernel has finished, and waits for it only before reading q or writing
- *   the workspace. So a kernel that allows early launch must not write those three inputs of
- *   the decode call that follows it. In particular the o / lse of one decode call may be the q
- *   of the next, but not its caches, block_table or seq_lens.
+ *   launched with programmatic stream serialisation. The decode grid may become resident while
+ *   the kernel enqueued just before it still runs, if that kernel allows dependents to launch
+ *   early, and the merge while the decode grid runs; both wait on the device for the completion
+ *   of the kernel in front before they use anything it may write. So the call keeps plain stream
+ *   order: any of its inputs may be what the call before it has written.
  */
 ATTN_API int attn_decode_paged(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
                       const int32_t* block_table, const int32_t* seq_lens, attn_bf16* o, float* lse, int B, int Hq,
@@ -380,9 +376,8 @@ ATTN_API int attn_qk_norm_rope_paged(const attn_bf16* q, const attn_bf16* k, con
  *   counted per request, KV head and row tile, is reported as ATTN_ERR_DEVICE_BOUNDS and not computed.)
  *   Enqueues two kernels with programmatic stream serialisation, the attention and the merge of its
  *   partial results. Both wait on the device for the kernels in front of them before they read or write
- *   anything; the merge allows the kernel behind it to start early, as the merge of attn_decode_paged
- *   does (the same rule: o and lse may be the q of a decode call that follows, not its caches, table or
- *   lengths).
+ *   anything; the merge allows the kernel behind it to be launched early, as the merge of
+ *   attn_decode_paged does.
  *   workspace: attn_workspace_size(ATTN_OP_TREE_PAGED, 0, Hq, Hkv, max_q_len, D, ...) bytes, 256-byte
  *   aligned: partial results of the key ranges that several CTAs share. Contents on entry do not matter.
  *   Calls that share a workspace must not overlap on the GPU.
