@@ -111,6 +111,16 @@ __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, unsign
     }
 }
 
+// Waits, bounded, for the copies that a ring of `depth` stages has on their way when a wait on its next one, at
+// (stage, phase), was given up: those of the next `left` fills, as many as have a stage.
+__device__ __forceinline__ void ring_drain(uint64_t* full, int stage, int phase, int depth, long long left, unsigned* status,
+                                           unsigned site) {
+    for (int n = 0; n < depth && n < left; ++n) {
+        mbar_drain(smem_u32(&full[stage]), phase, status, site);
+        if (++stage == depth) stage = 0, phase ^= 1;
+    }
+}
+
 // ---------------------------------------------------------------------------------
 // TMA
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,

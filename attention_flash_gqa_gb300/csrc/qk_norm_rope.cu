@@ -273,9 +273,9 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
             }
         }
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, abort_flag, a.status, 0x51))) {
-            // given up: copies into the ring may still be landing, the CTA must outlast them
-            const uint64_t since = globaltimer();
-            while (globaltimer() - since < 100000ull) __nanosleep(1000);
+            // given up: the CTA outlasts the copies that this warp has on their way
+            if (lane == 0) ring_drain(full, stage, phase, depth, ((long long)a.T - t + lanes - 1) / lanes, a.status, 0x53);
+            __syncwarp();
             break;
         }
         const uint8_t* xs = mine + stage * 2 * bytes;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const __grid_co
     __syncthreads();
     float* part = a.part + (size_t)blockIdx.x * 2 * D;
     for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-        float acc = 0.f;
+        float acc = *abort_flag ? NAN : 0.f;  // a wait was given up: the sums lack rows, and say so
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
             if (kinds[w] == i / D) acc += sums[w][i % D];
@@ -420,9 +420,9 @@ __global__ void __launch_bounds__(kThreads) norm_rope_ring_kernel(const __grid_c
             if (lane == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
         }
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, abort_flag, a.status, 0x52))) {
-            // given up: copies into the ring may still be landing, the CTA must outlast them
-            const uint64_t since = globaltimer();
-            while (globaltimer() - since < 100000ull) __nanosleep(1000);
+            // given up: the CTA outlasts the copies that this warp has on their way
+            if (lane == 0) ring_drain(full, stage, phase, kFwdRing, ((long long)a.T - t + lanes - 1) / lanes, a.status, 0x54);
+            __syncwarp();
             break;
         }
         const uint8_t* xs = mine + stage * kFwdStage;
