@@ -37,6 +37,8 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
 constexpr int kPage = 16;
+constexpr int kMaxReqs = 16384;
+constexpr size_t prefix_bytes(int R) { return (size_t)(R + 1) * 2 * sizeof(int); }
 
 // What request b asks for; an inconsistent one asks for nothing.
 struct Ask {
@@ -183,10 +185,13 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
 
 template <bool IN_PLACE, int PER>
 cudaError_t launch_t(const PlanLaunch& L, cudaStream_t stream) {
-    const size_t smem = (size_t)(L.R + 1) * 2 * sizeof(int);
+    const size_t smem = prefix_bytes(L.R);
     cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024 - 512)  // beyond what a kernel may use unasked (static shared memory counts)
-        e = cudaFuncSetAttribute(paged_plan_kernel<IN_PLACE, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // Beyond what a kernel may use unasked (static shared memory counts). The limit belongs to the kernel, not to the
+    // call: every call sets the same, so that none lowers it between another thread's setting and its launch.
+    if (smem > 48 * 1024 - 512)
+        e = cudaFuncSetAttribute(paged_plan_kernel<IN_PLACE, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)prefix_bytes(kMaxReqs));
     if (e != cudaSuccess) return e;
     const long long rows = ((long long)L.T + PER - 1) / PER, items = rows > L.R ? rows : L.R;
     const long long want = items > kThreads ? (items + kThreads - 1) / kThreads : 1, most = IN_PLACE ? kCluster : L.sms;
@@ -214,6 +219,7 @@ cudaError_t launch_t(const PlanLaunch& L, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_paged_plan(const PlanLaunch& L, cudaStream_t stream) {
+    if (L.R > kMaxReqs) return cudaErrorInvalidValue;
     const int threads = (L.in_place ? kCluster : L.sms) * kThreads;
     if (L.T / 4 > threads) return L.in_place ? launch_t<true, 8>(L, stream) : launch_t<false, 8>(L, stream);
     if (L.T > threads) return L.in_place ? launch_t<true, 4>(L, stream) : launch_t<false, 4>(L, stream);
