@@ -840,7 +840,10 @@ cudaError_t launch_decode_paged(const DecodeLaunch& L, cudaStream_t stream) {
     mg.part = L.part, mg.seq_lens = L.seq_lens, mg.o = L.o, mg.lse = L.lse, mg.status = L.status;
     mg.B = L.B, mg.Hq = L.Hq, mg.hb = a.hb, mg.decode_grid = L.grid, mg.max_pages = L.max_pages, mg.window = L.window;
     auto go = [&](auto kern, auto merge, int threads) -> cudaError_t {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // the limit belongs to the kernel: every call sets that of the most heads, so that none lowers it between
+        // another thread's setting and its launch
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)decode_smem_bytes(kUnitBytes / (kPage * L.D * 2), L.D));
         if (e != cudaSuccess) return e;
         // Both kernels are launched with programmatic stream serialisation: each may be scheduled
         // while its predecessor on the stream still runs, and waits on the device

@@ -26,7 +26,7 @@ def test_plans_from_several_threads(in_place):
     away what another's needs."""
     lib = attn.load_library()
     sizes = [16384, 6500, 12000, 9000]
-    start = threading.Barrier(len(sizes))
+    start = threading.Barrier(len(sizes), timeout=60)
     bad, results = [], {}
 
     def work(R):
