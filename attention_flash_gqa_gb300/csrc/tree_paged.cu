@@ -232,7 +232,11 @@ struct Walk {
 
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
-// ceil(x / y) for 1 <= y, 0 <= x < 2^22: the margin of half a unit in the numerator outweighs the roundings.
+// ceil(x / y) for 0 <= x, 1 <= y, x + y < kCeilDivSum. The numerator x + y - 1/2 is exact, and the exact quotient lies
+// 1 / (2 y) or more from an integer; __fdividef is off by 2 ulp at most, less than (x + y) / y * 2^-22, which is less
+// than 1 / (2 y) while x + y < 2^21. Calls here have x below kFewUnits (units, tiles, shares) and y below it too.
+constexpr int kCeilDivSum = 1 << 21;
+static_assert(2 * kFewUnits <= kCeilDivSum, "ceil_div's range");
 __device__ __forceinline__ int ceil_div(int x, int y) { return __float2int_rd(__fdividef((float)(x + y) - 0.5f, (float)y)); }
 
 // P units over G CTAs: the first P % G of them take one more than the others.
