@@ -405,6 +405,12 @@ def _native():
         import torch  # noqa: F401  (the module uses torch's own library)
 
         load_library()
+        from . import _build
+
+        built_for = _build.ops_tag()
+        if built_for is not None and built_for != _build.torch_tag():
+            raise RuntimeError(f"attention_flash_gqa_gb300/_ops.so was built for {built_for}, not {_build.torch_tag()}: build it "
+                               "again (python -m attention_flash_gqa_gb300._build or __graft_entry__.build())")
         try:
             from . import _ops as ops
         except ImportError as e:

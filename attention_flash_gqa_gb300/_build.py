@@ -2,12 +2,15 @@
 the Python binding into ``_ops.so``.
 
 The library: nvcc only, one ``-gencode`` for sm_103a, translation units compiled in parallel and
-linked with ``nvcc -shared``. The binding: one C++ file against torch's headers, by g++ beside them.
+linked with ``nvcc -shared``. The binding: one C++ file against torch's headers, by g++ beside them; it
+belongs to the torch it was built with. The library does not need it: it is linked where the binding
+cannot be built, and where torch is not installed there is no binding to build.
 Used by ``__graft_entry__.build()`` and the tests.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -18,6 +21,7 @@ LIB = os.path.join(HERE, "libattn_gb300.so")
 OPS = os.path.join(HERE, "_ops.so")
 OPS_SOURCE = os.path.join(CSRC, "py_ops.cpp")
 BUILD_DIR = os.path.join(HERE, "_build_tmp")
+OPS_TAG = os.path.join(BUILD_DIR, "ops_built_for.txt")  # what _ops.so was built for
 SOURCES = ["api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd_small.cu", "decode_paged.cu", "decode_paged_noalloc.cu",
            "merge_lse.cu", "paged_plan.cu", "qk_norm_rope.cu", "tree_paged.cu"]
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
@@ -36,13 +40,43 @@ def _inputs():
     return files
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(OPS):
-        return False
-    t = os.path.getmtime(LIB)
+def torch_tag() -> str | None:
+    """The torch and Python that a binding built now would belong to; None without torch."""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    import sysconfig
+
+    import torch
+
+    return f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')} abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+
+
+def ops_tag() -> str | None:
+    """What the present _ops.so was built for; None if that is not known."""
+    try:
+        with open(OPS_TAG) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def _newer(target, sources) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(f) <= os.path.getmtime(target) for f in sources)
+
+
+def lib_up_to_date() -> bool:
+    return _newer(LIB, _inputs())
+
+
+def ops_up_to_date() -> bool:
+    """Newer than its sources and built for this torch (or there is no torch to build it for)."""
+    tag = torch_tag()
     header = os.path.join(os.path.dirname(HERE), "include", "attn.h")
-    return (all(os.path.getmtime(f) <= t for f in _inputs()) and
-            all(os.path.getmtime(f) <= os.path.getmtime(OPS) for f in (OPS_SOURCE, header)))
+    return tag is None or (_newer(OPS, (OPS_SOURCE, header)) and ops_tag() == tag)
+
+
+def up_to_date() -> bool:
+    return lib_up_to_date() and ops_up_to_date()
 
 
 def _build_ops() -> None:
@@ -59,16 +93,37 @@ def _build_ops() -> None:
            "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
            "-I", os.path.join(cuda, "include"), "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
            "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"py_ops.cpp needs g++: {e}") from e
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for py_ops.cpp:\n{r.stdout}\n{r.stderr}")
+    if os.path.exists(OPS_TAG):
+        os.remove(OPS_TAG)
     os.replace(tmp, OPS)
+    with open(OPS_TAG, "w") as f:
+        f.write(torch_tag())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
+    """Builds what is missing or stale. Raises where the binding cannot be built, with the library linked all the same."""
+    do_lib, do_ops = force or not lib_up_to_date(), torch_tag() is not None and (force or not ops_up_to_date())
     os.makedirs(BUILD_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        ops = ex.submit(_build_ops) if do_ops else None
+        if do_lib:
+            _build_lib(verbose)
+        if ops is not None:
+            try:
+                ops.result()
+            except Exception as e:
+                raise RuntimeError(f"{LIB} is built, but the native part of the Python binding is not: the calls that go "
+                                   f"through it are missing\n{e}") from e
+    return LIB
+
+
+def _build_lib(verbose: bool) -> None:
     cc = nvcc()
     flags = [GENCODE, "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
              "--expt-relaxed-constexpr", "-I", os.path.join(os.path.dirname(HERE), "include")]
@@ -83,10 +138,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ops = ex.submit(_build_ops)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        ops.result()
     if verbose:
         for _, err in results:
             print(err)
@@ -96,7 +149,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
