@@ -10,6 +10,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <optional>
@@ -138,7 +139,7 @@ at::Tensor part_of(const at::Tensor& buf, int64_t first, int64_t count) {
     return t;
 }
 
-// Runs f, with what it throws as a Python error.
+// Runs f, with what it throws as the Python error that torch makes of it (out of memory: torch.OutOfMemoryError).
 template <class F>
 PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
     if (given != wanted) {
@@ -149,14 +150,13 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
         PyErr_SetString(PyExc_RuntimeError, "the attention library is not loaded");
         return nullptr;
     }
+    HANDLE_TH_ERRORS
     try {
         return f();
     } catch (const Raised&) {
         return nullptr;
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
     }
+    END_HANDLE_TH_ERRORS
 }
 
 // The tuple of some results, each a given Python object or a new tensor.
