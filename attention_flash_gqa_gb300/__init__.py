@@ -475,7 +475,9 @@ def attn_tree_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, tree_mask,
     q [T,Hq,D]: the drafted tokens of all requests packed by cu_q int32 [R+1], the last of their
     seq_lens int32 [R] cached tokens; tree_mask int32 [T, words]: bit d of a row (word d // 32) set where it
     sees its request's drafted token d; every row sees the context before the drafted tokens, with
-    window > 0 only the keys less than `window` behind its position (positions int32 [T]).
+    window > 0 only the keys less than `window` behind its position (positions int32 [T]). Among the drafted
+    tokens the mask alone decides: for a windowed layer whose trees are deeper than the window, clear the bits of
+    the ancestors `window` or more positions back.
     """
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])

@@ -362,6 +362,9 @@ ATTN_API int attn_qk_norm_rope_paged(const attn_bf16* q, const attn_bf16* k, con
  *     p_i = max(positions[i], L_b - n_b) is the row's position (context length + depth in its tree);
  *   key L_b - n_b + d (drafted token d): visible if bit d % 32 of word d / 32 of the row's mask is
  *     set (normally its ancestors and itself). Bits of d >= n_b are ignored.
+ *   So a window limits the context alone. attn_fwd_paged and attn_decode_paged apply theirs to the new tokens
+ *   too: for their result where a tree is deeper than the window, the caller clears the bits of the ancestors
+ *   that are `window` or more positions behind the row (p_i - p_d >= window).
  *   A row that sees no key gets o = 0 and lse = -inf. A row with a NaN score (NaN in its q or in a K that it
  *   sees) gets NaN for o and lse. Hidden keys' K may hold anything. V must be finite in
  *   all keys up to L_b of the pages that are read (with window > 0 from the page of key
