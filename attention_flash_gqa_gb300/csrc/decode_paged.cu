@@ -116,15 +116,23 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t& r0, uint3
                  : "r"(addr));
 }
 
-// Clamped length of request b (records a bounds fault for lengths beyond the table).
-__device__ __forceinline__ int req_len(const DecodeArgs& a, int b) {
-    int L = a.seq_lens[b];
+// A length within the table (`record`: one outside is recorded as a bounds fault).
+__device__ __forceinline__ int clamp_len(const DecodeArgs& a, int L, bool record) {
     int cap = a.max_pages * kPage;
     if (L < 0 || L > cap) {
-        atomicOr(a.status, DEVSTAT_BOUNDS);
+        if (record) atomicOr(a.status, DEVSTAT_BOUNDS);
         L = L < 0 ? 0 : cap;
     }
     return L;
+}
+// Clamped length of request b.
+__device__ __forceinline__ int req_len(const DecodeArgs& a, int b) { return clamp_len(a, a.seq_lens[b], true); }
+
+// A value that another kernel may be writing: read from L2, and again at every call.
+__device__ __forceinline__ int32_t load_l2(const int32_t* p) {
+    int32_t v;
+    asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
 }
 
 // First token the query of a request of length L sees (the window's start).
@@ -178,22 +186,32 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
         fence_mbar_init();
     }
     // Launched with programmatic stream serialisation: the CTAs may be resident before the kernel in front
-    // ends, but every thread waits for its end here, before the first read. Only this wait makes that kernel's
-    // writes visible, to plain loads and to the page copies, also where it lets this one start no earlier than its
-    // last CTA's exit: lengths, block table or pages may be what it wrote. A grid that finds nothing to do waits
-    // too, so that a kernel behind it that waits for it has waited for everything before. The merge may be
-    // scheduled from here on (it reads seq_lens, written by then, and waits for this grid before the rest).
-    griddep_wait();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // ends, but what they use is read after griddep_wait. Only this wait makes that kernel's writes visible, to
+    // plain loads and to the page copies, also where it lets this one start no earlier than its last CTA's exit:
+    // lengths, block table and pages may be what it wrote. Before it, with up to 256 requests, the CTA lays out its
+    // share on a guess: from lengths and page ids as they are in L2 at that time, with the first pages asked for
+    // in L2. After it the first page copies are issued by that layout, and while they are on their way every length
+    // and page id that went into it is read again; if one differs the copies are waited for and all of it is done
+    // anew. So a call behind a decode call, whose merge writes none of these, has its prologue done and its first
+    // pages near when the merge ends (64 requests of 256 to 1024 keys, call after call: 29.3 us, 31.4 without asking for
+    // the pages, 33.3 with everything after the wait; one request 8.1, 8.1, 9.1; behind a plan and a head norm, which
+    // let nothing start early, 37.4, 38.7 and 38.5 for the three calls, and with 4 requests 18.4, 18.1 and 17.5).
+    // A grid that finds nothing to do waits too, so that a kernel behind it that waits for it has waited for
+    // everything before.
+    const bool guess = B <= 256;  // a request a thread
+    int32_t* lens = start + 512;  // [256] lengths of the layout
 
     // ---- page prefix sums over requests: start[b] = pages before request b ----------
-    {
+    auto scan_requests = [&](bool record) {
         const int per = (B + 255) / 256;
         int local = 0;
         if (tid < 256) {
             for (int i = 0; i < per; ++i) {
                 int b = tid * per + i;
-                if (b < B) local += req_units(a, req_len(a, b));
+                if (b >= B) continue;
+                const int L = clamp_len(a, load_l2(a.seq_lens + b), record);
+                if (guess) lens[b] = L;
+                local += req_units(a, L);
             }
         }
         // inclusive scan of `local` over threads 0..255
@@ -214,43 +232,22 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
                 int b = tid * per + i;
                 if (b < B) {
                     start[b] = acc;
-                    acc += req_units(a, req_len(a, b));
+                    acc += guess ? local : req_units(a, req_len(a, b));
                 }
             }
             if (tid == 255) start[B] = acc;
         }
         __syncthreads();
-    }
-    const long long P = start[B];
-    // Pages are shared by Gc = min(grid, P) CTAs, so every participating CTA owns at
-    // least one page and the CTAs touching a request are exactly owner(first)..owner(last).
-    const int Gc = (int)(P < (long long)gridDim.x ? P : (long long)gridDim.x);
+    };
     const int k = blockIdx.x;
-
-    if (P == 0 || k >= Gc) return;
-    const long long u0 = (long long)k * P / Gc, u1 = (long long)(k + 1) * P / Gc;
-    if (u0 >= u1) return;
-
-    // first request overlapping [u0, u1): largest b with start[b] <= u0 and a nonempty range
-    int b_first = 0;
-    {
-        int lo = 0, hi = B - 1;
-        while (lo < hi) {
-            int mid = (lo + hi + 1) >> 1;
-            if (start[mid] <= u0) lo = mid;
-            else hi = mid - 1;
-        }
-        b_first = lo;
-        while (b_first < B && start[b_first + 1] <= u0) ++b_first;
-    }
-
+    long long u0 = 0, u1 = 0;  // the CTA's share of the units
+    int b_first = 0;           // first request overlapping it
     // (No L2 prefetch of the later requests' query rows here: it made graph-replayed calls
     // 0.35 us slower.)
     // Page table of this CTA's range, gathered once by all threads: entry = page id << 5 |
     // valid tokens in the page (1..16), or -1 for a page id outside the pool. The loops below
     // then never wait on a dependent global load.
-    const int n_units = (int)(u1 - u0);
-    auto make_entry = [&](int kk) -> int32_t {
+    auto make_entry = [&](int kk, bool record) -> int32_t {
         const long long u = u0 + kk;
         int lo = b_first, hi = B - 1;
         while (lo < hi) {
@@ -258,19 +255,16 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
             if (start[mid] <= u) lo = mid;
             else hi = mid - 1;
         }
-        const int L = req_len(a, lo);
+        const int L = guess ? lens[lo] : req_len(a, lo);
         const int p = (int)(u - start[lo]) + first_token(a, L) / kPage;  // page index in the request
-        const int page = a.block_table[(size_t)lo * a.max_pages + p];
+        const int page = load_l2(a.block_table + (size_t)lo * a.max_pages + p);
         if (page < 0 || page >= a.num_pages) {
-            atomicOr(a.status, DEVSTAT_BOUNDS);
+            if (record) atomicOr(a.status, DEVSTAT_BOUNDS);
             return -1;
         }
         const int nt = min(kPage, L - p * kPage);
         return (page << 5) | nt;
     };
-    // Warp 0 stages the first units itself and issues their pages at once, so the copies are in
-    // flight while the rest of the table is staged.
-    const int n_pre = min(n_units, kStages);
     // every cached byte is read once per step: evict-first keeps the stream from displacing
     // (or forcing the write-back of) other lines in L2
     const uint64_t policy = l2_policy_evict_first();
@@ -297,18 +291,91 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
             mbar_arrive(fb);
         }
     };
+    auto ask = [&](int32_t entry) {  // the unit's pages into L2
+        if (entry < 0) return;
+        if constexpr (DC::PACKED) {
+            prefetch_tile_5d(&tk, 0, 0, g0, 0, entry >> 5);
+            prefetch_tile_5d(&tv, 0, 0, g0, 0, entry >> 5);
+        } else if (a.nhb == 1) {
+            const size_t off = (size_t)(entry >> 5) * kPage * a.Hkv * D;
+            prefetch_bulk(a.kc + off, page_bytes);
+            prefetch_bulk(a.vc + off, page_bytes);
+        } else {
+            prefetch_tile_3d(&tk, 0, g0, (entry >> 5) * kPage);
+            prefetch_tile_3d(&tv, 0, g0, (entry >> 5) * kPage);
+        }
+    };
     // The warp that issues the first pages (the producer warp, or consumer warp 0 without one)
-    // stages units 0..31 itself
+    // stages units 0..31 itself and does so at once, so the copies are in flight while the rest
+    // of the table is staged.
     constexpr int kFirstWarp = DC::OWN_PRODUCER ? kConsumerWarps : 0;
     const int rot = (tid + kThreads - kFirstWarp * 32) % kThreads;
-    for (int kk = rot; kk < n_units && kk < kMaxUnits; kk += kThreads) unit_tab[kk] = make_entry(kk);
-    if (warp == kFirstWarp) {
-        __syncwarp();
-        if (lane == 0)
+    int n_units = 0, n_pre = 0;  // (0: no share)
+    auto lay_out = [&](bool record) {
+        scan_requests(record);
+        // Pages are shared by Gc = min(grid, P) CTAs, so every participating CTA owns at
+        // least one page and the CTAs touching a request are exactly owner(first)..owner(last).
+        const long long P = start[B];
+        const int Gc = (int)(P < (long long)gridDim.x ? P : (long long)gridDim.x);
+        n_units = n_pre = 0;
+        if (k >= Gc) return;  // P = 0 among them
+        u0 = (long long)k * P / Gc, u1 = (long long)(k + 1) * P / Gc;
+        // largest b with start[b] <= u0 and a nonempty range
+        int lo = 0, hi = B - 1;
+        while (lo < hi) {
+            int mid = (lo + hi + 1) >> 1;
+            if (start[mid] <= u0) lo = mid;
+            else hi = mid - 1;
+        }
+        b_first = lo;
+        while (b_first < B && start[b_first + 1] <= u0) ++b_first;
+        n_units = (int)(u1 - u0), n_pre = min(n_units, kStages);
+        for (int kk = rot; kk < n_units && kk < kMaxUnits; kk += kThreads) unit_tab[kk] = make_entry(kk, record);
+        if (warp == kFirstWarp) __syncwarp();
+    };
+    auto issue_first = [&]() {
+        if (warp == kFirstWarp && lane == 0)
             for (int i = 0; i < n_pre; ++i) issue(i, unit_tab[i]);
+    };
+    if (guess) {
+        lay_out(false);
+        if (warp == kFirstWarp && lane < n_pre) ask(unit_tab[lane]);
     }
-    __syncthreads();
-    auto unit_entry = [&](int kk) -> int32_t { return kk < kMaxUnits ? unit_tab[kk] : make_entry(kk); };
+    griddep_wait();
+    // the merge may be scheduled from here on (it reads seq_lens, written by then, and waits for this grid)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    uint32_t flip = 0u;  // 1: the full barriers are a phase ahead
+    bool same = guess;
+    if (guess) {
+        issue_first();
+        bool bad = false;  // to be reported, if the layout is the right one
+        if (tid < B) {
+            const int L = load_l2(a.seq_lens + tid), within = clamp_len(a, L, false);
+            same = within == lens[tid], bad = within != L;
+        }
+        for (int kk = rot; kk < n_units && kk < kMaxUnits; kk += kThreads) {
+            const int32_t entry = make_entry(kk, false);
+            same &= entry == unit_tab[kk], bad |= entry < 0;
+        }
+        same = __syncthreads_and(same);
+        if (same && bad) atomicOr(a.status, DEVSTAT_BOUNDS);
+        if (!same) {
+            if (warp == kFirstWarp && lane == 0)
+                for (int s = 0; s < kStages; ++s) {
+                    if (s >= n_pre) mbar_arrive(smem_u32(&full[s]));
+                    mbar_drain(smem_u32(&full[s]), 0, a.status, 0x34);
+                }
+            flip = 1u;
+            __syncthreads();
+        }
+    }
+    if (!same) {
+        lay_out(true);
+        issue_first();
+        __syncthreads();
+    }
+    if (n_units == 0) return;
+    auto unit_entry = [&](int kk) -> int32_t { return kk < kMaxUnits ? unit_tab[kk] : make_entry(kk, true); };
 
     if constexpr (DC::OWN_PRODUCER) {
         if (warp == kConsumerWarps) {
@@ -325,7 +392,7 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
                 const int issued = i;
                 for (int s = 0; s < kStages && s < issued; ++s) {
                     const int last = s + ((issued - 1 - s) / kStages) * kStages;
-                    mbar_drain(smem_u32(&full[s]), (last / kStages) & 1, a.status, 0x33);
+                    mbar_drain(smem_u32(&full[s]), ((last / kStages) & 1) ^ flip, a.status, 0x33);
                 }
             }
             return;
@@ -433,7 +500,7 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
             }
         }
         const int s = i % kStages, r = i / kStages;
-        ok = mbar_wait(smem_u32(&full[s]), r & 1, abort_flag, a.status, 0x32);
+        ok = mbar_wait(smem_u32(&full[s]), (r & 1) ^ flip, abort_flag, a.status, 0x32);
         if (!ok) break;
         const int32_t entry = unit_entry(i);
         const int nt = (entry >= 0 ? (entry & 31) : 0) - TPW * half;  // end of this warp's valid tokens (may be <= 0)
@@ -720,14 +787,15 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(MergeArgs m
     const int nh = m.hb * G / gridDim.z;  // heads of this CTA
     const int h0 = blockIdx.y * m.hb * G + blockIdx.z * nh;
     // Which decode CTAs covered request b follows from the request lengths alone (inputs, not
-    // written by the decode grid): this runs before the wait, beside the decode grid.
+    // written by the decode grid): this runs before the wait, beside the decode grid, which lets this
+    // one start only when the kernels in front of it have ended. (From L2: nothing orders this SM's L1.)
     // Every warp sums the unit counts over all requests itself (no shared memory, so these
     // CTAs fit beside a decode CTA).
     DecodeArgs la;  // the fields req_len / req_units read
     la.seq_lens = m.seq_lens, la.max_pages = m.max_pages, la.window = m.window, la.status = m.status;
     long long before = 0, total = 0;
     for (int i = threadIdx.x & 31; i < m.B; i += 32) {
-        const int n = req_units(la, req_len(la, i));
+        const int n = req_units(la, clamp_len(la, load_l2(la.seq_lens + i), true));
         total += n;
         if (i < b) before += n;
     }
@@ -737,7 +805,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(MergeArgs m
         total += __shfl_xor_sync(0xffffffffu, total, off);
     }
     const long long s0 = before, P = total;
-    const long long s1 = s0 + req_units(la, req_len(la, b));
+    const long long s1 = s0 + req_units(la, clamp_len(la, load_l2(la.seq_lens + b), true));
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int Gc = (int)(P < (long long)m.decode_grid ? P : (long long)m.decode_grid);
     const int nitems = nh * (D / DI);

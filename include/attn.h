@@ -188,7 +188,9 @@ ATTN_API int attn_bwd(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v
  *   the kernel enqueued just before it still runs, if that kernel allows dependents to launch
  *   early, and the merge while the decode grid runs; both wait on the device for the completion
  *   of the kernel in front before they use anything it may write. So the call keeps plain stream
- *   order: any of its inputs may be what the call before it has written.
+ *   order: any of its inputs may be what the call before it has written. (Lengths and page ids
+ *   may be looked at before that wait, as a guess that is checked after it; what stood there
+ *   before needs not be valid, but the memory must be there.)
  */
 ATTN_API int attn_decode_paged(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
                       const int32_t* block_table, const int32_t* seq_lens, attn_bf16* o, float* lse, int B, int Hq,

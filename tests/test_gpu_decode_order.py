@@ -1,6 +1,7 @@
 """Decode directly behind the calls that write what it reads: every step of a captured loop (plan in place, head norm
 into the pages, decode) sees that step's lengths, block table and pages, and a decode call without work does not let
-the kernel behind it run before the one in front of it has finished."""
+the kernel behind it run before the one in front of it has finished. Where a call in front lets decode start early, what
+decode reads before that call's end does not count."""
 import math
 
 import pytest
@@ -138,3 +139,76 @@ def test_empty_decode_keeps_the_order():
         assert torch.equal(o, keep) and torch.equal(y, want)
         assert (do == 0).all() and (dl == -math.inf).all()
     assert attn.attn_get_device_status() == 0
+
+
+def written_by_decode(ints, rows):
+    """A decode call (head_dim 256, one key a request) whose result is, bit for bit, these small int32 values, and the buffer
+    of its result. Its merge lets the kernel behind it start before it has written anything."""
+    flat = torch.zeros(rows * 4 * 128, dtype=torch.int32)
+    flat[: len(ints)] = torch.tensor(ints, dtype=torch.int32)
+    vc = torch.zeros(rows, 16, 4, 256, dtype=torch.bfloat16, device="cuda")
+    vc[:, 0] = flat.view(torch.bfloat16).view(rows, 4, 256).cuda()
+    kc, q = torch.ones_like(vc), torch.ones(rows, 4, 256, dtype=torch.bfloat16, device="cuda")
+    table = i32([[b] for b in range(rows)])
+    o, lse, one = torch.empty_like(q), torch.empty(rows, 4, device="cuda"), i32([1] * rows)
+    ws = torch.empty(attn.attn_workspace_size(attn.ATTN_OP_DECODE_PAGED, rows, 4, 4, 0, 256), dtype=torch.uint8, device="cuda")
+    return (lambda: attn.attn_decode_paged(q, kc, vc, table, one, o, lse, scale=0.1, workspace=ws)), o
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("what", ["lengths", "table", "pages", "all"])
+@pytest.mark.parametrize("Hq,Hkv,D,window", [(8, 2, 128, 0), (4, 4, 256, 0), (16, 8, 256, 50), (32, 8, 128, 30)])
+def test_inputs_written_by_the_call_in_front(Hq, Hkv, D, window, what, captured):
+    """Lengths, block table or pages are the result of a decode call directly in front, and what stood there before is
+    something else, valid or not: nothing of it reaches the result or the device status."""
+    R, cap, pages = 6, 10, 64
+    g = torch.Generator().manual_seed(Hq + D)
+    lens = [37, 0, 160, 5, 64, 1]
+    ids = torch.randperm(pages, generator=g)[: R * cap].tolist()
+    words = -(-max(R, R * cap) // 512)
+    call_l, o_l = written_by_decode(lens, words)
+    call_t, o_t = written_by_decode(ids, words)
+    bits = torch.randint(0, 1 << 14, (pages * 16 * Hkv * D,), generator=g, dtype=torch.int16)  # bf16 values below 2
+    call_k, o_k = written_by_decode(bits.view(torch.int32).tolist(), pages * 16 * Hkv * D // 1024)
+    kc, vc = (torch.randn(pages, 16, Hkv, D, generator=g).bfloat16().cuda() for _ in range(2))
+    q = torch.randn(R, Hq, D, generator=g).bfloat16().cuda()
+    front = {"lengths": [call_l], "table": [call_t], "pages": [call_k], "all": [call_t, call_k, call_l]}[what]
+    lengths = o_l.flatten().view(torch.int32)[:R] if what in ("lengths", "all") else i32(lens)
+    table = (o_t.flatten().view(torch.int32)[: R * cap] if what in ("table", "all") else i32(ids)).view(R, cap)
+    keys = o_k.view(pages, 16, Hkv, D) if what in ("pages", "all") else kc
+    o, lse = torch.empty_like(q), torch.empty(R, Hq, device="cuda")
+    ws = torch.empty(attn.attn_workspace_size(attn.ATTN_OP_DECODE_PAGED, R, Hq, Hkv, 0, D), dtype=torch.uint8, device="cuda")
+
+    def run():
+        for f in front:
+            f()
+        attn.attn_decode_paged(q, keys, vc, table, lengths, o, lse, scale=0.1, window=window, workspace=ws)
+
+    run()
+    torch.cuda.synchronize()
+    assert attn.attn_get_device_status() == 0
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+    now = keys.cpu()
+    assert torch.equal(lengths.cpu(), torch.tensor(lens, dtype=torch.int32)) and table.flatten().tolist() == ids
+    if keys is not kc:
+        assert torch.equal(now.view(torch.int16).flatten(), bits)
+    live = [b for b in range(R) if lens[b]]
+    ro, to, rl, tl = ref.tree(q.cpu()[live], now, vc.cpu(), table.cpu()[live], [lens[b] for b in live], list(range(len(live) + 1)),
+                              torch.ones(len(live), 1, dtype=torch.int32), 0.1, window, torch.tensor([lens[b] - 1 for b in live]))
+    for before in (0, 3, 160, -1, 2 ** 30, 7):  # as a length, and as a page id
+        if what in ("lengths", "all"):
+            lengths.fill_(before)
+        if what in ("table", "all"):
+            table.fill_(before)
+        if what in ("pages", "all"):
+            keys.fill_(math.nan)
+        o.fill_(5.0), lse.fill_(5.0)
+        torch.cuda.synchronize()
+        graph.replay() if captured else run()
+        assert attn.attn_get_device_status() == 0, before
+        ref.close("o", o[live], ro, to)
+        ref.close("lse", lse[live], rl.t(), tl.t())
+        assert (o[1] == 0).all() and (lse[1] == -math.inf).all()
