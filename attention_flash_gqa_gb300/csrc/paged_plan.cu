@@ -15,14 +15,15 @@
 // and pages. Where there are more rows than threads, a thread takes four consecutive ones, or eight if there
 // are more than four a thread: it finds the request of the first by bisection of the prefix sums, steps on
 // from there, reads a page id once for rows of one page, and stores 16 bytes at a time where the outputs are
-// aligned (1000 requests, 500 thousand rows: 7.2 us by eights, 7.6 by fours, 9.5 a row at a time). Otherwise
-// it takes one (64 requests of one row each: 3.3 us against 5.0 by fours, whose rows read the state of four
+// aligned (1000 requests, 500 thousand rows: 6.5 us by eights, 7.1 by fours, 9.4 a row at a time). Otherwise
+// it takes one (64 requests of one row each: 2.9 us against 4.2 by fours, whose rows read the state of four
 // requests one after the other). A new
 // page's id is read from the free list, not from the table, so no row waits for another thread's table
 // entry.
 //
 // The lengths, held pages and the free list's cursor may be updated in place: the CTAs are then one
-// cluster, and all of them have read the old state before the first writes the new (a cluster barrier).
+// cluster, and all of them have read the old state before the first writes the new (a cluster barrier): eight
+// SMs at most, so a long step takes longer (the 500 thousand rows 38 us; 64 requests of one row 3.4).
 // Otherwise the grid is as wide as the rows need. Programmatic serialisation hides the launch behind the
 // end of the kernel in front (1000 requests, call after call: 10.2 -> 7.5 us).
 #include <cuda_runtime.h>

@@ -356,9 +356,13 @@ __global__ void __launch_bounds__(kDwWarps * 32) norm_rope_dw_kernel(const float
 }
 
 // The paged form of long calls, with its rows in rings like the gradient's: 4 KB a stage, two stages a warp, five
-// CTAs an SM (8468 tokens, 10 + 2 + 2 heads of 512: 42.2 us against 53.9 with loads into registers; 12590 tokens,
-// 30 + 15 + 15 of 64: 35.4 against 43.7; 4096 tokens, 32 + 4 + 4 of 512: 56.2 against 57.7). The form that is not
-// paged keeps the registers: 16384 tokens, 32 + 16 heads of 256, 124.8 us against 138 to 142 with rings.
+// CTAs an SM (8468 tokens, 10 + 2 + 2 heads of 512: 41.4 us against 53.9 with loads into registers; 12590 tokens,
+// 30 + 15 + 15 of 64: 34.9 against 43.7; 4096 tokens, 32 + 4 + 4 of 512: 55.4 against 57.7). The form that is not
+// paged has none, and is better off without for long calls alone: 16384 tokens, 32 + 16 heads of 256, 125 us against
+// 138 to 142 with rings. Of the calls of 10 to 80 us most would gain a little (5749 tokens, 32 + 8 heads of 128: 24.6 us,
+// 22.4 with rings of two stages and four CTAs an SM; 2637, 50 + 10 of 64: 11.3, 10.6; 1197, 30 + 10 of 512: 21.5, 20.4;
+// 2470, 80 + 16 of 512: 78.9, 76.6; 421, 45 + 15 of 512: 12.5, 12.5), short ones lose up to 8 %. What makes the first
+// one lose is not known, so there is no rule to choose by yet.
 constexpr int kFwdRing = 2;
 constexpr int kFwdStage = 4096;
 constexpr int kFwdSmem = kWarps * kFwdRing * kFwdStage + kWarps * kFwdRing * 8 + 64;

@@ -540,8 +540,11 @@ __global__ void __launch_bounds__(TreeCfg<D>::kThreads, 1)
                     float2 rs[2] = {{0.f, 0.f}, {0.f, 0.f}};
                     const float2 sc = make_float2(a.scale_log2, a.scale_log2);
                     tc_fence_after();
-                    // l sums p in fp32; the P of the product is rounded to bf16 (an MMA takes both operands in V's
-                    // type), half a step of 2^-8 that averages out over the keys.
+                    // l sums p in fp32; the P of the product is rounded to bf16, since an MMA takes both operands in V's
+                    // type, as in the other attention kernels here: o is then off by 0.0023 of its size against 64
+                    // bits, 0.0017 of it the rounding of o itself. A second product, with what the rounding leaves of P,
+                    // takes the rest away and was measured: batch of 64 at D 128 46.4 us against 40.1, 12 long contexts
+                    // 213 against 166, D 64 59.8 against 51.4, windowed D 256 188.8 against 185.8, D 512 39.5 against 38.0.
                     // Two sets: the half tile's 64 scores in registers. One set: two passes over the tile, 64 scores at a
                     // time: the maximum of the lower and the upper half, then the exponentials of the upper half, still
                     // in registers, and of the lower one, read again. One loop, so that each part's code is there once:
