@@ -915,7 +915,7 @@ cudaError_t launch_decode_paged(const DecodeLaunch& L, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         // Both kernels are launched with programmatic stream serialisation: each may be scheduled
         // while its predecessor on the stream still runs, and waits on the device
-        // (griddepcontrol.wait) for that predecessor's completion before it reads anything the
+        // (griddepcontrol.wait) for that predecessor's completion before it uses anything the
         // predecessor may write.
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

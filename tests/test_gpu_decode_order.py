@@ -28,7 +28,7 @@ def i32(v):
     return torch.as_tensor(v, dtype=torch.int32).cuda()
 
 
-@pytest.mark.parametrize("R,Hq,Hkv,D,window", [(5, 8, 2, 128, 0), (37, 4, 2, 256, 60), (70, 8, 8, 128, 0), (300, 4, 1, 128, 0)])
+@pytest.mark.parametrize("R,Hq,Hkv,D,window", [(5, 8, 2, 128, 0), (37, 4, 2, 256, 60), (70, 8, 8, 128, 0), (256, 4, 1, 128, 0), (257, 4, 1, 128, 0)])
 def test_steps_in_one_graph(R, Hq, Hkv, D, window):
     """18 steps of one token each in a graph, replayed on other lengths, pages and tokens: unwritten slots hold NaN and
     the block table -1, so a step that saw an older state would show it."""
