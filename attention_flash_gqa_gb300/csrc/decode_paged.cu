@@ -118,10 +118,10 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t& r0, uint3
 
 // A length within the table (`record`: one outside is recorded as a bounds fault).
 __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int L, bool record) {
-    int cap = a.max_pages * kPage;
+    const long long cap = (long long)a.max_pages * kPage;
     if (L < 0 || L > cap) {
         if (record) atomicOr(a.status, DEVSTAT_BOUNDS);
-        L = L < 0 ? 0 : cap;
+        L = L < 0 ? 0 : (int)cap;
     }
     return L;
 }
@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
     // let nothing start early, 37.4, 38.7 and 38.5 for the three calls, and with 4 requests 18.4, 18.1 and 17.5).
     // A grid that finds nothing to do waits too, so that a kernel behind it that waits for it has waited for
     // everything before.
-    const bool guess = B <= 256;  // a request a thread
+    // (a request a thread; and whatever the lengths read before the wait are, their pages count in 32 bits)
+    const bool guess = B <= 256 && (long long)B * a.max_pages < 0x7fffffffll;
     int32_t* lens = start + 512;  // [256] lengths of the layout
 
     // ---- page prefix sums over requests: start[b] = pages before request b ----------
