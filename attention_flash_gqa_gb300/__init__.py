@@ -27,6 +27,10 @@ Entry points (same names as the C ABI):
 * ``attn_tree_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, tree_mask, max_q_len, ...)``
   drafted token trees over a paged cache: packed rows [T,Hq,D] -> (o, lse[Hq,T])
 * ``attn_workspace_size``, ``attn_get_device_status``, ``attn_status_string``
+* ``sink=`` of attn_fwd, attn_fwd_varlen, attn_fwd_paged, attn_bwd and attn_decode_paged: with a window, a sequence's first keys
+  that stay visible past it
+* ``attn_kv4_append(k, v, slots, kv_cache)`` keys and values into a paged cache of 4-bit codes, ``attn_kv4_unpack(kv_cache, pages)``
+  its pages back as bf16, ``attn_decode_kv4(q, kv_cache, block_table, seq_lens, ...)`` decode over it -> (o, lse[B,Hq])
 * ``attn_selftest_wait_timeout`` (exercises the bounded-wait failure reporting)
 """
 from __future__ import annotations
@@ -42,9 +46,9 @@ __all__ = [
     "attn_get_device_status", "attn_status_string", "library_path", "load_library",
     "attn_launch_count", "attn_profile_start", "attn_profile_stop", "attn_decode_paged_noalloc",
     "attn_selftest_wait_timeout", "attn_merge_lse", "attn_paged_plan", "PagedPlan", "attn_qk_norm_rope",
-    "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_paged", "attn_tree_paged",
+    "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_paged", "attn_tree_paged", "attn_kv4_append", "attn_kv4_unpack", "attn_decode_kv4",
     "ATTN_OP_FWD", "ATTN_OP_FWD_VARLEN", "ATTN_OP_BWD", "ATTN_OP_BWD_VARLEN", "ATTN_OP_DECODE_PAGED",
-    "ATTN_OP_QK_NORM_ROPE_BWD", "ATTN_OP_TREE_PAGED",
+    "ATTN_OP_QK_NORM_ROPE_BWD", "ATTN_OP_TREE_PAGED", "ATTN_OP_DECODE_KV4",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -53,7 +57,7 @@ _lock = threading.Lock()
 _lib = None
 
 ATTN_OP_FWD, ATTN_OP_FWD_VARLEN, ATTN_OP_BWD, ATTN_OP_BWD_VARLEN, ATTN_OP_DECODE_PAGED = 0, 1, 2, 3, 4
-ATTN_OP_QK_NORM_ROPE_BWD, ATTN_OP_TREE_PAGED = 5, 6
+ATTN_OP_QK_NORM_ROPE_BWD, ATTN_OP_TREE_PAGED, ATTN_OP_DECODE_KV4 = 5, 6, 7
 STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ERR_MISALIGNED",
           4: "ATTN_ERR_WORKSPACE", 5: "ATTN_ERR_LAUNCH", 6: "ATTN_ERR_DEVICE_TIMEOUT", 7: "ATTN_ERR_DEVICE_BOUNDS",
           8: "ATTN_ERR_NO_DEVICE"}
@@ -83,6 +87,16 @@ def load_library():
         lib.attn_fwd.argtypes = [P, P, P, P, P, I, I, I, I, I, F, I, I, P, Z, P]
         lib.attn_fwd_varlen.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, P, Z, P]
         lib.attn_fwd_paged.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, I, P]
+        lib.attn_fwd_sink.argtypes = [P, P, P, P, P, I, I, I, I, I, F, I, I, I, P, Z, P]
+        lib.attn_fwd_varlen_sink.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, P, Z, P]
+        lib.attn_fwd_paged_sink.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, I, I, P]
+        lib.attn_bwd_sink.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, F, I, I, I, P, I, I, P, Z, P]
+        lib.attn_bwd_sink_workspace_size.argtypes = [I] * 8
+        lib.attn_bwd_sink_workspace_size.restype = Z
+        lib.attn_decode_paged_sink.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, I, P, Z, P]
+        for f in (lib.attn_fwd_sink, lib.attn_fwd_varlen_sink, lib.attn_fwd_paged_sink, lib.attn_bwd_sink,
+                  lib.attn_decode_paged_sink):
+            f.restype = I
         lib.attn_merge_lse.argtypes = [P, P, P, P, I, I, I, I, I, P]
         lib.attn_merge_lse.restype = I
         lib.attn_bwd.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, F, I, I, P, I, I, P, Z, P]
@@ -107,6 +121,11 @@ def load_library():
         lib.attn_qk_norm_rope_bwd.argtypes = [P] * 12 + [I] * 6 + [LL] * 4 + [F, F, I, I, P, Z, P]
         lib.attn_qk_norm_rope_paged.argtypes = [P] * 11 + [I] * 8 + [LL] * 3 + [F, F, I, I, P]
         lib.attn_tree_paged.argtypes = [P] * 10 + [I] * 10 + [F, I, P, Z, P]
+        lib.attn_kv4_append.argtypes = [P] * 4 + [I] * 5 + [LL, LL, P]
+        lib.attn_kv4_unpack.argtypes = [P] * 4 + [I] * 5 + [P]
+        lib.attn_decode_kv4.argtypes = [P] * 6 + [I] * 7 + [F, I, I, P, Z, P]
+        for f in (lib.attn_kv4_append, lib.attn_kv4_unpack, lib.attn_decode_kv4):
+            f.restype = I
         for f in (lib.attn_paged_plan, lib.attn_qk_norm_rope, lib.attn_qk_norm_rope_bwd, lib.attn_qk_norm_rope_paged,
                   lib.attn_tree_paged):
             f.restype = I
@@ -203,9 +222,21 @@ def _workspace(nbytes: int, device, zero: bool, key: str):
     return buf
 
 
+def _call_workspace(nbytes: int, device, stream):
+    """A workspace of one call, from the memory of its stream (or of the graph that it is captured into): calls on different
+    streams, or in different graphs, share none."""
+    import torch
+
+    if stream is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
 def attn_fwd(q, k, v, o=None, lse=None, *, causal: bool = True, window: int = 0, scale: float | None = None,
-             stream=None):
-    """Forward of causal (optionally sliding-window) GQA attention, dense [B, S, H, D] layout."""
+             stream=None, sink: int = 0):
+    """Forward of causal (optionally sliding-window) GQA attention, dense [B, S, H, D] layout. With a window the
+    sequence's first ``sink`` keys (0 to 128) stay visible to every later query."""
     import torch
 
     B, S, Hq, D = q.shape
@@ -216,15 +247,17 @@ def attn_fwd(q, k, v, o=None, lse=None, *, causal: bool = True, window: int = 0,
     if lse is None:
         lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
     with torch.cuda.device(q.device):  # the library works on the current device
-        rc = load_library().attn_fwd(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse), B, Hq, Hkv,
-                                     S, D, scale, int(causal), int(window), None, 0, _stream_ptr(stream, q.device))
+        rc = load_library().attn_fwd_sink(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse), B, Hq, Hkv,
+                                          S, D, scale, int(causal), int(window), int(sink), None, 0,
+                                          _stream_ptr(stream, q.device))
     _check(rc, "attn_fwd")
     return o, lse
 
 
 def attn_fwd_varlen(q, k, v, cu_seqlens, max_seqlen: int, o=None, lse=None, *, causal: bool = True, window: int = 0,
-                    scale: float | None = None, stream=None):
-    """Forward over packed sequences: q [T, Hq, D], k/v [T, Hkv, D], cu_seqlens int32 [n+1] on the device."""
+                    scale: float | None = None, stream=None, sink: int = 0):
+    """Forward over packed sequences: q [T, Hq, D], k/v [T, Hkv, D], cu_seqlens int32 [n+1] on the device; ``sink`` as in
+    attn_fwd, for each sequence."""
     import torch
 
     T, Hq, D = q.shape
@@ -237,17 +270,18 @@ def attn_fwd_varlen(q, k, v, cu_seqlens, max_seqlen: int, o=None, lse=None, *, c
     if lse is None:
         lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
     with torch.cuda.device(q.device):  # the library works on the current device
-        rc = load_library().attn_fwd_varlen(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse),
+        rc = load_library().attn_fwd_varlen_sink(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse),
                                             _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, int(max_seqlen), Hq, Hkv, D,
-                                            scale, int(causal), int(window), None, 0, _stream_ptr(stream, q.device))
+                                            scale, int(causal), int(window), int(sink), None, 0, _stream_ptr(stream, q.device))
     _check(rc, "attn_fwd_varlen")
     return o, lse
 
 
 def attn_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q_len: int, o=None, lse=None, *,
-                   causal: bool = True, window: int = 0, scale: float | None = None, stream=None):
+                   causal: bool = True, window: int = 0, scale: float | None = None, stream=None, sink: int = 0):
     """Chunked prefill: q [T,Hq,D] new tokens packed by cu_q, caches [pages,16,Hkv,D], block_table int32
-    [R,max_pages], seq_lens int32 [R] (cached tokens including the new ones), cu_q int32 [R+1]."""
+    [R,max_pages], seq_lens int32 [R] (cached tokens including the new ones), cu_q int32 [R+1]; ``sink`` as in
+    attn_fwd, for each request."""
     import torch
 
     T, Hq, D = q.shape
@@ -261,10 +295,10 @@ def attn_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q_len: 
     if lse is None:
         lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
     with torch.cuda.device(q.device):  # the library works on the current device
-        rc = load_library().attn_fwd_paged(
+        rc = load_library().attn_fwd_paged_sink(
             _bf16(q, "q"), _bf16(k_cache, "k_cache"), _bf16(v_cache, "v_cache"), _ptr(block_table), _ptr(seq_lens),
             _ptr(cu_q), _bf16(o, "o"), _ptr(lse), cu_q.numel() - 1, T, int(max_q_len), Hq, Hkv, D, page_size,
-            block_table.shape[1], num_pages, scale, int(causal), int(window), _stream_ptr(stream, q.device))
+            block_table.shape[1], num_pages, scale, int(causal), int(window), int(sink), _stream_ptr(stream, q.device))
     _check(rc, "attn_fwd_paged")
     return o, lse
 
@@ -297,8 +331,8 @@ def attn_merge_lse(o_parts, lse_parts, o=None, lse=None, *, stream=None):
 
 
 def attn_bwd(q, k, v, o, lse, dO, dq=None, dk=None, dv=None, *, causal: bool = True, window: int = 0,
-             scale: float | None = None, cu_seqlens=None, max_seqlen: int = 0, workspace=None, stream=None):
-    """Gradients (dQ, dK, dV). Dense [B,S,H,D] when cu_seqlens is None, else packed [T,H,D]."""
+             scale: float | None = None, cu_seqlens=None, max_seqlen: int = 0, workspace=None, stream=None, sink: int = 0):
+    """Gradients (dQ, dK, dV). Dense [B,S,H,D] when cu_seqlens is None, else packed [T,H,D]; ``sink`` as in the forward."""
     import torch
 
     if cu_seqlens is None:
@@ -314,12 +348,15 @@ def attn_bwd(q, k, v, o, lse, dO, dq=None, dk=None, dv=None, *, causal: bool = T
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     need = attn_workspace_size(ATTN_OP_BWD if cu_seqlens is None else ATTN_OP_BWD_VARLEN, B, Hq, Hkv, S, D, nseq)
+    if sink and window > 0:
+        need = int(load_library().attn_bwd_sink_workspace_size(B, Hq, Hkv, S, D, nseq, int(window), int(sink)))
+        workspace = _call_workspace(need, q.device, stream) if workspace is None else workspace
     if workspace is None:
         workspace = _workspace(need, q.device, False, "bwd")
     with torch.cuda.device(q.device):  # the library works on the current device
-        rc = load_library().attn_bwd(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse),
+        rc = load_library().attn_bwd_sink(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse),
                                      _bf16(dO, "dO"), _bf16(dq, "dQ"), _bf16(dk, "dK"), _bf16(dv, "dV"), B, Hq, Hkv, S, D,
-                                     scale, int(causal), int(window), _ptr(cu_seqlens), nseq, int(max_seqlen),
+                                     scale, int(causal), int(window), int(sink), _ptr(cu_seqlens), nseq, int(max_seqlen),
                                      _ptr(workspace), workspace.numel() * workspace.element_size(),
                                      _stream_ptr(stream, q.device))
     _check(rc, "attn_bwd")
@@ -327,9 +364,9 @@ def attn_bwd(q, k, v, o, lse, dO, dq=None, dk=None, dv=None, *, causal: bool = T
 
 
 def attn_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=None, *, scale: float | None = None,
-                      window: int = 0, workspace=None, stream=None):
+                      window: int = 0, workspace=None, stream=None, sink: int = 0):
     """Single-token decode: q [B,Hq,D], caches [pages,16,Hkv,D], block_table int32 [B,max_pages], seq_lens int32 [B];
-    window > 0: the query sees only the last `window` keys."""
+    window > 0: the query sees only the last `window` keys, and the request's first `sink` ones (0 to 128)."""
     import torch
 
     B, Hq, D = q.shape
@@ -343,13 +380,15 @@ def attn_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=No
     if lse is None:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     need = attn_workspace_size(ATTN_OP_DECODE_PAGED, B, Hq, Hkv, 0, D)
+    if workspace is None and sink and window > 0:
+        workspace = _call_workspace(need, q.device, stream)
     if workspace is None:
         workspace = _workspace(need, q.device, False, "decode")
     with torch.cuda.device(q.device):  # the library works on the current device
-        rc = load_library().attn_decode_paged(_bf16(q, "q"), _bf16(k_cache, "k_cache"), _bf16(v_cache, "v_cache"),
+        rc = load_library().attn_decode_paged_sink(_bf16(q, "q"), _bf16(k_cache, "k_cache"), _bf16(v_cache, "v_cache"),
                                               _ptr(block_table), _ptr(seq_lens), _bf16(o, "o"), _ptr(lse), B, Hq, Hkv, D,
                                               page_size, block_table.shape[1], num_pages, scale, int(window),
-                                              _ptr(workspace),
+                                              int(sink), _ptr(workspace),
                                               workspace.numel() * workspace.element_size(), _stream_ptr(stream, q.device))
     _check(rc, "attn_decode_paged")
     return o, lse
@@ -483,3 +522,27 @@ def attn_tree_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, tree_mask,
         scale = 1.0 / math.sqrt(q.shape[-1])
     return (_bound or _native()).tree_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, tree_mask, max_q_len, o, lse, positions,
                                           window, scale, workspace, stream)
+
+
+def attn_kv4_append(k, v, slots, kv_cache, *, page_size: int = 16, stream=None) -> None:
+    """Keys and values into a paged cache in 4 bits, in place: k, v [T,Hkv,D] (or [B,S,H,D]) bf16, possibly slices of a fused
+    projection, slots int32 [T] (of attn_paged_plan; -1: padding), kv_cache uint8 [pages,Hkv,18,D].
+
+    32 dims of a token are held as n * s, n = -8 .. 7 and s a bf16 number of 5 significant bits; see include/attn.h.
+    """
+    (_bound or _native()).kv4_append(k, v, slots, kv_cache, page_size, stream)
+
+
+def attn_kv4_unpack(kv_cache, pages, k_pages=None, v_pages=None, *, page_size: int = 16, stream=None):
+    """Pages of a 4-bit cache as bf16, exactly -> (k_pages, v_pages) [n,16,Hkv,D]: what attn_fwd_paged and attn_tree_paged read, with a
+    block table of 0 .. n-1. pages int32 [n] (-1: left as it is)."""
+    return (_bound or _native()).kv4_unpack(kv_cache, pages, k_pages, v_pages, page_size, stream)
+
+
+def attn_decode_kv4(q, kv_cache, block_table, seq_lens, o=None, lse=None, *, scale: float | None = None, window: int = 0, sink: int = 0,
+                    page_size: int = 16, workspace=None, stream=None):
+    """Single-token decode over a 4-bit cache -> (o, lse[B,Hq]): q [B,Hq,D], kv_cache uint8 [pages,Hkv,18,D], block_table int32
+    [B,max_pages], seq_lens int32 [B]; window > 0: only the last `window` keys are seen, and the first `sink` ones."""
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    return (_bound or _native()).decode_kv4(q, kv_cache, block_table, seq_lens, o, lse, scale, window, sink, page_size, workspace, stream)

@@ -133,6 +133,10 @@ int check_common(int Hq, int Hkv, float scale, int causal, int window) {
     return ATTN_OK;
 }
 
+int check_sink(int sink) { return sink < 0 ? ATTN_ERR_INVALID_ARG : sink > ATTN_MAX_SINK ? ATTN_ERR_UNSUPPORTED : ATTN_OK; }
+// A window that no query of a sequence of at most `len` reaches the end of hides nothing.
+int reaching(int window, long long len) { return window >= len ? 0 : window; }
+
 int check_prefill_shape(long long rows, int Hq, int Hkv, int D, int S) {
     if (D != 64 && D != 128 && D != 256 && D != 512) return ATTN_ERR_UNSUPPORTED;
     if (S > 65535LL * 128) return ATTN_ERR_UNSUPPORTED;
@@ -146,6 +150,14 @@ int fwd_splits(int D) { return D > 256 ? D / 256 : 1; }
 
 size_t bwd_ws(long long rows, int Hq, int D) {
     return align256((size_t)rows * Hq * D * 4) + align256((size_t)rows * Hq * 4);
+}
+// Query tiles of a slice of the far queries: as many as a block of the window has, but not so few that the parts' bytes
+// (two rows of fp32 for each sink, KV head and slice) would count beside the queries'.
+int sink_slice_tiles(int window) { return (window + 127) / 128 + 1 > 8 ? (window + 127) / 128 + 1 : 8; }
+// Bytes of the parts; SinkSplit says how they lie.
+size_t sink_ws(long long rows, long long nseq, int Hkv, int D, int window, int sink) {
+    if (window <= 0 || sink <= 0) return 0;
+    return align256((size_t)(rows / (sink_slice_tiles(window) * 128LL) + 2 * nseq) * Hkv * 2 * sink * D * 4);
 }
 
 // CTAs per KV-head block of a decode launch at most: the blocks share decode_max_grid() CTAs.
@@ -197,6 +209,13 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 size_t norm_rope_bwd_ws(int D) { return align256((size_t)attn::norm_rope_bwd_max_ctas() * 2 * D * 4); }
 
+bool kv4_dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
+constexpr int kKv4MaxGrid = 256;  // blocks of a 4-bit decode at most
+size_t kv4_ws(int B, int Hq, int Hkv, int D) {
+    if (B < 0 || B > 4096 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 8 || !kv4_dim_ok(D)) return 0;
+    return align256(attn::decode_kv4_workspace_bytes(B, Hq / Hkv, D, kKv4MaxGrid));
+}
+
 bool tree_shape_ok(int Hq, int Hkv, int max_q, int D) {
     return Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && Hq / Hkv <= 128 && Hkv <= 256 && max_q >= 0 && max_q <= 256 && head_dim_ok(D);
 }
@@ -225,7 +244,7 @@ int check_token_stride(long long stride, int H, int D, bool out) {
 
 int fwd_common(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_bf16* o, float* lse,
                const int32_t* cu, int nseq, int S, long long rows, int batch_dim, int Hq, int Hkv, int D, float scale,
-               int window, void* stream) {
+               int window, int sink, void* stream) {
     const DeviceInfo* dev = device_info();
     if (!dev) return ATTN_ERR_NO_DEVICE;
     attn::FwdLaunch L;
@@ -240,7 +259,7 @@ int fwd_common(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_
     }
     L.o = o, L.lse = lse, L.cu_seqlens = cu, L.status = dev->status;
     L.nseq = nseq, L.Hq = Hq, L.Hkv = Hkv, L.S = S, L.D = D, L.total_rows = (int)rows, L.window = window;
-    L.scale = scale;
+    L.scale = scale, L.sink = sink;
     return attn::launch_fwd(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
@@ -366,50 +385,79 @@ size_t attn_workspace_size(int op, int B, int Hq, int Hkv, int S, int D, int num
         case ATTN_OP_BWD_VARLEN: return bwd_ws((long long)B * S, Hq, D);
         case ATTN_OP_DECODE_PAGED: return decode_ws(B, Hq, Hkv, D);
         case ATTN_OP_QK_NORM_ROPE_BWD: return head_dim_ok(D) ? norm_rope_bwd_ws(D) : 0;
+        case ATTN_OP_DECODE_KV4: return kv4_ws(B, Hq, Hkv, D);
         case ATTN_OP_TREE_PAGED: return tree_shape_ok(Hq, Hkv, S, D) ? tree_ws(Hq, Hkv, S, D) : 0;
         default: return 0;
     }
 }
 
+size_t attn_bwd_sink_workspace_size(int B, int Hq, int Hkv, int S, int D, int num_seqs, int window, int sink) {
+    if (B < 0 || Hq < 0 || Hkv < 0 || S < 0 || D < 0 || num_seqs < 0) return 0;
+    const long long rows = (long long)B * S;
+    return bwd_ws(rows, Hq, D) + sink_ws(rows, num_seqs > B ? num_seqs : B, Hkv, D, window, sink);
+}
+
 int attn_fwd(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_bf16* o, float* lse, int B, int Hq,
              int Hkv, int S, int D, float scale, int causal, int window, void* workspace, size_t workspace_bytes,
              void* stream) {
+    return attn_fwd_sink(q, k, v, o, lse, B, Hq, Hkv, S, D, scale, causal, window, 0, workspace, workspace_bytes, stream);
+}
+
+int attn_fwd_sink(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_bf16* o, float* lse, int B, int Hq,
+                  int Hkv, int S, int D, float scale, int causal, int window, int sink, void* workspace,
+                  size_t workspace_bytes, void* stream) {
     (void)workspace, (void)workspace_bytes;
     if (!q || !k || !v || !o || !lse || B < 0 || S < 0) return ATTN_ERR_INVALID_ARG;
     int st = check_common(Hq, Hkv, scale, causal, window);
-    if (st) return st;
+    if (st || (st = check_sink(sink))) return st;
     const long long rows = (long long)B * S;
     if ((st = check_prefill_shape(rows, Hq, Hkv, D, S))) return st;
     if (B > 65535 / fwd_splits(D)) return ATTN_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse)) return ATTN_ERR_MISALIGNED;
     if (rows == 0) return ATTN_OK;
-    return fwd_common(q, k, v, o, lse, nullptr, B, S, rows, B, Hq, Hkv, D, scale, window, stream);
+    return fwd_common(q, k, v, o, lse, nullptr, B, S, rows, B, Hq, Hkv, D, scale, reaching(window, S), sink, stream);
 }
 
 int attn_fwd_varlen(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_bf16* o, float* lse,
                     const int32_t* cu_seqlens, int num_seqs, int total_tokens, int max_seqlen, int Hq, int Hkv, int D,
                     float scale, int causal, int window, void* workspace, size_t workspace_bytes, void* stream) {
+    return attn_fwd_varlen_sink(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, max_seqlen, Hq, Hkv, D, scale, causal,
+                                window, 0, workspace, workspace_bytes, stream);
+}
+
+int attn_fwd_varlen_sink(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_bf16* o, float* lse,
+                         const int32_t* cu_seqlens, int num_seqs, int total_tokens, int max_seqlen, int Hq, int Hkv, int D,
+                         float scale, int causal, int window, int sink, void* workspace, size_t workspace_bytes,
+                         void* stream) {
     (void)workspace, (void)workspace_bytes;
     if (!q || !k || !v || !o || !lse || !cu_seqlens || num_seqs < 0 || total_tokens < 0 || max_seqlen < 0)
         return ATTN_ERR_INVALID_ARG;
     int st = check_common(Hq, Hkv, scale, causal, window);
-    if (st) return st;
+    if (st || (st = check_sink(sink))) return st;
     if ((st = check_prefill_shape(total_tokens, Hq, Hkv, D, max_seqlen))) return st;
     if (num_seqs > 65535 / fwd_splits(D)) return ATTN_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse)) return ATTN_ERR_MISALIGNED;
     if (num_seqs == 0 || total_tokens == 0 || max_seqlen == 0) return ATTN_OK;
-    return fwd_common(q, k, v, o, lse, cu_seqlens, num_seqs, max_seqlen, total_tokens, 1, Hq, Hkv, D, scale, window,
-                      stream);
+    return fwd_common(q, k, v, o, lse, cu_seqlens, num_seqs, max_seqlen, total_tokens, 1, Hq, Hkv, D, scale,
+                      reaching(window, max_seqlen), sink, stream);
 }
 
 int attn_fwd_paged(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache, const int32_t* block_table,
                    const int32_t* seq_lens, const int32_t* cu_q, attn_bf16* o, float* lse, int num_reqs, int total_q,
                    int max_q_len, int Hq, int Hkv, int D, int page_size, int max_pages_per_seq, int num_pages,
                    float scale, int causal, int window, void* stream) {
+    return attn_fwd_paged_sink(q, k_cache, v_cache, block_table, seq_lens, cu_q, o, lse, num_reqs, total_q, max_q_len, Hq,
+                               Hkv, D, page_size, max_pages_per_seq, num_pages, scale, causal, window, 0, stream);
+}
+
+int attn_fwd_paged_sink(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache, const int32_t* block_table,
+                        const int32_t* seq_lens, const int32_t* cu_q, attn_bf16* o, float* lse, int num_reqs, int total_q,
+                        int max_q_len, int Hq, int Hkv, int D, int page_size, int max_pages_per_seq, int num_pages,
+                        float scale, int causal, int window, int sink, void* stream) {
     if (num_reqs < 0 || total_q < 0 || max_q_len < 0 || max_pages_per_seq < 0 || num_pages < 0 || page_size <= 0)
         return ATTN_ERR_INVALID_ARG;
     int st = check_common(Hq, Hkv, scale, causal, window);
-    if (st) return st;
+    if (st || (st = check_sink(sink))) return st;
     if ((st = check_prefill_shape(total_q, Hq, Hkv, D, max_q_len))) return st;
     if (page_size != 16 || num_reqs > 65535 / fwd_splits(D) || max_pages_per_seq > (1 << 24)) return ATTN_ERR_UNSUPPORTED;
     if (num_reqs == 0 || total_q == 0 || max_q_len == 0) return ATTN_OK;  // nothing to read or write
@@ -432,7 +480,7 @@ int attn_fwd_paged(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16
     }
     L.o = o, L.lse = lse, L.cu_seqlens = nullptr, L.status = dev->status;
     L.nseq = num_reqs, L.Hq = Hq, L.Hkv = Hkv, L.S = max_q_len, L.D = D, L.total_rows = total_q, L.window = window;
-    L.scale = scale;
+    L.scale = scale, L.sink = sink;
     L.block_table = block_table, L.seq_lens = seq_lens, L.cu_q = cu_q;
     L.max_pages = max_pages_per_seq, L.num_pages = num_pages;
     return attn::launch_fwd(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
@@ -442,9 +490,17 @@ int attn_bwd(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, const a
              const attn_bf16* dO, attn_bf16* dQ, attn_bf16* dK, attn_bf16* dV, int B, int Hq, int Hkv, int S, int D,
              float scale, int causal, int window, const int32_t* cu_seqlens, int num_seqs, int max_seqlen,
              void* workspace, size_t workspace_bytes, void* stream) {
+    return attn_bwd_sink(q, k, v, o, lse, dO, dQ, dK, dV, B, Hq, Hkv, S, D, scale, causal, window, 0, cu_seqlens, num_seqs,
+                         max_seqlen, workspace, workspace_bytes, stream);
+}
+
+int attn_bwd_sink(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, const attn_bf16* o, const float* lse,
+                  const attn_bf16* dO, attn_bf16* dQ, attn_bf16* dK, attn_bf16* dV, int B, int Hq, int Hkv, int S, int D,
+                  float scale, int causal, int window, int sink, const int32_t* cu_seqlens, int num_seqs, int max_seqlen,
+                  void* workspace, size_t workspace_bytes, void* stream) {
     if (!q || !k || !v || !o || !lse || !dO || !dQ || !dK || !dV || B < 0 || S < 0) return ATTN_ERR_INVALID_ARG;
     int st = check_common(Hq, Hkv, scale, causal, window);
-    if (st) return st;
+    if (st || (st = check_sink(sink))) return st;
     const bool varlen = cu_seqlens != nullptr;
     if (varlen && (B != 1 || num_seqs < 0 || max_seqlen < 0)) return ATTN_ERR_INVALID_ARG;
     const long long rows = (long long)B * S;
@@ -454,7 +510,16 @@ int attn_bwd(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, const a
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(dO) ||
         !aligned16(dQ) || !aligned16(dK) || !aligned16(dV))
         return ATTN_ERR_MISALIGNED;
-    const size_t need = bwd_ws(rows, Hq, D);
+    window = reaching(window, grid_len);
+    attn::SinkSplit split = {};
+    if (window > 0 && sink > 0) {
+        split.sink = sink, split.tiles = sink_slice_tiles(window);
+        const int near = window + 127 < grid_len ? (window + 127 + 127) / 128 : (grid_len + 127) / 128;
+        split.slices = ((grid_len + 127) / 128 - near + split.tiles - 1) / split.tiles;
+        if (split.slices + (grid_len + 127) / 128 > 65535 || Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+    }
+    const long long nseq = varlen ? num_seqs : B;
+    const size_t need = bwd_ws(rows, Hq, D) + (split.slices > 0 ? sink_ws(rows, nseq, Hkv, D, window, sink) : 0);
     if (rows > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
     if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return ATTN_ERR_MISALIGNED;
     if (rows == 0 || (varlen && (num_seqs == 0 || max_seqlen == 0))) return ATTN_OK;
@@ -475,6 +540,8 @@ int attn_bwd(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, const a
     L.dq_acc = reinterpret_cast<float*>(ws);
     if (!make_map_f32(&L.tdq, L.dq_acc, D, Hq, map_rows, batch)) return ATTN_ERR_LAUNCH;
     L.delta = reinterpret_cast<float*>(ws + align256((size_t)rows * Hq * D * 4));
+    L.sink = split;
+    L.sink.part = reinterpret_cast<float*>(ws + bwd_ws(rows, Hq, D));
     L.cu_seqlens = cu_seqlens, L.status = dev->status;
     L.nseq = varlen ? num_seqs : B;
     L.Hq = Hq, L.Hkv = Hkv, L.S = grid_len, L.D = D, L.total_rows = (int)rows, L.window = window, L.scale = scale;
@@ -485,10 +552,19 @@ int attn_decode_paged(const attn_bf16* q, const attn_bf16* k_cache, const attn_b
                       const int32_t* block_table, const int32_t* seq_lens, attn_bf16* o, float* lse, int B, int Hq,
                       int Hkv, int D, int page_size, int max_pages_per_seq, int num_pages, float scale, int window,
                       void* workspace, size_t workspace_bytes, void* stream) {
+    return attn_decode_paged_sink(q, k_cache, v_cache, block_table, seq_lens, o, lse, B, Hq, Hkv, D, page_size,
+                                  max_pages_per_seq, num_pages, scale, window, 0, workspace, workspace_bytes, stream);
+}
+
+int attn_decode_paged_sink(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
+                           const int32_t* block_table, const int32_t* seq_lens, attn_bf16* o, float* lse, int B, int Hq,
+                           int Hkv, int D, int page_size, int max_pages_per_seq, int num_pages, float scale, int window,
+                           int sink, void* workspace, size_t workspace_bytes, void* stream) {
     if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o || !lse) return ATTN_ERR_INVALID_ARG;
     if (B < 0 || max_pages_per_seq < 0 || num_pages < 0 || page_size <= 0 || window < 0) return ATTN_ERR_INVALID_ARG;
     if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+    if (const int st = check_sink(sink)) return st;
     const int G = Hq / Hkv;
     if (!decode_shape_ok(Hq, Hkv, D) || page_size != 16 || Hkv > 256 || B > 4096 || num_pages > (1 << 26))
         return ATTN_ERR_UNSUPPORTED;
@@ -516,7 +592,7 @@ int attn_decode_paged(const attn_bf16* q, const attn_bf16* k_cache, const attn_b
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     L.part = reinterpret_cast<float*>(ws);
     L.B = B, L.Hq = Hq, L.Hkv = Hkv, L.D = D, L.max_pages = max_pages_per_seq, L.num_pages = num_pages;
-    L.scale = scale, L.window = window;
+    L.scale = scale, L.window = window, L.sink = sink;
     // the head blocks share the SMs: each block's pages are split over sms / nhb CTAs
     long long units = (long long)B * (max_pages_per_seq > 0 ? max_pages_per_seq : 1);
     int grid = dev->sms / nhb;
@@ -704,6 +780,69 @@ int attn_tree_paged(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf1
     L.R = num_reqs, L.T = total_q, L.max_q = max_q_len, L.words = mask_words, L.Hq = Hq, L.Hkv = Hkv, L.D = D;
     L.max_pages = max_pages_per_seq, L.num_pages = num_pages, L.window = window, L.sms = dev->sms, L.scale = scale;
     return attn::launch_tree_paged(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+int attn_kv4_append(const attn_bf16* k, const attn_bf16* v, const int32_t* slots, uint8_t* kv_cache, int T, int Hkv, int D,
+                    int page_size, int num_pages, long long k_stride, long long v_stride, void* stream) {
+    if (T < 0 || Hkv < 1 || num_pages < 0 || page_size <= 0) return ATTN_ERR_INVALID_ARG;
+    if (!kv4_dim_ok(D) || page_size != 16 || Hkv > 256 || num_pages > (1 << 26) || (long long)T * Hkv > 0x7fffffffLL)
+        return ATTN_ERR_UNSUPPORTED;
+    int st;
+    if ((st = check_token_stride(k_stride, Hkv, D, false)) || (st = check_token_stride(v_stride, Hkv, D, false))) return st;
+    if (T == 0) return ATTN_OK;
+    if (!k || !v || !slots || !kv_cache) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned4(slots) || !aligned16(kv_cache)) return ATTN_ERR_MISALIGNED;
+    const DeviceInfo* dev = device_info();
+    if (!dev) return ATTN_ERR_NO_DEVICE;
+    attn::Kv4Launch L;
+    std::memset(&L, 0, sizeof(L));
+    L.k = k, L.v = v, L.slots = slots, L.cache = kv_cache, L.status = dev->status;
+    L.k_stride = k_stride, L.v_stride = v_stride, L.n = T, L.Hkv = Hkv, L.D = D, L.num_pages = num_pages;
+    return attn::launch_kv4_append(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+int attn_kv4_unpack(const uint8_t* kv_cache, const int32_t* pages, attn_bf16* k_pages, attn_bf16* v_pages, int n, int Hkv,
+                    int D, int page_size, int num_pages, void* stream) {
+    if (n < 0 || Hkv < 1 || num_pages < 0 || page_size <= 0) return ATTN_ERR_INVALID_ARG;
+    if (!kv4_dim_ok(D) || page_size != 16 || Hkv > 256 || num_pages > (1 << 26) || (long long)n * 8 * Hkv > 0x7fffffffLL)
+        return ATTN_ERR_UNSUPPORTED;
+    if (n == 0) return ATTN_OK;
+    if (!kv_cache || !pages || !k_pages || !v_pages) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(kv_cache) || !aligned4(pages) || !aligned16(k_pages) || !aligned16(v_pages)) return ATTN_ERR_MISALIGNED;
+    const DeviceInfo* dev = device_info();
+    if (!dev) return ATTN_ERR_NO_DEVICE;
+    attn::Kv4Launch L;
+    std::memset(&L, 0, sizeof(L));
+    L.cache = const_cast<uint8_t*>(kv_cache), L.pages = pages, L.k_out = k_pages, L.v_out = v_pages, L.status = dev->status;
+    L.n = n, L.Hkv = Hkv, L.D = D, L.num_pages = num_pages;
+    return attn::launch_kv4_unpack(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
+}
+
+int attn_decode_kv4(const attn_bf16* q, const uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                    attn_bf16* o, float* lse, int B, int Hq, int Hkv, int D, int page_size, int max_pages_per_seq,
+                    int num_pages, float scale, int window, int sink, void* workspace, size_t workspace_bytes, void* stream) {
+    if (B < 0 || max_pages_per_seq < 0 || num_pages < 0 || page_size <= 0) return ATTN_ERR_INVALID_ARG;
+    int st = check_common(Hq, Hkv, scale, 1, window);
+    if (st || (st = check_sink(sink))) return st;
+    if (!kv4_dim_ok(D) || Hq / Hkv > 8 || page_size != 16 || Hkv > 256 || B > 4096 || num_pages > (1 << 26) ||
+        (long long)B * max_pages_per_seq * Hkv > 0x7fffffffLL)
+        return ATTN_ERR_UNSUPPORTED;
+    if (B == 0) return ATTN_OK;
+    if (!q || !seq_lens || !o || !lse || (max_pages_per_seq > 0 && (!kv_cache || !block_table))) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(o) || !aligned4(lse) || !aligned4(block_table) || !aligned4(seq_lens))
+        return ATTN_ERR_MISALIGNED;
+    if (!workspace || workspace_bytes < kv4_ws(B, Hq, Hkv, D)) return ATTN_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return ATTN_ERR_MISALIGNED;
+    const DeviceInfo* dev = device_info();
+    if (!dev) return ATTN_ERR_NO_DEVICE;
+    attn::DecodeKv4Launch L;
+    std::memset(&L, 0, sizeof(L));
+    L.q = q, L.cache = kv_cache, L.block_table = block_table, L.seq_lens = seq_lens, L.o = o, L.lse = lse;
+    L.status = dev->status, L.workspace = workspace;
+    L.B = B, L.Hq = Hq, L.Hkv = Hkv, L.D = D, L.max_pages = max_pages_per_seq, L.num_pages = num_pages;
+    L.window = window, L.sink = sink, L.scale = scale;
+    L.grid = dev->sms < kKv4MaxGrid ? dev->sms : kKv4MaxGrid;
+    return attn::launch_decode_kv4(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 
 int attn_selftest_wait_timeout(int limit_ms, void* stream) {

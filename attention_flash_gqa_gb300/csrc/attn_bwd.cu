@@ -83,6 +83,7 @@ struct BwdArgs {
     unsigned* status;
     int Hq, Hkv, S, window, T;
     float scale, scale_log2;
+    SinkSplit sink;
 };
 
 template <int D>
@@ -98,7 +99,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int share = s_role ? (int)rank : (int)rank - C::NHALF;  // query share of the role work
     const int c0 = (int)rank * 128;  // this CTA's column slice of D
     const int seq = blockIdx.y;
-    const int kv_tile = blockIdx.z;  // tile 0 sees the most queries: launched first
+    // the first a.sink.slices clusters share out the queries that see of tile 0 its sinks alone (the window has left
+    // it); behind them a cluster for each key tile, tile 0 first: it sees the most queries
+    const int slice = (int)blockIdx.z - a.sink.slices;
+    const bool far = slice < 0;
+    const int kv_tile = far ? 0 : slice;
     int seq_start = 0, L = a.S, bcoord = seq;
     if (a.cu_seqlens) {
         seq_start = a.cu_seqlens[seq];
@@ -106,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bcoord = 0;
         // every CTA of the cluster reads the same slice and returns together, before any barrier
         if (!varlen_seq_ok(seq_start, L, a.T, a.S)) {
-            if (threadIdx.x == 0 && blockIdx.x == 0 && kv_tile == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
+            if (threadIdx.x == 0 && blockIdx.x == 0 && slice == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
             return;
         }
     }
@@ -114,8 +119,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (k0 >= L) return;  // the same for every CTA of the cluster
     const int G = a.Hq / a.Hkv;
     const int q_last = a.window > 0 ? min(L, k0 + kB - 1 + a.window) : L;  // exclusive bound on queries
-    const int i_begin = k0 / kB, i_end = (q_last + kB - 1) / kB;
+    const int i_near = (q_last + kB - 1) / kB;
+    const int i_begin = far ? i_near + (int)blockIdx.z * a.sink.tiles : k0 / kB;
+    const int i_end = far ? min(i_begin + a.sink.tiles, (L + kB - 1) / kB) : i_near;
     const int n_qt = i_end - i_begin;
+    if (n_qt <= 0) return;  // no such slice (the same for every CTA of the cluster)
+    // whether this cluster's dK and dV of the sinks are one part of several
+    const bool parted = a.sink.slices > 0 && kv_tile == 0 && i_near * kB < L;
     const int n = G * n_qt;    // steps: (head, query tile)
     const int np = (n + 1) / 2;  // pair-steps: steps 2T and 2T + 1 (the latter absent when n is odd)
 
@@ -459,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // (c_hi < c_lo when no key of the tile is allowed: every key is masked)
                     const int c_hi = min(kB - 1, min(qa, L - 1) - k0);
                     const int c_lo = a.window > 0 ? max(0, qa - a.window + 1 - k0) : 0;
+                    const int c_sink = a.sink.sink - k0;  // keys below it are visible past the window too
                     const bool edge = c_lo > 0 || c_hi < kB - 1;
                     uint32_t rr[128];
 #pragma unroll
@@ -473,8 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float p0 = fast_exp2(fmaf(__uint_as_float(rr[c]), a.scale_log2, -v));
                             float p1 = fast_exp2(fmaf(__uint_as_float(rr[c + 1]), a.scale_log2, -v));
                             if (decltype(masked)::value) {
-                                if (c < c_lo || c > c_hi) p0 = 0.f;
-                                if (c + 1 < c_lo || c + 1 > c_hi) p1 = 0.f;
+                                if ((c < c_lo && c >= c_sink) || c > c_hi) p0 = 0.f;
+                                if ((c + 1 < c_lo && c + 1 >= c_sink) || c + 1 > c_hi) p1 = 0.f;
                             }
                             pk[c / 2] = pack_bf16x2(p0, p1);
                         }
@@ -548,13 +559,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t row = (size_t)(a.cu_seqlens ? seq_start + kabs : seq * a.S + kabs) * a.Hkv + g;
             uint16_t* dv_row = a.dV + row * D + c0;
             uint16_t* dk_row = a.dK + row * D + c0;
+            const bool part_row = parted && kabs < a.sink.sink;
+            float* part = parted ? a.sink.row(seq, a.cu_seqlens ? seq_start : seq * a.S, far ? 1 + blockIdx.z : 0, g, a.Hkv, j, D) + c0
+                                 : nullptr;
 #pragma unroll 1
             for (int c4 = 0; c4 < 4; ++c4) {
                 uint32_t rv[32], rk[32];
                 tmem_ld32(tDV + c4 * 32 + lane_base, rv);
                 tmem_ld32(tDK + c4 * 32 + lane_base, rk);
                 tmem_ld_wait();
-                if (key_ok) {
+                if (key_ok && part_row) {
+                    float* pv = part + c4 * 32;
+                    float* pk = pv + (size_t)a.sink.sink * D;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        *reinterpret_cast<float4*>(pv + e) = make_float4(__uint_as_float(rv[e]), __uint_as_float(rv[e + 1]),
+                                                                         __uint_as_float(rv[e + 2]), __uint_as_float(rv[e + 3]));
+                        *reinterpret_cast<float4*>(pk + e) =
+                            make_float4(__uint_as_float(rk[e]) * a.scale, __uint_as_float(rk[e + 1]) * a.scale,
+                                        __uint_as_float(rk[e + 2]) * a.scale, __uint_as_float(rk[e + 3]) * a.scale);
+                    }
+                } else if (key_ok && !far) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint4 wv, wk;
@@ -658,6 +683,38 @@ __global__ void __launch_bounds__(256) bwd_finalize_kernel(const float* __restri
     }
 }
 
+// dK and dV of the sinks of the sequences whose far queries were shared out: the sum of the near part and the slices',
+// in that order, whatever order they were computed in. A block owns one (sequence, KV head, sink, 8 dims a thread);
+// reading the parts, a few KB a block, is all that it takes.
+__global__ void __launch_bounds__(64) bwd_sink_sum_kernel(SinkSplit sk, uint16_t* __restrict__ dK, uint16_t* __restrict__ dV,
+                                                          const int32_t* __restrict__ cu, int S, int T, int Hkv, int D, int window) {
+    const int j = blockIdx.x, g = blockIdx.y, seq = blockIdx.z, d = 8 * threadIdx.x;
+    int start = seq * S, L = S;
+    if (cu) {
+        start = cu[seq], L = cu[seq + 1] - start;
+        if (!varlen_seq_ok(start, L, T, S)) return;
+    }
+    const int i_near = (min(L, kB - 1 + window) + kB - 1) / kB, n_qt = (L + kB - 1) / kB;
+    if (i_near >= n_qt || j >= L || d >= D) return;
+    const int parts = 1 + (n_qt - i_near + sk.tiles - 1) / sk.tiles;
+    float v[8] = {}, k[8] = {};
+    for (int p = 0; p < parts; ++p) {
+        const float* row = sk.row(seq, start, p, g, Hkv, j, D) + d;
+        const float* rowk = row + (size_t)sk.sink * D;
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(row + e), b = *reinterpret_cast<const float4*>(rowk + e);
+            v[e] += a.x, v[e + 1] += a.y, v[e + 2] += a.z, v[e + 3] += a.w;
+            k[e] += b.x, k[e + 1] += b.y, k[e + 2] += b.z, k[e + 3] += b.w;
+        }
+    }
+    const size_t at = ((size_t)(start + j) * Hkv + g) * D + d;
+    *reinterpret_cast<uint4*>(dV + at) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    *reinterpret_cast<uint4*>(dK + at) =
+        make_uint4(pack_bf16x2(k[0], k[1]), pack_bf16x2(k[2], k[3]), pack_bf16x2(k[4], k[5]), pack_bf16x2(k[6], k[7]));
+}
+
 template <int D>
 cudaError_t launch_bwd_t(const BwdLaunch& L, cudaStream_t stream) {
     const long long rh = (long long)L.total_rows * L.Hq;
@@ -682,6 +739,7 @@ cudaError_t launch_bwd_t(const BwdLaunch& L, cudaStream_t stream) {
         a.T = L.total_rows;
         a.scale = L.scale;
         a.scale_log2 = L.scale * kLog2e;
+        a.sink = L.sink;
         constexpr uint32_t kSmem = Cfg<D>::kSmem;
         cudaError_t e = cudaFuncSetAttribute(bwd_main_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
         if (e != cudaSuccess) return e;
@@ -692,7 +750,7 @@ cudaError_t launch_bwd_t(const BwdLaunch& L, cudaStream_t stream) {
         attr[0].val.clusterDim.x = NC;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
-        cfg.gridDim = dim3(L.Hkv * NC, L.nseq, (L.S + kB - 1) / kB);
+        cfg.gridDim = dim3(L.Hkv * NC, L.nseq, L.sink.slices + (L.S + kB - 1) / kB);
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = kSmem;
         cfg.stream = stream;
@@ -703,6 +761,14 @@ cudaError_t launch_bwd_t(const BwdLaunch& L, cudaStream_t stream) {
         prof_end(stream, m);
         if (e != cudaSuccess) return e;
         e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    if (L.sink.slices > 0) {
+        const ProfMark m = prof_begin(stream, "bwd_sink_sum");
+        bwd_sink_sum_kernel<<<dim3(L.sink.sink, L.Hkv, L.nseq), 64, 0, stream>>>(L.sink, L.dK, L.dV, L.cu_seqlens, L.S,
+                                                                                 L.total_rows, L.Hkv, D, L.window);
+        prof_end(stream, m);
+        cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     {

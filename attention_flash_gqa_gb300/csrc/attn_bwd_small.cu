@@ -95,6 +95,7 @@ struct SmallArgs {
     unsigned* status;
     int Hq, Hkv, S, window, T;
     float scale, scale_log2;
+    SinkSplit sink;
 };
 
 template <int D, int DS>
@@ -106,14 +107,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = blockIdx.x / C::NSL;        // KV head
     const int c0 = (blockIdx.x % C::NSL) * DS;  // this CTA's columns of dV, dK, dQ
     const int seq = blockIdx.y;
-    const int kv_tile = blockIdx.z;  // tile 0 sees the most queries: launched first
+    // the first a.sink.slices blocks share out the queries that see of tile 0 its sinks alone (the window has left
+    // it); behind them a block for each key tile, tile 0 first: it sees the most queries
+    const int slice = (int)blockIdx.z - a.sink.slices;
+    const bool far = slice < 0;
+    const int kv_tile = far ? 0 : slice;
     int seq_start = 0, L = a.S, bcoord = seq;
     if (a.cu_seqlens) {
         seq_start = a.cu_seqlens[seq];
         L = a.cu_seqlens[seq + 1] - seq_start;
         bcoord = 0;
         if (!varlen_seq_ok(seq_start, L, a.T, a.S)) {  // reported; nothing of the slice is touched
-            if (threadIdx.x == 0 && blockIdx.x == 0 && kv_tile == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
+            if (threadIdx.x == 0 && blockIdx.x == 0 && slice == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
             return;
         }
     }
@@ -121,8 +126,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (k0 >= L) return;  // uniform: before any barrier or TMEM use
     const int G = a.Hq / a.Hkv;
     const int q_last = a.window > 0 ? min(L, k0 + kB - 1 + a.window) : L;  // exclusive bound on queries
-    const int i_begin = k0 / kB, i_end = (q_last + kB - 1) / kB;
+    const int i_near = (q_last + kB - 1) / kB;
+    const int i_begin = far ? i_near + (int)blockIdx.z * a.sink.tiles : k0 / kB;
+    const int i_end = far ? min(i_begin + a.sink.tiles, (L + kB - 1) / kB) : i_near;
     const int n_qt = i_end - i_begin;
+    if (n_qt <= 0) return;  // no such slice (uniform)
+    // whether this block's dK and dV of the sinks are one part of several
+    const bool parted = a.sink.slices > 0 && kv_tile == 0 && i_near * kB < L;
     const int n = G * n_qt;  // steps: (head, query tile)
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -561,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     q0 + kB <= L && k0 + kB <= L);
                 // on edge tiles key j sees the queries qa with 0 <= qa - kabs < span
                 int qhi = key_ok ? L : kabs;
-                if (a.window > 0) qhi = min(qhi, kabs + a.window);
+                if (a.window > 0 && kabs >= a.sink.sink) qhi = min(qhi, kabs + a.window);
                 const unsigned span = qhi > kabs ? (unsigned)(qhi - kabs) : 0u;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -644,13 +654,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t row = (size_t)(a.cu_seqlens ? seq_start + kabs : seq * a.S + kabs) * a.Hkv + g;
             uint16_t* dv_row = a.dV + row * D + c0;
             uint16_t* dk_row = a.dK + row * D + c0;
+            const bool part_row = parted && kabs < a.sink.sink;
+            float* part = parted ? a.sink.row(seq, a.cu_seqlens ? seq_start : seq * a.S, far ? 1 + blockIdx.z : 0, g, a.Hkv, j, D) + c0
+                                 : nullptr;
 #pragma unroll 1
             for (int c4 = hf; c4 < DS / 32; c4 += 2) {  // the two warps of a lane quarter split the columns
                 uint32_t rv[32], rk[32];
                 tmem_ld32(tDV + c4 * 32 + lane_base, rv);
                 tmem_ld32(tDK + c4 * 32 + lane_base, rk);
                 tmem_ld_wait();
-                if (key_ok) {
+                if (key_ok && part_row) {
+                    float* pv = part + c4 * 32;
+                    float* pk = pv + (size_t)a.sink.sink * D;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        *reinterpret_cast<float4*>(pv + e) = make_float4(__uint_as_float(rv[e]), __uint_as_float(rv[e + 1]),
+                                                                         __uint_as_float(rv[e + 2]), __uint_as_float(rv[e + 3]));
+                        *reinterpret_cast<float4*>(pk + e) =
+                            make_float4(__uint_as_float(rk[e]) * a.scale, __uint_as_float(rk[e + 1]) * a.scale,
+                                        __uint_as_float(rk[e + 2]) * a.scale, __uint_as_float(rk[e + 3]) * a.scale);
+                    }
+                } else if (key_ok && !far) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint4 wv, wk;
@@ -687,11 +711,12 @@ cudaError_t launch_bwd_small_main(const BwdLaunch& L, cudaStream_t stream) {
     a.cu_seqlens = L.cu_seqlens, a.status = L.status;
     a.Hq = L.Hq, a.Hkv = L.Hkv, a.S = L.S, a.window = L.window, a.T = L.total_rows;
     a.scale = L.scale, a.scale_log2 = L.scale * kLog2e;
+    a.sink = L.sink;
     constexpr uint32_t kSmem = SmallCfg<D, DS>::kSmem;
     cudaError_t e =
         cudaFuncSetAttribute(bwd_small_kernel<D, DS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    const dim3 grid(L.Hkv * (D / DS), L.nseq, (L.S + kB - 1) / kB);
+    const dim3 grid(L.Hkv * (D / DS), L.nseq, L.sink.slices + (L.S + kB - 1) / kB);
     const ProfMark m = prof_begin(stream, D == 256 ? "bwd_main_d256" : D == 128 ? "bwd_main_d128" : "bwd_main_d64");
     bwd_small_kernel<D, DS><<<grid, kThreads, kSmem, stream>>>(L.tq, L.tk, L.tv, L.tdo, L.tdq, a);
     prof_end(stream, m);

@@ -80,6 +80,7 @@ struct FwdArgs {
     const int32_t* cu_seqlens;
     unsigned* status;
     int Hq, Hkv, S, D, window, n_qtiles, nsplit, T;
+    int sink;  // first keys of a sequence that stay visible past the window, at most one key tile (0: none)
     float scale_log2;
     // paged prefill: keys / values through a block table, new queries packed by cu_q
     const int32_t *block_table, *seq_lens, *cu_q;
@@ -150,7 +151,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kv_hi = min(L, qp0 + kBQ);
     const int kv_lo = a.window > 0 ? max(0, qp0 - a.window + 1) : 0;
     const int t_begin = kv_lo / kBKV, t_end = (kv_hi + kBKV - 1) / kBKV;
-    const int n = t_end - t_begin;
+    // key tiles in the order they are taken: the one of the sinks where the window has left it, then the window's
+    const int early = a.sink > 0 && t_begin > 0 ? 1 : 0;
+    const int n = t_end - t_begin + early;
+    auto key_tile = [&](int j) { return j < early ? 0 : t_begin - early + j; };
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -217,10 +221,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // -------------------- TMA producer, paged keys / values (whole warp) ---------------
         const int npg = (L + 15) / 16;  // pages of the request
         const int32_t* bt = a.block_table + (size_t)seq * a.max_pages;
-        auto page_id = [&](int tile) -> int {  // lane i < 8: id of page i of key tile `tile`
+        const int sink_pages = min((a.sink + 15) / 16, npg);
+        auto page_id = [&](int j) -> int {  // lane i < 8: id of page i of the j-th key tile
             if (lane >= 8) return 0;
-            const int pi = tile * 8 + lane;
-            int id = bt[pi < npg ? pi : 0];  // pages past the request: its first page (masked anyway)
+            int pi = key_tile(j) * 8 + lane;
+            // pages that no query of the tile sees (past the request, between sinks and window, before the window): one that
+            // is seen in their place, masked all the same. Their own table entries may be stale.
+            if (pi >= sink_pages) pi = j < early ? 0 : pi < npg ? max(pi, kv_lo / 16) : kv_lo / 16;
+            int id = bt[pi];
             if (id < 0 || id >= a.num_pages) {
                 atomicOr(a.status, DEVSTAT_BOUNDS);
                 id = 0;
@@ -279,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         // page ids one tile ahead, separately for the K and the V sequence
-        int k_cur = page_id(t_begin), k_nxt = n > 1 ? page_id(t_begin + 1) : 0;
+        int k_cur = page_id(0), k_nxt = n > 1 ? page_id(1) : 0;
         int v_cur = k_cur, v_nxt = k_nxt;
         int vs[C::kVChunks], vr[C::kVChunks];
         int kt = 0, vt = 0;  // next K / V tile to load
@@ -299,12 +307,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto next_k = [&]() {
             ++kt;
             k_cur = k_nxt;
-            k_nxt = kt + 1 < n ? page_id(t_begin + kt + 1) : 0;
+            k_nxt = kt + 1 < n ? page_id(kt + 1) : 0;
         };
         auto next_v = [&]() {
             ++vt;
             v_cur = v_nxt;
-            v_nxt = vt + 1 < n ? page_id(t_begin + vt + 1) : 0;
+            v_nxt = vt + 1 < n ? page_id(vt + 1) : 0;
         };
         // the issuer's order: K(0) .. K(kSBuf - 1), then V(j), K(j + kSBuf) for every step j
         for (int b = 0; ok && b < C::kSBuf && b < n; ++b) {
@@ -327,15 +335,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; !PAIR && ok && c < C::kVChunks; ++c)
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[vs[c]]), vr[c] & 1, abort_flag, a.status, 0x1e));
             if (ok) {
-                const int units = (kBQ - r_valid) * 8 * C::kSubs;  // 16-byte pieces of the rows past the end
-                for (int c = 0; c < C::kVChunks; ++c) {
-                    const uint32_t base = sSlots + vs[c] * C::kSlotBytes;
-                    for (int e = lane; e < units; e += 32) {
-                        const int row = r_valid + e / (8 * C::kSubs), chunk = (e >> 3) % C::kSubs, piece = e & 7;
-                        st_shared_v4(base + (row >> 3) * C::kPagedGroupStride + chunk * 1024 + (row & 7) * 128 + piece * 16,
-                                     0u, 0u, 0u, 0u);
+                auto zero_rows = [&](int from, int to) {
+                    const int units = (to - from) * 8 * C::kSubs;  // 16-byte pieces
+                    for (int c = 0; c < C::kVChunks; ++c) {
+                        const uint32_t base = sSlots + vs[c] * C::kSlotBytes;
+                        for (int e = lane; e < units; e += 32) {
+                            const int row = from + e / (8 * C::kSubs), chunk = (e >> 3) % C::kSubs, piece = e & 7;
+                            st_shared_v4(base + (row >> 3) * C::kPagedGroupStride + chunk * 1024 + (row & 7) * 128 + piece * 16,
+                                         0u, 0u, 0u, 0u);
+                        }
                     }
-                }
+                };
+                zero_rows(r_valid, kBQ);
+                // and those of pages in front of the window, which repeat its first one: here that may be the last page
+                if (t_end - t_begin == 1) zero_rows(t_begin == 0 ? 16 * sink_pages : 0, kv_lo / 16 * 16 - t_begin * kBKV);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -396,12 +409,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto load_k = [&](int t) -> bool {
                 for (int c = 0; c < C::kQChunks; ++c)
-                    if (!load_chunk(&tk, c * (PAIR ? 256 : C::kSlotCols), seq_start + (t_begin + t) * kBKV, true)) return false;
+                    if (!load_chunk(&tk, c * (PAIR ? 256 : C::kSlotCols), seq_start + key_tile(t) * kBKV, true)) return false;
                 return true;
             };
             auto load_v = [&](int t) -> bool {
                 for (int c = 0; c < C::kVChunks; ++c)
-                    if (!load_chunk(&tv, dv0 + c * C::kSlotCols, seq_start + (t_begin + t) * kBKV, false)) return false;
+                    if (!load_chunk(&tv, dv0 + c * C::kSlotCols, seq_start + key_tile(t) * kBKV, false)) return false;
                 return true;
             };
             // the issuer's order: K(0) .. K(kSBuf - 1), then V(j), K(j + kSBuf) for every step j
@@ -556,14 +569,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(raw[c][e]);
                 }
-                const int key0 = (t_begin + j) * kBKV + 64 * hf;
+                const int key0 = key_tile(j) * kBKV + 64 * hf;
                 const bool edge = (key0 + 63 > qp0) || (a.window > 0 && qp0 + kBQ - 1 - key0 >= a.window) ||
                                   (key0 + 64 > L);
                 if (edge) {
 #pragma unroll
                     for (int c = 0; c < 64; ++c) {
                         const int key = key0 + c;
-                        const bool allowed = key <= qi && key < L && (a.window <= 0 || qi - key < a.window);
+                        const bool allowed = key <= qi && key < L && (a.window <= 0 || qi - key < a.window || key < a.sink);
                         if (!allowed) s[c] = -INFINITY;
                     }
                 }
@@ -700,7 +713,7 @@ cudaError_t launch_fwd_t(const FwdLaunch& L, cudaStream_t stream) {
     a.o = L.o, a.lse = L.lse, a.cu_seqlens = L.cu_seqlens, a.status = L.status;
     a.block_table = L.block_table, a.seq_lens = L.seq_lens, a.cu_q = L.cu_q;
     a.max_pages = L.max_pages, a.num_pages = L.num_pages;
-    a.Hq = L.Hq, a.Hkv = L.Hkv, a.S = L.S, a.D = L.D, a.window = L.window;
+    a.Hq = L.Hq, a.Hkv = L.Hkv, a.S = L.S, a.D = L.D, a.window = L.window, a.sink = L.window > 0 ? L.sink : 0;
     a.n_qtiles = (L.S + kBQ - 1) / kBQ;
     a.nsplit = DQK / C::kDV;
     a.T = L.total_rows;

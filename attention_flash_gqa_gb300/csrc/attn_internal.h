@@ -28,7 +28,7 @@ struct DecodeLaunch {
     float* lse;
     float* part;
     unsigned* status;
-    int B, Hq, Hkv, D, max_pages, num_pages, grid, window;
+    int B, Hq, Hkv, D, max_pages, num_pages, grid, window, sink;
     float scale;
 };
 size_t decode_smem_bytes(int hb, int D);
@@ -62,10 +62,28 @@ struct FwdLaunch {
     const int32_t* seq_lens = nullptr;
     const int32_t* cu_q = nullptr;
     int max_pages = 0, num_pages = 0;
+    int sink = 0;  // first keys that stay visible past the window (0 .. 128)
 };
 cudaError_t launch_fwd(const FwdLaunch& L, cudaStream_t stream);
 
 // ---- backward ---------------------------------------------------------------------------
+// Sinks in the backward: the first `sink` keys of a sequence are seen by its every query, the other keys of their tile
+// by those of the window alone. The near queries, those of the tile's windows, belong to the tile's own block; the far ones
+// are shared out in slices of `tiles` query tiles, so that no block has much more to do than one of the window's. The
+// near block and each slice leave dV and dK of the sinks as parts in fp32, [part][Hkv][2][sink][D], and a small kernel
+// adds them up. Parts of a sequence start at floor(first row / rows of a slice) + 2 x its number: it has at most
+// floor(length / rows of a slice) + 2 of them, so none overlap, and nobody has to count those of the others.
+struct SinkSplit {
+    float* part;
+    int sink;    // 0: none
+    int slices;  // far slices of the longest sequence that there may be; 0: no query is far
+    int tiles;   // query tiles of a slice
+    __host__ __device__ float* row(int seq, int start, int p, int g, int Hkv, int j, int D) const {
+        const size_t at = (size_t)(start / (tiles * 128) + 2 * seq + p) * Hkv + g;
+        return part + (at * 2 * sink + j) * D;
+    }
+};
+
 struct BwdLaunch {
     CUtensorMap tq, tk, tv, tdo;
     CUtensorMap tqh, tdoh;  // q / dO with a 64 x 1 x (256*128/D) x 1 box: one cluster CTA's query share
@@ -79,6 +97,7 @@ struct BwdLaunch {
     unsigned* status;
     int nseq, Hq, Hkv, S, D, total_rows, window;
     float scale;
+    SinkSplit sink;
 };
 cudaError_t launch_bwd(const BwdLaunch& L, cudaStream_t stream);
 // main kernel of the backward at D = 64 / 128 (one CTA per key tile; attn_bwd_small.cu)
@@ -144,5 +163,33 @@ struct TreeLaunch {
 int tree_tokens_per_copy(int G, int max_q);  // drafted tokens of a copy of Q: those of a 128-row tile, or fewer
 size_t tree_workspace_bytes(int G, int max_q, int D);
 cudaError_t launch_tree_paged(const TreeLaunch& L, cudaStream_t stream);
+
+// ---- 4-bit paged cache (kv4.cuh): rows in by slot, pages out as bf16 ----------------------------
+struct Kv4Launch {
+    const uint16_t *k, *v;   // append: rows [n] of Hkv x D, token strides below
+    const int32_t* slots;    // append: [n]
+    const int32_t* pages;    // unpack: [n]
+    uint16_t *k_out, *v_out;  // unpack: [n, 16, Hkv, D]
+    uint8_t* cache;          // [num_pages, Hkv, 18 D]
+    unsigned* status;
+    long long k_stride, v_stride;  // elements
+    int n, Hkv, D, num_pages;
+};
+cudaError_t launch_kv4_append(const Kv4Launch& L, cudaStream_t stream);
+cudaError_t launch_kv4_unpack(const Kv4Launch& L, cudaStream_t stream);
+
+struct DecodeKv4Launch {
+    const uint16_t* q;
+    const uint8_t* cache;
+    const int32_t *block_table, *seq_lens;
+    uint16_t* o;
+    float* lse;
+    unsigned* status;
+    void* workspace;
+    int B, Hq, Hkv, D, max_pages, num_pages, window, sink, grid;
+    float scale;
+};
+size_t decode_kv4_workspace_bytes(int B, int G, int D, int grid);
+cudaError_t launch_decode_kv4(const DecodeKv4Launch& L, cudaStream_t stream);
 
 }  // namespace attn

@@ -84,6 +84,7 @@ struct DecodeArgs {
     unsigned* status;
     int B, Hq, Hkv, max_pages, num_pages;
     int window;        // <= 0: none
+    int sink;          // first keys of a request that stay visible past the window (SINK kernels)
     int hb, nhb;       // KV heads per unit, head blocks (hb * nhb = Hkv)
     float scale_log2;
 };
@@ -140,9 +141,16 @@ __device__ __forceinline__ int first_token(const DecodeArgs& a, int L) {
     return a.window > 0 && L > a.window ? L - a.window : 0;
 }
 
-// Units (pages holding keys the query sees) of a request of length L.
+// Pages of sinks in front of the window's first page.
+template <bool SINK>
+__device__ __forceinline__ int sink_pages(const DecodeArgs& a, int L) {
+    return SINK ? min((a.sink + kPage - 1) / kPage, first_token(a, L) / kPage) : 0;
+}
+
+// Units (pages holding keys the query sees) of a request of length L: those of its sinks, then the window's.
+template <bool SINK>
 __device__ __forceinline__ int req_units(const DecodeArgs& a, int L) {
-    return L > 0 ? (L - 1) / kPage - first_token(a, L) / kPage + 1 : 0;
+    return L > 0 ? (L - 1) / kPage - first_token(a, L) / kPage + 1 + sink_pages<SINK>(a, L) : 0;
 }
 
 // CTA that owns global page unit u when P units are split evenly over G CTAs
@@ -151,7 +159,9 @@ __device__ __forceinline__ int owner_of(long long u, long long P, int G) {
     return (int)(((u + 1) * (long long)G - 1) / P);
 }
 
-template <int G, int D>
+// SINK: the first a.sink keys of a request are visible past its window (a kernel of its own, so that calls without
+// sinks keep the code that they had).
+template <int G, int D, bool SINK>
 __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
     decode_paged_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, DecodeArgs a) {
     using DC = DecCfg<G, D>;
@@ -212,7 +222,7 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
                 if (b >= B) continue;
                 const int L = clamp_len(a, load_l2(a.seq_lens + b), record);
                 if (guess) lens[b] = L;
-                local += req_units(a, L);
+                local += req_units<SINK>(a, L);
             }
         }
         // inclusive scan of `local` over threads 0..255
@@ -233,7 +243,7 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
                 int b = tid * per + i;
                 if (b < B) {
                     start[b] = acc;
-                    acc += guess ? local : req_units(a, req_len(a, b));
+                    acc += guess ? local : req_units<SINK>(a, req_len(a, b));
                 }
             }
             if (tid == 255) start[B] = acc;
@@ -257,13 +267,19 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
             else hi = mid - 1;
         }
         const int L = guess ? lens[lo] : req_len(a, lo);
-        const int p = (int)(u - start[lo]) + first_token(a, L) / kPage;  // page index in the request
+        int p = (int)(u - start[lo]) + first_token(a, L) / kPage;  // page index in the request
+        int end = L;                                               // its tokens from here on are not visible
+        if (SINK) {
+            const int early = sink_pages<SINK>(a, L);
+            p -= early;
+            if ((int)(u - start[lo]) < early) p = (int)(u - start[lo]), end = a.sink;
+        }
         const int page = load_l2(a.block_table + (size_t)lo * a.max_pages + p);
         if (page < 0 || page >= a.num_pages) {
             if (record) atomicOr(a.status, DEVSTAT_BOUNDS);
             return -1;
         }
-        const int nt = min(kPage, L - p * kPage);
+        const int nt = min(kPage, end - p * kPage);
         return (page << 5) | nt;
     };
     // every cached byte is read once per step: evict-first keeps the stream from displacing
@@ -476,11 +492,16 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
     bool ok = true;
     int cur_b = -1;
     int lo_tok = 0;  // first visible token within the request's first unit (window)
+    int early = 0, sink_left = 0;  // SINK: units before that one, and tokens of it that are sinks
     for (long long u = u0; u < u1 && ok; ++u, ++i) {
         while (start[b + 1] <= u) ++b;
         if (b != cur_b) {
             cur_b = b;
             lo_tok = first_token(a, req_len(a, b)) % kPage;
+            if (SINK) {
+                early = sink_pages<SINK>(a, req_len(a, b));
+                sink_left = a.sink - first_token(a, req_len(a, b)) / kPage * kPage;
+            }
             if (PACKED && active && mg < G) {
                 const uint16_t* qrow = a.q + ((size_t)b * a.Hq + g * G + mg) * D + 2 * mc;
 #pragma unroll
@@ -505,14 +526,16 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
         if (!ok) break;
         const int32_t entry = unit_entry(i);
         const int nt = (entry >= 0 ? (entry & 31) : 0) - TPW * half;  // end of this warp's valid tokens (may be <= 0)
-        const int tlo = (u == start[b] ? lo_tok : 0) - TPW * half;     // first of them (may be < 0)
-        if (active && nt > 0 && tlo < TPW) {
+        const bool first_unit = SINK ? (int)(u - start[b]) == early : u == start[b];
+        const int tlo = (first_unit ? lo_tok : 0) - TPW * half;     // first of them (may be < 0)
+        const int tsink = SINK && first_unit ? sink_left - TPW * half : 0;  // and those below this, in the window's first page
+        if (active && nt > 0 && (tlo < TPW || (SINK && tsink > 0))) {
             const uint8_t* kp = stage_base + (size_t)s * 2 * page_bytes;
             const uint8_t* vp = kp + page_bytes;
             if constexpr (PACKED) {
                 const uint32_t kb = smem_u32(kp), vb = smem_u32(vp);
                 const uint32_t hbytes = (uint32_t)a.hb * kPage * 128u;  // one 64-dim half of every head
-                auto vis = [&](int t) { return t < nt && t >= tlo; };
+                auto vis = [&](int t) { return t < nt && (t >= tlo || (SINK && t < tsink)); };
                 // S = Q K^T: tiles of tokens 0-7 and 8-15. Per k-step one matrix load gives both
                 // tiles' B fragments: lanes 0-7 / 8-15 / 16-23 / 24-31 address tokens 0-7, 0-7,
                 // 8-15, 8-15 at the step's lower / upper / lower / upper 8 dims; the swizzle puts
@@ -628,7 +651,7 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
                     for (int j = 0; j < NF; ++j) {
                         const int idx = (lane >> (5 - KH)) * NF + j;  // t * G + hh within this lane's tokens
                         const int tw = idx / G;                        // token within the warp's 8
-                        sc[tw * G + idx % G] = tw < nt && tw >= tlo ? v[j] * a.scale_log2 : -INFINITY;
+                        sc[tw * G + idx % G] = tw < nt && (tw >= tlo || (SINK && tw < tsink)) ? v[j] * a.scale_log2 : -INFINITY;
                     }
                 }
                 __syncwarp();
@@ -674,7 +697,8 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
                 __syncwarp();
                 // o update: add this lane's tokens
                 const int tmax = nt < 8 ? nt : 8;
-                for (int t = tlo > 0 ? tlo : 0; t < tmax; ++t) {  // only the warp's visible tokens
+                for (int t = !(SINK && tsink > 0) && tlo > 0 ? tlo : 0; t < tmax; ++t) {  // only the warp's visible tokens
+                    if (SINK && t < tlo && t >= tsink) continue;
                     const uint8_t* vrow = vp + ((size_t)((TPW * half + t) * a.hb + gl) * D + dim0) * 2;
                     float vv[QD];
                     const uint4 w = *reinterpret_cast<const uint4*>(vrow);
@@ -768,14 +792,14 @@ struct MergeArgs {
     uint16_t* o;
     float* lse;
     unsigned* status;
-    int B, Hq, hb, decode_grid, max_pages, window;
+    int B, Hq, hb, decode_grid, max_pages, window, sink;
 };
 
 // Heads of a (request, head block) are split over gridDim.z CTAs of kMergeThreads, one
 // 16-dim item per thread, so the merge of a batch runs on every SM.
 constexpr int kMergeThreads = 64;
 
-template <int G, int D>
+template <int G, int D, bool SINK>
 __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(MergeArgs m) {
     using DC = DecCfg<G, D>;
     constexpr int kRowF = DC::kRowF;
@@ -793,10 +817,10 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(MergeArgs m
     // Every warp sums the unit counts over all requests itself (no shared memory, so these
     // CTAs fit beside a decode CTA).
     DecodeArgs la;  // the fields req_len / req_units read
-    la.seq_lens = m.seq_lens, la.max_pages = m.max_pages, la.window = m.window, la.status = m.status;
+    la.seq_lens = m.seq_lens, la.max_pages = m.max_pages, la.window = m.window, la.status = m.status, la.sink = m.sink;
     long long before = 0, total = 0;
     for (int i = threadIdx.x & 31; i < m.B; i += 32) {
-        const int n = req_units(la, clamp_len(la, load_l2(la.seq_lens + i), true));
+        const int n = req_units<SINK>(la, clamp_len(la, load_l2(la.seq_lens + i), true));
         total += n;
         if (i < b) before += n;
     }
@@ -806,7 +830,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(MergeArgs m
         total += __shfl_xor_sync(0xffffffffu, total, off);
     }
     const long long s0 = before, P = total;
-    const long long s1 = s0 + req_units(la, clamp_len(la, load_l2(la.seq_lens + b), true));
+    const long long s1 = s0 + req_units<SINK>(la, clamp_len(la, load_l2(la.seq_lens + b), true));
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int Gc = (int)(P < (long long)m.decode_grid ? P : (long long)m.decode_grid);
     const int nitems = nh * (D / DI);
@@ -900,6 +924,7 @@ cudaError_t launch_decode_paged(const DecodeLaunch& L, cudaStream_t stream) {
     a.o = L.o, a.lse = L.lse, a.part = L.part, a.status = L.status;
     a.B = L.B, a.Hq = L.Hq, a.Hkv = L.Hkv, a.max_pages = L.max_pages, a.num_pages = L.num_pages;
     a.window = L.window;
+    a.sink = L.window > 0 ? L.sink : 0;
     const int G = L.Hq / L.Hkv;
     a.hb = decode_heads_per_unit(L.Hkv, L.D, G);
     a.nhb = L.Hkv / a.hb;
@@ -908,6 +933,7 @@ cudaError_t launch_decode_paged(const DecodeLaunch& L, cudaStream_t stream) {
     MergeArgs mg;
     mg.part = L.part, mg.seq_lens = L.seq_lens, mg.o = L.o, mg.lse = L.lse, mg.status = L.status;
     mg.B = L.B, mg.Hq = L.Hq, mg.hb = a.hb, mg.decode_grid = L.grid, mg.max_pages = L.max_pages, mg.window = L.window;
+    mg.sink = a.sink;
     auto go = [&](auto kern, auto merge, int threads) -> cudaError_t {
         // the limit belongs to the kernel: every call sets that of the most heads, so that none lowers it between
         // another thread's setting and its launch
@@ -928,7 +954,8 @@ cudaError_t launch_decode_paged(const DecodeLaunch& L, cudaStream_t stream) {
         dcfg.stream = stream;
         dcfg.attrs = attr;
         dcfg.numAttrs = 1;
-        ProfMark m = prof_begin(stream, L.D == 128 ? "decode_paged" : "decode_paged_d256");
+        ProfMark m = prof_begin(stream, L.D == 128 ? (a.sink ? "decode_paged_sink" : "decode_paged")
+                                                    : (a.sink ? "decode_paged_sink_d256" : "decode_paged_d256"));
         e = cudaLaunchKernelEx(&dcfg, kern, L.tk, L.tv, a);
         prof_end(stream, m);
         if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
@@ -948,8 +975,10 @@ cudaError_t launch_decode_paged(const DecodeLaunch& L, cudaStream_t stream) {
         prof_end(stream, m);
         return e != cudaSuccess ? e : cudaGetLastError();
     };
-#define ATTN_DECODE_CASE(G_, D_) \
-    case G_: return go(decode_paged_kernel<G_, D_>, decode_merge_kernel<G_, D_>, DecCfg<G_, D_>::kThreads);
+#define ATTN_DECODE_CASE(G_, D_)                                                                                 \
+    case G_:                                                                                                     \
+        return a.sink > 0 ? go(decode_paged_kernel<G_, D_, true>, decode_merge_kernel<G_, D_, true>, DecCfg<G_, D_>::kThreads) \
+                          : go(decode_paged_kernel<G_, D_, false>, decode_merge_kernel<G_, D_, false>, DecCfg<G_, D_>::kThreads);
     if (L.D == 128) {
         switch (G) {
             ATTN_DECODE_CASE(1, 128)

@@ -26,6 +26,9 @@ struct Api {
     decltype(&attn_qk_norm_rope_bwd) norm_rope_bwd = nullptr;
     decltype(&attn_qk_norm_rope_paged) norm_rope_paged = nullptr;
     decltype(&attn_tree_paged) tree_paged = nullptr;
+    decltype(&attn_kv4_append) kv4_append = nullptr;
+    decltype(&attn_kv4_unpack) kv4_unpack = nullptr;
+    decltype(&attn_decode_kv4) decode_kv4 = nullptr;
     decltype(&attn_workspace_size) workspace_size = nullptr;
 };
 Api g_api;
@@ -59,7 +62,7 @@ T* checked(const at::Tensor& t, at::ScalarType type, at::IntArrayRef shape, int 
     if (t.scalar_type() == type && t.is_cuda() && t.get_device() == idx && t.sizes() == shape && t.is_contiguous())
         return static_cast<T*>(t.data_ptr());
     PyErr_Format(PyExc_ValueError, "%s must be a contiguous %s tensor of %d dimensions on cuda:%d with the call's sizes", name,
-                 type == at::kInt ? "int32" : type == at::kFloat ? "float32" : "bfloat16", (int)shape.size(), idx);
+                 type == at::kInt ? "int32" : type == at::kFloat ? "float32" : type == at::kByte ? "uint8" : "bfloat16", (int)shape.size(), idx);
     throw Raised();
 }
 int32_t* i32(PyObject* o, at::IntArrayRef shape, int idx, const char* name) {
@@ -480,6 +483,98 @@ PyObject* tree_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// ---- 4-bit paged cache -------------------------------------------------------------------------
+// A cache uint8 [num_pages, Hkv, 18, D].
+struct Kv4Cache {
+    uint8_t* at;
+    int num_pages, heads, D;
+    Kv4Cache(PyObject* o, int idx) {
+        const at::Tensor& t = tensor(o, "kv_cache");
+        if (t.dim() != 4 || t.size(2) != 18 || t.size(0) > INT32_MAX || t.size(1) > INT32_MAX || t.size(3) > INT32_MAX)
+            refuse("%s must be [num_pages, Hkv, 18, D]", "kv_cache");
+        at = checked<uint8_t>(t, at::kByte, t.sizes(), idx, "kv_cache");
+        num_pages = (int)t.size(0), heads = (int)t.size(1), D = (int)t.size(3);
+    }
+};
+
+// (k, v, slots, kv_cache, page_size, stream)
+PyObject* kv4_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 6, [&]() -> PyObject* {
+        const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
+        const int idx = index_of(k, "k");
+        const Rows rk = rows(k, "k", idx), rv = rows(v, "v", idx);
+        if (v.sizes() != k.sizes()) refuse("%s must have the shape of k", "v");
+        const Kv4Cache c(a[3], idx);
+        if (c.heads != rk.H || c.D != rk.D) refuse("%s are not k's", "the cache's heads");
+        const at::Tensor& s = tensor(a[2], "slots");
+        const int64_t flat[1] = {rk.T};
+        const int32_t* slots = checked<int32_t>(s, at::kInt, s.dim() == 1 ? at::IntArrayRef(flat) : k.sizes().slice(0, k.dim() - 2), idx, "slots");
+        Place place(a[5], idx);
+        check(g_api.kv4_append(rk.at, rv.at, slots, c.at, (int)rk.T, c.heads, c.D, as_int(a[4], "page_size"), c.num_pages, rk.step,
+                               rv.step, place.stream),
+              "attn_kv4_append");
+        Py_RETURN_NONE;
+    });
+}
+
+// (kv_cache, pages, k_pages, v_pages, page_size, stream)
+PyObject* kv4_unpack(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 6, [&]() -> PyObject* {
+        const int idx = index_of(tensor(a[0], "kv_cache"), "kv_cache");
+        const Kv4Cache c(a[0], idx);
+        const at::Tensor& p = tensor(a[1], "pages");
+        const int64_t P = p.numel(), sP[1] = {P};
+        if (P > INT32_MAX) refuse("%s is too large", "pages");
+        const int32_t* pages = checked<int32_t>(p, at::kInt, sP, idx, "pages");
+        const int page_size = as_int(a[4], "page_size");
+        const int64_t shape[4] = {P, page_size, c.heads, c.D};
+        if (page_size < 1) refuse("%s must be positive", "page_size");
+        Place place(a[5], idx);
+        Result r[2];
+        attn_bf16* out[2];
+        for (int i = 0; i < 2; ++i) {
+            const char* name = i ? "v_pages" : "k_pages";
+            r[i].given = a[2 + i];
+            if (a[2 + i] == Py_None) r[i].made = place.make(shape, at::kBFloat16);
+            out[i] = bf16(a[2 + i] == Py_None ? r[i].made : tensor(a[2 + i], name), shape, idx, name);
+        }
+        check(g_api.kv4_unpack(c.at, pages, out[0], out[1], (int)P, c.heads, c.D, page_size, c.num_pages, place.stream),
+              "attn_kv4_unpack");
+        return tuple(r);
+    });
+}
+
+// (q, kv_cache, block_table, seq_lens, o, lse, scale, window, sink, page_size, workspace, stream)
+PyObject* decode_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 12, [&]() -> PyObject* {
+        const at::Tensor& q = tensor(a[0], "q");
+        const int idx = index_of(q, "q");
+        const Kv4Cache c(a[1], idx);
+        if (q.dim() != 3 || q.size(0) > INT32_MAX || q.size(1) > INT32_MAX || q.size(2) != c.D) refuse("%s must be [B, Hq, D]", "q");
+        const int64_t B = q.size(0), Hq = q.size(1);
+        attn_bf16* qp = bf16(q, q.sizes(), idx, "q");
+        const at::Tensor& table = tensor(a[2], "block_table");
+        if (table.dim() != 2 || table.size(1) > INT32_MAX) refuse("%s must be [B, max_pages]", "block_table");
+        const int64_t sB[1] = {B}, sTab[2] = {B, table.size(1)}, sL[2] = {B, Hq};
+        const int32_t *tab = i32(a[2], sTab, idx, "block_table"), *lens = i32(a[3], sB, idx, "seq_lens");
+        const float scale = as_float(a[6]);
+        const int window = as_int(a[7], "window"), sink = as_int(a[8], "sink"), page_size = as_int(a[9], "page_size");
+        Place place(a[11], idx);
+        Result r[2];
+        attn_bf16* o = like(r[0], a[4], q, place, "o");
+        r[1].given = a[5];
+        if (a[5] == Py_None) r[1].made = place.make(sL, at::kFloat);
+        float* lse = checked<float>(a[5] == Py_None ? r[1].made : tensor(a[5], "lse"), at::kFloat, sL, idx, "lse");
+        at::Tensor own;
+        size_t bytes = 0;
+        void* ws = scratch(own, bytes, a[10], g_api.workspace_size(ATTN_OP_DECODE_KV4, (int)B, (int)Hq, c.heads, 0, c.D, 0, 0), place);
+        check(g_api.decode_kv4(qp, c.at, tab, lens, o, lse, (int)B, (int)Hq, c.heads, c.D, page_size, (int)table.size(1), c.num_pages, scale,
+                               window, sink, ws, bytes, place.stream),
+              "attn_decode_kv4");
+        return tuple(r);
+    });
+}
+
 // load(path of the library, AttnError, PagedPlan)
 PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (n != 3) {
@@ -507,6 +602,9 @@ PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
     find(api.norm_rope_bwd, "attn_qk_norm_rope_bwd");
     find(api.norm_rope_paged, "attn_qk_norm_rope_paged");
     find(api.tree_paged, "attn_tree_paged");
+    find(api.kv4_append, "attn_kv4_append");
+    find(api.kv4_unpack, "attn_kv4_unpack");
+    find(api.decode_kv4, "attn_decode_kv4");
     find(api.workspace_size, "attn_workspace_size");
     if (PyErr_Occurred()) return nullptr;
     g_api = api;
@@ -518,7 +616,8 @@ PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define ATTN_OP(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {ATTN_OP(load),           ATTN_OP(paged_plan), ATTN_OP(norm_rope), ATTN_OP(norm_rope_bwd),
-                          ATTN_OP(norm_rope_paged), ATTN_OP(tree_paged), {nullptr, nullptr, 0, nullptr}};
+                          ATTN_OP(norm_rope_paged), ATTN_OP(tree_paged), ATTN_OP(kv4_append), ATTN_OP(kv4_unpack),
+                          ATTN_OP(decode_kv4),      {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

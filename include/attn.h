@@ -69,6 +69,9 @@ typedef enum attn_status {
     ATTN_ERR_NO_DEVICE = 8       /* no usable sm_103 device is current */
 } attn_status;
 
+/* The most sinks that a call takes (see attn_fwd_sink). */
+#define ATTN_MAX_SINK 128
+
 /* Operation codes for attn_workspace_size(). */
 enum {
     ATTN_OP_FWD = 0,
@@ -77,7 +80,8 @@ enum {
     ATTN_OP_BWD_VARLEN = 3,
     ATTN_OP_DECODE_PAGED = 4,
     ATTN_OP_QK_NORM_ROPE_BWD = 5,
-    ATTN_OP_TREE_PAGED = 6
+    ATTN_OP_TREE_PAGED = 6,
+    ATTN_OP_DECODE_KV4 = 7
 };
 
 /*
@@ -227,6 +231,53 @@ ATTN_API int attn_decode_paged_noalloc(const attn_bf16* q, const attn_bf16* k_ca
 
 /* attn_decode_paged_noalloc_max_bytes -- size of the built-in decode scratch buffer (bytes). */
 ATTN_API size_t attn_decode_paged_noalloc_max_bytes(void);
+
+/*
+ * Sliding windows with sinks. The calls below are those of the same names without _sink, but the first `sink` keys of a
+ * sequence (packed: of each sequence; paged: of each request) stay visible to all of its later queries:
+ *
+ *   allowed(i,j) = j <= i  and  (window <= 0  or  i - j < window  or  j < sink)
+ *
+ * with 0 <= sink <= ATTN_MAX_SINK; a negative sink is rejected, and with window <= 0 or sink = 0 the results are those of the
+ * calls without. (No counterpart on the pages. A model with such layers keeps its scores' sums steady over contexts far longer
+ * than the window.) Everything else is as described there: layouts, checks, device checks, workspaces.
+ */
+ATTN_API int attn_fwd_sink(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_bf16* o, float* lse, int B,
+                           int Hq, int Hkv, int S, int D, float scale, int causal, int window, int sink, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+ATTN_API int attn_fwd_varlen_sink(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_bf16* o, float* lse,
+                                  const int32_t* cu_seqlens, int num_seqs, int total_tokens, int max_seqlen, int Hq,
+                                  int Hkv, int D, float scale, int causal, int window, int sink, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+ATTN_API int attn_fwd_paged_sink(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
+                                 const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, attn_bf16* o,
+                                 float* lse, int num_reqs, int total_q, int max_q_len, int Hq, int Hkv, int D,
+                                 int page_size, int max_pages_per_seq, int num_pages, float scale, int causal, int window,
+                                 int sink, void* stream);
+
+/* attn_bwd_sink -- gradient of attn_fwd_sink / attn_fwd_varlen_sink.
+ *   workspace: at least attn_bwd_sink_workspace_size() bytes, 256-byte aligned. dK and dV of a sequence's sinks are sums
+ *   over all of it; they are made in parts that lie in the workspace, and added up in one order (the same bits every time
+ *   for dK and dV; dQ, like attn_bwd's, is added up in fp32 in no fixed order). */
+ATTN_API int attn_bwd_sink(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, const attn_bf16* o,
+                           const float* lse, const attn_bf16* dO, attn_bf16* dQ, attn_bf16* dK, attn_bf16* dV, int B,
+                           int Hq, int Hkv, int S, int D, float scale, int causal, int window, int sink,
+                           const int32_t* cu_seqlens, int num_seqs, int max_seqlen, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* attn_bwd_sink_workspace_size -- bytes that attn_bwd_sink needs; packed: B = 1, S = total tokens and num_seqs, dense:
+ *   num_seqs = 0. Pure host arithmetic; needs no GPU. */
+ATTN_API size_t attn_bwd_sink_workspace_size(int B, int Hq, int Hkv, int S, int D, int num_seqs, int window, int sink);
+
+/* attn_decode_paged_sink: the pages of the sinks and those of the window are read, none between them. Workspace as for
+ *   attn_decode_paged (the same size). */
+ATTN_API int attn_decode_paged_sink(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
+                                    const int32_t* block_table, const int32_t* seq_lens, attn_bf16* o, float* lse, int B,
+                                    int Hq, int Hkv, int D, int page_size, int max_pages_per_seq, int num_pages,
+                                    float scale, int window, int sink, void* workspace, size_t workspace_bytes,
+                                    void* stream);
 
 /*
  * attn_merge_lse -- combine attention results computed over disjoint sets of keys into the
@@ -396,9 +447,60 @@ ATTN_API int attn_tree_paged(const attn_bf16* q, const attn_bf16* k_cache, const
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * A paged cache in 4 bits: keys and values of a page in 18 D bytes a KV head, against 64 D in bf16.
+ *
+ *   kv_cache uint8 [num_pages, Hkv, 18, D]: one record for the 16 tokens of a page and KV head, K and V. 32 consecutive dims of
+ *   a token's K or V are a group. It stands for the values n * s, n = -8 .. 7 (held as n + 8 in 4 bits) and s a bf16
+ *   number of 5 significant bits (or zero), so that every value is a bf16 number. The order within a record is that of
+ *   attention_flash_gqa_gb300/csrc/kv4.cuh; a cache needs no initialisation before tokens are written to it.
+ *
+ * attn_kv4_append -- rows into the cache. Of a group x, with a its value of largest magnitude (of two that are equal but for
+ * their sign the negative one):
+ *   s = -a / 8, rounded to 5 significant bits (ties to even); zero if that is below 2^-126, at most 31 * 2^118 in magnitude
+ *   n = x / s rounded to the nearest whole number (ties to even), at least -8 and at most 7; 0 where s = 0
+ *   A group with an infinity or a NaN stands for NaN in all of its 32 dims.
+ *   k, v [T, Hkv, D] bf16: heads contiguous within a token, tokens k_stride / v_stride elements apart (multiples of 8): k_out of
+ *   attn_qk_norm_rope and a slice of the projection. slots int32 [T], of attn_paged_plan: slot s is token s % 16 of page s / 16;
+ *   -1 is padding, nothing of it is written. Any other slot outside the cache is reported as ATTN_ERR_DEVICE_BOUNDS, and
+ *   nothing of its token is written. Slots of different tokens must differ (of two tokens with one slot, either one's codes and
+ *   scales may end up in each part of it). Nothing but the tokens' own bytes is written, and nothing of the cache is read.
+ *   Supported: D in {64, 128, 256}, page_size = 16, Hkv <= 256, num_pages <= 2^26, T * Hkv < 2^31. T = 0: nothing to do
+ *   (pointers may be NULL). No workspace.
+ *
+ * attn_kv4_unpack -- pages back as bf16, exactly: k_pages, v_pages [n, 16, Hkv, D] get the values of page pages[i] (int32 [n]) as
+ * their i-th page. Over them run the calls that read a bf16 cache (attn_fwd_paged, attn_tree_paged), with a block table of
+ * 0 .. n-1. A page id of -1 is skipped; any other outside [0, num_pages) is reported as ATTN_ERR_DEVICE_BOUNDS; both leave
+ * their page of the outputs as it was. Slots never written come out as whatever their bytes stand for. n * 8 * Hkv < 2^31,
+ * everything else as above.
+ *
+ * attn_decode_kv4 -- attn_decode_paged_sink over the values that the cache stands for: one new query token a request, q [B, Hq, D],
+ * block_table, seq_lens, window, sink, o and lse as there. K is used as it is, in products of fp32; P is rounded to bf16 for the
+ * product with V, as in the other attention calls. Hidden tokens' bytes may be anything. A request with L = 0 gets o = 0 and
+ * lse = -inf; a row with a NaN score gets NaN for both. Page ids outside [0, num_pages) and lengths outside the block-table
+ * row are reported as ATTN_ERR_DEVICE_BOUNDS, their tokens skipped.
+ *   Supported: D in {64, 128, 256}, Hq / Hkv in 1 .. 8, Hkv <= 256, B <= 4096, page_size = 16, num_pages <= 2^26,
+ *   B * max_pages_per_seq * Hkv < 2^31.
+ *   workspace: attn_workspace_size(ATTN_OP_DECODE_KV4, B, Hq, Hkv, 0, D, ...) bytes, 256-byte aligned; contents on entry do not
+ *   matter. Calls that share a workspace must not overlap on the GPU.
+ * All three are launched with programmatic stream serialisation: they may be placed on the GPU while the kernel in front
+ * ends, and wait there for all earlier work of the stream before they read or write anything. attn_decode_kv4 enqueues two
+ * kernels, the second of which joins the pieces of requests that several blocks shared.
+ */
+ATTN_API int attn_kv4_append(const attn_bf16* k, const attn_bf16* v, const int32_t* slots, uint8_t* kv_cache, int T, int Hkv,
+                             int D, int page_size, int num_pages, long long k_stride, long long v_stride, void* stream);
+
+ATTN_API int attn_kv4_unpack(const uint8_t* kv_cache, const int32_t* pages, attn_bf16* k_pages, attn_bf16* v_pages, int n,
+                             int Hkv, int D, int page_size, int num_pages, void* stream);
+
+ATTN_API int attn_decode_kv4(const attn_bf16* q, const uint8_t* kv_cache, const int32_t* block_table, const int32_t* seq_lens,
+                             attn_bf16* o, float* lse, int B, int Hq, int Hkv, int D, int page_size, int max_pages_per_seq,
+                             int num_pages, float scale, int window, int sink, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
  * attn_workspace_size -- bytes of workspace an operation needs (0 if none).
  *   For ATTN_OP_BWD: B, Hq, S, D; for ATTN_OP_BWD_VARLEN pass B = 1 and S = total tokens.
- *   For ATTN_OP_DECODE_PAGED: B, Hq, Hkv, D. For ATTN_OP_QK_NORM_ROPE_BWD: D. For ATTN_OP_TREE_PAGED: Hq,
+ *   For ATTN_OP_DECODE_PAGED and ATTN_OP_DECODE_KV4: B, Hq, Hkv, D. For ATTN_OP_QK_NORM_ROPE_BWD: D. For ATTN_OP_TREE_PAGED: Hq,
  *   Hkv, S = max_q_len, D. Unused arguments are ignored. Returns 0 for an
  *   unknown op, and for a decode problem no decode kernel takes (D not 128 / 256, Hq not a
  *   supported multiple of Hkv), whose call is rejected anyway. Pure host arithmetic; needs no
