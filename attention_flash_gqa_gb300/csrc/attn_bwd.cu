@@ -469,7 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // (c_hi < c_lo when no key of the tile is allowed: every key is masked)
                     const int c_hi = min(kB - 1, min(qa, L - 1) - k0);
                     const int c_lo = a.window > 0 ? max(0, qa - a.window + 1 - k0) : 0;
-                    const int c_sink = a.sink.sink - k0;  // keys below it are visible past the window too
+                    uint32_t see[4];  // a bit a key
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) see[w] = allowed_bits(w, c_lo, c_hi, a.sink.sink - k0);
                     const bool edge = c_lo > 0 || c_hi < kB - 1;
                     uint32_t rr[128];
 #pragma unroll
@@ -484,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float p0 = fast_exp2(fmaf(__uint_as_float(rr[c]), a.scale_log2, -v));
                             float p1 = fast_exp2(fmaf(__uint_as_float(rr[c + 1]), a.scale_log2, -v));
                             if (decltype(masked)::value) {
-                                if ((c < c_lo && c >= c_sink) || c > c_hi) p0 = 0.f;
-                                if ((c + 1 < c_lo && c + 1 >= c_sink) || c + 1 > c_hi) p1 = 0.f;
+                                if (!(see[c >> 5] >> (c & 31) & 1u)) p0 = 0.f;
+                                if (!(see[c >> 5] >> ((c + 1) & 31) & 1u)) p1 = 0.f;
                             }
                             pk[c / 2] = pack_bf16x2(p0, p1);
                         }

@@ -573,12 +573,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool edge = (key0 + 63 > qp0) || (a.window > 0 && qp0 + kBQ - 1 - key0 >= a.window) ||
                                   (key0 + 64 > L);
                 if (edge) {
+                    // a bit a column: the row's bounds once, then one test for each score
+                    const int lo = a.window > 0 ? qi - a.window + 1 - key0 : 0, hi = min(qi, L - 1) - key0;
+                    const uint32_t see[2] = {allowed_bits(0, lo, hi, a.sink - key0), allowed_bits(1, lo, hi, a.sink - key0)};
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        const int key = key0 + c;
-                        const bool allowed = key <= qi && key < L && (a.window <= 0 || qi - key < a.window || key < a.sink);
-                        if (!allowed) s[c] = -INFINITY;
-                    }
+                    for (int c = 0; c < 64; ++c)
+                        if (!(see[c >> 5] >> (c & 31) & 1u)) s[c] = -INFINITY;
                 }
                 // this half's row max over eight independent partials
                 float m8[8];

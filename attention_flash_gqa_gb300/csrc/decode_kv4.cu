@@ -10,10 +10,15 @@
 //  * A unit is two chains of warp MMAs with the tokens, then the dims, as the 16 rows and the group's query heads as the 8
 //    columns: S^T = K Q^T, O^T += V^T P^T. (With the heads as rows, as the bf16 decode has them, at least half of
 //    each product would be rows of zeros.) Codes become bf16 operands in registers:
-//      K: 16 + code by shift and mask. The products of a group of 32 dims start from -24 sum(q) of the group, so that they are
-//         sums of q (code - 8), and the group's scale is applied to the score in fp32;
-//      V: (16 + code) s - 24 s in one fused multiply-add for two tokens, exact. P is rounded to bf16, as everywhere
-//         in this library; turned from columns to rows by movmatrix.
+//      K: by masking alone. Bits 4 .. 7 of a bf16 pattern whose other bits are zero are the number code * 2^-129 (below the
+//         smallest exponent and in the one after it the spacing is the same), bits 0 .. 3 are code * 2^-133. The missing powers
+//         of two sit in q, whose rows are brought to 2^120 at the start of a segment, and in the factor of the scores. The
+//         products of a group of 32 dims start from those of q with code 8, so that they are sums of q (code - 8),
+//         and the group's scale is applied to the score in fp32;
+//      V: low nibbles as 128 + code by mask and magic bits, from which 136 is taken before s is multiplied in, high nibbles
+//         masked, times 2^127 and (code / 4) 4 s - 8 s in one fused multiply-add; every step exact. Masks and shifts share a pipe
+//         that is half as wide as the instruction rate, multiplications have another one: so no shift but the one by 8.
+//         P is rounded to bf16, as everywhere in this library; turned from columns to rows by movmatrix.
 //    The softmax stays in registers (running maximum that moves only past 2^8, as in the bf16 decode).
 //  * A stretch may hold several (request, head) segments and begin and end inside one. What a warp finishes alone it writes
 //    out. The other pieces (o, m, l) meet in shared memory at the end of the block; those that begin or end
@@ -33,9 +38,9 @@ constexpr int kMaxG = 8;  // query heads of a KV head: the columns of an MMA
 
 template <int D>
 struct Cfg {
-    static constexpr int kWarps = D == 256 ? 8 : 12;
+    static constexpr int kWarps = D == 256 ? 8 : D == 128 ? 16 : 16;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kStages = D == 64 ? 8 : D == 128 ? 5 : 3;  // units on their way in each warp's ring
+    static constexpr int kStages = D == 64 ? 8 : D == 128 ? 4 : 3;  // units on their way in each warp's ring
     static constexpr int kRow = D + 4;                             // floats of a piece's row: o, m, l, padding
     static constexpr uint32_t kOffHead = kWarps * kStages * kv4_record_bytes(D);     // [warp][head][kRow]: first pieces
     static constexpr uint32_t kOffStart = kOffHead + kWarps * kMaxG * kRow * 4;      // [kMaxB + 1] pages before a request
@@ -99,6 +104,10 @@ __device__ __forceinline__ int req_len(const Args& a, int b, bool record) {
     if (record) atomicOr(a.status, DEVSTAT_BOUNDS);
     return L < 0 ? 0 : (int)cap;
 }
+
+constexpr uint32_t kLowNibbles = 0x000f000fu, kHighNibbles = 0x00f000f0u;
+// two bf16 numbers each
+constexpr uint32_t k4 = 0x40804080u, k128 = 0x43004300u, k2to127 = 0x7f007f00u, kMinus8 = 0xc100c100u, kMinus136 = 0xc308c308u;
 
 // A unit as its warp needs it.
 struct Unit {
@@ -175,8 +184,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
     const int blocks = min((int)gridDim.x, units);  // every one that takes part has a unit
     if ((int)blockIdx.x >= blocks) return;
     const long long all = (long long)blocks * C::kWarps;
-    const long long j = (long long)blockIdx.x * C::kWarps + warp;
-    const int u0 = (int)(j * units / all), u1 = (int)((j + 1) * units / all), n = u1 - u0;
+    const long long mine = (long long)blockIdx.x * C::kWarps + warp;
+    const int u0 = (int)(mine * units / all), u1 = (int)((mine + 1) * units / all), n = u1 - u0;
 
     auto unit_at = [&](int u) -> Unit {
         Unit r = {-1, -1, 0u};
@@ -208,15 +217,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
         return r;
     };
     const uint64_t policy = l2_policy_evict_first();  // every byte is read once
-    auto issue = [&](int i, const Unit& of) {  // the whole warp; `of`: the batch of 32 that unit i is in
-        const int page = __shfl_sync(0xffffffffu, of.page, i & 31);
-        const uint32_t see = __shfl_sync(0xffffffffu, of.see, i & 31);
-        if (lane == 0) {
-            const int s = i % C::kStages;
+    auto issue = [&](int i, int s, const Unit& of) {  // unit i into stage s; `of`: the batch of 32 that it is in
+        if (lane == (i & 31)) {  // the lane that has it
             const uint32_t bar = smem_u32(&full[s]);
-            if (page >= 0) {
+            if (of.page >= 0) {
                 mbar_expect_tx(bar, F::kRecord);
-                bulk_load_hint(smem_u32(ring + s * F::kRecord), a.cache + ((size_t)page * a.Hkv + (see >> 18)) * F::kRecord,
+                bulk_load_hint(smem_u32(ring + s * F::kRecord), a.cache + ((size_t)of.page * a.Hkv + (of.see >> 18)) * F::kRecord,
                                F::kRecord, bar, policy);
             } else {
                 mbar_arrive(bar);
@@ -225,12 +231,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
     };
 
     Unit cur = unit_at(u0 + lane), nxt = unit_at(u0 + 32 + lane);
-    for (int i = 0; i < C::kStages && i < n; ++i) issue(i, cur);
+    for (int i = 0; i < C::kStages && i < n; ++i) issue(i, i, cur);
 
-    uint32_t qf[kGroups][4];  // lane (g, c): head g, dims 8c .. 8c+7 of a group
-    float cq[kGroups][2];     // -24 sum of q over a group, heads 2c and 2c+1
+    uint32_t qf[kGroups][4];  // lane (g, c): head g, dims 8c .. 8c+7 of a group, scaled
+    float cq[kGroups][2];     // what a group's products start from, heads 2c and 2c+1
+    float factor[2];          // of a product of heads 2c and 2c+1: softmax scale and the powers of two, in log2 units
     float o[kBlocks][kTiles][4] = {};  // tile t: dims 128 block + (W/8) g + 2 t, + 1 of heads 2c, 2c+1: {(d, h), (d, h+1), (d+1, h), (d+1, h+1)}
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // heads 2c, 2c+1 (l: this lane's share)
+    float m_use[2] = {0.f, 0.f};                             // m, but 0 where nothing was seen yet
+    int segment = 0;
     bool began = false;  // the segment began in this stretch
     bool ok = true;
     int stage = 0;
@@ -274,31 +283,47 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
 
     for (int i = 0; i < n; ++i) {
         if (i > 0 && (i & 31) == 0) cur = nxt, nxt = unit_at(u0 + i + 32 + lane);
-        const int segment = __shfl_sync(0xffffffffu, cur.segment, i & 31);
         const uint32_t see = __shfl_sync(0xffffffffu, cur.see, i & 31);
         if (i == 0 || (see & (1u << 16))) {
             // ---- a new segment ----
             began = (see & (1u << 16)) != 0;
+            segment = __shfl_sync(0xffffffffu, cur.segment, i & 31);
             const uint16_t* row = a.q + ((size_t)segment * a.G + g) * D + 8 * c;
 #pragma unroll
             for (int gr = 0; gr < kGroups; ++gr) {
                 const uint4 w = g < a.G ? *reinterpret_cast<const uint4*>(row + 32 * gr) : make_uint4(0, 0, 0, 0);
                 qf[gr][0] = w.x, qf[gr][1] = w.y, qf[gr][2] = w.z, qf[gr][3] = w.w;
             }
+            // The row's largest exponent goes to 120 (by 2^123 at most): then a product with a code, some 2^-129 of it, is a
+            // normal number. Words that meet low nibbles get 2^4 more.
+            uint32_t top = 0;
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) top = max(top, max(qf[gr][x] & 0x7f80u, qf[gr][x] >> 16 & 0x7f80u));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int up = min(247 - (int)(top >> 7), 123);
+            const uint32_t by = (uint32_t)(up + 127) * 0x00800080u, by16 = by + 4 * 0x00800080u;
 #pragma unroll
             for (int gr = 0; gr < kGroups; ++gr) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) qf[gr][x] = bf16x2_mul(qf[gr][x], x & 1 ? by : by16);
                 float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma(d, kMinus24, kMinus24, kMinus24, kMinus24, qf[gr][0], qf[gr][1]);
-                mma(d, kMinus24, kMinus24, kMinus24, kMinus24, qf[gr][2], qf[gr][3]);
+                constexpr uint32_t kLow = 0x80088008u, kHigh = 0x80808080u;  // -8 * 2^-133, -8 * 2^-129
+                mma(d, kLow, kLow, kHigh, kHigh, qf[gr][0], qf[gr][1]);
+                mma(d, kLow, kLow, kHigh, kHigh, qf[gr][2], qf[gr][3]);
                 cq[gr][0] = d[0], cq[gr][1] = d[1];
             }
+            const float fac = fminf(ldexpf(a.scale_log2, 129 - up), 3e38f);
+            factor[0] = __shfl_sync(0xffffffffu, fac, 8 * c), factor[1] = __shfl_sync(0xffffffffu, fac, 8 * c + 4);
 #pragma unroll
             for (int bl = 0; bl < kBlocks; ++bl)
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[bl][t][e] = 0.f;
-            m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.f;
+            m[0] = m[1] = -INFINITY, m_use[0] = m_use[1] = l[0] = l[1] = 0.f;
         }
         if (ok) {
             ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, abort_flag, a.status, 0x61));
@@ -332,8 +357,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
                 for (int x = 0; x < F::kBlockGroups; ++x) {
                     const int gr = bl * F::kBlockGroups + x;
                     float d[4] = {cq[gr][0], cq[gr][1], cq[gr][0], cq[gr][1]};
-                    mma(d, kv4_pair(kw[0][x], 0), kv4_pair(kw[1][x], 0), kv4_pair(kw[0][x], 1), kv4_pair(kw[1][x], 1), qf[gr][0], qf[gr][1]);
-                    mma(d, kv4_pair(kw[0][x], 2), kv4_pair(kw[1][x], 2), kv4_pair(kw[0][x], 3), kv4_pair(kw[1][x], 3), qf[gr][2], qf[gr][3]);
+                    const uint32_t w0 = kw[0][x], w1 = kw[1][x], u0 = w0 >> 8, u1 = w1 >> 8;
+                    mma(d, w0 & kLowNibbles, w1 & kLowNibbles, w0 & kHighNibbles, w1 & kHighNibbles, qf[gr][0], qf[gr][1]);
+                    mma(d, u0 & kLowNibbles, u1 & kLowNibbles, u0 & kHighNibbles, u1 & kHighNibbles, qf[gr][2], qf[gr][3]);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const float sc = __uint_as_float(gr & 1 ? sw[r][gr / 2] & 0xffff0000u : sw[r][gr / 2] << 16);
@@ -342,14 +368,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] *= a.scale_log2;
+            for (int e = 0; e < 4; ++e) s[e] *= factor[e & 1];
             const bool whole = (see & 0xffffu) == 0xffffu;
             if (!whole) {
                 if (!(see >> g & 1u)) s[0] = s[1] = -INFINITY;
                 if (!(see >> (g + 8) & 1u)) s[2] = s[3] = -INFINITY;
             }
             // ---- softmax: the maximum moves only when a score is past it by more than 8 (p <= 2^8) ----
-            const bool over = s[0] > m[0] + 8.f || s[2] > m[0] + 8.f || s[1] > m[1] + 8.f || s[3] > m[1] + 8.f;
+            const bool over = fmaxf(s[0], s[2]) > m[0] + 8.f || fmaxf(s[1], s[3]) > m[1] + 8.f;
             if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -358,7 +384,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
                     for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                     const float to = mx > m[e] + 8.f ? mx : m[e];
                     const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - to);
-                    m[e] = to, l[e] *= f;
+                    m[e] = to, l[e] *= f, m_use[e] = to == -INFINITY ? 0.f : to;
 #pragma unroll
                     for (int bl = 0; bl < kBlocks; ++bl)
 #pragma unroll
@@ -368,8 +394,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
             float p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float mm = m[e & 1] == -INFINITY ? 0.f : m[e & 1];
-                p[e] = fast_exp2(s[e] - mm);  // (0 for -inf)
+                p[e] = fast_exp2(s[e] - m_use[e & 1]);  // (0 for -inf)
                 l[e & 1] += p[e];
             }
             // ---- O^T += V^T P^T ----
@@ -392,21 +417,28 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
                 }
                 const int gr = bl * F::kBlockGroups + g / (8 / F::kBlockGroups);
                 const uint32_t s0 = lds32(rec + F::value_scale(gr, 2 * c)) & hide0, s1 = lds32(rec + F::value_scale(gr, 2 * c + 8)) & hide1;
-                const uint32_t c0 = bf16x2_mul(s0, kMinus24), c1 = bf16x2_mul(s1, kMinus24);
+                const uint32_t f0 = bf16x2_mul(s0, k4), f1 = bf16x2_mul(s1, k4), c0 = bf16x2_mul(s0, kMinus8), c1 = bf16x2_mul(s1, kMinus8);
+                auto low = [](uint32_t x, uint32_t s) { return bf16x2_mul(bf16x2_add((x & kLowNibbles) | k128, kMinus136), s); };
+                auto high = [](uint32_t x, uint32_t f, uint32_t c) { return bf16x2_fma(bf16x2_mul(x & kHighNibbles, k2to127), f, c); };
 #pragma unroll
                 for (int half = 0; half < 2 * kWords; ++half) {  // 4 dims of both tokens side by side
                     const uint32_t sel = half & 1 ? 0x7632u : 0x5410u;
                     const uint32_t x0 = __byte_perm(vw[0][0][half / 2], vw[0][1][half / 2], sel);
                     const uint32_t x1 = __byte_perm(vw[1][0][half / 2], vw[1][1][half / 2], sel);
 #pragma unroll
-                    for (int d = 0; d < 4; d += 2)
-                        mma(o[bl][half * 2 + d / 2], bf16x2_fma(kv4_pair(x0, d), s0, c0), bf16x2_fma(kv4_pair(x0, d + 1), s0, c0),
-                            bf16x2_fma(kv4_pair(x1, d), s1, c1), bf16x2_fma(kv4_pair(x1, d + 1), s1, c1), b0, b1);
+                    for (int d = 0; d < 4; d += 2) {
+                        const uint32_t y0 = x0 >> (4 * d), y1 = x1 >> (4 * d);
+                        mma(o[bl][half * 2 + d / 2], low(y0, s0), high(y0, f0, c0), low(y1, s1), high(y1, f1, c1), b0, b1);
+                    }
                 }
             }
         }
         __syncwarp();  // the record has been read
-        if (ok && i + C::kStages < n) issue(i + C::kStages, (i + C::kStages) / 32 == i / 32 ? cur : nxt);
+        if (ok && i + C::kStages < n) {
+            const int j = i + C::kStages;
+            if ((j ^ i) < 32) issue(j, stage, cur);
+            else issue(j, stage, nxt);
+        }
         if (++stage == C::kStages) stage = 0, phase ^= 1u;
         const bool ends = (see & (1u << 17)) != 0, last = i + 1 == n;
         if (ends || last) {

@@ -513,6 +513,14 @@ __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t col) {
     return row * 128u + ((((col >> 3) ^ (row & 7u)) & 7u) << 4) + ((col & 7u) << 1);
 }
 
+// Bits 0 .. n - 1 of a word (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// Bits c of the columns 32 w + c of a score row that are allowed: up to `hi`, and from `lo` on or below `sink`.
+__device__ __forceinline__ uint32_t allowed_bits(int w, int lo, int hi, int sink) {
+    return low_bits(hi + 1 - 32 * w) & (~low_bits(lo - 32 * w) | low_bits(sink - 32 * w));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
