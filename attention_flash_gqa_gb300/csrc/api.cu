@@ -213,7 +213,7 @@ bool kv4_dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
 constexpr int kKv4MaxGrid = 256;  // blocks of a 4-bit decode at most
 size_t kv4_ws(int B, int Hq, int Hkv, int D) {
     if (B < 0 || B > 4096 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 8 || !kv4_dim_ok(D)) return 0;
-    return align256(attn::decode_kv4_workspace_bytes(B, Hq / Hkv, D, kKv4MaxGrid));
+    return align256(attn::decode_kv4_workspace_bytes(Hq / Hkv, D, kKv4MaxGrid));
 }
 
 bool tree_shape_ok(int Hq, int Hkv, int max_q, int D) {
@@ -825,6 +825,7 @@ int attn_decode_kv4(const attn_bf16* q, const uint8_t* kv_cache, const int32_t* 
     int st = check_common(Hq, Hkv, scale, 1, window);
     if (st || (st = check_sink(sink))) return st;
     if (!kv4_dim_ok(D) || Hq / Hkv > 8 || page_size != 16 || Hkv > 256 || B > 4096 || num_pages > (1 << 26) ||
+        max_pages_per_seq > (1 << 24) ||
         (long long)B * max_pages_per_seq * Hkv > 0x7fffffffLL)
         return ATTN_ERR_UNSUPPORTED;
     if (B == 0) return ATTN_OK;

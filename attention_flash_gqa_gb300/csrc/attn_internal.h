@@ -189,7 +189,7 @@ struct DecodeKv4Launch {
     int B, Hq, Hkv, D, max_pages, num_pages, window, sink, grid;
     float scale;
 };
-size_t decode_kv4_workspace_bytes(int B, int G, int D, int grid);
+size_t decode_kv4_workspace_bytes(int G, int D, int grid);
 cudaError_t launch_decode_kv4(const DecodeKv4Launch& L, cudaStream_t stream);
 
 }  // namespace attn

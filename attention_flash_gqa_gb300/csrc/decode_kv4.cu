@@ -13,11 +13,12 @@
 //      K: by masking alone. Bits 4 .. 7 of a bf16 pattern whose other bits are zero are the number code * 2^-129 (below the
 //         smallest exponent and in the one after it the spacing is the same), bits 0 .. 3 are code * 2^-133. The missing powers
 //         of two sit in q, whose rows are brought to 2^120 at the start of a segment, and in the factor of the scores. The
-//         products of a group of 32 dims start from those of q with code 8, so that they are sums of q (code - 8),
-//         and the group's scale is applied to the score in fp32;
-//      V: low nibbles as 128 + code by mask and magic bits, from which 136 is taken before s is multiplied in, high nibbles
-//         masked, times 2^127 and (code / 4) 4 s - 8 s in one fused multiply-add; every step exact. Masks and shifts share a pipe
-//         that is half as wide as the instruction rate, multiplications have another one: so no shift but the one by 8.
+//         scale of a group of 32 dims is applied to its part of the score in fp32, and 8 sum(q) s taken away for all groups by one
+//         more MMA;
+//      V: by masking too, and one fused multiply-add for two tokens: (code 2^-129) (s 2^(129 - down)) - 8 s 2^-down, exact (at
+//         least for s above 2^(down - 126)). `down`, 6 at first, follows the largest scale that a lane's dims have met, as the
+//         softmax's maximum does, so that the factor stays finite. Masks and shifts share a pipe that is half as wide as the
+//         instruction rate, multiplications have another one.
 //         P is rounded to bf16, as everywhere in this library; turned from columns to rows by movmatrix.
 //    The softmax stays in registers (running maximum that moves only past 2^8, as in the bf16 decode).
 //  * A stretch may hold several (request, head) segments and begin and end inside one. What a warp finishes alone it writes
@@ -34,20 +35,21 @@ namespace {
 
 constexpr int kPage = 16;
 constexpr int kMaxB = 4096;
+constexpr uint32_t kSmemLimit = 232448;
 constexpr int kMaxG = 8;  // query heads of a KV head: the columns of an MMA
 
 template <int D>
 struct Cfg {
-    static constexpr int kWarps = D == 256 ? 8 : D == 128 ? 16 : 16;
+    static constexpr int kWarps = D == 256 ? 8 : 16;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kStages = D == 64 ? 8 : D == 128 ? 4 : 3;  // units on their way in each warp's ring
+    static constexpr int kStages = D == 64 ? 8 : 4;  // units on their way in each warp's ring
     static constexpr int kRow = D + 4;                             // floats of a piece's row: o, m, l, padding
-    static constexpr uint32_t kOffHead = kWarps * kStages * kv4_record_bytes(D);     // [warp][head][kRow]: first pieces
-    static constexpr uint32_t kOffStart = kOffHead + kWarps * kMaxG * kRow * 4;      // [kMaxB + 1] pages before a request
-    static constexpr uint32_t kOffBar = kOffStart + (kMaxB + 8) * 4;                 // [warp][stage]
-    static constexpr uint32_t kOffMeta = kOffBar + kWarps * kStages * 8;             // abort flag, sums, segments of pieces
-    static constexpr uint32_t kSmem = kOffMeta + 4 * (4 + 3 * kWarps) + 128;         // + slack for the alignment
-    static_assert(kSmem <= 232448, "shared memory");
+    static constexpr uint32_t kOffBar = kWarps * kStages * kv4_record_bytes(D);  // [warp][stage]
+    static constexpr uint32_t kOffMeta = kOffBar + kWarps * kStages * 8;         // abort flag, sums, segments of pieces
+    static constexpr uint32_t kOffHead = kOffMeta + (4 * (4 + 3 * kWarps) + 15) / 16 * 16;  // [warp][G][kRow]: first pieces
+    // behind it [B + 1] pages before a request, and [B] their lengths where there is room
+    static uint32_t smem_bytes(int B, int G, bool lens) { return kOffHead + kWarps * G * kRow * 4 + (B + 1) * 4 + (lens ? B * 4 : 0) + 128; }
+    static_assert(kOffHead + kWarps * kMaxG * kRow * 4 + (kMaxB + 1) * 4 + 128 <= kSmemLimit, "shared memory");
     // a warp's last piece is put where its own ring was
     static_assert(kMaxG * kRow * 4 <= kStages * kv4_record_bytes(D), "ring");
 };
@@ -58,10 +60,10 @@ struct Args {
     const int32_t *block_table, *seq_lens;
     uint16_t* o;
     float* lse;
-    int32_t* start;  // [B + 1], for the second kernel
     float* part;     // [block][2][G][kRow]
     unsigned* status;
     int B, Hq, Hkv, G, max_pages, num_pages, window, sink;
+    bool lens_here;  // the lengths are kept in shared memory
     float scale_log2;
 };
 
@@ -73,6 +75,13 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same from zero: d = a b.
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // An 8 x 8 matrix of 16-bit values, lane (g, c) holding columns 2c, 2c+1 of row g, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -96,9 +105,15 @@ __device__ __forceinline__ int sink_pages(const Args& a, int L) { return min((a.
 __device__ __forceinline__ int seen_pages(const Args& a, int L) {
     return L > 0 ? (L - 1) / kPage - first_token(a, L) / kPage + 1 + sink_pages(a, L) : 0;
 }
+// A value that another kernel may be writing: read from L2, and again at every call.
+__device__ __forceinline__ int32_t load_l2(const int32_t* p) {
+    int32_t v;
+    asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 // Length of request b within its block-table row.
 __device__ __forceinline__ int req_len(const Args& a, int b, bool record) {
-    const int L = a.seq_lens[b];
+    const int L = load_l2(a.seq_lens + b);
     const long long cap = (long long)a.max_pages * kPage;
     if (L >= 0 && L <= cap) return L;
     if (record) atomicOr(a.status, DEVSTAT_BOUNDS);
@@ -106,25 +121,26 @@ __device__ __forceinline__ int req_len(const Args& a, int b, bool record) {
 }
 
 constexpr uint32_t kLowNibbles = 0x000f000fu, kHighNibbles = 0x00f000f0u;
-// two bf16 numbers each
-constexpr uint32_t k4 = 0x40804080u, k128 = 0x43004300u, k2to127 = 0x7f007f00u, kMinus8 = 0xc100c100u, kMinus136 = 0xc308c308u;
+// Least and largest exponent by which O's sums are kept down. Scales up to 2^(down - 6) times 16 times 2^(129 - down) are finite.
+constexpr int kDownMin = 6, kDownMax = 129;
 
 // A unit as its warp needs it.
 struct Unit {
-    int page;      // -1: outside the pool (reported, its tokens are not seen)
-    int segment;   // request * Hkv + head
-    uint32_t see;  // bits 0 .. 15: visible tokens; 16: first of its segment; 17: last; 18 ..: KV head
+    const uint8_t* record;  // null: its page id is outside the pool (reported, its tokens are not seen)
+    int segment;            // request * Hkv + head
+    uint32_t see;           // bits 0 .. 15: visible tokens; 16: first of its segment; 17: last
 };
 
-// Folds a piece (o, m, l) into (O, M, L): both are weighed by the larger maximum.
-template <int N>
-__device__ __forceinline__ void fold(float (&O)[N], float& M, float& L, const float* o, float m, float l) {
-    const float top = fmaxf(M, m);
-    const float wa = M == -INFINITY ? 0.f : fast_exp2(M - top), wb = m == -INFINITY ? 0.f : fast_exp2(m - top);
-#pragma unroll
-    for (int e = 0; e < N; ++e) O[e] = O[e] * wa + o[e] * wb;
-    L = L * wa + l * wb, M = top;
-}
+// `units` are shared out over `blocks`, the first units % blocks of which have one more.
+struct Share {
+    int each, more;
+    __device__ Share(int units, int blocks) : each(units / blocks), more(units - each * blocks) {}
+    __device__ int first(int k) const { return k * each + min(k, more); }
+    __device__ int owner(int u) const {  // the block that unit u is in
+        const int at = u - more * (each + 1);
+        return at < 0 ? u / (each + 1) : more + at / each;
+    }
+};
 
 __device__ __forceinline__ float log_sum(float M, float L) { return L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f; }
 
@@ -136,11 +152,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     float* head_piece = reinterpret_cast<float*>(smem + C::kOffHead);
-    int32_t* start = reinterpret_cast<int32_t*>(smem + C::kOffStart);
+    int32_t* start = reinterpret_cast<int32_t*>(head_piece + C::kWarps * a.G * C::kRow);
+    int32_t* lens = a.lens_here ? start + a.B + 1 : nullptr;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMeta);
     int* warp_sum = reinterpret_cast<int*>(smem + C::kOffMeta) + 4;
-    int* head_seg = warp_sum + C::kWarps;  // segment of a warp's first piece, -1: none
-    int* tail_seg = head_seg + C::kWarps;  // of its last
+    // a warp's first piece and its last one: segment << 2 | whether it ends in the warp's stretch | whether it began there; -1: none
+    int* head_piece_of = warp_sum + C::kWarps;
+    int* tail_piece = head_piece_of + C::kWarps;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
     uint8_t* ring = smem + warp * (C::kStages * F::kRecord);
@@ -148,47 +166,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
     if (tid == 0) *abort_flag = 0;
     if (lane == 0) {
         for (int s = 0; s < C::kStages; ++s) mbar_init(smem_u32(&full[s]), 1);
-        head_seg[warp] = tail_seg[warp] = -1;
+        head_piece_of[warp] = tail_piece[warp] = -1;
         fence_mbar_init();
     }
-    griddep_wait();
-    // the second kernel may be placed from here on; it waits for this one's end
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    // ---- pages before every request -------------------------------------------------------------
-    {
-        const int per = (a.B + C::kThreads - 1) / C::kThreads, b0 = tid * per;
-        int mine = 0;
-        for (int b = b0; b < min(a.B, b0 + per); ++b) mine += seen_pages(a, req_len(a, b, blockIdx.x == 0));
-        int v = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int n = __shfl_up_sync(0xffffffffu, v, off);
-            if (lane >= off) v += n;
-        }
-        if (lane == 31) warp_sum[warp] = v;
-        __syncthreads();
-        int at = v - mine;
-        for (int w = 0; w < warp; ++w) at += warp_sum[w];
-        for (int b = b0; b < min(a.B, b0 + per); ++b) {
-            start[b] = at;
-            at += seen_pages(a, req_len(a, b, false));
-        }
-        if (b0 < a.B && b0 + per >= a.B) start[a.B] = at;
-        __syncthreads();
-        if (blockIdx.x == 0)
-            for (int b = tid; b <= a.B; b += C::kThreads) a.start[b] = start[b];
-    }
-    // ---- this block's and this warp's stretch -----------------------------------------------------
-    const int units = start[a.B] * a.Hkv;
-    const int blocks = min((int)gridDim.x, units);  // every one that takes part has a unit
-    if ((int)blockIdx.x >= blocks) return;
-    const long long all = (long long)blocks * C::kWarps;
-    const long long mine = (long long)blockIdx.x * C::kWarps + warp;
-    const int u0 = (int)(mine * units / all), u1 = (int)((mine + 1) * units / all), n = u1 - u0;
-
-    auto unit_at = [&](int u) -> Unit {
-        Unit r = {-1, -1, 0u};
+    const uint64_t policy = l2_policy_evict_first();  // every byte is read once
+    int u0 = 0, u1 = 0, n = 0;  // the warp's stretch
+    const int32_t* entry = nullptr;  // of the last unit worked out: its block-table entry and what it held
+    int entry_page = -1;
+    auto unit_at = [&](int u, bool record) -> Unit {
+        Unit r = {nullptr, -1, 0u};
+        entry = nullptr;
         if (u >= u1) return r;
         int lo = 0, hi = a.B - 1;  // the last request that starts at or before u: it has pages
         while (lo < hi) {
@@ -198,52 +185,123 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
         }
         const int np = start[lo + 1] - start[lo], rem = u - start[lo] * a.Hkv;
         const int h = rem / np, i = rem - h * np;
-        const int L = req_len(a, lo, false);
+        const int L = lens ? lens[lo] : req_len(a, lo, false);
         const int first = first_token(a, L), early = sink_pages(a, L);
         const int p = i < early ? i : first / kPage + i - early;
         const int end = min(kPage, (i < early ? a.sink : L) - p * kPage);
-        uint32_t see = (1u << end) - 1u;
-        if (i == early) {  // the window's first page: tokens before the window are seen only if they are sinks
-            const int keep = max(0, min(kPage, a.sink - p * kPage));
-            see &= ~((1u << (first % kPage)) - 1u) | ((1u << (a.window > 0 ? keep : 0)) - 1u);
-        }
-        r.page = a.block_table[(size_t)lo * a.max_pages + p];
-        if (r.page < 0 || r.page >= a.num_pages) {
-            if (h == 0) atomicOr(a.status, DEVSTAT_BOUNDS);
-            r.page = -1, see = 0u;
+        uint32_t see = low_bits(end);
+        // the window's first page: tokens before the window are seen only if they are sinks
+        if (i == early) see &= ~low_bits(first % kPage) | low_bits(a.sink - p * kPage);
+        entry = a.block_table + (size_t)lo * a.max_pages + p, entry_page = load_l2(entry);
+        if (entry_page >= 0 && entry_page < a.num_pages) {
+            r.record = a.cache + ((size_t)entry_page * a.Hkv + h) * F::kRecord;
+        } else {
+            if (record) atomicOr(a.status, DEVSTAT_BOUNDS);
+            see = 0u;
         }
         r.segment = lo * a.Hkv + h;
-        r.see = see | (i == 0 ? 1u << 16 : 0u) | (i == np - 1 ? 1u << 17 : 0u) | ((uint32_t)h << 18);
+        r.see = see | (i == 0 ? 1u << 16 : 0u) | (i == np - 1 ? 1u << 17 : 0u);
         return r;
     };
-    const uint64_t policy = l2_policy_evict_first();  // every byte is read once
-    auto issue = [&](int i, int s, const Unit& of) {  // unit i into stage s; `of`: the batch of 32 that it is in
-        if (lane == (i & 31)) {  // the lane that has it
+    auto issue = [&](int first, int count, const uint8_t* record) {  // units first .. first + count - 1: by the lanes that have them
+        const int x = (lane - first) & 31;
+        if (x < count) {
+            const int s = (uint32_t)(first + x) % C::kStages;
             const uint32_t bar = smem_u32(&full[s]);
-            if (of.page >= 0) {
+            if (record) {
                 mbar_expect_tx(bar, F::kRecord);
-                bulk_load_hint(smem_u32(ring + s * F::kRecord), a.cache + ((size_t)of.page * a.Hkv + (of.see >> 18)) * F::kRecord,
-                               F::kRecord, bar, policy);
+                bulk_load_hint(smem_u32(ring + s * F::kRecord), record, F::kRecord, bar, policy);
             } else {
                 mbar_arrive(bar);
             }
         }
     };
 
-    Unit cur = unit_at(u0 + lane), nxt = unit_at(u0 + 32 + lane);
-    for (int i = 0; i < C::kStages && i < n; ++i) issue(i, i, cur);
+    // ---- the layout: pages before every request, the warp's stretch and its first units -----------------
+    // Launched with programmatic serialisation the block may be here before the kernel in front ends. Lengths, block table and
+    // cache may be what that one writes, so what counts is read after griddep_wait; but with up to a request a thread the
+    // layout is made before it, on a guess, from lengths and page ids as they are in L2, and the first records asked for
+    // there. After the wait the first copies start by that layout, and while they are on their way what it was made
+    // from is read again; if anything differs the copies are waited for and all of it is done anew.
+    const bool guess = lens && a.B <= C::kThreads;
+    Unit nxt = {};
+    uint32_t flip = 0;  // 1: the barriers are a phase ahead
+    for (bool sure = !guess;;) {
+        if (!guess) griddep_wait();
+        const int per = (a.B + C::kThreads - 1) / C::kThreads, b0 = tid * per;
+        int mine = 0;
+        for (int b = b0; b < min(a.B, b0 + per); ++b) {
+            const int L = req_len(a, b, sure && blockIdx.x == 0);
+            if (lens) lens[b] = L;
+            mine += seen_pages(a, L);
+        }
+        int v = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, v, off);
+            if (lane >= off) v += y;
+        }
+        if (lane == 31) warp_sum[warp] = v;
+        __syncthreads();
+        int at = v - mine;
+        for (int w = 0; w < warp; ++w) at += warp_sum[w];
+        for (int b = b0; b < min(a.B, b0 + per); ++b) {
+            start[b] = at;
+            at += per == 1 ? mine : seen_pages(a, lens ? lens[b] : req_len(a, b, false));
+        }
+        if (b0 < a.B && b0 + per >= a.B) start[a.B] = at;
+        __syncthreads();
+        const int units = start[a.B] * a.Hkv;
+        const int blocks = min((int)gridDim.x, units);  // every one that takes part has a unit
+        u0 = u1 = n = 0;
+        if ((int)blockIdx.x < blocks) {
+            const Share share(units, blocks);
+            const int first = share.first(blockIdx.x), many = share.first(blockIdx.x + 1) - first;
+            // (a block's units times its warps stay within 32 bits: 2^31 units are at least 152 blocks')
+            u0 = first + (int)((uint32_t)many * warp / C::kWarps), u1 = first + (int)((uint32_t)many * (warp + 1) / C::kWarps);
+            n = u1 - u0;
+        }
+        nxt = unit_at(u0 + lane, sure);
+        if (!sure) {
+            if (lane < min(n, C::kStages) && nxt.record) prefetch_bulk(nxt.record, F::kRecord);
+            griddep_wait();
+        }
+        issue(0, min(n, C::kStages), nxt.record);
+        if (sure) break;
+        bool same = true, bad = false;
+        if (tid < a.B) {
+            const int L = load_l2(a.seq_lens + tid);
+            const bool within = L >= 0 && L <= (long long)a.max_pages * kPage;
+            same = lens[tid] == (within ? L : L < 0 ? 0 : a.max_pages * kPage), bad = !within;
+        }
+        if (entry) same &= load_l2(entry) == entry_page, bad |= !nxt.record;
+        same = __syncthreads_and(same);
+        if (same && bad) atomicOr(a.status, DEVSTAT_BOUNDS);
+        if (same) break;
+        if (lane == 0)
+            for (int s = 0; s < C::kStages; ++s) {
+                if (s >= n) mbar_arrive(smem_u32(&full[s]));
+                mbar_drain(smem_u32(&full[s]), 0, a.status, 0x63);
+            }
+        __syncwarp();
+        flip = 1, sure = true;
+    }
+    // the second kernel may be placed from here on; it waits for this one's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     uint32_t qf[kGroups][4];  // lane (g, c): head g, dims 8c .. 8c+7 of a group, scaled
-    float cq[kGroups][2];     // what a group's products start from, heads 2c and 2c+1
+    uint32_t eight[3];        // operand (b0, b1, and b0 of a second step) of the product that takes the codes' 8 away
     float factor[2];          // of a product of heads 2c and 2c+1: softmax scale and the powers of two, in log2 units
-    float o[kBlocks][kTiles][4] = {};  // tile t: dims 128 block + (W/8) g + 2 t, + 1 of heads 2c, 2c+1: {(d, h), (d, h+1), (d+1, h), (d+1, h+1)}
+    // tile t: dims 128 block + (W/8) g + 2 t, + 1 of heads 2c, 2c+1: {(d, h), (d, h+1), (d+1, h), (d+1, h+1)}, times 2^-down
+    float o[kBlocks][kTiles][4] = {};
+    int down[kBlocks];
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // heads 2c, 2c+1 (l: this lane's share)
     float m_use[2] = {0.f, 0.f};                             // m, but 0 where nothing was seen yet
     int segment = 0;
     bool began = false;  // the segment began in this stretch
     bool ok = true;
-    int stage = 0;
-    uint32_t phase = 0;
+    Unit cur = nxt;
+    int described = 1;  // batches of 32 units
 
     // this lane's values of head 2c + e, dims of block bl in order
     auto out_value = [&](int bl, int e, int d) -> float { return o[bl][d >> 1][(d & 1) * 2 + e]; };
@@ -261,7 +319,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
             if (g == 0) row[D] = l[e] == l[e] ? m[e] : INFINITY, row[D + 1] = l[e];  // (NaN: whatever it is joined with)
         }
     };
-    auto write_result = [&](int segment) {
+    auto write_result = [&]() {
         const size_t row0 = (size_t)segment * a.G;  // query head h G of request b: b Hq + h G
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -281,12 +339,19 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
         }
     };
 
-    for (int i = 0; i < n; ++i) {
-        if (i > 0 && (i & 31) == 0) cur = nxt, nxt = unit_at(u0 + i + 32 + lane);
-        const uint32_t see = __shfl_sync(0xffffffffu, cur.see, i & 31);
-        if (i == 0 || (see & (1u << 16))) {
+    // Two units at a time where the second one is of the same segment and of the same batch of 32: what is done once for a unit
+    // beside its products (flags, waits, the next copies) costs a quarter of the instructions of a page.
+    for (int i = 0, step; i < n; i += step) {
+        if (32 * described <= i + 16) {  // a batch is worked out half a batch ahead
+            nxt = unit_at(u0 + 32 * described + lane, true);
+            ++described;
+        }
+        if ((i & 31) == 0) cur = nxt;
+        const uint32_t flags = __shfl_sync(0xffffffffu, cur.see, i & 31), flags2 = __shfl_sync(0xffffffffu, cur.see, (i + 1) & 31);
+        step = i + 1 < n && (i & 31) != 31 && !(flags & (1u << 17)) ? 2 : 1;
+        if (i == 0 || (flags & (1u << 16))) {
             // ---- a new segment ----
-            began = (see & (1u << 16)) != 0;
+            began = (flags & (1u << 16)) != 0;
             segment = __shfl_sync(0xffffffffu, cur.segment, i & 31);
             const uint16_t* row = a.q + ((size_t)segment * a.G + g) * D + 8 * c;
 #pragma unroll
@@ -305,6 +370,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int up = min(247 - (int)(top >> 7), 123);
             const uint32_t by = (uint32_t)(up + 127) * 0x00800080u, by16 = by + 4 * 0x00800080u;
+            float minus[kGroups];  // -8 sum of q over a group, head g, in the units of the products
 #pragma unroll
             for (int gr = 0; gr < kGroups; ++gr) {
 #pragma unroll
@@ -313,21 +379,45 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
                 constexpr uint32_t kLow = 0x80088008u, kHigh = 0x80808080u;  // -8 * 2^-133, -8 * 2^-129
                 mma(d, kLow, kLow, kHigh, kHigh, qf[gr][0], qf[gr][1]);
                 mma(d, kLow, kLow, kHigh, kHigh, qf[gr][2], qf[gr][3]);
-                cq[gr][0] = d[0], cq[gr][1] = d[1];
+                const float even = __shfl_sync(0xffffffffu, d[0], g >> 1), odd = __shfl_sync(0xffffffffu, d[1], g >> 1);
+                minus[gr] = g & 1 ? odd : even;
+            }
+            {
+                // Taken away through an MMA whose columns are groups: scales (exact) times these sums in three bf16 parts, which
+                // hold all 24 bits. Column 2c (and 2c + 1) of a step: group pair kPair(c) of part kPart(c).
+                float x0 = minus[0], x1 = minus[1];
+#pragma unroll
+                for (int w = 1; w < kGroups / 2; ++w)
+                    if (c % (kGroups / 2) == w) x0 = minus[2 * w], x1 = minus[2 * w + 1];
+                uint32_t part[3];
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    part[x] = pack_bf16x2(x0, x1);
+                    x0 -= __uint_as_float(part[x] << 16), x1 -= __uint_as_float(part[x] & 0xffff0000u);
+                }
+                if (kGroups == 8) eight[0] = part[0], eight[1] = part[1], eight[2] = part[2];
+                else if (kGroups == 4) eight[0] = c < 2 ? part[0] : part[1], eight[1] = c < 2 ? part[2] : 0u;
+                else eight[0] = c == 0 ? part[0] : c == 1 ? part[1] : c == 2 ? part[2] : 0u, eight[1] = 0u;
             }
             const float fac = fminf(ldexpf(a.scale_log2, 129 - up), 3e38f);
             factor[0] = __shfl_sync(0xffffffffu, fac, 8 * c), factor[1] = __shfl_sync(0xffffffffu, fac, 8 * c + 4);
 #pragma unroll
-            for (int bl = 0; bl < kBlocks; ++bl)
+            for (int bl = 0; bl < kBlocks; ++bl) {
+                down[bl] = kDownMin;
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[bl][t][e] = 0.f;
+            }
             m[0] = m[1] = -INFINITY, m_use[0] = m_use[1] = l[0] = l[1] = 0.f;
         }
+#pragma unroll 1
+        for (int x = i; x < i + step; ++x) {
+        const uint32_t see = x == i ? flags : flags2;
+        const int stage = (uint32_t)x % C::kStages, phase = ((uint32_t)x / C::kStages & 1) ^ flip;
         if (ok) {
             ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, abort_flag, a.status, 0x61));
-            if (!ok && lane == 0) ring_drain(full, stage, (int)phase, C::kStages, n - i, a.status, 0x62);
+            if (!ok && lane == 0) ring_drain(full, stage, phase, C::kStages, n - x, a.status, 0x62);
             __syncwarp();
         }
         if (!ok) {  // given up: the rows of this unit and of those behind it in the stretch are NaN
@@ -335,7 +425,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
         } else if (see & 0xffffu) {
             const uint32_t rec = smem_u32(ring + stage * F::kRecord);
             // ---- S^T: tokens g and g + 8, heads 2c and 2c + 1 ----
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            float s[4];
+            {
+                const int w = 2 * (c % (kGroups / 2));
+                const uint32_t a0 = lds32(rec + F::key_scale(g, w)), a1 = lds32(rec + F::key_scale(g + 8, w));
+                mma0(s, a0, a1, a0, a1, eight[0], eight[1]);
+                if (kGroups == 8) mma(s, a0, a1, a0, a1, eight[2], 0u);
+            }
             uint32_t sw[2][kGroups / 2];  // scales of tokens g, g + 8: two groups a word
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -356,10 +452,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
 #pragma unroll
                 for (int x = 0; x < F::kBlockGroups; ++x) {
                     const int gr = bl * F::kBlockGroups + x;
-                    float d[4] = {cq[gr][0], cq[gr][1], cq[gr][0], cq[gr][1]};
-                    const uint32_t w0 = kw[0][x], w1 = kw[1][x], u0 = w0 >> 8, u1 = w1 >> 8;
-                    mma(d, w0 & kLowNibbles, w1 & kLowNibbles, w0 & kHighNibbles, w1 & kHighNibbles, qf[gr][0], qf[gr][1]);
-                    mma(d, u0 & kLowNibbles, u1 & kLowNibbles, u0 & kHighNibbles, u1 & kHighNibbles, qf[gr][2], qf[gr][3]);
+                    float d[4];
+                    const uint32_t w0 = kw[0][x], w1 = kw[1][x], y0 = w0 >> 8, y1 = w1 >> 8;
+                    mma0(d, w0 & kLowNibbles, w1 & kLowNibbles, w0 & kHighNibbles, w1 & kHighNibbles, qf[gr][0], qf[gr][1]);
+                    mma(d, y0 & kLowNibbles, y1 & kLowNibbles, y0 & kHighNibbles, y1 & kHighNibbles, qf[gr][2], qf[gr][3]);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const float sc = __uint_as_float(gr & 1 ? sw[r][gr / 2] & 0xffff0000u : sw[r][gr / 2] << 16);
@@ -375,12 +471,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
                 if (!(see >> (g + 8) & 1u)) s[2] = s[3] = -INFINITY;
             }
             // ---- softmax: the maximum moves only when a score is past it by more than 8 (p <= 2^8) ----
-            const bool over = fmaxf(s[0], s[2]) > m[0] + 8.f || fmaxf(s[1], s[3]) > m[1] + 8.f;
-            if (__any_sync(0xffffffffu, over)) {
+            const float top0 = fmaxf(s[0], s[2]), top1 = fmaxf(s[1], s[3]);
+            if (__any_sync(0xffffffffu, top0 > m[0] + 8.f || top1 > m[1] + 8.f)) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(s[e], s[e + 2]);
-#pragma unroll
+                    float mx = e ? top1 : top0;
+#pragma unroll 1
                     for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                     const float to = mx > m[e] + 8.f ? mx : m[e];
                     const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - to);
@@ -417,9 +513,25 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
                 }
                 const int gr = bl * F::kBlockGroups + g / (8 / F::kBlockGroups);
                 const uint32_t s0 = lds32(rec + F::value_scale(gr, 2 * c)) & hide0, s1 = lds32(rec + F::value_scale(gr, 2 * c + 8)) & hide1;
-                const uint32_t f0 = bf16x2_mul(s0, k4), f1 = bf16x2_mul(s1, k4), c0 = bf16x2_mul(s0, kMinus8), c1 = bf16x2_mul(s1, kMinus8);
-                auto low = [](uint32_t x, uint32_t s) { return bf16x2_mul(bf16x2_add((x & kLowNibbles) | k128, kMinus136), s); };
-                auto high = [](uint32_t x, uint32_t f, uint32_t c) { return bf16x2_fma(bf16x2_mul(x & kHighNibbles, k2to127), f, c); };
+                // a scale whose exponent is above what `down` allows: bit 15 of its half
+                const uint32_t past = (0x8000u - ((uint32_t)(down[bl] + 122) << 7)) * 0x10001u;
+                if (__any_sync(0xffffffffu, (((s0 & 0x7fff7fffu) + past) | ((s1 & 0x7fff7fffu) + past)) & 0x80008000u)) {
+                    uint32_t e = max(max(s0 & 0x7f80u, s0 >> 16 & 0x7f80u), max(s1 & 0x7f80u, s1 >> 16 & 0x7f80u)) >> 7;
+                    e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));  // the four lanes of a row
+                    e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
+                    const int to = (int)e > down[bl] + 121 ? min((int)e - 121 + 8, kDownMax) : down[bl];
+                    const float f = to - down[bl] > 126 ? 0.f : __int_as_float((127 - (to - down[bl])) << 23);
+                    down[bl] = to;
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[bl][t][x] *= f;
+                }
+                const uint32_t up_high = (uint32_t)(256 - down[bl]) * 0x00800080u;  // 2^(129 - down)
+                const uint32_t fh0 = bf16x2_mul(s0, up_high), fh1 = bf16x2_mul(s1, up_high);
+                const uint32_t up_low = up_high + 4 * 0x00800080u, minus8 = (up_high - 126 * 0x00800080u) | 0x80008000u;  // -8 * 2^-down
+                const uint32_t fl0 = bf16x2_mul(s0, up_low), fl1 = bf16x2_mul(s1, up_low);
+                const uint32_t c0 = bf16x2_mul(s0, minus8), c1 = bf16x2_mul(s1, minus8);
 #pragma unroll
                 for (int half = 0; half < 2 * kWords; ++half) {  // 4 dims of both tokens side by side
                     const uint32_t sel = half & 1 ? 0x7632u : 0x5410u;
@@ -428,111 +540,129 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
 #pragma unroll
                     for (int d = 0; d < 4; d += 2) {
                         const uint32_t y0 = x0 >> (4 * d), y1 = x1 >> (4 * d);
-                        mma(o[bl][half * 2 + d / 2], low(y0, s0), high(y0, f0, c0), low(y1, s1), high(y1, f1, c1), b0, b1);
+                        mma(o[bl][half * 2 + d / 2], bf16x2_fma(y0 & kLowNibbles, fl0, c0), bf16x2_fma(y0 & kHighNibbles, fh0, c0),
+                            bf16x2_fma(y1 & kLowNibbles, fl1, c1), bf16x2_fma(y1 & kHighNibbles, fh1, c1), b0, b1);
                     }
                 }
             }
         }
-        __syncwarp();  // the record has been read
-        if (ok && i + C::kStages < n) {
-            const int j = i + C::kStages;
-            if ((j ^ i) < 32) issue(j, stage, cur);
-            else issue(j, stage, nxt);
         }
-        if (++stage == C::kStages) stage = 0, phase ^= 1u;
-        const bool ends = (see & (1u << 17)) != 0, last = i + 1 == n;
+        __syncwarp();  // the records have been read
+        if (ok && i + C::kStages < n)
+            issue(i + C::kStages, min(step, n - i - C::kStages), lane >= (i & 31) ? cur.record : nxt.record);
+        const bool ends = ((step == 2 ? flags2 : flags) & (1u << 17)) != 0, last = i + step == n;
         if (ends || last) {
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-#pragma unroll
+#pragma unroll 1
                 for (int off = 4; off < 32; off <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
+#pragma unroll
+            for (int bl = 0; bl < kBlocks; ++bl) {
+                const float f = __int_as_float((127 + down[bl] / 2) << 23), f2 = __int_as_float((127 + down[bl] - down[bl] / 2) << 23);
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[bl][t][x] = o[bl][t][x] * f * f2;
+            }
             if (began && ends) {
-                write_result(segment);
-            } else if (!last) {  // it began in an earlier stretch
-                write_piece(head_piece + warp * kMaxG * C::kRow);
-                if (lane == 0) head_seg[warp] = segment;
-            } else {
-                write_piece(reinterpret_cast<float*>(ring));
-                if (lane == 0) tail_seg[warp] = segment;
+                write_result();
+            } else {  // its first piece, of a segment that began in an earlier stretch; or what is left at the end
+                write_piece(last ? reinterpret_cast<float*>(ring) : head_piece + warp * a.G * C::kRow);
+                if (lane == 0) (last ? tail_piece : head_piece_of)[warp] = segment << 2 | (ends ? 2 : 0) | (began ? 1 : 0);
             }
         }
     }
     __syncthreads();
     // ---- pieces of a segment that lie in this block: joined by the warp that has the first ------------
-    const int first_unit = (int)((long long)blockIdx.x * units / blocks), end_unit = (int)((long long)(blockIdx.x + 1) * units / blocks);
-    auto finish = [&](int w, bool head) {  // from warp w's piece on, in the order of the warps
-        const int segment = head ? head_seg[w] : tail_seg[w];
-        int more = 0;  // pieces behind the first: last pieces of warps that the segment fills, then a first piece
-        const int b = segment / a.Hkv, h = segment - b * a.Hkv, np = start[b + 1] - start[b];
-        const int s0 = start[b] * a.Hkv + h * np, s1 = s0 + np;
-        if (!head) more = C::kWarps - 1 - w;
-        const bool whole = s0 >= first_unit && s1 <= end_unit;
-        float* slot = a.part + ((size_t)blockIdx.x * 2 + (s0 < first_unit ? 0 : 1)) * a.G * C::kRow;
+    // Pieces: lanes 0 .. 15 have the warps' last ones, lanes 16 .. 31 their first ones. Those of one segment are the last pieces of
+    // warps that it fills or opens in, and the first piece of the warp that it ends in; the warps share out the heads of all segments.
+    const int piece = (lane & 15) < C::kWarps ? (lane < 16 ? tail_piece[lane] : head_piece_of[lane - 16]) : -1;
+    const uint32_t alike = __match_any_sync(0xffffffffu, piece >> 2);
+    uint32_t leads = __ballot_sync(0xffffffffu, piece >= 0 && __ffs(alike) - 1 == lane);  // one lane for each segment
+    const float* rows = lane < 16 ? reinterpret_cast<const float*>(smem + lane * (C::kStages * F::kRecord))
+                                  : head_piece + (lane - 16) * a.G * C::kRow;
+    const int tasks = __popc(leads) * a.G;
+    for (int task = warp, at = 0; task < tasks; task += C::kWarps) {
+        for (; at < task / a.G; ++at) leads &= leads - 1;  // the segment of this task
+        const int hh = task % a.G, seg = __shfl_sync(0xffffffffu, piece, __ffs(leads) - 1) >> 2;
+        const bool mine = piece >> 2 == seg;
+        uint32_t members = __ballot_sync(0xffffffffu, mine);
+        const bool begins = __any_sync(0xffffffffu, mine && (piece & 1)), ends = __any_sync(0xffffffffu, mine && (piece & 2));
         constexpr int N = D / 32;
-        for (int hh = 0; hh < a.G; ++hh) {
-            float O[N] = {}, M = -INFINITY, L = 0.f;
-            auto take = [&](const float* rows) {
-                const float* row = rows + hh * C::kRow;
-                float x[N];
+        const float pm = mine ? rows[hh * C::kRow + D] : -INFINITY, pl = mine ? rows[hh * C::kRow + D + 1] : 0.f;
+        float M = pm;
 #pragma unroll
-                for (int e = 0; e < N; e += 2) *reinterpret_cast<float2*>(x + e) = *reinterpret_cast<const float2*>(row + N * lane + e);
-                fold<N>(O, M, L, x, row[D], row[D + 1]);
-            };
-            take(head ? head_piece + w * kMaxG * C::kRow : reinterpret_cast<const float*>(smem + w * (C::kStages * F::kRecord)));
-            for (int x = w + 1; x <= w + more; ++x) {
-                if (head_seg[x] == segment) {
-                    take(head_piece + x * kMaxG * C::kRow);
-                    break;
+        for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        const float weight = pm == -INFINITY ? 0.f : fast_exp2(pm - M);
+        float L = weight * pl, O[N] = {};
+#pragma unroll
+        for (int off = 16; off; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+        while (members) {  // four pieces at a time (the last one again, with weight 0, where there are fewer)
+            float w[4], x[4][N];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int from = members ? __ffs(members) - 1 : 0;
+                const float there = __shfl_sync(0xffffffffu, weight, from);
+                w[k] = members ? there : 0.f;
+                const float* row = (from < 16 ? reinterpret_cast<const float*>(smem + from * (C::kStages * F::kRecord))
+                                              : head_piece + (from - 16) * a.G * C::kRow) + hh * C::kRow + N * lane;
+#pragma unroll
+                for (int e = 0; e < N; e += 2) {
+                    const float2 y = members ? *reinterpret_cast<const float2*>(row + e) : make_float2(0.f, 0.f);
+                    x[k][e] = y.x, x[k][e + 1] = y.y;
                 }
-                if (tail_seg[x] == segment) take(reinterpret_cast<const float*>(smem + x * (C::kStages * F::kRecord)));
+                members &= members - 1;
             }
-            const size_t at = (size_t)segment * a.G + hh;
-            if (whole) {
-                const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-                for (int e = 0; e < N; e += 2) *reinterpret_cast<uint32_t*>(a.o + at * D + N * lane + e) = pack_bf16x2(O[e] * inv, O[e + 1] * inv);
-                if (lane == 0) a.lse[at] = log_sum(M, L);
-            } else {
-                float* row = slot + hh * C::kRow;
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int e = 0; e < N; e += 2) *reinterpret_cast<float2*>(row + N * lane + e) = make_float2(O[e], O[e + 1]);
-                if (lane == 0) row[D] = L == L ? M : INFINITY, row[D + 1] = L;
-            }
+                for (int e = 0; e < N; ++e) O[e] = fmaf(w[k], x[k][e], O[e]);
         }
-    };
-    if (head_seg[warp] >= 0) {
-        // a first piece stands alone if no earlier warp of the block has one of its segment
-        bool alone = true;
-        for (int w = 0; w < warp; ++w) alone &= tail_seg[w] != head_seg[warp];
-        if (alone) finish(warp, true);
-    }
-    if (tail_seg[warp] >= 0) {
-        bool opens = true;
-        for (int w = 0; w < warp; ++w) opens &= tail_seg[w] != tail_seg[warp];
-        if (opens) finish(warp, false);
+        const size_t out = (size_t)seg * a.G + hh;
+        if (begins && ends) {
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+            for (int e = 0; e < N; e += 2) *reinterpret_cast<uint32_t*>(a.o + out * D + N * lane + e) = pack_bf16x2(O[e] * inv, O[e + 1] * inv);
+            if (lane == 0) a.lse[out] = log_sum(M, L);
+        } else {
+            // at most two segments of a block reach past it: slot 0 the one that began before it
+            float* row = a.part + (((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * a.G + hh) * C::kRow;
+#pragma unroll
+            for (int e = 0; e < N; e += 2) *reinterpret_cast<float2*>(row + N * lane + e) = make_float2(O[e], O[e + 1]);
+            if (lane == 0) row[D] = L == L ? M : INFINITY, row[D + 1] = L;
+        }
     }
 }
 
-struct JoinArgs {
-    const float* part;
-    const int32_t* start;
-    uint16_t* o;
-    float* lse;
-    int B, Hkv, G, grid;
-};
-
 // Joins the pieces of the segments that several blocks of the decode kernel shared, a block for each segment; the others are done,
-// but for the rows of requests without a key, which come out as o = 0, lse = -inf. A thread has 4 dims of a head and folds up to 8 pieces
-// with all their loads on the way at once.
+// but for the rows of requests without a key, which come out as o = 0, lse = -inf. Which pieces there are follows from the lengths
+// alone, inputs of the call, so that it is known before the decode kernel ends. A thread has 4 dims of a head; 8 pieces are on their
+// way at once.
 template <int D>
-__global__ void __launch_bounds__(128) decode_kv4_join_kernel(JoinArgs a) {
+__global__ void __launch_bounds__(128) decode_kv4_join_kernel(Args a, int grid) {
     using C = Cfg<D>;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    griddep_wait();
-    const int segment = blockIdx.x, b = segment / a.Hkv, h = segment - b * a.Hkv;
-    const int first = a.start[b], np = a.start[b + 1] - first, units = a.start[a.B] * a.Hkv;
+    const int segment = blockIdx.x, b = segment / a.Hkv, h = segment - b * a.Hkv, lane = threadIdx.x & 31;
+    int first = 0, units = 0;
+    for (int i = lane; i < a.B; i += 32) {
+        const int np = seen_pages(a, req_len(a, i, false));
+        units += np;
+        if (i < b) first += np;
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+        first += __shfl_xor_sync(0xffffffffu, first, off);
+        units += __shfl_xor_sync(0xffffffffu, units, off);
+    }
+    units *= a.Hkv;
+    const int np = seen_pages(a, req_len(a, b, false));
     const int items = a.G * (D / 4);
     const size_t row0 = (size_t)segment * a.G;
+    const int s0 = first * a.Hkv + h * np, s1 = s0 + np;
+    const Share share(max(units, 1), max(min(grid, units), 1));
+    const int kf = share.owner(s0), kl = share.owner(max(s1 - 1, s0));
+    const int opens = s0 < share.first(kf) ? 0 : 1;  // a block's first slot holds what began before it
+    griddep_wait();
     if (np == 0) {
         for (int it = threadIdx.x; it < items; it += 128) {
             *reinterpret_cast<uint2*>(a.o + row0 * D + 4 * it) = make_uint2(0, 0);
@@ -540,10 +670,6 @@ __global__ void __launch_bounds__(128) decode_kv4_join_kernel(JoinArgs a) {
         }
         return;
     }
-    const int s0 = first * a.Hkv + h * np, s1 = s0 + np;
-    const long long blocks = min(a.grid, units);
-    // the block that unit u belongs to: block k has units floor(k units / blocks) ..
-    const int kf = (int)(((s0 + 1) * blocks - 1) / units), kl = (int)((s1 * blocks - 1) / units);
     if (kf == kl) return;
     for (int it = threadIdx.x; it < items; it += 128) {
         const int hh = it / (D / 4), d = 4 * (it % (D / 4));
@@ -551,22 +677,26 @@ __global__ void __launch_bounds__(128) decode_kv4_join_kernel(JoinArgs a) {
         for (int k0 = kf; k0 <= kl; k0 += 8) {
             float4 x[8];
             float2 ml[8];
+            float top = M;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 x[j] = make_float4(0.f, 0.f, 0.f, 0.f), ml[j] = make_float2(-INFINITY, 0.f);
                 const int k = k0 + j;
                 if (k <= kl) {
-                    // a block's first slot holds what began before it
-                    const int which = s0 < (int)(k * (long long)units / blocks) ? 0 : 1;
-                    const float* row = a.part + (((size_t)k * 2 + which) * a.G + hh) * C::kRow;
+                    const float* row = a.part + (((size_t)k * 2 + (k == kf ? opens : 0)) * a.G + hh) * C::kRow;
                     x[j] = __ldcg(reinterpret_cast<const float4*>(row + d));
                     ml[j] = __ldcg(reinterpret_cast<const float2*>(row + D));
                 }
             }
 #pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, ml[j].x);
+            const float keep = M == -INFINITY ? 0.f : fast_exp2(M - top);
+            O[0] *= keep, O[1] *= keep, O[2] *= keep, O[3] *= keep, L *= keep, M = top;
+#pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float y[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                fold<4>(O, M, L, y, ml[j].x, ml[j].y);
+                const float w = ml[j].x == -INFINITY ? 0.f : fast_exp2(ml[j].x - top);
+                O[0] = fmaf(w, x[j].x, O[0]), O[1] = fmaf(w, x[j].y, O[1]), O[2] = fmaf(w, x[j].z, O[2]), O[3] = fmaf(w, x[j].w, O[3]);
+                L = fmaf(w, ml[j].y, L);
             }
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -575,19 +705,18 @@ __global__ void __launch_bounds__(128) decode_kv4_join_kernel(JoinArgs a) {
     }
 }
 
-size_t start_bytes(int B) { return ((size_t)(B + 1) * 4 + 255) & ~size_t(255); }
-
 template <int D>
 cudaError_t launch_t(const DecodeKv4Launch& L, cudaStream_t stream) {
     using C = Cfg<D>;
     Args a;
     a.q = L.q, a.cache = L.cache, a.block_table = L.block_table, a.seq_lens = L.seq_lens, a.o = L.o, a.lse = L.lse;
-    a.start = static_cast<int32_t*>(L.workspace);
-    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(L.workspace) + start_bytes(L.B));
+    a.part = static_cast<float*>(L.workspace);
     a.status = L.status, a.B = L.B, a.Hq = L.Hq, a.Hkv = L.Hkv, a.G = L.Hq / L.Hkv;
     a.max_pages = L.max_pages, a.num_pages = L.num_pages, a.window = L.window, a.sink = L.window > 0 ? L.sink : 0;
     a.scale_log2 = L.scale * 1.4426950408889634f;
-    cudaError_t e = cudaFuncSetAttribute(decode_kv4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    a.lens_here = C::smem_bytes(L.B, a.G, true) <= kSmemLimit;
+    // (the limit belongs to the kernel: the same in every call, whatever other threads call it with)
+    cudaError_t e = cudaFuncSetAttribute(decode_kv4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -595,7 +724,7 @@ cudaError_t launch_t(const DecodeKv4Launch& L, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(L.grid);
     cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.dynamicSmemBytes = C::smem_bytes(L.B, a.G, a.lens_here);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -603,20 +732,18 @@ cudaError_t launch_t(const DecodeKv4Launch& L, cudaStream_t stream) {
     e = cudaLaunchKernelEx(&cfg, decode_kv4_kernel<D>, a);
     prof_end(stream, mark);
     if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
-    JoinArgs ja;
-    ja.part = a.part, ja.start = a.start, ja.o = L.o, ja.lse = L.lse, ja.B = L.B, ja.Hkv = L.Hkv, ja.G = a.G, ja.grid = L.grid;
     cfg.gridDim = dim3(L.B * L.Hkv);
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
     mark = prof_begin(stream, "decode_kv4_join");
-    e = cudaLaunchKernelEx(&cfg, decode_kv4_join_kernel<D>, ja);
+    e = cudaLaunchKernelEx(&cfg, decode_kv4_join_kernel<D>, a, L.grid);
     prof_end(stream, mark);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-size_t decode_kv4_workspace_bytes(int B, int G, int D, int grid) { return start_bytes(B) + (size_t)grid * 2 * G * (D + 4) * 4; }
+size_t decode_kv4_workspace_bytes(int G, int D, int grid) { return (size_t)grid * 2 * G * (D + 4) * 4; }
 
 cudaError_t launch_decode_kv4(const DecodeKv4Launch& L, cudaStream_t stream) {
     if (L.D == 64) return launch_t<64>(L, stream);

@@ -475,7 +475,8 @@ ATTN_API int attn_tree_paged(const attn_bf16* q, const attn_bf16* k_cache, const
  *
  * attn_decode_kv4 -- attn_decode_paged_sink over the values that the cache stands for: one new query token a request, q [B, Hq, D],
  * block_table, seq_lens, window, sink, o and lse as there. K is used as it is, in products of fp32; P is rounded to bf16 for the
- * product with V, as in the other attention calls. Hidden tokens' bytes may be anything. A request with L = 0 gets o = 0 and
+ * product with V, as in the other attention calls. V is used as it is but for values below 2^-120 (or 2^-112 of the largest of their
+ * group of dims), which round to multiples of 2^-127 (2^-119 of that one). An infinity in q makes its row NaN. Hidden tokens' bytes may be anything. A request with L = 0 gets o = 0 and
  * lse = -inf; a row with a NaN score gets NaN for both. Page ids outside [0, num_pages) and lengths outside the block-table
  * row are reported as ATTN_ERR_DEVICE_BOUNDS, their tokens skipped.
  *   Supported: D in {64, 128, 256}, Hq / Hkv in 1 .. 8, Hkv <= 256, B <= 4096, page_size = 16, num_pages <= 2^26,

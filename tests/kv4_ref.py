@@ -95,7 +95,9 @@ def decode(q, cache, table, lens, scale, window=0, sink=0):
     The exponential is zero below 2^-126 (a subnormal result is flushed). It is taken relative to a running maximum that the row's
     largest score is never more than 2^8 below (the maximum only moves to scores that are there, and each piece is scaled to the
     largest of them), so the sum of the p is at least 2^-8 and a weight is off by 2^-118 at most, o by 2^-118 sum|v|. A result
-    below 2^-126 rounds to a multiple of 2^-133.
+    below 2^-126 rounds to a multiple of 2^-133. V enters the product times 2^-down, where a bf16 number below 2^-126 is a multiple of
+    2^-133: a value of V is off by 2^(down - 134) at most, and only if it is below 2^(down - 126). down is 6 or, with e the exponent of
+    the largest scale (2^e or more), at most e + 127 - 121 + 8 = e + 14 (bf16 holds e + 127): 2^-128, or 2^-120 of that scale.
     """
     B, Hq, D = q.shape
     Hkv = cache.shape[1]
@@ -120,6 +122,6 @@ def decode(q, cache, table, lens, scale, window=0, sink=0):
         y = torch.logsumexp(s, 1)
         p = (s - y[:, None]).exp()
         o[b], lse[b] = torch.einsum("hn,hnd->hd", p, v), y
-        to[b] = (BF + 2 * e + 2 * L * U)[:, None] * torch.einsum("hn,hnd->hd", p, v.abs()) + BF * o[b].abs() + 2.0 ** -118 * v.abs().sum(1) + 2.0 ** -134
+        to[b] = (BF + 2 * e + 2 * L * U)[:, None] * torch.einsum("hn,hnd->hd", p, v.abs()) + BF * o[b].abs() + 2.0 ** -118 * v.abs().sum(1) + 2.0 ** -134 + 2.0 ** -128 + 2.0 ** -120 * v.abs().amax()
         tl[b] = e + L * U + 2.0 ** -21 * (1 + y.abs())
     return o, to, lse, tl
