@@ -696,9 +696,8 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
                 }
                 __syncwarp();
                 // o update: add this lane's tokens
-                const int tmax = nt < 8 ? nt : 8;
-                for (int t = !(SINK && tsink > 0) && tlo > 0 ? tlo : 0; t < tmax; ++t) {  // only the warp's visible tokens
-                    if (SINK && t < tlo && t >= tsink) continue;
+                const int tmax = nt < 8 ? nt : 8, tfirst = !(SINK && tsink > 0) && tlo > 0 ? tlo : 0;
+                for (int t = tfirst; t < tmax; t = SINK && t + 1 == tsink && tlo > tsink ? tlo : t + 1) {  // only the warp's visible tokens
                     const uint8_t* vrow = vp + ((size_t)((TPW * half + t) * a.hb + gl) * D + dim0) * 2;
                     float vv[QD];
                     const uint4 w = *reinterpret_cast<const uint4*>(vrow);
