@@ -222,21 +222,13 @@ def _workspace(nbytes: int, device, zero: bool, key: str):
     return buf
 
 
-def _call_workspace(nbytes: int, device, stream):
-    """A workspace of one call, from the memory of its stream (or of the graph that it is captured into): calls on different
-    streams, or in different graphs, share none."""
-    import torch
-
-    if stream is None:
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-
-
 def attn_fwd(q, k, v, o=None, lse=None, *, causal: bool = True, window: int = 0, scale: float | None = None,
              stream=None, sink: int = 0):
     """Forward of causal (optionally sliding-window) GQA attention, dense [B, S, H, D] layout. With a window the
     sequence's first ``sink`` keys (0 to 128) stay visible to every later query."""
+    if sink:
+        scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+        return (_bound or _native()).fwd_sink(q, k, v, None, 0, o, lse, causal, window, sink, scale, stream)
     import torch
 
     B, S, Hq, D = q.shape
@@ -247,9 +239,8 @@ def attn_fwd(q, k, v, o=None, lse=None, *, causal: bool = True, window: int = 0,
     if lse is None:
         lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
     with torch.cuda.device(q.device):  # the library works on the current device
-        rc = load_library().attn_fwd_sink(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse), B, Hq, Hkv,
-                                          S, D, scale, int(causal), int(window), int(sink), None, 0,
-                                          _stream_ptr(stream, q.device))
+        rc = load_library().attn_fwd(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse), B, Hq, Hkv,
+                                     S, D, scale, int(causal), int(window), None, 0, _stream_ptr(stream, q.device))
     _check(rc, "attn_fwd")
     return o, lse
 
@@ -258,6 +249,9 @@ def attn_fwd_varlen(q, k, v, cu_seqlens, max_seqlen: int, o=None, lse=None, *, c
                     scale: float | None = None, stream=None, sink: int = 0):
     """Forward over packed sequences: q [T, Hq, D], k/v [T, Hkv, D], cu_seqlens int32 [n+1] on the device; ``sink`` as in
     attn_fwd, for each sequence."""
+    if sink:
+        scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+        return (_bound or _native()).fwd_sink(q, k, v, cu_seqlens, max_seqlen, o, lse, causal, window, sink, scale, stream)
     import torch
 
     T, Hq, D = q.shape
@@ -270,9 +264,9 @@ def attn_fwd_varlen(q, k, v, cu_seqlens, max_seqlen: int, o=None, lse=None, *, c
     if lse is None:
         lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
     with torch.cuda.device(q.device):  # the library works on the current device
-        rc = load_library().attn_fwd_varlen_sink(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse),
+        rc = load_library().attn_fwd_varlen(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse),
                                             _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, int(max_seqlen), Hq, Hkv, D,
-                                            scale, int(causal), int(window), int(sink), None, 0, _stream_ptr(stream, q.device))
+                                            scale, int(causal), int(window), None, 0, _stream_ptr(stream, q.device))
     _check(rc, "attn_fwd_varlen")
     return o, lse
 
@@ -333,6 +327,10 @@ def attn_merge_lse(o_parts, lse_parts, o=None, lse=None, *, stream=None):
 def attn_bwd(q, k, v, o, lse, dO, dq=None, dk=None, dv=None, *, causal: bool = True, window: int = 0,
              scale: float | None = None, cu_seqlens=None, max_seqlen: int = 0, workspace=None, stream=None, sink: int = 0):
     """Gradients (dQ, dK, dV). Dense [B,S,H,D] when cu_seqlens is None, else packed [T,H,D]; ``sink`` as in the forward."""
+    if sink:
+        scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+        return (_bound or _native()).bwd_sink(q, k, v, o, lse, dO, dq, dk, dv, causal, window, sink, scale, cu_seqlens, max_seqlen, workspace,
+                                            stream)
     import torch
 
     if cu_seqlens is None:
@@ -348,15 +346,12 @@ def attn_bwd(q, k, v, o, lse, dO, dq=None, dk=None, dv=None, *, causal: bool = T
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     need = attn_workspace_size(ATTN_OP_BWD if cu_seqlens is None else ATTN_OP_BWD_VARLEN, B, Hq, Hkv, S, D, nseq)
-    if sink and window > 0:
-        need = int(load_library().attn_bwd_sink_workspace_size(B, Hq, Hkv, S, D, nseq, int(window), int(sink)))
-        workspace = _call_workspace(need, q.device, stream) if workspace is None else workspace
     if workspace is None:
         workspace = _workspace(need, q.device, False, "bwd")
     with torch.cuda.device(q.device):  # the library works on the current device
-        rc = load_library().attn_bwd_sink(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse),
+        rc = load_library().attn_bwd(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse),
                                      _bf16(dO, "dO"), _bf16(dq, "dQ"), _bf16(dk, "dK"), _bf16(dv, "dV"), B, Hq, Hkv, S, D,
-                                     scale, int(causal), int(window), int(sink), _ptr(cu_seqlens), nseq, int(max_seqlen),
+                                     scale, int(causal), int(window), _ptr(cu_seqlens), nseq, int(max_seqlen),
                                      _ptr(workspace), workspace.numel() * workspace.element_size(),
                                      _stream_ptr(stream, q.device))
     _check(rc, "attn_bwd")
@@ -367,6 +362,9 @@ def attn_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=No
                       window: int = 0, workspace=None, stream=None, sink: int = 0):
     """Single-token decode: q [B,Hq,D], caches [pages,16,Hkv,D], block_table int32 [B,max_pages], seq_lens int32 [B];
     window > 0: the query sees only the last `window` keys, and the request's first `sink` ones (0 to 128)."""
+    if sink:
+        scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+        return (_bound or _native()).decode_paged_sink(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale, window, sink, workspace, stream)
     import torch
 
     B, Hq, D = q.shape
@@ -380,15 +378,13 @@ def attn_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=No
     if lse is None:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     need = attn_workspace_size(ATTN_OP_DECODE_PAGED, B, Hq, Hkv, 0, D)
-    if workspace is None and sink and window > 0:
-        workspace = _call_workspace(need, q.device, stream)
     if workspace is None:
         workspace = _workspace(need, q.device, False, "decode")
     with torch.cuda.device(q.device):  # the library works on the current device
-        rc = load_library().attn_decode_paged_sink(_bf16(q, "q"), _bf16(k_cache, "k_cache"), _bf16(v_cache, "v_cache"),
+        rc = load_library().attn_decode_paged(_bf16(q, "q"), _bf16(k_cache, "k_cache"), _bf16(v_cache, "v_cache"),
                                               _ptr(block_table), _ptr(seq_lens), _bf16(o, "o"), _ptr(lse), B, Hq, Hkv, D,
                                               page_size, block_table.shape[1], num_pages, scale, int(window),
-                                              int(sink), _ptr(workspace),
+                                              _ptr(workspace),
                                               workspace.numel() * workspace.element_size(), _stream_ptr(stream, q.device))
     _check(rc, "attn_decode_paged")
     return o, lse

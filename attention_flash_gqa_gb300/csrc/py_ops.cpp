@@ -26,6 +26,11 @@ struct Api {
     decltype(&attn_qk_norm_rope_bwd) norm_rope_bwd = nullptr;
     decltype(&attn_qk_norm_rope_paged) norm_rope_paged = nullptr;
     decltype(&attn_tree_paged) tree_paged = nullptr;
+    decltype(&attn_fwd_sink) fwd_sink = nullptr;
+    decltype(&attn_fwd_varlen_sink) fwd_varlen_sink = nullptr;
+    decltype(&attn_bwd_sink) bwd_sink = nullptr;
+    decltype(&attn_bwd_sink_workspace_size) bwd_sink_workspace_size = nullptr;
+    decltype(&attn_decode_paged_sink) decode_paged_sink = nullptr;
     decltype(&attn_kv4_append) kv4_append = nullptr;
     decltype(&attn_kv4_unpack) kv4_unpack = nullptr;
     decltype(&attn_decode_kv4) decode_kv4 = nullptr;
@@ -483,6 +488,118 @@ PyObject* tree_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// ---- windows with sinks ------------------------------------------------------------------------
+// q, k, v of a prompt, dense [B, S, H, D] (cu_seqlens None) or packed [T, H, D].
+struct Prompt {
+    const at::Tensor &q, &k;
+    int idx, B = 1, S, Hq, Hkv, D, nseq = 0, top = 0;
+    attn_bf16 *qp, *kp, *vp;
+    const int32_t* cu = nullptr;
+    Prompt(PyObject* q_, PyObject* k_, PyObject* v_, PyObject* cu_, PyObject* top_)
+        : q(tensor(q_, "q")), k(tensor(k_, "k")), idx(index_of(q, "q")) {
+        const bool packed = cu_ != Py_None;
+        const auto sq = q.sizes(), sk = k.sizes();
+        const size_t n = packed ? 3 : 4;
+        if (sq.size() != n || sk.size() != n || sk[n - 1] != sq[n - 1] || sk[0] != sq[0] || (!packed && sk[1] != sq[1]))
+            refuse(packed ? "%s must be [T, H, D], of the same tokens and head size" : "%s must be [B, S, H, D], of the same tokens and head size", "q and k");
+        for (const auto x : sq)
+            if (x > INT32_MAX) refuse("%s is too large", "q");
+        if (sk[n - 2] > INT32_MAX) refuse("%s is too large", "k");
+        if (!packed) B = (int)sq[0];
+        S = (int)sq[n - 3], Hq = (int)sq[n - 2], Hkv = (int)sk[n - 2], D = (int)sq[n - 1];
+        qp = bf16(q, sq, idx, "q"), kp = bf16(k, sk, idx, "k"), vp = bf16(tensor(v_, "v"), sk, idx, "v");
+        if (packed) {
+            const int64_t m = tensor(cu_, "cu_seqlens").numel(), sc[1] = {m};
+            if (m < 1 || m > INT32_MAX) refuse("%s must have an entry more than there are sequences", "cu_seqlens");
+            cu = i32(cu_, sc, idx, "cu_seqlens"), nseq = (int)m - 1, top = as_int(top_, "max_seqlen");
+        }
+    }
+    // lse [B, Hq, S], or [Hq, T]
+    float* lse(PyObject* given, Result* r, const Place* place) const {
+        const int64_t dense[3] = {B, Hq, S};
+        const at::IntArrayRef shape = cu ? at::IntArrayRef(dense + 1, 2) : at::IntArrayRef(dense, 3);
+        if (r) {
+            r->given = given;
+            if (given == Py_None) r->made = place->make(shape, at::kFloat);
+        }
+        return checked<float>(given == Py_None && r ? r->made : tensor(given, "lse"), at::kFloat, shape, idx, "lse");
+    }
+};
+
+// (q, k, v, cu_seqlens, max_seqlen, o, lse, causal, window, sink, scale, stream)
+PyObject* fwd_sink(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 12, [&]() -> PyObject* {
+        const Prompt x(a[0], a[1], a[2], a[3], a[4]);
+        const int causal = as_bool(a[7]), window = as_int(a[8], "window"), sink = as_int(a[9], "sink");
+        const float scale = as_float(a[10]);
+        Place place(a[11], x.idx);
+        Result r[2];
+        attn_bf16* o = like(r[0], a[5], x.q, place, "o");
+        float* lse = x.lse(a[6], &r[1], &place);
+        if (x.cu)
+            check(g_api.fwd_varlen_sink(x.qp, x.kp, x.vp, o, lse, x.cu, x.nseq, x.S, x.top, x.Hq, x.Hkv, x.D, scale, causal, window,
+                                        sink, nullptr, 0, place.stream),
+                  "attn_fwd_varlen");
+        else
+            check(g_api.fwd_sink(x.qp, x.kp, x.vp, o, lse, x.B, x.Hq, x.Hkv, x.S, x.D, scale, causal, window, sink, nullptr, 0,
+                                 place.stream),
+                  "attn_fwd");
+        return tuple(r);
+    });
+}
+
+// (q, k, v, o, lse, dO, dq, dk, dv, causal, window, sink, scale, cu_seqlens, max_seqlen, workspace, stream)
+PyObject* bwd_sink(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 17, [&]() -> PyObject* {
+        const Prompt x(a[0], a[1], a[2], a[13], a[14]);
+        const attn_bf16 *o = bf16(tensor(a[3], "o"), x.q.sizes(), x.idx, "o"), *dO = bf16(tensor(a[5], "dO"), x.q.sizes(), x.idx, "dO");
+        const float* lse = x.lse(a[4], nullptr, nullptr);
+        const int causal = as_bool(a[9]), window = as_int(a[10], "window"), sink = as_int(a[11], "sink");
+        const float scale = as_float(a[12]);
+        Place place(a[16], x.idx);
+        Result r[3];
+        attn_bf16 *dq = like(r[0], a[6], x.q, place, "dQ"), *dk = like(r[1], a[7], x.k, place, "dK"), *dv = like(r[2], a[8], x.k, place, "dV");
+        at::Tensor own;
+        size_t bytes = 0;
+        void* ws = scratch(own, bytes, a[15], g_api.bwd_sink_workspace_size(x.B, x.Hq, x.Hkv, x.S, x.D, x.nseq, window, sink), place);
+        check(g_api.bwd_sink(x.qp, x.kp, x.vp, o, lse, dO, dq, dk, dv, x.B, x.Hq, x.Hkv, x.S, x.D, scale, causal, window, sink, x.cu,
+                             x.nseq, x.top, ws, bytes, place.stream),
+              "attn_bwd");
+        return tuple(r);
+    });
+}
+
+// (q, k_cache, v_cache, block_table, seq_lens, o, lse, scale, window, sink, workspace, stream)
+PyObject* decode_paged_sink(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 12, [&]() -> PyObject* {
+        const at::Tensor& q = tensor(a[0], "q");
+        const int idx = index_of(q, "q");
+        if (q.dim() != 3 || q.size(0) > INT32_MAX || q.size(1) > INT32_MAX || q.size(2) > INT32_MAX) refuse("%s must be [B, Hq, D]", "q");
+        const int64_t B = q.size(0), Hq = q.size(1), D = q.size(2);
+        attn_bf16* qp = bf16(q, q.sizes(), idx, "q");
+        const Caches c(a[1], a[2], D, idx);
+        const at::Tensor& table = tensor(a[3], "block_table");
+        if (table.dim() != 2 || table.size(1) > INT32_MAX) refuse("%s must be [B, max_pages]", "block_table");
+        const int64_t sB[1] = {B}, sTab[2] = {B, table.size(1)}, sL[2] = {B, Hq};
+        const int32_t *tab = i32(a[3], sTab, idx, "block_table"), *lens = i32(a[4], sB, idx, "seq_lens");
+        const float scale = as_float(a[7]);
+        const int window = as_int(a[8], "window"), sink = as_int(a[9], "sink");
+        Place place(a[11], idx);
+        Result r[2];
+        attn_bf16* o = like(r[0], a[5], q, place, "o");
+        r[1].given = a[6];
+        if (a[6] == Py_None) r[1].made = place.make(sL, at::kFloat);
+        float* lse = checked<float>(a[6] == Py_None ? r[1].made : tensor(a[6], "lse"), at::kFloat, sL, idx, "lse");
+        at::Tensor own;
+        size_t bytes = 0;
+        void* ws = scratch(own, bytes, a[10], g_api.workspace_size(ATTN_OP_DECODE_PAGED, (int)B, (int)Hq, c.heads, 0, (int)D, 0, 0), place);
+        check(g_api.decode_paged_sink(qp, c.k, c.v, tab, lens, o, lse, (int)B, (int)Hq, c.heads, (int)D, c.page_size, (int)table.size(1),
+                                      c.num_pages, scale, window, sink, ws, bytes, place.stream),
+              "attn_decode_paged");
+        return tuple(r);
+    });
+}
+
 // ---- 4-bit paged cache -------------------------------------------------------------------------
 // A cache uint8 [num_pages, Hkv, 18, D].
 struct Kv4Cache {
@@ -602,6 +719,11 @@ PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
     find(api.norm_rope_bwd, "attn_qk_norm_rope_bwd");
     find(api.norm_rope_paged, "attn_qk_norm_rope_paged");
     find(api.tree_paged, "attn_tree_paged");
+    find(api.fwd_sink, "attn_fwd_sink");
+    find(api.fwd_varlen_sink, "attn_fwd_varlen_sink");
+    find(api.bwd_sink, "attn_bwd_sink");
+    find(api.bwd_sink_workspace_size, "attn_bwd_sink_workspace_size");
+    find(api.decode_paged_sink, "attn_decode_paged_sink");
     find(api.kv4_append, "attn_kv4_append");
     find(api.kv4_unpack, "attn_kv4_unpack");
     find(api.decode_kv4, "attn_decode_kv4");
@@ -616,7 +738,7 @@ PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define ATTN_OP(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {ATTN_OP(load),           ATTN_OP(paged_plan), ATTN_OP(norm_rope), ATTN_OP(norm_rope_bwd),
-                          ATTN_OP(norm_rope_paged), ATTN_OP(tree_paged), ATTN_OP(kv4_append), ATTN_OP(kv4_unpack),
+                          ATTN_OP(norm_rope_paged), ATTN_OP(tree_paged), ATTN_OP(fwd_sink), ATTN_OP(bwd_sink), ATTN_OP(decode_paged_sink), ATTN_OP(kv4_append), ATTN_OP(kv4_unpack),
                           ATTN_OP(decode_kv4),      {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
