@@ -52,6 +52,9 @@ constexpr int kThreads = 448;
 constexpr int kEw = 256;  // elementwise threads
 constexpr uint32_t kSub = 16384;  // 128 rows x 64 bf16, 128-byte swizzle
 constexpr float kLog2e = 1.4426950408889634f;
+// P is held times 2^15: at most 1, it then fits fp16 with all of its bits down to 2^-29. dS is formed from that (three bits more
+// than from the bf16 P that dV's product takes); dV, dK and dQ have the factor taken out where they leave tensor memory.
+constexpr float kPUp = 15.f, kPDown = 1.f / 32768.f;
 
 // D: head dim (the contraction of S^T and dP^T); DS: the columns of dV / dK / dQ this CTA owns.
 // DS = D (64, 128): K and V resident, one ring slot per Q or dO tile. DS = 128 < D = 256
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const int h = g * G + t / n_qt;
             const int q0 = (i_begin + t % n_qt) * kB;
-            const float f = (q0 + j < L) ? a.scale : 0.f;  // rows past the sequence end add zeros
+            const float f = (q0 + j < L) ? a.scale * kPDown : 0.f;  // rows past the sequence end add zeros
             // the whole row into registers first, so dQ's columns are handed back at once (at
             // D = 128 the next dP^T waits for them)
             uint32_t rq[DS];
@@ -551,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int h = g * G + t / n_qt;
             const int qa = (i_begin + t % n_qt) * kB + (tid & 127);
             const size_t lbase = a.cu_seqlens ? (size_t)h * a.T + seq_start : ((size_t)seq * a.Hq + h) * a.S;
-            if (tid < 128) return qa < L ? a.lse[lbase + qa] * kLog2e : INFINITY;  // +inf: P = 0 past the end
+            if (tid < 128) return qa < L ? fmaf(a.lse[lbase + qa], kLog2e, -kPUp) : INFINITY;  // +inf: P = 0 past the end
             return qa < L ? a.delta[lbase + qa] : 0.f;
         };
         float vnext = fetch(0);
@@ -564,21 +567,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 32 score columns at a time; this half's P columns [64 hf + 16c, +16) overwrite
             // scores of its own first chunk, already read
             ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(s_full), t & 1, abort_flag, a.status, 0x4b));
-            uint32_t pk[32];
+            uint32_t ph[32];  // P^T times 2^15 in fp16
             if (ok) {
                 tc_fence_after();
                 const bool edge = !(k0 + kB - 1 <= q0 && (a.window <= 0 || q0 + kB - 1 - k0 < a.window) &&
                                     q0 + kB <= L && k0 + kB <= L);
-                // on edge tiles key j sees the queries qa with 0 <= qa - kabs < span
+                // on edge tiles key j is seen by the queries kabs .. qhi - 1
                 int qhi = key_ok ? L : kabs;
                 if (a.window > 0 && kabs >= a.sink.sink) qhi = min(qhi, kabs + a.window);
-                const unsigned span = qhi > kabs ? (unsigned)(qhi - kabs) : 0u;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int col0 = 64 * hf + 32 * c;  // first query column of the chunk
                     uint32_t rr[32];
                     tmem_ld32(tR0 + col0 + lane_base, rr);
                     tmem_ld_wait();
+                    uint32_t w[16];
+                    const uint32_t see = low_bits(qhi - (q0 + col0)) & ~low_bits(kabs - (q0 + col0));  // a bit a query
                     auto p_chunk = [&](auto masked) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
@@ -588,17 +592,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int u = 0; u < 4; ++u) {
                                 p[u] = fast_exp2(fmaf(__uint_as_float(rr[e + u]), a.scale_log2, -lvs[u]));
-                                if (decltype(masked)::value && (unsigned)(q0 + col0 + e + u - kabs) >= span) p[u] = 0.f;
+                                if (decltype(masked)::value && !(see >> (e + u) & 1u)) p[u] = 0.f;
                             }
-                            pk[16 * c + e / 2] = pack_bf16x2(p[0], p[1]);
-                            pk[16 * c + e / 2 + 1] = pack_bf16x2(p[2], p[3]);
+                            w[e / 2] = pack_bf16x2(p[0], p[1]), w[e / 2 + 1] = pack_bf16x2(p[2], p[3]);
+                            ph[16 * c + e / 2] = pack_f16x2(p[0], p[1]), ph[16 * c + e / 2 + 1] = pack_f16x2(p[2], p[3]);
                         }
                     };
                     if (edge) p_chunk(std::true_type{});
                     else p_chunk(std::false_type{});
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = pk[16 * c + e];
                     tmem_st16(tR0 + 64 * hf + 16 * c + lane_base, w);
                 }
                 tmem_st_wait();
@@ -625,9 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int cc = ch * 8 + 2 * e;  // column within the 32-column chunk
-                            const uint32_t pw = pk[16 * c + cc / 2];
-                            out[e] = pack_bf16x2(__uint_as_float(pw << 16) * (__uint_as_float(rr[cc]) - dv[2 * e]),
-                                                 __uint_as_float(pw & 0xffff0000u) * (__uint_as_float(rr[cc + 1]) - dv[2 * e + 1]));
+                            const float2 pp = unpack_f16x2(ph[16 * c + cc / 2]);
+                            out[e] = pack_bf16x2(pp.x * (__uint_as_float(rr[cc]) - dv[2 * e]), pp.y * (__uint_as_float(rr[cc + 1]) - dv[2 * e + 1]));
                         }
                         st_shared_v4(sDS + hf * kSub + sw128_offset(j, 32 * c + 8 * ch), out[0], out[1], out[2], out[3]);
                     }
@@ -655,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint16_t* dv_row = a.dV + row * D + c0;
             uint16_t* dk_row = a.dK + row * D + c0;
             const bool part_row = parted && kabs < a.sink.sink;
+            const float kscale = a.scale * kPDown;
             float* part = parted ? a.sink.row(seq, a.cu_seqlens ? seq_start : seq * a.S, far ? 1 + blockIdx.z : 0, g, a.Hkv, j, D) + c0
                                  : nullptr;
 #pragma unroll 1
@@ -668,24 +669,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float* pk = pv + (size_t)a.sink.sink * D;
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        *reinterpret_cast<float4*>(pv + e) = make_float4(__uint_as_float(rv[e]), __uint_as_float(rv[e + 1]),
-                                                                         __uint_as_float(rv[e + 2]), __uint_as_float(rv[e + 3]));
+                        *reinterpret_cast<float4*>(pv + e) = make_float4(__uint_as_float(rv[e]) * kPDown, __uint_as_float(rv[e + 1]) * kPDown,
+                                                                         __uint_as_float(rv[e + 2]) * kPDown, __uint_as_float(rv[e + 3]) * kPDown);
                         *reinterpret_cast<float4*>(pk + e) =
-                            make_float4(__uint_as_float(rk[e]) * a.scale, __uint_as_float(rk[e + 1]) * a.scale,
-                                        __uint_as_float(rk[e + 2]) * a.scale, __uint_as_float(rk[e + 3]) * a.scale);
+                            make_float4(__uint_as_float(rk[e]) * kscale, __uint_as_float(rk[e + 1]) * kscale,
+                                        __uint_as_float(rk[e + 2]) * kscale, __uint_as_float(rk[e + 3]) * kscale);
                     }
                 } else if (key_ok && !far) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint4 wv, wk;
-                        wv.x = pack_bf16x2(__uint_as_float(rv[e]), __uint_as_float(rv[e + 1]));
-                        wv.y = pack_bf16x2(__uint_as_float(rv[e + 2]), __uint_as_float(rv[e + 3]));
-                        wv.z = pack_bf16x2(__uint_as_float(rv[e + 4]), __uint_as_float(rv[e + 5]));
-                        wv.w = pack_bf16x2(__uint_as_float(rv[e + 6]), __uint_as_float(rv[e + 7]));
-                        wk.x = pack_bf16x2(__uint_as_float(rk[e]) * a.scale, __uint_as_float(rk[e + 1]) * a.scale);
-                        wk.y = pack_bf16x2(__uint_as_float(rk[e + 2]) * a.scale, __uint_as_float(rk[e + 3]) * a.scale);
-                        wk.z = pack_bf16x2(__uint_as_float(rk[e + 4]) * a.scale, __uint_as_float(rk[e + 5]) * a.scale);
-                        wk.w = pack_bf16x2(__uint_as_float(rk[e + 6]) * a.scale, __uint_as_float(rk[e + 7]) * a.scale);
+                        wv.x = pack_bf16x2(__uint_as_float(rv[e]) * kPDown, __uint_as_float(rv[e + 1]) * kPDown);
+                        wv.y = pack_bf16x2(__uint_as_float(rv[e + 2]) * kPDown, __uint_as_float(rv[e + 3]) * kPDown);
+                        wv.z = pack_bf16x2(__uint_as_float(rv[e + 4]) * kPDown, __uint_as_float(rv[e + 5]) * kPDown);
+                        wv.w = pack_bf16x2(__uint_as_float(rv[e + 6]) * kPDown, __uint_as_float(rv[e + 7]) * kPDown);
+                        wk.x = pack_bf16x2(__uint_as_float(rk[e]) * kscale, __uint_as_float(rk[e + 1]) * kscale);
+                        wk.y = pack_bf16x2(__uint_as_float(rk[e + 2]) * kscale, __uint_as_float(rk[e + 3]) * kscale);
+                        wk.z = pack_bf16x2(__uint_as_float(rk[e + 4]) * kscale, __uint_as_float(rk[e + 5]) * kscale);
+                        wk.w = pack_bf16x2(__uint_as_float(rk[e + 6]) * kscale, __uint_as_float(rk[e + 7]) * kscale);
                         *reinterpret_cast<uint4*>(dv_row + c4 * 32 + e) = wv;
                         *reinterpret_cast<uint4*>(dk_row + c4 * 32 + e) = wk;
                     }
