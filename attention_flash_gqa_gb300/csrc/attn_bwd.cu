@@ -700,6 +700,7 @@ __global__ void __launch_bounds__(64) bwd_sink_sum_kernel(SinkSplit sk, uint16_t
     if (i_near >= n_qt || j >= L || d >= D) return;
     const int parts = 1 + (n_qt - i_near + sk.tiles - 1) / sk.tiles;
     float v[8] = {}, k[8] = {};
+#pragma unroll 8
     for (int p = 0; p < parts; ++p) {
         const float* row = sk.row(seq, start, p, g, Hkv, j, D) + d;
         const float* rowk = row + (size_t)sk.sink * D;
