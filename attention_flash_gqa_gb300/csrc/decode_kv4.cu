@@ -42,16 +42,16 @@ template <int D>
 struct Cfg {
     static constexpr int kWarps = D == 256 ? 8 : 16;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kStages = D == 64 ? 8 : 4;  // units on their way in each warp's ring
+    static constexpr int kStages = D == 64 ? 4 : 2;  // of each warp's ring: two units each
     static constexpr int kRow = D + 4;                             // floats of a piece's row: o, m, l, padding
-    static constexpr uint32_t kOffBar = kWarps * kStages * kv4_record_bytes(D);  // [warp][stage]
+    static constexpr uint32_t kOffBar = kWarps * kStages * 2 * kv4_record_bytes(D);  // [warp][stage]
     static constexpr uint32_t kOffMeta = kOffBar + kWarps * kStages * 8;         // abort flag, sums, segments of pieces
     static constexpr uint32_t kOffHead = kOffMeta + (4 * (4 + 3 * kWarps) + 15) / 16 * 16;  // [warp][G][kRow]: first pieces
     // behind it [B + 1] pages before a request, and [B] their lengths where there is room
     static uint32_t smem_bytes(int B, int G, bool lens) { return kOffHead + kWarps * G * kRow * 4 + (B + 1) * 4 + (lens ? B * 4 : 0) + 128; }
     static_assert(kOffHead + kWarps * kMaxG * kRow * 4 + (kMaxB + 1) * 4 + 128 <= kSmemLimit, "shared memory");
     // a warp's last piece is put where its own ring was
-    static_assert(kMaxG * kRow * 4 <= kStages * kv4_record_bytes(D), "ring");
+    static_assert(kMaxG * kRow * 4 <= kStages * 2 * kv4_record_bytes(D), "ring");
 };
 
 struct Args {
@@ -161,11 +161,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
     int* tail_piece = head_piece_of + C::kWarps;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3;
-    uint8_t* ring = smem + warp * (C::kStages * F::kRecord);
+    uint8_t* ring = smem + warp * (2 * C::kStages * F::kRecord);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * C::kStages;
     if (tid == 0) *abort_flag = 0;
     if (lane == 0) {
-        for (int s = 0; s < C::kStages; ++s) mbar_init(smem_u32(&full[s]), 1);
+        for (int s = 0; s < C::kStages; ++s) mbar_init(smem_u32(&full[s]), 2);
         head_piece_of[warp] = tail_piece[warp] = -1;
         fence_mbar_init();
     }
@@ -203,14 +203,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
         r.see = see | (i == 0 ? 1u << 16 : 0u) | (i == np - 1 ? 1u << 17 : 0u);
         return r;
     };
-    auto issue = [&](int first, int count, const uint8_t* record) {  // units first .. first + count - 1: by the lanes that have them
+    // Units first .. first + count - 1 (pairs of them), those from n on being none: by the lanes that have them.
+    auto issue = [&](int first, int count, const uint8_t* record) {
         const int x = (lane - first) & 31;
         if (x < count) {
-            const int s = (uint32_t)(first + x) % C::kStages;
-            const uint32_t bar = smem_u32(&full[s]);
-            if (record) {
+            const uint32_t u = first + x, slot = u % (2 * C::kStages), bar = smem_u32(&full[slot / 2]);
+            if ((int)u < n && record) {
                 mbar_expect_tx(bar, F::kRecord);
-                bulk_load_hint(smem_u32(ring + s * F::kRecord), record, F::kRecord, bar, policy);
+                bulk_load_hint(smem_u32(ring + slot * F::kRecord), record, F::kRecord, bar, policy);
             } else {
                 mbar_arrive(bar);
             }
@@ -263,10 +263,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
         }
         nxt = unit_at(u0 + lane, sure);
         if (!sure) {
-            if (lane < min(n, C::kStages) && nxt.record) prefetch_bulk(nxt.record, F::kRecord);
+            if (lane < min(n, 2 * C::kStages) && nxt.record) prefetch_bulk(nxt.record, F::kRecord);
             griddep_wait();
         }
-        issue(0, min(n, C::kStages), nxt.record);
+        issue(0, 2 * C::kStages, nxt.record);
         if (sure) break;
         bool same = true, bad = false;
         if (tid < a.B) {
@@ -279,10 +279,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
         if (same && bad) atomicOr(a.status, DEVSTAT_BOUNDS);
         if (same) break;
         if (lane == 0)
-            for (int s = 0; s < C::kStages; ++s) {
-                if (s >= n) mbar_arrive(smem_u32(&full[s]));
-                mbar_drain(smem_u32(&full[s]), 0, a.status, 0x63);
-            }
+            for (int s = 0; s < C::kStages; ++s) mbar_drain(smem_u32(&full[s]), 0, a.status, 0x63);
         __syncwarp();
         flip = 1, sure = true;
     }
@@ -339,238 +336,236 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
         }
     };
 
-    // Two units at a time where the second one is of the same segment and of the same batch of 32: what is done once for a unit
-    // beside its products (flags, waits, the next copies) costs a quarter of the instructions of a page.
-    for (int i = 0, step; i < n; i += step) {
+    // Two units at a time, whatever their segments: one wait and one refill for both.
+    for (int i = 0; i < n; i += 2) {
         if (32 * described <= i + 16) {  // a batch is worked out half a batch ahead
             nxt = unit_at(u0 + 32 * described + lane, true);
             ++described;
         }
         if ((i & 31) == 0) cur = nxt;
-        const uint32_t flags = __shfl_sync(0xffffffffu, cur.see, i & 31), flags2 = __shfl_sync(0xffffffffu, cur.see, (i + 1) & 31);
-        step = i + 1 < n && (i & 31) != 31 && !(flags & (1u << 17)) ? 2 : 1;
-        if (i == 0 || (flags & (1u << 16))) {
-            // ---- a new segment ----
-            began = (flags & (1u << 16)) != 0;
-            segment = __shfl_sync(0xffffffffu, cur.segment, i & 31);
-            const uint16_t* row = a.q + ((size_t)segment * a.G + g) * D + 8 * c;
-#pragma unroll
-            for (int gr = 0; gr < kGroups; ++gr) {
-                const uint4 w = g < a.G ? *reinterpret_cast<const uint4*>(row + 32 * gr) : make_uint4(0, 0, 0, 0);
-                qf[gr][0] = w.x, qf[gr][1] = w.y, qf[gr][2] = w.z, qf[gr][3] = w.w;
-            }
-            // The row's largest exponent goes to 120 (by 2^123 at most): then a product with a code, some 2^-129 of it, is a
-            // normal number. Words that meet low nibbles get 2^4 more.
-            uint32_t top = 0;
-#pragma unroll
-            for (int gr = 0; gr < kGroups; ++gr)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) top = max(top, max(qf[gr][x] & 0x7f80u, qf[gr][x] >> 16 & 0x7f80u));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int up = min(247 - (int)(top >> 7), 123);
-            const uint32_t by = (uint32_t)(up + 127) * 0x00800080u, by16 = by + 4 * 0x00800080u;
-            float minus[kGroups];  // -8 sum of q over a group, head g, in the units of the products
-#pragma unroll
-            for (int gr = 0; gr < kGroups; ++gr) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) qf[gr][x] = bf16x2_mul(qf[gr][x], x & 1 ? by : by16);
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                constexpr uint32_t kLow = 0x80088008u, kHigh = 0x80808080u;  // -8 * 2^-133, -8 * 2^-129
-                mma(d, kLow, kLow, kHigh, kHigh, qf[gr][0], qf[gr][1]);
-                mma(d, kLow, kLow, kHigh, kHigh, qf[gr][2], qf[gr][3]);
-                const float even = __shfl_sync(0xffffffffu, d[0], g >> 1), odd = __shfl_sync(0xffffffffu, d[1], g >> 1);
-                minus[gr] = g & 1 ? odd : even;
-            }
-            {
-                // Taken away through an MMA whose columns are groups: scales (exact) times these sums in three bf16 parts, which
-                // hold all 24 bits. Column 2c (and 2c + 1) of a step: group pair kPair(c) of part kPart(c).
-                float x0 = minus[0], x1 = minus[1];
-#pragma unroll
-                for (int w = 1; w < kGroups / 2; ++w)
-                    if (c % (kGroups / 2) == w) x0 = minus[2 * w], x1 = minus[2 * w + 1];
-                uint32_t part[3];
-#pragma unroll
-                for (int x = 0; x < 3; ++x) {
-                    part[x] = pack_bf16x2(x0, x1);
-                    x0 -= __uint_as_float(part[x] << 16), x1 -= __uint_as_float(part[x] & 0xffff0000u);
-                }
-                if (kGroups == 8) eight[0] = part[0], eight[1] = part[1], eight[2] = part[2];
-                else if (kGroups == 4) eight[0] = c < 2 ? part[0] : part[1], eight[1] = c < 2 ? part[2] : 0u;
-                else eight[0] = c == 0 ? part[0] : c == 1 ? part[1] : c == 2 ? part[2] : 0u, eight[1] = 0u;
-            }
-            const float fac = fminf(ldexpf(a.scale_log2, 129 - up), 3e38f);
-            factor[0] = __shfl_sync(0xffffffffu, fac, 8 * c), factor[1] = __shfl_sync(0xffffffffu, fac, 8 * c + 4);
-#pragma unroll
-            for (int bl = 0; bl < kBlocks; ++bl) {
-                down[bl] = kDownMin;
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[bl][t][e] = 0.f;
-            }
-            m[0] = m[1] = -INFINITY, m_use[0] = m_use[1] = l[0] = l[1] = 0.f;
-        }
-#pragma unroll 1
-        for (int x = i; x < i + step; ++x) {
-        const uint32_t see = x == i ? flags : flags2;
-        const int stage = (uint32_t)x % C::kStages, phase = ((uint32_t)x / C::kStages & 1) ^ flip;
+        const uint32_t stage = (uint32_t)i / 2 % C::kStages, phase = ((uint32_t)i / 2 / C::kStages & 1) ^ flip;
         if (ok) {
             ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[stage]), phase, abort_flag, a.status, 0x61));
-            if (!ok && lane == 0) ring_drain(full, stage, phase, C::kStages, n - x, a.status, 0x62);
+            if (!ok && lane == 0) ring_drain(full, stage, (int)phase, C::kStages, (n - i + 1) / 2, a.status, 0x62);
             __syncwarp();
         }
-        if (!ok) {  // given up: the rows of this unit and of those behind it in the stretch are NaN
-            m[0] = m[1] = INFINITY, l[0] = l[1] = __int_as_float(0x7fc00000);
-        } else if (see & 0xffffu) {
-            const uint32_t rec = smem_u32(ring + stage * F::kRecord);
-            // ---- S^T: tokens g and g + 8, heads 2c and 2c + 1 ----
-            float s[4];
-            {
-                const int w = 2 * (c % (kGroups / 2));
-                const uint32_t a0 = lds32(rec + F::key_scale(g, w)), a1 = lds32(rec + F::key_scale(g + 8, w));
-                mma0(s, a0, a1, a0, a1, eight[0], eight[1]);
-                if (kGroups == 8) mma(s, a0, a1, a0, a1, eight[2], 0u);
-            }
-            uint32_t sw[2][kGroups / 2];  // scales of tokens g, g + 8: two groups a word
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint32_t at = rec + F::key_scale(g + 8 * r, 0);
-                if constexpr (kGroups == 8) ld_shared_v4(at, sw[r][0], sw[r][1], sw[r][2], sw[r][3]);
-                else if constexpr (kGroups == 4) lds64(at, sw[r][0], sw[r][1]);
-                else sw[r][0] = lds32(at);
-            }
-#pragma unroll
-            for (int bl = 0; bl < kBlocks; ++bl) {
-                uint32_t kw[2][F::kBlockGroups];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint32_t at = rec + F::key_strip(bl, g + 8 * r, c);
-                    if constexpr (F::kBlockGroups == 4) ld_shared_v4(at, kw[r][0], kw[r][1], kw[r][2], kw[r][3]);
-                    else lds64(at, kw[r][0], kw[r][1]);
-                }
-#pragma unroll
-                for (int x = 0; x < F::kBlockGroups; ++x) {
-                    const int gr = bl * F::kBlockGroups + x;
-                    float d[4];
-                    const uint32_t w0 = kw[0][x], w1 = kw[1][x], y0 = w0 >> 8, y1 = w1 >> 8;
-                    mma0(d, w0 & kLowNibbles, w1 & kLowNibbles, w0 & kHighNibbles, w1 & kHighNibbles, qf[gr][0], qf[gr][1]);
-                    mma(d, y0 & kLowNibbles, y1 & kLowNibbles, y0 & kHighNibbles, y1 & kHighNibbles, qf[gr][2], qf[gr][3]);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float sc = __uint_as_float(gr & 1 ? sw[r][gr / 2] & 0xffff0000u : sw[r][gr / 2] << 16);
-                        s[2 * r] = fmaf(sc, d[2 * r], s[2 * r]), s[2 * r + 1] = fmaf(sc, d[2 * r + 1], s[2 * r + 1]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] *= factor[e & 1];
-            const bool whole = (see & 0xffffu) == 0xffffu;
-            if (!whole) {
-                if (!(see >> g & 1u)) s[0] = s[1] = -INFINITY;
-                if (!(see >> (g + 8) & 1u)) s[2] = s[3] = -INFINITY;
-            }
-            // ---- softmax: the maximum moves only when a score is past it by more than 8 (p <= 2^8) ----
-            const float top0 = fmaxf(s[0], s[2]), top1 = fmaxf(s[1], s[3]);
-            if (__any_sync(0xffffffffu, top0 > m[0] + 8.f || top1 > m[1] + 8.f)) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mx = e ? top1 : top0;
+        uint32_t rec = smem_u32(ring + stage * (2 * F::kRecord));
 #pragma unroll 1
-                    for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                    const float to = mx > m[e] + 8.f ? mx : m[e];
-                    const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - to);
-                    m[e] = to, l[e] *= f, m_use[e] = to == -INFINITY ? 0.f : to;
+        for (int x = i; x < min(i + 2, n); ++x, rec += F::kRecord) {
+            const uint32_t see = __shfl_sync(0xffffffffu, cur.see, x & 31);
+            if (x == 0 || (see & (1u << 16))) {
+                // ---- a new segment ----
+                began = (see & (1u << 16)) != 0;
+                segment = __shfl_sync(0xffffffffu, cur.segment, x & 31);
+                const uint16_t* row = a.q + ((size_t)segment * a.G + g) * D + 8 * c;
 #pragma unroll
-                    for (int bl = 0; bl < kBlocks; ++bl)
-#pragma unroll
-                        for (int t = 0; t < kTiles; ++t) o[bl][t][e] *= f, o[bl][t][e + 2] *= f;
+                for (int gr = 0; gr < kGroups; ++gr) {
+                    const uint4 w = g < a.G ? *reinterpret_cast<const uint4*>(row + 32 * gr) : make_uint4(0, 0, 0, 0);
+                    qf[gr][0] = w.x, qf[gr][1] = w.y, qf[gr][2] = w.z, qf[gr][3] = w.w;
                 }
-            }
-            float p[4];
+                // The row's largest exponent goes to 120 (by 2^123 at most): then a product with a code, some 2^-129 of it, is a
+                // normal number. Words that meet low nibbles get 2^4 more.
+                uint32_t top = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                p[e] = fast_exp2(s[e] - m_use[e & 1]);  // (0 for -inf)
-                l[e & 1] += p[e];
-            }
-            // ---- O^T += V^T P^T ----
-            const uint32_t b0 = transpose8(pack_bf16x2(p[0], p[1])), b1 = transpose8(pack_bf16x2(p[2], p[3]));
-            uint32_t hide0 = 0xffffffffu, hide1 = 0xffffffffu;  // tokens that are not seen may hold anything: scale 0
-            if (!whole) {
-                hide0 = (see >> (2 * c) & 1u ? 0xffffu : 0u) | (see >> (2 * c + 1) & 1u ? 0xffff0000u : 0u);
-                hide1 = (see >> (2 * c + 8) & 1u ? 0xffffu : 0u) | (see >> (2 * c + 9) & 1u ? 0xffff0000u : 0u);
-            }
+                for (int gr = 0; gr < kGroups; ++gr)
 #pragma unroll
-            for (int bl = 0; bl < kBlocks; ++bl) {
-                // words[pair][token of the pair][8 dims]
-                constexpr int kWords = F::W / 64;
-                uint32_t vw[2][2][kWords];
+                    for (int x = 0; x < 4; ++x) top = max(top, max(qf[gr][x] & 0x7f80u, qf[gr][x] >> 16 & 0x7f80u));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int up = min(247 - (int)(top >> 7), 123);
+                const uint32_t by = (uint32_t)(up + 127) * 0x00800080u, by16 = by + 4 * 0x00800080u;
+                float minus[kGroups];  // -8 sum of q over a group, head g, in the units of the products
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint32_t at = rec + F::value_chunk(bl, c + 4 * r, g);
-                    if constexpr (kWords == 2) ld_shared_v4(at, vw[r][0][0], vw[r][0][1], vw[r][1][0], vw[r][1][1]);
-                    else lds64(at, vw[r][0][0], vw[r][1][0]);
+                for (int gr = 0; gr < kGroups; ++gr) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) qf[gr][x] = bf16x2_mul(qf[gr][x], x & 1 ? by : by16);
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                    constexpr uint32_t kLow = 0x80088008u, kHigh = 0x80808080u;  // -8 * 2^-133, -8 * 2^-129
+                    mma(d, kLow, kLow, kHigh, kHigh, qf[gr][0], qf[gr][1]);
+                    mma(d, kLow, kLow, kHigh, kHigh, qf[gr][2], qf[gr][3]);
+                    const float even = __shfl_sync(0xffffffffu, d[0], g >> 1), odd = __shfl_sync(0xffffffffu, d[1], g >> 1);
+                    minus[gr] = g & 1 ? odd : even;
                 }
-                const int gr = bl * F::kBlockGroups + g / (8 / F::kBlockGroups);
-                const uint32_t s0 = lds32(rec + F::value_scale(gr, 2 * c)) & hide0, s1 = lds32(rec + F::value_scale(gr, 2 * c + 8)) & hide1;
-                // a scale whose exponent is above what `down` allows: bit 15 of its half
-                const uint32_t past = (0x8000u - ((uint32_t)(down[bl] + 122) << 7)) * 0x10001u;
-                if (__any_sync(0xffffffffu, (((s0 & 0x7fff7fffu) + past) | ((s1 & 0x7fff7fffu) + past)) & 0x80008000u)) {
-                    uint32_t e = max(max(s0 & 0x7f80u, s0 >> 16 & 0x7f80u), max(s1 & 0x7f80u, s1 >> 16 & 0x7f80u)) >> 7;
-                    e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));  // the four lanes of a row
-                    e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-                    const int to = (int)e > down[bl] + 121 ? min((int)e - 121 + 8, kDownMax) : down[bl];
-                    const float f = to - down[bl] > 126 ? 0.f : __int_as_float((127 - (to - down[bl])) << 23);
-                    down[bl] = to;
+                {
+                    // Taken away through an MMA whose columns are groups: scales (exact) times these sums in three bf16 parts, which
+                        // hold all 24 bits. Columns 2c, 2c + 1 of a step: a pair of groups of one part, as many parts a step as there is room for.
+                        float x0 = minus[0], x1 = minus[1];
+#pragma unroll
+                    for (int w = 1; w < kGroups / 2; ++w)
+                        if (c % (kGroups / 2) == w) x0 = minus[2 * w], x1 = minus[2 * w + 1];
+                    uint32_t part[3];
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) {
+                        part[x] = pack_bf16x2(x0, x1);
+                        x0 -= __uint_as_float(part[x] << 16), x1 -= __uint_as_float(part[x] & 0xffff0000u);
+                    }
+                    if (kGroups == 8) eight[0] = part[0], eight[1] = part[1], eight[2] = part[2];
+                    else if (kGroups == 4) eight[0] = c < 2 ? part[0] : part[1], eight[1] = c < 2 ? part[2] : 0u;
+                    else eight[0] = c == 0 ? part[0] : c == 1 ? part[1] : c == 2 ? part[2] : 0u, eight[1] = 0u;
+                }
+                const float fac = fminf(ldexpf(a.scale_log2, 129 - up), 3e38f);
+                factor[0] = __shfl_sync(0xffffffffu, fac, 8 * c), factor[1] = __shfl_sync(0xffffffffu, fac, 8 * c + 4);
+#pragma unroll
+                for (int bl = 0; bl < kBlocks; ++bl) {
+                    down[bl] = kDownMin;
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) o[bl][t][x] *= f;
+                        for (int e = 0; e < 4; ++e) o[bl][t][e] = 0.f;
                 }
-                const uint32_t up_high = (uint32_t)(256 - down[bl]) * 0x00800080u;  // 2^(129 - down)
-                const uint32_t fh0 = bf16x2_mul(s0, up_high), fh1 = bf16x2_mul(s1, up_high);
-                const uint32_t up_low = up_high + 4 * 0x00800080u, minus8 = (up_high - 126 * 0x00800080u) | 0x80008000u;  // -8 * 2^-down
-                const uint32_t fl0 = bf16x2_mul(s0, up_low), fl1 = bf16x2_mul(s1, up_low);
-                const uint32_t c0 = bf16x2_mul(s0, minus8), c1 = bf16x2_mul(s1, minus8);
+                m[0] = m[1] = -INFINITY, m_use[0] = m_use[1] = l[0] = l[1] = 0.f;
+            }
+            if (!ok) {  // given up: the rows of this unit and of those behind it in the stretch are NaN
+                m[0] = m[1] = INFINITY, l[0] = l[1] = __int_as_float(0x7fc00000);
+            } else if (see & 0xffffu) {
+                // ---- S^T: tokens g and g + 8, heads 2c and 2c + 1 ----
+                float s[4];
+                {
+                    const int w = 2 * (c % (kGroups / 2));
+                    const uint32_t a0 = lds32(rec + F::key_scale(g, w)), a1 = lds32(rec + F::key_scale(g + 8, w));
+                    mma0(s, a0, a1, a0, a1, eight[0], eight[1]);
+                    if (kGroups == 8) mma(s, a0, a1, a0, a1, eight[2], 0u);
+                }
+                uint32_t sw[2][kGroups / 2];  // scales of tokens g, g + 8: two groups a word
 #pragma unroll
-                for (int half = 0; half < 2 * kWords; ++half) {  // 4 dims of both tokens side by side
-                    const uint32_t sel = half & 1 ? 0x7632u : 0x5410u;
-                    const uint32_t x0 = __byte_perm(vw[0][0][half / 2], vw[0][1][half / 2], sel);
-                    const uint32_t x1 = __byte_perm(vw[1][0][half / 2], vw[1][1][half / 2], sel);
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t at = rec + F::key_scale(g + 8 * r, 0);
+                    if constexpr (kGroups == 8) ld_shared_v4(at, sw[r][0], sw[r][1], sw[r][2], sw[r][3]);
+                    else if constexpr (kGroups == 4) lds64(at, sw[r][0], sw[r][1]);
+                    else sw[r][0] = lds32(at);
+                }
 #pragma unroll
-                    for (int d = 0; d < 4; d += 2) {
-                        const uint32_t y0 = x0 >> (4 * d), y1 = x1 >> (4 * d);
-                        mma(o[bl][half * 2 + d / 2], bf16x2_fma(y0 & kLowNibbles, fl0, c0), bf16x2_fma(y0 & kHighNibbles, fh0, c0),
-                            bf16x2_fma(y1 & kLowNibbles, fl1, c1), bf16x2_fma(y1 & kHighNibbles, fh1, c1), b0, b1);
+                for (int bl = 0; bl < kBlocks; ++bl) {
+                    uint32_t kw[2][F::kBlockGroups];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t at = rec + F::key_strip(bl, g + 8 * r, c);
+                        if constexpr (F::kBlockGroups == 4) ld_shared_v4(at, kw[r][0], kw[r][1], kw[r][2], kw[r][3]);
+                        else lds64(at, kw[r][0], kw[r][1]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < F::kBlockGroups; ++x) {
+                        const int gr = bl * F::kBlockGroups + x;
+                        float d[4];
+                        const uint32_t w0 = kw[0][x], w1 = kw[1][x], y0 = w0 >> 8, y1 = w1 >> 8;
+                        mma0(d, w0 & kLowNibbles, w1 & kLowNibbles, w0 & kHighNibbles, w1 & kHighNibbles, qf[gr][0], qf[gr][1]);
+                        mma(d, y0 & kLowNibbles, y1 & kLowNibbles, y0 & kHighNibbles, y1 & kHighNibbles, qf[gr][2], qf[gr][3]);
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float sc = __uint_as_float(gr & 1 ? sw[r][gr / 2] & 0xffff0000u : sw[r][gr / 2] << 16);
+                            s[2 * r] = fmaf(sc, d[2 * r], s[2 * r]), s[2 * r + 1] = fmaf(sc, d[2 * r + 1], s[2 * r + 1]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] *= factor[e & 1];
+                const bool whole = (see & 0xffffu) == 0xffffu;
+                if (!whole) {
+                    if (!(see >> g & 1u)) s[0] = s[1] = -INFINITY;
+                    if (!(see >> (g + 8) & 1u)) s[2] = s[3] = -INFINITY;
+                }
+                // ---- softmax: the maximum moves only when a score is past it by more than 8 (p <= 2^8) ----
+                const float top0 = fmaxf(s[0], s[2]), top1 = fmaxf(s[1], s[3]);
+                if (__any_sync(0xffffffffu, top0 > m[0] + 8.f || top1 > m[1] + 8.f)) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = e ? top1 : top0;
+#pragma unroll 1
+                        for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                        const float to = mx > m[e] + 8.f ? mx : m[e];
+                        const float f = m[e] == -INFINITY ? 0.f : fast_exp2(m[e] - to);
+                        m[e] = to, l[e] *= f, m_use[e] = to == -INFINITY ? 0.f : to;
+#pragma unroll
+                        for (int bl = 0; bl < kBlocks; ++bl)
+#pragma unroll
+                            for (int t = 0; t < kTiles; ++t) o[bl][t][e] *= f, o[bl][t][e + 2] *= f;
+                    }
+                }
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = fast_exp2(s[e] - m_use[e & 1]);  // (0 for -inf)
+                    l[e & 1] += p[e];
+                }
+                // ---- O^T += V^T P^T ----
+                const uint32_t b0 = transpose8(pack_bf16x2(p[0], p[1])), b1 = transpose8(pack_bf16x2(p[2], p[3]));
+                uint32_t hide0 = 0xffffffffu, hide1 = 0xffffffffu;  // tokens that are not seen may hold anything: scale 0
+                if (!whole) {
+                    hide0 = (see >> (2 * c) & 1u ? 0xffffu : 0u) | (see >> (2 * c + 1) & 1u ? 0xffff0000u : 0u);
+                    hide1 = (see >> (2 * c + 8) & 1u ? 0xffffu : 0u) | (see >> (2 * c + 9) & 1u ? 0xffff0000u : 0u);
+                }
+#pragma unroll
+                for (int bl = 0; bl < kBlocks; ++bl) {
+                    // words[pair][token of the pair][8 dims]
+                    constexpr int kWords = F::W / 64;
+                    uint32_t vw[2][2][kWords];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t at = rec + F::value_chunk(bl, c + 4 * r, g);
+                        if constexpr (kWords == 2) ld_shared_v4(at, vw[r][0][0], vw[r][0][1], vw[r][1][0], vw[r][1][1]);
+                        else lds64(at, vw[r][0][0], vw[r][1][0]);
+                    }
+                    const int gr = bl * F::kBlockGroups + g / (8 / F::kBlockGroups);
+                    const uint32_t s0 = lds32(rec + F::value_scale(gr, 2 * c)) & hide0;
+                    const uint32_t s1 = lds32(rec + F::value_scale(gr, 2 * c + 8)) & hide1;
+                    // a scale whose exponent is above what `down` allows: bit 15 of its half
+                    const uint32_t past = (0x8000u - ((uint32_t)(down[bl] + 122) << 7)) * 0x10001u;
+                    if (__any_sync(0xffffffffu, (((s0 & 0x7fff7fffu) + past) | ((s1 & 0x7fff7fffu) + past)) & 0x80008000u)) {
+                        uint32_t e = max(max(s0 & 0x7f80u, s0 >> 16 & 0x7f80u), max(s1 & 0x7f80u, s1 >> 16 & 0x7f80u)) >> 7;
+                        e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));  // the four lanes of a row
+                        e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
+                        const int to = (int)e > down[bl] + 121 ? min((int)e - 121 + 8, kDownMax) : down[bl];
+                        const float f = to - down[bl] > 126 ? 0.f : __int_as_float((127 - (to - down[bl])) << 23);
+                        down[bl] = to;
+#pragma unroll
+                        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) o[bl][t][x] *= f;
+                    }
+                    const uint32_t up_high = (uint32_t)(256 - down[bl]) * 0x00800080u;  // 2^(129 - down)
+                    const uint32_t fh0 = bf16x2_mul(s0, up_high), fh1 = bf16x2_mul(s1, up_high);
+                    const uint32_t up_low = up_high + 4 * 0x00800080u;
+                    const uint32_t minus8 = (up_high - 126 * 0x00800080u) | 0x80008000u;  // -8 * 2^-down
+                    const uint32_t fl0 = bf16x2_mul(s0, up_low), fl1 = bf16x2_mul(s1, up_low);
+                    const uint32_t c0 = bf16x2_mul(s0, minus8), c1 = bf16x2_mul(s1, minus8);
+#pragma unroll
+                    for (int half = 0; half < 2 * kWords; ++half) {  // 4 dims of both tokens side by side
+                        const uint32_t sel = half & 1 ? 0x7632u : 0x5410u;
+                        const uint32_t x0 = __byte_perm(vw[0][0][half / 2], vw[0][1][half / 2], sel);
+                        const uint32_t x1 = __byte_perm(vw[1][0][half / 2], vw[1][1][half / 2], sel);
+#pragma unroll
+                        for (int d = 0; d < 4; d += 2) {
+                            const uint32_t y0 = x0 >> (4 * d), y1 = x1 >> (4 * d);
+                            mma(o[bl][half * 2 + d / 2], bf16x2_fma(y0 & kLowNibbles, fl0, c0), bf16x2_fma(y0 & kHighNibbles, fh0, c0),
+                                bf16x2_fma(y1 & kLowNibbles, fl1, c1), bf16x2_fma(y1 & kHighNibbles, fh1, c1), b0, b1);
+                        }
                     }
                 }
             }
-        }
+            const bool ends = (see & (1u << 17)) != 0, last = x + 1 == n;
+            if (ends || last) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll 1
+                    for (int off = 4; off < 32; off <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
+#pragma unroll
+                for (int bl = 0; bl < kBlocks; ++bl) {
+                    const float f = __int_as_float((127 + down[bl] / 2) << 23), f2 = __int_as_float((127 + down[bl] - down[bl] / 2) << 23);
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[bl][t][x] = o[bl][t][x] * f * f2;
+                }
+                if (began && ends) {
+                    write_result();
+                } else {  // its first piece, of a segment that began in an earlier stretch; or what is left at the end
+                    write_piece(last ? reinterpret_cast<float*>(ring) : head_piece + warp * a.G * C::kRow);
+                    if (lane == 0) (last ? tail_piece : head_piece_of)[warp] = segment << 2 | (ends ? 2 : 0) | (began ? 1 : 0);
+                }
+            }
         }
         __syncwarp();  // the records have been read
-        if (ok && i + C::kStages < n)
-            issue(i + C::kStages, min(step, n - i - C::kStages), lane >= (i & 31) ? cur.record : nxt.record);
-        const bool ends = ((step == 2 ? flags2 : flags) & (1u << 17)) != 0, last = i + step == n;
-        if (ends || last) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll 1
-                for (int off = 4; off < 32; off <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], off);
-#pragma unroll
-            for (int bl = 0; bl < kBlocks; ++bl) {
-                const float f = __int_as_float((127 + down[bl] / 2) << 23), f2 = __int_as_float((127 + down[bl] - down[bl] / 2) << 23);
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) o[bl][t][x] = o[bl][t][x] * f * f2;
-            }
-            if (began && ends) {
-                write_result();
-            } else {  // its first piece, of a segment that began in an earlier stretch; or what is left at the end
-                write_piece(last ? reinterpret_cast<float*>(ring) : head_piece + warp * a.G * C::kRow);
-                if (lane == 0) (last ? tail_piece : head_piece_of)[warp] = segment << 2 | (ends ? 2 : 0) | (began ? 1 : 0);
-            }
-        }
+        if (ok && i + 2 * C::kStages < n) issue(i + 2 * C::kStages, 2, lane >= (i & 31) ? cur.record : nxt.record);
     }
     __syncthreads();
     // ---- pieces of a segment that lie in this block: joined by the warp that has the first ------------
@@ -579,7 +574,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
     const int piece = (lane & 15) < C::kWarps ? (lane < 16 ? tail_piece[lane] : head_piece_of[lane - 16]) : -1;
     const uint32_t alike = __match_any_sync(0xffffffffu, piece >> 2);
     uint32_t leads = __ballot_sync(0xffffffffu, piece >= 0 && __ffs(alike) - 1 == lane);  // one lane for each segment
-    const float* rows = lane < 16 ? reinterpret_cast<const float*>(smem + lane * (C::kStages * F::kRecord))
+    const float* rows = lane < 16 ? reinterpret_cast<const float*>(smem + lane * (2 * C::kStages * F::kRecord))
                                   : head_piece + (lane - 16) * a.G * C::kRow;
     const int tasks = __popc(leads) * a.G;
     for (int task = warp, at = 0; task < tasks; task += C::kWarps) {
@@ -604,7 +599,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
                 const int from = members ? __ffs(members) - 1 : 0;
                 const float there = __shfl_sync(0xffffffffu, weight, from);
                 w[k] = members ? there : 0.f;
-                const float* row = (from < 16 ? reinterpret_cast<const float*>(smem + from * (C::kStages * F::kRecord))
+                const float* row = (from < 16 ? reinterpret_cast<const float*>(smem + from * (2 * C::kStages * F::kRecord))
                                               : head_piece + (from - 16) * a.G * C::kRow) + hh * C::kRow + N * lane;
 #pragma unroll
                 for (int e = 0; e < N; e += 2) {
