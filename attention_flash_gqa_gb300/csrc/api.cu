@@ -153,7 +153,7 @@ size_t bwd_ws(long long rows, int Hq, int D) {
 }
 // Query tiles of a slice of the far queries: as many as a block of the window has, but not so few that the parts' bytes
 // (two rows of fp32 for each sink, KV head and slice) would count beside the queries'.
-int sink_slice_tiles(int window) { return (window + 127) / 128 + 1 > 8 ? (window + 127) / 128 + 1 : 8; }
+int sink_slice_tiles(int window) { return (window - 1) / 128 + 2 > 8 ? (window - 1) / 128 + 2 : 8; }
 // Bytes of the parts; SinkSplit says how they lie.
 size_t sink_ws(long long rows, long long nseq, int Hkv, int D, int window, int sink) {
     if (window <= 0 || sink <= 0) return 0;

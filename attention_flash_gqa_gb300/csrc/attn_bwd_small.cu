@@ -53,7 +53,8 @@ constexpr int kEw = 256;  // elementwise threads
 constexpr uint32_t kSub = 16384;  // 128 rows x 64 bf16, 128-byte swizzle
 constexpr float kLog2e = 1.4426950408889634f;
 // P is held times 2^15: at most 1, it then fits fp16 with all of its bits down to 2^-29. dS is formed from that (three bits more
-// than from the bf16 P that dV's product takes); dV, dK and dQ have the factor taken out where they leave tensor memory.
+// than from the bf16 P that dV's product takes); dV, dK and dQ have the factor taken out where they leave tensor memory. (Scores of
+// 2^24 and more, whose logsumexp fp32 holds to whole numbers at best, give P above 1: past 2 it counts as 2 in dS.)
 constexpr float kPUp = 15.f, kPDown = 1.f / 32768.f;
 
 // D: head dim (the contraction of S^T and dP^T); DS: the columns of dV / dK / dQ this CTA owns.

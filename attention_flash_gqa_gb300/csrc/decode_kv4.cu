@@ -173,10 +173,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
     int u0 = 0, u1 = 0, n = 0;  // the warp's stretch
     const int32_t* entry = nullptr;  // of the last unit worked out: its block-table entry and what it held
     int entry_page = -1;
-    auto unit_at = [&](int u, bool record) -> Unit {
+    auto unit_at = [&](uint32_t at, bool record) -> Unit {
         Unit r = {nullptr, -1, 0u};
         entry = nullptr;
-        if (u >= u1) return r;
+        if (at >= (uint32_t)u1) return r;  // (past the last unit it may be above 2^31)
+        const int u = (int)at;
         int lo = 0, hi = a.B - 1;  // the last request that starts at or before u: it has pages
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
             u0 = first + (int)((uint32_t)many * warp / C::kWarps), u1 = first + (int)((uint32_t)many * (warp + 1) / C::kWarps);
             n = u1 - u0;
         }
-        nxt = unit_at(u0 + lane, sure);
+        nxt = unit_at((uint32_t)u0 + lane, sure);
         if (!sure) {
             if (lane < min(n, 2 * C::kStages) && nxt.record) prefetch_bulk(nxt.record, F::kRecord);
             griddep_wait();
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
     // Two units at a time, whatever their segments: one wait and one refill for both.
     for (int i = 0; i < n; i += 2) {
         if (32 * described <= i + 16) {  // a batch is worked out half a batch ahead
-            nxt = unit_at(u0 + 32 * described + lane, true);
+            nxt = unit_at((uint32_t)u0 + 32u * described + lane, true);
             ++described;
         }
         if ((i & 31) == 0) cur = nxt;

@@ -112,3 +112,8 @@ def test_binding_refuses_cpu_tensors(lib):
         attn.attn_decode_kv4(x, c, i.view(4, 1), i)
     with pytest.raises(TypeError):
         attn.attn_kv4_append(None, x, i, c)
+
+
+def test_bwd_workspace_of_the_largest_window(lib):
+    size = lib.attn_bwd_sink_workspace_size
+    assert size(1, 8, 2, 3000, 128, 0, 2 ** 31 - 1, 4) >= attn.attn_workspace_size(attn.ATTN_OP_BWD, 1, 8, 2, 3000, 128)

@@ -228,3 +228,18 @@ def test_bad_slices_are_reported():
     for i, t in enumerate((dq, dk, dv)):
         close("first", t[:1300], want[2 * i], want[2 * i + 1])
     assert (dk[1300:] == 7).all() and (dv[1300:] == 7).all() and (dq[1300:] == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+def test_gradient_of_scores_that_fp32_holds_coarsely(D):
+    """Scores of 2^27 and more: their logsumexp is off by whole numbers, P by powers of two, but nothing overflows."""
+    S = 200
+    q, k, v, do = (t.view(1, S, -1, D) for t in rows(S, 2, 1, D, 27))
+    q[..., 0] = 2.0 ** 13 * (1 + q[..., 0].abs() / 8)
+    k[..., 0] = 2.0 ** 14 * (1 + k[..., 0].abs() / 8)
+    q, k, v, do = (t.cuda() for t in (q, k, v, do))
+    for window, sink in ((0, 0), (70, 4)):
+        o, lse = attn.attn_fwd(q, k, v, window=window, sink=sink, scale=1.0)
+        got = attn.attn_bwd(q, k, v, o, lse, do, window=window, sink=sink, scale=1.0)
+        assert attn.attn_get_device_status() == 0
+        assert all(bool(t.isfinite().all()) for t in (o, lse, *got))
