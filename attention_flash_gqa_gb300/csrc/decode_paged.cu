@@ -492,15 +492,16 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
     bool ok = true;
     int cur_b = -1;
     int lo_tok = 0;  // first visible token within the request's first unit (window)
-    int early = 0, sink_left = 0;  // SINK: units before that one, and tokens of it that are sinks
+    int first_at = 0, sink_left = 0;  // SINK: which of the CTA's units that one is, and how many of its tokens are sinks
     for (long long u = u0; u < u1 && ok; ++u, ++i) {
         while (start[b + 1] <= u) ++b;
         if (b != cur_b) {
             cur_b = b;
             lo_tok = first_token(a, req_len(a, b)) % kPage;
             if (SINK) {
-                early = sink_pages<SINK>(a, req_len(a, b));
-                sink_left = a.sink - first_token(a, req_len(a, b)) / kPage * kPage;
+                const int L = req_len(a, b);
+                first_at = (int)(start[b] - u0) + sink_pages<SINK>(a, L);
+                sink_left = a.sink - first_token(a, L) / kPage * kPage;
             }
             if (PACKED && active && mg < G) {
                 const uint16_t* qrow = a.q + ((size_t)b * a.Hq + g * G + mg) * D + 2 * mc;
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
         if (!ok) break;
         const int32_t entry = unit_entry(i);
         const int nt = (entry >= 0 ? (entry & 31) : 0) - TPW * half;  // end of this warp's valid tokens (may be <= 0)
-        const bool first_unit = SINK ? (int)(u - start[b]) == early : u == start[b];
+        const bool first_unit = SINK ? i == first_at : u == start[b];
         const int tlo = (first_unit ? lo_tok : 0) - TPW * half;     // first of them (may be < 0)
         const int tsink = SINK && first_unit ? sink_left - TPW * half : 0;  // and those below this, in the window's first page
         if (active && nt > 0 && (tlo < TPW || (SINK && tsink > 0))) {
@@ -535,7 +536,8 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
             if constexpr (PACKED) {
                 const uint32_t kb = smem_u32(kp), vb = smem_u32(vp);
                 const uint32_t hbytes = (uint32_t)a.hb * kPage * 128u;  // one 64-dim half of every head
-                auto vis = [&](int t) { return t < nt && (t >= tlo || (SINK && t < tsink)); };
+                const uint32_t see = SINK ? allowed_bits(0, tlo, nt - 1, tsink) : 0u;  // a bit a token
+                auto vis = [&](int t) -> bool { return SINK ? see >> t & 1u : t < nt && t >= tlo; };
                 // S = Q K^T: tiles of tokens 0-7 and 8-15. Per k-step one matrix load gives both
                 // tiles' B fragments: lanes 0-7 / 8-15 / 16-23 / 24-31 address tokens 0-7, 0-7,
                 // 8-15, 8-15 at the step's lower / upper / lower / upper 8 dims; the swizzle puts
@@ -589,7 +591,7 @@ __global__ void __launch_bounds__(DecCfg<G, D>::kThreads, 1)
                 const uint32_t pa0 = pack_bf16x2(pv[0], pv[1]), pa1 = pack_bf16x2(pv[2], pv[3]);
                 // tokens past the end hold arbitrary bytes: zero them (p is 0 there, but 0 * NaN is not)
                 uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
-                if (!(nt >= TPW && tlo <= 0)) {
+                if (SINK ? see != 0xffffu : !(nt >= TPW && tlo <= 0)) {
                     vm0 = (vis(t0) ? 0x0000ffffu : 0u) | (vis(t0 + 1) ? 0xffff0000u : 0u);
                     vm1 = (vis(t0 + 8) ? 0x0000ffffu : 0u) | (vis(t0 + 9) ? 0xffff0000u : 0u);
                 }
