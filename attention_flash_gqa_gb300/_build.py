@@ -22,7 +22,7 @@ OPS = os.path.join(HERE, "_ops.so")
 OPS_SOURCE = os.path.join(CSRC, "py_ops.cpp")
 BUILD_DIR = os.path.join(HERE, "_build_tmp")
 OPS_TAG = os.path.join(BUILD_DIR, "ops_built_for.txt")  # what _ops.so was built for
-SOURCES = ["api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd_small.cu", "decode_paged.cu", "decode_paged_noalloc.cu",
+SOURCES = ["api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd_small.cu", "attn_bwd_sink.cu", "decode_paged.cu", "decode_paged_noalloc.cu",
            "decode_kv4.cu", "kv4_pages.cu", "merge_lse.cu", "paged_plan.cu", "qk_norm_rope.cu", "tree_paged.cu"]
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
 

@@ -151,13 +151,32 @@ int fwd_splits(int D) { return D > 256 ? D / 256 : 1; }
 size_t bwd_ws(long long rows, int Hq, int D) {
     return align256((size_t)rows * Hq * D * 4) + align256((size_t)rows * Hq * 4);
 }
-// Query tiles of a slice of the far queries: as many as a block of the window has, but not so few that the parts' bytes
-// (two rows of fp32 for each sink, KV head and slice) would count beside the queries'.
-int sink_slice_tiles(int window) { return (window - 1) / 128 + 2 > 8 ? (window - 1) / 128 + 2 : 8; }
+// Whether the far queries' sinks are a kernel's own (attn_bwd_sink.cu): where they fit its MMAs and q is large. In small calls the
+// slices in the main kernel mostly fill what its last wave of blocks leaves idle. (The whole gradient, this way and that, us: q of 2^27
+// elements, window 1000, head_dim 256 3075 and 3271, 128 1922 and 2100; of 2^25, eleven shapes: from 10 % less to 8 % more, 4 % less in
+// the mean; of 2^24, 32 heads of 128: 308 and 285 at window 1000, 171 and 159 at 250.)
+bool sinks_apart(long long rows, int Hq, int D, int sink) { return D <= 256 && sink <= attn::kFewSinks && rows * Hq * D >= 1ll << 25; }
+// Rows of a slice of the far queries, and shares of its heads. Blocks of the main kernel: as many rows as a block of the window has, but
+// not so few that the parts' bytes (two rows of fp32 for each sink, KV head and slice) would count beside the queries'. The kernel
+// of their own: 512 rows' worth of a head a block, 64 rows at least, and fewer where they would not be 4 blocks an SM.
+void sink_slices(attn::SinkSplit& s, long long rows, int Hq, int Hkv, int D, int window, int sink) {
+    s.sink = sink, s.shares = 1;
+    if (!sinks_apart(rows, Hq, D, sink)) {
+        s.rows = 128 * ((window - 1) / 128 + 2 > 8 ? (window - 1) / 128 + 2 : 8);
+        return;
+    }
+    const int G = Hkv > 0 && Hq >= Hkv ? Hq / Hkv : 1;
+    const long long most = rows * Hq / 64 / (4 * 152);
+    const int steps = most < 1 ? 1 : most > 8 ? 8 : (int)most;
+    s.rows = 64 * (steps > G ? steps / G : 1);
+    s.shares = steps < G ? (G + steps - 1) / steps : 1;
+}
 // Bytes of the parts; SinkSplit says how they lie.
-size_t sink_ws(long long rows, long long nseq, int Hkv, int D, int window, int sink) {
+size_t sink_ws(long long rows, long long nseq, int Hq, int Hkv, int D, int window, int sink) {
     if (window <= 0 || sink <= 0) return 0;
-    return align256((size_t)(rows / (sink_slice_tiles(window) * 128LL) + 2 * nseq) * Hkv * 2 * sink * D * 4);
+    attn::SinkSplit s;
+    sink_slices(s, rows, Hq, Hkv, D, window, sink);
+    return align256((size_t)(rows / s.rows + 2 * nseq) * s.shares * Hkv * 2 * sink * D * 4);
 }
 
 // CTAs per KV-head block of a decode launch at most: the blocks share decode_max_grid() CTAs.
@@ -394,7 +413,7 @@ size_t attn_workspace_size(int op, int B, int Hq, int Hkv, int S, int D, int num
 size_t attn_bwd_sink_workspace_size(int B, int Hq, int Hkv, int S, int D, int num_seqs, int window, int sink) {
     if (B < 0 || Hq < 0 || Hkv < 0 || S < 0 || D < 0 || num_seqs < 0) return 0;
     const long long rows = (long long)B * S;
-    return bwd_ws(rows, Hq, D) + sink_ws(rows, num_seqs > B ? num_seqs : B, Hkv, D, window, sink);
+    return bwd_ws(rows, Hq, D) + sink_ws(rows, num_seqs > B ? num_seqs : B, Hq, Hkv, D, window, sink);
 }
 
 int attn_fwd(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_bf16* o, float* lse, int B, int Hq,
@@ -513,13 +532,14 @@ int attn_bwd_sink(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, co
     window = reaching(window, grid_len);
     attn::SinkSplit split = {};
     if (window > 0 && sink > 0) {
-        split.sink = sink, split.tiles = sink_slice_tiles(window);
-        const int near = window + 127 < grid_len ? (window + 127 + 127) / 128 : (grid_len + 127) / 128;
-        split.slices = ((grid_len + 127) / 128 - near + split.tiles - 1) / split.tiles;
-        if (split.slices + (grid_len + 127) / 128 > 65535 || Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
+        sink_slices(split, rows, Hq, Hkv, D, window, sink);
+        const int far = attn::far_from(grid_len, window);
+        split.slices = far < grid_len ? (grid_len - far + split.rows - 1) / split.rows : 0;
+        split.in_main = sinks_apart(rows, Hq, D, sink) ? 0 : split.slices;
+        if (split.in_main + (grid_len + 127) / 128 > 65535 || Hkv > 65535) return ATTN_ERR_UNSUPPORTED;
     }
     const long long nseq = varlen ? num_seqs : B;
-    const size_t need = bwd_ws(rows, Hq, D) + (split.slices > 0 ? sink_ws(rows, nseq, Hkv, D, window, sink) : 0);
+    const size_t need = bwd_ws(rows, Hq, D) + (split.slices > 0 ? sink_ws(rows, nseq, Hq, Hkv, D, window, sink) : 0);
     if (rows > 0 && (!workspace || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
     if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return ATTN_ERR_MISALIGNED;
     if (rows == 0 || (varlen && (num_seqs == 0 || max_seqlen == 0))) return ATTN_OK;

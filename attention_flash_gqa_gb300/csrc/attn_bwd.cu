@@ -99,9 +99,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int share = s_role ? (int)rank : (int)rank - C::NHALF;  // query share of the role work
     const int c0 = (int)rank * 128;  // this CTA's column slice of D
     const int seq = blockIdx.y;
-    // the first a.sink.slices clusters share out the queries that see of tile 0 its sinks alone (the window has left
+    // the first a.sink.in_main clusters share out the queries that see of tile 0 its sinks alone (the window has left
     // it); behind them a cluster for each key tile, tile 0 first: it sees the most queries
-    const int slice = (int)blockIdx.z - a.sink.slices;
+    const int slice = (int)blockIdx.z - a.sink.in_main;
     const bool far = slice < 0;
     const int kv_tile = far ? 0 : slice;
     int seq_start = 0, L = a.S, bcoord = seq;
@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int G = a.Hq / a.Hkv;
     const int q_last = a.window > 0 ? min(L, k0 + kB - 1 + a.window) : L;  // exclusive bound on queries
     const int i_near = (q_last + kB - 1) / kB;
-    const int i_begin = far ? i_near + (int)blockIdx.z * a.sink.tiles : k0 / kB;
-    const int i_end = far ? min(i_begin + a.sink.tiles, (L + kB - 1) / kB) : i_near;
+    const int i_begin = far ? i_near + (int)blockIdx.z * (a.sink.rows / kB) : k0 / kB;
+    const int i_end = far ? min(i_begin + a.sink.rows / kB, (L + kB - 1) / kB) : i_near;
     const int n_qt = i_end - i_begin;
     if (n_qt <= 0) return;  // no such slice (the same for every CTA of the cluster)
     // whether this cluster's dK and dV of the sinks are one part of several
@@ -615,60 +615,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Delta = rowsum(dO * o) per (row, head) and zero the fp32 dQ accumulator.
-// One warp per (row, head); D / 32 elements per lane.
+// Whether a row of packed sequences is a far query of its own. (The sequence is looked for by its first row; if the slices are out of
+// order the answer may be no, and the row is then written twice, the far kernel's being the last.)
+__device__ __forceinline__ bool row_is_far(int row, const int32_t* cu, int nseq, int S, int T, int window) {
+    int lo = 0, hi = nseq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= row) lo = mid;
+        else hi = mid - 1;
+    }
+    const int start = cu[lo], L = cu[lo + 1] - start;
+    return varlen_seq_ok(start, L, T, S) && row >= start && row - start < L && row - start >= far_from(L, window);
+}
+
+// Delta = rowsum(dO * o) per (row, head), and zeros in the fp32 dQ accumulator: 4 bytes read and 4 written an element. D / 8 lanes
+// (a warp at most) share a row; a warp has kPrep times its rows in flight, and the grid's warps walk on from there (B = 4, S = 8192,
+// 32 heads of 128: 263 us with one row a warp and a warp for each, 167 so; the bytes take 158).
+// far_window > 0: not of the rows that bwd_far_sink_kernel has; of dense sequences only the others are walked at all.
+template <int D>
+constexpr int kPrep = D == 512 ? 2 : 4;
 template <int D>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint16_t* __restrict__ o, const uint16_t* __restrict__ dO,
                                                        float* __restrict__ delta, float* __restrict__ dq_acc,
-                                                       const int32_t* cu_seqlens, int nseq, int S, int T, int Hq,
-                                                       long long rows_times_heads) {
-    const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31;
-    if (w >= rows_times_heads) return;
-    const long long row = w / Hq;
-    const int h = (int)(w % Hq);
-    constexpr int E = D / 32;  // 2, 4, 8 or 16 elements per lane
-    const uint16_t* orow = o + w * D + lane * E;
-    const uint16_t* drow = dO + w * D + lane * E;
-    float acc = 0.f;
+                                                       const int32_t* __restrict__ cu_seqlens, int nseq, int S, int T, int Hq,
+                                                       int far_window, long long pairs) {
+    constexpr int kLanes = D >= 256 ? 32 : D / 8, kPairs = 32 / kLanes, N = D / kLanes / 8, U = kPrep<D>;
+    const int lane = threadIdx.x & 31, part = lane % kLanes;
+    const int near = min(far_from(S, far_window), S);  // (dense) rows of a sequence that are not far
+    const long long warps = ((long long)gridDim.x * blockDim.x) >> 5;
     auto dot2 = [](uint32_t x, uint32_t y) {
         return __uint_as_float(x << 16) * __uint_as_float(y << 16) +
                __uint_as_float(x & 0xffff0000u) * __uint_as_float(y & 0xffff0000u);
     };
-    if constexpr (E >= 8) {
+    for (long long at = (((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5) * (U * kPairs); at < pairs; at += warps * (U * kPairs)) {
+        uint4 x[U][N], y[U][N];
+        size_t w[U], li[U];
+        bool mine[U];
 #pragma unroll
-        for (int e = 0; e < E; e += 8) {
-            const uint4 a = *reinterpret_cast<const uint4*>(orow + e);
-            const uint4 b = *reinterpret_cast<const uint4*>(drow + e);
-            acc += dot2(a.x, b.x) + dot2(a.y, b.y) + dot2(a.z, b.z) + dot2(a.w, b.w);
+        for (int i = 0; i < U; ++i) {
+            const long long pair = at + i * kPairs + lane / kLanes;
+            mine[i] = pair < pairs;
+            long long row = pair / Hq;
+            const int h = (int)(pair - row * Hq);
+            if (cu_seqlens) {
+                li[i] = (size_t)h * T + row;  // packed rows are token indices
+                if (far_window > 0 && mine[i]) mine[i] = !row_is_far((int)row, cu_seqlens, nseq, S, T, far_window);
+            } else {
+                const int per = far_window > 0 ? near : S;
+                const long long b = row / per, s = row - b * per;
+                li[i] = ((size_t)b * Hq + h) * S + s;
+                row = b * S + s;
+            }
+            w[i] = ((size_t)row * Hq + h) * D + part * (8 * N);
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                x[i][n] = mine[i] ? *reinterpret_cast<const uint4*>(o + w[i] + 8 * n) : make_uint4(0, 0, 0, 0);
+                y[i][n] = mine[i] ? *reinterpret_cast<const uint4*>(dO + w[i] + 8 * n) : make_uint4(0, 0, 0, 0);
+            }
         }
-    } else if constexpr (E == 4) {
-        const uint2 a = *reinterpret_cast<const uint2*>(orow);
-        const uint2 b = *reinterpret_cast<const uint2*>(drow);
-        acc = dot2(a.x, b.x) + dot2(a.y, b.y);
-    } else {
-        acc = dot2(*reinterpret_cast<const uint32_t*>(orow), *reinterpret_cast<const uint32_t*>(drow));
-    }
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    float* dq = dq_acc + w * D + lane * E;
-    if constexpr (E >= 4) {
+        for (int i = 0; i < U; ++i) {
+            float acc = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(dq + e) = make_float4(0.f, 0.f, 0.f, 0.f);
-    } else {
-        *reinterpret_cast<float2*>(dq) = make_float2(0.f, 0.f);
-    }
-    if (lane == 0) {
-        size_t li;
-        if (cu_seqlens) {
-            li = (size_t)h * T + row;  // packed rows are token indices
-        } else {
-            const long long b = row / S, s = row % S;
-            li = ((size_t)b * Hq + h) * S + s;
+            for (int n = 0; n < N; ++n)
+                acc += dot2(x[i][n].x, y[i][n].x) + dot2(x[i][n].y, y[i][n].y) + dot2(x[i][n].z, y[i][n].z) + dot2(x[i][n].w, y[i][n].w);
+#pragma unroll
+            for (int off = kLanes / 2; off; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+            if (!mine[i]) continue;
+#pragma unroll
+            for (int n = 0; n < 2 * N; ++n) *reinterpret_cast<float4*>(dq_acc + w[i] + 4 * n) = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (part == 0) delta[li[i]] = acc;
         }
-        delta[li] = acc;
     }
-    (void)nseq;
 }
 
 __global__ void __launch_bounds__(256) bwd_finalize_kernel(const float* __restrict__ acc, uint16_t* __restrict__ dq,
@@ -685,50 +703,23 @@ __global__ void __launch_bounds__(256) bwd_finalize_kernel(const float* __restri
     }
 }
 
-// dK and dV of the sinks of the sequences whose far queries were shared out: the sum of the near part and the slices',
-// in that order, whatever order they were computed in. A block owns one (sequence, KV head, sink, 8 dims a thread);
-// reading the parts, a few KB a block, is all that it takes.
-__global__ void __launch_bounds__(64) bwd_sink_sum_kernel(SinkSplit sk, uint16_t* __restrict__ dK, uint16_t* __restrict__ dV,
-                                                          const int32_t* __restrict__ cu, int S, int T, int Hkv, int D, int window) {
-    const int j = blockIdx.x, g = blockIdx.y, seq = blockIdx.z, d = 8 * threadIdx.x;
-    int start = seq * S, L = S;
-    if (cu) {
-        start = cu[seq], L = cu[seq + 1] - start;
-        if (!varlen_seq_ok(start, L, T, S)) return;
-    }
-    const int i_near = (min(L, kB - 1 + window) + kB - 1) / kB, n_qt = (L + kB - 1) / kB;
-    if (i_near >= n_qt || j >= L || d >= D) return;
-    const int parts = 1 + (n_qt - i_near + sk.tiles - 1) / sk.tiles;
-    float v[8] = {}, k[8] = {};
-#pragma unroll 8
-    for (int p = 0; p < parts; ++p) {
-        const float* row = sk.row(seq, start, p, g, Hkv, j, D) + d;
-        const float* rowk = row + (size_t)sk.sink * D;
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(row + e), b = *reinterpret_cast<const float4*>(rowk + e);
-            v[e] += a.x, v[e + 1] += a.y, v[e + 2] += a.z, v[e + 3] += a.w;
-            k[e] += b.x, k[e + 1] += b.y, k[e + 2] += b.z, k[e + 3] += b.w;
-        }
-    }
-    const size_t at = ((size_t)(start + j) * Hkv + g) * D + d;
-    *reinterpret_cast<uint4*>(dV + at) =
-        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    *reinterpret_cast<uint4*>(dK + at) =
-        make_uint4(pack_bf16x2(k[0], k[1]), pack_bf16x2(k[2], k[3]), pack_bf16x2(k[4], k[5]), pack_bf16x2(k[6], k[7]));
-}
-
 template <int D>
 cudaError_t launch_bwd_t(const BwdLaunch& L, cudaStream_t stream) {
     const long long rh = (long long)L.total_rows * L.Hq;
+    const bool apart = L.sink.slices > L.sink.in_main;  // the far queries' sinks are a kernel's own
     {
-        const long long threads = rh * 32;
-        const unsigned blocks = (unsigned)((threads + 255) / 256);
+        const long long pairs = apart && !L.cu_seqlens ? (long long)L.nseq * std::min(far_from(L.S, L.window), L.S) * L.Hq : rh;
+        const long long per_block = 8 * kPrep<D> * (D >= 256 ? 1 : 256 / D);
+        const unsigned blocks = (unsigned)std::min<long long>((pairs + per_block - 1) / per_block, 152LL * 8);
         const ProfMark m = prof_begin(stream, "bwd_prep");
         bwd_prep_kernel<D><<<blocks, 256, 0, stream>>>(L.o, L.dO, L.delta, L.dq_acc, L.cu_seqlens, L.nseq, L.S,
-                                                       L.total_rows, L.Hq, rh);
+                                                       L.total_rows, L.Hq, apart ? L.window : 0, pairs);
         prof_end(stream, m);
         cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    if (apart) {
+        cudaError_t e = launch_bwd_far_sinks(L, stream);
         if (e != cudaSuccess) return e;
     }
     if constexpr (D <= 256) {  // one CTA per key tile and 128-column slice, no cluster
@@ -753,7 +744,7 @@ cudaError_t launch_bwd_t(const BwdLaunch& L, cudaStream_t stream) {
         attr[0].val.clusterDim.x = NC;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
-        cfg.gridDim = dim3(L.Hkv * NC, L.nseq, L.sink.slices + (L.S + kB - 1) / kB);
+        cfg.gridDim = dim3(L.Hkv * NC, L.nseq, L.sink.in_main + (L.S + kB - 1) / kB);
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = kSmem;
         cfg.stream = stream;
@@ -767,11 +758,7 @@ cudaError_t launch_bwd_t(const BwdLaunch& L, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     if (L.sink.slices > 0) {
-        const ProfMark m = prof_begin(stream, "bwd_sink_sum");
-        bwd_sink_sum_kernel<<<dim3(L.sink.sink, L.Hkv, L.nseq), 64, 0, stream>>>(L.sink, L.dK, L.dV, L.cu_seqlens, L.S,
-                                                                                 L.total_rows, L.Hkv, D, L.window);
-        prof_end(stream, m);
-        cudaError_t e = cudaGetLastError();
+        cudaError_t e = launch_bwd_sink_sum(L, stream);
         if (e != cudaSuccess) return e;
     }
     {

@@ -111,9 +111,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = blockIdx.x / C::NSL;        // KV head
     const int c0 = (blockIdx.x % C::NSL) * DS;  // this CTA's columns of dV, dK, dQ
     const int seq = blockIdx.y;
-    // the first a.sink.slices blocks share out the queries that see of tile 0 its sinks alone (the window has left
+    // the first a.sink.in_main blocks share out the queries that see of tile 0 its sinks alone (the window has left
     // it); behind them a block for each key tile, tile 0 first: it sees the most queries
-    const int slice = (int)blockIdx.z - a.sink.slices;
+    const int slice = (int)blockIdx.z - a.sink.in_main;
     const bool far = slice < 0;
     const int kv_tile = far ? 0 : slice;
     int seq_start = 0, L = a.S, bcoord = seq;
@@ -131,8 +131,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int G = a.Hq / a.Hkv;
     const int q_last = a.window > 0 ? min(L, k0 + kB - 1 + a.window) : L;  // exclusive bound on queries
     const int i_near = (q_last + kB - 1) / kB;
-    const int i_begin = far ? i_near + (int)blockIdx.z * a.sink.tiles : k0 / kB;
-    const int i_end = far ? min(i_begin + a.sink.tiles, (L + kB - 1) / kB) : i_near;
+    const int i_begin = far ? i_near + (int)blockIdx.z * (a.sink.rows / kB) : k0 / kB;
+    const int i_end = far ? min(i_begin + a.sink.rows / kB, (L + kB - 1) / kB) : i_near;
     const int n_qt = i_end - i_begin;
     if (n_qt <= 0) return;  // no such slice (uniform)
     // whether this block's dK and dV of the sinks are one part of several
@@ -718,7 +718,7 @@ cudaError_t launch_bwd_small_main(const BwdLaunch& L, cudaStream_t stream) {
     cudaError_t e =
         cudaFuncSetAttribute(bwd_small_kernel<D, DS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    const dim3 grid(L.Hkv * (D / DS), L.nseq, L.sink.slices + (L.S + kB - 1) / kB);
+    const dim3 grid(L.Hkv * (D / DS), L.nseq, L.sink.in_main + (L.S + kB - 1) / kB);
     const ProfMark m = prof_begin(stream, D == 256 ? "bwd_main_d256" : D == 128 ? "bwd_main_d128" : "bwd_main_d64");
     bwd_small_kernel<D, DS><<<grid, kThreads, kSmem, stream>>>(L.tq, L.tk, L.tv, L.tdo, L.tdq, a);
     prof_end(stream, m);

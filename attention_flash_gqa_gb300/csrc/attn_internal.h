@@ -69,17 +69,20 @@ cudaError_t launch_fwd(const FwdLaunch& L, cudaStream_t stream);
 // ---- backward ---------------------------------------------------------------------------
 // Sinks in the backward: the first `sink` keys of a sequence are seen by its every query, the other keys of their tile
 // by those of the window alone. The near queries, those of the tile's windows, belong to the tile's own block; the far ones
-// are shared out in slices of `tiles` query tiles, so that no block has much more to do than one of the window's. The
-// near block and each slice leave dV and dK of the sinks as parts in fp32, [part][Hkv][2][sink][D], and a small kernel
-// adds them up. Parts of a sequence start at floor(first row / rows of a slice) + 2 x its number: it has at most
-// floor(length / rows of a slice) + 2 of them, so none overlap, and nobody has to count those of the others.
+// are shared out in slices of `rows` queries: to a kernel of their own where the sinks are few enough for its warp MMAs, else to
+// blocks of the main kernel, so that none has much more to do than one of the window's. The near block and each slice
+// (in its kernel: each share of a slice) leave dV and dK of the sinks as parts in fp32, [part][Hkv][2][sink][D], and a small kernel
+// adds them up. Parts of a sequence start at (floor(first row / rows of a slice) + 2 x its number) x shares: it has at most
+// (floor(length / rows of a slice) + 1) x shares + 1 of them, so none overlap, and nobody has to count those of the others.
 struct SinkSplit {
     float* part;
     int sink;    // 0: none
-    int slices;  // far slices of the longest sequence that there may be; 0: no query is far
-    int tiles;   // query tiles of a slice
+    int slices;   // far slices of the longest sequence that there may be; 0: no query is far
+    int rows;     // queries of a slice
+    int shares;   // of the heads of a group, each a block and a part of its own
+    int in_main;  // far slices that are blocks of the main kernel: all of them, or none where a kernel of their own has them
     __host__ __device__ float* row(int seq, int start, int p, int g, int Hkv, int j, int D) const {
-        const size_t at = (size_t)(start / (tiles * 128) + 2 * seq + p) * Hkv + g;
+        const size_t at = ((size_t)(start / rows + 2 * seq) * shares + p) * Hkv + g;
         return part + (at * 2 * sink + j) * D;
     }
 };
@@ -100,6 +103,11 @@ struct BwdLaunch {
     SinkSplit sink;
 };
 cudaError_t launch_bwd(const BwdLaunch& L, cudaStream_t stream);
+constexpr int kFewSinks = 16;  // sinks that launch_bwd_far_sinks takes at most (and head_dim 256 at most)
+cudaError_t launch_bwd_far_sinks(const BwdLaunch& L, cudaStream_t stream);
+cudaError_t launch_bwd_sink_sum(const BwdLaunch& L, cudaStream_t stream);
+// First far query of a sequence of L tokens (a multiple of 128; L or more: there are none).
+__host__ __device__ __forceinline__ int far_from(int L, int window) { return ((127 + window < L ? 127 + window : L) + 127) / 128 * 128; }
 // main kernel of the backward at D = 64 / 128 (one CTA per key tile; attn_bwd_small.cu)
 template <int D>
 cudaError_t launch_bwd_small_main(const BwdLaunch& L, cudaStream_t stream);

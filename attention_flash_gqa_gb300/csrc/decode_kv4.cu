@@ -67,27 +67,12 @@ struct Args {
     float scale_log2;
 };
 
-// d += a b on one warp: a 16 x 16 (row-major), b 16 x 8 (column-major), bf16 in, fp32 out.
-// Fragments: g = lane / 4, c = lane % 4; a = {(g, 2c..2c+1), (g+8, 2c..), (g, 2c+8..2c+9), (g+8, 2c+8..)},
-// b = {(2c..2c+1, g), (2c+8.., g)}, d = {(g, 2c), (g, 2c+1), (g+8, 2c), (g+8, 2c+1)}.
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// The same from zero: d = a b.
+// mma_16x8x16_bf16 from zero: d = a b.
 __device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-// An 8 x 8 matrix of 16-bit values, lane (g, c) holding columns 2c, 2c+1 of row g, transposed.
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
 }
 __device__ __forceinline__ void lds64(uint32_t addr, uint32_t& a, uint32_t& b) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr) : "memory");
@@ -382,8 +367,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
                     for (int x = 0; x < 4; ++x) qf[gr][x] = bf16x2_mul(qf[gr][x], x & 1 ? by : by16);
                     float d[4] = {0.f, 0.f, 0.f, 0.f};
                     constexpr uint32_t kLow = 0x80088008u, kHigh = 0x80808080u;  // -8 * 2^-133, -8 * 2^-129
-                    mma(d, kLow, kLow, kHigh, kHigh, qf[gr][0], qf[gr][1]);
-                    mma(d, kLow, kLow, kHigh, kHigh, qf[gr][2], qf[gr][3]);
+                    mma_16x8x16_bf16(d, kLow, kLow, kHigh, kHigh, qf[gr][0], qf[gr][1]);
+                    mma_16x8x16_bf16(d, kLow, kLow, kHigh, kHigh, qf[gr][2], qf[gr][3]);
                     const float even = __shfl_sync(0xffffffffu, d[0], g >> 1), odd = __shfl_sync(0xffffffffu, d[1], g >> 1);
                     minus[gr] = g & 1 ? odd : even;
                 }
@@ -425,7 +410,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
                     const int w = 2 * (c % (kGroups / 2));
                     const uint32_t a0 = lds32(rec + F::key_scale(g, w)), a1 = lds32(rec + F::key_scale(g + 8, w));
                     mma0(s, a0, a1, a0, a1, eight[0], eight[1]);
-                    if (kGroups == 8) mma(s, a0, a1, a0, a1, eight[2], 0u);
+                    if (kGroups == 8) mma_16x8x16_bf16(s, a0, a1, a0, a1, eight[2], 0u);
                 }
                 uint32_t sw[2][kGroups / 2];  // scales of tokens g, g + 8: two groups a word
 #pragma unroll
@@ -450,7 +435,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
                         float d[4];
                         const uint32_t w0 = kw[0][x], w1 = kw[1][x], y0 = w0 >> 8, y1 = w1 >> 8;
                         mma0(d, w0 & kLowNibbles, w1 & kLowNibbles, w0 & kHighNibbles, w1 & kHighNibbles, qf[gr][0], qf[gr][1]);
-                        mma(d, y0 & kLowNibbles, y1 & kLowNibbles, y0 & kHighNibbles, y1 & kHighNibbles, qf[gr][2], qf[gr][3]);
+                        mma_16x8x16_bf16(d, y0 & kLowNibbles, y1 & kLowNibbles, y0 & kHighNibbles, y1 & kHighNibbles, qf[gr][2], qf[gr][3]);
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             const float sc = __uint_as_float(gr & 1 ? sw[r][gr / 2] & 0xffff0000u : sw[r][gr / 2] << 16);
@@ -537,7 +522,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
 #pragma unroll
                         for (int d = 0; d < 4; d += 2) {
                             const uint32_t y0 = x0 >> (4 * d), y1 = x1 >> (4 * d);
-                            mma(o[bl][half * 2 + d / 2], bf16x2_fma(y0 & kLowNibbles, fl0, c0), bf16x2_fma(y0 & kHighNibbles, fh0, c0),
+                            mma_16x8x16_bf16(o[bl][half * 2 + d / 2], bf16x2_fma(y0 & kLowNibbles, fl0, c0), bf16x2_fma(y0 & kHighNibbles, fh0, c0),
                                 bf16x2_fma(y1 & kLowNibbles, fl1, c1), bf16x2_fma(y1 & kHighNibbles, fh1, c1), b0, b1);
                         }
                     }

@@ -86,6 +86,60 @@ def test_gradient(D, Hq, Hkv, S, window, sink):
     assert torch.equal(got[1], again[1]) and torch.equal(got[2], again[2])
 
 
+# queries past the first tile's windows in many sequences, with empty ones and some without such queries between them
+MANY = [([130, 0, 129, 257, 5, 0, 300, 193] * 5, 1), ([700, 1, 1100], 60), ([4] * 1100 + [260, 40, 280], 3)]
+
+
+def check_gradient_packed(D, Hq, Hkv, sink, lens, window, device="cpu"):
+    scale, T = 1 / math.sqrt(D), sum(lens)
+    q, k, v, do = (x.to(device) for x in rows(T + 3, Hq, Hkv, D, sink + D))  # three rows behind the last sequence
+    with torch.device(device):
+        want = ref.packed(lambda *x: ref.backward(*x, scale, window, sink), lens, *(x[:T] for x in (q, k, v, do)))
+    q, k, v, do = (x.cuda() for x in (q, k, v, do))
+    o, lse = attn.attn_fwd_varlen(q, k, v, cu_of(lens), max(lens), window=window, sink=sink, scale=scale)
+    dq, dk, dv = (torch.full_like(x, 7.0) for x in (q, k, v))
+    attn.attn_bwd(q, k, v, o, lse, do, dq, dk, dv, window=window, sink=sink, scale=scale, cu_seqlens=cu_of(lens), max_seqlen=max(lens))
+    assert attn.attn_get_device_status() == 0
+    assert bool((dk[T:] == 7.0).all()) and bool((dv[T:] == 7.0).all())
+    for i, (name, got) in enumerate((("dq", dq), ("dk", dk), ("dv", dv))):
+        close(name, got[:T].cpu(), want[2 * i].cpu(), want[2 * i + 1].cpu())
+    return q, k, v, o, lse, do, dk, dv
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 3, 1), (128, 4, 2), (256, 2, 1), (512, 2, 2)])
+@pytest.mark.parametrize("sink", [2, 16, 17])
+@pytest.mark.parametrize("lens,window", MANY)
+def test_gradient_packed(D, Hq, Hkv, sink, lens, window):
+    check_gradient_packed(D, Hq, Hkv, sink, lens, window)
+
+
+# 2^25 elements of q and more, with few sinks: the far queries are a kernel's own. (The 64-bit side on the GPU as well.)
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 64, 64), (64, 96, 2), (128, 40, 8), (128, 64, 1), (256, 32, 16), (256, 33, 11)])
+@pytest.mark.parametrize("sink", [1, 16])
+@pytest.mark.parametrize("lens,window", [(x * (9000 // sum(x) + 1), w) for x, w in MANY[:2]] + [([40] * 200 + [261] * 5, 3)])
+def test_gradient_packed_of_large_calls(D, Hq, Hkv, sink, lens, window):
+    assert (sum(lens) + 3) * Hq * D >= 2 ** 25
+    q, k, v, o, lse, do, dk, dv = check_gradient_packed(D, Hq, Hkv, sink, lens, window, "cuda")
+    again = attn.attn_bwd(q, k, v, o, lse, do, window=window, sink=sink, scale=1 / math.sqrt(D), cu_seqlens=cu_of(lens), max_seqlen=max(lens))
+    T = sum(lens)
+    assert torch.equal(again[1][:T], dk[:T]) and torch.equal(again[2][:T], dv[:T])
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,B,S,window,sink", [(64, 64, 8, 33, 257, 1, 16), (128, 32, 16, 3, 2777, 130, 5), (256, 24, 4, 8, 700, 300, 3)])
+def test_gradient_of_large_calls(D, Hq, Hkv, B, S, window, sink):
+    assert B * S * Hq * D >= 2 ** 25
+    scale = 1 / math.sqrt(D)
+    x = [t.cuda() for t in rows(B * S, Hq, Hkv, D, S + D)]
+    with torch.device("cuda"):
+        want = ref.packed(lambda *t: ref.backward(*t, scale, window, sink), [S] * B, *x)
+    q, k, v, do = (t.view(B, S, -1, D) for t in x)
+    o, lse = attn.attn_fwd(q, k, v, window=window, sink=sink, scale=scale)
+    got = attn.attn_bwd(q, k, v, o, lse, do, window=window, sink=sink, scale=scale)
+    assert attn.attn_get_device_status() == 0
+    for i, name in enumerate(("dq", "dk", "dv")):
+        close(name, got[i].flatten(0, 1).cpu(), want[2 * i].cpu(), want[2 * i + 1].cpu())
+
+
 @pytest.mark.parametrize("D", [64, 128, 256, 512])
 def test_gradient_against_differences(D):
     """The GPU's gradient along a direction against the difference of the 64-bit loss on both sides."""
