@@ -10,7 +10,8 @@
 // backend support ..." ("3x fwd / 6x bwd vs SDPA": the backward is where the time goes).
 //
 // Kernels:
-//  1. bwd_prep: Delta per query row (fp32) and zeroing of the fp32 dQ accumulator.
+//  1. bwd_prep: Delta per query row (fp32) and zeroing of the fp32 dQ accumulator. (With sinks, attn_bwd_sink.cu may do that for the queries
+//     past key tile 0's windows.)
 //  2. bwd_main: one thread-block cluster per (KV tile of 128 keys, KV head); its
 //     NC = D / 128 = 4 CTAs each own one 128-wide column slice c of D and accumulate dV_c
 //     and dK_c for the tile in tensor memory while looping over every query head of the

@@ -34,6 +34,10 @@
 // UMMA issuer and TMEM owner. The issuer computes dQ before dK, so the readout starts while dK
 // runs. Each half of the score columns keeps its P^T (bf16 pairs) in the first 32 columns of its
 // own half of R0.
+//
+// Sinks: every query of a sequence sees key tile 0 then, where its other keys are seen by the window's queries alone. SinkSplit
+// (attn_internal.h) says how those far queries are shared out: to bwd_far_sink_kernel, or in slices to blocks of this kernel, which are
+// first in the grid so that they do not end last. An edge tile's mask is a word with a bit a query for each 32 of them.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -53,7 +57,7 @@ constexpr int kEw = 256;  // elementwise threads
 constexpr uint32_t kSub = 16384;  // 128 rows x 64 bf16, 128-byte swizzle
 constexpr float kLog2e = 1.4426950408889634f;
 // P is held times 2^15: at most 1, it then fits fp16 with all of its bits down to 2^-29. dS is formed from that (three bits more
-// than from the bf16 P that dV's product takes); dV, dK and dQ have the factor taken out where they leave tensor memory. (Scores of
+// than from the bf16 P that dV's product takes: dQ and dK 0.0024 off the 64-bit result, relatively, instead of 0.0029); dV, dK and dQ have the factor taken out where they leave tensor memory. (Scores of
 // 2^24 and more, whose logsumexp fp32 holds to whole numbers at best, give P above 1: past 2 it counts as 2 in dS.)
 constexpr float kPUp = 15.f, kPDown = 1.f / 32768.f;
 

@@ -5,7 +5,9 @@
 // so that value is n = -8, the one level that has no counterpart, and a step is an eighth of it instead of a seventh. Nothing is read
 // of the record, and no byte holds two tokens: tokens of a call may be any.
 // unpack: pages back as bf16 pages, exactly. A thread has 8 dims of two neighbouring tokens (which share the V sectors).
-// Both are bound by memory: see the table of measured cases.
+// 8192 tokens, 16 heads of 256: append 31 us (172 MB, 0.81 of the copy rate; behind other work 36, 0.70 of its issue slots used: its
+// arithmetic is kept on the pipe of the multiplications as far as that goes, before which it took 66), unpack 28.5 (0.89). A
+// decode step's few rows are launch and latency: 2.9 and 6 us, the latter the host's (two outputs to allocate).
 #include <cuda_runtime.h>
 
 #include "attn_internal.h"

@@ -36,7 +36,8 @@
  *    exceeded its time limit) do not trap: the kernel records a flag and finishes,
  *    and attn_get_device_status() reports it.
  *  - Supported shapes: D in {64, 128, 256, 512} for prefill / backward, D in {128, 256} for
- *    decode, D in {64, 128, 256, 512} for the merge, the head norm and the tree attention;
+ *    decode, D in {64, 128, 256, 512} for the merge, the head norm and the tree attention, D in
+ *    {64, 128, 256} for the 4-bit cache;
  *    Hq % Hkv == 0, causal = 1. bf16 values are passed as raw 16-bit patterns.
  */
 #ifndef ATTN_GB300_ATTN_H
@@ -240,7 +241,9 @@ ATTN_API size_t attn_decode_paged_noalloc_max_bytes(void);
  *
  * with 0 <= sink <= ATTN_MAX_SINK; a negative sink is rejected, and with window <= 0 or sink = 0 the results are those of the
  * calls without. (No counterpart on the pages. A model with such layers keeps its scores' sums steady over contexts far longer
- * than the window.) Everything else is as described there: layouts, checks, device checks, workspaces.
+ * than the window.) Everything else is as described there: layouts, checks, device checks, workspaces. K and V are read by tiles of 128
+ * keys (decode: pages of 16); of a tile or page that is read, keys hidden by the mask have probability 0, but their K and V must be
+ * finite where they belong to the sequence (decode: any).
  */
 ATTN_API int attn_fwd_sink(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_bf16* o, float* lse, int B,
                            int Hq, int Hkv, int S, int D, float scale, int causal, int window, int sink, void* workspace,
