@@ -153,7 +153,7 @@ size_t bwd_ws(long long rows, int Hq, int D) {
 }
 // Whether the far queries' sinks are a kernel's own (attn_bwd_sink.cu): where they fit its MMAs and q is large. In small calls the
 // slices in the main kernel mostly fill what its last wave of blocks leaves idle. (The whole gradient, this way and that, us: q of 2^27
-// elements, window 1000, head_dim 256 3075 and 3271, 128 1922 and 2100; of 2^25, eleven shapes: from 10 % less to 8 % more, 4 % less in
+// elements, window 1000, head_dim 256 3067 and 3257, 128 1920 and 2090; of 2^25, eleven shapes: from 10 % less to 8 % more, 4 % less in
 // the mean; of 2^24, 32 heads of 128: 308 and 285 at window 1000, 171 and 159 at 250.)
 bool sinks_apart(long long rows, int Hq, int D, int sink) { return D <= 256 && sink <= attn::kFewSinks && rows * Hq * D >= 1ll << 25; }
 // Rows of a slice of the far queries, and shares of its heads. Blocks of the main kernel: as many rows as a block of the window has, but

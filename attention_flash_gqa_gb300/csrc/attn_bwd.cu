@@ -630,63 +630,53 @@ __device__ __forceinline__ bool row_is_far(int row, const int32_t* cu, int nseq,
 }
 
 // Delta = rowsum(dO * o) per (row, head), and zeros in the fp32 dQ accumulator: 4 bytes read and 4 written an element. D / 8 lanes
-// (a warp at most) share a row; a warp has kPrep times its rows in flight, and the grid's warps walk on from there (B = 4, S = 8192,
-// 32 heads of 128: 263 us with one row a warp and a warp for each, 167 so; the bytes take 158).
-// far_window > 0: not of the rows that bwd_far_sink_kernel has; of dense sequences only the others are walked at all.
-template <int D>
-constexpr int kPrep = D == 512 ? 2 : 4;
+// (a warp at most) share a row, 16 bytes each (4 x 8192 rows of 32 heads of 128: 155 us, 1.02 of the copy rate; 184 with a warp a row.
+// Heads of 64, 16384 rows: 43 and 88. Several rows in flight and fewer warps that walk on were slower by 3 to 20 %).
+// far_window > 0: not of the rows that bwd_far_sink_kernel has; of dense sequences the warps are the other rows' alone, of packed ones
+// a warp looks at kLook places.
+constexpr int kLook = 8;
 template <int D>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint16_t* __restrict__ o, const uint16_t* __restrict__ dO,
                                                        float* __restrict__ delta, float* __restrict__ dq_acc,
                                                        const int32_t* __restrict__ cu_seqlens, int nseq, int S, int T, int Hq,
                                                        int far_window, long long pairs) {
-    constexpr int kLanes = D >= 256 ? 32 : D / 8, kPairs = 32 / kLanes, N = D / kLanes / 8, U = kPrep<D>;
+    constexpr int kLanes = D >= 256 ? 32 : D / 8, kPairs = 32 / kLanes, N = D / kLanes / 8;
     const int lane = threadIdx.x & 31, part = lane % kLanes;
-    const int near = min(far_from(S, far_window), S);  // (dense) rows of a sequence that are not far
     const long long warps = ((long long)gridDim.x * blockDim.x) >> 5;
     auto dot2 = [](uint32_t x, uint32_t y) {
         return __uint_as_float(x << 16) * __uint_as_float(y << 16) +
                __uint_as_float(x & 0xffff0000u) * __uint_as_float(y & 0xffff0000u);
     };
-    for (long long at = (((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5) * (U * kPairs); at < pairs; at += warps * (U * kPairs)) {
-        uint4 x[U][N], y[U][N];
-        size_t w[U], li[U];
-        bool mine[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const long long pair = at + i * kPairs + lane / kLanes;
-            mine[i] = pair < pairs;
-            long long row = pair / Hq;
-            const int h = (int)(pair - row * Hq);
-            if (cu_seqlens) {
-                li[i] = (size_t)h * T + row;  // packed rows are token indices
-                if (far_window > 0 && mine[i]) mine[i] = !row_is_far((int)row, cu_seqlens, nseq, S, T, far_window);
-            } else {
-                const int per = far_window > 0 ? near : S;
-                const long long b = row / per, s = row - b * per;
-                li[i] = ((size_t)b * Hq + h) * S + s;
-                row = b * S + s;
-            }
-            w[i] = ((size_t)row * Hq + h) * D + part * (8 * N);
+    for (long long at = (((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5) * kPairs; at < pairs; at += warps * kPairs) {
+        const long long pair = at + lane / kLanes;
+        bool mine = pair < pairs;
+        long long row = pair / Hq;
+        const int h = (int)(pair - row * Hq);
+        size_t li;
+        if (cu_seqlens) {
+            li = (size_t)h * T + row;  // packed rows are token indices
+            if (far_window > 0 && mine) mine = !row_is_far((int)row, cu_seqlens, nseq, S, T, far_window);
+        } else {
+            const int per = far_window > 0 ? min(far_from(S, far_window), S) : S;
+            const long long b = row / per, s = row - b * per;
+            li = ((size_t)b * Hq + h) * S + s;
+            row = b * S + s;
+        }
+        const size_t w = ((size_t)row * Hq + h) * D + part * (8 * N);
+        float acc = 0.f;
+        if (mine) {
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                x[i][n] = mine[i] ? *reinterpret_cast<const uint4*>(o + w[i] + 8 * n) : make_uint4(0, 0, 0, 0);
-                y[i][n] = mine[i] ? *reinterpret_cast<const uint4*>(dO + w[i] + 8 * n) : make_uint4(0, 0, 0, 0);
+                const uint4 x = *reinterpret_cast<const uint4*>(o + w + 8 * n), y = *reinterpret_cast<const uint4*>(dO + w + 8 * n);
+                acc += dot2(x.x, y.x) + dot2(x.y, y.y) + dot2(x.z, y.z) + dot2(x.w, y.w);
             }
         }
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            float acc = 0.f;
+        for (int off = kLanes / 2; off; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+        if (!mine) continue;
 #pragma unroll
-            for (int n = 0; n < N; ++n)
-                acc += dot2(x[i][n].x, y[i][n].x) + dot2(x[i][n].y, y[i][n].y) + dot2(x[i][n].z, y[i][n].z) + dot2(x[i][n].w, y[i][n].w);
-#pragma unroll
-            for (int off = kLanes / 2; off; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-            if (!mine[i]) continue;
-#pragma unroll
-            for (int n = 0; n < 2 * N; ++n) *reinterpret_cast<float4*>(dq_acc + w[i] + 4 * n) = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (part == 0) delta[li[i]] = acc;
-        }
+        for (int n = 0; n < 2 * N; ++n) *reinterpret_cast<float4*>(dq_acc + w + 4 * n) = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (part == 0) delta[li] = acc;
     }
 }
 
@@ -710,8 +700,8 @@ cudaError_t launch_bwd_t(const BwdLaunch& L, cudaStream_t stream) {
     const bool apart = L.sink.slices > L.sink.in_main;  // the far queries' sinks are a kernel's own
     {
         const long long pairs = apart && !L.cu_seqlens ? (long long)L.nseq * std::min(far_from(L.S, L.window), L.S) * L.Hq : rh;
-        const long long per_block = 8 * kPrep<D> * (D >= 256 ? 1 : 256 / D);
-        const unsigned blocks = (unsigned)std::min<long long>((pairs + per_block - 1) / per_block, 152LL * 8);
+        const long long per_block = 8 * (D >= 256 ? 1 : 256 / D) * (apart && L.cu_seqlens ? kLook : 1);
+        const unsigned blocks = (unsigned)((pairs + per_block - 1) / per_block);
         const ProfMark m = prof_begin(stream, "bwd_prep");
         bwd_prep_kernel<D><<<blocks, 256, 0, stream>>>(L.o, L.dO, L.delta, L.dq_acc, L.cu_seqlens, L.nseq, L.S,
                                                        L.total_rows, L.Hq, apart ? L.window : 0, pairs);

@@ -16,7 +16,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 //   S^T = K Q^T, dP^T = V dO^T (16 keys x 16 rows a warp, by k = D), Delta = rowsum(dO o), P^T = exp2(S^T - lse),
 //   dS^T = P^T (dP^T - Delta), dQ = dS K to the accumulator, dV += P^T dO, dK += dS^T Q.
 // So it is bound by memory: 6 bytes read and 4 written an element of q (the pass without q and sums: 4 and 4). At B = 2, S = 8192, 32 heads of
-// 256, window 1024: 203 us for 1.15 GB, 0.83 of the copy rate, where the slices in the main kernel take 260 and the pass 136 more.
+// 256, window 1024: 203 us for 1.15 GB, 0.83 of the copy rate, where the slices in the main kernel take 260 and the pass 128 more.
 // A block has a slice of queries and the query heads of one KV head or a share of them, 64 rows a step, copied to shared memory by cp.async (chunks of
 // 16 bytes at chunk ^ row % 8, so that the matrix loads touch every bank once). A warp has 16 of the rows for S, dP and dQ,
 // then all 64 rows and a quarter of the dims for dV and dK, which stay in registers over the slice. P and dS are rounded to bf16 for their
