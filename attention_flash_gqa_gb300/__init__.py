@@ -26,7 +26,7 @@ Entry points (same names as the C ABI):
   ``attn_qk_norm_rope_paged`` the same with K and V written into the paged caches by slot -> q_out
 * ``attn_tree_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, tree_mask, max_q_len, ...)``
   drafted token trees over a paged cache: packed rows [T,Hq,D] -> (o, lse[Hq,T])
-* ``attn_workspace_size``, ``attn_get_device_status``, ``attn_status_string``
+* ``attn_workspace_size``, ``attn_bwd_sink_workspace_size``, ``attn_get_device_status``, ``attn_status_string``
 * ``sink=`` of attn_fwd, attn_fwd_varlen, attn_fwd_paged, attn_bwd and attn_decode_paged: with a window, a sequence's first keys
   that stay visible past it
 * ``attn_kv4_append(k, v, slots, kv_cache)`` keys and values into a paged cache of 4-bit codes, ``attn_kv4_unpack(kv_cache, pages)``
@@ -47,6 +47,7 @@ __all__ = [
     "attn_launch_count", "attn_profile_start", "attn_profile_stop", "attn_decode_paged_noalloc",
     "attn_selftest_wait_timeout", "attn_merge_lse", "attn_paged_plan", "PagedPlan", "attn_qk_norm_rope",
     "attn_qk_norm_rope_bwd", "attn_qk_norm_rope_paged", "attn_tree_paged", "attn_kv4_append", "attn_kv4_unpack", "attn_decode_kv4",
+    "attn_bwd_sink_workspace_size",
     "ATTN_OP_FWD", "ATTN_OP_FWD_VARLEN", "ATTN_OP_BWD", "ATTN_OP_BWD_VARLEN", "ATTN_OP_DECODE_PAGED",
     "ATTN_OP_QK_NORM_ROPE_BWD", "ATTN_OP_TREE_PAGED", "ATTN_OP_DECODE_KV4",
 ]
@@ -142,6 +143,11 @@ def attn_status_string(status: int) -> str:
 def attn_workspace_size(op: int, B: int = 0, Hq: int = 0, Hkv: int = 0, S: int = 0, D: int = 0, num_seqs: int = 0,
                         max_pages_per_seq: int = 0) -> int:
     return int(load_library().attn_workspace_size(op, B, Hq, Hkv, S, D, num_seqs, max_pages_per_seq))
+
+
+def attn_bwd_sink_workspace_size(B: int, Hq: int, Hkv: int, S: int, D: int, num_seqs: int = 0, window: int = 0, sink: int = 0) -> int:
+    """Bytes of attn_bwd's workspace for a window with sinks; packed sequences: B = 1, S = total tokens and num_seqs."""
+    return int(load_library().attn_bwd_sink_workspace_size(B, Hq, Hkv, S, D, num_seqs, window, sink))
 
 
 def attn_launch_count() -> int:

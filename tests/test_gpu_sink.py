@@ -297,3 +297,24 @@ def test_gradient_of_scores_that_fp32_holds_coarsely(D):
         got = attn.attn_bwd(q, k, v, o, lse, do, window=window, sink=sink, scale=1.0)
         assert attn.attn_get_device_status() == 0
         assert all(bool(t.isfinite().all()) for t in (o, lse, *got))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,sink,lens,window", [
+    (128, 4, 2, 100, [700, 1, 0, 1100, 130, 129], 1), (512, 4, 1, 4, [900, 640, 3], 100), (64, 3, 3, 16, [2000, 129, 128], 5),
+    (128, 40, 8, 16, [300, 150, 129, 700] * 6, 20), (256, 33, 11, 3, [129] * 40, 1), (64, 96, 2, 7, [5999], 1)])
+def test_gradient_in_a_given_workspace(D, Hq, Hkv, sink, lens, window):
+    """Exactly the bytes that attn_bwd_sink_workspace_size names, whatever they hold, and none behind them."""
+    T, scale = sum(lens), 1 / math.sqrt(D)
+    q, k, v, do = (x.cuda() for x in rows(T, Hq, Hkv, D, 31))
+    at = dict(window=window, sink=sink, scale=scale, cu_seqlens=cu_of(lens), max_seqlen=max(lens))
+    o, lse = attn.attn_fwd_varlen(q, k, v, at["cu_seqlens"], max(lens), window=window, sink=sink, scale=scale)
+    want = attn.attn_bwd(q, k, v, o, lse, do, **at)
+    n = attn.attn_bwd_sink_workspace_size(1, Hq, Hkv, T, D, len(lens), window, sink)
+    room = torch.full((n + (64 << 20),), 255, dtype=torch.uint8, device="cuda")  # (NaN, were it read)
+    given = [torch.empty_like(x) for x in (q, k, v)]
+    got = attn.attn_bwd(q, k, v, o, lse, do, *given, workspace=room[:n], **at)
+    assert all(a is b for a, b in zip(got, given)) and attn.attn_get_device_status() == 0
+    assert bool((room[n:] == 255).all())
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2]) and bool(got[0].isfinite().all())
+    with pytest.raises(attn.AttnError):
+        attn.attn_bwd(q, k, v, o, lse, do, *given, workspace=room[:n - 1], **at)
