@@ -318,3 +318,47 @@ def test_gradient_in_a_given_workspace(D, Hq, Hkv, sink, lens, window):
     assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2]) and bool(got[0].isfinite().all())
     with pytest.raises(attn.AttnError):
         attn.attn_bwd(q, k, v, o, lse, do, *given, workspace=room[:n - 1], **at)
+
+
+def test_bad_slices_of_a_large_call():
+    """As above, where the far queries are a kernel's own."""
+    D, Hq, how = 128, 96, dict(window=30, sink=4, scale=0.1)
+    lens = [1300, 1400, 300]
+    assert sum(lens) * Hq * D >= 2 ** 25
+    x = [t.cuda() for t in rows(sum(lens), Hq, 3, D, 12)]
+    with torch.device("cuda"):
+        want = ref.packed(lambda *t: ref.backward(*t, 0.1, 30, 4), [1300], *(t[:1300] for t in x))
+    q, k, v, do = x
+    o, lse = attn.attn_fwd_varlen(q, k, v, cu_of(lens), 1400, **how)
+    dq, dk, dv = (torch.full_like(t, 7) for t in (q, k, v))
+    cu = torch.tensor([0, 1300, 2700, 3100], dtype=torch.int32).cuda()
+    attn.attn_bwd(q, k, v, o, lse, do, dq, dk, dv, cu_seqlens=cu, max_seqlen=1350, **how)
+    assert attn.attn_get_device_status() == 7
+    for i, t in enumerate((dq, dk, dv)):
+        close("first", t[:1300].cpu(), want[2 * i].cpu(), want[2 * i + 1].cpu())
+    assert (dk[1300:] == 7).all() and (dv[1300:] == 7).all() and (dq[1300:] == 0).all()
+
+
+def test_large_gradient_captured_and_on_two_streams():
+    S, D, how = 4200, 256, dict(window=500, sink=16)
+    q, k, v, do = (t.view(1, S, -1, D).cuda() for t in rows(S, 32, 16, D, 8))
+    assert q.numel() >= 2 ** 25
+    o, lse = attn.attn_fwd(q, k, v, **how)
+    want = attn.attn_bwd(q, k, v, o, lse, do, **how)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = [attn.attn_bwd(q, k, v, o, lse, do, stream=s, **how) for s in streams]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for g in got for x, y in zip(g[1:], want[1:]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = attn.attn_bwd(q, k, v, o, lse, do, **how)
+    for _ in range(2):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+        assert (got[0].float() - want[0].float()).abs().max() <= 2.0 ** -7 * want[0].float().abs().max()  # (fp32 sums in no fixed order)
+    assert attn.attn_get_device_status() == 0
