@@ -4,7 +4,7 @@
 // at 18 D bytes a page and KV head against 64 D in bf16 the arithmetic is no longer free. Measured, call after call: 12 contexts of 5 to
 // 60 thousand keys, 8 heads of 128: 105 us for 498 MB, 0.70 of the copy rate (in bf16 its 1.77 GB alone would take 261); 64 requests of 256
 // to 1024: 20.0 us for 46 MB; 33 requests, 16 heads of 256, window 1024, 4 sinks: 40.0 us for 150 MB. What bounds it: the same rings
-// without arithmetic take 82 us over the long contexts. A unit at D = 128 is 366 instructions of a warp, 164 of them shifts and masks, whose
+// without arithmetic take 82 us over the long contexts. A unit at D = 128 is 360 instructions of a warp, 162 of them shifts and masks, whose
 // pipe is half as wide, and 63 % of the issue slots are used: K's part alone takes 89 us, V's alone 100. The batch pays 5 us of layout and
 // first records, and 2 of the join's launch.
 //
@@ -113,6 +113,7 @@ __device__ __forceinline__ int req_len(const Args& a, int b, bool record) {
 constexpr uint32_t kLowNibbles = 0x000f000fu, kHighNibbles = 0x00f000f0u;
 // Least and largest exponent by which O's sums are kept down. Scales up to 2^(down - 6) times 16 times 2^(129 - down) are finite.
 constexpr int kDownMin = 6, kDownMax = 129;
+static_assert(kDownMin + 121 >= 127, "scales below 2 need no look");
 
 // A unit as its warp needs it.
 struct Unit {
@@ -499,9 +500,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
                     const int gr = bl * F::kBlockGroups + g / (8 / F::kBlockGroups);
                     const uint32_t s0 = lds32(rec + F::value_scale(gr, 2 * c)) & hide0;
                     const uint32_t s1 = lds32(rec + F::value_scale(gr, 2 * c + 8)) & hide1;
-                    // a scale whose exponent is above what `down` allows: bit 15 of its half
+                    // Every `down` allows scales below 2: bit 14 of a half says whether there is a larger one, and only then it is looked at
+                    // closer, whether its exponent is above what `down` allows (bit 15 of a sum).
                     const uint32_t past = (0x8000u - ((uint32_t)(down[bl] + 122) << 7)) * 0x10001u;
-                    if (__any_sync(0xffffffffu, (((s0 & 0x7fff7fffu) + past) | ((s1 & 0x7fff7fffu) + past)) & 0x80008000u)) {
+                    if (__any_sync(0xffffffffu, (s0 | s1) & 0x40004000u) &&
+                        __any_sync(0xffffffffu, (((s0 & 0x7fff7fffu) + past) | ((s1 & 0x7fff7fffu) + past)) & 0x80008000u)) {
                         uint32_t e = max(max(s0 & 0x7f80u, s0 >> 16 & 0x7f80u), max(s1 & 0x7f80u, s1 >> 16 & 0x7f80u)) >> 7;
                         e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));  // the four lanes of a row
                         e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
