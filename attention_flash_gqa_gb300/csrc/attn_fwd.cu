@@ -88,6 +88,7 @@ struct FwdArgs {
     const int32_t* cu_seqlens;
     unsigned* status;
     int Hq, Hkv, S, D, window, n_qtiles, nsplit, T;
+    int heads;  // query heads of a CTA (MULTI)
     int sink;  // first keys of a sequence that stay visible past the window, at most one key tile (0: none)
     float scale_log2;
     // paged prefill: keys / values through a block table, new queries packed by cu_q
@@ -117,13 +118,22 @@ struct FwdArgs {
 // groups of four 1 KB sub-tile atoms, 4 KB apart); its V slot is the paged V slot of its 128
 // columns. The last tile's V slot, when keys past the end must be zeroed, completes on a
 // barrier of its own CTA instead: each CTA zeroes its rows and reports on the even CTA's vfix.
-template <int DQK, bool PAGED, bool PAIR>
+// MULTI: a CTA takes several query heads for its query tile, one after the other (the keys and masks of all are the same). Rings, buffers
+// and phases run on from head to head: while one head's last P V and its end are at work, the next one's Q and first K are on
+// their way and its first scores are made. Of the 7.9 us that a CTA costs beside its key steps at head_dim 256 (start, tensor memory, Q, the
+// first K, the end) a further head pays about half. us with 1, 2 and 4 heads a CTA: 2 x 8192 tokens, 32 heads of 256, window 1024 582, 569,
+// 569; 8 prompts of 1 to 4096, 32 heads of 128, window 500 289, 266, 254; 2 x 4096, 32 heads of 64, window 500 115, 107, 110, causal
+// 262, 255, 255. With few CTAs the last ones run longer alone: 16000 tokens, 8 heads of 128, window 700 (1000 tiles) 94, 104, 102.
+// (An instance of its own: what the loops over heads cost would be 1 to 4 % where there is one.)
+template <int DQK, bool PAGED, bool PAIR, bool MULTI>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                const __grid_constant__ CUtensorMap tv, FwdArgs a) {
     using C = FwdCfg<DQK, PAIR>;
     // ---- which tile ------------------------------------------------------------------
-    const int h = blockIdx.x;
+    static_assert(!MULTI || (!PAGED && !PAIR), "several heads: single CTAs without pages");
+    const int h0 = MULTI ? (int)blockIdx.x * a.heads : (int)blockIdx.x;  // first query head
+    const int heads = MULTI ? min(a.heads, a.Hq - h0) : 1;
     const int seq = blockIdx.y / a.nsplit, split = blockIdx.y % a.nsplit;
     const int q_tile = a.n_qtiles - 1 - (int)blockIdx.z;  // longest tiles first
     int seq_start = 0, L = a.S, bcoord = seq;
@@ -135,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bcoord = 0;
         if (seq_start < 0 || nq < 0 || nq > a.S || seq_start > a.T - nq || nq > L || L > a.max_pages * 16) {
             // inconsistent request: reported, nothing read or written
-            if (threadIdx.x == 0 && split == 0 && h == 0 && q_tile == a.n_qtiles - 1) atomicOr(a.status, DEVSTAT_BOUNDS);
+            if (threadIdx.x == 0 && split == 0 && blockIdx.x == 0 && q_tile == a.n_qtiles - 1) atomicOr(a.status, DEVSTAT_BOUNDS);
             return;
         }
         qoff = L - nq;
@@ -147,14 +157,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!varlen_seq_ok(seq_start, L, a.T, a.S)) {
             // a slice outside the packed rows, or longer than the grid covers: reported, and no
             // row of it is read or written
-            if (threadIdx.x == 0 && split == 0 && h == 0 && q_tile == a.n_qtiles - 1) atomicOr(a.status, DEVSTAT_BOUNDS);
+            if (threadIdx.x == 0 && split == 0 && blockIdx.x == 0 && q_tile == a.n_qtiles - 1) atomicOr(a.status, DEVSTAT_BOUNDS);
             return;
         }
     }
     const int q0 = q_tile * kBQ;
     if (q0 >= nq) return;  // uniform: before any barrier or TMEM use
     const int qp0 = qoff + q0;  // position of the tile's first query
-    const int g = h / (a.Hq / a.Hkv);
+    const int G = a.Hq / a.Hkv;
     const int dv0 = split * C::kDV;
     const int kv_hi = min(L, qp0 + kBQ);
     const int kv_lo = a.window > 0 ? max(0, qp0 - a.window + 1) : 0;
@@ -162,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // key tiles in the order they are taken: the one of the sinks where the window has left it, then the window's
     const int early = a.sink > 0 && t_begin > 0 ? 1 : 0;
     const int n = t_end - t_begin + early;
+    const int steps = heads * n;  // of all heads, one after the other: buffers, ring slots and phases go by these
     auto key_tile = [&](int j) { return j < early ? 0 : t_begin - early + j; };
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -180,8 +191,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* mma_idle = pv_done + 3;          // 1
     uint64_t* vfix = mma_idle + 1;             // 1 (paged): the last tile's V rows past the end are zeroed
     uint64_t* vtail = vfix + 1;                // 1 (paged pair): this CTA's copy of that V slot landed
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(vtail + 1);
+    uint64_t* q_empty = vtail + 1;             // 1: every S of a head is complete, Q may be overwritten
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_empty + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* tile = abort_flag + 1;  // [6]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -199,7 +212,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(mma_idle), 1);
         mbar_init(smem_u32(vfix), PAIR ? 2 : 1);
         mbar_init(smem_u32(vtail), 1);
+        mbar_init(smem_u32(q_empty), 1);
         *abort_flag = 0;
+        // what a head's end needs, kept here so that the softmax's registers need not
+        const int ends[6] = {seq, seq_start, q0, nq, dv0, h0};
+        for (int i = 0; i < 6; ++i) tile[i] = ends[i];
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -227,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool tail_fix = PAGED && (t_end * kBKV > L);
     if (warp == 0 && PAGED) {
         // -------------------- TMA producer, paged keys / values (whole warp) ---------------
+        const int h = h0, g = h / G;
         const int npg = (L + 15) / 16;  // pages of the request
         const int32_t* bt = a.block_table + (size_t)seq * a.max_pages;
         const int sink_pages = min((a.sink + 15) / 16, npg);
@@ -383,20 +401,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tmap(&tk);
             prefetch_tmap(&tv);
             const int row_q = seq_start + q0;
+            auto load_q = [&](int h, uint64_t* bar) {
+                for (int c = 0; c < DQK / 64; ++c) {
+                    if (PAIR) tma_load_4d_pair(sQ + c * kSubBytes, &tq, lead_bar(bar), c * 64, h, row_q, bcoord);
+                    else tma_load_4d(sQ + c * kSubBytes, &tq, smem_u32(bar), c * 64, h, row_q, bcoord);
+                }
+            };
             // pair: the even CTA expects both CTAs' bytes on its barriers, and the copies of both
             // complete there
             if (crank == 0) mbar_expect_tx(smem_u32(q_full), (PAIR ? 2 : 1) * C::kQBytes);
-            for (int c = 0; c < DQK / 64; ++c) {
-                if (PAIR) tma_load_4d_pair(sQ + c * kSubBytes, &tq, lead_bar(q_full), c * 64, h, row_q, bcoord);
-                else tma_load_4d(sQ + c * kSubBytes, &tq, smem_u32(q_full), c * 64, h, row_q, bcoord);
-            }
+            load_q(h0, q_full);
             int slot = 0, round = 0;
             bool ok = true;
             // one slot: kSubs sub-tiles of 128 rows x 64 columns (col0 + 64 sub, rows row0 ..); pair
             // K slots: four sub-tiles of 64 rows (this CTA's keys) x 64 columns
-            auto load_chunk = [&](const CUtensorMap* map, int col0, int row0, bool k_half) -> bool {
+            // `extra`: bytes of another copy that the slot's barrier counts too
+            auto load_chunk = [&](const CUtensorMap* map, int col0, int row0, int g, bool k_half, uint32_t extra) -> bool {
                 if (round > 0 && !mbar_wait(smem_u32(&empty[slot]), (round - 1) & 1, abort_flag, a.status, 0x11)) return false;
-                if (crank == 0) mbar_expect_tx(smem_u32(&full[slot]), (PAIR ? 2 : 1) * C::kSlotBytes);
+                if (crank == 0) mbar_expect_tx(smem_u32(&full[slot]), (PAIR ? 2 : 1) * C::kSlotBytes + extra);
                 const uint32_t dst = sSlots + slot * C::kSlotBytes;
                 if (PAIR) {
                     const uint32_t fb = lead_bar(&full[slot]);
@@ -415,21 +437,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++slot == C::kStages) slot = 0, ++round;
                 return true;
             };
-            auto load_k = [&](int t) -> bool {
-                for (int c = 0; c < C::kQChunks; ++c)
-                    if (!load_chunk(&tk, c * (PAIR ? 256 : C::kSlotCols), seq_start + key_tile(t) * kBKV, true)) return false;
+            // next K / V tile to load, and the head it is for. A further head's Q comes with its first K slot, once every S of the head
+            // before is in tensor memory.
+            int kt = 0, kh = h0, vt = 0, vh = h0;
+            auto next_k = [&](int J) -> bool {
+                const bool with_q = kt == 0 && J > 0;
+                if (with_q) {
+                    if (!mbar_wait(smem_u32(q_empty), (kh - h0 - 1) & 1, abort_flag, a.status, 0x1b)) return false;
+                }
+                for (int c = 0; c < C::kQChunks; ++c) {
+                    uint64_t* bar = &full[slot];
+                    const bool here = with_q && c == 0;
+                    if (!load_chunk(&tk, c * (PAIR ? 256 : C::kSlotCols), seq_start + key_tile(kt) * kBKV, kh / G, true, here ? C::kQBytes : 0u))
+                        return false;
+                    if (here) load_q(kh, bar);
+                }
+                if (++kt == n) kt = 0, ++kh;
                 return true;
             };
-            auto load_v = [&](int t) -> bool {
+            auto next_v = [&]() -> bool {
                 for (int c = 0; c < C::kVChunks; ++c)
-                    if (!load_chunk(&tv, dv0 + c * C::kSlotCols, seq_start + key_tile(t) * kBKV, false)) return false;
+                    if (!load_chunk(&tv, dv0 + c * C::kSlotCols, seq_start + key_tile(vt) * kBKV, vh / G, false, 0u)) return false;
+                if (++vt == n) vt = 0, ++vh;
                 return true;
             };
             // the issuer's order: K(0) .. K(kSBuf - 1), then V(j), K(j + kSBuf) for every step j
-            for (int b = 0; ok && b < C::kSBuf && b < n; ++b) ok = load_k(b);
-            for (int j = 0; ok && j < n; ++j) {
-                ok = load_v(j);
-                if (ok && j + C::kSBuf < n) ok = load_k(j + C::kSBuf);
+            for (int b = 0; ok && b < C::kSBuf && b < steps; ++b) ok = next_k(b);
+            for (int j = 0; ok && j < steps; ++j) {
+                ok = next_v();
+                if (ok && j + C::kSBuf < steps) ok = next_k(j + C::kSBuf);
             }
             // Drain: wait (bounded) for the last copy issued into every slot. Pair: the even CTA's
             // barriers count both CTAs' copies, and the odd CTA stays until then (the cluster
@@ -470,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // descriptor bases, stepped with sdesc_at in the loops
             const uint64_t dQk = sdesc_sw128(sQ, 16, 1024);
+            int s_left = n;  // S of the head yet to come
             auto issue_s = [&](int buf) -> bool {
                 const uint32_t dst = tS0 + buf * 128;
                 for (int c = 0; c < C::kQChunks; ++c) {
@@ -500,12 +537,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     release_slot();
                 }
                 commit(&s_full[buf]);
+                if (MULTI && --s_left == 0) commit(q_empty), s_left = n;
                 return true;
             };
+            int pv = 0;  // P V of the head so far
             auto issue_pv = [&](int j) -> bool {
                 for (int c = 0; c < C::kVChunks; ++c) {
                     if (!next_slot()) return false;
-                    if (tail_fix && j == n - 1 && c == 0) {  // the producer zeroed the rows past the end
+                    if (tail_fix && pv == n - 1 && c == 0) {  // the producer zeroed the rows past the end
                         if (!mbar_wait(smem_u32(vfix), 0, abort_flag, a.status, 0x1f)) return false;
                         tc_fence_after();
                     }
@@ -517,25 +556,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < 8; ++kk) {  // 16 keys per step
                         const uint64_t bd = sdesc_at(dv, PAGED ? kk * 2 * C::kPagedGroupStride : kk * 2048);
                         if (PAIR)
-                            umma_pair_ts(tO, tP + (kk >> 2) * 64 + (kk & 3) * 8, bd, idO, (j > 0 || kk > 0) ? 1u : 0u);
+                            umma_pair_ts(tO, tP + (kk >> 2) * 64 + (kk & 3) * 8, bd, idO, (pv > 0 || kk > 0) ? 1u : 0u);
                         else
                             umma_bf16_ts(tO + c * C::kSlotCols, tP + (kk >> 2) * 64 + (kk & 3) * 8, bd, idO,
-                                         (j > 0 || kk > 0) ? 1u : 0u);
+                                         (pv > 0 || kk > 0) ? 1u : 0u);
                     }
                     release_slot();
                 }
                 commit(&pv_done[j % C::kSBuf]);
+                if (++pv == n) pv = 0;  // (the next head's O: its first P is ready only when every softmax thread has read this one's)
                 return true;
             };
-            for (int b = 0; ok && b < C::kSBuf && b < n; ++b) ok = issue_s(b);
-            for (int j = 0; ok && j < n; ++j) {
+            for (int b = 0; ok && b < C::kSBuf && b < steps; ++b) ok = issue_s(b);
+            for (int j = 0; ok && j < steps; ++j) {
                 ok = mbar_wait(smem_u32(&p_full[j % C::kSBuf]), (j / C::kSBuf) & 1, abort_flag, a.status, 0x14);
                 if (!ok) break;
                 tc_fence_after();
                 ok = issue_pv(j);
                 // S(j + kSBuf) over the buffer P(j) came from: the pipe runs in order, so P V(j)
                 // has read P(j) first
-                if (ok && j + C::kSBuf < n) ok = issue_s(j % C::kSBuf);
+                if (ok && j + C::kSBuf < steps) ok = issue_s(j % C::kSBuf);
             }
             // every issued UMMA has finished before TMEM may be released
             if (PAIR) umma_commit_pair(smem_u32(mma_idle), (uint16_t)1);
@@ -559,10 +599,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* xch = reinterpret_cast<float*>(smem + C::kOffXch);  // [2][128]
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
-            const int buf = j % C::kSBuf;
+        // J: steps of all heads, j: of this one
+        for (int J = 0, j = 0; J < steps; ++J, ++j) {
+            const int buf = J % C::kSBuf;
             bool okw = __all_sync(0xffffffffu,
-                                  mbar_wait(smem_u32(&s_full[buf]), (j / C::kSBuf) & 1, abort_flag, a.status, 0x15));
+                                  mbar_wait(smem_u32(&s_full[buf]), (J / C::kSBuf) & 1, abort_flag, a.status, 0x15));
             float s[64];
             float mx = -INFINITY;
             if (okw) {
@@ -628,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // rescale O: P V(j-1), and so every earlier P V (the MMA pipe completes in order),
                 // must be complete. Its barrier has no older phase pending: s_full(j) implies
                 // P V(j - kSBuf) is complete.
-                const int jp = j - 1;
+                const int jp = J - 1;
                 okw = __all_sync(0xffffffffu, mbar_wait(smem_u32(&pv_done[jp % C::kSBuf]), (jp / C::kSBuf) & 1,
                                                         abort_flag, a.status, 0x16));
                 ok = named_bar_and(pair_bar, 64, okw);
@@ -659,20 +700,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 mbar_arrive(smem_u32(&p_full[buf]));
             }
-        }
+        if (j < n - 1) continue;
         // ---- epilogue: O / l -> bf16, lse -------------------------------------------------
         // the last P V, and so every earlier one; its barrier has no older phase pending
-        bool okw = ok;
+        okw = ok;
         if (okw)
-            okw = mbar_wait(smem_u32(&pv_done[(n - 1) % C::kSBuf]), ((n - 1) / C::kSBuf) & 1, abort_flag, a.status, 0x17);
+            okw = mbar_wait(smem_u32(&pv_done[J % C::kSBuf]), (J / C::kSBuf) & 1, abort_flag, a.status, 0x17);
         okw = __all_sync(0xffffffffu, okw);
         if (ok) xch[hf * 128 + r] = l;  // the exchange buffer is free: both read it before the last barrier
         ok = named_bar_and(pair_bar, 64, ok && okw);
         tc_fence_after();
         if (ok) {
             l += xch[(1 - hf) * 128 + r];
-            const int qrow = q0 + r;  // query row index within the sequence's rows
-            const bool row_ok = qrow < nq;
+            const int seq = tile[0], seq_start = tile[1], dv0 = tile[4], h = tile[5] + J / n;
+            const int qrow = tile[2] + r;  // query row index within the sequence's rows
+            const bool row_ok = qrow < tile[3];
             const bool packed = PAGED || a.cu_seqlens;
             const float inv = l == 0.f ? 0.f : 1.f / l;  // (l is NaN where a score is)
             uint16_t* orow = a.o + ((size_t)(packed ? seq_start + qrow : seq * a.S + qrow) * a.Hq + h) * a.D + dv0;
@@ -693,13 +735,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (row_ok && split == 0 && hf == 0) {
+            if (row_ok && dv0 == 0 && hf == 0) {
                 const float lse = l == 0.f ? -INFINITY : (m_ref + __log2f(l)) * 0.69314718055994531f;
                 const size_t li = packed ? (size_t)h * a.T + seq_start + qrow : ((size_t)seq * a.Hq + h) * a.S + qrow;
                 a.lse[li] = lse;
             }
         }
         tc_fence_before();
+        if (!ok || J + 1 == steps) break;
+        named_bar_sync(pair_bar, 64);  // both have read the row sums before the buffer is reused
+        m_ref = -INFINITY, l = 0.f, j = -1;
+        }
     }
     __syncthreads();
     if (PAIR) {  // the even CTA has drained every copy and product of the pair
@@ -714,8 +760,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (PAIR) cluster_sync_all();  // neither CTA leaves while the other may still address it
 }
 
-template <int DQK, bool PAGED, bool PAIR>
-cudaError_t launch_fwd_t(const FwdLaunch& L, cudaStream_t stream) {
+template <int DQK, bool PAGED, bool PAIR, bool MULTI = false>
+cudaError_t launch_fwd_t(const FwdLaunch& L, int heads, cudaStream_t stream) {
     using C = FwdCfg<DQK, PAIR>;
     FwdArgs a;
     a.o = L.o, a.lse = L.lse, a.cu_seqlens = L.cu_seqlens, a.status = L.status;
@@ -725,11 +771,12 @@ cudaError_t launch_fwd_t(const FwdLaunch& L, cudaStream_t stream) {
     a.n_qtiles = (L.S + kBQ - 1) / kBQ;
     a.nsplit = DQK / C::kDV;
     a.T = L.total_rows;
+    a.heads = heads;
     a.scale_log2 = L.scale * 1.4426950408889634f;
     cudaError_t e =
-        cudaFuncSetAttribute(fwd_kernel<DQK, PAGED, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+        cudaFuncSetAttribute(fwd_kernel<DQK, PAGED, PAIR, MULTI>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    dim3 grid(L.Hq, L.nseq * a.nsplit, a.n_qtiles);
+    dim3 grid((L.Hq + heads - 1) / heads, L.nseq * a.nsplit, a.n_qtiles);
     static const char* const kNames[2][4] = {{"fwd_d64", "fwd_d128", "fwd_d256", "fwd_d512"},
                                              {"fwd_paged_d64", "fwd_paged_d128", "fwd_paged_d256", "fwd_paged_d512"}};
     const char* name = kNames[PAGED ? 1 : 0][DQK == 64 ? 0 : DQK == 128 ? 1 : DQK == 256 ? 2 : 3];
@@ -748,12 +795,12 @@ cudaError_t launch_fwd_t(const FwdLaunch& L, cudaStream_t stream) {
         cfg.stream = stream;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, fwd_kernel<DQK, PAGED, PAIR>, L.tq, L.tk_half, L.tv, a);
+        e = cudaLaunchKernelEx(&cfg, fwd_kernel<DQK, PAGED, PAIR, MULTI>, L.tq, L.tk_half, L.tv, a);
         prof_end(stream, m);
         if (e != cudaSuccess) return e;
         return cudaGetLastError();
     }
-    fwd_kernel<DQK, PAGED, PAIR><<<grid, kThreads, C::kSmem, stream>>>(L.tq, L.tk, L.tv, a);
+    fwd_kernel<DQK, PAGED, PAIR, MULTI><<<grid, kThreads, C::kSmem, stream>>>(L.tq, L.tk, L.tv, a);
     prof_end(stream, m);
     return cudaGetLastError();
 }
@@ -769,14 +816,21 @@ cudaError_t launch_fwd(const FwdLaunch& L, cudaStream_t stream) {
     // CTA) measured slower in pairs (0.713 against 0.665 ms), the pair's fixed cost outweighing
     // the halved stream, so 256 keeps single CTAs.
     const bool pair = L.pair_ok && (L.Hq / L.Hkv) % 2 == 0 && L.D == 512;
-    if (L.D == 64) return paged ? launch_fwd_t<64, true, false>(L, stream) : launch_fwd_t<64, false, false>(L, stream);
-    if (L.D == 128) return paged ? launch_fwd_t<128, true, false>(L, stream) : launch_fwd_t<128, false, false>(L, stream);
+    // several heads a CTA (MULTI) where there are enough tiles for that: 12 for each SM, 24 for four heads
+    const long long tiles = (long long)L.Hq * L.nseq * ((L.S + kBQ - 1) / kBQ);
+    const int heads = paged || L.D > 256 ? 1 : tiles >= 24 * 152 ? 4 : tiles >= 12 * 152 ? 2 : 1;
+    if (L.D == 64)
+        return paged ? launch_fwd_t<64, true, false>(L, 1, stream)
+                     : heads > 1 ? launch_fwd_t<64, false, false, true>(L, heads, stream) : launch_fwd_t<64, false, false>(L, 1, stream);
+    if (L.D == 128)
+        return paged ? launch_fwd_t<128, true, false>(L, 1, stream)
+                     : heads > 1 ? launch_fwd_t<128, false, false, true>(L, heads, stream) : launch_fwd_t<128, false, false>(L, 1, stream);
     if (L.D == 256)
-        return paged ? launch_fwd_t<256, true, false>(L, stream)
-                     : pair ? launch_fwd_t<256, false, true>(L, stream) : launch_fwd_t<256, false, false>(L, stream);
+        return paged ? launch_fwd_t<256, true, false>(L, 1, stream)
+                     : heads > 1 ? launch_fwd_t<256, false, false, true>(L, heads, stream) : launch_fwd_t<256, false, false>(L, 1, stream);
     if (L.D == 512)
-        return paged ? (pair ? launch_fwd_t<512, true, true>(L, stream) : launch_fwd_t<512, true, false>(L, stream))
-                     : pair ? launch_fwd_t<512, false, true>(L, stream) : launch_fwd_t<512, false, false>(L, stream);
+        return paged ? (pair ? launch_fwd_t<512, true, true>(L, 1, stream) : launch_fwd_t<512, true, false>(L, 1, stream))
+                     : pair ? launch_fwd_t<512, false, true>(L, 1, stream) : launch_fwd_t<512, false, false>(L, 1, stream);
     return cudaErrorInvalidValue;
 }
 
