@@ -214,9 +214,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(vtail), 1);
         mbar_init(smem_u32(q_empty), 1);
         *abort_flag = 0;
-        // what a head's end needs, kept here so that the softmax's registers need not
-        const int ends[6] = {seq, seq_start, q0, nq, dv0, h0};
-        for (int i = 0; i < 6; ++i) tile[i] = ends[i];
+        if (MULTI) {  // what a head's end needs, kept here so that the softmax's registers need not
+            const int ends[6] = {seq, seq_start, q0, nq, dv0, h0};
+            for (int i = 0; i < 6; ++i) tile[i] = ends[i];
+        }
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -439,26 +440,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // next K / V tile to load, and the head it is for. A further head's Q comes with its first K slot, once every S of the head
             // before is in tensor memory.
-            int kt = 0, kh = h0, vt = 0, vh = h0;
+            int kt = 0, kh = h0, kg = h0 / G, vt = 0, vh = h0, vg = kg;
             auto next_k = [&](int J) -> bool {
-                const bool with_q = kt == 0 && J > 0;
+                const bool with_q = MULTI && kt == 0 && J > 0;
                 if (with_q) {
                     if (!mbar_wait(smem_u32(q_empty), (kh - h0 - 1) & 1, abort_flag, a.status, 0x1b)) return false;
                 }
                 for (int c = 0; c < C::kQChunks; ++c) {
                     uint64_t* bar = &full[slot];
                     const bool here = with_q && c == 0;
-                    if (!load_chunk(&tk, c * (PAIR ? 256 : C::kSlotCols), seq_start + key_tile(kt) * kBKV, kh / G, true, here ? C::kQBytes : 0u))
+                    if (!load_chunk(&tk, c * (PAIR ? 256 : C::kSlotCols), seq_start + key_tile(kt) * kBKV, kg, true, here ? C::kQBytes : 0u))
                         return false;
                     if (here) load_q(kh, bar);
                 }
-                if (++kt == n) kt = 0, ++kh;
+                if (++kt == n && MULTI) kt = 0, kg = ++kh / G;
                 return true;
             };
             auto next_v = [&]() -> bool {
                 for (int c = 0; c < C::kVChunks; ++c)
-                    if (!load_chunk(&tv, dv0 + c * C::kSlotCols, seq_start + key_tile(vt) * kBKV, vh / G, false, 0u)) return false;
-                if (++vt == n) vt = 0, ++vh;
+                    if (!load_chunk(&tv, dv0 + c * C::kSlotCols, seq_start + key_tile(vt) * kBKV, vg, false, 0u)) return false;
+                if (++vt == n && MULTI) vt = 0, vg = ++vh / G;
                 return true;
             };
             // the issuer's order: K(0) .. K(kSBuf - 1), then V(j), K(j + kSBuf) for every step j
@@ -540,8 +541,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (MULTI && --s_left == 0) commit(q_empty), s_left = n;
                 return true;
             };
-            int pv = 0;  // P V of the head so far
+            int of_head = 0;
             auto issue_pv = [&](int j) -> bool {
+                const int pv = MULTI ? of_head : j;  // P V of the head so far
                 for (int c = 0; c < C::kVChunks; ++c) {
                     if (!next_slot()) return false;
                     if (tail_fix && pv == n - 1 && c == 0) {  // the producer zeroed the rows past the end
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     release_slot();
                 }
                 commit(&pv_done[j % C::kSBuf]);
-                if (++pv == n) pv = 0;  // (the next head's O: its first P is ready only when every softmax thread has read this one's)
+                if (MULTI && ++of_head == n) of_head = 0;  // (the next head's O: its first P is ready only when every softmax thread has read this one's)
                 return true;
             };
             for (int b = 0; ok && b < C::kSBuf && b < steps; ++b) ok = issue_s(b);
@@ -599,6 +601,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* xch = reinterpret_cast<float*>(smem + C::kOffXch);  // [2][128]
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
+        auto finish = [&](int J) {
+            // ---- epilogue: O / l -> bf16, lse -------------------------------------------------
+            // the last P V, and so every earlier one; its barrier has no older phase pending
+            bool okw = ok;
+            if (okw)
+                okw = mbar_wait(smem_u32(&pv_done[J % C::kSBuf]), (J / C::kSBuf) & 1, abort_flag, a.status, 0x17);
+            okw = __all_sync(0xffffffffu, okw);
+            if (ok) xch[hf * 128 + r] = l;  // the exchange buffer is free: both read it before the last barrier
+            ok = named_bar_and(pair_bar, 64, ok && okw);
+            tc_fence_after();
+            if (ok) {
+                l += xch[(1 - hf) * 128 + r];
+                const int qrow = (MULTI ? tile[2] : q0) + r;  // query row index within the sequence's rows
+                const bool row_ok = qrow < (MULTI ? tile[3] : nq);
+                const int h = MULTI ? tile[5] + J / n : h0, first = MULTI ? tile[1] : seq_start, sq = MULTI ? tile[0] : seq;
+                const int d0 = MULTI ? tile[4] : dv0;
+                const bool packed = PAGED || a.cu_seqlens;
+                const float inv = l == 0.f ? 0.f : 1.f / l;  // (l is NaN where a score is)
+                uint16_t* orow = a.o + ((size_t)(packed ? first + qrow : sq * a.S + qrow) * a.Hq + h) * a.D + d0;
+#pragma unroll 1
+                for (int c = hf * (C::kDV / 64); c < (hf + 1) * (C::kDV / 64); ++c) {
+                    uint32_t raw[32];
+                    tmem_ld32(tO + c * 32 + lane_base, raw);
+                    tmem_ld_wait();
+                    if (row_ok) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint4 w;
+                            w.x = pack_bf16x2(__uint_as_float(raw[e]) * inv, __uint_as_float(raw[e + 1]) * inv);
+                            w.y = pack_bf16x2(__uint_as_float(raw[e + 2]) * inv, __uint_as_float(raw[e + 3]) * inv);
+                            w.z = pack_bf16x2(__uint_as_float(raw[e + 4]) * inv, __uint_as_float(raw[e + 5]) * inv);
+                            w.w = pack_bf16x2(__uint_as_float(raw[e + 6]) * inv, __uint_as_float(raw[e + 7]) * inv);
+                            *reinterpret_cast<uint4*>(orow + c * 32 + e) = w;
+                        }
+                    }
+                }
+                if (row_ok && d0 == 0 && hf == 0) {
+                    const float lse = l == 0.f ? -INFINITY : (m_ref + __log2f(l)) * 0.69314718055994531f;
+                    const size_t li = packed ? (size_t)h * a.T + first + qrow : ((size_t)sq * a.Hq + h) * a.S + qrow;
+                    a.lse[li] = lse;
+                }
+            }
+            tc_fence_before();
+        };
         // J: steps of all heads, j: of this one
         for (int J = 0, j = 0; J < steps; ++J, ++j) {
             const int buf = J % C::kSBuf;
@@ -700,52 +746,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 mbar_arrive(smem_u32(&p_full[buf]));
             }
-        if (j < n - 1) continue;
-        // ---- epilogue: O / l -> bf16, lse -------------------------------------------------
-        // the last P V, and so every earlier one; its barrier has no older phase pending
-        okw = ok;
-        if (okw)
-            okw = mbar_wait(smem_u32(&pv_done[J % C::kSBuf]), (J / C::kSBuf) & 1, abort_flag, a.status, 0x17);
-        okw = __all_sync(0xffffffffu, okw);
-        if (ok) xch[hf * 128 + r] = l;  // the exchange buffer is free: both read it before the last barrier
-        ok = named_bar_and(pair_bar, 64, ok && okw);
-        tc_fence_after();
-        if (ok) {
-            l += xch[(1 - hf) * 128 + r];
-            const int seq = tile[0], seq_start = tile[1], dv0 = tile[4], h = tile[5] + J / n;
-            const int qrow = tile[2] + r;  // query row index within the sequence's rows
-            const bool row_ok = qrow < tile[3];
-            const bool packed = PAGED || a.cu_seqlens;
-            const float inv = l == 0.f ? 0.f : 1.f / l;  // (l is NaN where a score is)
-            uint16_t* orow = a.o + ((size_t)(packed ? seq_start + qrow : seq * a.S + qrow) * a.Hq + h) * a.D + dv0;
-#pragma unroll 1
-            for (int c = hf * (C::kDV / 64); c < (hf + 1) * (C::kDV / 64); ++c) {
-                uint32_t raw[32];
-                tmem_ld32(tO + c * 32 + lane_base, raw);
-                tmem_ld_wait();
-                if (row_ok) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint4 w;
-                        w.x = pack_bf16x2(__uint_as_float(raw[e]) * inv, __uint_as_float(raw[e + 1]) * inv);
-                        w.y = pack_bf16x2(__uint_as_float(raw[e + 2]) * inv, __uint_as_float(raw[e + 3]) * inv);
-                        w.z = pack_bf16x2(__uint_as_float(raw[e + 4]) * inv, __uint_as_float(raw[e + 5]) * inv);
-                        w.w = pack_bf16x2(__uint_as_float(raw[e + 6]) * inv, __uint_as_float(raw[e + 7]) * inv);
-                        *reinterpret_cast<uint4*>(orow + c * 32 + e) = w;
-                    }
-                }
-            }
-            if (row_ok && dv0 == 0 && hf == 0) {
-                const float lse = l == 0.f ? -INFINITY : (m_ref + __log2f(l)) * 0.69314718055994531f;
-                const size_t li = packed ? (size_t)h * a.T + seq_start + qrow : ((size_t)seq * a.Hq + h) * a.S + qrow;
-                a.lse[li] = lse;
+            if (MULTI && j == n - 1) {
+                finish(J);
+                if (!ok || J + 1 == steps) break;
+                named_bar_sync(pair_bar, 64);  // both have read the row sums before the buffer is reused
+                m_ref = -INFINITY, l = 0.f, j = -1;
             }
         }
-        tc_fence_before();
-        if (!ok || J + 1 == steps) break;
-        named_bar_sync(pair_bar, 64);  // both have read the row sums before the buffer is reused
-        m_ref = -INFINITY, l = 0.f, j = -1;
-        }
+        if (!MULTI) finish(n - 1);
     }
     __syncthreads();
     if (PAIR) {  // the even CTA has drained every copy and product of the pair
