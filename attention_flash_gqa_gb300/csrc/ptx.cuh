@@ -261,6 +261,12 @@ __device__ __forceinline__ void bulk_copy_to_peer(uint32_t dst_cluster, uint32_t
         "r"(src), "r"(bytes), "r"(bar_cluster)
         : "memory");
 }
+// 16 bytes of registers to shared memory of any CTA of the cluster, counted by an mbarrier of that CTA (both by cluster addresses).
+__device__ __forceinline__ void store_to_peer(uint32_t dst_cluster, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t bar_cluster) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst_cluster), "r"(a),
+                 "r"(b), "r"(c), "r"(d), "r"(bar_cluster)
+                 : "memory");
+}
 // True in one lane of a converged warp, the same one every time. Unlike a test of the lane number
 // the compiler knows that a single thread passes it.
 __device__ __forceinline__ bool elect_one() {
