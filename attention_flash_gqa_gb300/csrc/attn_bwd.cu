@@ -674,6 +674,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint16_t* __restric
                                                        float* __restrict__ delta, float* __restrict__ dq_acc,
                                                        const int32_t* __restrict__ cu_seqlens, int nseq, int S, int T, int Hq,
                                                        int far_window, long long pairs) {
+    griddep_wait();
     constexpr int kLanes = D >= 256 ? 32 : D / 8, kPairs = 32 / kLanes, N = D / kLanes / 8;
     const int lane = threadIdx.x & 31, part = lane % kLanes;
     const long long warps = ((long long)gridDim.x * blockDim.x) >> 5;
@@ -716,6 +717,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint16_t* __restric
 
 __global__ void __launch_bounds__(256) bwd_finalize_kernel(const float* __restrict__ acc, uint16_t* __restrict__ dq,
                                                            long long n8) {
+    griddep_wait();
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n8; i += (long long)gridDim.x * blockDim.x) {
         const float4 a = reinterpret_cast<const float4*>(acc)[2 * i];
         const float4 b = reinterpret_cast<const float4*>(acc)[2 * i + 1];
@@ -737,10 +739,9 @@ cudaError_t launch_bwd_t(const BwdLaunch& L, cudaStream_t stream) {
         const long long per_block = 8 * (D >= 256 ? 1 : 256 / D) * (apart && L.cu_seqlens ? kLook : 1);
         const unsigned blocks = (unsigned)((pairs + per_block - 1) / per_block);
         const ProfMark m = prof_begin(stream, "bwd_prep");
-        bwd_prep_kernel<D><<<blocks, 256, 0, stream>>>(L.o, L.dO, L.delta, L.dq_acc, L.cu_seqlens, L.nseq, L.S,
-                                                       L.total_rows, L.Hq, apart ? L.window : 0, pairs);
+        const cudaError_t e = launch_behind(bwd_prep_kernel<D>, dim3(blocks), dim3(256), 0, stream, L.o, L.dO, L.delta, L.dq_acc, L.cu_seqlens,
+                                            L.nseq, L.S, L.total_rows, L.Hq, apart ? L.window : 0, pairs);
         prof_end(stream, m);
-        cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     if (apart) {
@@ -791,9 +792,9 @@ cudaError_t launch_bwd_t(const BwdLaunch& L, cudaStream_t stream) {
         const long long n8 = rh * D / 8;
         const unsigned blocks = (unsigned)std::min<long long>((n8 + 255) / 256, 152LL * 16);
         const ProfMark m = prof_begin(stream, "bwd_finalize");
-        bwd_finalize_kernel<<<blocks, 256, 0, stream>>>(L.dq_acc, L.dQ, n8);
+        const cudaError_t e = launch_behind(bwd_finalize_kernel, dim3(blocks), dim3(256), 0, stream, L.dq_acc, L.dQ, n8);
         prof_end(stream, m);
-        return cudaGetLastError();
+        return e;
     }
 }
 

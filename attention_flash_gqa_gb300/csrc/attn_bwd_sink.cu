@@ -60,6 +60,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, FarCfg<D>::kResident) bwd_far_sink_kernel(FarArgs a) {
     using C = FarCfg<D>;
     constexpr int kChunks = D / 8, kMine = D / kWarps / 8;  // chunks of 16 bytes of a row; n-tiles of 8 dims of a warp's quarter
+    griddep_wait();
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int hk = blockIdx.y, seq = blockIdx.z;
@@ -265,6 +266,7 @@ constexpr int kSumThreads = 512;
 
 __global__ void __launch_bounds__(kSumThreads) bwd_sink_sum_kernel(SinkSplit sk, uint16_t* __restrict__ dK, uint16_t* __restrict__ dV,
                                                                    const int32_t* __restrict__ cu, int S, int T, int Hkv, int D, int window) {
+    griddep_wait();
     __shared__ float4 sums[kSumThreads];
     const int j = blockIdx.x >> 1, g = blockIdx.y, seq = blockIdx.z, per = D / 4, group = threadIdx.x / per, d = 4 * (threadIdx.x % per);
     int start = seq * S, L = S;
@@ -305,9 +307,9 @@ cudaError_t launch_far(const BwdLaunch& L, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(bwd_far_sink_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const ProfMark m = prof_begin(stream, "bwd_far_sink");
-    bwd_far_sink_kernel<D><<<dim3(L.sink.slices * L.sink.shares, L.Hkv, L.nseq), kThreads, kSmem, stream>>>(a);
+    e = launch_behind(bwd_far_sink_kernel<D>, dim3(L.sink.slices * L.sink.shares, L.Hkv, L.nseq), dim3(kThreads), kSmem, stream, a);
     prof_end(stream, m);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace
@@ -321,10 +323,10 @@ cudaError_t launch_bwd_far_sinks(const BwdLaunch& L, cudaStream_t stream) {
 
 cudaError_t launch_bwd_sink_sum(const BwdLaunch& L, cudaStream_t stream) {
     const ProfMark m = prof_begin(stream, "bwd_sink_sum");
-    bwd_sink_sum_kernel<<<dim3(2 * L.sink.sink, L.Hkv, L.nseq), kSumThreads, 0, stream>>>(L.sink, L.dK, L.dV, L.cu_seqlens, L.S, L.total_rows, L.Hkv,
-                                                                             L.D, L.window);
+    const cudaError_t e = launch_behind(bwd_sink_sum_kernel, dim3(2 * L.sink.sink, L.Hkv, L.nseq), dim3(kSumThreads), 0, stream, L.sink, L.dK,
+                                        L.dV, L.cu_seqlens, L.S, L.total_rows, L.Hkv, L.D, L.window);
     prof_end(stream, m);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace attn

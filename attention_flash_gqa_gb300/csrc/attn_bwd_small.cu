@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                      const __grid_constant__ CUtensorMap tdq, SmallArgs a) {
     using C = SmallCfg<D, DS>;
+    griddep_wait();
     const int g = blockIdx.x / C::NSL;        // KV head
     const int c0 = (blockIdx.x % C::NSL) * DS;  // this CTA's columns of dV, dK, dQ
     const int seq = blockIdx.y;
@@ -724,9 +725,9 @@ cudaError_t launch_bwd_small_main(const BwdLaunch& L, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const dim3 grid(L.Hkv * (D / DS), L.nseq, L.sink.in_main + (L.S + kB - 1) / kB);
     const ProfMark m = prof_begin(stream, D == 256 ? "bwd_main_d256" : D == 128 ? "bwd_main_d128" : "bwd_main_d64");
-    bwd_small_kernel<D, DS><<<grid, kThreads, kSmem, stream>>>(L.tq, L.tk, L.tv, L.tdo, L.tdq, a);
+    e = launch_behind(bwd_small_kernel<D, DS>, grid, dim3(kThreads), kSmem, stream, L.tq, L.tk, L.tv, L.tdo, L.tdq, a);
     prof_end(stream, m);
-    return cudaGetLastError();
+    return e;
 }
 
 template cudaError_t launch_bwd_small_main<64>(const BwdLaunch&, cudaStream_t);

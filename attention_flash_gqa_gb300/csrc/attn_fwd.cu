@@ -130,6 +130,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                const __grid_constant__ CUtensorMap tv, FwdArgs a) {
     using C = FwdCfg<DQK, PAIR>;
+    // (not in pairs) launched with programmatic serialisation: a short call's start is then hidden by the kernel in front
+    griddep_wait();
     // ---- which tile ------------------------------------------------------------------
     static_assert(!MULTI || (!PAGED && !PAIR), "several heads: single CTAs without pages");
     const int h0 = MULTI ? (int)blockIdx.x * a.heads : (int)blockIdx.x;  // first query head
@@ -235,6 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_sync_all();
     }
     tc_fence_after();
+    // behind the allocation: no block of a later kernel can take tensor memory that this one waits for
+    if (!PAIR) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tbase = *tmem_slot;
     const uint32_t tO = tbase, tS0 = tbase + 512 - C::kSBuf * 128;
     const uint32_t crank = PAIR ? cluster_ctarank() : 0;  // 0: the CTA that issues the pair's MMAs
@@ -808,9 +812,9 @@ cudaError_t launch_fwd_t(const FwdLaunch& L, int heads, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         return cudaGetLastError();
     }
-    fwd_kernel<DQK, PAGED, PAIR, MULTI><<<grid, kThreads, C::kSmem, stream>>>(L.tq, L.tk, L.tv, a);
+    e = launch_behind(fwd_kernel<DQK, PAGED, PAIR, MULTI>, grid, dim3(kThreads), C::kSmem, stream, L.tq, L.tk, L.tv, a);
     prof_end(stream, m);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace

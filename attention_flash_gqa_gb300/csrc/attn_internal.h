@@ -17,6 +17,20 @@ struct ProfMark {
 ProfMark prof_begin(cudaStream_t stream, const char* kernel);
 void prof_end(cudaStream_t stream, ProfMark m);
 
+// A launch with programmatic stream serialisation: the kernel may be placed while the one in front ends, so it has to wait
+// (griddepcontrol.wait, every thread of every block, also of blocks that have nothing to do) before it reads or writes anything of the call's.
+template <class... Params, class... Args>
+cudaError_t launch_behind(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const Args&... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid, cfg.blockDim = block, cfg.dynamicSmemBytes = smem, cfg.stream = stream;
+    cfg.attrs = attr, cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // ---- paged decode -----------------------------------------------------------------------
 // tk / tv: 3-D maps over the caches (D, Hkv, num_pages * 16) with a D x hb x 16 box, no swizzle;
 // used only when the KV heads are split into several blocks (hb < Hkv).
