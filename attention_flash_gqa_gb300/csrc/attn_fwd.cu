@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();
     // ---- which tile ------------------------------------------------------------------
     static_assert(!MULTI || (!PAGED && !PAIR), "several heads: single CTAs without pages");
+    constexpr bool kKeep = MULTI || PAGED;  // (the others have the registers)
     const int h0 = MULTI ? (int)blockIdx.x * a.heads : (int)blockIdx.x;  // first query head
     const int heads = MULTI ? min(a.heads, a.Hq - h0) : 1;
     const int seq = blockIdx.y / a.nsplit, split = blockIdx.y % a.nsplit;
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(vtail), 1);
         mbar_init(smem_u32(q_empty), 1);
         *abort_flag = 0;
-        if (MULTI) {  // what a head's end needs, kept here so that the softmax's registers need not
+        if (kKeep) {  // what a head's end needs, kept here so that the softmax's registers need not
             const int ends[6] = {seq, seq_start, q0, nq, dv0, h0};
             for (int i = 0; i < 6; ++i) tile[i] = ends[i];
         }
@@ -617,10 +618,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (ok) {
                 l += xch[(1 - hf) * 128 + r];
-                const int qrow = (MULTI ? tile[2] : q0) + r;  // query row index within the sequence's rows
-                const bool row_ok = qrow < (MULTI ? tile[3] : nq);
-                const int h = MULTI ? tile[5] + J / n : h0, first = MULTI ? tile[1] : seq_start, sq = MULTI ? tile[0] : seq;
-                const int d0 = MULTI ? tile[4] : dv0;
+                const int qrow = (kKeep ? tile[2] : q0) + r;  // query row index within the sequence's rows
+                const bool row_ok = qrow < (kKeep ? tile[3] : nq);
+                const int h = MULTI ? tile[5] + J / n : h0, first = kKeep ? tile[1] : seq_start, sq = kKeep ? tile[0] : seq;
+                const int d0 = kKeep ? tile[4] : dv0;
                 const bool packed = PAGED || a.cu_seqlens;
                 const float inv = l == 0.f ? 0.f : 1.f / l;  // (l is NaN where a score is)
                 uint16_t* orow = a.o + ((size_t)(packed ? first + qrow : sq * a.S + qrow) * a.Hq + h) * a.D + d0;
