@@ -29,6 +29,9 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = the legacy default stream).
  *    Calls only enqueue work: they return before the GPU finishes and never
  *    synchronise the device.
+ *  - Most kernels, those of the forward and the gradient among them, are launched with programmatic
+ *    stream serialisation: they may be placed while the kernel in front ends, and wait on the
+ *    device for all earlier work of the stream before they use anything of the call's.
  *  - Arguments are checked on the host before anything is launched; on a bad
  *    argument nothing is enqueued and an attn_status code is returned. Nothing
  *    throws across this interface.
