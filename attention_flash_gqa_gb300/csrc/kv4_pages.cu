@@ -76,7 +76,7 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t ends) {
 // Codes of 8 values with the group's scale, that of value i in nibble (kSplit: i / 2 + 4 (i % 2), else i) of the word.
 // x / s is at least 2^-10 from half of an odd number unless it is one (x has 8 bits, s has 5), and x (1 / s) is off by 2^-19 at
 // most: rounded to multiples of 2^-12 first, it ties where x / s does and nowhere else. So, in the pipe of the multiplications
-// alone: (x / s + 9) / 16 cut to 1 from above (7; below -8.25 it does not get), times 16 + 3072, whose last place is 2^-12, and the
+// alone: (x / s + 9) / 16 cut to 1 from above (7; below -8.25 it does not get), times 16 + 1.5 * 2^11, whose last place is 2^-12, and the
 // sum with 1.5 * 2^23 that leaves code + 0x4b400000 as its bits; the upper parts drop out of the word by one subtraction.
 template <bool kSplit>
 __device__ __forceinline__ uint32_t codes_of(uint32_t* w, uint32_t s) {
@@ -93,7 +93,8 @@ __device__ __forceinline__ uint32_t codes_of(uint32_t* w, uint32_t s) {
         const float x = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : mad(w[i / 2], 1u << 16, 0u));
         float y;
         asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(x), "f"(inv), "f"(0.5625f));
-        const float z = __fadd_rn(__fmaf_rn(y, 16.f, 3071.f), 12582912.f - 3072.f);
+        constexpr float kTies = 1.5f * 2048.f;
+        const float z = __fadd_rn(__fmaf_rn(y, 16.f, kTies - 1.f), 12582912.f - kTies);
         word = mad(__float_as_uint(z), 1u << (4 * (kSplit ? i / 2 + 4 * (i & 1) : i)), word);
     }
     return word;

@@ -111,3 +111,41 @@ def test_plan_then_chunk_then_decode():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
     assert attn.attn_get_device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 256, 512])
+def test_captured_with_two_streams(D):
+    """Inputs made on two streams that join in front of the call, and its results used on both."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    src = [torch.randn(1, 500, h, D, generator=g, device="cuda", dtype=torch.bfloat16) for h in (4, 2, 2, 4)]
+    q, k, v, do = (torch.zeros_like(t) for t in src)
+    how = dict(window=70, sink=4)
+
+    def step(side):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            q.copy_(src[0]), do.copy_(src[3])
+        k.copy_(src[1]), v.copy_(src[2])
+        main.wait_stream(side)
+        o, lse = attn.attn_fwd(q, k, v, **how)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            twice = o * 2
+        grads = attn.attn_bwd(q, k, v, o, lse, do, **how)
+        main.wait_stream(side)
+        return [twice, lse, *grads[1:]]
+
+    side = torch.cuda.Stream()
+    want = [t.clone() for t in step(side)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(side)
+    for _ in range(3):
+        for t in (q, k, v, do, *got):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert attn.attn_get_device_status() == 0
