@@ -227,6 +227,14 @@ def test_many_requests(D, B):
     check(*problem(lens, 2, 2, D, 13))
 
 
+@pytest.mark.parametrize("D,G", [(64, 8), (128, 8), (256, 8), (256, 1)])
+def test_most_requests(D, G):
+    """As many as a call takes: with a group of 8 their lengths no longer fit in shared memory beside the rings."""
+    lens = torch.randint(0, 20, (4096,), generator=gen(D + G)).tolist()
+    lens[4095] = 300
+    check(*problem(lens, 1, G, D, 17, 0, 0))
+
+
 @pytest.mark.parametrize("D,Hkv", [(64, 1), (128, 1), (256, 1), (128, 4)])
 def test_one_long_request(D, Hkv):
     """Every block of the GPU has a piece of it."""
