@@ -33,7 +33,7 @@
 //     with TMA bulk reduce-adds. Consumption of the exchanged tiles is signalled back to
 //     their writers with multicast tcgen05.commit arrivals. P is double-buffered (one
 //     buffer per step of a pair-step); dS is single-buffered.
-//     FINE (calls with sinks): dS is formed from P in fp16, times 2^15 (as attn_bwd_small.cu has it for the other head sizes): an S-role CTA's
+//     FINE (calls with sinks): dS is formed from P in fp16, times 2^15: an S-role CTA's
 //     threads store that straight into its partner's P tile, whose elementwise warps leave it there in bf16 for dV. dQ and dK come out
 //     0.0024 off the 64-bit result, relatively, instead of 0.0028, for a tenth of the time (2 x 4096 tokens, window 1000, 4 sinks: 3279 us;
 //     without sinks 2747, 2988 that way, and so the calls without keep theirs).

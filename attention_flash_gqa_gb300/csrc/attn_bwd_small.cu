@@ -35,6 +35,13 @@
 // runs. Each half of the score columns keeps its P^T (bf16 pairs) in the first 32 columns of its
 // own half of R0.
 //
+// P^T for dS stays in registers from one part of a step to the next: at D = 256 in fp32 (dQ and dK 0.0024 off the 64-bit result,
+// relatively), at D <= 128 as the bf16 pairs of dV's product (0.0029). Both have all of fp32's range, so that keys far below their
+// rows' maxima get their gradient too (fp16 would lose bits from P = 2^-29 on and all of them at 2^-39, with its range used to the full).
+// The 64 registers cost what hides the loads of dP^T where the step is short. The whole gradient, fp32 and bf16, us: D = 256, 2 x 8192
+// tokens of 32 heads, window 1024 2946 and 2968, 2 x 4096 causal 2705 and 2720; D = 128, 4 x 4096 of 32 heads 1653 and 1599, one of
+// 16000 with 8 heads, window 700 235 and 229; D = 64, 4 x 4096 1088 and 1073.
+//
 // Sinks: every query of a sequence sees key tile 0 then, where its other keys are seen by the window's queries alone. SinkSplit
 // (attn_internal.h) says how those far queries are shared out: to bwd_far_sink_kernel, or in slices to blocks of this kernel, which are
 // first in the grid so that they do not end last. An edge tile's mask is a word with a bit a query for each 32 of them.
@@ -56,10 +63,6 @@ constexpr int kThreads = 448;
 constexpr int kEw = 256;  // elementwise threads
 constexpr uint32_t kSub = 16384;  // 128 rows x 64 bf16, 128-byte swizzle
 constexpr float kLog2e = 1.4426950408889634f;
-// P is held times 2^15: at most 1, it then fits fp16 with all of its bits down to 2^-29. dS is formed from that (three bits more
-// than from the bf16 P that dV's product takes: dQ and dK 0.0024 off the 64-bit result, relatively, instead of 0.0029); dV, dK and dQ have the factor taken out where they leave tensor memory. (Scores of
-// 2^24 and more, whose logsumexp fp32 holds to whole numbers at best, give P above 1: past 2 it counts as 2 in dS.)
-constexpr float kPUp = 15.f, kPDown = 1.f / 32768.f;
 
 // D: head dim (the contraction of S^T and dP^T); DS: the columns of dV / dK / dQ this CTA owns.
 // DS = D (64, 128): K and V resident, one ring slot per Q or dO tile. DS = 128 < D = 256
@@ -112,6 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                      const __grid_constant__ CUtensorMap tdq, SmallArgs a) {
     using C = SmallCfg<D, DS>;
+    constexpr bool kWide = D == 256;  // P^T for dS in fp32
     griddep_wait();
     const int g = blockIdx.x / C::NSL;        // KV head
     const int c0 = (blockIdx.x % C::NSL) * DS;  // this CTA's columns of dV, dK, dQ
@@ -503,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const int h = g * G + t / n_qt;
             const int q0 = (i_begin + t % n_qt) * kB;
-            const float f = (q0 + j < L) ? a.scale * kPDown : 0.f;  // rows past the sequence end add zeros
+            const float f = (q0 + j < L) ? a.scale : 0.f;  // rows past the sequence end add zeros
             // the whole row into registers first, so dQ's columns are handed back at once (at
             // D = 128 the next dP^T waits for them)
             uint32_t rq[DS];
@@ -560,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int h = g * G + t / n_qt;
             const int qa = (i_begin + t % n_qt) * kB + (tid & 127);
             const size_t lbase = a.cu_seqlens ? (size_t)h * a.T + seq_start : ((size_t)seq * a.Hq + h) * a.S;
-            if (tid < 128) return qa < L ? fmaf(a.lse[lbase + qa], kLog2e, -kPUp) : INFINITY;  // +inf: P = 0 past the end
+            if (tid < 128) return qa < L ? a.lse[lbase + qa] * kLog2e : INFINITY;  // +inf: P = 0 past the end
             return qa < L ? a.delta[lbase + qa] : 0.f;
         };
         float vnext = fetch(0);
@@ -573,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 32 score columns at a time; this half's P columns [64 hf + 16c, +16) overwrite
             // scores of its own first chunk, already read
             ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(s_full), t & 1, abort_flag, a.status, 0x4b));
-            uint32_t ph[32];  // P^T times 2^15 in fp16
+            uint32_t pt[kWide ? 64 : 32];  // P^T for dS: in fp32, or bf16 pairs
             if (ok) {
                 tc_fence_after();
                 const bool edge = !(k0 + kB - 1 <= q0 && (a.window <= 0 || q0 + kB - 1 - k0 < a.window) &&
@@ -601,7 +605,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (decltype(masked)::value && !(see >> (e + u) & 1u)) p[u] = 0.f;
                             }
                             w[e / 2] = pack_bf16x2(p[0], p[1]), w[e / 2 + 1] = pack_bf16x2(p[2], p[3]);
-                            ph[16 * c + e / 2] = pack_f16x2(p[0], p[1]), ph[16 * c + e / 2 + 1] = pack_f16x2(p[2], p[3]);
+                            if constexpr (kWide) {
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) pt[32 * c + e + u] = __float_as_uint(p[u]);
+                            } else {
+                                pt[16 * c + e / 2] = w[e / 2], pt[16 * c + e / 2 + 1] = w[e / 2 + 1];
+                            }
                         }
                     };
                     if (edge) p_chunk(std::true_type{});
@@ -632,8 +641,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int cc = ch * 8 + 2 * e;  // column within the 32-column chunk
-                            const float2 pp = unpack_f16x2(ph[16 * c + cc / 2]);
-                            out[e] = pack_bf16x2(pp.x * (__uint_as_float(rr[cc]) - dv[2 * e]), pp.y * (__uint_as_float(rr[cc + 1]) - dv[2 * e + 1]));
+                            float p0, p1;
+                            if constexpr (kWide) {
+                                p0 = __uint_as_float(pt[32 * c + cc]), p1 = __uint_as_float(pt[32 * c + cc + 1]);
+                            } else {
+                                const uint32_t pw = pt[16 * c + cc / 2];
+                                p0 = __uint_as_float(pw << 16), p1 = __uint_as_float(pw & 0xffff0000u);
+                            }
+                            out[e] = pack_bf16x2(p0 * (__uint_as_float(rr[cc]) - dv[2 * e]), p1 * (__uint_as_float(rr[cc + 1]) - dv[2 * e + 1]));
                         }
                         st_shared_v4(sDS + hf * kSub + sw128_offset(j, 32 * c + 8 * ch), out[0], out[1], out[2], out[3]);
                     }
@@ -661,7 +676,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint16_t* dv_row = a.dV + row * D + c0;
             uint16_t* dk_row = a.dK + row * D + c0;
             const bool part_row = parted && kabs < a.sink.sink;
-            const float kscale = a.scale * kPDown;
             float* part = parted ? a.sink.row(seq, a.cu_seqlens ? seq_start : seq * a.S, far ? 1 + blockIdx.z : 0, g, a.Hkv, j, D) + c0
                                  : nullptr;
 #pragma unroll 1
@@ -675,24 +689,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float* pk = pv + (size_t)a.sink.sink * D;
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        *reinterpret_cast<float4*>(pv + e) = make_float4(__uint_as_float(rv[e]) * kPDown, __uint_as_float(rv[e + 1]) * kPDown,
-                                                                         __uint_as_float(rv[e + 2]) * kPDown, __uint_as_float(rv[e + 3]) * kPDown);
+                        *reinterpret_cast<float4*>(pv + e) = make_float4(__uint_as_float(rv[e]), __uint_as_float(rv[e + 1]),
+                                                                         __uint_as_float(rv[e + 2]), __uint_as_float(rv[e + 3]));
                         *reinterpret_cast<float4*>(pk + e) =
-                            make_float4(__uint_as_float(rk[e]) * kscale, __uint_as_float(rk[e + 1]) * kscale,
-                                        __uint_as_float(rk[e + 2]) * kscale, __uint_as_float(rk[e + 3]) * kscale);
+                            make_float4(__uint_as_float(rk[e]) * a.scale, __uint_as_float(rk[e + 1]) * a.scale,
+                                        __uint_as_float(rk[e + 2]) * a.scale, __uint_as_float(rk[e + 3]) * a.scale);
                     }
                 } else if (key_ok && !far) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint4 wv, wk;
-                        wv.x = pack_bf16x2(__uint_as_float(rv[e]) * kPDown, __uint_as_float(rv[e + 1]) * kPDown);
-                        wv.y = pack_bf16x2(__uint_as_float(rv[e + 2]) * kPDown, __uint_as_float(rv[e + 3]) * kPDown);
-                        wv.z = pack_bf16x2(__uint_as_float(rv[e + 4]) * kPDown, __uint_as_float(rv[e + 5]) * kPDown);
-                        wv.w = pack_bf16x2(__uint_as_float(rv[e + 6]) * kPDown, __uint_as_float(rv[e + 7]) * kPDown);
-                        wk.x = pack_bf16x2(__uint_as_float(rk[e]) * kscale, __uint_as_float(rk[e + 1]) * kscale);
-                        wk.y = pack_bf16x2(__uint_as_float(rk[e + 2]) * kscale, __uint_as_float(rk[e + 3]) * kscale);
-                        wk.z = pack_bf16x2(__uint_as_float(rk[e + 4]) * kscale, __uint_as_float(rk[e + 5]) * kscale);
-                        wk.w = pack_bf16x2(__uint_as_float(rk[e + 6]) * kscale, __uint_as_float(rk[e + 7]) * kscale);
+                        wv.x = pack_bf16x2(__uint_as_float(rv[e]), __uint_as_float(rv[e + 1]));
+                        wv.y = pack_bf16x2(__uint_as_float(rv[e + 2]), __uint_as_float(rv[e + 3]));
+                        wv.z = pack_bf16x2(__uint_as_float(rv[e + 4]), __uint_as_float(rv[e + 5]));
+                        wv.w = pack_bf16x2(__uint_as_float(rv[e + 6]), __uint_as_float(rv[e + 7]));
+                        wk.x = pack_bf16x2(__uint_as_float(rk[e]) * a.scale, __uint_as_float(rk[e + 1]) * a.scale);
+                        wk.y = pack_bf16x2(__uint_as_float(rk[e + 2]) * a.scale, __uint_as_float(rk[e + 3]) * a.scale);
+                        wk.z = pack_bf16x2(__uint_as_float(rk[e + 4]) * a.scale, __uint_as_float(rk[e + 5]) * a.scale);
+                        wk.w = pack_bf16x2(__uint_as_float(rk[e + 6]) * a.scale, __uint_as_float(rk[e + 7]) * a.scale);
                         *reinterpret_cast<uint4*>(dv_row + c4 * 32 + e) = wv;
                         *reinterpret_cast<uint4*>(dk_row + c4 * 32 + e) = wk;
                     }
