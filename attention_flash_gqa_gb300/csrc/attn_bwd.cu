@@ -33,10 +33,6 @@
 //     with TMA bulk reduce-adds. Consumption of the exchanged tiles is signalled back to
 //     their writers with multicast tcgen05.commit arrivals. P is double-buffered (one
 //     buffer per step of a pair-step); dS is single-buffered.
-//     FINE (calls with sinks): dS is formed from P in fp16, times 2^15: an S-role CTA's
-//     threads store that straight into its partner's P tile, whose elementwise warps leave it there in bf16 for dV. dQ and dK come out
-//     0.0024 off the 64-bit result, relatively, instead of 0.0028, for a tenth of the time (2 x 4096 tokens, window 1000, 4 sinks: 3279 us;
-//     without sinks 2747, 2988 that way, and so the calls without keep theirs).
 //     Tensor memory (512 columns): [0,128) dV_c, [128,256) dK_c, [256,384) dQ_c,
 //     [384,512) the role result of a pair-step.
 //  3. bwd_finalize: dQ accumulator -> bf16.
@@ -58,7 +54,6 @@ constexpr uint32_t kSub = 16384;    // 128 rows x 128 bytes, 128-byte swizzle
 constexpr uint32_t kSmemMax = 232448;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPUp = 15.f, kPDown = 1.f / 32768.f;  // (FINE) P is held times 2^15: at most that in fp16, and all of its bits down to 2^-29
 
 // Configuration of the cluster kernel (D = 512: four CTAs, two per role).
 template <int D>
@@ -92,7 +87,7 @@ struct BwdArgs {
     SinkSplit sink;
 };
 
-template <int D, bool FINE>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_main_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -343,16 +338,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!mbar_wait(smem_u32(&p_full[pb]), (t >> 1) & 1, abort_flag, a.status, 0x23)) return false;
                 tc_fence_after();
                 mbar_expect_tx(smem_u32(&p_full[pb]), p_rem);  // arm the buffer's next use
-                // (FINE: a dP-role CTA's elementwise warps leave their rows of P in bf16 first)
-                if (FINE && !s_role) {
-                    if (!mbar_wait(smem_u32(&p_read[pb]), (t >> 1) & 1, abort_flag, a.status, 0x34)) return false;
-                    tc_fence_after();
-                }
                 if (!grad_pair(tDV, sP + pb * 2 * kSub, t > 0)) return false;  // dV_c += P^T dO_c
                 // an S-role CTA is done with P(t) here; a dP-role CTA also reads it in its
                 // elementwise warps (to form dS(t)), so it releases the buffer once they have
                 // (released after the dS products instead, the kernel measured 0.6 % slower)
-                if (!FINE && !s_role && !mbar_wait(smem_u32(&p_read[pb]), (t >> 1) & 1, abort_flag, a.status, 0x34)) return false;
+                if (!s_role && !mbar_wait(smem_u32(&p_read[pb]), (t >> 1) & 1, abort_flag, a.status, 0x34)) return false;
                 umma_commit_multicast(smem_u32(&p_free[pb]), mask_s);
                 if (!mbar_wait(smem_u32(ds_full), t & 1, abort_flag, a.status, 0x24)) return false;
                 tc_fence_after();
@@ -431,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
 
         // this thread's row of the share -> the step's tile, then the warp's 32 rows to every peer
-        auto send = [&](const uint32_t (&pk)[64], uint32_t dst, uint32_t fbar, uint32_t but) {
+        auto send = [&](const uint32_t (&pk)[64], uint32_t dst, uint32_t fbar) {
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
@@ -443,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 const uint32_t row0 = (uint32_t)(share * C::NQ + (quad & 1) * 32) * 128;  // the warp's 32 rows
                 for (uint32_t peer = 0; peer < (uint32_t)C::NC; ++peer) {
-                    if (peer == rank || peer == but) continue;
+                    if (peer == rank) continue;
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
                         const uint32_t rows = dst + hh * kSub + row0;
@@ -468,11 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (real) {
                 const int h = head_of(t);
                 const size_t li = (a.cu_seqlens ? (size_t)h * a.T + seq_start : ((size_t)seq * a.Hq + h) * a.S) + qa;
-                v = qa < L ? (s_role ? fmaf(a.lse[li], kLog2e, FINE ? -kPUp : 0.f) : a.delta[li]) : (s_role ? INFINITY : 0.f);
+                v = qa < L ? (s_role ? a.lse[li] * kLog2e : a.delta[li]) : (s_role ? INFINITY : 0.f);
             }
             ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(r_full), T & 1, abort_flag, a.status, 0x2a));
             uint32_t pk[64];  // this row of P or dS over the 128 keys, bf16 pairs
-            uint32_t ph[64];  // (FINE, S role) this row of P times 2^15, fp16 pairs: for the CTA that forms dS of it
             if (ok) {
                 tc_fence_after();
                 if (s_role) {
@@ -502,7 +491,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (!(see[c >> 5] >> ((c + 1) & 31) & 1u)) p1 = 0.f;
                             }
                             pk[c / 2] = pack_bf16x2(p0, p1);
-                            if (FINE) ph[c / 2] = pack_f16x2(p0, p1);
                         }
                     };
                     if (edge) p_row(std::true_type{});
@@ -510,17 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // buffer t & 1 was last read at step t - 2
                     if (real && t >= 2)
                         ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&p_free[half]), ((t >> 1) - 1) & 1, abort_flag, a.status, 0x2b));
-                    if (real && ok) {
-                        const uint32_t dst = sP + half * 2 * kSub, peer = share + C::NHALF;  // the dP-role CTA of this share
-                        if (FINE) {
-                            const uint32_t there = mapa_shared(dst, peer), bar = mapa_shared(smem_u32(&p_full[half]), peer);
-#pragma unroll
-                            for (int x = 0; x < 16; ++x)
-                                store_to_peer(there + (x >> 3) * kSub + sw128_offset(trow, (x & 7) * 8), ph[4 * x], ph[4 * x + 1], ph[4 * x + 2],
-                                              ph[4 * x + 3], bar);
-                        }
-                        send(pk, dst, smem_u32(&p_full[half]), FINE ? peer : rank);
-                    }
+                    if (real && ok) send(pk, sP + half * 2 * kSub, smem_u32(&p_full[half]));
                 } else {
                     // dS = P (dP - Delta), P from the S-role partner's rows. The role result is read
                     // out and handed back first, so the next pair-step's products need not wait for P.
@@ -534,43 +512,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (real) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&p_full[half]), (t >> 1) & 1, abort_flag, a.status, 0x2c));
                     if (real && ok) {
                         const uint32_t ptile = sP + half * 2 * kSub;
-                        const float v_down = -v * kPDown;
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
                             for (int ch = 0; ch < 8; ++ch) {
                                 uint32_t pw[4];
-                                const uint32_t at = ptile + hh * kSub + sw128_offset(trow, ch * 8);
-                                ld_shared_v4(at, pw[0], pw[1], pw[2], pw[3]);
+                                ld_shared_v4(ptile + hh * kSub + sw128_offset(trow, ch * 8), pw[0], pw[1], pw[2], pw[3]);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     const int c = hh * 64 + ch * 8 + 2 * e;
-                                    if (FINE) {
-                                        const float2 p = unpack_f16x2(pw[e]);
-                                        pk[c / 2] = pack_bf16x2(p.x * fmaf(__uint_as_float(rr[c]), kPDown, v_down),
-                                                                p.y * fmaf(__uint_as_float(rr[c + 1]), kPDown, v_down));
-                                        pw[e] = pack_bf16x2(p.x, p.y);
-                                    } else {
-                                        pk[c / 2] = pack_bf16x2(__uint_as_float(pw[e] << 16) * (__uint_as_float(rr[c]) - v),
-                                                                __uint_as_float(pw[e] & 0xffff0000u) * (__uint_as_float(rr[c + 1]) - v));
-                                    }
+                                    pk[c / 2] = pack_bf16x2(__uint_as_float(pw[e] << 16) * (__uint_as_float(rr[c]) - v),
+                                                            __uint_as_float(pw[e] & 0xffff0000u) * (__uint_as_float(rr[c + 1]) - v));
                                 }
-                                if (FINE) st_shared_v4(at, pw[0], pw[1], pw[2], pw[3]);
                             }
-                        if (FINE) fence_proxy_async_smem();
                         mbar_arrive(smem_u32(&p_read[half]));  // this row of P(t) has been read
                     }
                     // the first step's dS: its buffer was last read at step 2T - 1
                     if (half == 0 && real) {
                         if (t > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(ds_free), (t - 1) & 1, abort_flag, a.status, 0x2f));
-                        if (ok) send(pk, sDS, smem_u32(ds_full), rank);
+                        if (ok) send(pk, sDS, smem_u32(ds_full));
                     }
                 }
             }
             if (T > 0) ok = drain_dq(2 * T - 1) && ok;
             if (!s_role && half == 1 && real) {  // the second step's dS, once dK / dQ of the first have read the buffer
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(ds_free), (t - 1) & 1, abort_flag, a.status, 0x2f));
-                if (ok) send(pk, sDS, smem_u32(ds_full), rank);
+                if (ok) send(pk, sDS, smem_u32(ds_full));
             }
             ok = drain_dq(2 * T) && ok;
             ok = named_bar_and(3, 128, ok);
@@ -596,7 +563,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint16_t* dv_row = a.dV + row * D + c0;
             uint16_t* dk_row = a.dK + row * D + c0;
             const bool part_row = parted && kabs < a.sink.sink;
-            const float vscale = FINE ? kPDown : 1.f;
             float* part = parted ? a.sink.row(seq, a.cu_seqlens ? seq_start : seq * a.S, far ? 1 + blockIdx.z : 0, g, a.Hkv, j, D) + c0
                                  : nullptr;
 #pragma unroll 1
@@ -610,8 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float* pk = pv + (size_t)a.sink.sink * D;
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        *reinterpret_cast<float4*>(pv + e) = make_float4(__uint_as_float(rv[e]) * vscale, __uint_as_float(rv[e + 1]) * vscale,
-                                                                         __uint_as_float(rv[e + 2]) * vscale, __uint_as_float(rv[e + 3]) * vscale);
+                        *reinterpret_cast<float4*>(pv + e) = make_float4(__uint_as_float(rv[e]), __uint_as_float(rv[e + 1]),
+                                                                         __uint_as_float(rv[e + 2]), __uint_as_float(rv[e + 3]));
                         *reinterpret_cast<float4*>(pk + e) =
                             make_float4(__uint_as_float(rk[e]) * a.scale, __uint_as_float(rk[e + 1]) * a.scale,
                                         __uint_as_float(rk[e + 2]) * a.scale, __uint_as_float(rk[e + 3]) * a.scale);
@@ -620,10 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint4 wv, wk;
-                        wv.x = pack_bf16x2(__uint_as_float(rv[e]) * vscale, __uint_as_float(rv[e + 1]) * vscale);
-                        wv.y = pack_bf16x2(__uint_as_float(rv[e + 2]) * vscale, __uint_as_float(rv[e + 3]) * vscale);
-                        wv.z = pack_bf16x2(__uint_as_float(rv[e + 4]) * vscale, __uint_as_float(rv[e + 5]) * vscale);
-                        wv.w = pack_bf16x2(__uint_as_float(rv[e + 6]) * vscale, __uint_as_float(rv[e + 7]) * vscale);
+                        wv.x = pack_bf16x2(__uint_as_float(rv[e]), __uint_as_float(rv[e + 1]));
+                        wv.y = pack_bf16x2(__uint_as_float(rv[e + 2]), __uint_as_float(rv[e + 3]));
+                        wv.z = pack_bf16x2(__uint_as_float(rv[e + 4]), __uint_as_float(rv[e + 5]));
+                        wv.w = pack_bf16x2(__uint_as_float(rv[e + 6]), __uint_as_float(rv[e + 7]));
                         wk.x = pack_bf16x2(__uint_as_float(rk[e]) * a.scale, __uint_as_float(rk[e + 1]) * a.scale);
                         wk.y = pack_bf16x2(__uint_as_float(rk[e + 2]) * a.scale, __uint_as_float(rk[e + 3]) * a.scale);
                         wk.z = pack_bf16x2(__uint_as_float(rk[e + 4]) * a.scale, __uint_as_float(rk[e + 5]) * a.scale);
@@ -761,8 +727,7 @@ cudaError_t launch_bwd_t(const BwdLaunch& L, cudaStream_t stream) {
         a.scale_log2 = L.scale * kLog2e;
         a.sink = L.sink;
         constexpr uint32_t kSmem = Cfg<D>::kSmem;
-        const auto kern = L.sink.sink > 0 ? bwd_main_kernel<D, true> : bwd_main_kernel<D, false>;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        cudaError_t e = cudaFuncSetAttribute(bwd_main_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
         if (e != cudaSuccess) return e;
         constexpr int NC = Cfg<D>::NC;
         cudaLaunchConfig_t cfg = {};
@@ -778,7 +743,7 @@ cudaError_t launch_bwd_t(const BwdLaunch& L, cudaStream_t stream) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         const ProfMark m = prof_begin(stream, D == 256 ? "bwd_main_d256" : "bwd_main_d512");
-        e = cudaLaunchKernelEx(&cfg, kern, L.tq, L.tk, L.tv, L.tdo, L.tqh, L.tdoh, L.tdq, a);
+        e = cudaLaunchKernelEx(&cfg, bwd_main_kernel<D>, L.tq, L.tk, L.tv, L.tdo, L.tqh, L.tdoh, L.tdq, a);
         prof_end(stream, m);
         if (e != cudaSuccess) return e;
         e = cudaGetLastError();

@@ -10,7 +10,6 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 namespace attn {
 
@@ -260,12 +259,6 @@ __device__ __forceinline__ void bulk_copy_to_peer(uint32_t dst_cluster, uint32_t
             dst_cluster),
         "r"(src), "r"(bytes), "r"(bar_cluster)
         : "memory");
-}
-// 16 bytes of registers to shared memory of any CTA of the cluster, counted by an mbarrier of that CTA (both by cluster addresses).
-__device__ __forceinline__ void store_to_peer(uint32_t dst_cluster, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t bar_cluster) {
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst_cluster), "r"(a),
-                 "r"(b), "r"(c), "r"(d), "r"(bar_cluster)
-                 : "memory");
 }
 // True in one lane of a converged warp, the same one every time. Unlike a test of the lane number
 // the compiler knows that a single thread passes it.
@@ -532,14 +525,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
 }
-
-// Two values in fp16, those past its range as its largest.
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-__device__ __forceinline__ float2 unpack_f16x2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
 // d += a b on one warp: a 16 x 16 (row-major), b 16 x 8 (column-major), bf16 in, fp32 out.
 // Fragments: g = lane / 4, c = lane % 4; a = {(g, 2c..2c+1), (g+8, 2c..), (g, 2c+8..), (g+8, 2c+8..)},

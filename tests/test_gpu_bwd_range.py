@@ -9,7 +9,7 @@ import sink_ref as ref
 from operator_ref import close
 
 pytestmark = pytest.mark.gpu
-SHAPES = [(64, 3, 1), (128, 4, 2), (256, 2, 1)]
+SHAPES = [(64, 3, 1), (128, 4, 2), (256, 2, 1), (512, 2, 1), (512, 3, 1)]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -52,7 +52,7 @@ def test_keys_of_small_probability(D, Hq, Hkv, window, sink):
     tiny = (0, 2.0 ** -126 * least.sum(1).transpose(0, 1), 2.0 ** -126 * (see.T @ (1 + ad)).sum(1).transpose(0, 1))
     for i, name in enumerate(("dq", "dk", "dv")):
         close(name, got[i].flatten(0, 1), want[2 * i], want[2 * i + 1] + tiny[i])
-    # the bounds tell enough of these gradients from zero
+    # the bounds tell enough of these gradients from zero (one of 14 at least: over 512 dims the error of Delta takes up most of them)
     assert all((want[2 * i][1::2].abs() > want[2 * i + 1][1::2]).float().mean() > 0.05 for i in (1, 2))
 
 
