@@ -213,40 +213,46 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
 
-_ws_cache: dict = {}
-
-
-def _workspace(nbytes: int, device, zero: bool, key: str):
-    """Reusable workspace per (device, purpose); grown when too small (allocation is torch's)."""
+def _on(stream, device):
+    """Context of a call: what is allocated in it belongs to the stream that the call's kernels run on, and the library works on
+    the current device."""
     import torch
 
-    k = (str(device), key)
-    buf = _ws_cache.get(k)
-    if buf is None or buf.numel() < nbytes:
-        buf = (torch.zeros if zero else torch.empty)(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _ws_cache[k] = buf
-    return buf
+    if stream is None:
+        return torch.cuda.device(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    if stream.device != device:
+        raise ValueError("stream is on another device than the tensors")
+    return torch.cuda.stream(stream)
+
+
+def _scratch(nbytes: int, device):
+    """A workspace of one call's own (another stream or thread may be using the last one, and a graph keeps its own)."""
+    import torch
+
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def attn_fwd(q, k, v, o=None, lse=None, *, causal: bool = True, window: int = 0, scale: float | None = None,
              stream=None, sink: int = 0):
     """Forward of causal (optionally sliding-window) GQA attention, dense [B, S, H, D] layout. With a window the
     sequence's first ``sink`` keys (0 to 128) stay visible to every later query."""
-    if sink:
-        scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
-        return (_bound or _native()).fwd_sink(q, k, v, None, 0, o, lse, causal, window, sink, scale, stream)
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    if ops := _bound or _native_for(sink):
+        return ops.fwd_sink(q, k, v, None, 0, o, lse, causal, int(window), sink or 0, scale, stream)
     import torch
 
     B, S, Hq, D = q.shape
     Hkv = k.shape[2]
-    scale = float(scale if scale is not None else 1.0 / math.sqrt(D))
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
-    with torch.cuda.device(q.device):  # the library works on the current device
+    with _on(stream, q.device):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, Hq, S), dtype=torch.float32, device=q.device)
         rc = load_library().attn_fwd(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse), B, Hq, Hkv,
-                                     S, D, scale, int(causal), int(window), None, 0, _stream_ptr(stream, q.device))
+                                     S, D, float(scale), int(causal), int(window), None, 0, _stream_ptr(stream, q.device))
     _check(rc, "attn_fwd")
     return o, lse
 
@@ -255,24 +261,24 @@ def attn_fwd_varlen(q, k, v, cu_seqlens, max_seqlen: int, o=None, lse=None, *, c
                     scale: float | None = None, stream=None, sink: int = 0):
     """Forward over packed sequences: q [T, Hq, D], k/v [T, Hkv, D], cu_seqlens int32 [n+1] on the device; ``sink`` as in
     attn_fwd, for each sequence."""
-    if sink:
-        scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
-        return (_bound or _native()).fwd_sink(q, k, v, cu_seqlens, max_seqlen, o, lse, causal, window, sink, scale, stream)
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    if ops := _bound or _native_for(sink):
+        return ops.fwd_sink(q, k, v, cu_seqlens, int(max_seqlen), o, lse, causal, int(window), sink or 0, scale, stream)
     import torch
 
     T, Hq, D = q.shape
     Hkv = k.shape[1]
-    scale = float(scale if scale is not None else 1.0 / math.sqrt(D))
     if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda:
         raise ValueError("cu_seqlens must be an int32 CUDA tensor")
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-    with torch.cuda.device(q.device):  # the library works on the current device
+    with _on(stream, q.device):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
         rc = load_library().attn_fwd_varlen(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse),
                                             _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, int(max_seqlen), Hq, Hkv, D,
-                                            scale, int(causal), int(window), None, 0, _stream_ptr(stream, q.device))
+                                            float(scale), int(causal), int(window), None, 0, _stream_ptr(stream, q.device))
     _check(rc, "attn_fwd_varlen")
     return o, lse
 
@@ -290,11 +296,11 @@ def attn_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, max_q_len: 
     for t, n in ((block_table, "block_table"), (seq_lens, "seq_lens"), (cu_q, "cu_q")):
         if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{n} must be a contiguous int32 CUDA tensor")
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-    with torch.cuda.device(q.device):  # the library works on the current device
+    with _on(stream if o is None or lse is None else None, q.device):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
         rc = load_library().attn_fwd_paged_sink(
             _bf16(q, "q"), _bf16(k_cache, "k_cache"), _bf16(v_cache, "v_cache"), _ptr(block_table), _ptr(seq_lens),
             _ptr(cu_q), _bf16(o, "o"), _ptr(lse), cu_q.numel() - 1, T, int(max_q_len), Hq, Hkv, D, page_size,
@@ -319,11 +325,11 @@ def attn_merge_lse(o_parts, lse_parts, o=None, lse=None, *, stream=None):
         raise ValueError("lse_parts must be a contiguous float32 CUDA tensor")
     if tuple(lse_parts.shape) != ((P, H, S) if packed else (P, B, H, S)):
         raise ValueError("lse_parts shape does not match o_parts")
-    if o is None:
-        o = torch.empty(o_parts.shape[1:], dtype=torch.bfloat16, device=o_parts.device)
-    if lse is None:
-        lse = torch.empty(lse_parts.shape[1:], dtype=torch.float32, device=o_parts.device)
-    with torch.cuda.device(o_parts.device):  # the library works on the current device
+    with _on(stream if o is None or lse is None else None, o_parts.device):
+        if o is None:
+            o = torch.empty(o_parts.shape[1:], dtype=torch.bfloat16, device=o_parts.device)
+        if lse is None:
+            lse = torch.empty(lse_parts.shape[1:], dtype=torch.float32, device=o_parts.device)
         rc = load_library().attn_merge_lse(_bf16(o_parts, "o_parts"), _ptr(lse_parts), _bf16(o, "o"), _ptr(lse), P, B,
                                            S, H, D, _stream_ptr(stream, o_parts.device))
     _check(rc, "attn_merge_lse")
@@ -333,10 +339,10 @@ def attn_merge_lse(o_parts, lse_parts, o=None, lse=None, *, stream=None):
 def attn_bwd(q, k, v, o, lse, dO, dq=None, dk=None, dv=None, *, causal: bool = True, window: int = 0,
              scale: float | None = None, cu_seqlens=None, max_seqlen: int = 0, workspace=None, stream=None, sink: int = 0):
     """Gradients (dQ, dK, dV). Dense [B,S,H,D] when cu_seqlens is None, else packed [T,H,D]; ``sink`` as in the forward."""
-    if sink:
-        scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
-        return (_bound or _native()).bwd_sink(q, k, v, o, lse, dO, dq, dk, dv, causal, window, sink, scale, cu_seqlens, max_seqlen, workspace,
-                                            stream)
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    if ops := _bound or _native_for(sink):
+        return ops.bwd_sink(q, k, v, o, lse, dO, dq, dk, dv, causal, int(window), sink or 0, scale, cu_seqlens, int(max_seqlen), workspace, stream)
     import torch
 
     if cu_seqlens is None:
@@ -347,17 +353,16 @@ def attn_bwd(q, k, v, o, lse, dO, dq=None, dk=None, dv=None, *, causal: bool = T
         B, (S, Hq, D) = 1, q.shape
         Hkv = k.shape[1]
         nseq = cu_seqlens.numel() - 1
-    scale = float(scale if scale is not None else 1.0 / math.sqrt(D))
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    need = attn_workspace_size(ATTN_OP_BWD if cu_seqlens is None else ATTN_OP_BWD_VARLEN, B, Hq, Hkv, S, D, nseq)
-    if workspace is None:
-        workspace = _workspace(need, q.device, False, "bwd")
-    with torch.cuda.device(q.device):  # the library works on the current device
+    with _on(stream, q.device):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        need = attn_workspace_size(ATTN_OP_BWD if cu_seqlens is None else ATTN_OP_BWD_VARLEN, B, Hq, Hkv, S, D, nseq)
+        if workspace is None:
+            workspace = _scratch(need, q.device)
         rc = load_library().attn_bwd(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v"), _bf16(o, "o"), _ptr(lse),
                                      _bf16(dO, "dO"), _bf16(dq, "dQ"), _bf16(dk, "dK"), _bf16(dv, "dV"), B, Hq, Hkv, S, D,
-                                     scale, int(causal), int(window), _ptr(cu_seqlens), nseq, int(max_seqlen),
+                                     float(scale), int(causal), int(window), _ptr(cu_seqlens), nseq, int(max_seqlen),
                                      _ptr(workspace), workspace.numel() * workspace.element_size(),
                                      _stream_ptr(stream, q.device))
     _check(rc, "attn_bwd")
@@ -368,28 +373,28 @@ def attn_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=No
                       window: int = 0, workspace=None, stream=None, sink: int = 0):
     """Single-token decode: q [B,Hq,D], caches [pages,16,Hkv,D], block_table int32 [B,max_pages], seq_lens int32 [B];
     window > 0: the query sees only the last `window` keys, and the request's first `sink` ones (0 to 128)."""
-    if sink:
-        scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
-        return (_bound or _native()).decode_paged_sink(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale, window, sink, workspace, stream)
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    if ops := _bound or _native_for(sink):
+        return ops.decode_paged_sink(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale, int(window), sink or 0, workspace, stream)
     import torch
 
     B, Hq, D = q.shape
     num_pages, page_size, Hkv, _ = k_cache.shape
-    scale = float(scale if scale is not None else 1.0 / math.sqrt(D))
     for t, n in ((block_table, "block_table"), (seq_lens, "seq_lens")):
         if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{n} must be a contiguous int32 CUDA tensor")
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    need = attn_workspace_size(ATTN_OP_DECODE_PAGED, B, Hq, Hkv, 0, D)
-    if workspace is None:
-        workspace = _workspace(need, q.device, False, "decode")
-    with torch.cuda.device(q.device):  # the library works on the current device
+    with _on(stream, q.device):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        need = attn_workspace_size(ATTN_OP_DECODE_PAGED, B, Hq, Hkv, 0, D)
+        if workspace is None:
+            workspace = _scratch(need, q.device)
         rc = load_library().attn_decode_paged(_bf16(q, "q"), _bf16(k_cache, "k_cache"), _bf16(v_cache, "v_cache"),
                                               _ptr(block_table), _ptr(seq_lens), _bf16(o, "o"), _ptr(lse), B, Hq, Hkv, D,
-                                              page_size, block_table.shape[1], num_pages, scale, int(window),
+                                              page_size, block_table.shape[1], num_pages, float(scale), int(window),
                                               _ptr(workspace),
                                               workspace.numel() * workspace.element_size(), _stream_ptr(stream, q.device))
     _check(rc, "attn_decode_paged")
@@ -436,9 +441,12 @@ class PagedPlan(NamedTuple):
 _bound = None
 
 
+_unbound = False  # _native() has failed
+
+
 def _native():
-    """The native part of the binding (csrc/py_ops.cpp): the calls below are short on the GPU, so their argument
-    checks, output allocation and C call are one function of it each. Outputs and workspaces that are not given
+    """The native part of the binding (csrc/py_ops.cpp): many calls are short on the GPU, so the argument
+    checks, output allocation and C call of each are one function of it. Outputs and workspaces that are not given
     belong to the stream of the call (or to the graph being captured): calls on different streams, or in
     different graphs, never share them."""
     global _bound
@@ -460,6 +468,19 @@ def _native():
         ops.load(_LIB_PATH, AttnError, PagedPlan)
         _bound = ops
     return _bound
+
+
+def _native_for(sink):
+    """_native(), or None where it is missing and a call without sinks goes to the C library from here."""
+    global _unbound
+    if sink:
+        return _native()
+    if not _unbound:
+        try:
+            return _native()
+        except RuntimeError:
+            _unbound = True
+    return None
 
 
 def attn_paged_plan(kv_lens, new_lens, free_pages, block_table, pages_held, free_used, total_new: int, *, num_pages: int,

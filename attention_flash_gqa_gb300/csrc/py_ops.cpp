@@ -77,6 +77,16 @@ attn_bf16* bf16(const at::Tensor& t, at::IntArrayRef shape, int idx, const char*
     return checked<attn_bf16>(t, at::kBFloat16, shape, idx, name);
 }
 
+// A contiguous tensor of that type on GPU idx, whatever its shape, that holds `count` values or more (a buffer of a larger batch).
+template <class T>
+T* holding(const at::Tensor& t, at::ScalarType type, int64_t count, int idx, const char* name) {
+    if (t.scalar_type() == type && t.is_cuda() && t.get_device() == idx && t.numel() >= count && t.is_contiguous())
+        return static_cast<T*>(t.data_ptr());
+    PyErr_Format(PyExc_ValueError, "%s must be a contiguous %s tensor of %lld values on cuda:%d", name,
+                 type == at::kInt ? "int32" : type == at::kFloat ? "float32" : "bfloat16", (long long)count, idx);
+    throw Raised();
+}
+
 int as_int(PyObject* o, const char* name) {
     const long long v = PyLong_AsLongLong(o);
     if (v == -1 && PyErr_Occurred()) throw Raised();
@@ -94,7 +104,7 @@ bool as_bool(PyObject* o) {
     return v != 0;
 }
 
-// The device and stream that the call runs on, current for its duration: a torch stream object, or None.
+// The device and stream that the call runs on, current for its duration: a torch stream object, another with its `cuda_stream`, or None.
 struct Place {
     c10::cuda::OptionalCUDAGuard device;
     std::optional<c10::cuda::CUDAStreamGuard> guard;
@@ -104,6 +114,17 @@ struct Place {
         if (o == Py_None) {
             device.set_index((c10::DeviceIndex)idx);
             stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)idx).stream();
+            return;
+        }
+        if (!PyObject_HasAttrString(o, "stream_id")) {
+            PyObject* x = PyObject_GetAttrString(o, "cuda_stream");
+            if (!x) throw Raised();
+            void* at = PyLong_AsVoidPtr(x);
+            Py_DECREF(x);
+            if (!at && PyErr_Occurred()) throw Raised();
+            const auto s = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(at), (c10::DeviceIndex)idx);
+            guard.emplace(s);
+            stream = s.stream();
             return;
         }
         long long v[3];
@@ -488,14 +509,22 @@ PyObject* tree_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// ---- windows with sinks ------------------------------------------------------------------------
+// ---- prefill, gradient and decode, with sinks or without ------------------------------------------
+// A bf16 result: made with that shape, or a given buffer that holds as many values.
+attn_bf16* room_for(Result& r, PyObject* given, at::IntArrayRef shape, int64_t count, const Place& place, const char* name) {
+    r.given = given;
+    if (given != Py_None) return holding<attn_bf16>(tensor(given, name), at::kBFloat16, count, place.idx, name);
+    r.made = place.make(shape, at::kBFloat16);
+    return static_cast<attn_bf16*>(r.made.data_ptr());
+}
+
 // q, k, v of a prompt, dense [B, S, H, D] (cu_seqlens None) or packed [T, H, D].
 struct Prompt {
     const at::Tensor &q, &k;
     int idx, B = 1, S, Hq, Hkv, D, nseq = 0, top = 0;
     attn_bf16 *qp, *kp, *vp;
     const int32_t* cu = nullptr;
-    Prompt(PyObject* q_, PyObject* k_, PyObject* v_, PyObject* cu_, PyObject* top_)
+    Prompt(PyObject* q_, PyObject* k_, PyObject* cu_, PyObject* top_)
         : q(tensor(q_, "q")), k(tensor(k_, "k")), idx(index_of(q, "q")) {
         const bool packed = cu_ != Py_None;
         const auto sq = q.sizes(), sk = k.sizes();
@@ -507,35 +536,46 @@ struct Prompt {
         if (sk[n - 2] > INT32_MAX) refuse("%s is too large", "k");
         if (!packed) B = (int)sq[0];
         S = (int)sq[n - 3], Hq = (int)sq[n - 2], Hkv = (int)sk[n - 2], D = (int)sq[n - 1];
-        qp = bf16(q, sq, idx, "q"), kp = bf16(k, sk, idx, "k"), vp = bf16(tensor(v_, "v"), sk, idx, "v");
         if (packed) {
-            const int64_t m = tensor(cu_, "cu_seqlens").numel(), sc[1] = {m};
+            const at::Tensor& c = tensor(cu_, "cu_seqlens");
+            const int64_t m = c.numel();
             if (m < 1 || m > INT32_MAX) refuse("%s must have an entry more than there are sequences", "cu_seqlens");
-            cu = i32(cu_, sc, idx, "cu_seqlens"), nseq = (int)m - 1, top = as_int(top_, "max_seqlen");
+            cu = holding<int32_t>(c, at::kInt, m, idx, "cu_seqlens"), nseq = (int)m - 1, top = as_int(top_, "max_seqlen");
         }
+    }
+    // q, k, v checked (behind the results, whose making may raise torch's out of memory first).
+    void inputs(PyObject* v_) {
+        qp = bf16(q, q.sizes(), idx, "q"), kp = bf16(k, k.sizes(), idx, "k"), vp = bf16(tensor(v_, "v"), k.sizes(), idx, "v");
+    }
+    // A result as large as x: made with its shape, or a given buffer that holds it.
+    attn_bf16* result(Result& r, PyObject* given, const at::Tensor& x, const Place& place, const char* name) const {
+        return room_for(r, given, x.sizes(), x.numel(), place, name);
     }
     // lse [B, Hq, S], or [Hq, T]
     float* lse(PyObject* given, Result* r, const Place* place) const {
-        const int64_t dense[3] = {B, Hq, S};
-        const at::IntArrayRef shape = cu ? at::IntArrayRef(dense + 1, 2) : at::IntArrayRef(dense, 3);
+        const int64_t dense[3] = {B, Hq, S}, n = (int64_t)B * Hq * S;
         if (r) {
             r->given = given;
-            if (given == Py_None) r->made = place->make(shape, at::kFloat);
+            if (given == Py_None) {
+                r->made = place->make(cu ? at::IntArrayRef(dense + 1, 2) : at::IntArrayRef(dense, 3), at::kFloat);
+                return static_cast<float*>(r->made.data_ptr());
+            }
         }
-        return checked<float>(given == Py_None && r ? r->made : tensor(given, "lse"), at::kFloat, shape, idx, "lse");
+        return holding<float>(tensor(given, "lse"), at::kFloat, n, idx, "lse");
     }
 };
 
 // (q, k, v, cu_seqlens, max_seqlen, o, lse, causal, window, sink, scale, stream)
 PyObject* fwd_sink(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 12, [&]() -> PyObject* {
-        const Prompt x(a[0], a[1], a[2], a[3], a[4]);
+        Prompt x(a[0], a[1], a[3], a[4]);
         const int causal = as_bool(a[7]), window = as_int(a[8], "window"), sink = as_int(a[9], "sink");
         const float scale = as_float(a[10]);
         Place place(a[11], x.idx);
         Result r[2];
-        attn_bf16* o = like(r[0], a[5], x.q, place, "o");
+        attn_bf16* o = x.result(r[0], a[5], x.q, place, "o");
         float* lse = x.lse(a[6], &r[1], &place);
+        x.inputs(a[2]);
         if (x.cu)
             check(g_api.fwd_varlen_sink(x.qp, x.kp, x.vp, o, lse, x.cu, x.nseq, x.S, x.top, x.Hq, x.Hkv, x.D, scale, causal, window,
                                         sink, nullptr, 0, place.stream),
@@ -551,14 +591,17 @@ PyObject* fwd_sink(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (q, k, v, o, lse, dO, dq, dk, dv, causal, window, sink, scale, cu_seqlens, max_seqlen, workspace, stream)
 PyObject* bwd_sink(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 17, [&]() -> PyObject* {
-        const Prompt x(a[0], a[1], a[2], a[13], a[14]);
-        const attn_bf16 *o = bf16(tensor(a[3], "o"), x.q.sizes(), x.idx, "o"), *dO = bf16(tensor(a[5], "dO"), x.q.sizes(), x.idx, "dO");
+        Prompt x(a[0], a[1], a[13], a[14]);
+        const attn_bf16* o = holding<attn_bf16>(tensor(a[3], "o"), at::kBFloat16, x.q.numel(), x.idx, "o");
+        const attn_bf16* dO = holding<attn_bf16>(tensor(a[5], "dO"), at::kBFloat16, x.q.numel(), x.idx, "dO");
         const float* lse = x.lse(a[4], nullptr, nullptr);
         const int causal = as_bool(a[9]), window = as_int(a[10], "window"), sink = as_int(a[11], "sink");
         const float scale = as_float(a[12]);
         Place place(a[16], x.idx);
         Result r[3];
-        attn_bf16 *dq = like(r[0], a[6], x.q, place, "dQ"), *dk = like(r[1], a[7], x.k, place, "dK"), *dv = like(r[2], a[8], x.k, place, "dV");
+        attn_bf16 *dq = x.result(r[0], a[6], x.q, place, "dQ"), *dk = x.result(r[1], a[7], x.k, place, "dK"),
+                  *dv = x.result(r[2], a[8], x.k, place, "dV");
+        x.inputs(a[2]);
         at::Tensor own;
         size_t bytes = 0;
         void* ws = scratch(own, bytes, a[15], g_api.bwd_sink_workspace_size(x.B, x.Hq, x.Hkv, x.S, x.D, x.nseq, window, sink), place);
@@ -579,17 +622,18 @@ PyObject* decode_paged_sink(PyObject*, PyObject* const* a, Py_ssize_t n) {
         attn_bf16* qp = bf16(q, q.sizes(), idx, "q");
         const Caches c(a[1], a[2], D, idx);
         const at::Tensor& table = tensor(a[3], "block_table");
-        if (table.dim() != 2 || table.size(1) > INT32_MAX) refuse("%s must be [B, max_pages]", "block_table");
-        const int64_t sB[1] = {B}, sTab[2] = {B, table.size(1)}, sL[2] = {B, Hq};
-        const int32_t *tab = i32(a[3], sTab, idx, "block_table"), *lens = i32(a[4], sB, idx, "seq_lens");
+        if (table.dim() != 2 || table.size(0) < B || table.size(1) > INT32_MAX) refuse("%s must be [B, max_pages]", "block_table");
+        const int64_t sL[2] = {B, Hq};
+        const int32_t *tab = holding<int32_t>(table, at::kInt, 0, idx, "block_table"),
+                      *lens = holding<int32_t>(tensor(a[4], "seq_lens"), at::kInt, B, idx, "seq_lens");
         const float scale = as_float(a[7]);
         const int window = as_int(a[8], "window"), sink = as_int(a[9], "sink");
         Place place(a[11], idx);
         Result r[2];
-        attn_bf16* o = like(r[0], a[5], q, place, "o");
+        attn_bf16* o = room_for(r[0], a[5], q.sizes(), q.numel(), place, "o");
         r[1].given = a[6];
         if (a[6] == Py_None) r[1].made = place.make(sL, at::kFloat);
-        float* lse = checked<float>(a[6] == Py_None ? r[1].made : tensor(a[6], "lse"), at::kFloat, sL, idx, "lse");
+        float* lse = holding<float>(a[6] == Py_None ? r[1].made : tensor(a[6], "lse"), at::kFloat, B * Hq, idx, "lse");
         at::Tensor own;
         size_t bytes = 0;
         void* ws = scratch(own, bytes, a[10], g_api.workspace_size(ATTN_OP_DECODE_PAGED, (int)B, (int)Hq, c.heads, 0, (int)D, 0, 0), place);
