@@ -278,7 +278,7 @@ int fwd_common(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, attn_
     }
     L.o = o, L.lse = lse, L.cu_seqlens = cu, L.status = dev->status;
     L.nseq = nseq, L.Hq = Hq, L.Hkv = Hkv, L.S = S, L.D = D, L.total_rows = (int)rows, L.window = window;
-    L.scale = scale, L.sink = sink;
+    L.scale = scale, L.sink = sink, L.sms = dev->sms;
     return attn::launch_fwd(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 

@@ -829,9 +829,7 @@ cudaError_t launch_fwd(const FwdLaunch& L, cudaStream_t stream) {
     // CTA) measured slower in pairs (0.713 against 0.665 ms), the pair's fixed cost outweighing
     // the halved stream, so 256 keeps single CTAs.
     const bool pair = L.pair_ok && (L.Hq / L.Hkv) % 2 == 0 && L.D == 512;
-    // several heads a CTA (MULTI) where there are enough tiles for that: 12 for each SM, 24 for four heads
-    const long long tiles = (long long)L.Hq * L.nseq * ((L.S + kBQ - 1) / kBQ);
-    const int heads = paged || L.D > 256 ? 1 : tiles >= 24 * 152 ? 4 : tiles >= 12 * 152 ? 2 : 1;
+    const int heads = paged || L.D > 256 ? 1 : fwd_heads(L.Hq, L.nseq, L.S, L.total_rows, L.cu_seqlens != nullptr, L.window, L.sms);
     if (L.D == 64)
         return paged ? launch_fwd_t<64, true, false>(L, 1, stream)
                      : heads > 1 ? launch_fwd_t<64, false, false, true>(L, heads, stream) : launch_fwd_t<64, false, false>(L, 1, stream);

@@ -77,7 +77,26 @@ struct FwdLaunch {
     const int32_t* cu_q = nullptr;
     int max_pages = 0, num_pages = 0;
     int sink = 0;  // first keys that stay visible past the window (0 .. 128)
+    int sms = 0;
 };
+// Query heads that a block of the forward without pages takes at head_dim <= 256, one after the other (1, 2 or 4, Hq at most).
+//  * Two where every SM has 12 query tiles for certain, four from 24 on (attn_fwd.cu, MULTI, has both sides). Dense calls know their tiles; of
+//    packed ones the host knows only that no tile holds more than 128 rows, and none more than max_seqlen.
+//  * Also where the grid has so many blocks that the empty ones count: of packed sequences far shorter than max_seqlen most blocks find no rows, 0.9 us
+//    each on its SM. A further head costs at most the longest tile's time, about 2 us a key tile and 6. (Heads of 128, us with 1 and 4 heads a
+//    block: one sequence of 4096 and 300 of 16, 8 heads, 77 thousand blocks 457 and 183; 4096 and 63 of 16, 16 thousand 132 and
+//    162; one of 1000 where max_seqlen is 32768, 16 heads, 4 thousand 35 and 56.)
+inline int fwd_heads(int Hq, int nseq, int S, int rows, bool packed, int window, int sms) {
+    if (S < 1) return 1;  // (nothing to launch)
+    const long long blocks = (long long)Hq * nseq * ((S + 127) / 128);
+    const int tile = S < 128 ? S : 128, longest = S < rows ? S : rows;
+    const long long tiles = packed ? (long long)Hq * ((rows + (long long)tile - 1) / tile) : blocks;
+    long long keys = (longest + 127) / 128;  // key tiles of the longest query tile
+    if (window > 0 && (window + 254ll) / 128 + 1 < keys) keys = (window + 254ll) / 128 + 1;
+    for (int heads = 4; heads > 1; heads /= 2)
+        if (heads <= Hq && (tiles >= 6ll * heads * sms || blocks >= heads * sms * (2 * keys + 7))) return heads;
+    return 1;
+}
 cudaError_t launch_fwd(const FwdLaunch& L, cudaStream_t stream);
 
 // ---- backward ---------------------------------------------------------------------------
