@@ -413,6 +413,7 @@ size_t attn_workspace_size(int op, int B, int Hq, int Hkv, int S, int D, int num
 size_t attn_bwd_sink_workspace_size(int B, int Hq, int Hkv, int S, int D, int num_seqs, int window, int sink) {
     if (B < 0 || Hq < 0 || Hkv < 0 || S < 0 || D < 0 || num_seqs < 0) return 0;
     const long long rows = (long long)B * S;
+    window = reaching(window, S);  // (packed: no sequence is longer than all of them)
     return bwd_ws(rows, Hq, D) + sink_ws(rows, num_seqs > B ? num_seqs : B, Hq, Hkv, D, window, sink);
 }
 
@@ -529,7 +530,7 @@ int attn_bwd_sink(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, co
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(dO) ||
         !aligned16(dQ) || !aligned16(dK) || !aligned16(dV))
         return ATTN_ERR_MISALIGNED;
-    window = reaching(window, grid_len);
+    window = reaching(window, grid_len < rows ? grid_len : rows);
     attn::SinkSplit split = {};
     if (window > 0 && sink > 0) {
         sink_slices(split, rows, Hq, Hkv, D, window, sink);
