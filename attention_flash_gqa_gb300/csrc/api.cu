@@ -137,9 +137,11 @@ int check_sink(int sink) { return sink < 0 ? ATTN_ERR_INVALID_ARG : sink > ATTN_
 // A window that no query of a sequence of at most `len` reaches the end of hides nothing.
 int reaching(int window, long long len) { return window >= len ? 0 : window; }
 
+constexpr int kMaxLen = 65535 * 128;  // of a sequence: a grid's third dimension of tiles
+
 int check_prefill_shape(long long rows, int Hq, int Hkv, int D, int S) {
     if (D != 64 && D != 128 && D != 256 && D != 512) return ATTN_ERR_UNSUPPORTED;
-    if (S > 65535LL * 128) return ATTN_ERR_UNSUPPORTED;
+    if (S > kMaxLen) return ATTN_ERR_UNSUPPORTED;
     if (rows > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;  // TMA row coordinates are int32
     (void)Hq, (void)Hkv;
     return ATTN_OK;
@@ -161,6 +163,7 @@ bool sinks_apart(long long rows, int Hq, int D, int sink) { return D <= 256 && s
 // of their own: 512 rows' worth of a head a block, 64 rows at least, and fewer where they would not be 4 blocks an SM.
 void sink_slices(attn::SinkSplit& s, long long rows, int Hq, int Hkv, int D, int window, int sink) {
     s.sink = sink, s.shares = 1;
+    if (window > kMaxLen) window = kMaxLen;  // (of sizes that no call takes)
     if (!sinks_apart(rows, Hq, D, sink)) {
         s.rows = 128 * ((window - 1) / 128 + 2 > 8 ? (window - 1) / 128 + 2 : 8);
         return;

@@ -32,3 +32,11 @@ def test_call_and_size_agree(lib):
             assert call(**packed, wsb=attn.attn_workspace_size(attn.ATTN_OP_BWD, 1, 8, 2, 700, 128) - 1) == WORKSPACE
             # (so many bytes are enough: what is refused then is where they start)
             assert call(**packed, wsb=need, ws=A + 16) == MISALIGNED, (top, window)
+
+
+def test_sizes_that_no_call_takes(lib):
+    """The size is host arithmetic over any numbers: two parts of one sequence's sinks at least, for the longest too."""
+    for S in (65535 * 128, 2 ** 31 - 1):
+        for window in (1, 65535 * 128 - 1, S - 1):
+            parts = lib.attn_bwd_sink_workspace_size(1, 8, 2, S, 128, 0, window, 4) - attn.attn_workspace_size(attn.ATTN_OP_BWD, 1, 8, 2, S, 128)
+            assert parts >= 2 * 2 * 2 * 4 * 128 * 4, (S, window)
