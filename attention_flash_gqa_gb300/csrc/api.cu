@@ -164,6 +164,7 @@ bool sinks_apart(long long rows, int Hq, int D, int sink) { return D <= 256 && s
 void sink_slices(attn::SinkSplit& s, long long rows, int Hq, int Hkv, int D, int window, int sink) {
     s.sink = sink, s.shares = 1;
     if (window > kMaxLen) window = kMaxLen;  // (of sizes that no call takes)
+    s.reach = window + 127;
     if (!sinks_apart(rows, Hq, D, sink)) {
         s.rows = 128 * ((window - 1) / 128 + 2 > 8 ? (window - 1) / 128 + 2 : 8);
         return;
@@ -179,7 +180,7 @@ size_t sink_ws(long long rows, long long nseq, int Hq, int Hkv, int D, int windo
     if (window <= 0 || sink <= 0) return 0;
     attn::SinkSplit s;
     sink_slices(s, rows, Hq, Hkv, D, window, sink);
-    return align256((size_t)(rows / s.rows + 2 * nseq) * s.shares * Hkv * 2 * sink * D * 4);
+    return align256((size_t)s.parts(rows, nseq) * Hkv * 2 * sink * D * 4);
 }
 
 // CTAs per KV-head block of a decode launch at most: the blocks share decode_max_grid() CTAs.

@@ -105,8 +105,9 @@ cudaError_t launch_fwd(const FwdLaunch& L, cudaStream_t stream);
 // are shared out in slices of `rows` queries: to a kernel of their own where the sinks are few enough for its warp MMAs, else to
 // blocks of the main kernel, so that none has much more to do than one of the window's. The near block and each slice
 // (in its kernel: each share of a slice) leave dV and dK of the sinks as parts in fp32, [part][Hkv][2][sink][D], and a small kernel
-// adds them up. Parts of a sequence start at (floor(first row / rows of a slice) + 2 x its number) x shares: it has at most
-// (floor(length / rows of a slice) + 1) x shares + 1 of them, so none overlap, and nobody has to count those of the others.
+// adds them up. Parts of a sequence start at (floor(first row / rows of a slice) + 2 m) x shares, m being the smaller of its number and
+// floor(first row / reach): it has at most (floor(length / rows of a slice) + 1) x shares + 1 of them, and a sequence with far queries has more than
+// `reach` rows, so that m rises by one at least from one of those to the next. So none overlap, nobody has to count those of the others, and short sequences need no room.
 struct SinkSplit {
     float* part;
     int sink;    // 0: none
@@ -114,8 +115,18 @@ struct SinkSplit {
     int rows;     // queries of a slice
     int shares;   // of the heads of a group, each a block and a part of its own
     int in_main;  // far slices that are blocks of the main kernel: all of them, or none where a kernel of their own has them
+    int reach;    // window + 127: a sequence with far queries is longer
+    // Bound on the parts of all sequences with far queries.
+    __host__ __device__ long long parts(long long total_rows, long long nseq) const {
+        const long long m = total_rows / reach;
+        return (total_rows / rows + 2 * (m < nseq ? m : nseq)) * shares;
+    }
+    __host__ __device__ long long first_part(int seq, int start) const {
+        const int m = start / reach;
+        return (long long)(start / rows + 2 * (m < seq ? m : seq)) * shares;
+    }
     __host__ __device__ float* row(int seq, int start, int p, int g, int Hkv, int j, int D) const {
-        const size_t at = ((size_t)(start / rows + 2 * seq) * shares + p) * Hkv + g;
+        const size_t at = (size_t)(first_part(seq, start) + p) * Hkv + g;
         return part + (at * 2 * sink + j) * D;
     }
 };

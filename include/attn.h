@@ -274,7 +274,8 @@ ATTN_API int attn_bwd_sink(const attn_bf16* q, const attn_bf16* k, const attn_bf
                            size_t workspace_bytes, void* stream);
 
 /* attn_bwd_sink_workspace_size -- bytes that attn_bwd_sink needs; packed: B = 1, S = total tokens and num_seqs, dense:
- *   num_seqs = 0. Pure host arithmetic; needs no GPU. */
+ *   num_seqs = 0. On top of the plain gradient's: the sinks' parts, of the sequences only that can be longer than the window.
+ *   Pure host arithmetic; needs no GPU. */
 ATTN_API size_t attn_bwd_sink_workspace_size(int B, int Hq, int Hkv, int S, int D, int num_seqs, int window, int sink);
 
 /* attn_decode_paged_sink: the pages of the sinks and those of the window are read, none between them. Workspace as for
