@@ -503,7 +503,9 @@ int attn_fwd_paged_sink(const attn_bf16* q, const attn_bf16* k_cache, const attn
         L.pair_ok = true;
     }
     L.o = o, L.lse = lse, L.cu_seqlens = nullptr, L.status = dev->status;
-    L.nseq = num_reqs, L.Hq = Hq, L.Hkv = Hkv, L.S = max_q_len, L.D = D, L.total_rows = total_q, L.window = window;
+    L.nseq = num_reqs, L.Hq = Hq, L.Hkv = Hkv, L.S = max_q_len, L.D = D, L.total_rows = total_q;
+    // (no request is longer than its table row; the kernel's bounds, position - window - key, stay within 32 bits)
+    L.window = reaching(window, max_pages_per_seq * 16ll);
     L.scale = scale, L.sink = sink;
     L.block_table = block_table, L.seq_lens = seq_lens, L.cu_q = cu_q;
     L.max_pages = max_pages_per_seq, L.num_pages = num_pages;
