@@ -236,7 +236,7 @@ bool kv4_dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
 constexpr int kKv4MaxGrid = 256;  // blocks of a 4-bit decode at most
 size_t kv4_ws(int B, int Hq, int Hkv, int D) {
     if (B < 0 || B > 4096 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Hq / Hkv > 8 || !kv4_dim_ok(D)) return 0;
-    return align256(attn::decode_kv4_workspace_bytes(Hq / Hkv, D, kKv4MaxGrid));
+    return align256(attn::decode_kv4_workspace_bytes(B, Hq / Hkv, D, kKv4MaxGrid));
 }
 
 bool tree_shape_ok(int Hq, int Hkv, int max_q, int D) {
@@ -869,7 +869,7 @@ int attn_decode_kv4(const attn_bf16* q, const uint8_t* kv_cache, const int32_t* 
     L.status = dev->status, L.workspace = workspace;
     L.B = B, L.Hq = Hq, L.Hkv = Hkv, L.D = D, L.max_pages = max_pages_per_seq, L.num_pages = num_pages;
     L.window = window, L.sink = sink, L.scale = scale;
-    L.grid = dev->sms < kKv4MaxGrid ? dev->sms : kKv4MaxGrid;
+    L.grid = dev->sms < kKv4MaxGrid ? dev->sms : kKv4MaxGrid, L.max_grid = kKv4MaxGrid;
     return attn::launch_decode_kv4(L, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_LAUNCH;
 }
 

@@ -239,9 +239,10 @@ struct DecodeKv4Launch {
     unsigned* status;
     void* workspace;
     int B, Hq, Hkv, D, max_pages, num_pages, window, sink, grid;
+    int max_grid;  // that the workspace is made for
     float scale;
 };
-size_t decode_kv4_workspace_bytes(int G, int D, int grid);
+size_t decode_kv4_workspace_bytes(int B, int G, int D, int max_grid);
 cudaError_t launch_decode_kv4(const DecodeKv4Launch& L, cudaStream_t stream);
 
 }  // namespace attn

@@ -31,6 +31,8 @@
 //    outside it go to the workspace, at most two a block, and a second kernel joins them.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "attn_internal.h"
 #include "kv4.cuh"
 #include "ptx.cuh"
@@ -66,6 +68,7 @@ struct Args {
     uint16_t* o;
     float* lse;
     float* part;     // [block][2][G][kRow]
+    int32_t* starts;  // [B + 1] pages before a request, for the join of many requests; null: it sums the lengths itself
     unsigned* status;
     int B, Hq, Hkv, G, max_pages, num_pages, window, sink;
     bool lens_here;  // the lengths are kept in shared memory
@@ -275,6 +278,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
         __syncwarp();
         flip = 1, sure = true;
     }
+    if (a.starts && blockIdx.x == 0)
+        for (int b = tid; b <= a.B; b += C::kThreads) a.starts[b] = start[b];
     // the second kernel may be placed from here on; it waits for this one's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -623,49 +628,36 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kv4_kernel(Args a)
     }
 }
 
-// Joins the pieces of the segments that several blocks of the decode kernel shared, a block for each segment; the others are done,
-// but for the rows of requests without a key, which come out as o = 0, lse = -inf. Which pieces there are follows from the lengths
-// alone, inputs of the call, so that it is known before the decode kernel ends. A thread has 4 dims of a head; 8 pieces are on their
-// way at once. (It adds 2 us. Registers that let its warps be placed beside the decode kernel's blocks, 32 a thread here and 120 there, would
-// gain 0.1 of 20.7 in a batch of 64 and lose 5 of 106 over long contexts; a block for each border between blocks instead of each segment
-// loses 1 in the batch.)
+// ---- the second kernel ----------------------------------------------------------------------------
+// Joins the pieces of the segments that several blocks of the decode kernel shared; the others are done, but for the rows of requests
+// without a key, which come out as o = 0, lse = -inf.
+constexpr int kJoinThreads = 128;
+
+// Where the pieces of a segment of `np` units, the first of them `s0`, are: blocks kf .. kl, of kf in its slot `opens` (a block's first
+// slot holds what began before it).
+struct Pieces {
+    int kf, kl, opens;
+    __device__ Pieces(const Share& share, int s0, int np) : kf(share.owner(s0)), kl(share.owner(max(s0 + np - 1, s0))), opens(s0 < share.first(kf) ? 0 : 1) {}
+};
+
+// A thread has 4 dims of a head; 8 pieces are on their way at once.
 template <int D>
-__global__ void __launch_bounds__(128) decode_kv4_join_kernel(Args a, int grid) {
+__device__ __forceinline__ void join_segment(const Args& a, int segment, int np, const Pieces& at) {
     using C = Cfg<D>;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int segment = blockIdx.x, b = segment / a.Hkv, h = segment - b * a.Hkv, lane = threadIdx.x & 31;
-    int first = 0, units = 0;
-    for (int i = lane; i < a.B; i += 32) {
-        const int np = seen_pages(a, req_len(a, i, false));
-        units += np;
-        if (i < b) first += np;
-    }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) {
-        first += __shfl_xor_sync(0xffffffffu, first, off);
-        units += __shfl_xor_sync(0xffffffffu, units, off);
-    }
-    units *= a.Hkv;
-    const int np = seen_pages(a, req_len(a, b, false));
     const int items = a.G * (D / 4);
     const size_t row0 = (size_t)segment * a.G;
-    const int s0 = first * a.Hkv + h * np, s1 = s0 + np;
-    const Share share(max(units, 1), max(min(grid, units), 1));
-    const int kf = share.owner(s0), kl = share.owner(max(s1 - 1, s0));
-    const int opens = s0 < share.first(kf) ? 0 : 1;  // a block's first slot holds what began before it
-    griddep_wait();
     if (np == 0) {
-        for (int it = threadIdx.x; it < items; it += 128) {
+        for (int it = threadIdx.x; it < items; it += kJoinThreads) {
             *reinterpret_cast<uint2*>(a.o + row0 * D + 4 * it) = make_uint2(0, 0);
             if (it % (D / 4) == 0) a.lse[row0 + it / (D / 4)] = -INFINITY;
         }
         return;
     }
-    if (kf == kl) return;
-    for (int it = threadIdx.x; it < items; it += 128) {
+    if (at.kf == at.kl) return;
+    for (int it = threadIdx.x; it < items; it += kJoinThreads) {
         const int hh = it / (D / 4), d = 4 * (it % (D / 4));
         float O[4] = {}, M = -INFINITY, L = 0.f;
-        for (int k0 = kf; k0 <= kl; k0 += 8) {
+        for (int k0 = at.kf; k0 <= at.kl; k0 += 8) {
             float4 x[8];
             float2 ml[8];
             float top = M;
@@ -673,8 +665,8 @@ __global__ void __launch_bounds__(128) decode_kv4_join_kernel(Args a, int grid) 
             for (int j = 0; j < 8; ++j) {
                 x[j] = make_float4(0.f, 0.f, 0.f, 0.f), ml[j] = make_float2(-INFINITY, 0.f);
                 const int k = k0 + j;
-                if (k <= kl) {
-                    const float* row = a.part + (((size_t)k * 2 + (k == kf ? opens : 0)) * a.G + hh) * C::kRow;
+                if (k <= at.kl) {
+                    const float* row = a.part + (((size_t)k * 2 + (k == at.kf ? at.opens : 0)) * a.G + hh) * C::kRow;
                     x[j] = __ldcg(reinterpret_cast<const float4*>(row + d));
                     ml[j] = __ldcg(reinterpret_cast<const float2*>(row + D));
                 }
@@ -696,13 +688,82 @@ __global__ void __launch_bounds__(128) decode_kv4_join_kernel(Args a, int grid) 
     }
 }
 
+// Up to kSumRequests requests: a block for each segment. Which pieces there are follows from the lengths
+// alone, inputs of the call, so that it is known before the decode kernel ends. (It adds 2 us. Registers that let its warps be placed beside the
+// decode kernel's blocks, 32 a thread here and 120 there, would gain 0.1 of 20.7 in a batch of 64 and lose 5 of 106 over long contexts; a block
+// for each border between blocks instead of each segment loses 1 in the batch.)
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) decode_kv4_join_kernel(Args a, int grid) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int segment = blockIdx.x, b = segment / a.Hkv, h = segment - b * a.Hkv, lane = threadIdx.x & 31;
+    int first = 0, units = 0;
+    for (int i = lane; i < a.B; i += 32) {
+        const int np = seen_pages(a, req_len(a, i, false));
+        units += np;
+        if (i < b) first += np;
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+        first += __shfl_xor_sync(0xffffffffu, first, off);
+        units += __shfl_xor_sync(0xffffffffu, units, off);
+    }
+    units *= a.Hkv;
+    const int np = seen_pages(a, req_len(a, b, false));
+    const Share share(max(units, 1), max(min(grid, units), 1));
+    const Pieces at(share, first * a.Hkv + h * np, np);
+    griddep_wait();
+    join_segment<D>(a, segment, np, at);
+}
+
+// More requests: each block looks at `per` segments, one a thread, by the pages that the decode kernel counted, and joins those that need it
+// (every block summing all lengths took B^2 Hkv reads).
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) decode_kv4_join_many_kernel(Args a, int grid, int per) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    griddep_wait();
+    __shared__ uint32_t todo[kJoinThreads / 32];
+    const int first = blockIdx.x * per, units = __ldcg(a.starts + a.B) * a.Hkv;
+    const Share share(max(units, 1), max(min(grid, units), 1));
+    auto pages = [&](int segment, int& s0) -> int {
+        const int b = segment / a.Hkv, at = __ldcg(a.starts + b), np = __ldcg(a.starts + b + 1) - at;
+        s0 = at * a.Hkv + (segment - b * a.Hkv) * np;
+        return np;
+    };
+    bool mine = false;
+    if ((int)threadIdx.x < per && first + (int)threadIdx.x < a.B * a.Hkv) {
+        int s0;
+        const int np = pages(first + threadIdx.x, s0);
+        const Pieces at(share, s0, np);
+        mine = np == 0 || at.kf != at.kl;
+    }
+    const uint32_t vote = __ballot_sync(0xffffffffu, mine);
+    if ((threadIdx.x & 31) == 0) todo[threadIdx.x >> 5] = vote;
+    __syncthreads();
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+        for (uint32_t left = todo[w]; left; left &= left - 1) {
+            const int segment = first + 32 * w + __ffs(left) - 1;
+            int s0;
+            const int np = pages(segment, s0);
+            join_segment<D>(a, segment, np, Pieces(share, s0, np));
+        }
+    }
+}
+
+// Requests up to which the join's blocks sum the lengths, which they do while the decode kernel runs. (The whole call, us, this way and by counted
+// pages, 8 heads of 128: 64 requests of 512 27 and 28, 128 of 300 28.0 and 29.5, 200 of 300 40 and 37, 1024 of 100 101 and 55, 4096 of 100 849 and
+// 152, of 17 779 and 80; 2 heads, 128 of 300 19.2 and 20.3.)
+constexpr int kSumRequests = 128;
+
+size_t part_bytes(int G, int D, int grid) { return (size_t)grid * 2 * G * (D + 4) * 4; }
+
 template <int D>
 cudaError_t launch_t(const DecodeKv4Launch& L, cudaStream_t stream) {
     using C = Cfg<D>;
-    Args a;
+    Args a = {};
     a.q = L.q, a.cache = L.cache, a.block_table = L.block_table, a.seq_lens = L.seq_lens, a.o = L.o, a.lse = L.lse;
     a.part = static_cast<float*>(L.workspace);
     a.status = L.status, a.B = L.B, a.Hq = L.Hq, a.Hkv = L.Hkv, a.G = L.Hq / L.Hkv;
+    a.starts = L.B > kSumRequests ? reinterpret_cast<int32_t*>(static_cast<uint8_t*>(L.workspace) + part_bytes(a.G, D, L.max_grid)) : nullptr;
     a.max_pages = L.max_pages, a.num_pages = L.num_pages, a.window = L.window, a.sink = L.window > 0 ? L.sink : 0;
     a.scale_log2 = L.scale * 1.4426950408889634f;
     a.lens_here = C::smem_bytes(L.B, a.G, true) <= kSmemLimit;
@@ -723,18 +784,27 @@ cudaError_t launch_t(const DecodeKv4Launch& L, cudaStream_t stream) {
     e = cudaLaunchKernelEx(&cfg, decode_kv4_kernel<D>, a);
     prof_end(stream, mark);
     if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
-    cfg.gridDim = dim3(L.B * L.Hkv);
-    cfg.blockDim = dim3(128);
+    const int segments = L.B * L.Hkv;
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     mark = prof_begin(stream, "decode_kv4_join");
-    e = cudaLaunchKernelEx(&cfg, decode_kv4_join_kernel<D>, a, L.grid);
+    if (a.starts) {
+        const int per = std::min((segments + 8 * L.grid - 1) / (8 * L.grid), kJoinThreads);  // 8 blocks an SM, where that is enough
+        cfg.gridDim = dim3((segments + per - 1) / per);
+        e = cudaLaunchKernelEx(&cfg, decode_kv4_join_many_kernel<D>, a, L.grid, per);
+    } else {
+        cfg.gridDim = dim3(segments);
+        e = cudaLaunchKernelEx(&cfg, decode_kv4_join_kernel<D>, a, L.grid);
+    }
     prof_end(stream, mark);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-size_t decode_kv4_workspace_bytes(int G, int D, int grid) { return (size_t)grid * 2 * G * (D + 4) * 4; }
+size_t decode_kv4_workspace_bytes(int B, int G, int D, int max_grid) {
+    return part_bytes(G, D, max_grid) + (B > kSumRequests ? (size_t)(B + 1) * 4 : 0);
+}
 
 cudaError_t launch_decode_kv4(const DecodeKv4Launch& L, cudaStream_t stream) {
     if (L.D == 64) return launch_t<64>(L, stream);
