@@ -237,7 +237,8 @@ def _scratch(nbytes: int, device):
 def attn_fwd(q, k, v, o=None, lse=None, *, causal: bool = True, window: int = 0, scale: float | None = None,
              stream=None, sink: int = 0):
     """Forward of causal (optionally sliding-window) GQA attention, dense [B, S, H, D] layout. With a window the
-    sequence's first ``sink`` keys (0 to 128) stay visible to every later query."""
+    sequence's first ``sink`` keys (0 to 128) stay visible to every later query; K and V of its first 128 keys, whose tile is
+    then read, must be finite."""
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     if ops := _bound or _native_for(sink):
@@ -406,7 +407,7 @@ def attn_decode_paged_noalloc(q, k_cache, v_cache, block_table, seq_lens, o, lse
     """attn_decode_paged without a workspace: the library's built-in scratch buffer is used.
 
     For callers that cannot allocate device memory on their decode path, so the outputs
-    ``o`` [B,Hq,D] and ``lse`` [B,Hq] must be supplied by the caller. Calls that overlap
+    ``o`` [B,Hq,D] and ``lse`` [B,Hq] must be supplied by the caller. It takes no sinks. Calls that overlap
     on the GPU share the buffer and race; see include/attn.h for the size limit.
     """
     import torch
@@ -539,7 +540,7 @@ def attn_tree_paged(q, k_cache, v_cache, block_table, seq_lens, cu_q, tree_mask,
     sees its request's drafted token d; every row sees the context before the drafted tokens, with
     window > 0 only the keys less than `window` behind its position (positions int32 [T]). Among the drafted
     tokens the mask alone decides: for a windowed layer whose trees are deeper than the window, clear the bits of
-    the ancestors `window` or more positions back.
+    the ancestors `window` or more positions back. There are no sinks past the window here.
     """
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
@@ -558,7 +559,7 @@ def attn_kv4_append(k, v, slots, kv_cache, *, page_size: int = 16, stream=None) 
 
 def attn_kv4_unpack(kv_cache, pages, k_pages=None, v_pages=None, *, page_size: int = 16, stream=None):
     """Pages of a 4-bit cache as bf16, exactly -> (k_pages, v_pages) [n,16,Hkv,D]: what attn_fwd_paged and attn_tree_paged read, with a
-    block table of 0 .. n-1. pages int32 [n] (-1: left as it is)."""
+    block table of 0 .. n-1. pages int32 [n] (-1: that page of the results is left as it is, in new ones as it was allocated)."""
     return (_bound or _native()).kv4_unpack(kv_cache, pages, k_pages, v_pages, page_size, stream)
 
 

@@ -36,7 +36,7 @@
 // Sinks (the first `sink` keys stay visible past the window, one key tile at most): a query tile whose window has left key
 // tile 0 takes that tile first, all of it loaded and masked to its sinks, then the window's. A row's mask is two words with a bit
 // a column, from its bounds, whatever it is made of; compared column by column, the third condition cost every masked tile
-// 12 to 25 %. B = 2, S = 8192, 32 + 16 heads of 256, window 1024: 605 us with 1 to 128 sinks, 563 without (10 tiles for 9). A tile
+// 12 to 25 %. B = 2, S = 8192, 32 + 16 heads of 256, window 1024: 608 us with 1 to 128 sinks, 567 without (10 tiles for 9). A tile
 // of its own width for a few sinks would save 14 us of that, but step widths known only at run time cost the issuer 7 % of every call.
 // Over a paged cache, pages of these tiles that nobody sees (between the sinks and the window's first page) are not looked up: a page
 // that is seen is loaded in their place.

@@ -2,7 +2,7 @@
 //
 // Definition: attn_decode_paged over the values that the cache stands for. Every visible byte of the cache is read once;
 // at 18 D bytes a page and KV head against 64 D in bf16 the arithmetic is no longer free. Measured, call after call: 12 contexts of 5 to
-// 60 thousand keys, 8 heads of 128: 105 us for 498 MB, 0.70 of the copy rate (in bf16 its 1.77 GB alone would take 261); 64 requests of 256
+// 60 thousand keys, 8 heads of 128: 104 us for 498 MB, 0.70 of the copy rate (in bf16 its 1.77 GB alone would take 261); 64 requests of 256
 // to 1024: 20.0 us for 46 MB; 33 requests, 16 heads of 256, window 1024, 4 sinks: 40.0 us for 150 MB. What bounds it: the same rings
 // without arithmetic take 82 us over the long contexts. A unit at D = 128 is 360 instructions of a warp, 162 of them shifts and masks, whose
 // pipe is half as wide, and 63 % of the issue slots are used: K's part alone takes 89 us, V's alone 100. The batch pays 5 us of layout and

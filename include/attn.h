@@ -214,7 +214,7 @@ ATTN_API int attn_decode_paged(const attn_bf16* q, const attn_bf16* k_cache, con
  * takes no workspace: the kernel's scratch comes from a 16 MiB buffer compiled into the
  * library (attn_decode_paged_noalloc_max_bytes()), which every GPU that loads the library
  * keeps until the process exits. It allocates nothing and calls no allocating routine.
- *   Arguments, layouts and results are those of attn_decode_paged.
+ *   Arguments, layouts and results are those of attn_decode_paged (there is no form with sinks).
  *   Limit: attn_workspace_size(ATTN_OP_DECODE_PAGED, B, Hq, Hkv, 0, D, 0, max_pages) must
  *   not exceed attn_decode_paged_noalloc_max_bytes() (e.g. Hq = 32 allows B up to 240);
  *   larger problems are rejected with ATTN_ERR_WORKSPACE before anything is enqueued.
@@ -422,7 +422,7 @@ ATTN_API int attn_qk_norm_rope_paged(const attn_bf16* q, const attn_bf16* k, con
  *     p_i = max(positions[i], L_b - n_b) is the row's position (context length + depth in its tree);
  *   key L_b - n_b + d (drafted token d): visible if bit d % 32 of word d / 32 of the row's mask is
  *     set (normally its ancestors and itself). Bits of d >= n_b are ignored.
- *   So a window limits the context alone. attn_fwd_paged and attn_decode_paged apply theirs to the new tokens
+ *   So a window limits the context alone, all of it: this call takes no sinks (attn_fwd_paged_sink). attn_fwd_paged and attn_decode_paged apply theirs to the new tokens
  *   too: for their result where a tree is deeper than the window, the caller clears the bits of the ancestors
  *   that are `window` or more positions behind the row (p_i - p_d >= window).
  *   A row that sees no key gets o = 0 and lse = -inf. A row with a NaN score (NaN in its q or in a K that it
