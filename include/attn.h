@@ -266,7 +266,8 @@ ATTN_API int attn_fwd_paged_sink(const attn_bf16* q, const attn_bf16* k_cache, c
 /* attn_bwd_sink -- gradient of attn_fwd_sink / attn_fwd_varlen_sink.
  *   workspace: at least attn_bwd_sink_workspace_size() bytes, 256-byte aligned. dK and dV of a sequence's sinks are sums
  *   over all of it; they are made in parts that lie in the workspace, and added up in one order (the same bits every time
- *   for dK and dV; dQ, like attn_bwd's, is added up in fp32 in no fixed order). */
+ *   for dK and dV; dQ, like attn_bwd's, is added up in fp32 in no fixed order). Tiles of 128 queries and slices of the far
+ *   ones (1024 or more queries each) are at most 65535 together: sequences (packed: max_seqlen) of up to 7.4 million tokens. */
 ATTN_API int attn_bwd_sink(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, const attn_bf16* o,
                            const float* lse, const attn_bf16* dO, attn_bf16* dQ, attn_bf16* dK, attn_bf16* dV, int B,
                            int Hq, int Hkv, int S, int D, float scale, int causal, int window, int sink,

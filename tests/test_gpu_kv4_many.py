@@ -67,10 +67,11 @@ def test_more_segments_than_a_block_looks_at():
     assert attn.attn_get_device_status() == 0
 
 
-def test_workspace_and_chains():
+@pytest.mark.parametrize("B", [300, 700])  # (up to 512 the layout is first made on a guess)
+def test_workspace_and_chains(B):
     """In exactly the bytes that are named, whatever they hold; calls of different lengths one after the other in one workspace, and in a
     graph, lengths made by the kernel in front."""
-    B, Hkv, G, D = 700, 2, 2, 128
+    Hkv, G, D = 2, 2, 128
     lens = torch.randint(0, 60, (B,), generator=gen(1))
     q, cache, table, _ = problem([60] * B, Hkv, G, D, 25)
     q, cache, table = q.cuda(), cache.cuda(), table.cuda()
