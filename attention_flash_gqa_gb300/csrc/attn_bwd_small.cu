@@ -35,12 +35,13 @@
 // runs. Each half of the score columns keeps its P^T (bf16 pairs) in the first 32 columns of its
 // own half of R0.
 //
-// P^T for dS stays in registers from one part of a step to the next: at D = 256 in fp32 (dQ and dK 0.0024 off the 64-bit result,
-// relatively), at D <= 128 as the bf16 pairs of dV's product (0.0029). Both have all of fp32's range, so that keys far below their
+// P^T for dS stays in registers from one part of a step to the next: at D = 256 and in calls with sinks in fp32 (WIDE; dQ and dK 0.0024 off the
+// 64-bit result, relatively), else as the bf16 pairs of dV's product (0.0029). Both have all of fp32's range, so that keys far below their
 // rows' maxima get their gradient too (fp16 would lose bits from P = 2^-29 on and all of them at 2^-39, with its range used to the full).
 // The 64 registers cost what hides the loads of dP^T where the step is short. The whole gradient, fp32 and bf16, us: D = 256, 2 x 8192
 // tokens of 32 heads, window 1024 2946 and 2968, 2 x 4096 causal 2705 and 2720; D = 128, 4 x 4096 of 32 heads 1653 and 1599, one of
-// 16000 with 8 heads, window 700 235 and 229; D = 64, 4 x 4096 1088 and 1073.
+// 16000 with 8 heads, window 700 235 and 229, with 16 sinks 240.6 both, 2 x 8192 of
+// 32, window 1024, 4 sinks 1008 and 983; D = 64, 4 x 4096 1088 and 1073, 2 x 8192, window 500, 4 sinks 450 and 441.
 //
 // Sinks: every query of a sequence sees key tile 0 then, where its other keys are seen by the window's queries alone. SinkSplit
 // (attn_internal.h) says how those far queries are shared out: to bwd_far_sink_kernel, or in slices to blocks of this kernel, which are
@@ -109,13 +110,12 @@ struct SmallArgs {
     SinkSplit sink;
 };
 
-template <int D, int DS>
+template <int D, int DS, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_small_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                      const __grid_constant__ CUtensorMap tdq, SmallArgs a) {
     using C = SmallCfg<D, DS>;
-    constexpr bool kWide = D == 256;  // P^T for dS in fp32
     griddep_wait();
     const int g = blockIdx.x / C::NSL;        // KV head
     const int c0 = (blockIdx.x % C::NSL) * DS;  // this CTA's columns of dV, dK, dQ
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 32 score columns at a time; this half's P columns [64 hf + 16c, +16) overwrite
             // scores of its own first chunk, already read
             ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(s_full), t & 1, abort_flag, a.status, 0x4b));
-            uint32_t pt[kWide ? 64 : 32];  // P^T for dS: in fp32, or bf16 pairs
+            uint32_t pt[WIDE ? 64 : 32];  // P^T for dS: in fp32, or bf16 pairs
             if (ok) {
                 tc_fence_after();
                 const bool edge = !(k0 + kB - 1 <= q0 && (a.window <= 0 || q0 + kB - 1 - k0 < a.window) &&
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (decltype(masked)::value && !(see >> (e + u) & 1u)) p[u] = 0.f;
                             }
                             w[e / 2] = pack_bf16x2(p[0], p[1]), w[e / 2 + 1] = pack_bf16x2(p[2], p[3]);
-                            if constexpr (kWide) {
+                            if constexpr (WIDE) {
 #pragma unroll
                                 for (int u = 0; u < 4; ++u) pt[32 * c + e + u] = __float_as_uint(p[u]);
                             } else {
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 4; ++e) {
                             const int cc = ch * 8 + 2 * e;  // column within the 32-column chunk
                             float p0, p1;
-                            if constexpr (kWide) {
+                            if constexpr (WIDE) {
                                 p0 = __uint_as_float(pt[32 * c + cc]), p1 = __uint_as_float(pt[32 * c + cc + 1]);
                             } else {
                                 const uint32_t pw = pt[16 * c + cc / 2];
@@ -734,12 +734,12 @@ cudaError_t launch_bwd_small_main(const BwdLaunch& L, cudaStream_t stream) {
     a.scale = L.scale, a.scale_log2 = L.scale * kLog2e;
     a.sink = L.sink;
     constexpr uint32_t kSmem = SmallCfg<D, DS>::kSmem;
-    cudaError_t e =
-        cudaFuncSetAttribute(bwd_small_kernel<D, DS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    const auto kern = D == 256 || L.sink.sink > 0 ? bwd_small_kernel<D, DS, true> : bwd_small_kernel<D, DS, D == 256>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
     const dim3 grid(L.Hkv * (D / DS), L.nseq, L.sink.in_main + (L.S + kB - 1) / kB);
     const ProfMark m = prof_begin(stream, D == 256 ? "bwd_main_d256" : D == 128 ? "bwd_main_d128" : "bwd_main_d64");
-    e = launch_behind(bwd_small_kernel<D, DS>, grid, dim3(kThreads), kSmem, stream, L.tq, L.tk, L.tv, L.tdo, L.tdq, a);
+    e = launch_behind(kern, grid, dim3(kThreads), kSmem, stream, L.tq, L.tk, L.tv, L.tdo, L.tdq, a);
     prof_end(stream, m);
     return e;
 }
